@@ -73,7 +73,12 @@ typedef enum {
 typedef enum { OOMB_BF16 = 0, OOMB_FP32 = 1 } oomb_dtype;
 
 /* Operation selector for oomb_workspace_size. */
-typedef enum { OOMB_OP_SELECT = 0, OOMB_OP_BWD = 1 } oomb_op;
+typedef enum {
+  OOMB_OP_SELECT = 0,
+  OOMB_OP_BWD = 1,
+  OOMB_OP_SCORE_FWD = 2, /* oomb_score_attn_fwd (may be 0) */
+  OOMB_OP_SCORE_BWD = 3  /* oomb_score_attn_bwd */
+} oomb_op;
 
 /* Device error-word bits (see oomb_check). */
 #define OOMB_DEVERR_TIMEOUT 0x1u  /* an mbarrier wait ran out */
@@ -338,6 +343,69 @@ OOMB_API oomb_status oomb_chunk_attn_bwd(oomb_pool* pool, const void* q, const v
                                 int64_t q_start, int n_q, const int32_t* sel, const int32_t* sel_count, int max_sel,
                                 float softmax_scale, void* dq, void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------- modified attention scores
+ * Chunk attention whose scores are capped, get a bias that falls with distance, and are
+ * masked per query row: what models with capped attention logits, distance-biased heads,
+ * packed documents or bidirectional prefixes put in place of the plain causal scores. */
+typedef struct {
+  float softcap;            /* s = softcap * tanh(scale q.k / softcap); 0: not capped */
+  const float* slopes;      /* device fp32 [Hq], s -= slopes[hq] * |i - j| (token positions),
+                               or NULL.  A constant of the model: no gradient is formed */
+  const int64_t* key_begin; /* device [n_q]: row i sees no key before key_begin[i]; NULL: 0 */
+  const int64_t* key_end;   /* device [n_q]: row i sees no key at or after key_end[i]; NULL:
+                               q_start + i + 1 (causal).  Ranges are cut to the tokens
+                               appended; an empty one leaves the row without keys */
+} oomb_score_mod;
+
+/* Forward of the chunk's queries over the selected pages, as oomb_chunk_attn_fwd with the
+ * scores of `mod` (NULL: none, plain causal attention): O = softmax(s) V over the keys that
+ * are in a selected page and in the row's range, LSE its natural-log sum.  A row that sees
+ * no key gets O = 0 and LSE = -inf.  Differences from oomb_chunk_attn_fwd:
+ *  - q_start may be any position (one new token, a chunk that starts inside a page); the
+ *    chunk's own K/V must be appended.
+ *  - with key_end given, the selection may name any appended page, so that a row can see
+ *    keys after its own position (a prefix); without it, pages up to the chunk's end.
+ *  - pages that no row of a tile can see are not read; where there are few rows the keys are
+ *    split over thread blocks, whose parts are joined in a fixed order.
+ *  - a selection that is not strictly ascending pages of that view, or a page that is not
+ *    mapped, sets OOMB_DEVERR_SEL / OOMB_DEVERR_PAGE; the entry is left out.
+ * K and V must be finite in the pages read: a masked key weighs nothing, but 0 times an
+ * infinity or a NaN in V is a NaN.  Workspace: oomb_workspace_size(OOMB_OP_SCORE_FWD, n_q)
+ * bytes (may be 0), contents scratch; two calls that may run at once need one each.
+ * Capturable in a CUDA graph (the number of tokens appended is the one at capture).
+ * Errors: ARG (also a softcap that is negative or not finite), ALIGN, WORKSPACE, CUDA. */
+OOMB_API oomb_status oomb_score_attn_fwd(oomb_pool* pool, const void* q, int64_t q_start, int n_q, const int32_t* sel,
+                                         const int32_t* sel_count, int max_sel, float softmax_scale,
+                                         const oomb_score_mod* mod, void* o, float* lse, void* workspace,
+                                         size_t ws_bytes, void* stream);
+
+/* Backward of oomb_score_attn_fwd (same q, sel, scale and mod; o and lse as it wrote them):
+ * with P = exp(s - LSE), dP = dO V^T, D_i = dO_i . O_i and
+ * dA = P (dP - D) (1 - tanh^2(scale q.k / softcap)),
+ *   dq = scale dA K (written),  dK_pool += scale dA^T Q,  dV_pool += P^T dO
+ * over the G query heads of each KV head.  Masked pairs and rows without keys send nothing;
+ * pages that no row sees are not touched.  dK/dV, their staging (offload_grads) and dq are
+ * as in oomb_chunk_attn_bwd: one writer per pool row in a fixed order (the same bits on
+ * every run), dq summed in fp32 (tensor-core shapes: in no fixed order, so equal to
+ * rounding).  Workspace: oomb_workspace_size(OOMB_OP_SCORE_BWD, n_q) bytes.
+ * Errors: those of oomb_score_attn_fwd. */
+OOMB_API oomb_status oomb_score_attn_bwd(oomb_pool* pool, const void* q, const void* o, const void* d_o,
+                                         const float* lse, int64_t q_start, int n_q, const int32_t* sel,
+                                         const int32_t* sel_count, int max_sel, float softmax_scale,
+                                         const oomb_score_mod* mod, void* dq, void* workspace, size_t ws_bytes,
+                                         void* stream);
+
+/* Key ranges of packed documents for oomb_score_mod, from the documents' boundaries:
+ * doc_start [n_docs + 1] (device, ascending token positions; document c is
+ * [doc_start[c], doc_start[c + 1]), possibly empty).  Row i, at position t = q_start + i in
+ * document c, gets key_begin[i] = doc_start[c] and key_end[i] = t + 1; with prefix_len
+ * ([n_docs], device) every row of document c also sees all of that document's first
+ * prefix_len[c] tokens: key_end[i] = max(t + 1, min(doc_start[c] + prefix_len[c],
+ * doc_start[c + 1])).  A row outside every document gets an empty range.
+ * Errors: ARG, ALIGN (arrays not on 8 bytes), CUDA. */
+OOMB_API oomb_status oomb_doc_spans(const int64_t* doc_start, const int64_t* prefix_len, int n_docs, int64_t q_start,
+                                    int n_q, int64_t* key_begin, int64_t* key_end, void* stream);
+
 /* Offload mode (explainer 2.C "Asynchronous KV Cache CPU Offloading"): copy the
  * selected (page, KV head) blocks of K and V from the pinned host pools into
  * staging buffer `stage_buf` (0 or 1) on `stream` (normally a side stream;
@@ -423,6 +491,54 @@ OOMB_API oomb_status oomb_gemm(int m, int n, int k, int trans_a, int trans_b, co
  * bias not on a multiple of its element size), CUDA. */
 OOMB_API oomb_status oomb_bias_rope(const void* in, int in_dtype, const float* bias, void* out, int out_dtype, int n,
                                     int H, int d, int64_t pos0, float theta, int mode, void* stream);
+
+/* oomb_bias_rope with positions in several axes (time, height, width of images and video):
+ * pair j of token i is turned by the angle
+ *   positions[pair_axis[j] * n + i] * theta^(-e_j)
+ * with e_j = 2j/d (own_ladder = 0: the pairs share one frequency ladder), or, with
+ * own_ladder = 1, e_j = r / c for the r-th (from 0) of the c pairs of its axis.
+ * positions: device int64 [n_axes, n], any sign; pair_axis: host [d/2], entries in
+ * [0, n_axes), read before the call returns; bias, dtypes, in == out and mode as there
+ * (mode 0: bias and cast only, positions and pair_axis not read).  n_axes up to 8.
+ * Angles are reduced to a turn in 64-bit integers, so far positions lose nothing.
+ * Errors: those of oomb_bias_rope, ARG also for a bad axis. */
+OOMB_API oomb_status oomb_bias_rope_axes(const void* in, int in_dtype, const float* bias, void* out, int out_dtype,
+                                         int n, int H, int d, const int64_t* positions, int n_axes,
+                                         const uint8_t* pair_axis, float theta, int own_ladder, int mode,
+                                         void* stream);
+
+/* The norms before and after a block, with the block's gate and residual scale, over rows of
+ * D elements (token-major [n, D], dtype; the residual stream x and the block's output y):
+ *   z = y * r_post * w_post,  r_post = 1 / sqrt(mean(y^2) + eps)   (w_post NULL: z = y)
+ *   x_out = x + res_scale * gate * z                               (y NULL: x_out = x)
+ *   u = x_out * r_pre * w_pre,  r_pre = 1 / sqrt(mean(x_out^2) + eps)   (w_pre NULL: no u)
+ * w_post, w_pre: fp32 [D].  gate: fp32 [D] (gate_rows = 0), [n, D] in dtype (gate_rows = 1),
+ * or NULL (1).  x_out may be NULL when y is (nothing would be added), and may be x.  rstd_post
+ * and rstd_pre ([n] fp32, or NULL) keep r_post and r_pre for the backward.  fp32 arithmetic,
+ * each output rounded once (u is formed from the unrounded x_out).  Other overlaps of outputs
+ * and inputs are not allowed.  Pointers on their element's size; rows of a multiple of 8
+ * elements (16 above 8192) with every pointer on 16 bytes take the fast variant.
+ * Errors: ARG, ALIGN, DTYPE, UNSUPPORTED (D > 16384), CUDA. */
+OOMB_API oomb_status oomb_block_norm_fwd(const void* x, const void* y, const float* w_post, const void* gate,
+                                         int gate_rows, const float* w_pre, float res_scale, float eps, int n, int D,
+                                         int dtype, void* x_out, void* u, float* rstd_post, float* rstd_pre,
+                                         void* stream);
+
+/* Its backward, from the forward's inputs and rstd's: du is the gradient of u (given exactly
+ * when w_pre is), dx_out the gradient that reaches x_out by other ways (NULL: none).
+ * Written: dx and dy ([n, D], dtype; dy NULL: not wanted; dx may be dx_out), and, where not
+ * NULL, the parameter gradients dw_post and dw_pre (fp32 [D]) and dgate (like gate).  Those
+ * summed over the rows (fp32 [D]) are added to what their buffers hold when accumulate is not
+ * 0, as chunk after chunk of a sequence needs it; they are summed in a fixed order, so they
+ * are the same bits on every run.  Workspace: oomb_block_norm_workspace(n, D) bytes, contents
+ * scratch.  Errors: ARG, ALIGN, DTYPE, UNSUPPORTED (D > 16384), WORKSPACE, CUDA. */
+OOMB_API oomb_status oomb_block_norm_bwd(const void* x, const void* y, const float* w_post, const void* gate,
+                                         int gate_rows, const float* w_pre, float res_scale, int n, int D, int dtype,
+                                         const float* rstd_post, const float* rstd_pre, const void* du,
+                                         const void* dx_out, void* dx, void* dy, float* dw_post, void* dgate,
+                                         float* dw_pre, int accumulate, void* workspace, size_t ws_bytes,
+                                         void* stream);
+OOMB_API size_t oomb_block_norm_workspace(int n, int D);
 
 /* dK, dV of tokens [first_token, first_token + n_tokens) read from the paged fp32
  * gradient pool through the page table into token-major [n_tokens, Hkv, d] fp32

@@ -17,7 +17,7 @@ HEADER = os.path.join(os.path.dirname(PKG), "include", "oomb.h")
 
 OOMB_BF16, OOMB_FP32 = 0, 1
 OOMB_CTRL_WORDS = 16  # uint32 words of a pool's control block (error bits + selection barrier state)
-OOMB_OP_SELECT, OOMB_OP_BWD = 0, 1
+OOMB_OP_SELECT, OOMB_OP_BWD, OOMB_OP_SCORE_FWD, OOMB_OP_SCORE_BWD = 0, 1, 2, 3
 STATUS = {0: "OK", 1: "ERR_ARG", 2: "ERR_OUT_OF_PAGES", 3: "ERR_ALIGN", 4: "ERR_DTYPE", 5: "ERR_KERNEL",
           6: "ERR_TIMEOUT", 7: "ERR_CUDA", 8: "ERR_UNSUPPORTED", 9: "ERR_WORKSPACE"}
 
@@ -38,6 +38,10 @@ class PoolDesc(C.Structure):
         ("stage_max_sel", C.c_int), ("offload_grads", C.c_int), ("stage_dk", C.c_void_p),
         ("stage_dv", C.c_void_p), ("grad_state", C.c_void_p),
     ]
+
+
+class ScoreMod(C.Structure):
+    _fields_ = [("softcap", C.c_float), ("slopes", C.c_void_p), ("key_begin", C.c_void_p), ("key_end", C.c_void_p)]
 
 
 _lib: Optional[C.CDLL] = None
@@ -70,11 +74,20 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         "oomb_page_select": (i32, [vp, vp, i64, i32, i32, i32, vp, vp, i32, vp, sz, vp]),
         "oomb_chunk_attn_fwd": (i32, [vp, vp, i64, i32, vp, vp, i32, f32, vp, vp, vp]),
         "oomb_chunk_attn_bwd": (i32, [vp, vp, vp, vp, vp, i64, i32, vp, vp, i32, f32, vp, vp, sz, vp]),
+        "oomb_score_attn_fwd": (i32, [vp, vp, i64, i32, vp, vp, i32, f32, C.POINTER(ScoreMod), vp, vp, vp, sz, vp]),
+        "oomb_score_attn_bwd": (i32, [vp, vp, vp, vp, vp, i64, i32, vp, vp, i32, f32, C.POINTER(ScoreMod), vp, vp, sz,
+                                      vp]),
+        "oomb_doc_spans": (i32, [vp, vp, i32, i64, i32, vp, vp, vp]),
         "oomb_prefetch": (i32, [vp, vp, vp, i32, i32, vp]),
         "oomb_pool_set_stage": (i32, [vp, i32]),
         "oomb_prefetch_pages": (i32, [vp, vp, vp, i32, i32, i64, i64, vp]),
         "oomb_gemm": (i32, [i32, i32, i32, i32, i32, vp, vp, vp, i32, i32, f32, f32, vp, sz, vp]),
         "oomb_bias_rope": (i32, [vp, i32, vp, vp, i32, i32, i32, i32, i64, f32, i32, vp]),
+        "oomb_bias_rope_axes": (i32, [vp, i32, vp, vp, i32, i32, i32, i32, vp, i32, vp, f32, i32, i32, vp]),
+        "oomb_block_norm_fwd": (i32, [vp, vp, vp, vp, i32, vp, f32, f32, i32, i32, i32, vp, vp, vp, vp, vp]),
+        "oomb_block_norm_bwd": (i32, [vp, vp, vp, vp, i32, vp, f32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                      i32, vp, sz, vp]),
+        "oomb_block_norm_workspace": (sz, [i32, i32]),
         "oomb_grad_gather": (i32, [vp, i64, i32, vp, vp, vp]),
         "oomb_grad_prefetch": (i32, [vp, vp, vp, i32, vp, vp, i32, vp]),
         "oomb_grad_carry": (i32, [vp, vp, vp, i32, vp, vp, i32, vp]),
@@ -121,14 +134,42 @@ def _ok(name: str, st: int):
         raise OombError(name, st, detail)
 
 
+# Head layout and dtype of the live pools, by handle: what the tensors of the calls below
+# that take a pool and check their tensors are checked against.
+_pools = {}
+
+
+def _need(func: str, name: str, t, shape=None, dtype=None, optional: bool = False):
+    """Refuses a tensor that a kernel would misread: not on the current CUDA device, not
+    contiguous, of another shape (None: any extent) or dtype.  Returns the tensor."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{func}: {name} is missing")
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{func}: {name} has to be a tensor, not {type(t).__name__}")
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{func}: {name} is on {t.device}, not on the current CUDA device")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{func}: {name} has to be {dtype}, not {t.dtype}")
+    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape))):
+        raise ValueError(f"{func}: {name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{func}: {name} is not contiguous")
+    return t
+
+
 # ---------------------------------------------------------------- entry points
 def oomb_pool_create(desc: PoolDesc) -> int:
     h = C.c_void_p()
     _ok("oomb_pool_create", load().oomb_pool_create(C.byref(desc), C.byref(h)))
+    _pools[h.value] = (desc.n_q_heads, desc.n_kv_heads, desc.head_dim, desc.dtype)
     return h.value
 
 
 def oomb_pool_destroy(pool: int) -> None:
+    _pools.pop(pool, None)
     load().oomb_pool_destroy(pool)
 
 
@@ -197,6 +238,61 @@ def oomb_chunk_attn_bwd(pool: int, q, o, d_o, lse, q_start: int, sel, sel_count,
                                                           _ptr(dq), _ptr(workspace), ws_bytes, _stream(stream)))
 
 
+def _score_call(func: str, pool: int, q, rows, lse, sel, sel_count, workspace, softcap, slopes, key_begin, key_end):
+    """Checks the tensors of a score_attn call; (n_q, ScoreMod, workspace bytes)."""
+    import torch
+    if pool not in _pools:
+        raise ValueError(f"{func}: not a live pool")
+    Hq, Hkv, d, code = _pools[pool]
+    dt = torch.float32 if code == OOMB_FP32 else torch.bfloat16
+    _need(func, "q", q, (None, Hq, d), dt)
+    n = q.shape[0]
+    for name, t in rows.items():
+        _need(func, name, t, (n, Hq, d), dt)
+    _need(func, "lse", lse, (Hq, n), torch.float32)
+    _need(func, "sel", sel, (Hkv, None), torch.int32)
+    _need(func, "sel_count", sel_count, (Hkv,), torch.int32)
+    mod = ScoreMod(softcap, _ptr(_need(func, "slopes", slopes, (Hq,), torch.float32, True)),
+                   _ptr(_need(func, "key_begin", key_begin, (n,), torch.int64, True)),
+                   _ptr(_need(func, "key_end", key_end, (n,), torch.int64, True)))
+    _need(func, "workspace", workspace, optional=True)
+    return n, mod, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def oomb_score_attn_fwd(pool: int, q, q_start: int, sel, sel_count, softmax_scale: float, o, lse, workspace=None,
+                        softcap: float = 0.0, slopes=None, key_begin=None, key_end=None, stream=None) -> None:
+    """oomb_chunk_attn_fwd with capped scores, a distance bias and per-row key ranges."""
+    n, mod, ws_bytes = _score_call("oomb_score_attn_fwd", pool, q, {"o": o}, lse, sel, sel_count, workspace, softcap,
+                                   slopes, key_begin, key_end)
+    _ok("oomb_score_attn_fwd", load().oomb_score_attn_fwd(pool, _ptr(q), q_start, n, _ptr(sel), _ptr(sel_count),
+                                                          sel.shape[-1], softmax_scale, C.byref(mod), _ptr(o),
+                                                          _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def oomb_score_attn_bwd(pool: int, q, o, d_o, lse, q_start: int, sel, sel_count, softmax_scale: float, dq, workspace,
+                        softcap: float = 0.0, slopes=None, key_begin=None, key_end=None, stream=None) -> None:
+    """The backward of oomb_score_attn_fwd: dq written, dK/dV added into the gradient pools."""
+    n, mod, ws_bytes = _score_call("oomb_score_attn_bwd", pool, q, {"o": o, "d_o": d_o, "dq": dq}, lse, sel,
+                                   sel_count, workspace, softcap, slopes, key_begin, key_end)
+    _ok("oomb_score_attn_bwd", load().oomb_score_attn_bwd(pool, _ptr(q), _ptr(o), _ptr(d_o), _ptr(lse), q_start, n,
+                                                          _ptr(sel), _ptr(sel_count), sel.shape[-1], softmax_scale,
+                                                          C.byref(mod), _ptr(dq), _ptr(workspace), ws_bytes,
+                                                          _stream(stream)))
+
+
+def oomb_doc_spans(doc_start, q_start: int, key_begin, key_end, prefix_len=None, stream=None) -> None:
+    """Key ranges of packed documents (boundaries doc_start [n_docs + 1], optional prefix_len [n_docs])."""
+    import torch
+    f = "oomb_doc_spans"
+    _need(f, "doc_start", doc_start, (None,), torch.int64)
+    n_docs = doc_start.shape[0] - 1
+    _need(f, "prefix_len", prefix_len, (n_docs,), torch.int64, True)
+    _need(f, "key_begin", key_begin, (None,), torch.int64)
+    _need(f, "key_end", key_end, (key_begin.shape[0],), torch.int64)
+    _ok(f, load().oomb_doc_spans(_ptr(doc_start), _ptr(prefix_len), n_docs, q_start, key_begin.shape[0],
+                                 _ptr(key_begin), _ptr(key_end), _stream(stream)))
+
+
 def oomb_prefetch(pool: int, sel, sel_count, stage_buf: int, stream=None) -> None:
     _ok("oomb_prefetch", load().oomb_prefetch(pool, _ptr(sel), _ptr(sel_count), sel.shape[-1], stage_buf,
                                               _stream(stream)))
@@ -228,6 +324,85 @@ def oomb_bias_rope(x_in, bias, x_out, n_heads: int, pos0: int, theta: float, mod
     _ok("oomb_bias_rope", load().oomb_bias_rope(_ptr(x_in), _dtype_code(x_in), _ptr(bias), _ptr(x_out),
                                                 _dtype_code(x_out), n, n_heads, d, pos0, theta, mode,
                                                 _stream(stream)))
+
+
+def oomb_bias_rope_axes(x_in, bias, x_out, n_heads: int, positions, pair_axis, theta: float, mode: int,
+                        own_ladder: bool = False, stream=None) -> None:
+    """oomb_bias_rope with positions [n_axes, n] (int64); pair_axis[j] is the axis of pair j (d/2 entries)."""
+    import torch
+    f = "oomb_bias_rope_axes"
+    _need(f, "x_in", x_in)
+    _need(f, "x_out", x_out)
+    n = x_in.shape[0] if x_in.dim() else 0
+    if n <= 0 or n_heads <= 0 or x_in.numel() % (n * n_heads) or x_out.numel() != x_in.numel():
+        raise ValueError(f"{f}: x_in {tuple(x_in.shape)} and x_out {tuple(x_out.shape)} do not hold rows of "
+                         f"{n_heads} heads")
+    d = x_in.numel() // (n * n_heads)
+    _need(f, "bias", None if bias is None else bias.view(-1), (n_heads * d,), torch.float32, True)
+    axes, n_axes = None, 0
+    if mode != 0:
+        axes = bytes(pair_axis)
+        if 2 * len(axes) != d:
+            raise ValueError(f"{f}: pair_axis has {len(axes)} entries, needs {d // 2}")
+        _need(f, "positions", positions, (None, n), torch.int64)
+        n_axes = positions.shape[0]
+    _ok(f, load().oomb_bias_rope_axes(_ptr(x_in), _dtype_code(x_in), _ptr(bias), _ptr(x_out), _dtype_code(x_out), n,
+                                      n_heads, d, _ptr(positions) if mode != 0 else None, n_axes, axes, theta,
+                                      int(own_ladder), mode, _stream(stream)))
+
+
+def _norm_call(f: str, x, y, w_pre, w_post, gate):
+    """Checks the inputs common to both directions; (n, D, dtype, gate_rows)."""
+    import torch
+    _need(f, "x", x, (None, None))
+    n, D = x.shape
+    _need(f, "y", y, (n, D), x.dtype, True)
+    _need(f, "w_pre", w_pre, (D,), torch.float32, True)
+    _need(f, "w_post", w_post, (D,), torch.float32, True)
+    rows = gate is not None and gate.dim() == 2
+    _need(f, "gate", gate, (n, D) if rows else (D,), x.dtype if rows else torch.float32, True)
+    return n, D, x.dtype, int(rows)
+
+
+def oomb_block_norm_fwd(x, y, x_out, u=None, w_pre=None, w_post=None, gate=None, res_scale: float = 1.0,
+                        eps: float = 1e-6, rstd_pre=None, rstd_post=None, stream=None) -> None:
+    """x_out = x + res_scale * gate * norm(y; w_post), u = norm(x_out; w_pre).  gate: fp32 [D] or [n, D] like x."""
+    import torch
+    f = "oomb_block_norm_fwd"
+    n, D, dt, rows = _norm_call(f, x, y, w_pre, w_post, gate)
+    _need(f, "x_out", x_out, (n, D), dt, True)
+    _need(f, "u", u, (n, D), dt, True)
+    _need(f, "rstd_pre", rstd_pre, (n,), torch.float32, True)
+    _need(f, "rstd_post", rstd_post, (n,), torch.float32, True)
+    _ok(f, load().oomb_block_norm_fwd(_ptr(x), _ptr(y), _ptr(w_post), _ptr(gate), rows, _ptr(w_pre), res_scale, eps,
+                                      n, D, _dtype_code(x), _ptr(x_out), _ptr(u), _ptr(rstd_post), _ptr(rstd_pre),
+                                      _stream(stream)))
+
+
+def oomb_block_norm_bwd(x, y, dx, dy=None, du=None, dx_out=None, rstd_pre=None, rstd_post=None, w_pre=None,
+                        w_post=None, gate=None, dw_pre=None, dw_post=None, dgate=None, res_scale: float = 1.0,
+                        accumulate: bool = False, workspace=None, stream=None) -> None:
+    """The backward of oomb_block_norm_fwd; accumulate adds the parameter gradients to their buffers."""
+    import torch
+    f = "oomb_block_norm_bwd"
+    n, D, dt, rows = _norm_call(f, x, y, w_pre, w_post, gate)
+    for name, t in (("dx", dx), ("dy", dy), ("du", du), ("dx_out", dx_out)):
+        _need(f, name, t, (n, D), dt, name != "dx")
+    for name, t in (("rstd_pre", rstd_pre), ("rstd_post", rstd_post)):
+        _need(f, name, t, (n,), torch.float32, True)
+    for name, t in (("dw_pre", dw_pre), ("dw_post", dw_post)):
+        _need(f, name, t, (D,), torch.float32, True)
+    _need(f, "dgate", dgate, (n, D) if rows else (D,), dt if rows else torch.float32, True)
+    _need(f, "workspace", workspace)
+    _ok(f, load().oomb_block_norm_bwd(_ptr(x), _ptr(y), _ptr(w_post), _ptr(gate), rows, _ptr(w_pre), res_scale, n, D,
+                                      _dtype_code(x), _ptr(rstd_post), _ptr(rstd_pre), _ptr(du), _ptr(dx_out),
+                                      _ptr(dx), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre), int(accumulate),
+                                      _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                      _stream(stream)))
+
+
+def oomb_block_norm_workspace(n: int, D: int) -> int:
+    return int(load().oomb_block_norm_workspace(n, D))
 
 
 def oomb_grad_gather(pool: int, first_token: int, dk, dv, stream=None) -> None:

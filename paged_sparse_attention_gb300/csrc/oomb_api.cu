@@ -2,11 +2,13 @@
 // dispatch to the kernels.  No call here allocates device memory.
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <cstring>
 #include <new>
 
 #include "append_unit.cuh"
 #include "oomb_internal.h"
+#include "score_common.cuh"
 
 using namespace oomb;
 
@@ -51,17 +53,17 @@ int oomb::device_sm_count() {
   return count[dev];
 }
 
-namespace {
+static thread_local const char* t_last_cuda_error = "";
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-thread_local const char* t_last_cuda_error = "";
-
-oomb_status cuda_status(cudaError_t e) {
+oomb_status oomb::cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return OOMB_OK;
   t_last_cuda_error = cudaGetErrorString(e);
   return OOMB_ERR_CUDA;
 }
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 Geometry geometry_of(const oomb_pool_desc& d) {
   Geometry g;
@@ -341,6 +343,8 @@ size_t oomb_workspace_size(const oomb_pool* p, int op, int n_q) {
   if (!p || n_q <= 0) return 0;
   if (op == OOMB_OP_SELECT) return select_workspace_bytes(p->g, n_q);
   if (op == OOMB_OP_BWD) return bwd_workspace_bytes(p->g, n_q);
+  if (op == OOMB_OP_SCORE_FWD) return score_fwd_workspace_bytes(p->g, n_q);
+  if (op == OOMB_OP_SCORE_BWD) return score_bwd_workspace_bytes(p->g, n_q);
   return 0;
 }
 
@@ -530,6 +534,77 @@ oomb_status oomb_chunk_attn_bwd(oomb_pool* p, const void* q, const void* o, cons
   cudaError_t e = tc_supported(p->g) ? launch_attn_bwd_tc(a, (cudaStream_t)stream)
                                      : launch_attn_bwd_simt(a, (cudaStream_t)stream);
   return cuda_status(e);
+}
+
+// Checks and arguments shared by oomb_score_attn_fwd and oomb_score_attn_bwd.
+static oomb_status make_score_args(oomb_pool* p, const void* q, int64_t q_start, int n_q, const int32_t* sel,
+                                   const int32_t* sel_count, int max_sel, float scale, const oomb_score_mod* mod,
+                                   void* ws, size_t ws_bytes, size_t need, ScoreArgs* s) {
+  if (!p || !q || !sel || !sel_count) return OOMB_ERR_ARG;
+  if (n_q <= 0 || q_start < 0 || max_sel <= 0) return OOMB_ERR_ARG;
+  if (q_start > p->n_tokens || n_q > p->n_tokens - q_start) return OOMB_ERR_ARG;  // own K/V appended
+  if (!aligned(q, 16) || !aligned(sel, 4) || !aligned(sel_count, 4)) return OOMB_ERR_ALIGN;
+  if (p->d.offload && max_sel > p->d.stage_max_sel) return OOMB_ERR_ARG;
+  if (need > 0 && (!ws || ws_bytes < need)) return OOMB_ERR_WORKSPACE;
+  if (ws && !aligned(ws, 16)) return OOMB_ERR_ALIGN;
+  std::memset(s, 0, sizeof(*s));
+  s->a = make_args(p, q, q_start, n_q, sel, sel_count, max_sel, scale);
+  s->a.ws = ws;
+  s->a.ws_bytes = ws_bytes;
+  s->total = p->n_tokens;
+  s->n_split = 1;
+  if (mod) {
+    if (!(mod->softcap >= 0.f) || std::isinf(mod->softcap)) return OOMB_ERR_ARG;
+    if (!aligned(mod->slopes, 4) || !aligned(mod->key_begin, 8) || !aligned(mod->key_end, 8)) return OOMB_ERR_ALIGN;
+    s->cap = mod->softcap;
+    s->slopes = mod->slopes;
+    s->begin = mod->key_begin;
+    s->end = mod->key_end;
+  }
+  const int64_t view = s->end ? p->n_tokens : q_start + n_q;
+  s->n_view = (int)((view + p->g.P - 1) / p->g.P);
+  return OOMB_OK;
+}
+
+oomb_status oomb_score_attn_fwd(oomb_pool* p, const void* q, int64_t q_start, int n_q, const int32_t* sel,
+                                const int32_t* sel_count, int max_sel, float scale, const oomb_score_mod* mod,
+                                void* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (!p || n_q <= 0 || !o || !lse) return OOMB_ERR_ARG;
+  ScoreArgs a;
+  oomb_status s = make_score_args(p, q, q_start, n_q, sel, sel_count, max_sel, scale, mod, ws, ws_bytes,
+                                  score_fwd_workspace_bytes(p->g, n_q), &a);
+  if (s != OOMB_OK) return s;
+  if (!aligned(o, 16) || !aligned(lse, 4)) return OOMB_ERR_ALIGN;
+  a.a.o_out = o;
+  a.a.lse_out = lse;
+  return cuda_status(launch_score_fwd(a, (cudaStream_t)stream));
+}
+
+oomb_status oomb_score_attn_bwd(oomb_pool* p, const void* q, const void* o, const void* d_o, const float* lse,
+                                int64_t q_start, int n_q, const int32_t* sel, const int32_t* sel_count, int max_sel,
+                                float scale, const oomb_score_mod* mod, void* dq, void* ws, size_t ws_bytes,
+                                void* stream) {
+  if (!p || n_q <= 0 || !o || !d_o || !lse || !dq) return OOMB_ERR_ARG;
+  ScoreArgs a;
+  oomb_status s = make_score_args(p, q, q_start, n_q, sel, sel_count, max_sel, scale, mod, ws, ws_bytes,
+                                  score_bwd_workspace_bytes(p->g, n_q), &a);
+  if (s != OOMB_OK) return s;
+  if (!aligned(o, 16) || !aligned(d_o, 16) || !aligned(dq, 16) || !aligned(lse, 4)) return OOMB_ERR_ALIGN;
+  a.a.o = o;
+  a.a.dout = d_o;
+  a.a.lse_in = lse;
+  a.a.dq = dq;
+  return cuda_status(launch_score_bwd(a, (cudaStream_t)stream));
+}
+
+oomb_status oomb_doc_spans(const int64_t* doc_start, const int64_t* prefix_len, int n_docs, int64_t q_start, int n_q,
+                           int64_t* key_begin, int64_t* key_end, void* stream) {
+  if (!doc_start || !key_begin || !key_end || n_docs <= 0 || n_q <= 0 || q_start < 0) return OOMB_ERR_ARG;
+  if (n_docs == INT_MAX) return OOMB_ERR_ARG;
+  if (!aligned(doc_start, 8) || !aligned(prefix_len, 8) || !aligned(key_begin, 8) || !aligned(key_end, 8))
+    return OOMB_ERR_ALIGN;
+  return cuda_status(launch_doc_spans(doc_start, prefix_len, n_docs, q_start, n_q, key_begin, key_end,
+                                      (cudaStream_t)stream));
 }
 
 oomb_status oomb_prefetch_pages(oomb_pool* p, const int32_t* sel, const int32_t* sel_count, int max_sel,

@@ -120,6 +120,8 @@ cudaError_t launch_grad_gather(const Geometry& g, const float* dk_pool, const fl
 __host__ __device__ inline size_t dtype_size(int dt) { return dt == OOMB_FP32 ? 4 : 2; }
 // Count of kernel launches issued by the library (reported by oomb_launch_count).
 void count_launches(int n);
+// OOMB_OK, or OOMB_ERR_CUDA with the text kept for oomb_last_cuda_error.
+oomb_status cuda_status(cudaError_t e);
 
 // Per-device host caches (CUDA function attributes and device properties are per device).
 constexpr int kMaxDevices = 64;

@@ -1,0 +1,645 @@
+// Chunk attention with capped scores, a distance bias and per-row key ranges on the CUDA
+// cores in fp32, for fp32 pools and for the bf16 shapes the tensor-core kernels do not
+// take; also the join of split forwards and the document ranges.
+//
+// Tiles of 64 query rows x 64 keys, 256 threads, a 4 x 4 block of scores per thread: each
+// 16-byte read of shared memory feeds 8 multiply-adds, so the kernels are bound by the
+// FMA pipe and not by shared memory.  The keys of a tile are 64 consecutive tokens of the
+// selected pages written one after another, so a page may be of any size: a tile can hold
+// several small pages or a part of a large one.  Rows whose range is empty, or meets no
+// selected page, get O = 0 and LSE = -inf and send no gradient.
+//
+//   score_fwd_simt   a block per (64 rows, query head, share of the keys); running maximum
+//                    and sum, O in registers
+//   score_join       the shares of a split forward joined by their log-sum-exps
+//   score_dot        D_i = dO_i . O_i
+//   score_dq_simt    a block per (64 rows, query head): dQ
+//   score_dkdv_simt  a block per (64 keys of the selection, KV head): dK and dV of those
+//                    keys over all query heads of the group and all rows, added once into
+//                    the pool rows, which no other block touches (same bits on every run)
+#include <cmath>
+
+#include "score_common.cuh"
+
+namespace oomb {
+namespace {
+
+constexpr int kRows = 64;   // query rows of a tile
+constexpr int kKeys = 64;   // keys of a tile
+constexpr int kThreads = 256;
+constexpr int kMaxD = 128;
+constexpr int kC = kMaxD / 64;  // float4 columns per thread: columns 4 tx + 64 c
+constexpr int kLdP = kKeys + 4;
+
+// fp32 tiles in shared memory: row length d padded to a multiple of 4 plus 4, so that rows
+// start on 16 bytes and 8 rows one apart fall into different banks.
+__host__ __device__ constexpr int tile_ld(int d) { return d + 4; }
+
+struct KeyList {
+  int64_t pos[kKeys];  // token position, -1: no key
+  int64_t off[kKeys];  // element offset of the row in the pools, -1: no key
+};
+
+// Keys v0 .. v0 + 63 of the selection's token sequence (entry v / P, token v % P); a key
+// outside positions [lo, hi) is left out, so whatever stands there (a NaN, say) stays there.
+__device__ __forceinline__ void list_keys(const ScoreArgs& s, int h, int64_t v0, int64_t v1, int64_t lo, int64_t hi,
+                                          KeyList* kl) {
+  const int P = s.a.g.P;
+  if (threadIdx.x < kKeys) {
+    const int64_t v = v0 + threadIdx.x;
+    int64_t pos = -1, off = -1;
+    if (v < v1) {
+      const int j = (int)(v / P), t = (int)(v % P);
+      const int p = s.a.sel[(size_t)h * s.a.max_sel + j];
+      const int64_t blk = score_block(s, h, j, p), at = (int64_t)p * P + t;
+      if (blk >= 0 && at >= lo && at < hi) {
+        pos = at;
+        off = (blk * P + t) * s.a.g.d;
+      }
+    }
+    kl->pos[threadIdx.x] = pos;
+    kl->off[threadIdx.x] = off;
+  }
+}
+
+// K (and V) rows of the listed keys as fp32; absent keys are zero.
+template <typename T>
+__device__ __forceinline__ void load_keys(const ScoreArgs& s, const KeyList* kl, float* sk, float* sv) {
+  const int d = s.a.g.d, ld = tile_ld(d);
+  const T* k = reinterpret_cast<const T*>(s.a.kv.k);
+  const T* v = reinterpret_cast<const T*>(s.a.kv.v);
+  for (int idx = threadIdx.x; idx < kKeys * d; idx += kThreads) {
+    const int r = idx / d, e = idx % d;
+    const int64_t off = kl->off[r];
+    sk[r * ld + e] = off >= 0 ? to_float<T>(k[off + e]) : 0.f;
+    sv[r * ld + e] = off >= 0 ? to_float<T>(v[off + e]) : 0.f;
+  }
+}
+
+// Rows i0 .. i0 + 63 of head hq of a token-major tensor as fp32; rows past n_q are zero.
+template <typename T>
+__device__ __forceinline__ void load_rows(const ScoreArgs& s, const void* src, int i0, int hq, float* dst) {
+  const int d = s.a.g.d, ld = tile_ld(d);
+  const T* x = reinterpret_cast<const T*>(src);
+  for (int idx = threadIdx.x; idx < kRows * d; idx += kThreads) {
+    const int r = idx / d, e = idx % d, i = i0 + r;
+    dst[r * ld + e] = i < s.a.n_q ? to_float<T>(x[((size_t)i * s.a.g.Hq + hq) * d + e]) : 0.f;
+  }
+}
+
+// acc[r][c] = A[ty + 16 r] . B[tx + 16 c] over d columns (d is a multiple of 4).
+__device__ __forceinline__ void dot_tile(const float* A, const float* B, int d, int ty, int tx, float (&acc)[4][4]) {
+  const int ld = tile_ld(d);
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
+  for (int e = 0; e < d; e += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = *reinterpret_cast<const float4*>(A + (ty + 16 * r) * ld + e);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const float4*>(B + (tx + 16 * c) * ld + e);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        acc[r][c] += x[r].x * y[c].x + x[r].y * y[c].y + x[r].z * y[c].z + x[r].w * y[c].w;
+  }
+}
+
+// acc[r][c] (columns 4 tx + 64 c) += sum_j W[ty + 16 r][j] X[j], j over 64 rows of X.
+__device__ __forceinline__ void weigh_rows(const float* W, const float* X, int d, int ty, int tx,
+                                           float4 (&acc)[4][kC]) {
+  const int ld = tile_ld(d);
+  for (int j = 0; j < 64; j += 4) {
+    float4 w[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) w[r] = *reinterpret_cast<const float4*>(W + (ty + 16 * r) * kLdP + j);
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      const int col = 4 * tx + 64 * c;
+      if (col >= d) continue;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float4 x = *reinterpret_cast<const float4*>(X + (j + u) * ld + col);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float p = u == 0 ? w[r].x : u == 1 ? w[r].y : u == 2 ? w[r].z : w[r].w;
+          acc[r][c].x += p * x.x;
+          acc[r][c].y += p * x.y;
+          acc[r][c].z += p * x.z;
+          acc[r][c].w += p * x.w;
+        }
+      }
+    }
+  }
+}
+
+// Modified score of raw dot product `dot`, and tanh of the capped argument in *t (0 uncapped).
+__device__ __forceinline__ float modify(float dot, float scale, float cap, float slope, int64_t qpos, int64_t kpos,
+                                        float* t) {
+  float x = dot * scale;
+  *t = 0.f;
+  if (cap > 0.f) {
+    *t = tanhf(x / cap);
+    x = cap * *t;
+  }
+  if (slope != 0.f) {
+    const int64_t dist = qpos > kpos ? qpos - kpos : kpos - qpos;
+    x -= slope * (float)dist;
+  }
+  return x;
+}
+
+// Ranges of the tile's rows in shared memory and the union [lo, hi) of the non-empty ones.
+struct RowSpans {
+  int64_t b[kRows], e[kRows];
+  int64_t lo, hi;
+};
+__device__ __forceinline__ void load_spans(const ScoreArgs& s, int i0, RowSpans* rs) {
+  if (threadIdx.x < kRows) {
+    int64_t b = 0, e = 0;
+    if (i0 + (int)threadIdx.x < s.a.n_q) row_span(s, i0 + threadIdx.x, b, e);
+    rs->b[threadIdx.x] = b;
+    rs->e[threadIdx.x] = e;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int64_t lo = INT64_MAX, hi = 0;
+    for (int r = threadIdx.x; r < kRows; r += 32)
+      if (rs->e[r] > rs->b[r]) {
+        lo = min(lo, rs->b[r]);
+        hi = max(hi, rs->e[r]);
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    if (threadIdx.x == 0) {
+      rs->lo = hi > 0 ? lo : 0;
+      rs->hi = hi;
+    }
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------------ forward
+size_t fwd_smem(int d) { return (size_t)(3 * kKeys * tile_ld(d) + kRows * kLdP) * 4; }
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) score_fwd_simt(const ScoreArgs s) {
+  const int d = s.a.g.d, P = s.a.g.P, ld = tile_ld(d);
+  const int hq = blockIdx.y, h = hq / s.a.g.G, i0 = blockIdx.x * kRows;
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  extern __shared__ __align__(16) float dyn[];
+  float* sq = dyn;
+  float* sk = sq + kRows * ld;
+  float* sv = sk + kKeys * ld;
+  float* sp = sv + kKeys * ld;
+  __shared__ KeyList kl;
+  __shared__ RowSpans rs;
+  if (blockIdx.x == 0 && blockIdx.z == 0 && hq % s.a.g.G == 0) check_selection(s, h, threadIdx.x, kThreads);
+  const int count = sel_count_checked(s.a, h);
+  load_spans(s, i0, &rs);
+  load_rows<T>(s, s.a.q, i0, hq, sq);
+  // entries the tile can see, and this block's share of their tokens (whole key tiles)
+  const int j0 = first_entry(s.a, h, count, rs.lo / P);
+  const int j1 = rs.hi > rs.lo ? first_entry(s.a, h, count, (rs.hi + P - 1) / P) : j0;
+  const int64_t n_tiles = ((int64_t)(j1 - j0) * P + kKeys - 1) / kKeys;
+  const int64_t t0 = n_tiles * blockIdx.z / s.n_split, t1 = n_tiles * (blockIdx.z + 1) / s.n_split;
+  const int64_t v_end = (int64_t)j1 * P;
+  const float slope = s.slopes ? s.slopes[hq] : 0.f;
+
+  float m[4], l[4];
+  float4 o[4][kC];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int64_t t = t0; t < t1; ++t) {
+    __syncthreads();
+    list_keys(s, h, (int64_t)j0 * P + t * kKeys, v_end, rs.lo, rs.hi, &kl);
+    __syncthreads();
+    load_keys<T>(s, &kl, sk, sv);
+    __syncthreads();
+    float x[4][4];
+    dot_tile(sq, sk, d, ty, tx, x);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = ty + 16 * r;
+      const int64_t b = rs.b[row], e = rs.e[row], qpos = s.a.q_start + i0 + row;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int64_t kpos = kl.pos[tx + 16 * c];
+        float th;
+        const bool see = kpos >= b && kpos < e;  // an absent key has position -1
+        x[r][c] = see ? modify(x[r][c], s.a.scale, s.cap, slope, qpos, kpos, &th) : -INFINITY;
+        mx = fmaxf(mx, x[r][c]);
+      }
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      const float m_new = fmaxf(m[r], mx);
+      const float shift = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = expf(m[r] - shift);  // 0 while the row has seen nothing
+      float sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float p = expf(x[r][c] - shift);
+        sp[row * kLdP + tx + 16 * c] = p;
+        sum += p;
+      }
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      l[r] = l[r] * alpha + sum;
+      m[r] = m_new;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        o[r][c].x *= alpha;
+        o[r][c].y *= alpha;
+        o[r][c].z *= alpha;
+        o[r][c].w *= alpha;
+      }
+    }
+    __syncthreads();
+    weigh_rows(sp, sv, d, ty, tx, o);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int i = i0 + ty + 16 * r;
+    if (i >= s.a.n_q) continue;
+    const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
+    const float lse = l[r] > 0.f ? m[r] + logf(l[r]) : -INFINITY;
+    const size_t rh = (size_t)i * s.a.g.Hq + hq;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      const int col = 4 * tx + 64 * c;
+      if (col >= d) continue;
+      const float v[4] = {o[r][c].x * inv, o[r][c].y * inv, o[r][c].z * inv, o[r][c].w * inv};
+      if (s.n_split > 1) {
+        float* dst = s.part_o + ((size_t)blockIdx.z * s.a.n_q * s.a.g.Hq + rh) * d + col;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[e] = v[e];
+      } else {
+        T* dst = reinterpret_cast<T*>(s.a.o_out) + rh * d + col;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[e] = from_float<T>(v[e]);
+      }
+    }
+    if (tx == 0) {
+      if (s.n_split > 1)
+        s.part_lse[(size_t)blockIdx.z * s.a.n_q * s.a.g.Hq + rh] = lse;
+      else
+        s.a.lse_out[(size_t)hq * s.a.n_q + i] = lse;
+    }
+  }
+}
+
+// One warp per (row, head): O = sum_z w_z O_z / sum_z w_z with w_z = exp(LSE_z - max LSE).
+template <typename T>
+__global__ void __launch_bounds__(256) score_join(const ScoreArgs s) {
+  const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32;
+  const int lane = threadIdx.x % 32, Hq = s.a.g.Hq, d = s.a.g.d;
+  const int64_t rows = (int64_t)s.a.n_q * Hq;
+  if (w >= rows) return;
+  float m = -INFINITY;
+  for (int z = lane; z < s.n_split; z += 32) m = fmaxf(m, s.part_lse[z * rows + w]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  const float shift = m == -INFINITY ? 0.f : m;
+  float acc[kMaxD / 32] = {}, den = 0.f;
+  for (int z = 0; z < s.n_split; ++z) {
+    const float lz = s.part_lse[z * rows + w];
+    if (lz == -INFINITY) continue;  // nothing visible in this share
+    const float wz = expf(lz - shift);
+    den += wz;
+    const float* src = s.part_o + (z * rows + w) * d;
+#pragma unroll
+    for (int c = 0; c < kMaxD / 32; ++c)
+      if (lane + 32 * c < d) acc[c] += wz * src[lane + 32 * c];
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  T* dst = reinterpret_cast<T*>(s.a.o_out) + w * d;
+#pragma unroll
+  for (int c = 0; c < kMaxD / 32; ++c)
+    if (lane + 32 * c < d) dst[lane + 32 * c] = from_float<T>(acc[c] * inv);
+  if (lane == 0) s.a.lse_out[(size_t)(w % Hq) * s.a.n_q + w / Hq] = den > 0.f ? m + logf(den) : m;
+}
+
+// ----------------------------------------------------------------- backward
+template <typename T>
+__global__ void __launch_bounds__(256) score_dot(const ScoreArgs s, float* __restrict__ Dbuf) {
+  const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32;
+  const int lane = threadIdx.x % 32, Hq = s.a.g.Hq, d = s.a.g.d;
+  if (w >= (int64_t)s.a.n_q * Hq) return;
+  const T* o = reinterpret_cast<const T*>(s.a.o) + w * d;
+  const T* dout = reinterpret_cast<const T*>(s.a.dout) + w * d;
+  float acc = 0.f;
+  for (int e = lane; e < d; e += 32) acc += to_float<T>(o[e]) * to_float<T>(dout[e]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+  if (lane == 0) Dbuf[(size_t)(w % Hq) * s.a.n_q + w / Hq] = acc;
+}
+
+// P and dA of a thread's 4 x 4 block into shared memory, laid out [row][key] or, for the
+// dK/dV kernel, [key][row].
+template <bool KEY_MAJOR>
+__device__ __forceinline__ void probs_tile(const ScoreArgs& s, const float (&x)[4][4], const float (&dp)[4][4],
+                                           const RowSpans* rs, const KeyList* kl, const float* slse, const float* sD,
+                                           float slope, int i0, int ty, int tx, float* sp, float* sda) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = ty + 16 * r;
+    const int64_t b = rs->b[row], e = rs->e[row], qpos = s.a.q_start + i0 + row;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int key = tx + 16 * c;
+      const int64_t kpos = kl->pos[key];
+      float p = 0.f, da = 0.f;
+      if (kpos >= b && kpos < e && slse[row] > -INFINITY) {
+        float t;
+        p = expf(modify(x[r][c], s.a.scale, s.cap, slope, qpos, kpos, &t) - slse[row]);
+        da = p * (dp[r][c] - sD[row]) * (1.f - t * t);
+      }
+      const int at = KEY_MAJOR ? key * kLdP + row : row * kLdP + key;
+      if (sp) sp[at] = p;
+      sda[at] = da;
+    }
+  }
+}
+
+__device__ __forceinline__ void load_stats(const ScoreArgs& s, const float* Dbuf, int i0, int hq, float* slse,
+                                           float* sD) {
+  if (threadIdx.x < kRows) {
+    const int i = i0 + threadIdx.x;
+    slse[threadIdx.x] = i < s.a.n_q ? s.a.lse_in[(size_t)hq * s.a.n_q + i] : -INFINITY;
+    sD[threadIdx.x] = i < s.a.n_q ? Dbuf[(size_t)hq * s.a.n_q + i] : 0.f;
+  }
+}
+
+size_t dq_smem(int d) { return (size_t)(4 * kKeys * tile_ld(d) + kRows * kLdP) * 4; }
+size_t dkdv_smem(int d) { return (size_t)(4 * kKeys * tile_ld(d) + 2 * kRows * kLdP) * 4; }
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) score_dq_simt(const ScoreArgs s, const float* __restrict__ Dbuf) {
+  const int d = s.a.g.d, P = s.a.g.P, ld = tile_ld(d);
+  const int hq = blockIdx.y, h = hq / s.a.g.G, i0 = blockIdx.x * kRows;
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  extern __shared__ __align__(16) float dyn[];
+  float* sq = dyn;
+  float* sdo = sq + kRows * ld;
+  float* sk = sdo + kRows * ld;
+  float* sv = sk + kKeys * ld;
+  float* sda = sv + kKeys * ld;
+  __shared__ KeyList kl;
+  __shared__ RowSpans rs;
+  __shared__ float slse[kRows], sD[kRows];
+  if (blockIdx.x == 0 && hq % s.a.g.G == 0) check_selection(s, h, threadIdx.x, kThreads);
+  const int count = sel_count_checked(s.a, h);
+  load_spans(s, i0, &rs);
+  load_rows<T>(s, s.a.q, i0, hq, sq);
+  load_rows<T>(s, s.a.dout, i0, hq, sdo);
+  load_stats(s, Dbuf, i0, hq, slse, sD);
+  const int j0 = first_entry(s.a, h, count, rs.lo / P);
+  const int j1 = rs.hi > rs.lo ? first_entry(s.a, h, count, (rs.hi + P - 1) / P) : j0;
+  const float slope = s.slopes ? s.slopes[hq] : 0.f;
+  float4 dq[4][kC];
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < kC; ++c) dq[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int64_t v = (int64_t)j0 * P; v < (int64_t)j1 * P; v += kKeys) {
+    __syncthreads();
+    list_keys(s, h, v, (int64_t)j1 * P, rs.lo, rs.hi, &kl);
+    __syncthreads();
+    load_keys<T>(s, &kl, sk, sv);
+    __syncthreads();
+    float x[4][4], dp[4][4];
+    dot_tile(sq, sk, d, ty, tx, x);
+    dot_tile(sdo, sv, d, ty, tx, dp);
+    probs_tile<false>(s, x, dp, &rs, &kl, slse, sD, slope, i0, ty, tx, nullptr, sda);
+    __syncthreads();
+    weigh_rows(sda, sk, d, ty, tx, dq);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int i = i0 + ty + 16 * r;
+    if (i >= s.a.n_q) continue;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      const int col = 4 * tx + 64 * c;
+      if (col >= d) continue;
+      T* dst = reinterpret_cast<T*>(s.a.dq) + ((size_t)i * s.a.g.Hq + hq) * d + col;
+      dst[0] = from_float<T>(dq[r][c].x * s.a.scale);
+      dst[1] = from_float<T>(dq[r][c].y * s.a.scale);
+      dst[2] = from_float<T>(dq[r][c].z * s.a.scale);
+      dst[3] = from_float<T>(dq[r][c].w * s.a.scale);
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) score_dkdv_simt(const ScoreArgs s, const float* __restrict__ Dbuf) {
+  const int d = s.a.g.d, P = s.a.g.P, G = s.a.g.G, ld = tile_ld(d);
+  const int h = blockIdx.y;
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  extern __shared__ __align__(16) float dyn[];
+  float* sq = dyn;
+  float* sdo = sq + kRows * ld;
+  float* sk = sdo + kRows * ld;
+  float* sv = sk + kKeys * ld;
+  float* sp = sv + kKeys * ld;
+  float* sda = sp + kRows * kLdP;
+  __shared__ KeyList kl;
+  __shared__ RowSpans rs;
+  __shared__ float slse[kRows], sD[kRows];
+  __shared__ int64_t key_lo, key_hi;
+  const int count = sel_count_checked(s.a, h);
+  const int64_t v0 = (int64_t)blockIdx.x * kKeys, v1 = (int64_t)count * P;
+  if (v0 >= v1) return;
+  list_keys(s, h, v0, v1, 0, s.total, &kl);
+  // an entry out of order may name a page that another block owns: leave it out
+  if (threadIdx.x < kKeys && kl.pos[threadIdx.x] >= 0) {
+    const int j = (int)((v0 + threadIdx.x) / P);
+    const int32_t* row = s.a.sel + (size_t)h * s.a.max_sel;
+    if ((j > 0 && row[j - 1] >= row[j]) || (j + 1 < count && row[j + 1] <= row[j]))
+      kl.pos[threadIdx.x] = kl.off[threadIdx.x] = -1;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int64_t lo = INT64_MAX, hi = -1;
+    for (int r = 0; r < kKeys; ++r)
+      if (kl.pos[r] >= 0) {
+        lo = min(lo, kl.pos[r]);
+        hi = max(hi, kl.pos[r]);
+      }
+    key_lo = lo;
+    key_hi = hi;
+  }
+  load_keys<T>(s, &kl, sk, sv);
+  __syncthreads();
+  if (key_hi < 0) return;
+  float4 dk[4][kC], dv[4][kC];
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < kC; ++c) dk[r][c] = dv[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < s.a.n_q; i0 += kRows) {
+    __syncthreads();
+    load_spans(s, i0, &rs);
+    if (rs.hi <= key_lo || rs.lo > key_hi) continue;  // no row of the tile sees these keys
+    for (int gq = 0; gq < G; ++gq) {
+      const int hq = h * G + gq;
+      __syncthreads();
+      load_rows<T>(s, s.a.q, i0, hq, sq);
+      load_rows<T>(s, s.a.dout, i0, hq, sdo);
+      load_stats(s, Dbuf, i0, hq, slse, sD);
+      __syncthreads();
+      float x[4][4], dp[4][4];
+      dot_tile(sq, sk, d, ty, tx, x);
+      dot_tile(sdo, sv, d, ty, tx, dp);
+      probs_tile<true>(s, x, dp, &rs, &kl, slse, sD, s.slopes ? s.slopes[hq] : 0.f, i0, ty, tx, sp, sda);
+      __syncthreads();
+      weigh_rows(sp, sdo, d, ty, tx, dv);
+      weigh_rows(sda, sq, d, ty, tx, dk);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int key = ty + 16 * r;
+    if (kl.pos[key] < 0) continue;
+    const int j = (int)((v0 + key) / P), t = (int)((v0 + key) % P);
+    const int phys = s.a.kv.table[s.a.sel[(size_t)h * s.a.max_sel + j]];  // checked by list_keys
+    const size_t base = (grad_block(s.a, h, j, phys) * P + t) * d;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      const int col = 4 * tx + 64 * c;
+      if (col >= d) continue;
+      float4* gk = reinterpret_cast<float4*>(s.a.dk_pool + base + col);
+      float4* gv = reinterpret_cast<float4*>(s.a.dv_pool + base + col);
+      float4 a = *gk, b = *gv;
+      a.x += s.a.scale * dk[r][c].x;
+      a.y += s.a.scale * dk[r][c].y;
+      a.z += s.a.scale * dk[r][c].z;
+      a.w += s.a.scale * dk[r][c].w;
+      b.x += dv[r][c].x;
+      b.y += dv[r][c].y;
+      b.z += dv[r][c].z;
+      b.w += dv[r][c].w;
+      *gk = a;
+      *gv = b;
+    }
+  }
+}
+
+// Row i at position t = q_start + i in document c (doc_start[c] <= t < doc_start[c + 1]):
+// keys [doc_start[c], max(t + 1, min(doc_start[c] + prefix_len[c], doc_start[c + 1]))).
+__global__ void doc_spans(const int64_t* __restrict__ doc_start, const int64_t* __restrict__ prefix_len, int n_docs,
+                          int64_t q_start, int n_q, int64_t* __restrict__ key_begin, int64_t* __restrict__ key_end) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n_q) return;
+  const int64_t t = q_start + i;
+  int lo = 0, hi = n_docs + 1;  // boundaries <= t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (doc_start[mid] <= t) lo = mid + 1; else hi = mid;
+  }
+  int64_t b = t, e = t;  // outside every document: nothing is visible
+  if (lo >= 1 && lo <= n_docs) {
+    const int c = lo - 1;
+    b = doc_start[c];
+    e = t + 1;
+    if (prefix_len) {
+      const int64_t last = doc_start[c + 1];
+      const int64_t pe = prefix_len[c] > last - b ? last : b + prefix_len[c];
+      e = pe > e ? pe : e;
+    }
+  }
+  key_begin[i] = b;
+  key_end[i] = e;
+}
+
+template <typename T>
+cudaError_t fwd_simt(ScoreArgs& s, cudaStream_t st) {
+  static size_t smem_set[kMaxDevices] = {};
+  cudaError_t e = set_smem_limit((const void*)score_fwd_simt<T>, fwd_smem(kMaxD), smem_set);
+  if (e != cudaSuccess) return e;
+  const int64_t key_tiles = ((int64_t)s.a.max_sel * s.a.g.P + kKeys - 1) / kKeys;
+  s.n_split = (int)std::min<int64_t>(score_split_limit(s.a.g, s.a.n_q), std::max<int64_t>(1, key_tiles / 2));
+  dim3 grid((s.a.n_q + kRows - 1) / kRows, s.a.g.Hq, s.n_split);
+  score_fwd_simt<T><<<grid, kThreads, fwd_smem(s.a.g.d), st>>>(s);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t bwd_simt(const ScoreArgs& s, cudaStream_t st) {
+  static size_t set_dq[kMaxDevices] = {}, set_dkdv[kMaxDevices] = {};
+  cudaError_t e = set_smem_limit((const void*)score_dq_simt<T>, dq_smem(kMaxD), set_dq);
+  if (e == cudaSuccess) e = set_smem_limit((const void*)score_dkdv_simt<T>, dkdv_smem(kMaxD), set_dkdv);
+  if (e != cudaSuccess) return e;
+  const int d = s.a.g.d;
+  float* Dbuf = reinterpret_cast<float*>(s.a.ws);
+  const int64_t warps = (int64_t)s.a.n_q * s.a.g.Hq;
+  score_dot<T><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(s, Dbuf);
+  dim3 gq((s.a.n_q + kRows - 1) / kRows, s.a.g.Hq);
+  score_dq_simt<T><<<gq, kThreads, dq_smem(d), st>>>(s, Dbuf);
+  dim3 gk((unsigned)(((int64_t)s.a.max_sel * s.a.g.P + kKeys - 1) / kKeys), s.a.g.Hkv);
+  score_dkdv_simt<T><<<gk, kThreads, dkdv_smem(d), st>>>(s, Dbuf);
+  count_launches(3);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Thread blocks that may share one tile's keys: as many as fill the SMs twice (two blocks
+// fit an SM) when the rows alone do not, at most 32 (the join reads every share).
+int score_split_limit(const Geometry& g, int n_q) {
+  const int64_t tiles = (int64_t)((n_q + kRows - 1) / kRows) * g.Hq;
+  return (int)std::min<int64_t>(32, std::max<int64_t>(1, 2 * (int64_t)device_sm_count() / tiles));
+}
+
+size_t score_fwd_workspace_bytes(const Geometry& g, int n_q) {
+  const int n = score_split_limit(g, n_q);
+  if (n <= 1) return 0;
+  const size_t rows = (size_t)n_q * g.Hq * n;
+  return align_up(rows * g.d * 4, 256) + align_up(rows * 4, 256);
+}
+
+size_t score_bwd_workspace_bytes(const Geometry& g, int n_q) { return align_up((size_t)g.Hq * n_q * 4, 256); }
+
+cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st) {
+  const int limit = score_split_limit(s.a.g, s.a.n_q);
+  s.part_o = reinterpret_cast<float*>(s.a.ws);
+  s.part_lse = reinterpret_cast<float*>(reinterpret_cast<char*>(s.a.ws) +
+                                        align_up((size_t)s.a.n_q * s.a.g.Hq * limit * s.a.g.d * 4, 256));
+  const bool f32 = s.a.g.dtype == OOMB_FP32;
+  cudaError_t e = f32 ? fwd_simt<float>(s, st) : fwd_simt<__nv_bfloat16>(s, st);
+  if (e != cudaSuccess || s.n_split <= 1) return e;
+  const int64_t warps = (int64_t)s.a.n_q * s.a.g.Hq;
+  const unsigned blocks = (unsigned)((warps + 7) / 8);
+  if (f32)
+    score_join<float><<<blocks, 256, 0, st>>>(s);
+  else
+    score_join<__nv_bfloat16><<<blocks, 256, 0, st>>>(s);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_score_bwd(const ScoreArgs& s, cudaStream_t st) {
+  return s.a.g.dtype == OOMB_FP32 ? bwd_simt<float>(s, st) : bwd_simt<__nv_bfloat16>(s, st);
+}
+
+cudaError_t launch_doc_spans(const int64_t* doc_start, const int64_t* prefix_len, int n_docs, int64_t q_start, int n_q,
+                             int64_t* key_begin, int64_t* key_end, cudaStream_t st) {
+  doc_spans<<<(n_q + 127) / 128, 128, 0, st>>>(doc_start, prefix_len, n_docs, q_start, n_q, key_begin, key_end);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace oomb
