@@ -300,35 +300,44 @@ __global__ void __launch_bounds__(kThreads) score_fwd_simt(const ScoreArgs s) {
   }
 }
 
-// One warp per (row, head): O = sum_z w_z O_z / sum_z w_z with w_z = exp(LSE_z - max LSE).
+// A block per (row, head): O = sum_z w_z O_z / sum_z w_z with w_z = exp(LSE_z - max LSE).  Its
+// 8 warps take the parts z = w, w + 8, ..., so that the reads of all parts are in flight at
+// once, and are joined in order.
 template <typename T>
 __global__ void __launch_bounds__(256) score_join(const ScoreArgs s) {
-  const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32;
-  const int lane = threadIdx.x % 32, Hq = s.a.g.Hq, d = s.a.g.d;
-  const int64_t rows = (int64_t)s.a.n_q * Hq;
-  if (w >= rows) return;
+  __shared__ float acc_s[8][kMaxD], den_s[8];
+  const int64_t rh = blockIdx.x, rows = (int64_t)s.a.n_q * s.a.g.Hq;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, Hq = s.a.g.Hq, d = s.a.g.d;
   float m = -INFINITY;
-  for (int z = lane; z < s.n_split; z += 32) m = fmaxf(m, s.part_lse[z * rows + w]);
+  for (int z = lane; z < s.n_split; z += 32) m = fmaxf(m, s.part_lse[z * rows + rh]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   const float shift = m == -INFINITY ? 0.f : m;
   float acc[kMaxD / 32] = {}, den = 0.f;
-  for (int z = 0; z < s.n_split; ++z) {
-    const float lz = s.part_lse[z * rows + w];
-    if (lz == -INFINITY) continue;  // nothing visible in this share
+#pragma unroll 4
+  for (int z = warp; z < s.n_split; z += 8) {
+    const float lz = s.part_lse[z * rows + rh];
     const float wz = expf(lz - shift);
     den += wz;
-    const float* src = s.part_o + (z * rows + w) * d;
+    const float* src = s.part_o + (z * rows + rh) * d;
 #pragma unroll
     for (int c = 0; c < kMaxD / 32; ++c)
-      if (lane + 32 * c < d) acc[c] += wz * src[lane + 32 * c];
+      if (lane + 32 * c < d && lz > -INFINITY) acc[c] += wz * src[lane + 32 * c];  // else nothing was written
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
-  T* dst = reinterpret_cast<T*>(s.a.o_out) + w * d;
 #pragma unroll
-  for (int c = 0; c < kMaxD / 32; ++c)
-    if (lane + 32 * c < d) dst[lane + 32 * c] = from_float<T>(acc[c] * inv);
-  if (lane == 0) s.a.lse_out[(size_t)(w % Hq) * s.a.n_q + w / Hq] = den > 0.f ? m + logf(den) : m;
+  for (int c = 0; c < kMaxD / 32; ++c) acc_s[warp][lane + 32 * c] = acc[c];
+  if (lane == 0) den_s[warp] = den;
+  __syncthreads();
+  if (threadIdx.x >= d) return;
+  float o = 0.f;
+  den = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    o += acc_s[w][threadIdx.x];
+    den += den_s[w];
+  }
+  reinterpret_cast<T*>(s.a.o_out)[rh * d + threadIdx.x] = from_float<T>(den > 0.f ? o / den : 0.f);
+  if (threadIdx.x == 0) s.a.lse_out[(size_t)(rh % Hq) * s.a.n_q + rh / Hq] = den > 0.f ? m + logf(den) : m;
 }
 
 // ----------------------------------------------------------------- backward
@@ -564,13 +573,25 @@ __global__ void doc_spans(const int64_t* __restrict__ doc_start, const int64_t* 
   key_end[i] = e;
 }
 
+// Thread blocks that may share one tile's keys: as many as fill the SMs twice (two blocks
+// fit an SM) when the rows alone do not, at most 32 (the join reads every share).
+int simt_split_limit(const Geometry& g, int n_q) {
+  const int64_t tiles = (int64_t)((n_q + kRows - 1) / kRows) * g.Hq;
+  return (int)std::min<int64_t>(32, std::max<int64_t>(1, 2 * (int64_t)device_sm_count() / tiles));
+}
+
+// Parts the keys of a row may be cut into.
+int parts_limit(const Geometry& g, int n_q) {
+  return tc_supported(g) ? score_tc_parts_limit(g, n_q) : simt_split_limit(g, n_q);
+}
+
 template <typename T>
 cudaError_t fwd_simt(ScoreArgs& s, cudaStream_t st) {
   static size_t smem_set[kMaxDevices] = {};
   cudaError_t e = set_smem_limit((const void*)score_fwd_simt<T>, fwd_smem(kMaxD), smem_set);
   if (e != cudaSuccess) return e;
   const int64_t key_tiles = ((int64_t)s.a.max_sel * s.a.g.P + kKeys - 1) / kKeys;
-  s.n_split = (int)std::min<int64_t>(score_split_limit(s.a.g, s.a.n_q), std::max<int64_t>(1, key_tiles / 2));
+  s.n_split = (int)std::min<int64_t>(simt_split_limit(s.a.g, s.a.n_q), std::max<int64_t>(1, key_tiles / 2));
   dim3 grid((s.a.n_q + kRows - 1) / kRows, s.a.g.Hq, s.n_split);
   score_fwd_simt<T><<<grid, kThreads, fwd_smem(s.a.g.d), st>>>(s);
   count_launches(1);
@@ -597,15 +618,8 @@ cudaError_t bwd_simt(const ScoreArgs& s, cudaStream_t st) {
 
 }  // namespace
 
-// Thread blocks that may share one tile's keys: as many as fill the SMs twice (two blocks
-// fit an SM) when the rows alone do not, at most 32 (the join reads every share).
-int score_split_limit(const Geometry& g, int n_q) {
-  const int64_t tiles = (int64_t)((n_q + kRows - 1) / kRows) * g.Hq;
-  return (int)std::min<int64_t>(32, std::max<int64_t>(1, 2 * (int64_t)device_sm_count() / tiles));
-}
-
 size_t score_fwd_workspace_bytes(const Geometry& g, int n_q) {
-  const int n = score_split_limit(g, n_q);
+  const int n = parts_limit(g, n_q);
   if (n <= 1) return 0;
   const size_t rows = (size_t)n_q * g.Hq * n;
   return align_up(rows * g.d * 4, 256) + align_up(rows * 4, 256);
@@ -614,15 +628,16 @@ size_t score_fwd_workspace_bytes(const Geometry& g, int n_q) {
 size_t score_bwd_workspace_bytes(const Geometry& g, int n_q) { return align_up((size_t)g.Hq * n_q * 4, 256); }
 
 cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st) {
-  const int limit = score_split_limit(s.a.g, s.a.n_q);
+  const int limit = parts_limit(s.a.g, s.a.n_q);
   s.part_o = reinterpret_cast<float*>(s.a.ws);
   s.part_lse = reinterpret_cast<float*>(reinterpret_cast<char*>(s.a.ws) +
                                         align_up((size_t)s.a.n_q * s.a.g.Hq * limit * s.a.g.d * 4, 256));
   const bool f32 = s.a.g.dtype == OOMB_FP32;
-  cudaError_t e = f32 ? fwd_simt<float>(s, st) : fwd_simt<__nv_bfloat16>(s, st);
+  cudaError_t e = tc_supported(s.a.g) ? launch_score_fwd_tc(s, st)
+                  : f32               ? fwd_simt<float>(s, st)
+                                      : fwd_simt<__nv_bfloat16>(s, st);
   if (e != cudaSuccess || s.n_split <= 1) return e;
-  const int64_t warps = (int64_t)s.a.n_q * s.a.g.Hq;
-  const unsigned blocks = (unsigned)((warps + 7) / 8);
+  const unsigned blocks = (unsigned)(s.a.n_q * s.a.g.Hq);
   if (f32)
     score_join<float><<<blocks, 256, 0, st>>>(s);
   else

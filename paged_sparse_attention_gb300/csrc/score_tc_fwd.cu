@@ -1,0 +1,653 @@
+// tcgen05 forward of the attention with modified scores (bf16, head_dim 128, page 128).
+//
+// Two layouts of a thread block's two 128-row tiles A and B:
+//  rows   tiles A and B are neighbouring 128-row tiles of one query head.  Both read the same
+//         pages, each K and V tile loaded once.  Heaviest (last) pairs first.
+//  packed where all rows of the G heads of a group fit one tile (n_q G <= 128: single tokens
+//         and short tails): row r is token r / G, head r % G, so K and V are read once for
+//         the whole group, and A and B hold the same rows and take alternate pages.
+// Pages that no row of the block can see are left out: the ranges of the rows give an
+// interval of the ascending selection.  Where the tiles do not fill the SMs, n_split thread
+// blocks share the interval, their parts joined by score_join (packed: A and B of one block
+// are two parts).  A block is bound by the exponential unit with many rows (as the plain
+// forward) and by HBM in the packed layout.
+//
+// Warp roles (320 threads): warp 0 TMA producer (K ring of 3, V ring of 2 tiles), warp 1 MMA
+// issuer and TMEM owner, warps 2-5 softmax of tile A, 6-9 of tile B (thread = query row, its
+// 128 scores in registers).  The tensor core runs PV_A(j), S_A(j+1), PV_B(j), S_B(j+1).  MMAs
+// complete in order, so the softmax warp that has seen S_X(j) knows that PV_X(j-1) is done and
+// frees the ring slots.  TMEM columns: S_A, S_B (P over S, bf16), O_A, O_B, 128 each.
+// Scores and row sums are fp32; P is rounded to bf16, the operand type of the second product.
+#include "score_tc_common.cuh"
+
+namespace oomb {
+namespace {
+
+using namespace tc;
+
+constexpr int kKStages = 3;
+constexpr int kVStages = 2;
+constexpr int kThreads = 320;
+constexpr int kGroupThreads = 128;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled when the row maximum grows by more
+
+struct ScoreFwdParams {
+  ScoreArgs s;
+  CapConst cap;
+  float scale_log2;
+  int n_tiles, n_pairs;
+};
+
+struct __align__(8) FwdBarriers {
+  uint64_t q_full;
+  uint64_t k_full[kKStages];
+  uint64_t k_empty[kKStages];
+  uint64_t v_full[kVStages];
+  uint64_t v_empty[kVStages];
+  uint64_t s_full[2];
+  uint64_t p_full[2];
+  uint64_t o_done[2];
+  uint64_t mma_done;
+  int64_t lo[8], hi[8];  // key range seen by each softmax warp's rows
+  int below[4];          // selected pages below: tile A's first, A's end, B's first, B's end
+  uint32_t tmem_base;
+  int abort;
+};
+
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffK = 2 * kTileBytes;
+constexpr uint32_t kOffV = kOffK + kKStages * kTileBytes;
+constexpr uint32_t kOffBar = kOffV + kVStages * kTileBytes;
+constexpr size_t kSmemBytes = 1024 + kOffBar + sizeof(FwdBarriers);
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+// The pages of the two tiles, as entries of the selection.  rows: tile x reads [first[x],
+// first[x] + n[x]), and the ring holds the entries [lo, lo + n_ring) in order.  packed: tile x
+// reads its own n[x] entries from first[x], and the ring alternates between the tiles.
+struct TilePages {
+  int first[2], n[2], lo, n_ring;
+};
+
+template <bool PACK>
+__device__ __forceinline__ int ring_of(const TilePages& t, int x, int j) {  // ring entry of tile x's page j
+  return PACK ? 2 * j + x : t.first[x] - t.lo + j;
+}
+
+template <bool PACK>
+__device__ __forceinline__ TilePages tile_pages(const ScoreFwdParams& p, const int (&below)[4]) {
+  TilePages t;
+  int a0 = below[0], a1 = max(below[0], below[1]), b0 = below[2], b1 = max(below[2], below[3]);
+  if (PACK) {
+    // the interval's share of this block, half of it for each tile.  A takes the odd page: its
+    // ring slots were its own before, so every slot that is waited for is freed by its last user
+    const int n = a1 - a0;
+    const int c0 = a0 + (int)((int64_t)n * blockIdx.z / p.s.n_split);
+    const int c1 = a0 + (int)((int64_t)n * (blockIdx.z + 1) / p.s.n_split);
+    t.first[0] = c0;
+    t.n[0] = (c1 - c0 + 1) / 2;
+    t.first[1] = c0 + t.n[0];
+    t.n[1] = c1 - c0 - t.n[0];
+    t.lo = 0;
+    t.n_ring = c1 - c0;
+    return t;
+  }
+  // this block's share of the union of the two intervals
+  const bool ea = a0 == a1, eb = b0 == b1;
+  const int lo = ea ? b0 : eb ? a0 : min(a0, b0), hi = ea ? b1 : eb ? a1 : max(a1, b1);
+  const int c0 = lo + (int)((int64_t)(hi - lo) * blockIdx.z / p.s.n_split);
+  const int c1 = lo + (int)((int64_t)(hi - lo) * (blockIdx.z + 1) / p.s.n_split);
+  a0 = min(max(a0, c0), c1);
+  a1 = min(max(a1, c0), c1);
+  b0 = min(max(b0, c0), c1);
+  b1 = min(max(b1, c0), c1);
+  // B ends no earlier than A and no page between them is left out (pages a tile cannot see
+  // are masked): the ring's slots are then freed by B where B reads the page, else by A
+  if (b0 >= b1) {
+    b0 = b1 = a1;
+  } else if (a0 >= a1) {
+    a0 = a1 = b0;
+  } else {
+    b1 = max(b1, a1);
+    b0 = min(b0, a1);
+  }
+  t.first[0] = a0;
+  t.n[0] = a1 - a0;
+  t.first[1] = b0;
+  t.n[1] = b1 - b0;
+  t.lo = a0 < a1 ? min(a0, b0) : b0;
+  t.n_ring = max(a1, b1) - t.lo;
+  return t;
+}
+
+template <bool CAP, bool BIAS, bool PACK>
+__global__ void __launch_bounds__(kThreads, 1)
+    score_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ ScoreFwdParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  FwdBarriers* bar = reinterpret_cast<FwdBarriers*>(sm + kOffBar);
+  const AttnArgs& a = p.s.a;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int G = a.g.G, Hq = a.g.Hq;
+  const int h = PACK ? (int)blockIdx.x : (int)blockIdx.x / G;
+  const int pair = p.n_pairs - 1 - (int)blockIdx.y;
+  const int tA = 2 * pair, tB = 2 * pair + 1;
+  const bool hasB = PACK || tB < p.n_tiles;
+  int count = a.sel_count[h];
+  count = count < 0 ? 0 : min(count, a.max_sel);  // flagged by check_selection
+  volatile int* abort = &bar->abort;
+
+  // softmax thread: its row, query head and key range
+  const int x = warp < 2 ? 0 : (warp - 2) >> 2;  // tile
+  const int r = (warp & 3) * 32 + lane;          // row of the tile == TMEM lane
+  int row = 0, hq = 0;
+  bool valid = false;
+  int64_t kb = 0, ke = INT64_MAX;  // rows that do not exist ask for no masking
+  if (warp >= 2) {
+    if (PACK) {
+      valid = r < a.n_q * G;
+      row = valid ? r / G : 0;
+      hq = h * G + (valid ? r % G : 0);
+    } else {
+      row = (x == 0 ? tA : tB) * kTile + r;
+      valid = row < a.n_q;
+      hq = (int)blockIdx.x;
+    }
+    if (valid) row_span(p.s, row, kb, ke);
+    int64_t lo = valid && ke > kb ? kb : INT64_MAX, hi = valid && ke > kb ? ke : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    if (lane == 0) {
+      bar->lo[warp - 2] = lo;
+      bar->hi[warp - 2] = hi;
+    }
+    if (PACK) {  // rows of Q that no load fills
+      const int used = a.n_q * G;
+      for (int idx = (int)threadIdx.x - 64; idx < (kTile - used) * 16; idx += 2 * kGroupThreads) {
+        const int rr = used + idx / 16, c = idx % 16;
+        *reinterpret_cast<uint4*>(sm + kOffQ + (c >> 3) * kHalfBytes + rr * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+    }
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(&bar->q_full, 1);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&bar->k_full[i], 1);
+      mbar_init(&bar->k_empty[i], 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&bar->v_full[i], 1);
+      mbar_init(&bar->v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->s_full[i], 1);
+      mbar_init(&bar->p_full[i], kGroupThreads / 32);
+      mbar_init(&bar->o_done[i], 1);
+    }
+    mbar_init(&bar->mma_done, 1);
+    bar->abort = 0;
+    for (int i = 0; i < 4; ++i) bar->below[i] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&bar->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+  {
+    // entries below the first page a tile sees and below the end of the last one, counted by
+    // all threads (the selection ascends); the selection is checked in the same pass
+    int64_t page[4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      int64_t lo = INT64_MAX, hi = 0;
+      for (int w = 4 * t; w < 4 * t + 4; ++w) {
+        lo = min(lo, bar->lo[w]);
+        hi = max(hi, bar->hi[w]);
+      }
+      page[2 * t] = hi > 0 ? lo / kTile : 0;
+      page[2 * t + 1] = (hi + kTile - 1) / kTile;
+    }
+    const int32_t* sel = a.sel + (size_t)h * a.max_sel;
+    int n[4] = {0, 0, 0, 0};
+    bool bad = false;
+    for (int e = threadIdx.x; e < count; e += kThreads) {
+      const int pg = sel[e];
+      bad |= pg < 0 || pg >= p.s.n_view || (e > 0 && sel[e - 1] >= pg);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n[i] += pg < page[i] ? 1 : 0;
+    }
+    if (bad || (threadIdx.x == 0 && count != a.sel_count[h])) atomicOr(a.err, OOMB_DEVERR_SEL);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int sum = __reduce_add_sync(0xffffffffu, n[i]);
+      if (lane == 0 && sum) atomicAdd(&bar->below[i], sum);
+    }
+  }
+  __syncthreads();
+  const int below[4] = {bar->below[0], bar->below[1], bar->below[2], bar->below[3]};
+  const TilePages t = tile_pages<PACK>(p, below);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0 && t.n_ring > 0) {
+      tma_prefetch_desc(&tq);
+      tma_prefetch_desc(&tk);
+      tma_prefetch_desc(&tv);
+      if (PACK) {
+        const uint32_t bytes = (uint32_t)(a.n_q * G) * 128u;
+        mbar_arrive_expect_tx(&bar->q_full, 2 * bytes);
+        tma_load_3d(sm + kOffQ, &tq, &bar->q_full, 0, h * G, 0);
+        tma_load_3d(sm + kOffQ + kHalfBytes, &tq, &bar->q_full, 64, h * G, 0);
+      } else {
+        mbar_arrive_expect_tx(&bar->q_full, (hasB ? 2u : 1u) * kTileBytes);
+        for (int i = 0; i < (hasB ? 2 : 1); ++i) {
+          tma_load_3d(sm + kOffQ + i * kTileBytes, &tq, &bar->q_full, 0, (int)blockIdx.x, (tA + i) * kTile);
+          tma_load_3d(sm + kOffQ + i * kTileBytes + kHalfBytes, &tq, &bar->q_full, 64, (int)blockIdx.x,
+                      (tA + i) * kTile);
+        }
+      }
+      auto row_of = [&](int e) -> int {  // first row of ring entry e's block in the K/V maps
+        const int j = PACK ? t.first[e & 1] + (e >> 1) : t.lo + e;
+        const int64_t blk = score_block(p.s, h, j, a.sel[(size_t)h * a.max_sel + j]);
+        return blk < 0 ? 0 : (int)(blk * kTile);  // a page left out is masked whole: any block will do
+      };
+      int jk = 0, jv = 0;
+      long long last = clock64();
+      while (jv < t.n_ring) {
+        bool progressed = false;
+        if (jk < t.n_ring) {
+          const int ks = jk % kKStages;
+          if (jk < kKStages || mbar_test_wait(&bar->k_empty[ks], ((jk / kKStages) - 1) & 1)) {
+            const int rw = row_of(jk);
+            mbar_arrive_expect_tx(&bar->k_full[ks], kTileBytes);
+            tma_load_2d(sm + kOffK + ks * kTileBytes, &tk, &bar->k_full[ks], 0, rw);
+            tma_load_2d(sm + kOffK + ks * kTileBytes + kHalfBytes, &tk, &bar->k_full[ks], 64, rw);
+            ++jk;
+            progressed = true;
+          }
+        }
+        if (jv < jk) {
+          const int vs = jv % kVStages;
+          if (jv < kVStages || mbar_test_wait(&bar->v_empty[vs], ((jv / kVStages) - 1) & 1)) {
+            const int rw = row_of(jv);
+            mbar_arrive_expect_tx(&bar->v_full[vs], kTileBytes);
+            tma_load_2d(sm + kOffV + vs * kTileBytes, &tv, &bar->v_full[vs], 0, rw);
+            tma_load_2d(sm + kOffV + vs * kTileBytes + kHalfBytes, &tv, &bar->v_full[vs], 64, rw);
+            ++jv;
+            progressed = true;
+          }
+        }
+        if (progressed) {
+          last = clock64();
+        } else if (*abort) {
+          break;
+        } else if (clock64() - last > (1ll << 31)) {
+          atomicOr(a.err, kErrMbarTimeout);
+          *abort = 1;
+          break;
+        }
+      }
+      // drain: every armed stage must have landed before the block may exit
+      for (int jj = (jk > kKStages ? jk - kKStages : 0); jj < jk; ++jj)
+        mbar_wait(&bar->k_full[jj % kKStages], (jj / kKStages) & 1, a.err, nullptr);
+      for (int jj = (jv > kVStages ? jv - kVStages : 0); jj < jv; ++jj)
+        mbar_wait(&bar->v_full[jj % kVStages], (jj / kVStages) & 1, a.err, nullptr);
+      mbar_wait(&bar->q_full, 0, a.err, nullptr);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && t.n_ring > 0) {
+      const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+      const uint32_t idesc_o = idesc_bf16_f32(128, 128, false, true);
+      bool ok = mbar_wait(&bar->q_full, 0, a.err, abort);
+      auto issue_s = [&](int xx, int j) -> bool {  // S = Q K_j^T
+        const int e = ring_of<PACK>(t, xx, j);
+        if (!mbar_wait(&bar->k_full[e % kKStages], (e / kKStages) & 1, a.err, abort)) return false;
+        tc_fence_after();
+        const uint32_t aQ = smem_u32(sm + kOffQ + (PACK ? 0 : xx * kTileBytes));
+        const uint32_t aK = smem_u32(sm + kOffK + (e % kKStages) * kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ss(tmem + xx * 128, desc_kmajor(aQ, kk), desc_kmajor(aK, kk), idesc_s, kk > 0);
+        mma_commit(&bar->s_full[xx]);
+        return true;
+      };
+      auto issue_pv = [&](int xx, int j) -> bool {  // O += P V_j
+        const int e = ring_of<PACK>(t, xx, j);
+        if (!mbar_wait(&bar->v_full[e % kVStages], (e / kVStages) & 1, a.err, abort)) return false;
+        if (!mbar_wait(&bar->p_full[xx], j & 1, a.err, abort)) return false;
+        tc_fence_after();
+        const uint32_t aV = smem_u32(sm + kOffV + (e % kVStages) * kTileBytes);
+        const uint32_t ap = tmem + xx * 128, o = tmem + 256 + xx * 128;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(o, ap + kk * 8, desc_mnmajor(aV, kk), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+        if (j == t.n[xx] - 1) mma_commit(&bar->o_done[xx]);
+        return true;
+      };
+      // step i: rows, ring entry i; packed, page i of each tile
+      const int steps = PACK ? max(t.n[0], t.n[1]) : t.n_ring;
+      int off[2];  // page of tile x at step i is i - off[x]
+#pragma unroll
+      for (int xx = 0; xx < 2; ++xx) off[xx] = PACK ? 0 : t.first[xx] - t.lo;
+      for (int xx = 0; ok && xx < 2; ++xx)
+        if (t.n[xx] > 0 && off[xx] == 0) ok = issue_s(xx, 0);
+      for (int i = 0; ok && i < steps; ++i)
+        for (int xx = 0; ok && xx < 2; ++xx) {
+          const int j = i - off[xx];
+          if (j >= 0 && j < t.n[xx]) ok = issue_pv(xx, j);
+          if (ok && j + 1 >= 0 && j + 1 < t.n[xx]) ok = issue_s(xx, j + 1);
+        }
+      // every issued MMA must finish before TMEM is released
+      mma_commit(&bar->mma_done);
+      mbar_wait(&bar->mma_done, 0, a.err, nullptr);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax warps
+    const int nx = t.n[x];
+    const uint32_t lane_off = tmem_lane_base(warp);
+    const uint32_t tS = tmem + lane_off + x * 128;
+    const uint32_t tO = tmem + lane_off + 256 + x * 128;
+    const int64_t qpos = a.q_start + row;
+    const float slope2 = BIAS ? p.s.slopes[hq] * kLog2e : 0.f;
+    const int32_t* sel = a.sel + (size_t)h * a.max_sel + t.first[x];
+    const int b_first = t.first[1] - t.lo, b_end = b_first + t.n[1];  // rows: ring entries of tile B
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    int pg = nx > 0 ? sel[0] : 0;
+    for (int j = 0; j < nx; ++j) {
+      const bool known = pg >= 0 && pg < p.s.n_view && pg < a.g.max_logical;
+      const int phys = known ? a.kv.table[pg] : -1;
+      const int64_t p0 = (int64_t)pg * kTile;
+      // keys [cb, ce) of the page are visible to this row; a page left out has none
+      const bool mapped = phys >= 0 && phys < a.g.num_phys;
+      const bool whole = __all_sync(0xffffffffu, mapped && kb <= p0 && ke >= p0 + kTile);
+      const int pg_next = j + 1 < nx ? sel[j + 1] : 0;
+      if (ok) ok = mbar_wait(&bar->s_full[x], j & 1, a.err, abort);
+      ok = __all_sync(0xffffffffu, ok);  // TMEM loads and stores below are warp-collective
+      if (!ok) break;
+      tc_fence_after();
+      const int e = ring_of<PACK>(t, x, j);
+      if ((warp & 3) == 2 && lane == 0) {
+        if (PACK) {  // each ring entry has one user
+          mbar_arrive(&bar->k_empty[e % kKStages]);
+          if (j > 0) mbar_arrive(&bar->v_empty[ring_of<PACK>(t, x, j - 1) % kVStages]);
+        } else if (x == 1 || e < b_first || e >= b_end) {  // the last user of page e
+          mbar_arrive(&bar->k_empty[e % kKStages]);
+          if (e > 0) mbar_arrive(&bar->v_empty[(e - 1) % kVStages]);
+        }
+      }
+      uint32_t sr[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+      tmem_wait_ld();
+      // scores in log2 units (without cap and bias the scale is folded into the exponent)
+      if constexpr (CAP) {
+        float mx[4], mn[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          mx[k] = fmaxf(__uint_as_float(sr[k]), __uint_as_float(sr[4 + k]));
+          mn[k] = fminf(__uint_as_float(sr[k]), __uint_as_float(sr[4 + k]));
+        }
+#pragma unroll
+        for (int c = 8; c < 128; c += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            mx[k] = fmax3(mx[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 4 + k]));
+            mn[k] = fmin3(mn[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 4 + k]));
+          }
+        const float amax = fmaxf(fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]),
+                                 -fmin3(fminf(mn[0], mn[1]), mn[2], mn[3]));
+        if (__all_sync(0xffffffffu, amax <= p.cap.s_small)) {
+          uint64_t co[kTanhTerms];
+#pragma unroll
+          for (int i = 0; i < kTanhTerms; ++i) co[i] = f32x2(p.cap.poly[i], p.cap.poly[i]);
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            const uint64_t S = f32x2(sr[2 * c], sr[2 * c + 1]);
+            const uint64_t z = fmul2(S, S);
+            uint64_t v = co[kTanhTerms - 1];
+#pragma unroll
+            for (int i = kTanhTerms - 2; i >= 0; --i) v = ffma2(v, z, co[i]);
+            float y0, y1;
+            f32x2_split(fmul2(v, S), y0, y1);
+            sr[2 * c] = __float_as_uint(y0);
+            sr[2 * c + 1] = __float_as_uint(y1);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            sr[c] = __float_as_uint(p.cap.cap2 * tanh_wide(__uint_as_float(sr[c]), p.cap));
+        }
+      }
+      if constexpr (BIAS) {
+        const float f0 = (float)(qpos - p0);  // distance of key column c: |f0 - c|
+        const float sc = CAP ? 1.f : p.scale_log2;
+        if (__all_sync(0xffffffffu, f0 >= (float)kTile)) {  // every key behind the row: linear in c
+          const uint64_t sc2 = f32x2(sc, sc), step = f32x2(2.f * slope2, 2.f * slope2);
+          uint64_t bias = f32x2(-slope2 * f0, -slope2 * (f0 - 1.f));
+          const float b0 = -slope2 * f0;
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            if (c % 8 == 0)  // restart: the running sum gathers no more than 8 roundings
+              bias = f32x2(fmaf(slope2, (float)(2 * c), b0), fmaf(slope2, (float)(2 * c + 1), b0));
+            float y0, y1;
+            f32x2_split(ffma2(f32x2(sr[2 * c], sr[2 * c + 1]), sc2, bias), y0, y1);
+            sr[2 * c] = __float_as_uint(y0);
+            sr[2 * c + 1] = __float_as_uint(y1);
+            bias = fadd2(bias, step);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), sc, -slope2 * fabsf(f0 - (float)c)));
+        }
+      }
+      if (!whole) {
+        const int64_t rb = kb - p0, re = ke - p0;
+        const int cb = mapped ? (int)max((int64_t)0, min(rb, (int64_t)kTile)) : kTile;
+        const int ce = mapped ? (int)max((int64_t)0, min(re, (int64_t)kTile)) : 0;
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c < cb || c >= ce) sr[c] = 0xff800000u;  // -inf
+      }
+      constexpr bool kRaw = !CAP && !BIAS;  // sr still holds q.k
+      float mx[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mx[k] = fmaxf(__uint_as_float(sr[k]), __uint_as_float(sr[8 + k]));
+#pragma unroll
+      for (int c = 16; c < 128; c += 16)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mx[k] = fmax3(mx[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
+      float tmax = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+      if (kRaw) tmax *= p.scale_log2;
+      bool rescale_o = false;
+      float alpha = 1.f;
+      if (tmax > m + kRescaleThreshold || (m == -INFINITY && tmax > -INFINITY)) {
+        const float m_new = fmaxf(m, tmax);
+        alpha = exp2f(m - m_new);  // 0 when m == -inf
+        rescale_o = (j > 0) && (m > -INFINITY);
+        l *= alpha;
+        m = m_new;
+      }
+      const float neg_m = (m == -INFINITY) ? 0.f : -m;
+      const float sc = kRaw ? p.scale_log2 : 1.f;
+      const uint64_t scale2 = f32x2(sc, sc), negm2 = f32x2(neg_m, neg_m);
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 64; ++c) {
+        float t0, t1;
+        const uint64_t s2 = f32x2(sr[2 * c], sr[2 * c + 1]);
+        f32x2_split(kRaw ? ffma2(s2, scale2, negm2) : fadd2(s2, negm2), t0, t1);
+        const float p0v = ex2_approx(t0), p1v = ex2_approx(t1);
+        sum[c & 3] += p0v + p1v;
+        sr[c] = pack_bf16x2(p0v, p1v);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if (__any_sync(0xffffffffu, rescale_o)) {  // PV of the previous page finished before this S
+        if (!rescale_o) alpha = 1.f;
+#pragma unroll 1
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t o[32];
+          tmem_ld32(tO + cc * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int ee = 0; ee < 32; ++ee) o[ee] = __float_as_uint(__uint_as_float(o[ee]) * alpha);
+          tmem_st32(tO + cc * 32, o);
+        }
+      }
+      tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+      tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->p_full[x]);
+      pg = pg_next;
+    }
+    // epilogue: this thread's row of O, normalised
+    const size_t rows = (size_t)a.n_q * Hq, rh = (size_t)row * Hq + hq;
+    const int part = PACK ? 2 * (int)blockIdx.z + x : (int)blockIdx.z;
+    const bool split = PACK || p.s.n_split > 1;
+    const bool done = __all_sync(0xffffffffu, ok && nx > 0 && mbar_wait(&bar->o_done[x], 0, a.err, abort));
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float lse = done ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (done) {
+      tc_fence_after();
+#pragma unroll 1
+      for (int cc = 0; cc < 4; ++cc) {
+        uint32_t o[32];
+        tmem_ld32(tO + cc * 32, o);
+        tmem_wait_ld();
+        if (!valid) continue;
+        if (split) {
+          float4* dst = reinterpret_cast<float4*>(p.s.part_o + ((size_t)part * rows + rh) * kD + cc * 32);
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                                 __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o_out) + rh * kD + cc * 32);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint4 w;
+            w.x = pack_bf16x2(__uint_as_float(o[8 * v + 0]) * inv, __uint_as_float(o[8 * v + 1]) * inv);
+            w.y = pack_bf16x2(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv);
+            w.z = pack_bf16x2(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv);
+            w.w = pack_bf16x2(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv);
+            dst[v] = w;
+          }
+        }
+      }
+    } else if (!split && valid) {
+      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o_out) + rh * kD);
+      for (int v = 0; v < 16; ++v) dst[v] = make_uint4(0, 0, 0, 0);
+    }
+    if (valid) {
+      if (split)
+        p.s.part_lse[(size_t)part * rows + rh] = lse;  // -inf: score_join does not read the part's O
+      else
+        a.lse_out[(size_t)hq * a.n_q + row] = lse;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// 3-D map over a token-major [n, H, 128] bf16 tensor: box = every token, G heads, 64 columns.
+bool make_tmap_group(CUtensorMap* m, const void* base, int n, int H, int G) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)H, (cuuint64_t)n};
+  cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)H * kD * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)n};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool CAP, bool BIAS, bool PACK>
+cudaError_t launch_one(const ScoreFwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                       cudaStream_t st) {
+  static size_t smem_set[kMaxDevices] = {};
+  cudaError_t e = set_smem_limit((const void*)score_fwd_tc<CAP, BIAS, PACK>, kSmemBytes, smem_set);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(PACK ? p.s.a.g.Hkv : p.s.a.g.Hq, p.n_pairs, p.s.n_split);
+  score_fwd_tc<CAP, BIAS, PACK><<<grid, kThreads, kSmemBytes, st>>>(tq, tk, tv, p);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <bool CAP, bool BIAS>
+cudaError_t launch_pack(bool pack, const ScoreFwdParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                        const CUtensorMap& tv, cudaStream_t st) {
+  return pack ? launch_one<CAP, BIAS, true>(p, tq, tk, tv, st) : launch_one<CAP, BIAS, false>(p, tq, tk, tv, st);
+}
+
+}  // namespace
+
+bool score_tc_packs(const Geometry& g, int n_q) { return (int64_t)n_q * g.G <= kTile; }
+
+// Parts the keys of a tile may be cut into.
+int score_tc_parts_limit(const Geometry& g, int n_q) {
+  const int sms = device_sm_count();
+  if (score_tc_packs(g, n_q)) return 2 * std::max(1, sms / g.Hkv);
+  const int64_t units = (int64_t)((n_q + 2 * kTile - 1) / (2 * kTile)) * g.Hq;
+  return (int)std::max<int64_t>(1, 4 * (int64_t)sms / units);
+}
+
+cudaError_t launch_score_fwd_tc(ScoreArgs& s, cudaStream_t st) {
+  const Geometry& g = s.a.g;
+  const bool pack = score_tc_packs(g, s.a.n_q);
+  const int limit = score_tc_parts_limit(g, s.a.n_q), sms = device_sm_count();
+  ScoreFwdParams p;
+  p.n_tiles = (s.a.n_q + kTile - 1) / kTile;
+  p.n_pairs = pack ? 1 : (p.n_tiles + 1) / 2;
+  if (pack) {
+    // one block per SM, each with at least two pages for either tile
+    s.n_split = std::max(1, std::min(limit / 2, (s.a.max_sel + 3) / 4));
+  } else {
+    // waves of blocks, each as long as its pages plus about kFixed pages of set-up and
+    // epilogue (and the join, once the keys are cut)
+    constexpr double kFixed = 4.0;
+    const int64_t units = (int64_t)p.n_pairs * g.Hq;
+    double best = 0.0;
+    for (int n = 1; n <= limit && (n == 1 || s.a.max_sel / n >= 4); ++n) {
+      const double t = (double)((units * n + sms - 1) / sms) * ((double)s.a.max_sel / n + kFixed) + (n > 1 ? kFixed : 0.0);
+      if (n == 1 || t < 0.95 * best) {
+        best = t;
+        s.n_split = n;
+      }
+    }
+  }
+  CUtensorMap tq, tk, tv;
+  const bool ok = pack ? make_tmap_group(&tq, s.a.q, s.a.n_q, g.Hq, g.G) : make_tmap_heads(&tq, s.a.q, s.a.n_q, g.Hq);
+  if (!ok || !make_tmap_rows(&tk, s.a.kv.k, kv_rows(s.a)) || !make_tmap_rows(&tv, s.a.kv.v, kv_rows(s.a)))
+    return cudaErrorInvalidValue;
+  p.s = s;
+  p.cap = make_cap(s.cap, s.a.scale);
+  p.scale_log2 = s.a.scale * kLog2e;
+  cudaError_t e;
+  if (s.cap > 0.f)
+    e = s.slopes ? launch_pack<true, true>(pack, p, tq, tk, tv, st) : launch_pack<true, false>(pack, p, tq, tk, tv, st);
+  else
+    e = s.slopes ? launch_pack<false, true>(pack, p, tq, tk, tv, st)
+                 : launch_pack<false, false>(pack, p, tq, tk, tv, st);
+  s.n_split = pack ? 2 * s.n_split : s.n_split;  // parts for the join
+  return e;
+}
+
+}  // namespace oomb
