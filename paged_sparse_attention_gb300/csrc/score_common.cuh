@@ -76,6 +76,8 @@ __device__ __forceinline__ int64_t score_block(const ScoreArgs& s, int h, int j,
 bool score_tc_packs(const Geometry& g, int n_q);       // tensor cores: a group's rows fit one tile
 int score_tc_parts_limit(const Geometry& g, int n_q);  // most parts the keys of a tile are cut into
 cudaError_t launch_score_fwd_tc(ScoreArgs& s, cudaStream_t st);
+cudaError_t launch_score_bwd_tc(const ScoreArgs& s, cudaStream_t st);
+size_t score_bwd_tc_workspace_bytes(const Geometry& g, int n_q);
 size_t score_fwd_workspace_bytes(const Geometry& g, int n_q);
 size_t score_bwd_workspace_bytes(const Geometry& g, int n_q);
 cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st);

@@ -625,7 +625,9 @@ size_t score_fwd_workspace_bytes(const Geometry& g, int n_q) {
   return align_up(rows * g.d * 4, 256) + align_up(rows * 4, 256);
 }
 
-size_t score_bwd_workspace_bytes(const Geometry& g, int n_q) { return align_up((size_t)g.Hq * n_q * 4, 256); }
+size_t score_bwd_workspace_bytes(const Geometry& g, int n_q) {
+  return tc_supported(g) ? score_bwd_tc_workspace_bytes(g, n_q) : align_up((size_t)g.Hq * n_q * 4, 256);
+}
 
 cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st) {
   const int limit = parts_limit(s.a.g, s.a.n_q);
@@ -647,6 +649,7 @@ cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st) {
 }
 
 cudaError_t launch_score_bwd(const ScoreArgs& s, cudaStream_t st) {
+  if (tc_supported(s.a.g)) return launch_score_bwd_tc(s, st);
   return s.a.g.dtype == OOMB_FP32 ? bwd_simt<float>(s, st) : bwd_simt<__nv_bfloat16>(s, st);
 }
 
