@@ -122,7 +122,8 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a Stream object costs microseconds
+        return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -139,25 +140,38 @@ def _ok(name: str, st: int):
 _pools = {}
 
 
-def _need(func: str, name: str, t, shape=None, dtype=None, optional: bool = False):
-    """Refuses a tensor that a kernel would misread: not on the current CUDA device, not
-    contiguous, of another shape (None: any extent) or dtype.  Returns the tensor."""
+def _need(func: str, name: str, t, shape, dtype, dev: int) -> int:
+    """Address of a tensor that a kernel reads or writes as it is: on CUDA device ``dev``,
+    contiguous, of this shape and dtype.  Anything else is refused."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t is None:
-        if optional:
-            return None
         raise ValueError(f"{func}: {name} is missing")
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{func}: {name} has to be a tensor, not {type(t).__name__}")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{func}: {name} is on {t.device}, not on the current CUDA device")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{func}: {name} has to be {dtype}, not {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape))):
+    if t.shape != shape:
         raise ValueError(f"{func}: {name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{func}: {name} is not contiguous")
-    return t
+    if t.get_device() != dev:
+        raise ValueError(f"{func}: {name} is on {t.device}, not on the current CUDA device")
+    raise ValueError(f"{func}: {name} is not contiguous")
+
+
+def _opt(func: str, name: str, t, shape, dtype, dev: int) -> Optional[int]:
+    return None if t is None else _need(func, name, t, shape, dtype, dev)
+
+
+def _dims(func: str, name: str, t, n: int):
+    """Shape of a tensor that sets the sizes the others are checked against."""
+    if t is None or t.dim() != n:
+        raise ValueError(f"{func}: {name} has to have {n} dimensions")
+    return t.shape
+
+
+def _scratch(func: str, t, dev: int):
+    """Address and bytes of a workspace (None: no bytes)."""
+    if t is None:
+        return None, 0
+    return _need(func, "workspace", t, t.shape, t.dtype, dev), t.numel() * t.element_size()
 
 
 # ---------------------------------------------------------------- entry points
@@ -239,58 +253,59 @@ def oomb_chunk_attn_bwd(pool: int, q, o, d_o, lse, q_start: int, sel, sel_count,
 
 
 def _score_call(func: str, pool: int, q, rows, lse, sel, sel_count, workspace, softcap, slopes, key_begin, key_end):
-    """Checks the tensors of a score_attn call; (n_q, ScoreMod, workspace bytes)."""
+    """Checks the tensors of a score_attn call; (n_q, max_sel, ScoreMod, addresses by name)."""
     import torch
     if pool not in _pools:
         raise ValueError(f"{func}: not a live pool")
     Hq, Hkv, d, code = _pools[pool]
-    dt = torch.float32 if code == OOMB_FP32 else torch.bfloat16
-    _need(func, "q", q, (None, Hq, d), dt)
-    n = q.shape[0]
+    dt, i32, f32, i64 = (torch.float32 if code == OOMB_FP32 else torch.bfloat16), torch.int32, torch.float32, torch.int64
+    dev = torch.cuda.current_device()
+    n = _dims(func, "q", q, 3)[0]
+    shape = (n, Hq, d)
+    at = {"q": _need(func, "q", q, shape, dt, dev)}
     for name, t in rows.items():
-        _need(func, name, t, (n, Hq, d), dt)
-    _need(func, "lse", lse, (Hq, n), torch.float32)
-    _need(func, "sel", sel, (Hkv, None), torch.int32)
-    _need(func, "sel_count", sel_count, (Hkv,), torch.int32)
-    mod = ScoreMod(softcap, _ptr(_need(func, "slopes", slopes, (Hq,), torch.float32, True)),
-                   _ptr(_need(func, "key_begin", key_begin, (n,), torch.int64, True)),
-                   _ptr(_need(func, "key_end", key_end, (n,), torch.int64, True)))
-    _need(func, "workspace", workspace, optional=True)
-    return n, mod, 0 if workspace is None else workspace.numel() * workspace.element_size()
+        at[name] = _need(func, name, t, shape, dt, dev)
+    at["lse"] = _need(func, "lse", lse, (Hq, n), f32, dev)
+    max_sel = _dims(func, "sel", sel, 2)[1]
+    at["sel"] = _need(func, "sel", sel, (Hkv, max_sel), i32, dev)
+    at["sel_count"] = _need(func, "sel_count", sel_count, (Hkv,), i32, dev)
+    mod = ScoreMod(softcap, _opt(func, "slopes", slopes, (Hq,), f32, dev),
+                   _opt(func, "key_begin", key_begin, (n,), i64, dev), _opt(func, "key_end", key_end, (n,), i64, dev))
+    at["ws"], at["ws_bytes"] = _scratch(func, workspace, dev)
+    return n, max_sel, mod, at
 
 
 def oomb_score_attn_fwd(pool: int, q, q_start: int, sel, sel_count, softmax_scale: float, o, lse, workspace=None,
                         softcap: float = 0.0, slopes=None, key_begin=None, key_end=None, stream=None) -> None:
     """oomb_chunk_attn_fwd with capped scores, a distance bias and per-row key ranges."""
-    n, mod, ws_bytes = _score_call("oomb_score_attn_fwd", pool, q, {"o": o}, lse, sel, sel_count, workspace, softcap,
-                                   slopes, key_begin, key_end)
-    _ok("oomb_score_attn_fwd", load().oomb_score_attn_fwd(pool, _ptr(q), q_start, n, _ptr(sel), _ptr(sel_count),
-                                                          sel.shape[-1], softmax_scale, C.byref(mod), _ptr(o),
-                                                          _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
+    n, max_sel, mod, at = _score_call("oomb_score_attn_fwd", pool, q, {"o": o}, lse, sel, sel_count, workspace, softcap,
+                                      slopes, key_begin, key_end)
+    _ok("oomb_score_attn_fwd", load().oomb_score_attn_fwd(pool, at["q"], q_start, n, at["sel"], at["sel_count"], max_sel,
+                                                          softmax_scale, C.byref(mod), at["o"], at["lse"], at["ws"],
+                                                          at["ws_bytes"], _stream(stream)))
 
 
 def oomb_score_attn_bwd(pool: int, q, o, d_o, lse, q_start: int, sel, sel_count, softmax_scale: float, dq, workspace,
                         softcap: float = 0.0, slopes=None, key_begin=None, key_end=None, stream=None) -> None:
     """The backward of oomb_score_attn_fwd: dq written, dK/dV added into the gradient pools."""
-    n, mod, ws_bytes = _score_call("oomb_score_attn_bwd", pool, q, {"o": o, "d_o": d_o, "dq": dq}, lse, sel,
-                                   sel_count, workspace, softcap, slopes, key_begin, key_end)
-    _ok("oomb_score_attn_bwd", load().oomb_score_attn_bwd(pool, _ptr(q), _ptr(o), _ptr(d_o), _ptr(lse), q_start, n,
-                                                          _ptr(sel), _ptr(sel_count), sel.shape[-1], softmax_scale,
-                                                          C.byref(mod), _ptr(dq), _ptr(workspace), ws_bytes,
+    n, max_sel, mod, at = _score_call("oomb_score_attn_bwd", pool, q, {"o": o, "d_o": d_o, "dq": dq}, lse, sel,
+                                      sel_count, workspace, softcap, slopes, key_begin, key_end)
+    _ok("oomb_score_attn_bwd", load().oomb_score_attn_bwd(pool, at["q"], at["o"], at["d_o"], at["lse"], q_start, n,
+                                                          at["sel"], at["sel_count"], max_sel, softmax_scale,
+                                                          C.byref(mod), at["dq"], at["ws"], at["ws_bytes"],
                                                           _stream(stream)))
 
 
 def oomb_doc_spans(doc_start, q_start: int, key_begin, key_end, prefix_len=None, stream=None) -> None:
     """Key ranges of packed documents (boundaries doc_start [n_docs + 1], optional prefix_len [n_docs])."""
     import torch
-    f = "oomb_doc_spans"
-    _need(f, "doc_start", doc_start, (None,), torch.int64)
-    n_docs = doc_start.shape[0] - 1
-    _need(f, "prefix_len", prefix_len, (n_docs,), torch.int64, True)
-    _need(f, "key_begin", key_begin, (None,), torch.int64)
-    _need(f, "key_end", key_end, (key_begin.shape[0],), torch.int64)
-    _ok(f, load().oomb_doc_spans(_ptr(doc_start), _ptr(prefix_len), n_docs, q_start, key_begin.shape[0],
-                                 _ptr(key_begin), _ptr(key_end), _stream(stream)))
+    f, dev, i64 = "oomb_doc_spans", torch.cuda.current_device(), torch.int64
+    n_docs = _dims(f, "doc_start", doc_start, 1)[0] - 1
+    n = _dims(f, "key_begin", key_begin, 1)[0]
+    _ok(f, load().oomb_doc_spans(_need(f, "doc_start", doc_start, (n_docs + 1,), i64, dev),
+                                 _opt(f, "prefix_len", prefix_len, (n_docs,), i64, dev), n_docs, q_start, n,
+                                 _need(f, "key_begin", key_begin, (n,), i64, dev),
+                                 _need(f, "key_end", key_end, (n,), i64, dev), _stream(stream)))
 
 
 def oomb_prefetch(pool: int, sel, sel_count, stage_buf: int, stream=None) -> None:
@@ -330,53 +345,50 @@ def oomb_bias_rope_axes(x_in, bias, x_out, n_heads: int, positions, pair_axis, t
                         own_ladder: bool = False, stream=None) -> None:
     """oomb_bias_rope with positions [n_axes, n] (int64); pair_axis[j] is the axis of pair j (d/2 entries)."""
     import torch
-    f = "oomb_bias_rope_axes"
-    _need(f, "x_in", x_in)
-    _need(f, "x_out", x_out)
-    n = x_in.shape[0] if x_in.dim() else 0
-    if n <= 0 or n_heads <= 0 or x_in.numel() % (n * n_heads) or x_out.numel() != x_in.numel():
+    f, dev = "oomb_bias_rope_axes", torch.cuda.current_device()
+    ti, to = _dtype_code(x_in), _dtype_code(x_out)
+    total, n = x_in.numel(), x_in.shape[0] if x_in.dim() else 0
+    if n <= 0 or n_heads <= 0 or total == 0 or total % (n * n_heads) or x_out.numel() != total:
         raise ValueError(f"{f}: x_in {tuple(x_in.shape)} and x_out {tuple(x_out.shape)} do not hold rows of "
                          f"{n_heads} heads")
-    d = x_in.numel() // (n * n_heads)
-    _need(f, "bias", None if bias is None else bias.view(-1), (n_heads * d,), torch.float32, True)
-    axes, n_axes = None, 0
+    d = total // (n * n_heads)
+    a_in, a_out = _need(f, "x_in", x_in, x_in.shape, x_in.dtype, dev), _need(f, "x_out", x_out, x_out.shape, x_out.dtype, dev)
+    if bias is not None and bias.numel() != n_heads * d:
+        raise ValueError(f"{f}: bias has {bias.numel()} elements, needs {n_heads * d}")
+    a_bias = None if bias is None else _need(f, "bias", bias, bias.shape, torch.float32, dev)
+    axes, a_pos, n_axes = None, None, 0
     if mode != 0:
         axes = bytes(pair_axis)
         if 2 * len(axes) != d:
             raise ValueError(f"{f}: pair_axis has {len(axes)} entries, needs {d // 2}")
-        _need(f, "positions", positions, (None, n), torch.int64)
-        n_axes = positions.shape[0]
-    _ok(f, load().oomb_bias_rope_axes(_ptr(x_in), _dtype_code(x_in), _ptr(bias), _ptr(x_out), _dtype_code(x_out), n,
-                                      n_heads, d, _ptr(positions) if mode != 0 else None, n_axes, axes, theta,
+        n_axes = _dims(f, "positions", positions, 2)[0]
+        a_pos = _need(f, "positions", positions, (n_axes, n), torch.int64, dev)
+    _ok(f, load().oomb_bias_rope_axes(a_in, ti, a_bias, a_out, to, n, n_heads, d, a_pos, n_axes, axes, theta,
                                       int(own_ladder), mode, _stream(stream)))
 
 
-def _norm_call(f: str, x, y, w_pre, w_post, gate):
-    """Checks the inputs common to both directions; (n, D, dtype, gate_rows)."""
+def _norm_call(f: str, x, y, w_pre, w_post, gate, dev: int):
+    """Checks the inputs common to both directions; (n, D, gate_rows, addresses)."""
     import torch
-    _need(f, "x", x, (None, None))
-    n, D = x.shape
-    _need(f, "y", y, (n, D), x.dtype, True)
-    _need(f, "w_pre", w_pre, (D,), torch.float32, True)
-    _need(f, "w_post", w_post, (D,), torch.float32, True)
+    f32, dt = torch.float32, x.dtype
+    n, D = shape = _dims(f, "x", x, 2)
     rows = gate is not None and gate.dim() == 2
-    _need(f, "gate", gate, (n, D) if rows else (D,), x.dtype if rows else torch.float32, True)
-    return n, D, x.dtype, int(rows)
+    return n, D, int(rows), (_need(f, "x", x, shape, dt, dev), _opt(f, "y", y, shape, dt, dev),
+                             _opt(f, "w_post", w_post, (D,), f32, dev),
+                             _opt(f, "gate", gate, shape if rows else (D,), dt if rows else f32, dev),
+                             _opt(f, "w_pre", w_pre, (D,), f32, dev))
 
 
 def oomb_block_norm_fwd(x, y, x_out, u=None, w_pre=None, w_post=None, gate=None, res_scale: float = 1.0,
                         eps: float = 1e-6, rstd_pre=None, rstd_post=None, stream=None) -> None:
     """x_out = x + res_scale * gate * norm(y; w_post), u = norm(x_out; w_pre).  gate: fp32 [D] or [n, D] like x."""
     import torch
-    f = "oomb_block_norm_fwd"
-    n, D, dt, rows = _norm_call(f, x, y, w_pre, w_post, gate)
-    _need(f, "x_out", x_out, (n, D), dt, True)
-    _need(f, "u", u, (n, D), dt, True)
-    _need(f, "rstd_pre", rstd_pre, (n,), torch.float32, True)
-    _need(f, "rstd_post", rstd_post, (n,), torch.float32, True)
-    _ok(f, load().oomb_block_norm_fwd(_ptr(x), _ptr(y), _ptr(w_post), _ptr(gate), rows, _ptr(w_pre), res_scale, eps,
-                                      n, D, _dtype_code(x), _ptr(x_out), _ptr(u), _ptr(rstd_post), _ptr(rstd_pre),
-                                      _stream(stream)))
+    f, dev, f32, dt = "oomb_block_norm_fwd", torch.cuda.current_device(), torch.float32, x.dtype
+    n, D, rows, (ax, ay, awp, ag, aw) = _norm_call(f, x, y, w_pre, w_post, gate, dev)
+    _ok(f, load().oomb_block_norm_fwd(ax, ay, awp, ag, rows, aw, res_scale, eps, n, D, _dtype_code(x),
+                                      _opt(f, "x_out", x_out, (n, D), dt, dev), _opt(f, "u", u, (n, D), dt, dev),
+                                      _opt(f, "rstd_post", rstd_post, (n,), f32, dev),
+                                      _opt(f, "rstd_pre", rstd_pre, (n,), f32, dev), _stream(stream)))
 
 
 def oomb_block_norm_bwd(x, y, dx, dy=None, du=None, dx_out=None, rstd_pre=None, rstd_post=None, w_pre=None,
@@ -384,20 +396,17 @@ def oomb_block_norm_bwd(x, y, dx, dy=None, du=None, dx_out=None, rstd_pre=None, 
                         accumulate: bool = False, workspace=None, stream=None) -> None:
     """The backward of oomb_block_norm_fwd; accumulate adds the parameter gradients to their buffers."""
     import torch
-    f = "oomb_block_norm_bwd"
-    n, D, dt, rows = _norm_call(f, x, y, w_pre, w_post, gate)
-    for name, t in (("dx", dx), ("dy", dy), ("du", du), ("dx_out", dx_out)):
-        _need(f, name, t, (n, D), dt, name != "dx")
-    for name, t in (("rstd_pre", rstd_pre), ("rstd_post", rstd_post)):
-        _need(f, name, t, (n,), torch.float32, True)
-    for name, t in (("dw_pre", dw_pre), ("dw_post", dw_post)):
-        _need(f, name, t, (D,), torch.float32, True)
-    _need(f, "dgate", dgate, (n, D) if rows else (D,), dt if rows else torch.float32, True)
-    _need(f, "workspace", workspace)
-    _ok(f, load().oomb_block_norm_bwd(_ptr(x), _ptr(y), _ptr(w_post), _ptr(gate), rows, _ptr(w_pre), res_scale, n, D,
-                                      _dtype_code(x), _ptr(rstd_post), _ptr(rstd_pre), _ptr(du), _ptr(dx_out),
-                                      _ptr(dx), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre), int(accumulate),
-                                      _ptr(workspace), workspace.numel() * workspace.element_size(),
+    f, dev, f32, dt = "oomb_block_norm_bwd", torch.cuda.current_device(), torch.float32, x.dtype
+    n, D, rows, (ax, ay, awp, ag, aw) = _norm_call(f, x, y, w_pre, w_post, gate, dev)
+    shape = (n, D)
+    ws, ws_bytes = _scratch(f, workspace, dev)
+    _ok(f, load().oomb_block_norm_bwd(ax, ay, awp, ag, rows, aw, res_scale, n, D, _dtype_code(x),
+                                      _opt(f, "rstd_post", rstd_post, (n,), f32, dev),
+                                      _opt(f, "rstd_pre", rstd_pre, (n,), f32, dev), _opt(f, "du", du, shape, dt, dev),
+                                      _opt(f, "dx_out", dx_out, shape, dt, dev), _need(f, "dx", dx, shape, dt, dev),
+                                      _opt(f, "dy", dy, shape, dt, dev), _opt(f, "dw_post", dw_post, (D,), f32, dev),
+                                      _opt(f, "dgate", dgate, shape if rows else (D,), dt if rows else f32, dev),
+                                      _opt(f, "dw_pre", dw_pre, (D,), f32, dev), int(accumulate), ws, ws_bytes,
                                       _stream(stream)))
 
 

@@ -21,6 +21,7 @@
 
 #include "attn_common.cuh"
 #include "block_norm.h"
+#include "sm103_ptx.cuh"
 
 namespace oomb {
 namespace {
@@ -84,7 +85,7 @@ __device__ __forceinline__ void load_param(const float* p, int c, float (&f)[E],
 
 // ------------------------------------------------------------------ forward
 template <typename T, int E>
-__global__ void __launch_bounds__(16384 / E < 1024 ? 16384 / E : 1024) norm_fwd(const NormArgs a) {
+__global__ void __launch_bounds__(1024, 1) norm_fwd(const NormArgs a) {
   __shared__ float buf[64];
   int turn = 0;
   const int c = threadIdx.x * E;
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kSlowThreads) norm_fwd_any(const NormArgs a) {
 // A block's three sums of a column, in shared memory: [dw_pre | dw_post | dgate] x D.  Each
 // column belongs to one thread.
 template <typename T, int E>
-__global__ void __launch_bounds__(16384 / E < 1024 ? 16384 / E : 1024) norm_bwd(const NormArgs a) {
+__global__ void __launch_bounds__(1024, 1) norm_bwd(const NormArgs a) {
   extern __shared__ __align__(16) float acc[];
   __shared__ float buf[64];
   int turn = 0;
@@ -368,6 +369,237 @@ __global__ void __launch_bounds__(256) norm_join(const float* __restrict__ part,
   }
 }
 
+// ------------------------------------------------------------ rows through a ring
+// Many rows: a block walks its rows with the next ones in flight.  One thread copies whole
+// rows of every tensor that is read (cp.async.bulk) into a ring of kept stages in shared
+// memory; the threads wait for a stage, take their elements into registers and hand the stage
+// back.  So a block keeps stages x tensors x row bytes of loads in flight whatever its barriers
+// wait for, and two blocks of an SM hide each other's sums.
+constexpr int kMaxStages = 4;
+constexpr int kMaxRowTensors = 5;
+
+struct RowRing {
+  const char* src[kMaxRowTensors];  // tensors read, in the order they stand in a stage
+  int n_src;
+  uint32_t row_bytes;
+  int stages;
+};
+
+struct __align__(16) RingBars {
+  uint64_t full[kMaxStages];
+};
+
+__device__ __forceinline__ void ring_issue(const RowRing& r, uint8_t* base, RingBars* bars, int64_t row, int k) {
+  mbar_arrive_expect_tx(&bars->full[k], r.row_bytes * (uint32_t)r.n_src);
+  uint8_t* dst = base + (size_t)k * r.n_src * r.row_bytes;
+  for (int i = 0; i < r.n_src; ++i)
+    bulk_load(dst + (size_t)i * r.row_bytes, r.src[i] + (size_t)row * r.row_bytes, r.row_bytes, &bars->full[k]);
+}
+
+// Sets the ring up and starts the first rows' copies.
+__device__ __forceinline__ void ring_start(const RowRing& r, uint8_t* base, RingBars* bars, int64_t n) {
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < r.stages; ++k) mbar_init(&bars->full[k], 1);
+    fence_mbar_init();
+    for (int k = 0; k < r.stages; ++k) {
+      const int64_t row = blockIdx.x + (int64_t)k * gridDim.x;
+      if (row < n) ring_issue(r, base, bars, row, k);
+    }
+  }
+  __syncthreads();
+}
+
+template <typename T, int E>
+__global__ void __launch_bounds__(512, E == 8 ? 2 : 1)
+    norm_fwd_ring(const __grid_constant__ NormArgs a, const __grid_constant__ RowRing ring) {
+  extern __shared__ __align__(128) uint8_t stage_mem[];
+  __shared__ RingBars bars;
+  __shared__ float buf[64];
+  int turn = 0, k = 0;
+  uint32_t phase = 0;
+  const int c = threadIdx.x * E;
+  const bool in = c < a.D;
+  const bool row_gate = a.gate && a.gate_rows;
+  ring_start(ring, stage_mem, &bars, a.n);
+  float wp[E], g[E], w[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) wp[e] = g[e] = w[e] = 0.f;
+  if (in) {
+    load_param<E>(a.w_post, c, wp, 1.f);
+    load_param<E>(row_gate ? nullptr : reinterpret_cast<const float*>(a.gate), c, g, 1.f);
+    load_param<E>(a.w_pre, c, w, 1.f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) wp[e] *= a.res_scale * g[e];  // one factor for z on its way to x'
+  }
+  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+    float f[E], r[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = r[e] = 0.f;
+    if (!mbar_wait(&bars.full[k], phase, nullptr)) return;  // the copy cannot fail to end
+    const T* st = reinterpret_cast<const T*>(stage_mem + (size_t)k * ring.n_src * ring.row_bytes) + c;
+    if (in) {
+      load_vec<T, E>(st, f);
+      if (a.y) load_vec<T, E>(st + a.D, r);
+      if (row_gate) load_vec<T, E>(st + 2 * a.D, g);
+    }
+    __syncthreads();
+    const int64_t later = row + (int64_t)ring.stages * gridDim.x;
+    if (threadIdx.x == 0 && later < a.n) ring_issue(ring, stage_mem, &bars, later, k);
+    if (++k == ring.stages) {
+      k = 0;
+      phase ^= 1;
+    }
+    const size_t at = (size_t)row * a.D + c;
+    if (a.y) {
+      float rstd = 1.f;
+      if (a.w_post) {
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s += r[e] * r[e];
+        rstd = rsqrtf(block_sum(s, buf, turn) * a.inv_D + a.eps);
+        if (a.rstd_post && threadIdx.x == 0) a.rstd_post[row] = rstd;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = fmaf(r[e] * rstd, row_gate ? wp[e] * g[e] : wp[e], f[e]);
+    }
+    if (a.x_out && in) store_vec<T, E>(reinterpret_cast<T*>(a.x_out) + at, f);
+    if (a.w_pre) {
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) s += f[e] * f[e];
+      const float rstd = rsqrtf(block_sum(s, buf, turn) * a.inv_D + a.eps);
+      if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[row] = rstd;
+      if (in) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] *= rstd * w[e];
+        store_vec<T, E>(reinterpret_cast<T*>(a.u) + at, f);
+      }
+    }
+  }
+}
+
+// The parameters stay in shared memory ([w_pre | res_scale g | w_post] x D fp32, a thread reads
+// its own columns), the sums of their gradients in registers.
+template <typename T, int E>
+__global__ void __launch_bounds__(512, E == 8 ? 2 : 1)
+    norm_bwd_ring(const __grid_constant__ NormArgs a, const __grid_constant__ RowRing ring) {
+  extern __shared__ __align__(128) uint8_t stage_mem[];
+  __shared__ RingBars bars;
+  __shared__ float buf[64];
+  int turn = 0, k = 0;
+  uint32_t phase = 0;
+  const int c = threadIdx.x * E;
+  const bool in = c < a.D;
+  const bool row_gate = a.gate && a.gate_rows, pre = a.w_pre != nullptr, post = a.w_post != nullptr;
+  float* par = reinterpret_cast<float*>(stage_mem + (size_t)ring.stages * ring.n_src * ring.row_bytes);
+  ring_start(ring, stage_mem, &bars, a.n);
+  if (in) {
+    float f[E];
+    load_param<E>(a.w_pre, c, f, 1.f);
+    store_vec<float, E>(par + c, f);
+    load_param<E>(row_gate ? nullptr : reinterpret_cast<const float*>(a.gate), c, f, 1.f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] *= a.res_scale;
+    store_vec<float, E>(par + a.D + c, f);
+    load_param<E>(a.w_post, c, f, 1.f);
+    store_vec<float, E>(par + 2 * a.D + c, f);
+  }
+  // stage order: x (with a pre-norm), y, du, dx', gate rows, each where it is read
+  const int at_y = pre ? 1 : 0, at_du = at_y + (a.y ? 1 : 0), at_dx = at_du + (pre ? 1 : 0),
+            at_g = at_dx + (a.dx_in ? 1 : 0);
+  float a_pre[E], a_post[E], a_gate[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) a_pre[e] = a_post[e] = a_gate[e] = 0.f;
+  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+    const float r_post = post ? a.rstd_post[row] : 1.f, r_pre = pre ? a.rstd_pre[row] : 1.f;
+    float xn[E], yn[E], dx[E], t[E], g[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) xn[e] = yn[e] = dx[e] = t[e] = g[e] = 0.f;
+    if (!mbar_wait(&bars.full[k], phase, nullptr)) return;  // the copy cannot fail to end
+    const T* st = reinterpret_cast<const T*>(stage_mem + (size_t)k * ring.n_src * ring.row_bytes) + c;
+    if (in) {
+      if (pre) {
+        load_vec<T, E>(st, xn);
+        load_vec<T, E>(st + at_du * a.D, t);
+      }
+      if (a.y) load_vec<T, E>(st + at_y * a.D, yn);
+      if (a.dx_in) load_vec<T, E>(st + at_dx * a.D, dx);
+      load_vec<float, E>(par + a.D + c, g);
+      if (row_gate) {
+        float gr[E];
+        load_vec<T, E>(st + at_g * a.D, gr);
+#pragma unroll
+        for (int e = 0; e < E; ++e) g[e] *= gr[e];
+      }
+    }
+    __syncthreads();
+    const int64_t later = row + (int64_t)ring.stages * gridDim.x;
+    if (threadIdx.x == 0 && later < a.n) ring_issue(ring, stage_mem, &bars, later, k);
+    if (++k == ring.stages) {
+      k = 0;
+      phase ^= 1;
+    }
+    const size_t at = (size_t)row * a.D + c;
+#pragma unroll
+    for (int e = 0; e < E; ++e) yn[e] *= r_post;
+    if (pre) {
+      float s = 0.f;
+      if (in) {
+        float w[E];
+        if (a.y) {
+          load_vec<float, E>(par + 2 * a.D + c, w);
+#pragma unroll
+          for (int e = 0; e < E; ++e) xn[e] = fmaf(g[e], yn[e] * w[e], xn[e]);
+        }
+        load_vec<float, E>(par + c, w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          xn[e] *= r_pre;
+          a_pre[e] = fmaf(t[e], xn[e], a_pre[e]);
+          t[e] *= w[e];
+          s = fmaf(t[e], xn[e], s);
+        }
+      }
+      const float mean = block_sum(s, buf, turn) * a.inv_D;
+#pragma unroll
+      for (int e = 0; e < E; ++e) dx[e] = fmaf(r_pre, t[e] - xn[e] * mean, dx[e]);
+    }
+    if (in && a.dx) store_vec<T, E>(reinterpret_cast<T*>(a.dx) + at, dx);
+    if (!a.y) continue;
+    float s = 0.f;
+    if (in) {
+      float w[E];
+      load_vec<float, E>(par + 2 * a.D + c, w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float z = yn[e] * w[e], dgz = a.res_scale * dx[e], dz = g[e] * dx[e];
+        t[e] = dgz * z;                                // gradient of the gate
+        a_post[e] = fmaf(dz, yn[e], a_post[e]);
+        dx[e] = dz * w[e];
+        s = fmaf(dx[e], yn[e], s);
+      }
+      if (row_gate && a.dgate) {
+        store_vec<T, E>(reinterpret_cast<T*>(a.dgate) + at, t);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) a_gate[e] += t[e];
+      }
+    }
+    if (post) {
+      const float mean = block_sum(s, buf, turn) * a.inv_D;
+#pragma unroll
+      for (int e = 0; e < E; ++e) dx[e] = r_post * (dx[e] - yn[e] * mean);
+    }
+    if (in && a.dy) store_vec<T, E>(reinterpret_cast<T*>(a.dy) + at, dx);
+  }
+  if (in) {
+    float* dst = a.part + (size_t)blockIdx.x * 3 * a.D + c;
+    store_vec<float, E>(dst, a_pre);
+    store_vec<float, E>(dst + a.D, a_post);
+    store_vec<float, E>(dst + 2 * a.D, a_gate);
+  }
+}
+
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Elements a thread holds in the 16-byte variant: 1024 threads have to span a row.
@@ -385,15 +617,62 @@ bool vector_rows(const NormArgs& a) {
 
 int threads_for(int D, int E) { return (int)align_up((size_t)((D + E - 1) / E), 32); }
 
+// Rows through the ring where every block has at least four of them to walk and a stage
+// fits; else a row is read straight into registers.
+constexpr size_t kRingBytes = 200 * 1024;  // of an SM's shared memory, for all its blocks' stages
+bool ring_setup(const NormArgs& a, size_t es, bool backward, RowRing* r, unsigned* grid, size_t* smem) {
+  if (a.D > 8192) return false;
+  const int E = a.D <= 4096 ? 8 : 16, T = threads_for(a.D, E);
+  auto add = [&](const void* p) {
+    if (p) r->src[r->n_src++] = reinterpret_cast<const char*>(p);
+  };
+  *r = {};
+  if (backward) {
+    if (a.w_pre) add(a.x);
+    add(a.y);
+    add(a.du);
+    add(a.dx_in);
+  } else {
+    add(a.x);
+    add(a.y);
+  }
+  if (a.gate_rows) add(a.gate);
+  const size_t bytes = es * a.D;
+  r->row_bytes = (uint32_t)bytes;
+  const int per_sm = norm_blocks_per_sm(T);
+  const int64_t blocks = std::min<int64_t>(a.n, (int64_t)per_sm * device_sm_count());
+  if (a.n < 4 * blocks) return false;
+  const size_t fixed = backward ? (size_t)3 * a.D * 4 : 0, room = kRingBytes / per_sm;
+  if (room < fixed + 2 * bytes * r->n_src) return false;
+  r->stages = (int)std::min<size_t>(kMaxStages, (room - fixed) / (bytes * r->n_src));
+  *grid = (unsigned)blocks;
+  *smem = r->stages * bytes * r->n_src + fixed;
+  return true;
+}
+
 template <typename T>
 cudaError_t fwd(const NormArgs& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)std::min<int64_t>(a.n, 1 << 20);
-  if (!vector_rows(a))
-    norm_fwd_any<T><<<grid, kSlowThreads, 0, st>>>(a);
-  else if (elements(a.D) == 8)
-    norm_fwd<T, 8><<<grid, threads_for(a.D, 8), 0, st>>>(a);
-  else
-    norm_fwd<T, 16><<<grid, threads_for(a.D, 16), 0, st>>>(a);
+  static size_t set8[kMaxDevices] = {}, set16[kMaxDevices] = {};
+  const unsigned rows = (unsigned)std::min<int64_t>(a.n, 1 << 20);
+  RowRing ring;
+  unsigned grid;
+  size_t smem;
+  if (!vector_rows(a)) {
+    norm_fwd_any<T><<<rows, kSlowThreads, 0, st>>>(a);
+  } else if (ring_setup(a, sizeof(T), false, &ring, &grid, &smem)) {
+    const bool narrow = a.D <= 4096;
+    cudaError_t e = narrow ? set_smem_limit((const void*)norm_fwd_ring<T, 8>, kRingBytes, set8)
+                           : set_smem_limit((const void*)norm_fwd_ring<T, 16>, kRingBytes, set16);
+    if (e != cudaSuccess) return e;
+    if (narrow)
+      norm_fwd_ring<T, 8><<<grid, threads_for(a.D, 8), smem, st>>>(a, ring);
+    else
+      norm_fwd_ring<T, 16><<<grid, threads_for(a.D, 16), smem, st>>>(a, ring);
+  } else if (elements(a.D) == 8) {
+    norm_fwd<T, 8><<<rows, threads_for(a.D, 8), 0, st>>>(a);
+  } else {
+    norm_fwd<T, 16><<<rows, threads_for(a.D, 16), 0, st>>>(a);
+  }
   count_launches(1);
   return cudaGetLastError();
 }
@@ -401,13 +680,24 @@ cudaError_t fwd(const NormArgs& a, cudaStream_t st) {
 template <typename T>
 cudaError_t bwd(const NormArgs& a, cudaStream_t st) {
   static size_t set8[kMaxDevices] = {}, set16[kMaxDevices] = {}, set_any[kMaxDevices] = {};
-  const size_t smem = (size_t)3 * a.D * 4;
-  const int grid = norm_parts(a.n, a.D);
+  static size_t ring8[kMaxDevices] = {}, ring16[kMaxDevices] = {};
+  size_t smem = (size_t)3 * a.D * 4;
+  unsigned grid = (unsigned)norm_parts(a.n, a.D);
+  RowRing ring;
   cudaError_t e;
   if (!vector_rows(a)) {
     e = set_smem_limit((const void*)norm_bwd_any<T>, (size_t)3 * kMaxWidth * 4, set_any);
     if (e != cudaSuccess) return e;
     norm_bwd_any<T><<<grid, kSlowThreads, smem, st>>>(a);
+  } else if (ring_setup(a, sizeof(T), true, &ring, &grid, &smem)) {
+    const bool narrow = a.D <= 4096;
+    e = narrow ? set_smem_limit((const void*)norm_bwd_ring<T, 8>, kRingBytes, ring8)
+               : set_smem_limit((const void*)norm_bwd_ring<T, 16>, kRingBytes, ring16);
+    if (e != cudaSuccess) return e;
+    if (narrow)
+      norm_bwd_ring<T, 8><<<grid, threads_for(a.D, 8), smem, st>>>(a, ring);
+    else
+      norm_bwd_ring<T, 16><<<grid, threads_for(a.D, 16), smem, st>>>(a, ring);
   } else if (elements(a.D) == 8) {
     e = set_smem_limit((const void*)norm_bwd<T, 8>, (size_t)3 * 8192 * 4, set8);
     if (e != cudaSuccess) return e;
@@ -422,7 +712,8 @@ cudaError_t bwd(const NormArgs& a, cudaStream_t st) {
   count_launches(1);
   float* dgate = a.gate && !a.gate_rows ? reinterpret_cast<float*>(a.dgate) : nullptr;
   if (a.dw_pre || a.dw_post || dgate) {
-    norm_join<<<dim3((a.D + 31) / 32, 3), 256, 0, st>>>(a.part, grid, a.D, a.dw_pre, a.dw_post, dgate, a.accumulate);
+    norm_join<<<dim3((a.D + 31) / 32, 3), 256, 0, st>>>(a.part, (int)grid, a.D, a.dw_pre, a.dw_post, dgate,
+                                                        a.accumulate);
     count_launches(1);
   }
   return cudaGetLastError();
@@ -430,9 +721,13 @@ cudaError_t bwd(const NormArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+// Thread blocks of T threads on an SM: about 28 warps, at most 8 blocks.
+int norm_blocks_per_sm(int T) { return std::max(1, std::min(8, 1024 / T)); }
+
 int norm_parts(int64_t n, int D) {
-  (void)D;
-  return (int)std::min<int64_t>(n, 2 * (int64_t)device_sm_count());
+  const int E = D <= 4096 ? 8 : 16;
+  return (int)std::min<int64_t>(n, (int64_t)norm_blocks_per_sm((int)align_up((size_t)((D + E - 1) / E), 32)) *
+                                       device_sm_count());
 }
 
 }  // namespace oomb

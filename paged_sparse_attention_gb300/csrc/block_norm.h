@@ -30,6 +30,7 @@ struct NormArgs {
   float* part;         // [norm_parts, 3, D]
 };
 
+int norm_blocks_per_sm(int T);
 // Thread blocks of the backward, each with its own partial weight gradients.
 int norm_parts(int64_t n, int D);
 

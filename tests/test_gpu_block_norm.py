@@ -150,6 +150,18 @@ def test_rows(n):
     compare(run(t, -1.5, 1e-5, BF), ref, tol)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("n,D", [(1301, 3584), (2001, 2048), (5003, 256), (2501, 4112), (1303, 8192)])
+@pytest.mark.parametrize("kw", [dict(gate="channel", post=True), dict(gate="token", post=True, dx_out=False),
+                                dict(gate="none", post=False), dict(gate="none", post=False, block=False),
+                                dict(gate="token", post=True, pre=False)])
+def test_many_rows(dtype, n, D, kw):
+    """Enough rows for each thread block to walk several."""
+    t = make(n, D, dtype, seed=n, **kw)
+    ref, tol = reference(t, 0.7, 1e-6, dtype)
+    compare(run(t, 0.7, 1e-6, dtype), ref, tol)
+
+
 @pytest.mark.parametrize("D", [256, 255])
 @pytest.mark.parametrize("kind", ["pre_only", "post_only", "no_residual_gradient", "gate_only"])
 def test_parts_left_out(kind, D):
