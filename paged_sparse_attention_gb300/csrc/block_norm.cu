@@ -15,8 +15,8 @@
 // registers from its load to its stores: every tensor is read once and written once.  The
 // rows' sums over the weight gradients stay with the block (rows b, b + grid, ...), go to the
 // workspace once a block and are summed there in block order, so they are the same bits on
-// every run.  Widths that are no multiple of the vector, or rows off 16 bytes, take the
-// element-wise variant, which reads a row again (from L1/L2) for each pass over it.
+// every run.  Widths that are no multiple of the vector, or rows off 16 bytes, are held the same
+// way with one-element accesses, neighbouring threads on neighbouring elements.
 #include <cmath>
 
 #include "attn_common.cuh"
@@ -27,7 +27,6 @@ namespace oomb {
 namespace {
 
 constexpr int kMaxWidth = 16384;
-constexpr int kSlowThreads = 512;
 
 // Sum over the block; every thread gets it.  `buf` holds 2 x 32 floats, used in turns so that
 // one barrier a sum is enough.
@@ -83,267 +82,185 @@ __device__ __forceinline__ void load_param(const float* p, int c, float (&f)[E],
   }
 }
 
+// How a block's threads share a row.  VEC: E consecutive elements each, 16-byte accesses.  Else
+// elements threadIdx.x + e blockDim.x: any width and any alignment, still whole lines a warp.
+template <int E, bool VEC>
+struct Share {
+  int c[VEC ? 1 : E];
+  int D;
+  __device__ explicit Share(int width) : D(width) {
+    if constexpr (VEC) {
+      c[0] = threadIdx.x * E;
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) c[e] = threadIdx.x + e * blockDim.x;
+    }
+  }
+  __device__ __forceinline__ bool has(int e) const { return (VEC ? c[0] : c[e]) < D; }
+  __device__ __forceinline__ int at(int e) const { return VEC ? c[0] + e : c[e]; }
+  template <typename T>
+  __device__ __forceinline__ void load(const T* row, float (&f)[E]) const {  // absent elements are 0
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = 0.f;
+    if constexpr (VEC) {
+      if (has(0)) load_vec<T, E>(row + c[0], f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (has(e)) f[e] = to_float<T>(row[c[e]]);
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, const float (&f)[E]) const {
+    if constexpr (VEC) {
+      if (has(0)) store_vec<T, E>(row + c[0], f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (has(e)) row[c[e]] = from_float<T>(f[e]);
+    }
+  }
+  __device__ __forceinline__ void param(const float* p, float (&f)[E]) const {  // 1 where there is none
+    if (p) {
+      load<float>(p, f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = 1.f;
+    }
+  }
+};
+
+template <typename T, int E, bool VEC>
+__device__ __forceinline__ void load_gate(const NormArgs& a, const Share<E, VEC>& sh, size_t row0, float (&g)[E]) {
+  if (a.gate && a.gate_rows)
+    sh.template load<T>(reinterpret_cast<const T*>(a.gate) + row0, g);
+  else
+    sh.param(reinterpret_cast<const float*>(a.gate), g);
+}
+
 // ------------------------------------------------------------------ forward
-template <typename T, int E>
-__global__ void __launch_bounds__(1024, 1) norm_fwd(const NormArgs a) {
+template <typename T, int E, bool VEC>
+__global__ void __launch_bounds__(1024, 1) norm_fwd(const __grid_constant__ NormArgs a) {
   __shared__ float buf[64];
   int turn = 0;
-  const int c = threadIdx.x * E;
-  const bool in = c < a.D;
-  const T* y = reinterpret_cast<const T*>(a.y);
-  const T* x = reinterpret_cast<const T*>(a.x);
+  const Share<E, VEC> sh(a.D);
   for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
-    const size_t at = (size_t)row * a.D + c;
+    const size_t row0 = (size_t)row * a.D;
     float f[E], r[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = r[e] = 0.f;
-    if (in) load_vec<T, E>(x + at, f);
+    sh.template load<T>(reinterpret_cast<const T*>(a.x) + row0, f);
     if (a.y) {
-      if (in) load_vec<T, E>(y + at, r);
+      sh.template load<T>(reinterpret_cast<const T*>(a.y) + row0, r);
+      float g[E];
+      load_gate<T, E, VEC>(a, sh, row0, g);
       if (a.w_post) {
-        float s = 0.f;
+        float w[E], s = 0.f;
+        sh.param(a.w_post, w);
 #pragma unroll
         for (int e = 0; e < E; ++e) s += r[e] * r[e];
         const float rstd = rsqrtf(block_sum(s, buf, turn) * a.inv_D + a.eps);
         if (a.rstd_post && threadIdx.x == 0) a.rstd_post[row] = rstd;
-        if (in) {
-          float w[E];
-          load_param<E>(a.w_post, c, w, 1.f);
 #pragma unroll
-          for (int e = 0; e < E; ++e) r[e] *= rstd * w[e];
-        }
+        for (int e = 0; e < E; ++e) r[e] *= rstd * w[e];
       }
-      if (in) {
-        float g[E];
-        if (a.gate && a.gate_rows)
-          load_vec<T, E>(reinterpret_cast<const T*>(a.gate) + at, g);
-        else
-          load_param<E>(reinterpret_cast<const float*>(a.gate), c, g, 1.f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) f[e] += a.res_scale * g[e] * r[e];
-      }
+      for (int e = 0; e < E; ++e) f[e] += a.res_scale * g[e] * r[e];
     }
     if (a.w_pre) {
-      float s = 0.f;
+      float w[E], s = 0.f;
+      sh.param(a.w_pre, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) s += f[e] * f[e];
       const float rstd = rsqrtf(block_sum(s, buf, turn) * a.inv_D + a.eps);
       if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[row] = rstd;
-      if (in) {
-        float w[E];
-        load_param<E>(a.w_pre, c, w, 1.f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) w[e] *= f[e] * rstd;
-        store_vec<T, E>(reinterpret_cast<T*>(a.u) + at, w);
-      }
+      for (int e = 0; e < E; ++e) w[e] *= f[e] * rstd;
+      sh.template store<T>(reinterpret_cast<T*>(a.u) + row0, w);
     }
-    if (a.x_out && in) store_vec<T, E>(reinterpret_cast<T*>(a.x_out) + at, f);
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ float gate_at(const NormArgs& a, size_t at, int c) {
-  if (!a.gate) return 1.f;
-  return a.gate_rows ? to_float<T>(reinterpret_cast<const T*>(a.gate)[at]) : reinterpret_cast<const float*>(a.gate)[c];
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kSlowThreads) norm_fwd_any(const NormArgs a) {
-  __shared__ float buf[64];
-  int turn = 0;
-  const T* y = reinterpret_cast<const T*>(a.y);
-  const T* x = reinterpret_cast<const T*>(a.x);
-  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
-    const size_t at0 = (size_t)row * a.D;
-    float r_post = 1.f, r_pre = 1.f;
-    if (a.y && a.w_post) {
-      float s = 0.f;
-      for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
-        const float v = to_float<T>(y[at0 + c]);
-        s += v * v;
-      }
-      r_post = rsqrtf(block_sum(s, buf, turn) * a.inv_D + a.eps);
-      if (a.rstd_post && threadIdx.x == 0) a.rstd_post[row] = r_post;
-    }
-    auto value = [&](int c) {
-      float v = to_float<T>(x[at0 + c]);
-      if (a.y) {
-        float z = to_float<T>(y[at0 + c]);
-        if (a.w_post) z *= r_post * a.w_post[c];
-        v += a.res_scale * gate_at<T>(a, at0 + c, c) * z;
-      }
-      return v;
-    };
-    if (a.w_pre) {
-      float s = 0.f;
-      for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
-        const float v = value(c);
-        s += v * v;
-      }
-      r_pre = rsqrtf(block_sum(s, buf, turn) * a.inv_D + a.eps);
-      if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[row] = r_pre;
-    }
-    for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
-      const float v = value(c);
-      if (a.w_pre) reinterpret_cast<T*>(a.u)[at0 + c] = from_float<T>(v * r_pre * a.w_pre[c]);
-      if (a.x_out) reinterpret_cast<T*>(a.x_out)[at0 + c] = from_float<T>(v);
-    }
+    if (a.x_out) sh.template store<T>(reinterpret_cast<T*>(a.x_out) + row0, f);
   }
 }
 
 // ----------------------------------------------------------------- backward
 // A block's three sums of a column, in shared memory: [dw_pre | dw_post | dgate] x D.  Each
 // column belongs to one thread.
-template <typename T, int E>
-__global__ void __launch_bounds__(1024, 1) norm_bwd(const NormArgs a) {
+template <typename T, int E, bool VEC>
+__global__ void __launch_bounds__(1024, 1) norm_bwd(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) float acc[];
   __shared__ float buf[64];
   int turn = 0;
-  const int c = threadIdx.x * E;
-  const bool in = c < a.D;
+  const Share<E, VEC> sh(a.D);
+  const bool row_gate = a.gate && a.gate_rows;
   const bool sum_gate = a.gate && !a.gate_rows && a.dgate;
-  if (in)
+  {
+    float zero[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[c + e] = acc[a.D + c + e] = acc[2 * a.D + c + e] = 0.f;
+    for (int e = 0; e < E; ++e) zero[e] = 0.f;
+    for (int k = 0; k < 3; ++k) sh.template store<float>(acc + (size_t)k * a.D, zero);
+  }
   for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
-    const size_t at = (size_t)row * a.D + c;
-    float g[E], z[E], dx[E];
+    const size_t row0 = (size_t)row * a.D;
+    float g[E], z[E], dx[E], w[E];
     const float r_post = a.w_post ? a.rstd_post[row] : 1.f;
+    if (a.dx_in) {
+      sh.template load<T>(reinterpret_cast<const T*>(a.dx_in) + row0, dx);
+    } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e) dx[e] = z[e] = 0.f;
-    if (in && a.y) {
-      load_vec<T, E>(reinterpret_cast<const T*>(a.y) + at, z);  // y
-      if (a.gate && a.gate_rows)
-        load_vec<T, E>(reinterpret_cast<const T*>(a.gate) + at, g);
-      else
-        load_param<E>(reinterpret_cast<const float*>(a.gate), c, g, 1.f);
+      for (int e = 0; e < E; ++e) dx[e] = 0.f;
     }
-    if (in && a.dx_in) load_vec<T, E>(reinterpret_cast<const T*>(a.dx_in) + at, dx);
+    if (a.y) {
+      sh.template load<T>(reinterpret_cast<const T*>(a.y) + row0, z);
+      load_gate<T, E, VEC>(a, sh, row0, g);
+#pragma unroll
+      for (int e = 0; e < E; ++e) z[e] *= r_post;  // yn
+    }
     if (a.w_pre) {
       const float r_pre = a.rstd_pre[row];
       float t[E], xn[E], s = 0.f;
+      sh.template load<T>(reinterpret_cast<const T*>(a.x) + row0, xn);
+      sh.template load<T>(reinterpret_cast<const T*>(a.du) + row0, t);
+      if (a.y) {
+        sh.param(a.w_post, w);
 #pragma unroll
-      for (int e = 0; e < E; ++e) t[e] = xn[e] = 0.f;
-      if (in) {
-        load_vec<T, E>(reinterpret_cast<const T*>(a.x) + at, xn);
-        if (a.y) {
-          float w[E];
-          load_param<E>(a.w_post, c, w, 1.f);
+        for (int e = 0; e < E; ++e) xn[e] += a.res_scale * g[e] * (z[e] * w[e]);
+      }
+      sh.param(a.w_pre, w);
 #pragma unroll
-          for (int e = 0; e < E; ++e) xn[e] += a.res_scale * g[e] * (z[e] * (a.w_post ? r_post * w[e] : 1.f));
-        }
-        float du[E], w[E];
-        load_vec<T, E>(reinterpret_cast<const T*>(a.du) + at, du);
-        load_param<E>(a.w_pre, c, w, 1.f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          xn[e] *= r_pre;
-          t[e] = du[e] * w[e];
-          s += t[e] * xn[e];
-          acc[c + e] += du[e] * xn[e];
-        }
+      for (int e = 0; e < E; ++e) {
+        xn[e] *= r_pre;
+        if (sh.has(e)) acc[sh.at(e)] += t[e] * xn[e];
+        t[e] *= w[e];
+        s += t[e] * xn[e];
       }
       const float mean = block_sum(s, buf, turn) * a.inv_D;
 #pragma unroll
       for (int e = 0; e < E; ++e) dx[e] += r_pre * (t[e] - xn[e] * mean);
     }
-    if (in && a.dx) store_vec<T, E>(reinterpret_cast<T*>(a.dx) + at, dx);
+    if (a.dx) sh.template store<T>(reinterpret_cast<T*>(a.dx) + row0, dx);
     if (!a.y) continue;
-    float q[E], s = 0.f;
+    float s = 0.f, dg[E];
+    sh.param(a.w_post, w);
 #pragma unroll
-    for (int e = 0; e < E; ++e) q[e] = 0.f;
-    if (in) {
-      float w[E], dg[E];
-      load_param<E>(a.w_post, c, w, 1.f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float yn = z[e] * r_post, dgz = a.res_scale * dx[e], dz = dgz * g[e];
-        dg[e] = dgz * (yn * w[e]);
-        if (a.w_post) acc[a.D + c + e] += dz * yn;
-        if (sum_gate) acc[2 * a.D + c + e] += dg[e];
-        q[e] = dz * w[e];
-        z[e] = yn;
-        s += q[e] * yn;
-      }
-      if (a.gate && a.gate_rows && a.dgate) store_vec<T, E>(reinterpret_cast<T*>(a.dgate) + at, dg);
+    for (int e = 0; e < E; ++e) {
+      const float dgz = a.res_scale * dx[e], dz = dgz * g[e];
+      dg[e] = dgz * (z[e] * w[e]);
+      if (a.w_post && sh.has(e)) acc[a.D + sh.at(e)] += dz * z[e];
+      if (sum_gate && sh.has(e)) acc[2 * a.D + sh.at(e)] += dg[e];
+      dx[e] = dz * w[e];
+      s += dx[e] * z[e];
     }
+    if (row_gate && a.dgate) sh.template store<T>(reinterpret_cast<T*>(a.dgate) + row0, dg);
     if (a.w_post) {
       const float mean = block_sum(s, buf, turn) * a.inv_D;
 #pragma unroll
-      for (int e = 0; e < E; ++e) q[e] = r_post * (q[e] - z[e] * mean);
+      for (int e = 0; e < E; ++e) dx[e] = r_post * (dx[e] - z[e] * mean);
     }
-    if (in && a.dy) store_vec<T, E>(reinterpret_cast<T*>(a.dy) + at, q);
+    if (a.dy) sh.template store<T>(reinterpret_cast<T*>(a.dy) + row0, dx);
   }
-  if (in) {
-    float* dst = a.part + (size_t)blockIdx.x * 3 * a.D + c;
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-#pragma unroll
-      for (int e = 0; e < E; e += 4)
-        *reinterpret_cast<float4*>(dst + (size_t)k * a.D + e) =
-            *reinterpret_cast<const float4*>(acc + (size_t)k * a.D + c + e);
+  for (int k = 0; k < 3; ++k) {
+    float f[E];
+    sh.template load<float>(acc + (size_t)k * a.D, f);
+    sh.template store<float>(a.part + ((size_t)blockIdx.x * 3 + k) * a.D, f);
   }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kSlowThreads) norm_bwd_any(const NormArgs a) {
-  extern __shared__ __align__(16) float acc[];
-  __shared__ float buf[64];
-  int turn = 0;
-  const bool sum_gate = a.gate && !a.gate_rows && a.dgate;
-  const T* y = reinterpret_cast<const T*>(a.y);
-  const T* x = reinterpret_cast<const T*>(a.x);
-  const T* du = reinterpret_cast<const T*>(a.du);
-  for (int c = threadIdx.x; c < 3 * a.D; c += blockDim.x) acc[c] = 0.f;
-  __syncthreads();
-  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
-    const size_t at0 = (size_t)row * a.D;
-    const float r_post = a.w_post ? a.rstd_post[row] : 1.f, r_pre = a.w_pre ? a.rstd_pre[row] : 1.f;
-    auto normed = [&](int c) {  // x' r_pre
-      float v = to_float<T>(x[at0 + c]);
-      if (a.y) {
-        const float z = to_float<T>(y[at0 + c]) * (a.w_post ? r_post * a.w_post[c] : 1.f);
-        v += a.res_scale * gate_at<T>(a, at0 + c, c) * z;
-      }
-      return v * r_pre;
-    };
-    float mean_pre = 0.f, mean_post = 0.f;
-    if (a.w_pre) {
-      float s = 0.f;
-      for (int c = threadIdx.x; c < a.D; c += blockDim.x) s += to_float<T>(du[at0 + c]) * a.w_pre[c] * normed(c);
-      mean_pre = block_sum(s, buf, turn) * a.inv_D;
-    }
-    auto grad_x = [&](int c, float xn) {
-      float v = a.dx_in ? to_float<T>(reinterpret_cast<const T*>(a.dx_in)[at0 + c]) : 0.f;
-      if (a.w_pre) v += r_pre * (to_float<T>(du[at0 + c]) * a.w_pre[c] - xn * mean_pre);
-      return v;
-    };
-    if (a.y && a.w_post) {
-      float s = 0.f;
-      for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
-        const float dx = grad_x(c, a.w_pre ? normed(c) : 0.f);
-        s += a.res_scale * dx * gate_at<T>(a, at0 + c, c) * a.w_post[c] * (to_float<T>(y[at0 + c]) * r_post);
-      }
-      mean_post = block_sum(s, buf, turn) * a.inv_D;
-    }
-    for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
-      const float xn = a.w_pre ? normed(c) : 0.f;
-      const float dx = grad_x(c, xn);
-      if (a.w_pre) acc[c] += to_float<T>(du[at0 + c]) * xn;
-      if (a.y) {
-        const float yn = to_float<T>(y[at0 + c]) * r_post, w = a.w_post ? a.w_post[c] : 1.f;
-        const float g = gate_at<T>(a, at0 + c, c), dgz = a.res_scale * dx, dz = dgz * g, dg = dgz * (yn * w);
-        if (a.w_post) acc[a.D + c] += dz * yn;
-        if (sum_gate) acc[2 * a.D + c] += dg;
-        if (a.gate && a.gate_rows && a.dgate) reinterpret_cast<T*>(a.dgate)[at0 + c] = from_float<T>(dg);
-        if (a.dy)
-          reinterpret_cast<T*>(a.dy)[at0 + c] = from_float<T>(a.w_post ? r_post * (dz * w - yn * mean_post) : dz * w);
-      }
-      if (a.dx) reinterpret_cast<T*>(a.dx)[at0 + c] = from_float<T>(dx);  // last: dx may be dx_in
-    }
-  }
-  __syncthreads();
-  for (int c = threadIdx.x; c < 3 * a.D; c += blockDim.x) a.part[(size_t)blockIdx.x * 3 * a.D + c] = acc[c];
 }
 
 // Column sums over the blocks' parts, in block order: 32 columns a block, 8 strips of the
@@ -375,6 +292,7 @@ __global__ void __launch_bounds__(256) norm_join(const float* __restrict__ part,
 // memory; the threads wait for a stage, take their elements into registers and hand the stage
 // back.  So a block keeps stages x tensors x row bytes of loads in flight whatever its barriers
 // wait for, and two blocks of an SM hide each other's sums.
+constexpr int kNarrow = 448;  // threads up to which a thread holds 8 elements: two blocks fit 72 registers
 constexpr int kMaxStages = 4;
 constexpr int kMaxRowTensors = 5;
 
@@ -410,7 +328,7 @@ __device__ __forceinline__ void ring_start(const RowRing& r, uint8_t* base, Ring
 }
 
 template <typename T, int E>
-__global__ void __launch_bounds__(512, E == 8 ? 2 : 1)
+__global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
     norm_fwd_ring(const __grid_constant__ NormArgs a, const __grid_constant__ RowRing ring) {
   extern __shared__ __align__(128) uint8_t stage_mem[];
   __shared__ RingBars bars;
@@ -481,7 +399,7 @@ __global__ void __launch_bounds__(512, E == 8 ? 2 : 1)
 // The parameters stay in shared memory ([w_pre | res_scale g | w_post] x D fp32, a thread reads
 // its own columns), the sums of their gradients in registers.
 template <typename T, int E>
-__global__ void __launch_bounds__(512, E == 8 ? 2 : 1)
+__global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
     norm_bwd_ring(const __grid_constant__ NormArgs a, const __grid_constant__ RowRing ring) {
   extern __shared__ __align__(128) uint8_t stage_mem[];
   __shared__ RingBars bars;
@@ -617,12 +535,14 @@ bool vector_rows(const NormArgs& a) {
 
 int threads_for(int D, int E) { return (int)align_up((size_t)((D + E - 1) / E), 32); }
 
+int ring_elements(int D) { return D <= 8 * kNarrow ? 8 : 16; }
+
 // Rows through the ring where every block has at least four of them to walk and a stage
 // fits; else a row is read straight into registers.
 constexpr size_t kRingBytes = 200 * 1024;  // of an SM's shared memory, for all its blocks' stages
 bool ring_setup(const NormArgs& a, size_t es, bool backward, RowRing* r, unsigned* grid, size_t* smem) {
-  if (a.D > 8192) return false;
-  const int E = a.D <= 4096 ? 8 : 16, T = threads_for(a.D, E);
+  if (a.D > 8192 || a.D % ring_elements(a.D)) return false;
+  const int T = threads_for(a.D, ring_elements(a.D));
   auto add = [&](const void* p) {
     if (p) r->src[r->n_src++] = reinterpret_cast<const char*>(p);
   };
@@ -650,64 +570,62 @@ bool ring_setup(const NormArgs& a, size_t es, bool backward, RowRing* r, unsigne
   return true;
 }
 
-template <typename T>
-cudaError_t fwd(const NormArgs& a, cudaStream_t st) {
-  static size_t set8[kMaxDevices] = {}, set16[kMaxDevices] = {};
-  const unsigned rows = (unsigned)std::min<int64_t>(a.n, 1 << 20);
-  RowRing ring;
-  unsigned grid;
-  size_t smem;
-  if (!vector_rows(a)) {
-    norm_fwd_any<T><<<rows, kSlowThreads, 0, st>>>(a);
-  } else if (ring_setup(a, sizeof(T), false, &ring, &grid, &smem)) {
-    const bool narrow = a.D <= 4096;
-    cudaError_t e = narrow ? set_smem_limit((const void*)norm_fwd_ring<T, 8>, kRingBytes, set8)
-                           : set_smem_limit((const void*)norm_fwd_ring<T, 16>, kRingBytes, set16);
-    if (e != cudaSuccess) return e;
-    if (narrow)
-      norm_fwd_ring<T, 8><<<grid, threads_for(a.D, 8), smem, st>>>(a, ring);
-    else
-      norm_fwd_ring<T, 16><<<grid, threads_for(a.D, 16), smem, st>>>(a, ring);
-  } else if (elements(a.D) == 8) {
-    norm_fwd<T, 8><<<rows, threads_for(a.D, 8), 0, st>>>(a);
-  } else {
-    norm_fwd<T, 16><<<rows, threads_for(a.D, 16), 0, st>>>(a);
-  }
-  count_launches(1);
+template <typename T, int E, bool VEC>
+cudaError_t fwd_direct(const NormArgs& a, cudaStream_t st) {
+  norm_fwd<T, E, VEC><<<(unsigned)std::min<int64_t>(a.n, 1 << 20), threads_for(a.D, E), 0, st>>>(a);
+  return cudaGetLastError();
+}
+template <typename T, int E>
+cudaError_t fwd_ring(const NormArgs& a, const RowRing& ring, unsigned grid, size_t smem, cudaStream_t st) {
+  static size_t set[kMaxDevices] = {};
+  const cudaError_t e = set_smem_limit((const void*)norm_fwd_ring<T, E>, kRingBytes, set);
+  if (e != cudaSuccess) return e;
+  norm_fwd_ring<T, E><<<grid, threads_for(a.D, E), smem, st>>>(a, ring);
+  return cudaGetLastError();
+}
+template <typename T, int E, bool VEC>
+cudaError_t bwd_direct(const NormArgs& a, unsigned grid, cudaStream_t st) {
+  static size_t set[kMaxDevices] = {};
+  const cudaError_t e = set_smem_limit((const void*)norm_bwd<T, E, VEC>, (size_t)3 * 1024 * E * 4, set);
+  if (e != cudaSuccess) return e;
+  norm_bwd<T, E, VEC><<<grid, threads_for(a.D, E), (size_t)3 * a.D * 4, st>>>(a);
+  return cudaGetLastError();
+}
+template <typename T, int E>
+cudaError_t bwd_ring(const NormArgs& a, const RowRing& ring, unsigned grid, size_t smem, cudaStream_t st) {
+  static size_t set[kMaxDevices] = {};
+  const cudaError_t e = set_smem_limit((const void*)norm_bwd_ring<T, E>, kRingBytes, set);
+  if (e != cudaSuccess) return e;
+  norm_bwd_ring<T, E><<<grid, threads_for(a.D, E), smem, st>>>(a, ring);
   return cudaGetLastError();
 }
 
 template <typename T>
+cudaError_t fwd(const NormArgs& a, cudaStream_t st) {
+  RowRing ring;
+  unsigned grid;
+  size_t smem;
+  count_launches(1);
+  const bool small = elements(a.D) == 8;
+  if (!vector_rows(a)) return small ? fwd_direct<T, 8, false>(a, st) : fwd_direct<T, 16, false>(a, st);
+  if (ring_setup(a, sizeof(T), false, &ring, &grid, &smem))
+    return ring_elements(a.D) == 8 ? fwd_ring<T, 8>(a, ring, grid, smem, st) : fwd_ring<T, 16>(a, ring, grid, smem, st);
+  return small ? fwd_direct<T, 8, true>(a, st) : fwd_direct<T, 16, true>(a, st);
+}
+
+template <typename T>
 cudaError_t bwd(const NormArgs& a, cudaStream_t st) {
-  static size_t set8[kMaxDevices] = {}, set16[kMaxDevices] = {}, set_any[kMaxDevices] = {};
-  static size_t ring8[kMaxDevices] = {}, ring16[kMaxDevices] = {};
-  size_t smem = (size_t)3 * a.D * 4;
+  size_t smem;
   unsigned grid = (unsigned)norm_parts(a.n, a.D);
   RowRing ring;
   cudaError_t e;
-  if (!vector_rows(a)) {
-    e = set_smem_limit((const void*)norm_bwd_any<T>, (size_t)3 * kMaxWidth * 4, set_any);
-    if (e != cudaSuccess) return e;
-    norm_bwd_any<T><<<grid, kSlowThreads, smem, st>>>(a);
-  } else if (ring_setup(a, sizeof(T), true, &ring, &grid, &smem)) {
-    const bool narrow = a.D <= 4096;
-    e = narrow ? set_smem_limit((const void*)norm_bwd_ring<T, 8>, kRingBytes, ring8)
-               : set_smem_limit((const void*)norm_bwd_ring<T, 16>, kRingBytes, ring16);
-    if (e != cudaSuccess) return e;
-    if (narrow)
-      norm_bwd_ring<T, 8><<<grid, threads_for(a.D, 8), smem, st>>>(a, ring);
-    else
-      norm_bwd_ring<T, 16><<<grid, threads_for(a.D, 16), smem, st>>>(a, ring);
-  } else if (elements(a.D) == 8) {
-    e = set_smem_limit((const void*)norm_bwd<T, 8>, (size_t)3 * 8192 * 4, set8);
-    if (e != cudaSuccess) return e;
-    norm_bwd<T, 8><<<grid, threads_for(a.D, 8), smem, st>>>(a);
-  } else {
-    e = set_smem_limit((const void*)norm_bwd<T, 16>, (size_t)3 * kMaxWidth * 4, set16);
-    if (e != cudaSuccess) return e;
-    norm_bwd<T, 16><<<grid, threads_for(a.D, 16), smem, st>>>(a);
-  }
-  e = cudaGetLastError();
+  const bool small = elements(a.D) == 8;
+  if (!vector_rows(a))
+    e = small ? bwd_direct<T, 8, false>(a, grid, st) : bwd_direct<T, 16, false>(a, grid, st);
+  else if (ring_setup(a, sizeof(T), true, &ring, &grid, &smem))
+    e = ring_elements(a.D) == 8 ? bwd_ring<T, 8>(a, ring, grid, smem, st) : bwd_ring<T, 16>(a, ring, grid, smem, st);
+  else
+    e = small ? bwd_direct<T, 8, true>(a, grid, st) : bwd_direct<T, 16, true>(a, grid, st);
   if (e != cudaSuccess) return e;
   count_launches(1);
   float* dgate = a.gate && !a.gate_rows ? reinterpret_cast<float*>(a.dgate) : nullptr;
@@ -725,7 +643,7 @@ cudaError_t bwd(const NormArgs& a, cudaStream_t st) {
 int norm_blocks_per_sm(int T) { return std::max(1, std::min(8, 1024 / T)); }
 
 int norm_parts(int64_t n, int D) {
-  const int E = D <= 4096 ? 8 : 16;
+  const int E = ring_elements(D);
   return (int)std::min<int64_t>(n, (int64_t)norm_blocks_per_sm((int)align_up((size_t)((D + E - 1) / E), 32)) *
                                        device_sm_count());
 }
