@@ -29,20 +29,31 @@ namespace {
 constexpr int kMaxWidth = 16384;
 
 // Sum over the block; every thread gets it.  `buf` holds 2 x 32 floats, used in turns so that
-// one barrier a sum is enough.
+// one barrier a sum is enough; the warps' sums are read as vectors by every thread (a second
+// round of shuffles would wait five times as long).
 __device__ __forceinline__ float block_sum(float v, float* buf, int& turn) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  const int warps = blockDim.x / 32, lane = threadIdx.x % 32;
+  const int warps = blockDim.x / 32;
   if (warps == 1) return v;
   float* b = buf + 32 * turn;
   turn ^= 1;
-  if (lane == 0) b[threadIdx.x / 32] = v;
+  if (threadIdx.x % 32 == 0) b[threadIdx.x / 32] = v;
   __syncthreads();
-  v = lane < warps ? b[lane] : 0.f;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int w = 0; w < warps; w += 4) {  // the entries behind the last warp stay 0
+    const float4 x = *reinterpret_cast<const float4*>(b + w);
+    t.x += x.x;
+    t.y += x.y;
+    t.z += x.z;
+    t.w += x.w;
+  }
+  return (t.x + t.y) + (t.z + t.w);
+}
+// Before the first sum: no barrier of its own, the first sum's writes come before its barrier
+// and touch other entries.
+__device__ __forceinline__ void clear_sums(float* buf) {
+  if (threadIdx.x < 64 && threadIdx.x % 32 >= blockDim.x / 32) buf[threadIdx.x] = 0.f;
 }
 
 // E consecutive elements as fp32, and back with one rounding.
@@ -141,7 +152,8 @@ __device__ __forceinline__ void load_gate(const NormArgs& a, const Share<E, VEC>
 // ------------------------------------------------------------------ forward
 template <typename T, int E, bool VEC>
 __global__ void __launch_bounds__(1024, 1) norm_fwd(const __grid_constant__ NormArgs a) {
-  __shared__ float buf[64];
+  __shared__ __align__(16) float buf[64];
+  clear_sums(buf);
   int turn = 0;
   const Share<E, VEC> sh(a.D);
   for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
@@ -186,7 +198,8 @@ __global__ void __launch_bounds__(1024, 1) norm_fwd(const __grid_constant__ Norm
 template <typename T, int E, bool VEC>
 __global__ void __launch_bounds__(1024, 1) norm_bwd(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) float acc[];
-  __shared__ float buf[64];
+  __shared__ __align__(16) float buf[64];
+  clear_sums(buf);
   int turn = 0;
   const Share<E, VEC> sh(a.D);
   const bool row_gate = a.gate && a.gate_rows;
@@ -275,6 +288,7 @@ __global__ void __launch_bounds__(256) norm_join(const float* __restrict__ part,
   const int p0 = n_parts * w / 8, p1 = n_parts * (w + 1) / 8;
   float s = 0.f;
   if (c < D)
+#pragma unroll 8
     for (int p = p0; p < p1; ++p) s += part[((size_t)p * 3 + k) * D + c];
   strip[w][lane] = s;
   __syncthreads();
@@ -327,38 +341,104 @@ __device__ __forceinline__ void ring_start(const RowRing& r, uint8_t* base, Ring
   __syncthreads();
 }
 
+// Packed pairs of fp32 (two elements an instruction): a row's work is bound by instructions as
+// much as by its bytes.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t both(float v) { return f32x2(v, v); }
+__device__ __forceinline__ float halves(uint64_t v) {
+  float a, b;
+  f32x2_split(v, a, b);
+  return a + b;
+}
 template <typename T, int E>
+__device__ __forceinline__ void load2(const T* p, uint64_t (&f)[E / 2]) {
+  constexpr int V = 16 / sizeof(T);
+#pragma unroll
+  for (int i = 0; i < E; i += V) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p + i);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[i / 2 + k] = f32x2(x[k] << 16, x[k] & 0xffff0000u);
+    } else {
+      f[i / 2] = f32x2(x[0], x[1]);
+      f[i / 2 + 1] = f32x2(x[2], x[3]);
+    }
+  }
+}
+template <typename T, int E>
+__device__ __forceinline__ void store2(T* p, const uint64_t (&f)[E / 2]) {
+  constexpr int V = 16 / sizeof(T);
+#pragma unroll
+  for (int i = 0; i < E; i += V) {
+    uint32_t x[4];
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float a, b;
+        f32x2_split(f[i / 2 + k], a, b);
+        x[k] = pack_bf16x2(a, b);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float a, b;
+        f32x2_split(f[i / 2 + k], a, b);
+        x[2 * k] = __float_as_uint(a);
+        x[2 * k + 1] = __float_as_uint(b);
+      }
+    }
+    *reinterpret_cast<uint4*>(p + i) = make_uint4(x[0], x[1], x[2], x[3]);
+  }
+}
+
+// x' = x + (c g) (y r_post), c = res_scale gate w_post of the channel, g the token's gate.
+template <typename T, int E, bool ROWGATE>
 __global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
     norm_fwd_ring(const __grid_constant__ NormArgs a, const __grid_constant__ RowRing ring) {
+  constexpr int H = E / 2;
   extern __shared__ __align__(128) uint8_t stage_mem[];
   __shared__ RingBars bars;
-  __shared__ float buf[64];
+  __shared__ __align__(16) float buf[64];
+  clear_sums(buf);
   int turn = 0, k = 0;
   uint32_t phase = 0;
   const int c = threadIdx.x * E;
   const bool in = c < a.D;
-  const bool row_gate = a.gate && a.gate_rows;
   ring_start(ring, stage_mem, &bars, a.n);
-  float wp[E], g[E], w[E];
+  uint64_t cw[H], w[H];
 #pragma unroll
-  for (int e = 0; e < E; ++e) wp[e] = g[e] = w[e] = 0.f;
+  for (int e = 0; e < H; ++e) cw[e] = w[e] = 0;
   if (in) {
-    load_param<E>(a.w_post, c, wp, 1.f);
-    load_param<E>(row_gate ? nullptr : reinterpret_cast<const float*>(a.gate), c, g, 1.f);
-    load_param<E>(a.w_pre, c, w, 1.f);
+    float f[E], g[E];
+    load_param<E>(a.w_post, c, f, 1.f);
+    load_param<E>(ROWGATE ? nullptr : reinterpret_cast<const float*>(a.gate), c, g, 1.f);
 #pragma unroll
-    for (int e = 0; e < E; ++e) wp[e] *= a.res_scale * g[e];  // one factor for z on its way to x'
+    for (int e = 0; e < H; ++e)
+      cw[e] = f32x2(a.res_scale * g[2 * e] * f[2 * e], a.res_scale * g[2 * e + 1] * f[2 * e + 1]);
+    load_param<E>(a.w_pre, c, f, 1.f);
+#pragma unroll
+    for (int e = 0; e < H; ++e) w[e] = f32x2(f[2 * e], f[2 * e + 1]);
   }
   for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
-    float f[E], r[E];
+    uint64_t f[H], r[H], g[H];
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = r[e] = 0.f;
+    for (int e = 0; e < H; ++e) f[e] = r[e] = g[e] = 0;
     if (!mbar_wait(&bars.full[k], phase, nullptr)) return;  // the copy cannot fail to end
     const T* st = reinterpret_cast<const T*>(stage_mem + (size_t)k * ring.n_src * ring.row_bytes) + c;
     if (in) {
-      load_vec<T, E>(st, f);
-      if (a.y) load_vec<T, E>(st + a.D, r);
-      if (row_gate) load_vec<T, E>(st + 2 * a.D, g);
+      load2<T, E>(st, f);
+      if (a.y) load2<T, E>(st + a.D, r);
+      if (ROWGATE) load2<T, E>(st + 2 * a.D, g);
     }
     __syncthreads();
     const int64_t later = row + (int64_t)ring.stages * gridDim.x;
@@ -371,84 +451,83 @@ __global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
     if (a.y) {
       float rstd = 1.f;
       if (a.w_post) {
-        float s = 0.f;
+        uint64_t s = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) s += r[e] * r[e];
-        rstd = rsqrtf(block_sum(s, buf, turn) * a.inv_D + a.eps);
+        for (int e = 0; e < H; ++e) s = fma2(r[e], r[e], s);
+        rstd = rsqrtf(block_sum(halves(s), buf, turn) * a.inv_D + a.eps);
         if (a.rstd_post && threadIdx.x == 0) a.rstd_post[row] = rstd;
       }
+      const uint64_t rs = both(rstd);
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = fmaf(r[e] * rstd, row_gate ? wp[e] * g[e] : wp[e], f[e]);
+      for (int e = 0; e < H; ++e) f[e] = fma2(mul2(r[e], rs), ROWGATE ? mul2(cw[e], g[e]) : cw[e], f[e]);
     }
-    if (a.x_out && in) store_vec<T, E>(reinterpret_cast<T*>(a.x_out) + at, f);
+    if (a.x_out && in) store2<T, E>(reinterpret_cast<T*>(a.x_out) + at, f);
     if (a.w_pre) {
-      float s = 0.f;
+      uint64_t s = 0;
 #pragma unroll
-      for (int e = 0; e < E; ++e) s += f[e] * f[e];
-      const float rstd = rsqrtf(block_sum(s, buf, turn) * a.inv_D + a.eps);
+      for (int e = 0; e < H; ++e) s = fma2(f[e], f[e], s);
+      const float rstd = rsqrtf(block_sum(halves(s), buf, turn) * a.inv_D + a.eps);
       if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[row] = rstd;
+      const uint64_t rs = both(rstd);
       if (in) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) f[e] *= rstd * w[e];
-        store_vec<T, E>(reinterpret_cast<T*>(a.u) + at, f);
+        for (int e = 0; e < H; ++e) f[e] = mul2(mul2(f[e], rs), w[e]);
+        store2<T, E>(reinterpret_cast<T*>(a.u) + at, f);
       }
     }
   }
 }
 
-// The parameters stay in shared memory ([w_pre | res_scale g | w_post] x D fp32, a thread reads
-// its own columns), the sums of their gradients in registers.
-template <typename T, int E>
+// With c as above and a = dx yn: dz yn = (res_scale gate) a and the gate's gradient is
+// (res_scale w_post) a, so for a gate per channel one sum over the rows of a gives both
+// parameter gradients.  The parameters stand in shared memory ([w_pre | c] x D fp32, a thread
+// reads its own columns), the sums in registers.
+template <typename T, int E, bool ROWGATE>
 __global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
     norm_bwd_ring(const __grid_constant__ NormArgs a, const __grid_constant__ RowRing ring) {
+  constexpr int H = E / 2;
   extern __shared__ __align__(128) uint8_t stage_mem[];
   __shared__ RingBars bars;
-  __shared__ float buf[64];
+  __shared__ __align__(16) float buf[64];
+  clear_sums(buf);
   int turn = 0, k = 0;
   uint32_t phase = 0;
   const int c = threadIdx.x * E;
   const bool in = c < a.D;
-  const bool row_gate = a.gate && a.gate_rows, pre = a.w_pre != nullptr, post = a.w_post != nullptr;
+  const bool pre = a.w_pre != nullptr, post = a.w_post != nullptr;
   float* par = reinterpret_cast<float*>(stage_mem + (size_t)ring.stages * ring.n_src * ring.row_bytes);
   ring_start(ring, stage_mem, &bars, a.n);
   if (in) {
-    float f[E];
+    float f[E], g[E];
     load_param<E>(a.w_pre, c, f, 1.f);
     store_vec<float, E>(par + c, f);
-    load_param<E>(row_gate ? nullptr : reinterpret_cast<const float*>(a.gate), c, f, 1.f);
-#pragma unroll
-    for (int e = 0; e < E; ++e) f[e] *= a.res_scale;
-    store_vec<float, E>(par + a.D + c, f);
     load_param<E>(a.w_post, c, f, 1.f);
-    store_vec<float, E>(par + 2 * a.D + c, f);
+    load_param<E>(ROWGATE ? nullptr : reinterpret_cast<const float*>(a.gate), c, g, 1.f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] *= a.res_scale * g[e];
+    store_vec<float, E>(par + a.D + c, f);
   }
   // stage order: x (with a pre-norm), y, du, dx', gate rows, each where it is read
   const int at_y = pre ? 1 : 0, at_du = at_y + (a.y ? 1 : 0), at_dx = at_du + (pre ? 1 : 0),
             at_g = at_dx + (a.dx_in ? 1 : 0);
-  float a_pre[E], a_post[E], a_gate[E];
+  uint64_t a_pre[H], a_post[H];
 #pragma unroll
-  for (int e = 0; e < E; ++e) a_pre[e] = a_post[e] = a_gate[e] = 0.f;
+  for (int e = 0; e < H; ++e) a_pre[e] = a_post[e] = 0;
   for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
     const float r_post = post ? a.rstd_post[row] : 1.f, r_pre = pre ? a.rstd_pre[row] : 1.f;
-    float xn[E], yn[E], dx[E], t[E], g[E];
+    uint64_t xo[H], yn[H], dx[H], t[H], g[H];
 #pragma unroll
-    for (int e = 0; e < E; ++e) xn[e] = yn[e] = dx[e] = t[e] = g[e] = 0.f;
+    for (int e = 0; e < H; ++e) xo[e] = yn[e] = dx[e] = t[e] = g[e] = 0;
     if (!mbar_wait(&bars.full[k], phase, nullptr)) return;  // the copy cannot fail to end
     const T* st = reinterpret_cast<const T*>(stage_mem + (size_t)k * ring.n_src * ring.row_bytes) + c;
     if (in) {
       if (pre) {
-        load_vec<T, E>(st, xn);
-        load_vec<T, E>(st + at_du * a.D, t);
+        load2<T, E>(st, xo);
+        load2<T, E>(st + at_du * a.D, t);
       }
-      if (a.y) load_vec<T, E>(st + at_y * a.D, yn);
-      if (a.dx_in) load_vec<T, E>(st + at_dx * a.D, dx);
-      load_vec<float, E>(par + a.D + c, g);
-      if (row_gate) {
-        float gr[E];
-        load_vec<T, E>(st + at_g * a.D, gr);
-#pragma unroll
-        for (int e = 0; e < E; ++e) g[e] *= gr[e];
-      }
+      if (a.y) load2<T, E>(st + at_y * a.D, yn);
+      if (a.dx_in) load2<T, E>(st + at_dx * a.D, dx);
+      if (ROWGATE) load2<T, E>(st + at_g * a.D, g);
     }
     __syncthreads();
     const int64_t later = row + (int64_t)ring.stages * gridDim.x;
@@ -458,63 +537,82 @@ __global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
       phase ^= 1;
     }
     const size_t at = (size_t)row * a.D + c;
+    const uint64_t rp2 = both(r_post);
 #pragma unroll
-    for (int e = 0; e < E; ++e) yn[e] *= r_post;
-    if (pre) {
-      float s = 0.f;
-      if (in) {
-        float w[E];
-        if (a.y) {
-          load_vec<float, E>(par + 2 * a.D + c, w);
-#pragma unroll
-          for (int e = 0; e < E; ++e) xn[e] = fmaf(g[e], yn[e] * w[e], xn[e]);
-        }
-        load_vec<float, E>(par + c, w);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          xn[e] *= r_pre;
-          a_pre[e] = fmaf(t[e], xn[e], a_pre[e]);
-          t[e] *= w[e];
-          s = fmaf(t[e], xn[e], s);
-        }
-      }
-      const float mean = block_sum(s, buf, turn) * a.inv_D;
-#pragma unroll
-      for (int e = 0; e < E; ++e) dx[e] = fmaf(r_pre, t[e] - xn[e] * mean, dx[e]);
-    }
-    if (in && a.dx) store_vec<T, E>(reinterpret_cast<T*>(a.dx) + at, dx);
-    if (!a.y) continue;
-    float s = 0.f;
+    for (int e = 0; e < H; ++e) yn[e] = mul2(yn[e], rp2);
+    uint64_t cw[H];
     if (in) {
-      float w[E];
-      load_vec<float, E>(par + 2 * a.D + c, w);
+      load2<float, E>(par + a.D + c, cw);
+    } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float z = yn[e] * w[e], dgz = a.res_scale * dx[e], dz = g[e] * dx[e];
-        t[e] = dgz * z;                                // gradient of the gate
-        a_post[e] = fmaf(dz, yn[e], a_post[e]);
-        dx[e] = dz * w[e];
-        s = fmaf(dx[e], yn[e], s);
+      for (int e = 0; e < H; ++e) cw[e] = 0;
+    }
+    if (pre) {
+      uint64_t s = 0;
+      const uint64_t r2 = both(r_pre);
+      if (in) {
+        uint64_t w[H];
+        load2<float, E>(par + c, w);
+        if (a.y) {
+#pragma unroll
+          for (int e = 0; e < H; ++e) xo[e] = fma2(ROWGATE ? mul2(cw[e], g[e]) : cw[e], yn[e], xo[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+          a_pre[e] = fma2(mul2(t[e], r2), xo[e], a_pre[e]);
+          t[e] = mul2(t[e], w[e]);
+          s = fma2(t[e], xo[e], s);
+        }
       }
-      if (row_gate && a.dgate) {
-        store_vec<T, E>(reinterpret_cast<T*>(a.dgate) + at, t);
+      // xn mean(t xn) r_pre = x' r_pre^3 sum(t x') / D
+      const float sum = block_sum(halves(s), buf, turn) * a.inv_D;
+      const uint64_t m2 = both(-(r_pre * r_pre * r_pre) * sum);
+#pragma unroll
+      for (int e = 0; e < H; ++e) dx[e] = fma2(xo[e], m2, fma2(t[e], r2, dx[e]));
+    }
+    if (in && a.dx) store2<T, E>(reinterpret_cast<T*>(a.dx) + at, dx);
+    if (!a.y) continue;
+    uint64_t s = 0;
+#pragma unroll
+    for (int e = 0; e < H; ++e) {
+      const uint64_t p = mul2(dx[e], yn[e]);
+      if (ROWGATE) {
+        a_post[e] = fma2(g[e], p, a_post[e]);
+        t[e] = mul2(cw[e], p);
+        dx[e] = mul2(mul2(cw[e], g[e]), dx[e]);
       } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) a_gate[e] += t[e];
+        a_post[e] = fma2(dx[e], yn[e], a_post[e]);
+        dx[e] = mul2(cw[e], dx[e]);
       }
+      s = fma2(dx[e], yn[e], s);
     }
+    if (ROWGATE && a.dgate && in) store2<T, E>(reinterpret_cast<T*>(a.dgate) + at, t);
     if (post) {
-      const float mean = block_sum(s, buf, turn) * a.inv_D;
+      const float mean = block_sum(halves(s), buf, turn) * a.inv_D;
+      const uint64_t m2 = both(-r_post * mean);
 #pragma unroll
-      for (int e = 0; e < E; ++e) dx[e] = r_post * (dx[e] - yn[e] * mean);
+      for (int e = 0; e < H; ++e) dx[e] = fma2(yn[e], m2, mul2(dx[e], rp2));
     }
-    if (in && a.dy) store_vec<T, E>(reinterpret_cast<T*>(a.dy) + at, dx);
+    if (in && a.dy) store2<T, E>(reinterpret_cast<T*>(a.dy) + at, dx);
   }
   if (in) {
     float* dst = a.part + (size_t)blockIdx.x * 3 * a.D + c;
-    store_vec<float, E>(dst, a_pre);
-    store_vec<float, E>(dst + a.D, a_post);
-    store_vec<float, E>(dst + 2 * a.D, a_gate);
+    float s[E], w[E], g[E];
+#pragma unroll
+    for (int e = 0; e < H; ++e) f32x2_split(a_pre[e], s[2 * e], s[2 * e + 1]);
+    store_vec<float, E>(dst, s);
+    load_param<E>(a.w_post, c, w, 1.f);
+    load_param<E>(ROWGATE ? nullptr : reinterpret_cast<const float*>(a.gate), c, g, 1.f);
+#pragma unroll
+    for (int e = 0; e < H; ++e) f32x2_split(a_post[e], s[2 * e], s[2 * e + 1]);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float v = a.res_scale * s[e];
+      s[e] = v * g[e];
+      w[e] *= v;
+    }
+    store_vec<float, E>(dst + a.D, s);
+    store_vec<float, E>(dst + 2 * a.D, w);  // not used for a gate per token
   }
 }
 
@@ -562,7 +660,7 @@ bool ring_setup(const NormArgs& a, size_t es, bool backward, RowRing* r, unsigne
   const int per_sm = norm_blocks_per_sm(T);
   const int64_t blocks = std::min<int64_t>(a.n, (int64_t)per_sm * device_sm_count());
   if (a.n < 4 * blocks) return false;
-  const size_t fixed = backward ? (size_t)3 * a.D * 4 : 0, room = kRingBytes / per_sm;
+  const size_t fixed = backward ? (size_t)2 * a.D * 4 : 0, room = kRingBytes / per_sm;
   if (room < fixed + 2 * bytes * r->n_src) return false;
   r->stages = (int)std::min<size_t>(kMaxStages, (room - fixed) / (bytes * r->n_src));
   *grid = (unsigned)blocks;
@@ -575,13 +673,18 @@ cudaError_t fwd_direct(const NormArgs& a, cudaStream_t st) {
   norm_fwd<T, E, VEC><<<(unsigned)std::min<int64_t>(a.n, 1 << 20), threads_for(a.D, E), 0, st>>>(a);
   return cudaGetLastError();
 }
+template <typename T, int E, bool ROWGATE>
+cudaError_t fwd_ring_one(const NormArgs& a, const RowRing& ring, unsigned grid, size_t smem, cudaStream_t st) {
+  static size_t set[kMaxDevices] = {};
+  const cudaError_t e = set_smem_limit((const void*)norm_fwd_ring<T, E, ROWGATE>, kRingBytes, set);
+  if (e != cudaSuccess) return e;
+  norm_fwd_ring<T, E, ROWGATE><<<grid, threads_for(a.D, E), smem, st>>>(a, ring);
+  return cudaGetLastError();
+}
 template <typename T, int E>
 cudaError_t fwd_ring(const NormArgs& a, const RowRing& ring, unsigned grid, size_t smem, cudaStream_t st) {
-  static size_t set[kMaxDevices] = {};
-  const cudaError_t e = set_smem_limit((const void*)norm_fwd_ring<T, E>, kRingBytes, set);
-  if (e != cudaSuccess) return e;
-  norm_fwd_ring<T, E><<<grid, threads_for(a.D, E), smem, st>>>(a, ring);
-  return cudaGetLastError();
+  return a.gate && a.gate_rows ? fwd_ring_one<T, E, true>(a, ring, grid, smem, st)
+                               : fwd_ring_one<T, E, false>(a, ring, grid, smem, st);
 }
 template <typename T, int E, bool VEC>
 cudaError_t bwd_direct(const NormArgs& a, unsigned grid, cudaStream_t st) {
@@ -591,13 +694,18 @@ cudaError_t bwd_direct(const NormArgs& a, unsigned grid, cudaStream_t st) {
   norm_bwd<T, E, VEC><<<grid, threads_for(a.D, E), (size_t)3 * a.D * 4, st>>>(a);
   return cudaGetLastError();
 }
+template <typename T, int E, bool ROWGATE>
+cudaError_t bwd_ring_one(const NormArgs& a, const RowRing& ring, unsigned grid, size_t smem, cudaStream_t st) {
+  static size_t set[kMaxDevices] = {};
+  const cudaError_t e = set_smem_limit((const void*)norm_bwd_ring<T, E, ROWGATE>, kRingBytes, set);
+  if (e != cudaSuccess) return e;
+  norm_bwd_ring<T, E, ROWGATE><<<grid, threads_for(a.D, E), smem, st>>>(a, ring);
+  return cudaGetLastError();
+}
 template <typename T, int E>
 cudaError_t bwd_ring(const NormArgs& a, const RowRing& ring, unsigned grid, size_t smem, cudaStream_t st) {
-  static size_t set[kMaxDevices] = {};
-  const cudaError_t e = set_smem_limit((const void*)norm_bwd_ring<T, E>, kRingBytes, set);
-  if (e != cudaSuccess) return e;
-  norm_bwd_ring<T, E><<<grid, threads_for(a.D, E), smem, st>>>(a, ring);
-  return cudaGetLastError();
+  return a.gate && a.gate_rows ? bwd_ring_one<T, E, true>(a, ring, grid, smem, st)
+                               : bwd_ring_one<T, E, false>(a, ring, grid, smem, st);
 }
 
 template <typename T>
