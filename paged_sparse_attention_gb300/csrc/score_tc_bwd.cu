@@ -47,6 +47,9 @@ struct TileSpan {
   int64_t lo, hi, clo, chi;
 };
 
+template <TanhForm F>
+using Const = std::integral_constant<TanhForm, F>;
+
 struct ScoreBwdParams {
   ScoreArgs s;
   CapConst cap;
@@ -338,21 +341,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float f0 = BIAS ? (float)(a.q_start + q0 - kpos) : 0.f;  // distance of column i: |f0 + i|
-        bool small = true;
-        if constexpr (CAP) {
-          float mx = fmaxf(__uint_as_float(sr[0]), __uint_as_float(sr[1]));
-          float mn = fminf(__uint_as_float(sr[0]), __uint_as_float(sr[1]));
-#pragma unroll
-          for (int i = 2; i < 32; i += 2) {
-            mx = fmax3(mx, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
-            mn = fmin3(mn, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
-          }
-          small = __all_sync(0xffffffffu, fmaxf(mx, -mn) <= p.cap.s_small);
-        }
         uint32_t pk[16], dk[16];
-        // P and dA of column pairs; WIDE: the tanh by its exponential form
-        auto columns = [&](auto wide) {
-          constexpr bool WIDE = decltype(wide)::value;
+        // P and dA of the columns, four at a time
+        auto columns = [&](auto form, auto ranged) {
+          constexpr TanhForm F = decltype(form)::value;
+          constexpr bool RANGED = decltype(ranged)::value;
 #pragma unroll
           for (int c4 = 0; c4 < 8; ++c4) {
             const float4 L = vs4[c4], Dv = vs4[16 + c4];
@@ -364,17 +357,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float S = __uint_as_float(sr[i]);
               float shift = -l4[e];
               if (BIAS) shift = fmaf(-slope2, fabsf(f0 + (float)i), shift);
-              float th = 0.f, s2;
-              if constexpr (CAP) {
-                th = WIDE ? tanh_wide(S, p.cap) : tanh_small(S, p.cap);
-                s2 = fmaf(th, p.cap.cap2, shift);
-              } else {
-                s2 = fmaf(S, p.scale_log2, shift);
-              }
-              float pv = ex2_approx(s2);
+              float th = 0.f;
+              if constexpr (CAP) th = tanh_of<F>(S, p.cap);
+              float pv = ex2_approx(CAP ? fmaf(th, p.cap.cap2, shift) : fmaf(S, p.scale_log2, shift));
               float da = pv * (__uint_as_float(dr[i]) - d4[e]);
               if constexpr (CAP) da *= fmaf(-th, th, 1.f);
-              if (masked && !((see >> i) & 1u)) pv = da = 0.f;
+              if (RANGED && !((see >> i) & 1u)) pv = da = 0.f;
               pr[e] = pv;
               dar[e] = da;
             }
@@ -384,10 +372,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             dk[2 * c4 + 1] = pack_bf16x2(dar[2], dar[3]);
           }
         };
-        if (!CAP || small)
-          columns(std::false_type{});
-        else
-          columns(std::true_type{});
+        TanhForm form = kWide;
+        if constexpr (CAP) {
+          float mx = fmaxf(__uint_as_float(sr[0]), __uint_as_float(sr[1]));
+          float mn = fminf(__uint_as_float(sr[0]), __uint_as_float(sr[1]));
+#pragma unroll
+          for (int i = 2; i < 32; i += 2) {
+            mx = fmax3(mx, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+            mn = fmin3(mn, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+          }
+          form = __all_sync(0xffffffffu, fmaxf(mx, -mn) <= p.cap.edge2) ? kDegree2 : kWide;
+        }
+        if (CAP && form == kDegree2) {
+          if (masked) columns(Const<kDegree2>{}, std::true_type{}); else columns(Const<kDegree2>{}, std::false_type{});
+        } else {
+          if (masked) columns(Const<kWide>{}, std::true_type{}); else columns(Const<kWide>{}, std::false_type{});
+        }
         // P^T and dA^T go over this thread's own (already loaded) S^T columns
         tmem_st16(base, pk);
         tmem_st16(base + 16, dk);

@@ -1,45 +1,43 @@
 // Score arithmetic shared by the tensor-core kernels of the attention with modified scores.
 //
-// Scores are kept in units of log2: s2 = s log2(e), so that P = 2^(s2 - m).  For |x| <= 1,
-// x = scale q.k / cap, the capped score is S times a polynomial in S^2 (S the raw dot
-// product, the cap and the scale folded into the coefficients): tanh(x) / x as a polynomial
-// of degree 5 in x^2 fitted on [0, 1] for the least relative error (5.9e-7).  That is seven
-// packed multiply-adds for two scores and leaves the exponential unit, which bounds these
-// kernels, to the softmax; tanh.approx would be one instruction but is off by 2^-11, half a
-// unit of the score at a cap of 1000.  Outside, tanh(x) = 1 - 2 / (1 + e^2x), two operations
-// of that unit each, exact at saturation.
+// Scores are kept in units of log2: s2 = s log2(e), so that P = 2^(s2 - m).  With
+// x = scale q.k / cap the capped score is cap tanh(x).  Where all of a warp's |x| are small,
+// tanh(x) = x times a polynomial in x^2, fitted for the least relative error: degree 2 up to
+// 1/4 (4.0e-7) and degree 3 up to 1/2 (5.4e-7); the scale and the cap are folded into the
+// coefficients, so a score costs two or three multiply-adds more than an uncapped one.
+// Elsewhere tanh(x) = 1 - 2 / (1 + e^2x), exact at saturation, for two more operations of the
+// exponential unit.  (tanh.approx is one instruction, but off by 2^-11: 0.02 of a score at a
+// cap of 50.)
 #pragma once
 #include "score_common.cuh"
 #include "tc_common.cuh"
 
 namespace oomb {
 
-constexpr int kTanhTerms = 6;
+constexpr float kTanhEdge2 = 0.25f, kTanhEdge3 = 0.5f;  // |x| up to which degree 2 and 3 hold
 
 struct CapConst {
-  float poly[kTanhTerms];  // s2 = S (poly[0] + poly[1] S^2 + ...), |S| <= s_small
-  float s_small;           // |S| up to which the polynomial holds
-  float arg;               // 2 scale log2(e) / cap:  e^2x = 2^(arg S)
-  float cap2;              // cap log2(e)
-  float unit;              // scale / cap:  x = unit S
-  float poly_t[kTanhTerms];  // tanh(x) = S (poly_t[0] + poly_t[1] S^2 + ...)
+  float poly2[3], poly3[4];  // tanh(x) = S (poly[0] + poly[1] S^2 + ...), S the raw dot product
+  float edge2, edge3;        // |S| up to which they hold
+  float arg;                 // 2 scale log2(e) / cap:  e^2x = 2^(arg S)
+  float cap2;                // cap log2(e)
 };
 
 inline CapConst make_cap(float cap, float scale) {
-  static const double kFit[kTanhTerms] = {0.9999994135992796,   -0.333290423785063,  0.1328143388055857,
-                                          -0.05160567399853968, 0.016743115061095788, -0.003067060325955233};
+  static const double kFit2[3] = {0.9999996043444983, -0.33321908225036645, 0.1284161343106791};
+  static const double kFit3[4] = {0.9999994557709395, -0.3332631793593743, 0.13190296603150334, -0.04440222612595766};
   CapConst c = {};
   if (!(cap > 0.f)) return c;
-  const double k = (double)scale / (double)cap;
+  const double k = (double)scale / (double)cap, ak = k < 0 ? -k : k;
   double p = k;
-  for (int i = 0; i < kTanhTerms; ++i, p *= k * k) {
-    c.poly[i] = (float)(kFit[i] * p * (double)cap * 1.4426950408889634);
-    c.poly_t[i] = (float)(kFit[i] * p);
+  for (int i = 0; i < 4; ++i, p *= k * k) {
+    if (i < 3) c.poly2[i] = (float)(kFit2[i] * p);
+    c.poly3[i] = (float)(kFit3[i] * p);
   }
-  c.s_small = k != 0.0 ? (float)(1.0 / (k < 0 ? -k : k)) : INFINITY;
+  c.edge2 = ak > 0.0 ? (float)(kTanhEdge2 / ak) : INFINITY;
+  c.edge3 = ak > 0.0 ? (float)(kTanhEdge3 / ak) : INFINITY;
   c.arg = (float)(2.0 * k * 1.4426950408889634);
   c.cap2 = (float)((double)cap * 1.4426950408889634);
-  c.unit = (float)k;
   return c;
 }
 
@@ -49,25 +47,22 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float tanh_wide(float S, const CapConst& c) {
-  return fmaf(-2.f, rcp_approx(1.f + ex2_approx(c.arg * S)), 1.f);
-}
-__device__ __forceinline__ float tanh_small(float S, const CapConst& c) {
+enum TanhForm { kDegree2, kDegree3, kWide };
+
+template <TanhForm F>
+__device__ __forceinline__ float tanh_of(float S, const CapConst& c) {
+  if constexpr (F == kWide) return fmaf(-2.f, rcp_approx(1.f + ex2_approx(c.arg * S)), 1.f);
   const float z = S * S;
-  float p = c.poly_t[kTanhTerms - 1];
-#pragma unroll
-  for (int i = kTanhTerms - 2; i >= 0; --i) p = fmaf(p, z, c.poly_t[i]);
-  return S * p;
+  if constexpr (F == kDegree2) return S * fmaf(fmaf(c.poly2[2], z, c.poly2[1]), z, c.poly2[0]);
+  return S * fmaf(fmaf(fmaf(c.poly3[3], z, c.poly3[2]), z, c.poly3[1]), z, c.poly3[0]);
 }
-__device__ __forceinline__ float capped(float S, const CapConst& c) {
-  if (fabsf(S) <= c.s_small) {
-    const float z = S * S;
-    float p = c.poly[kTanhTerms - 1];
-#pragma unroll
-    for (int i = kTanhTerms - 2; i >= 0; --i) p = fmaf(p, z, c.poly[i]);
-    return S * p;
-  }
-  return c.cap2 * tanh_wide(S, c);
+// A form that holds for every |S| <= amax (NaN: the wide one).
+__device__ __forceinline__ TanhForm tanh_form(float amax, const CapConst& c) {
+  return amax <= c.edge2 ? kDegree2 : amax <= c.edge3 ? kDegree3 : kWide;
+}
+__device__ __forceinline__ float tanh_any(float S, const CapConst& c) {
+  const TanhForm f = tanh_form(fabsf(S), c);
+  return f == kDegree2 ? tanh_of<kDegree2>(S, c) : f == kDegree3 ? tanh_of<kDegree3>(S, c) : tanh_of<kWide>(S, c);
 }
 
 }  // namespace oomb

@@ -12,12 +12,18 @@
 // are two parts).  A block is bound by the exponential unit with many rows (as the plain
 // forward) and by HBM in the packed layout.
 //
-// Warp roles (320 threads): warp 0 TMA producer (K ring of 3, V ring of 2 tiles), warp 1 MMA
-// issuer and TMEM owner, warps 2-5 softmax of tile A, 6-9 of tile B (thread = query row, its
-// 128 scores in registers).  The tensor core runs PV_A(j), S_A(j+1), PV_B(j), S_B(j+1).  MMAs
-// complete in order, so the softmax warp that has seen S_X(j) knows that PV_X(j-1) is done and
-// frees the ring slots.  TMEM columns: S_A, S_B (P over S, bf16), O_A, O_B, 128 each.
+// Warp roles (576 threads): warp 0 TMA producer (K ring of 3, V ring of 2 tiles), warp 1 MMA
+// issuer and TMEM owner, warps 2-9 softmax of tile A, 10-17 of tile B.  A query row belongs to
+// two threads, 64 scores each: with one thread a row the score arithmetic of one tile takes
+// longer than the products of the other, and two warps of a scheduler can share the units
+// that one warp alone leaves idle while it waits for its own results.  The two exchange their
+// maxima through shared memory and a barrier of their pair of warps.  The tensor core runs
+// PV_A(j), S_A(j+1), PV_B(j), S_B(j+1).  MMAs complete in order, so the softmax warp that has
+// seen S_X(j) knows that PV_X(j-1) is done and frees the ring slots.
+// TMEM columns: S_A, S_B (P over S, bf16), O_A, O_B, 128 each.
 // Scores and row sums are fp32; P is rounded to bf16, the operand type of the second product.
+#include <type_traits>
+
 #include "score_tc_common.cuh"
 
 namespace oomb {
@@ -27,9 +33,12 @@ using namespace tc;
 
 constexpr int kKStages = 3;
 constexpr int kVStages = 2;
-constexpr int kThreads = 320;
-constexpr int kGroupThreads = 128;
+constexpr int kThreads = 576;
+constexpr int kTileWarps = 8;  // softmax warps of a tile
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled when the row maximum grows by more
+
+template <TanhForm F>
+using Const = std::integral_constant<TanhForm, F>;
 
 struct ScoreFwdParams {
   ScoreArgs s;
@@ -48,17 +57,21 @@ struct __align__(8) FwdBarriers {
   uint64_t p_full[2];
   uint64_t o_done[2];
   uint64_t mma_done;
-  int64_t lo[8], hi[8];  // key range seen by each softmax warp's rows
+  float half[2][2][kTile];  // per tile, column half and row: maximum of the scores, at the end the sum of P
+  int64_t lo[8], hi[8];     // key range seen by each 32 rows of the tiles
   int below[4];          // selected pages below: tile A's first, A's end, B's first, B's end
   uint32_t tmem_base;
   int abort;
+  int fail[2][4];  // page (+ 1) at which a warp of the pair that shares these 32 rows gave up waiting
 };
 
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = 2 * kTileBytes;
 constexpr uint32_t kOffV = kOffK + kKStages * kTileBytes;
 constexpr uint32_t kOffBar = kOffV + kVStages * kTileBytes;
-constexpr size_t kSmemBytes = 1024 + kOffBar + sizeof(FwdBarriers);
+// No alignment slack: there is no static shared memory, and the dynamic window starts on a
+// 1 KB boundary (checked at entry; the swizzled tiles need it).
+constexpr size_t kSmemBytes = kOffBar + sizeof(FwdBarriers);
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 // The pages of the two tiles, as entries of the selection.  rows: tile x reads [first[x],
@@ -124,9 +137,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     score_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ ScoreFwdParams p) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  FwdBarriers* bar = reinterpret_cast<FwdBarriers*>(sm + kOffBar);
   const AttnArgs& a = p.s.a;
+  if (smem_u32(smem_raw) & 1023u) {  // uniform over the grid: every block leaves here
+    if (threadIdx.x == 0) atomicOr(a.err, OOMB_DEVERR_SMEM);
+    return;
+  }
+  uint8_t* sm = smem_raw;
+  FwdBarriers* bar = reinterpret_cast<FwdBarriers*>(sm + kOffBar);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int G = a.g.G, Hq = a.g.Hq;
   const int h = PACK ? (int)blockIdx.x : (int)blockIdx.x / G;
@@ -138,8 +155,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &bar->abort;
 
   // softmax thread: its row, query head and key range
-  const int x = warp < 2 ? 0 : (warp - 2) >> 2;  // tile
-  const int r = (warp & 3) * 32 + lane;          // row of the tile == TMEM lane
+  const int x = warp < 2 ? 0 : (warp - 2) >> 3;      // tile
+  const int half = warp < 2 ? 0 : (warp - 2) >> 2 & 1;  // key columns [64 half, 64 half + 64)
+  const int r = (warp & 3) * 32 + lane;              // row of the tile == TMEM lane
   int row = 0, hq = 0;
   bool valid = false;
   int64_t kb = 0, ke = INT64_MAX;  // rows that do not exist ask for no masking
@@ -160,13 +178,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
       hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
-    if (lane == 0) {
-      bar->lo[warp - 2] = lo;
-      bar->hi[warp - 2] = hi;
+    if (lane == 0 && half == 0) {
+      bar->lo[4 * x + (warp & 3)] = lo;
+      bar->hi[4 * x + (warp & 3)] = hi;
     }
     if (PACK) {  // rows of Q that no load fills
       const int used = a.n_q * G;
-      for (int idx = (int)threadIdx.x - 64; idx < (kTile - used) * 16; idx += 2 * kGroupThreads) {
+      for (int idx = (int)threadIdx.x - 64; idx < (kTile - used) * 16; idx += kThreads - 64) {
         const int rr = used + idx / 16, c = idx % 16;
         *reinterpret_cast<uint4*>(sm + kOffQ + (c >> 3) * kHalfBytes + rr * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
       }
@@ -185,12 +203,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->s_full[i], 1);
-      mbar_init(&bar->p_full[i], kGroupThreads / 32);
+      mbar_init(&bar->p_full[i], kTileWarps);
       mbar_init(&bar->o_done[i], 1);
     }
     mbar_init(&bar->mma_done, 1);
     bar->abort = 0;
-    for (int i = 0; i < 4; ++i) bar->below[i] = 0;
+    for (int i = 0; i < 4; ++i) bar->below[i] = bar->fail[0][i] = bar->fail[1][i] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -355,7 +373,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nx = t.n[x];
     const uint32_t lane_off = tmem_lane_base(warp);
     const uint32_t tS = tmem + lane_off + x * 128;
-    const uint32_t tO = tmem + lane_off + 256 + x * 128;
+    const uint32_t tO = tmem + lane_off + 256 + x * 128 + half * 64;  // this thread's columns of O
+    const int pair_bar = 1 + 4 * x + (warp & 3);  // barrier of the two warps that share the rows
+    volatile float* mine = &bar->half[x][half][r];
+    volatile float* other = &bar->half[x][half ^ 1][r];
+    volatile int* fail = &bar->fail[x][warp & 3];
     const int64_t qpos = a.q_start + row;
     const float slope2 = BIAS ? p.s.slopes[hq] * kLog2e : 0.f;
     const int32_t* sel = a.sel + (size_t)h * a.max_sel + t.first[x];
@@ -366,17 +388,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 0; j < nx; ++j) {
       const bool known = pg >= 0 && pg < p.s.n_view && pg < a.g.max_logical;
       const int phys = known ? a.kv.table[pg] : -1;
-      const int64_t p0 = (int64_t)pg * kTile;
-      // keys [cb, ce) of the page are visible to this row; a page left out has none
-      const bool mapped = phys >= 0 && phys < a.g.num_phys;
-      const bool whole = __all_sync(0xffffffffu, mapped && kb <= p0 && ke >= p0 + kTile);
+      const int64_t p0 = (int64_t)pg * kTile + half * 64;  // this thread's first key
+      const bool mapped = phys >= 0 && phys < a.g.num_phys;  // a page left out has no visible key
+      const bool whole = __all_sync(0xffffffffu, mapped && kb <= p0 && ke >= p0 + 64);
       const int pg_next = j + 1 < nx ? sel[j + 1] : 0;
       if (ok) ok = mbar_wait(&bar->s_full[x], j & 1, a.err, abort);
       ok = __all_sync(0xffffffffu, ok);  // TMEM loads and stores below are warp-collective
-      if (!ok) break;
+      if (!ok) {  // meet the other warp of the pair at its barrier, so that both leave here
+        if (lane == 0) *fail = j + 1;
+        named_bar_sync(pair_bar, 64);
+        break;
+      }
       tc_fence_after();
-      const int e = ring_of<PACK>(t, x, j);
-      if ((warp & 3) == 2 && lane == 0) {
+      if (((warp - 2) & 7) == 0 && lane == 0) {
+        const int e = ring_of<PACK>(t, x, j);
         if (PACK) {  // each ring entry has one user
           mbar_arrive(&bar->k_empty[e % kKStages]);
           if (j > 0) mbar_arrive(&bar->v_empty[ring_of<PACK>(t, x, j - 1) % kVStages]);
@@ -385,11 +410,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (e > 0) mbar_arrive(&bar->v_empty[(e - 1) % kVStages]);
         }
       }
-      uint32_t sr[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+      uint32_t sr[64];
+      tmem_ld32(tS + half * 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+      tmem_ld32(tS + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
       tmem_wait_ld();
-      // scores in log2 units (without cap and bias the scale is folded into the exponent)
+      // Where every key is visible and there is no bias, the row maximum comes from the raw
+      // dot products (the cap is monotonic) and the cap is applied inside the exponent.
+      // Elsewhere the scores are formed in place first, in log2 units.
+      const bool direct = !BIAS && whole;
+      TanhForm form = kWide;
+      float tmax;
       if constexpr (CAP) {
         float mx[4], mn[4];
 #pragma unroll
@@ -398,45 +428,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           mn[k] = fminf(__uint_as_float(sr[k]), __uint_as_float(sr[4 + k]));
         }
 #pragma unroll
-        for (int c = 8; c < 128; c += 8)
+        for (int c = 8; c < 64; c += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             mx[k] = fmax3(mx[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 4 + k]));
             mn[k] = fmin3(mn[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 4 + k]));
           }
-        const float amax = fmaxf(fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]),
-                                 -fmin3(fminf(mn[0], mn[1]), mn[2], mn[3]));
-        if (__all_sync(0xffffffffu, amax <= p.cap.s_small)) {
-          uint64_t co[kTanhTerms];
+        const float top = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+        const float amax = fmaxf(top, -fmin3(fminf(mn[0], mn[1]), mn[2], mn[3]));
+        form = __all_sync(0xffffffffu, amax <= p.cap.edge2)   ? kDegree2
+               : __all_sync(0xffffffffu, amax <= p.cap.edge3) ? kDegree3
+                                                              : kWide;
+        // the scale's sign decides whether the largest dot product is the largest score
+        tmax = p.cap.cap2 * tanh_any(p.scale_log2 >= 0.f ? top : fmin3(fminf(mn[0], mn[1]), mn[2], mn[3]), p.cap);
+        if (!direct) {
+          auto cap_all = [&](auto f) {
 #pragma unroll
-          for (int i = 0; i < kTanhTerms; ++i) co[i] = f32x2(p.cap.poly[i], p.cap.poly[i]);
-#pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            const uint64_t S = f32x2(sr[2 * c], sr[2 * c + 1]);
-            const uint64_t z = fmul2(S, S);
-            uint64_t v = co[kTanhTerms - 1];
-#pragma unroll
-            for (int i = kTanhTerms - 2; i >= 0; --i) v = ffma2(v, z, co[i]);
-            float y0, y1;
-            f32x2_split(fmul2(v, S), y0, y1);
-            sr[2 * c] = __float_as_uint(y0);
-            sr[2 * c + 1] = __float_as_uint(y1);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            sr[c] = __float_as_uint(p.cap.cap2 * tanh_wide(__uint_as_float(sr[c]), p.cap));
+            for (int c = 0; c < 64; ++c)
+              sr[c] = __float_as_uint(p.cap.cap2 * tanh_of<decltype(f)::value>(__uint_as_float(sr[c]), p.cap));
+          };
+          if (form == kDegree2)
+            cap_all(Const<kDegree2>{});
+          else if (form == kDegree3)
+            cap_all(Const<kDegree3>{});
+          else
+            cap_all(Const<kWide>{});
         }
       }
       if constexpr (BIAS) {
         const float f0 = (float)(qpos - p0);  // distance of key column c: |f0 - c|
         const float sc = CAP ? 1.f : p.scale_log2;
-        if (__all_sync(0xffffffffu, f0 >= (float)kTile)) {  // every key behind the row: linear in c
+        if (__all_sync(0xffffffffu, f0 >= 64.f)) {  // every key behind the row: linear in c
           const uint64_t sc2 = f32x2(sc, sc), step = f32x2(2.f * slope2, 2.f * slope2);
-          uint64_t bias = f32x2(-slope2 * f0, -slope2 * (f0 - 1.f));
+          uint64_t bias = 0;
           const float b0 = -slope2 * f0;
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
+          for (int c = 0; c < 32; ++c) {
             if (c % 8 == 0)  // restart: the running sum gathers no more than 8 roundings
               bias = f32x2(fmaf(slope2, (float)(2 * c), b0), fmaf(slope2, (float)(2 * c + 1), b0));
             float y0, y1;
@@ -447,29 +474,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
+          for (int c = 0; c < 64; ++c)
             sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), sc, -slope2 * fabsf(f0 - (float)c)));
         }
       }
       if (!whole) {
         const int64_t rb = kb - p0, re = ke - p0;
-        const int cb = mapped ? (int)max((int64_t)0, min(rb, (int64_t)kTile)) : kTile;
-        const int ce = mapped ? (int)max((int64_t)0, min(re, (int64_t)kTile)) : 0;
+        const int cb = mapped ? (int)max((int64_t)0, min(rb, (int64_t)64)) : 64;
+        const int ce = mapped ? (int)max((int64_t)0, min(re, (int64_t)64)) : 0;
+        const float sc = !CAP && !BIAS ? p.scale_log2 : 1.f;
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c < cb || c >= ce) sr[c] = 0xff800000u;  // -inf
+        for (int c = 0; c < 64; ++c)
+          sr[c] = c < cb || c >= ce ? 0xff800000u : __float_as_uint(sc * __uint_as_float(sr[c]));
       }
-      constexpr bool kRaw = !CAP && !BIAS;  // sr still holds q.k
-      float mx[8];
+      if (!CAP || !direct) {
+        float mx[8];
+        const bool flip = direct && p.scale_log2 < 0.f;  // raw dot products under a negative scale
 #pragma unroll
-      for (int k = 0; k < 8; ++k) mx[k] = fmaxf(__uint_as_float(sr[k]), __uint_as_float(sr[8 + k]));
+        for (int k = 0; k < 8; ++k) mx[k] = fmaxf(__uint_as_float(sr[k]), __uint_as_float(sr[8 + k]));
 #pragma unroll
-      for (int c = 16; c < 128; c += 16)
+        for (int c = 16; c < 64; c += 16)
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mx[k] = fmax3(mx[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
-      float tmax = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-      if (kRaw) tmax *= p.scale_log2;
+          for (int k = 0; k < 8; ++k)
+            mx[k] = fmax3(mx[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
+        tmax = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+        if (flip) {
+          float mn = __uint_as_float(sr[0]);
+#pragma unroll
+          for (int c = 1; c < 64; ++c) mn = fminf(mn, __uint_as_float(sr[c]));
+          tmax = mn;
+        }
+        if (!CAP && direct) tmax *= p.scale_log2;
+      }
+      // the row's maximum over both halves.  One buffer is enough: no warp sees the next S
+      // before every warp of the tile has handed in its P of this page
+      *mine = tmax;
+      named_bar_sync(pair_bar, 64);
+      if (*fail == j + 1) {  // (a later page's failure is met at that page's barrier)
+        ok = false;
+        break;
+      }
+      tmax = fmaxf(tmax, *other);
       bool rescale_o = false;
       float alpha = 1.f;
       if (tmax > m + kRescaleThreshold || (m == -INFINITY && tmax > -INFINITY)) {
@@ -480,23 +525,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = m_new;
       }
       const float neg_m = (m == -INFINITY) ? 0.f : -m;
-      const float sc = kRaw ? p.scale_log2 : 1.f;
-      const uint64_t scale2 = f32x2(sc, sc), negm2 = f32x2(neg_m, neg_m);
+      // P = 2^(score - m) of column pairs: arg(pair) is the exponent
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      auto exponentials = [&](auto arg) {
 #pragma unroll
-      for (int c = 0; c < 64; ++c) {
-        float t0, t1;
-        const uint64_t s2 = f32x2(sr[2 * c], sr[2 * c + 1]);
-        f32x2_split(kRaw ? ffma2(s2, scale2, negm2) : fadd2(s2, negm2), t0, t1);
-        const float p0v = ex2_approx(t0), p1v = ex2_approx(t1);
-        sum[c & 3] += p0v + p1v;
-        sr[c] = pack_bf16x2(p0v, p1v);
+        for (int c = 0; c < 32; ++c) {
+          float t0, t1;
+          arg(c, t0, t1);
+          const float p0v = ex2_approx(t0), p1v = ex2_approx(t1);
+          sum[c & 3] += p0v + p1v;
+          sr[c] = pack_bf16x2(p0v, p1v);
+        }
+      };
+      const uint64_t negm2 = f32x2(neg_m, neg_m);
+      auto pair_of = [&](int c) { return f32x2(sr[2 * c], sr[2 * c + 1]); };
+      if (!direct) {
+        exponentials([&](int c, float& t0, float& t1) { f32x2_split(fadd2(pair_of(c), negm2), t0, t1); });
+      } else if constexpr (!CAP) {
+        const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2);
+        exponentials([&](int c, float& t0, float& t1) { f32x2_split(ffma2(pair_of(c), sc2, negm2), t0, t1); });
+      } else if (form == kDegree2) {
+        const float* q = p.cap.poly2;
+        const float k2 = p.cap.cap2;
+        const uint64_t q0 = f32x2(q[0] * k2, q[0] * k2), q1 = f32x2(q[1] * k2, q[1] * k2), q2 = f32x2(q[2] * k2, q[2] * k2);
+        exponentials([&](int c, float& t0, float& t1) {
+          const uint64_t S = pair_of(c), z = fmul2(S, S);
+          f32x2_split(ffma2(S, ffma2(ffma2(q2, z, q1), z, q0), negm2), t0, t1);
+        });
+      } else if (form == kDegree3) {
+        const float* q = p.cap.poly3;
+        const float k2 = p.cap.cap2;
+        const uint64_t q0 = f32x2(q[0] * k2, q[0] * k2), q1 = f32x2(q[1] * k2, q[1] * k2),
+                       q2 = f32x2(q[2] * k2, q[2] * k2), q3 = f32x2(q[3] * k2, q[3] * k2);
+        exponentials([&](int c, float& t0, float& t1) {
+          const uint64_t S = pair_of(c), z = fmul2(S, S);
+          f32x2_split(ffma2(S, ffma2(ffma2(ffma2(q3, z, q2), z, q1), z, q0), negm2), t0, t1);
+        });
+      } else {
+        exponentials([&](int c, float& t0, float& t1) {
+          t0 = fmaf(p.cap.cap2, tanh_of<kWide>(__uint_as_float(sr[2 * c]), p.cap), neg_m);
+          t1 = fmaf(p.cap.cap2, tanh_of<kWide>(__uint_as_float(sr[2 * c + 1]), p.cap), neg_m);
+        });
       }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      // The rescale is decided per row but the TMEM accesses are warp-collective: the warp
+      // rescales when any of its rows needs it, the other rows scale by alpha = 1 (exact).
       if (__any_sync(0xffffffffu, rescale_o)) {  // PV of the previous page finished before this S
         if (!rescale_o) alpha = 1.f;
 #pragma unroll 1
-        for (int cc = 0; cc < 4; ++cc) {
+        for (int cc = 0; cc < 2; ++cc) {
           uint32_t o[32];
           tmem_ld32(tO + cc * 32, o);
           tmem_wait_ld();
@@ -505,37 +582,48 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st32(tO + cc * 32, o);
         }
       }
-      tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-      tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+      // packed key columns 2c, 2c + 1 of this half -> column 32 half + c (both halves of S are
+      // in registers since the pair's barrier)
+      tmem_st32(tS + half * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->p_full[x]);
       pg = pg_next;
     }
-    // epilogue: this thread's row of O, normalised
+    // epilogue: this thread's half row of O, normalised by the sum over both halves
     const size_t rows = (size_t)a.n_q * Hq, rh = (size_t)row * Hq + hq;
     const int part = PACK ? 2 * (int)blockIdx.z + x : (int)blockIdx.z;
     const bool split = PACK || p.s.n_split > 1;
-    const bool done = __all_sync(0xffffffffu, ok && nx > 0 && mbar_wait(&bar->o_done[x], 0, a.err, abort));
+    bool done = __all_sync(0xffffffffu, ok && nx > 0 && mbar_wait(&bar->o_done[x], 0, a.err, abort));
+    if (nx > 0) {  // (done: the last PV has run, so every warp of the tile is past its last exchange)
+      if (done)
+        *mine = l;
+      else if (lane == 0)
+        *fail = nx + 1;
+      named_bar_sync(pair_bar, 64);
+      done = done && !*fail;
+      if (done) l += *other;
+    }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const float lse = done ? (m + log2f(l)) * kLn2 : -INFINITY;
     if (done) {
       tc_fence_after();
 #pragma unroll 1
-      for (int cc = 0; cc < 4; ++cc) {
+      for (int cc = 0; cc < 2; ++cc) {
         uint32_t o[32];
         tmem_ld32(tO + cc * 32, o);
         tmem_wait_ld();
         if (!valid) continue;
+        const size_t at = rh * kD + half * 64 + cc * 32;
         if (split) {
-          float4* dst = reinterpret_cast<float4*>(p.s.part_o + ((size_t)part * rows + rh) * kD + cc * 32);
+          float4* dst = reinterpret_cast<float4*>(p.s.part_o + (size_t)part * rows * kD + at);
 #pragma unroll
           for (int v = 0; v < 8; ++v)
             dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
                                  __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o_out) + rh * kD + cc * 32);
+          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o_out) + at);
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint4 w;
@@ -548,10 +636,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (!split && valid) {
-      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o_out) + rh * kD);
-      for (int v = 0; v < 16; ++v) dst[v] = make_uint4(0, 0, 0, 0);
+      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o_out) + rh * kD + half * 64);
+      for (int v = 0; v < 8; ++v) dst[v] = make_uint4(0, 0, 0, 0);
     }
-    if (valid) {
+    if (valid && half == 0) {
       if (split)
         p.s.part_lse[(size_t)part * rows + rh] = lse;  // -inf: score_join does not read the part's O
       else
