@@ -374,14 +374,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         TanhForm form = kWide;
         if constexpr (CAP) {
-          float mx = fmaxf(__uint_as_float(sr[0]), __uint_as_float(sr[1]));
-          float mn = fminf(__uint_as_float(sr[0]), __uint_as_float(sr[1]));
+          float amax = 0.f;
 #pragma unroll
-          for (int i = 2; i < 32; i += 2) {
-            mx = fmax3(mx, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
-            mn = fmin3(mn, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
-          }
-          form = __all_sync(0xffffffffu, fmaxf(mx, -mn) <= p.cap.edge2) ? kDegree2 : kWide;
+          for (int i = 0; i < 32; i += 2) amax = fmax3_abs(amax, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+          form = __all_sync(0xffffffffu, amax <= p.cap.edge2) ? kDegree2 : kWide;
         }
         if (CAP && form == kDegree2) {
           if (masked) columns(Const<kDegree2>{}, std::true_type{}); else columns(Const<kDegree2>{}, std::false_type{});

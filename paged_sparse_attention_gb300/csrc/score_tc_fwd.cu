@@ -36,6 +36,9 @@ constexpr int kVStages = 2;
 constexpr int kThreads = 576;
 constexpr int kTileWarps = 8;  // softmax warps of a tile
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled when the row maximum grows by more
+constexpr float kGentle = 0.35f;           // log2 units a token: the bias changes by less than 45 over a page
+constexpr float kNarrowScores = 20.0f;     // log2 units: capped scores of this size differ by less than 40
+constexpr float kNothing = -127.0f;        // log2 units: 2^x is zero in fp32 with flushed denormals
 
 template <TanhForm F>
 using Const = std::integral_constant<TanhForm, F>;
@@ -74,9 +77,10 @@ constexpr uint32_t kOffBar = kOffV + kVStages * kTileBytes;
 constexpr size_t kSmemBytes = kOffBar + sizeof(FwdBarriers);
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
-// The pages of the two tiles, as entries of the selection.  rows: tile x reads [first[x],
-// first[x] + n[x]), and the ring holds the entries [lo, lo + n_ring) in order.  packed: tile x
-// reads its own n[x] entries from first[x], and the ring alternates between the tiles.
+// The pages of the two tiles, as steps of the walk over the selection (step i is entry i, or
+// count - 1 - i in the reversed walk).  rows: tile x reads [first[x], first[x] + n[x]), and the
+// ring holds the steps [lo, lo + n_ring) in order.  packed: tile x reads its own n[x] steps
+// from first[x], and the ring alternates between the tiles.
 struct TilePages {
   int first[2], n[2], lo, n_ring;
 };
@@ -86,10 +90,17 @@ __device__ __forceinline__ int ring_of(const TilePages& t, int x, int j) {  // r
   return PACK ? 2 * j + x : t.first[x] - t.lo + j;
 }
 
-template <bool PACK>
-__device__ __forceinline__ TilePages tile_pages(const ScoreFwdParams& p, const int (&below)[4]) {
+template <bool PACK, bool REVERSED>
+__device__ __forceinline__ TilePages tile_pages(const ScoreFwdParams& p, const int (&below)[4], int count) {
   TilePages t;
   int a0 = below[0], a1 = max(below[0], below[1]), b0 = below[2], b1 = max(below[2], below[3]);
+  if (REVERSED) {
+    const int u = a0, v = b0;
+    a0 = count - a1;
+    a1 = count - u;
+    b0 = count - b1;
+    b1 = count - v;
+  }
   if (PACK) {
     // the interval's share of this block, half of it for each tile.  A takes the odd page: its
     // ring slots were its own before, so every slot that is waited for is freed by its last user
@@ -132,6 +143,21 @@ __device__ __forceinline__ TilePages tile_pages(const ScoreFwdParams& p, const i
   return t;
 }
 
+// Reduction of 64 scores by a three-operand function, in eight chains.
+template <typename F>
+__device__ __forceinline__ float row_reduce(const uint32_t (&s)[64], F f) {
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = f(__uint_as_float(s[k]), __uint_as_float(s[8 + k]), __uint_as_float(s[16 + k]));
+#pragma unroll
+  for (int c = 24; c < 56; c += 16)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = f(v[k], __uint_as_float(s[c + k]), __uint_as_float(s[c + 8 + k]));
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = f(v[k], __uint_as_float(s[56 + k]), __uint_as_float(s[56 + k]));
+  return f(f(v[0], v[1], v[2]), f(v[3], v[4], v[5]), f(v[6], v[7], v[7]));
+}
+
 template <bool CAP, bool BIAS, bool PACK>
 __global__ void __launch_bounds__(kThreads, 1)
     score_fwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -148,26 +174,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = a.g.G, Hq = a.g.Hq;
   const int h = PACK ? (int)blockIdx.x : (int)blockIdx.x / G;
   const int pair = p.n_pairs - 1 - (int)blockIdx.y;
-  const int tA = 2 * pair, tB = 2 * pair + 1;
-  const bool hasB = PACK || tB < p.n_tiles;
+  // With a bias the pages are walked from the nearest to the farthest: the row maximum then
+  // comes first and O is hardly ever rescaled (upwards, a head whose bias changes by more than
+  // 2^8 over a page would rescale at every page).  The tile that ends the walk last has to be
+  // B: the later rows in the upward walk, the earlier ones (which start below) in the reversed.
+  constexpr bool REVERSED = BIAS;
+  const int tile[2] = {2 * pair + (REVERSED ? 1 : 0), 2 * pair + (REVERSED ? 0 : 1)};
   int count = a.sel_count[h];
   count = count < 0 ? 0 : min(count, a.max_sel);  // flagged by check_selection
   volatile int* abort = &bar->abort;
 
-  // softmax thread: its row, query head and key range
+  // softmax thread: its row and query head
   const int x = warp < 2 ? 0 : (warp - 2) >> 3;      // tile
   const int half = warp < 2 ? 0 : (warp - 2) >> 2 & 1;  // key columns [64 half, 64 half + 64)
   const int r = (warp & 3) * 32 + lane;              // row of the tile == TMEM lane
   int row = 0, hq = 0;
   bool valid = false;
-  int64_t kb = 0, ke = INT64_MAX;  // rows that do not exist ask for no masking
+  int64_t kb = 0, ke = INT64_MAX;  // range common to the warp's rows (rows that do not exist ask for no masking)
   if (warp >= 2) {
     if (PACK) {
       valid = r < a.n_q * G;
       row = valid ? r / G : 0;
       hq = h * G + (valid ? r % G : 0);
     } else {
-      row = (x == 0 ? tA : tB) * kTile + r;
+      row = tile[x] * kTile + r;
       valid = row < a.n_q;
       hq = (int)blockIdx.x;
     }
@@ -177,6 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int o = 16; o > 0; o >>= 1) {
       lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
       hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      kb = max(kb, __shfl_xor_sync(0xffffffffu, kb, o));
+      ke = min(ke, __shfl_xor_sync(0xffffffffu, ke, o));
     }
     if (lane == 0 && half == 0) {
       bar->lo[4 * x + (warp & 3)] = lo;
@@ -251,7 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const int below[4] = {bar->below[0], bar->below[1], bar->below[2], bar->below[3]};
-  const TilePages t = tile_pages<PACK>(p, below);
+  const TilePages t = tile_pages<PACK, REVERSED>(p, below, count);
+  auto entry = [&](int step) { return REVERSED ? count - 1 - step : step; };  // of the selection
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -265,15 +298,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_3d(sm + kOffQ, &tq, &bar->q_full, 0, h * G, 0);
         tma_load_3d(sm + kOffQ + kHalfBytes, &tq, &bar->q_full, 64, h * G, 0);
       } else {
-        mbar_arrive_expect_tx(&bar->q_full, (hasB ? 2u : 1u) * kTileBytes);
-        for (int i = 0; i < (hasB ? 2 : 1); ++i) {
-          tma_load_3d(sm + kOffQ + i * kTileBytes, &tq, &bar->q_full, 0, (int)blockIdx.x, (tA + i) * kTile);
-          tma_load_3d(sm + kOffQ + i * kTileBytes + kHalfBytes, &tq, &bar->q_full, 64, (int)blockIdx.x,
-                      (tA + i) * kTile);
+        // a tile past the last one has no pages and is not loaded
+        mbar_arrive_expect_tx(&bar->q_full, (2 * pair + 1 < p.n_tiles ? 2u : 1u) * kTileBytes);
+        for (int i = 0; i < 2; ++i) {
+          if (tile[i] >= p.n_tiles) continue;
+          uint8_t* dst = sm + kOffQ + i * kTileBytes;
+          tma_load_3d(dst, &tq, &bar->q_full, 0, (int)blockIdx.x, tile[i] * kTile);
+          tma_load_3d(dst + kHalfBytes, &tq, &bar->q_full, 64, (int)blockIdx.x, tile[i] * kTile);
         }
       }
       auto row_of = [&](int e) -> int {  // first row of ring entry e's block in the K/V maps
-        const int j = PACK ? t.first[e & 1] + (e >> 1) : t.lo + e;
+        const int j = entry(PACK ? t.first[e & 1] + (e >> 1) : t.lo + e);
         const int64_t blk = score_block(p.s, h, j, a.sel[(size_t)h * a.max_sel + j]);
         return blk < 0 ? 0 : (int)(blk * kTile);  // a page left out is masked whole: any block will do
       };
@@ -380,7 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* fail = &bar->fail[x][warp & 3];
     const int64_t qpos = a.q_start + row;
     const float slope2 = BIAS ? p.s.slopes[hq] * kLog2e : 0.f;
-    const int32_t* sel = a.sel + (size_t)h * a.max_sel + t.first[x];
+    const int32_t* sel = a.sel + (size_t)h * a.max_sel + entry(t.first[x]);
+    constexpr int kNext = REVERSED ? -1 : 1;
     const int b_first = t.first[1] - t.lo, b_end = b_first + t.n[1];  // rows: ring entries of tile B
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -390,8 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int phys = known ? a.kv.table[pg] : -1;
       const int64_t p0 = (int64_t)pg * kTile + half * 64;  // this thread's first key
       const bool mapped = phys >= 0 && phys < a.g.num_phys;  // a page left out has no visible key
-      const bool whole = __all_sync(0xffffffffu, mapped && kb <= p0 && ke >= p0 + 64);
-      const int pg_next = j + 1 < nx ? sel[j + 1] : 0;
+      const bool whole = mapped && kb <= p0 && ke >= p0 + 64;  // the same for the whole warp
+      const int pg_next = j + 1 < nx ? sel[kNext * (j + 1)] : 0;
       if (ok) ok = mbar_wait(&bar->s_full[x], j & 1, a.err, abort);
       ok = __all_sync(0xffffffffu, ok);  // TMEM loads and stores below are warp-collective
       if (!ok) {  // meet the other warp of the pair at its barrier, so that both leave here
@@ -414,34 +450,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(tS + half * 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
       tmem_ld32(tS + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
       tmem_wait_ld();
-      // Where every key is visible and there is no bias, the row maximum comes from the raw
-      // dot products (the cap is monotonic) and the cap is applied inside the exponent.
-      // Elsewhere the scores are formed in place first, in log2 units.
-      const bool direct = !BIAS && whole;
+      // ref: no less than the largest score of this half row.  `direct` (every key visible; a
+      // bias that is linear and gentle over the page; a cap whose argument is small): it is
+      // also within about 2^90 of it, so that P = 2^(score - m) neither overflows nor loses
+      // what counts, and the scores are formed inside the exponent from one pass over the raw
+      // dot products.  `nothing`: that far below the row's maximum every P is zero in fp32.
+      // Elsewhere the scores are formed in place, in log2 units, and ref is their maximum.
+      const float f0 = BIAS ? (float)(qpos - p0) : 0.f;  // distance of key column c: |f0 - c|
+      const float b0 = -slope2 * f0;
+      const bool behind = BIAS && __all_sync(0xffffffffu, f0 >= 64.f);  // every key behind its row: linear in c
+      bool direct = whole && (!BIAS || (behind && __all_sync(0xffffffffu, fabsf(slope2) <= kGentle)));
       TanhForm form = kWide;
-      float tmax;
+      float ref;
       if constexpr (CAP) {
-        float mx[4], mn[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          mx[k] = fmaxf(__uint_as_float(sr[k]), __uint_as_float(sr[4 + k]));
-          mn[k] = fminf(__uint_as_float(sr[k]), __uint_as_float(sr[4 + k]));
-        }
-#pragma unroll
-        for (int c = 8; c < 64; c += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            mx[k] = fmax3(mx[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 4 + k]));
-            mn[k] = fmin3(mn[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 4 + k]));
-          }
-        const float top = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-        const float amax = fmaxf(top, -fmin3(fminf(mn[0], mn[1]), mn[2], mn[3]));
+        const float amax = row_reduce(sr, [](float u, float v, float w) { return fmax3_abs(u, v, w); });
         form = __all_sync(0xffffffffu, amax <= p.cap.edge2)   ? kDegree2
                : __all_sync(0xffffffffu, amax <= p.cap.edge3) ? kDegree3
                                                               : kWide;
-        // the scale's sign decides whether the largest dot product is the largest score
-        tmax = p.cap.cap2 * tanh_any(p.scale_log2 >= 0.f ? top : fmin3(fminf(mn[0], mn[1]), mn[2], mn[3]), p.cap);
-        if (!direct) {
+        ref = fabsf(p.cap.cap2 * tanh_any(amax, p.cap));
+        direct = direct && form != kWide && __all_sync(0xffffffffu, ref <= kNarrowScores);
+      } else {
+        ref = p.scale_log2 * row_reduce(sr, [](float u, float v, float w) { return fmax3(u, v, w); });
+        if (p.scale_log2 < 0.f) {
+          ref = INFINITY;
+          direct = false;
+        }
+      }
+      if constexpr (BIAS) ref += fmaxf(b0, fmaf(slope2, 63.f, b0));
+      const bool nothing = behind && __all_sync(0xffffffffu, ref - m < kNothing);
+      if (!direct && !nothing) {
+        if constexpr (CAP) {
           auto cap_all = [&](auto f) {
 #pragma unroll
             for (int c = 0; c < 64; ++c)
@@ -453,121 +491,100 @@ __global__ void __launch_bounds__(kThreads, 1)
             cap_all(Const<kDegree3>{});
           else
             cap_all(Const<kWide>{});
-        }
-      }
-      if constexpr (BIAS) {
-        const float f0 = (float)(qpos - p0);  // distance of key column c: |f0 - c|
-        const float sc = CAP ? 1.f : p.scale_log2;
-        if (__all_sync(0xffffffffu, f0 >= 64.f)) {  // every key behind the row: linear in c
-          const uint64_t sc2 = f32x2(sc, sc), step = f32x2(2.f * slope2, 2.f * slope2);
-          uint64_t bias = 0;
-          const float b0 = -slope2 * f0;
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if (c % 8 == 0)  // restart: the running sum gathers no more than 8 roundings
-              bias = f32x2(fmaf(slope2, (float)(2 * c), b0), fmaf(slope2, (float)(2 * c + 1), b0));
-            float y0, y1;
-            f32x2_split(ffma2(f32x2(sr[2 * c], sr[2 * c + 1]), sc2, bias), y0, y1);
-            sr[2 * c] = __float_as_uint(y0);
-            sr[2 * c + 1] = __float_as_uint(y1);
-            bias = fadd2(bias, step);
-          }
         } else {
 #pragma unroll
+          for (int c = 0; c < 64; ++c) sr[c] = __float_as_uint(p.scale_log2 * __uint_as_float(sr[c]));
+        }
+        if constexpr (BIAS) {
+#pragma unroll
           for (int c = 0; c < 64; ++c)
-            sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), sc, -slope2 * fabsf(f0 - (float)c)));
+            sr[c] = __float_as_uint(fmaf(-slope2, fabsf(f0 - (float)c), __uint_as_float(sr[c])));
         }
-      }
-      if (!whole) {
-        const int64_t rb = kb - p0, re = ke - p0;
-        const int cb = mapped ? (int)max((int64_t)0, min(rb, (int64_t)64)) : 64;
-        const int ce = mapped ? (int)max((int64_t)0, min(re, (int64_t)64)) : 0;
-        const float sc = !CAP && !BIAS ? p.scale_log2 : 1.f;
+        if (!whole) {
+          int64_t rb = p0, re = p0 + 64;  // the row's own range, read again: few pages are cut by it
+          if (valid) row_span(p.s, row, rb, re);
+          rb -= p0;
+          re -= p0;
+          const int cb = mapped ? (int)max((int64_t)0, min(rb, (int64_t)64)) : 64;
+          const int ce = mapped ? (int)max((int64_t)0, min(re, (int64_t)64)) : 0;
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          sr[c] = c < cb || c >= ce ? 0xff800000u : __float_as_uint(sc * __uint_as_float(sr[c]));
-      }
-      if (!CAP || !direct) {
-        float mx[8];
-        const bool flip = direct && p.scale_log2 < 0.f;  // raw dot products under a negative scale
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mx[k] = fmaxf(__uint_as_float(sr[k]), __uint_as_float(sr[8 + k]));
-#pragma unroll
-        for (int c = 16; c < 64; c += 16)
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mx[k] = fmax3(mx[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
-        tmax = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-        if (flip) {
-          float mn = __uint_as_float(sr[0]);
-#pragma unroll
-          for (int c = 1; c < 64; ++c) mn = fminf(mn, __uint_as_float(sr[c]));
-          tmax = mn;
+          for (int c = 0; c < 64; ++c)
+            if (c < cb || c >= ce) sr[c] = 0xff800000u;  // -inf
         }
-        if (!CAP && direct) tmax *= p.scale_log2;
+        ref = row_reduce(sr, [](float u, float v, float w) { return fmax3(u, v, w); });
       }
       // the row's maximum over both halves.  One buffer is enough: no warp sees the next S
       // before every warp of the tile has handed in its P of this page
-      *mine = tmax;
+      *mine = ref;
       named_bar_sync(pair_bar, 64);
       if (*fail == j + 1) {  // (a later page's failure is met at that page's barrier)
         ok = false;
         break;
       }
-      tmax = fmaxf(tmax, *other);
+      ref = fmaxf(ref, *other);
       bool rescale_o = false;
       float alpha = 1.f;
-      if (tmax > m + kRescaleThreshold || (m == -INFINITY && tmax > -INFINITY)) {
-        const float m_new = fmaxf(m, tmax);
+      if (ref > m + kRescaleThreshold || (m == -INFINITY && ref > -INFINITY)) {
+        const float m_new = fmaxf(m, ref);
         alpha = exp2f(m - m_new);  // 0 when m == -inf
         rescale_o = (j > 0) && (m > -INFINITY);
         l *= alpha;
         m = m_new;
       }
       const float neg_m = (m == -INFINITY) ? 0.f : -m;
-      // P = 2^(score - m) of column pairs: arg(pair) is the exponent
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      auto exponentials = [&](auto arg) {
+      if (!(BIAS && nothing)) {
+        // P = 2^(score - m) of column pairs: arg(pair) is the exponent
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        auto exponentials = [&](auto arg) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          float t0, t1;
-          arg(c, t0, t1);
-          const float p0v = ex2_approx(t0), p1v = ex2_approx(t1);
-          sum[c & 3] += p0v + p1v;
-          sr[c] = pack_bf16x2(p0v, p1v);
+          for (int c = 0; c < 32; ++c) {
+            float t0, t1;
+            arg(c, t0, t1);
+            const float p0v = ex2_approx(t0), p1v = ex2_approx(t1);
+            sum[c & 3] += p0v + p1v;
+            sr[c] = pack_bf16x2(p0v, p1v);
+          }
+        };
+        const uint64_t negm2 = f32x2(neg_m, neg_m);
+        auto pair_of = [&](int c) { return f32x2(sr[2 * c], sr[2 * c + 1]); };
+        // what the exponent adds to a score: -m, and in the direct case the bias
+        const float b0m = b0 + neg_m;
+        const uint64_t step = f32x2(2.f * slope2, 2.f * slope2);
+        uint64_t shift = negm2;
+        auto next_shift = [&](int c) {
+          if constexpr (BIAS) {
+            if (c % 8 == 0)  // restart: the running sum gathers no more than 8 roundings
+              shift = f32x2(fmaf(slope2, (float)(2 * c), b0m), fmaf(slope2, (float)(2 * c + 1), b0m));
+            else
+              shift = fadd2(shift, step);
+          }
+          return shift;
+        };
+        if (!direct) {
+          exponentials([&](int c, float& t0, float& t1) { f32x2_split(fadd2(pair_of(c), negm2), t0, t1); });
+        } else if constexpr (!CAP) {
+          const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2);
+          exponentials([&](int c, float& t0, float& t1) { f32x2_split(ffma2(pair_of(c), sc2, next_shift(c)), t0, t1); });
+        } else if (form == kDegree2) {
+          const float* q = p.cap.poly2;
+          const float k2 = p.cap.cap2;
+          const uint64_t q0 = f32x2(q[0] * k2, q[0] * k2), q1 = f32x2(q[1] * k2, q[1] * k2), q2 = f32x2(q[2] * k2, q[2] * k2);
+          exponentials([&](int c, float& t0, float& t1) {
+            const uint64_t S = pair_of(c), z = fmul2(S, S);
+            f32x2_split(ffma2(S, ffma2(ffma2(q2, z, q1), z, q0), next_shift(c)), t0, t1);
+          });
+        } else {
+          const float* q = p.cap.poly3;
+          const float k2 = p.cap.cap2;
+          const uint64_t q0 = f32x2(q[0] * k2, q[0] * k2), q1 = f32x2(q[1] * k2, q[1] * k2),
+                         q2 = f32x2(q[2] * k2, q[2] * k2), q3 = f32x2(q[3] * k2, q[3] * k2);
+          exponentials([&](int c, float& t0, float& t1) {
+            const uint64_t S = pair_of(c), z = fmul2(S, S);
+            f32x2_split(ffma2(S, ffma2(ffma2(ffma2(q3, z, q2), z, q1), z, q0), next_shift(c)), t0, t1);
+          });
         }
-      };
-      const uint64_t negm2 = f32x2(neg_m, neg_m);
-      auto pair_of = [&](int c) { return f32x2(sr[2 * c], sr[2 * c + 1]); };
-      if (!direct) {
-        exponentials([&](int c, float& t0, float& t1) { f32x2_split(fadd2(pair_of(c), negm2), t0, t1); });
-      } else if constexpr (!CAP) {
-        const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2);
-        exponentials([&](int c, float& t0, float& t1) { f32x2_split(ffma2(pair_of(c), sc2, negm2), t0, t1); });
-      } else if (form == kDegree2) {
-        const float* q = p.cap.poly2;
-        const float k2 = p.cap.cap2;
-        const uint64_t q0 = f32x2(q[0] * k2, q[0] * k2), q1 = f32x2(q[1] * k2, q[1] * k2), q2 = f32x2(q[2] * k2, q[2] * k2);
-        exponentials([&](int c, float& t0, float& t1) {
-          const uint64_t S = pair_of(c), z = fmul2(S, S);
-          f32x2_split(ffma2(S, ffma2(ffma2(q2, z, q1), z, q0), negm2), t0, t1);
-        });
-      } else if (form == kDegree3) {
-        const float* q = p.cap.poly3;
-        const float k2 = p.cap.cap2;
-        const uint64_t q0 = f32x2(q[0] * k2, q[0] * k2), q1 = f32x2(q[1] * k2, q[1] * k2),
-                       q2 = f32x2(q[2] * k2, q[2] * k2), q3 = f32x2(q[3] * k2, q[3] * k2);
-        exponentials([&](int c, float& t0, float& t1) {
-          const uint64_t S = pair_of(c), z = fmul2(S, S);
-          f32x2_split(ffma2(S, ffma2(ffma2(ffma2(q3, z, q2), z, q1), z, q0), negm2), t0, t1);
-        });
-      } else {
-        exponentials([&](int c, float& t0, float& t1) {
-          t0 = fmaf(p.cap.cap2, tanh_of<kWide>(__uint_as_float(sr[2 * c]), p.cap), neg_m);
-          t1 = fmaf(p.cap.cap2, tanh_of<kWide>(__uint_as_float(sr[2 * c + 1]), p.cap), neg_m);
-        });
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       // The rescale is decided per row but the TMEM accesses are warp-collective: the warp
       // rescales when any of its rows needs it, the other rows scale by alpha = 1 (exact).
       if (__any_sync(0xffffffffu, rescale_o)) {  // PV of the previous page finished before this S
@@ -582,9 +599,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st32(tO + cc * 32, o);
         }
       }
-      // packed key columns 2c, 2c + 1 of this half -> column 32 half + c (both halves of S are
-      // in registers since the pair's barrier)
-      tmem_st32(tS + half * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+      if (BIAS && nothing) {
+        uint32_t zero[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) zero[c] = 0u;
+        tmem_st32(tS + half * 32, zero);
+      } else {
+        // packed key columns 2c, 2c + 1 of this half -> column 32 half + c (both halves of S are
+        // in registers since the pair's barrier)
+        tmem_st32(tS + half * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();

@@ -351,9 +351,10 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
-__device__ __forceinline__ float fmin3(float a, float b, float c) {
+// max(|a|, |b|, |c|)
+__device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
   float d;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
