@@ -13,10 +13,13 @@
 //                    and sum, O in registers
 //   score_join       the shares of a split forward joined by their log-sum-exps
 //   score_dot        D_i = dO_i . O_i
-//   score_dq_simt    a block per (64 rows, query head): dQ
-//   score_dkdv_simt  a block per (64 keys of the selection, KV head): dK and dV of those
-//                    keys over all query heads of the group and all rows, added once into
-//                    the pool rows, which no other block touches (same bits on every run)
+//   score_dq_simt    a block per (64 rows, query head, share of the keys): dQ
+//   score_dkdv_simt  a block per (64 keys of the selection, KV head, share of the rows and
+//                    query heads of the group): dK and dV of those keys, added once into the
+//                    pool rows, which no other block touches (same bits on every run)
+//   score_dq_join, score_dkdv_join   the shares of both added up in order, where tiles alone do
+//                    not fill the SMs
+#include <climits>
 #include <cmath>
 
 #include "score_common.cuh"
@@ -28,8 +31,8 @@ constexpr int kRows = 64;   // query rows of a tile
 constexpr int kKeys = 64;   // keys of a tile
 constexpr int kThreads = 256;
 constexpr int kMaxD = 128;
-constexpr int kC = kMaxD / 64;  // float4 columns per thread: columns 4 tx + 64 c
 constexpr int kLdP = kKeys + 4;
+constexpr int kMaxParts = 1024;  // of a split forward; 32 on this path, 2 an SM at most on the tensor cores
 
 // fp32 tiles in shared memory: row length d padded to a multiple of 4 plus 4, so that rows
 // start on 16 bytes and 8 rows one apart fall into different banks.
@@ -62,28 +65,40 @@ __device__ __forceinline__ void list_keys(const ScoreArgs& s, int h, int64_t v0,
   }
 }
 
-// K (and V) rows of the listed keys as fp32; absent keys are zero.
+// Four elements as fp32 (d is a multiple of 4, rows start on 16 bytes or, bf16, on 8).
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+
+// K and V rows of the listed keys as fp32; absent keys are zero.
 template <typename T>
 __device__ __forceinline__ void load_keys(const ScoreArgs& s, const KeyList* kl, float* sk, float* sv) {
-  const int d = s.a.g.d, ld = tile_ld(d);
+  const int d4 = s.a.g.d / 4, ld = tile_ld(s.a.g.d);
   const T* k = reinterpret_cast<const T*>(s.a.kv.k);
   const T* v = reinterpret_cast<const T*>(s.a.kv.v);
-  for (int idx = threadIdx.x; idx < kKeys * d; idx += kThreads) {
-    const int r = idx / d, e = idx % d;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int idx = threadIdx.x; idx < kKeys * d4; idx += kThreads) {
+    const int r = idx / d4, e = 4 * (idx % d4);
     const int64_t off = kl->off[r];
-    sk[r * ld + e] = off >= 0 ? to_float<T>(k[off + e]) : 0.f;
-    sv[r * ld + e] = off >= 0 ? to_float<T>(v[off + e]) : 0.f;
+    *reinterpret_cast<float4*>(sk + r * ld + e) = off >= 0 ? load4(k + off + e) : zero;
+    *reinterpret_cast<float4*>(sv + r * ld + e) = off >= 0 ? load4(v + off + e) : zero;
   }
 }
 
 // Rows i0 .. i0 + 63 of head hq of a token-major tensor as fp32; rows past n_q are zero.
 template <typename T>
 __device__ __forceinline__ void load_rows(const ScoreArgs& s, const void* src, int i0, int hq, float* dst) {
-  const int d = s.a.g.d, ld = tile_ld(d);
+  const int d = s.a.g.d, d4 = d / 4, ld = tile_ld(d);
   const T* x = reinterpret_cast<const T*>(src);
-  for (int idx = threadIdx.x; idx < kRows * d; idx += kThreads) {
-    const int r = idx / d, e = idx % d, i = i0 + r;
-    dst[r * ld + e] = i < s.a.n_q ? to_float<T>(x[((size_t)i * s.a.g.Hq + hq) * d + e]) : 0.f;
+#pragma unroll 4
+  for (int idx = threadIdx.x; idx < kRows * d4; idx += kThreads) {
+    const int r = idx / d4, e = 4 * (idx % d4), i = i0 + r;
+    *reinterpret_cast<float4*>(dst + r * ld + e) =
+        i < s.a.n_q ? load4(x + ((size_t)i * s.a.g.Hq + hq) * d + e) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
 }
 
@@ -109,15 +124,17 @@ __device__ __forceinline__ void dot_tile(const float* A, const float* B, int d, 
 }
 
 // acc[r][c] (columns 4 tx + 64 c) += sum_j W[ty + 16 r][j] X[j], j over 64 rows of X.
+// C: groups of 64 columns a row has (1 for d <= 64, else 2).
+template <int C>
 __device__ __forceinline__ void weigh_rows(const float* W, const float* X, int d, int ty, int tx,
-                                           float4 (&acc)[4][kC]) {
+                                           float4 (&acc)[4][C]) {
   const int ld = tile_ld(d);
   for (int j = 0; j < 64; j += 4) {
     float4 w[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) w[r] = *reinterpret_cast<const float4*>(W + (ty + 16 * r) * kLdP + j);
 #pragma unroll
-    for (int c = 0; c < kC; ++c) {
+    for (int c = 0; c < C; ++c) {
       const int col = 4 * tx + 64 * c;
       if (col >= d) continue;
 #pragma unroll
@@ -188,8 +205,8 @@ __device__ __forceinline__ void load_spans(const ScoreArgs& s, int i0, RowSpans*
 // ------------------------------------------------------------------ forward
 size_t fwd_smem(int d) { return (size_t)(3 * kKeys * tile_ld(d) + kRows * kLdP) * 4; }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) score_fwd_simt(const ScoreArgs s) {
+template <typename T, int C>
+__global__ void __launch_bounds__(kThreads, 2) score_fwd_simt(const __grid_constant__ ScoreArgs s) {
   const int d = s.a.g.d, P = s.a.g.P, ld = tile_ld(d);
   const int hq = blockIdx.y, h = hq / s.a.g.G, i0 = blockIdx.x * kRows;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
@@ -213,13 +230,13 @@ __global__ void __launch_bounds__(kThreads) score_fwd_simt(const ScoreArgs s) {
   const float slope = s.slopes ? s.slopes[hq] : 0.f;
 
   float m[4], l[4];
-  float4 o[4][kC];
+  float4 o[4][C];
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     m[r] = -INFINITY;
     l[r] = 0.f;
 #pragma unroll
-    for (int c = 0; c < kC; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < C; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   for (int64_t t = t0; t < t1; ++t) {
     __syncthreads();
@@ -259,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) score_fwd_simt(const ScoreArgs s) {
       l[r] = l[r] * alpha + sum;
       m[r] = m_new;
 #pragma unroll
-      for (int c = 0; c < kC; ++c) {
+      for (int c = 0; c < C; ++c) {
         o[r][c].x *= alpha;
         o[r][c].y *= alpha;
         o[r][c].z *= alpha;
@@ -277,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) score_fwd_simt(const ScoreArgs s) {
     const float lse = l[r] > 0.f ? m[r] + logf(l[r]) : -INFINITY;
     const size_t rh = (size_t)i * s.a.g.Hq + hq;
 #pragma unroll
-    for (int c = 0; c < kC; ++c) {
+    for (int c = 0; c < C; ++c) {
       const int col = 4 * tx + 64 * c;
       if (col >= d) continue;
       const float v[4] = {o[r][c].x * inv, o[r][c].y * inv, o[r][c].z * inv, o[r][c].w * inv};
@@ -300,42 +317,45 @@ __global__ void __launch_bounds__(kThreads) score_fwd_simt(const ScoreArgs s) {
   }
 }
 
-// A block per (row, head): O = sum_z w_z O_z / sum_z w_z with w_z = exp(LSE_z - max LSE).  Its
-// 8 warps take the parts z = w, w + 8, ..., so that the reads of all parts are in flight at
-// once, and are joined in order.
+// A block per (row, head): O = sum_z w_z O_z / sum_z w_z with w_z = exp(LSE_z - max LSE).  The
+// weights are formed first, so that the reads of all parts are in flight at once; 8 warps take
+// the parts z = w, w + 8, ... and are joined in order.
 template <typename T>
-__global__ void __launch_bounds__(256) score_join(const ScoreArgs s) {
-  __shared__ float acc_s[8][kMaxD], den_s[8];
+__global__ void __launch_bounds__(256) score_join(const __grid_constant__ ScoreArgs s) {
+  __shared__ float weight[kMaxParts], acc_s[8][kMaxD], max_s[8];
   const int64_t rh = blockIdx.x, rows = (int64_t)s.a.n_q * s.a.g.Hq;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, Hq = s.a.g.Hq, d = s.a.g.d;
   float m = -INFINITY;
-  for (int z = lane; z < s.n_split; z += 32) m = fmaxf(m, s.part_lse[z * rows + rh]);
+  for (int z = threadIdx.x; z < s.n_split; z += 256) {
+    weight[z] = s.part_lse[z * rows + rh];
+    m = fmaxf(m, weight[z]);
+  }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if (lane == 0) max_s[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m = fmaxf(m, max_s[w]);
   const float shift = m == -INFINITY ? 0.f : m;
-  float acc[kMaxD / 32] = {}, den = 0.f;
-#pragma unroll 4
+  float acc[kMaxD / 32] = {};
+#pragma unroll 8
   for (int z = warp; z < s.n_split; z += 8) {
-    const float lz = s.part_lse[z * rows + rh];
-    const float wz = expf(lz - shift);
-    den += wz;
+    const float lz = weight[z], wz = expf(lz - shift);
     const float* src = s.part_o + (z * rows + rh) * d;
 #pragma unroll
-    for (int c = 0; c < kMaxD / 32; ++c)
-      if (lane + 32 * c < d && lz > -INFINITY) acc[c] += wz * src[lane + 32 * c];  // else nothing was written
+    for (int c = 0; c < kMaxD / 32; ++c) {
+      const float x = lane + 32 * c < d ? src[lane + 32 * c] : 0.f;
+      acc[c] += lz > -INFINITY ? wz * x : 0.f;  // a part without keys has written no O
+    }
   }
 #pragma unroll
   for (int c = 0; c < kMaxD / 32; ++c) acc_s[warp][lane + 32 * c] = acc[c];
-  if (lane == 0) den_s[warp] = den;
   __syncthreads();
   if (threadIdx.x >= d) return;
-  float o = 0.f;
-  den = 0.f;
+  float o = 0.f, den = 0.f;
+  for (int z = 0; z < s.n_split; ++z) den += expf(weight[z] - shift);
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    o += acc_s[w][threadIdx.x];
-    den += den_s[w];
-  }
+  for (int w = 0; w < 8; ++w) o += acc_s[w][threadIdx.x];
   reinterpret_cast<T*>(s.a.o_out)[rh * d + threadIdx.x] = from_float<T>(den > 0.f ? o / den : 0.f);
   if (threadIdx.x == 0) s.a.lse_out[(size_t)(rh % Hq) * s.a.n_q + rh / Hq] = den > 0.f ? m + logf(den) : m;
 }
@@ -394,8 +414,24 @@ __device__ __forceinline__ void load_stats(const ScoreArgs& s, const float* Dbuf
 size_t dq_smem(int d) { return (size_t)(4 * kKeys * tile_ld(d) + kRows * kLdP) * 4; }
 size_t dkdv_smem(int d) { return (size_t)(4 * kKeys * tile_ld(d) + 2 * kRows * kLdP) * 4; }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) score_dq_simt(const ScoreArgs s, const float* __restrict__ Dbuf) {
+// list_keys for the keys that a block writes: an entry out of order may name a page that another
+// block owns and is left out.
+__device__ __forceinline__ void list_owned_keys(const ScoreArgs& s, int h, int64_t v0, int64_t v1, int count,
+                                                KeyList* kl) {
+  list_keys(s, h, v0, v1, 0, s.total, kl);
+  if (threadIdx.x < kKeys && kl->pos[threadIdx.x] >= 0) {
+    const int j = (int)((v0 + threadIdx.x) / s.a.g.P);
+    const int32_t* row = s.a.sel + (size_t)h * s.a.max_sel;
+    if ((j > 0 && row[j - 1] >= row[j]) || (j + 1 < count && row[j + 1] <= row[j]))
+      kl->pos[threadIdx.x] = kl->off[threadIdx.x] = -1;
+  }
+}
+
+// n_split > 1: dQ (unscaled) of the block's share of the keys goes to part[share], [n_q Hq, d].
+template <typename T, int C>
+__global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
+    score_dq_simt(const __grid_constant__ ScoreArgs s, const float* __restrict__ Dbuf, float* __restrict__ part,
+                  int n_split) {
   const int d = s.a.g.d, P = s.a.g.P, ld = tile_ld(d);
   const int hq = blockIdx.y, h = hq / s.a.g.G, i0 = blockIdx.x * kRows;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
@@ -416,15 +452,17 @@ __global__ void __launch_bounds__(kThreads) score_dq_simt(const ScoreArgs s, con
   load_stats(s, Dbuf, i0, hq, slse, sD);
   const int j0 = first_entry(s.a, h, count, rs.lo / P);
   const int j1 = rs.hi > rs.lo ? first_entry(s.a, h, count, (rs.hi + P - 1) / P) : j0;
+  const int64_t n_tiles = ((int64_t)(j1 - j0) * P + kKeys - 1) / kKeys;
+  const int64_t t0 = n_tiles * blockIdx.z / n_split, t1 = n_tiles * (blockIdx.z + 1) / n_split;
   const float slope = s.slopes ? s.slopes[hq] : 0.f;
-  float4 dq[4][kC];
+  float4 dq[4][C];
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int c = 0; c < kC; ++c) dq[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int64_t v = (int64_t)j0 * P; v < (int64_t)j1 * P; v += kKeys) {
+    for (int c = 0; c < C; ++c) dq[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int64_t t = t0; t < t1; ++t) {
     __syncthreads();
-    list_keys(s, h, v, (int64_t)j1 * P, rs.lo, rs.hi, &kl);
+    list_keys(s, h, (int64_t)j0 * P + t * kKeys, (int64_t)j1 * P, rs.lo, rs.hi, &kl);
     __syncthreads();
     load_keys<T>(s, &kl, sk, sv);
     __syncthreads();
@@ -440,10 +478,15 @@ __global__ void __launch_bounds__(kThreads) score_dq_simt(const ScoreArgs s, con
     const int i = i0 + ty + 16 * r;
     if (i >= s.a.n_q) continue;
 #pragma unroll
-    for (int c = 0; c < kC; ++c) {
+    for (int c = 0; c < C; ++c) {
       const int col = 4 * tx + 64 * c;
       if (col >= d) continue;
-      T* dst = reinterpret_cast<T*>(s.a.dq) + ((size_t)i * s.a.g.Hq + hq) * d + col;
+      const size_t at = ((size_t)i * s.a.g.Hq + hq) * d + col;
+      if (n_split > 1) {
+        *reinterpret_cast<float4*>(part + (size_t)blockIdx.z * s.a.n_q * s.a.g.Hq * d + at) = dq[r][c];
+        continue;
+      }
+      T* dst = reinterpret_cast<T*>(s.a.dq) + at;
       dst[0] = from_float<T>(dq[r][c].x * s.a.scale);
       dst[1] = from_float<T>(dq[r][c].y * s.a.scale);
       dst[2] = from_float<T>(dq[r][c].z * s.a.scale);
@@ -452,8 +495,12 @@ __global__ void __launch_bounds__(kThreads) score_dq_simt(const ScoreArgs s, con
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) score_dkdv_simt(const ScoreArgs s, const float* __restrict__ Dbuf) {
+// n_split > 1: dK (unscaled) and dV of the block's share of the (row tile, query head) pairs go
+// to part[share][KV head][key tile], two [64, d] tiles.
+template <typename T, int C>
+__global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
+    score_dkdv_simt(const __grid_constant__ ScoreArgs s, const float* __restrict__ Dbuf, float* __restrict__ part,
+                    int n_split) {
   const int d = s.a.g.d, P = s.a.g.P, G = s.a.g.G, ld = tile_ld(d);
   const int h = blockIdx.y;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
@@ -471,14 +518,7 @@ __global__ void __launch_bounds__(kThreads) score_dkdv_simt(const ScoreArgs s, c
   const int count = sel_count_checked(s.a, h);
   const int64_t v0 = (int64_t)blockIdx.x * kKeys, v1 = (int64_t)count * P;
   if (v0 >= v1) return;
-  list_keys(s, h, v0, v1, 0, s.total, &kl);
-  // an entry out of order may name a page that another block owns: leave it out
-  if (threadIdx.x < kKeys && kl.pos[threadIdx.x] >= 0) {
-    const int j = (int)((v0 + threadIdx.x) / P);
-    const int32_t* row = s.a.sel + (size_t)h * s.a.max_sel;
-    if ((j > 0 && row[j - 1] >= row[j]) || (j + 1 < count && row[j + 1] <= row[j]))
-      kl.pos[threadIdx.x] = kl.off[threadIdx.x] = -1;
-  }
+  list_owned_keys(s, h, v0, v1, count, &kl);
   __syncthreads();
   if (threadIdx.x == 0) {
     int64_t lo = INT64_MAX, hi = -1;
@@ -492,17 +532,20 @@ __global__ void __launch_bounds__(kThreads) score_dkdv_simt(const ScoreArgs s, c
   }
   load_keys<T>(s, &kl, sk, sv);
   __syncthreads();
-  if (key_hi < 0) return;
-  float4 dk[4][kC], dv[4][kC];
+  if (key_hi < 0) return;  // (the join skips these keys too)
+  float4 dk[4][C], dv[4][C];
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int c = 0; c < kC; ++c) dk[r][c] = dv[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < s.a.n_q; i0 += kRows) {
+    for (int c = 0; c < C; ++c) dk[r][c] = dv[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int n_items = (s.a.n_q + kRows - 1) / kRows * G;  // (row tile, query head)
+  const int u0 = (int)((int64_t)n_items * blockIdx.z / n_split), u1 = (int)((int64_t)n_items * (blockIdx.z + 1) / n_split);
+  for (int tile = u0 / G; tile * G < u1; ++tile) {
+    const int i0 = tile * kRows;
     __syncthreads();
     load_spans(s, i0, &rs);
     if (rs.hi <= key_lo || rs.lo > key_hi) continue;  // no row of the tile sees these keys
-    for (int gq = 0; gq < G; ++gq) {
+    for (int gq = max(0, u0 - tile * G); gq < min(G, u1 - tile * G); ++gq) {
       const int hq = h * G + gq;
       __syncthreads();
       load_rows<T>(s, s.a.q, i0, hq, sq);
@@ -521,12 +564,23 @@ __global__ void __launch_bounds__(kThreads) score_dkdv_simt(const ScoreArgs s, c
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int key = ty + 16 * r;
+    if (n_split > 1) {
+      float* dst = part + (((size_t)blockIdx.z * gridDim.y + h) * gridDim.x + blockIdx.x) * 2 * kKeys * d;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int col = 4 * tx + 64 * c;
+        if (col >= d) continue;
+        *reinterpret_cast<float4*>(dst + key * d + col) = dk[r][c];
+        *reinterpret_cast<float4*>(dst + (kKeys + key) * d + col) = dv[r][c];
+      }
+      continue;
+    }
     if (kl.pos[key] < 0) continue;
     const int j = (int)((v0 + key) / P), t = (int)((v0 + key) % P);
     const int phys = s.a.kv.table[s.a.sel[(size_t)h * s.a.max_sel + j]];  // checked by list_keys
     const size_t base = (grad_block(s.a, h, j, phys) * P + t) * d;
 #pragma unroll
-    for (int c = 0; c < kC; ++c) {
+    for (int c = 0; c < C; ++c) {
       const int col = 4 * tx + 64 * c;
       if (col >= d) continue;
       float4* gk = reinterpret_cast<float4*>(s.a.dk_pool + base + col);
@@ -543,6 +597,70 @@ __global__ void __launch_bounds__(kThreads) score_dkdv_simt(const ScoreArgs s, c
       *gk = a;
       *gv = b;
     }
+  }
+}
+
+// dq = scale * sum of the shares, in order.
+template <typename T>
+__global__ void __launch_bounds__(256) score_dq_join(const __grid_constant__ ScoreArgs s, const float* __restrict__ part,
+                                                     int n_split) {
+  const int64_t total = (int64_t)s.a.n_q * s.a.g.Hq * s.a.g.d;
+  const int64_t at = 4 * ((int64_t)blockIdx.x * blockDim.x + threadIdx.x);
+  if (at >= total) return;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int z = 0; z < n_split; ++z) {
+    const float4 x = *reinterpret_cast<const float4*>(part + z * total + at);
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
+  }
+  T* dst = reinterpret_cast<T*>(s.a.dq) + at;
+  dst[0] = from_float<T>(acc.x * s.a.scale);
+  dst[1] = from_float<T>(acc.y * s.a.scale);
+  dst[2] = from_float<T>(acc.z * s.a.scale);
+  dst[3] = from_float<T>(acc.w * s.a.scale);
+}
+
+// dK += scale * sum of the shares, dV += sum of the shares, for the 64 keys of a block.
+__global__ void __launch_bounds__(256) score_dkdv_join(const __grid_constant__ ScoreArgs s,
+                                                       const float* __restrict__ part, int n_split) {
+  const int d = s.a.g.d, d4 = d / 4, P = s.a.g.P, h = blockIdx.y;
+  __shared__ KeyList kl;
+  const int count = sel_count_checked(s.a, h);
+  const int64_t v0 = (int64_t)blockIdx.x * kKeys, v1 = (int64_t)count * P;
+  if (v0 >= v1) return;
+  list_owned_keys(s, h, v0, v1, count, &kl);
+  __syncthreads();
+  bool any = false;  // a tile without keys has written no shares
+  for (int r = 0; r < kKeys; ++r) any |= kl.pos[r] >= 0;
+  if (!any) return;
+  const size_t tile = 2 * (size_t)kKeys * d, step = (size_t)gridDim.y * gridDim.x * tile;
+  const float* src = part + ((size_t)h * gridDim.x + blockIdx.x) * tile;
+  for (int idx = threadIdx.x; idx < 2 * kKeys * d4; idx += blockDim.x) {
+    const int r = idx / d4, key = r % kKeys, col = 4 * (idx % d4);
+    if (kl.pos[key] < 0) continue;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int z = 0; z < n_split; ++z) {
+      const float4 x = *reinterpret_cast<const float4*>(src + z * step + (size_t)r * d + col);
+      acc.x += x.x;
+      acc.y += x.y;
+      acc.z += x.z;
+      acc.w += x.w;
+    }
+    const int j = (int)((v0 + key) / P), t = (int)((v0 + key) % P);
+    const int phys = s.a.kv.table[s.a.sel[(size_t)h * s.a.max_sel + j]];  // checked by list_owned_keys
+    const size_t at = (grad_block(s.a, h, j, phys) * P + t) * d + col;
+    const float f = r < kKeys ? s.a.scale : 1.f;
+    float4* g = reinterpret_cast<float4*>((r < kKeys ? s.a.dk_pool : s.a.dv_pool) + at);
+    float4 y = *g;
+    y.x += f * acc.x;
+    y.y += f * acc.y;
+    y.z += f * acc.z;
+    y.w += f * acc.w;
+    *g = y;
   }
 }
 
@@ -585,35 +703,69 @@ int parts_limit(const Geometry& g, int n_q) {
   return tc_supported(g) ? score_tc_parts_limit(g, n_q) : simt_split_limit(g, n_q);
 }
 
-template <typename T>
+template <typename T, int C>
 cudaError_t fwd_simt(ScoreArgs& s, cudaStream_t st) {
   static size_t smem_set[kMaxDevices] = {};
-  cudaError_t e = set_smem_limit((const void*)score_fwd_simt<T>, fwd_smem(kMaxD), smem_set);
+  cudaError_t e = set_smem_limit((const void*)score_fwd_simt<T, C>, fwd_smem(64 * C), smem_set);
   if (e != cudaSuccess) return e;
   const int64_t key_tiles = ((int64_t)s.a.max_sel * s.a.g.P + kKeys - 1) / kKeys;
   s.n_split = (int)std::min<int64_t>(simt_split_limit(s.a.g, s.a.n_q), std::max<int64_t>(1, key_tiles / 2));
   dim3 grid((s.a.n_q + kRows - 1) / kRows, s.a.g.Hq, s.n_split);
-  score_fwd_simt<T><<<grid, kThreads, fwd_smem(s.a.g.d), st>>>(s);
+  score_fwd_simt<T, C><<<grid, kThreads, fwd_smem(s.a.g.d), st>>>(s);
   count_launches(1);
   return cudaGetLastError();
 }
 
-template <typename T>
+// Backward: shares of a tile, so that the tiles fill the SMs (two blocks fit one for d <= 64).
+struct BwdSplit {
+  int dq, dkdv;
+  size_t dq_bytes, dkdv_bytes;  // of the shares' sums
+};
+int64_t simt_slots(const Geometry& g) { return (int64_t)device_sm_count() * (g.d <= 64 ? 2 : 1); }
+size_t dkdv_tile_bytes(const Geometry& g) { return (size_t)2 * kKeys * g.d * 4; }
+BwdSplit simt_bwd_split(const Geometry& g, int n_q, int max_sel) {
+  BwdSplit b;
+  const int64_t slots = simt_slots(g), row_tiles = (n_q + kRows - 1) / kRows;
+  const int64_t key_tiles = ((int64_t)max_sel * g.P + kKeys - 1) / kKeys;
+  b.dq = (int)std::min<int64_t>(std::max<int64_t>(1, slots / (row_tiles * g.Hq)), std::max<int64_t>(1, key_tiles / 2));
+  b.dkdv = (int)std::min<int64_t>(std::max<int64_t>(1, slots / (key_tiles * g.Hkv)), row_tiles * g.G);
+  b.dq_bytes = b.dq > 1 ? align_up((size_t)b.dq * n_q * g.Hq * g.d * 4, 256) : 0;
+  b.dkdv_bytes = b.dkdv > 1 ? (size_t)b.dkdv * key_tiles * g.Hkv * dkdv_tile_bytes(g) : 0;
+  return b;
+}
+
+template <typename T, int C>
 cudaError_t bwd_simt(const ScoreArgs& s, cudaStream_t st) {
   static size_t set_dq[kMaxDevices] = {}, set_dkdv[kMaxDevices] = {};
-  cudaError_t e = set_smem_limit((const void*)score_dq_simt<T>, dq_smem(kMaxD), set_dq);
-  if (e == cudaSuccess) e = set_smem_limit((const void*)score_dkdv_simt<T>, dkdv_smem(kMaxD), set_dkdv);
+  cudaError_t e = set_smem_limit((const void*)score_dq_simt<T, C>, dq_smem(64 * C), set_dq);
+  if (e == cudaSuccess) e = set_smem_limit((const void*)score_dkdv_simt<T, C>, dkdv_smem(64 * C), set_dkdv);
   if (e != cudaSuccess) return e;
-  const int d = s.a.g.d;
-  float* Dbuf = reinterpret_cast<float*>(s.a.ws);
-  const int64_t warps = (int64_t)s.a.n_q * s.a.g.Hq;
+  const Geometry& g = s.a.g;
+  const int d = g.d;
+  const BwdSplit b = simt_bwd_split(g, s.a.n_q, s.a.max_sel);
+  char* ws = reinterpret_cast<char*>(s.a.ws);
+  float* Dbuf = reinterpret_cast<float*>(ws);
+  float* part_dq = reinterpret_cast<float*>(ws + align_up((size_t)g.Hq * s.a.n_q * 4, 256));
+  float* part_kv = reinterpret_cast<float*>(reinterpret_cast<char*>(part_dq) + b.dq_bytes);
+  const int64_t warps = (int64_t)s.a.n_q * g.Hq;
   score_dot<T><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(s, Dbuf);
-  dim3 gq((s.a.n_q + kRows - 1) / kRows, s.a.g.Hq);
-  score_dq_simt<T><<<gq, kThreads, dq_smem(d), st>>>(s, Dbuf);
-  dim3 gk((unsigned)(((int64_t)s.a.max_sel * s.a.g.P + kKeys - 1) / kKeys), s.a.g.Hkv);
-  score_dkdv_simt<T><<<gk, kThreads, dkdv_smem(d), st>>>(s, Dbuf);
-  count_launches(3);
+  dim3 gq((s.a.n_q + kRows - 1) / kRows, g.Hq, b.dq);
+  score_dq_simt<T, C><<<gq, kThreads, dq_smem(d), st>>>(s, Dbuf, part_dq, b.dq);
+  if (b.dq > 1) score_dq_join<T><<<(unsigned)((warps * d / 4 + 255) / 256), 256, 0, st>>>(s, part_dq, b.dq);
+  dim3 gk((unsigned)(((int64_t)s.a.max_sel * g.P + kKeys - 1) / kKeys), g.Hkv, b.dkdv);
+  score_dkdv_simt<T, C><<<gk, kThreads, dkdv_smem(d), st>>>(s, Dbuf, part_kv, b.dkdv);
+  if (b.dkdv > 1) score_dkdv_join<<<dim3(gk.x, gk.y), 256, 0, st>>>(s, part_kv, b.dkdv);
+  count_launches(3 + (b.dq > 1) + (b.dkdv > 1));
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t fwd_width(ScoreArgs& s, cudaStream_t st) {
+  return s.a.g.d <= 64 ? fwd_simt<T, 1>(s, st) : fwd_simt<T, 2>(s, st);
+}
+template <typename T>
+cudaError_t bwd_width(const ScoreArgs& s, cudaStream_t st) {
+  return s.a.g.d <= 64 ? bwd_simt<T, 1>(s, st) : bwd_simt<T, 2>(s, st);
 }
 
 }  // namespace
@@ -626,7 +778,10 @@ size_t score_fwd_workspace_bytes(const Geometry& g, int n_q) {
 }
 
 size_t score_bwd_workspace_bytes(const Geometry& g, int n_q) {
-  return tc_supported(g) ? score_bwd_tc_workspace_bytes(g, n_q) : align_up((size_t)g.Hq * n_q * 4, 256);
+  if (tc_supported(g)) return score_bwd_tc_workspace_bytes(g, n_q);
+  // D, and the most that the shares of dQ (any number of keys) and of dK/dV can take
+  const BwdSplit b = simt_bwd_split(g, n_q, INT_MAX / (2 * g.P));
+  return align_up((size_t)g.Hq * n_q * 4, 256) + b.dq_bytes + (size_t)simt_slots(g) * dkdv_tile_bytes(g);
 }
 
 cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st) {
@@ -636,8 +791,8 @@ cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st) {
                                         align_up((size_t)s.a.n_q * s.a.g.Hq * limit * s.a.g.d * 4, 256));
   const bool f32 = s.a.g.dtype == OOMB_FP32;
   cudaError_t e = tc_supported(s.a.g) ? launch_score_fwd_tc(s, st)
-                  : f32               ? fwd_simt<float>(s, st)
-                                      : fwd_simt<__nv_bfloat16>(s, st);
+                  : f32               ? fwd_width<float>(s, st)
+                                      : fwd_width<__nv_bfloat16>(s, st);
   if (e != cudaSuccess || s.n_split <= 1) return e;
   const unsigned blocks = (unsigned)(s.a.n_q * s.a.g.Hq);
   if (f32)
@@ -650,7 +805,7 @@ cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st) {
 
 cudaError_t launch_score_bwd(const ScoreArgs& s, cudaStream_t st) {
   if (tc_supported(s.a.g)) return launch_score_bwd_tc(s, st);
-  return s.a.g.dtype == OOMB_FP32 ? bwd_simt<float>(s, st) : bwd_simt<__nv_bfloat16>(s, st);
+  return s.a.g.dtype == OOMB_FP32 ? bwd_width<float>(s, st) : bwd_width<__nv_bfloat16>(s, st);
 }
 
 cudaError_t launch_doc_spans(const int64_t* doc_start, const int64_t* prefix_len, int n_docs, int64_t q_start, int n_q,

@@ -100,6 +100,17 @@ __device__ __forceinline__ uint32_t stage_off(int j, int c) {
   return (uint32_t)j * kStageRow + (uint32_t)((c ^ (j & 7)) * 16);
 }
 
+// Transpose of the 32 x 32 bit matrix whose row `lane` is x.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
+  uint32_t m = 0x0000ffffu;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1, m ^= m << s) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, s);
+    x = lane & s ? (x & ~m) | ((y & ~m) >> s) : (x & m) | ((y & m) << s);
+  }
+  return x;
+}
+
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
     score_bwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
@@ -333,12 +344,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q0 = t * kTile + hh * kHalf + 32 * hc;  // query row of this thread's column 0
         uint32_t see = 0xffffffffu;                       // columns whose row sees this key
         if (masked) {
-          see = 0u;
-#pragma unroll 4
-          for (int i = 0; i < 32; ++i) {
-            const longlong2 w = p.span[q0 + i];
-            see |= (kpos >= w.x && kpos < w.y ? 1u : 0u) << i;
-          }
+          // lane i: the warp's 32 keys that row q0 + i sees, as bits; transposed, lane k has the
+          // rows that see its key
+          const longlong2 w = p.span[q0 + lane];
+          const int64_t k0 = kpos - lane;
+          const int b = (int)max((int64_t)0, min((int64_t)(w.x - k0), (int64_t)32));
+          const int e = (int)max((int64_t)0, min((int64_t)(w.y - k0), (int64_t)32));
+          see = transpose_bits(b >= e ? 0u : (0xffffffffu >> (32 - (e - b))) << b, lane);
         }
         const float f0 = BIAS ? (float)(a.q_start + q0 - kpos) : 0.f;  // distance of column i: |f0 + i|
         uint32_t pk[16], dk[16];

@@ -716,9 +716,9 @@ bool score_tc_packs(const Geometry& g, int n_q) { return (int64_t)n_q * g.G <= k
 // Parts the keys of a tile may be cut into.
 int score_tc_parts_limit(const Geometry& g, int n_q) {
   const int sms = device_sm_count();
-  if (score_tc_packs(g, n_q)) return 2 * std::max(1, sms / g.Hkv);
+  if (score_tc_packs(g, n_q)) return 2 * std::max(1, std::min(sms, 512) / g.Hkv);
   const int64_t units = (int64_t)((n_q + 2 * kTile - 1) / (2 * kTile)) * g.Hq;
-  return (int)std::max<int64_t>(1, 4 * (int64_t)sms / units);
+  return (int)std::min<int64_t>(1024, std::max<int64_t>(1, 4 * (int64_t)sms / units));
 }
 
 cudaError_t launch_score_fwd_tc(ScoreArgs& s, cudaStream_t st) {
