@@ -355,9 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f0 = BIAS ? (float)(a.q_start + q0 - kpos) : 0.f;  // distance of column i: |f0 + i|
         uint32_t pk[16], dk[16];
         // P and dA of the columns, four at a time
-        auto columns = [&](auto form, auto ranged) {
+        auto columns = [&](auto form) {
           constexpr TanhForm F = decltype(form)::value;
-          constexpr bool RANGED = decltype(ranged)::value;
 #pragma unroll
           for (int c4 = 0; c4 < 8; ++c4) {
             const float4 L = vs4[c4], Dv = vs4[16 + c4];
@@ -371,12 +370,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (BIAS) shift = fmaf(-slope2, fabsf(f0 + (float)i), shift);
               float th = 0.f;
               if constexpr (CAP) th = tanh_of<F>(S, p.cap);
-              float pv = ex2_approx(CAP ? fmaf(th, p.cap.cap2, shift) : fmaf(S, p.scale_log2, shift));
-              float da = pv * (__uint_as_float(dr[i]) - d4[e]);
-              if constexpr (CAP) da *= fmaf(-th, th, 1.f);
-              if (RANGED && !((see >> i) & 1u)) pv = da = 0.f;
-              pr[e] = pv;
-              dar[e] = da;
+              pr[e] = ex2_approx(CAP ? fmaf(th, p.cap.cap2, shift) : fmaf(S, p.scale_log2, shift));
+              dar[e] = pr[e] * (__uint_as_float(dr[i]) - d4[e]);
+              if constexpr (CAP) dar[e] *= fmaf(-th, th, 1.f);
             }
             pk[2 * c4] = pack_bf16x2(pr[0], pr[1]);
             pk[2 * c4 + 1] = pack_bf16x2(pr[2], pr[3]);
@@ -384,17 +380,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             dk[2 * c4 + 1] = pack_bf16x2(dar[2], dar[3]);
           }
         };
-        TanhForm form = kWide;
+        bool small = true;
         if constexpr (CAP) {
           float amax = 0.f;
 #pragma unroll
           for (int i = 0; i < 32; i += 2) amax = fmax3_abs(amax, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
-          form = __all_sync(0xffffffffu, amax <= p.cap.edge2) ? kDegree2 : kWide;
+          small = __all_sync(0xffffffffu, amax <= p.cap.edge3);
         }
-        if (CAP && form == kDegree2) {
-          if (masked) columns(Const<kDegree2>{}, std::true_type{}); else columns(Const<kDegree2>{}, std::false_type{});
-        } else {
-          if (masked) columns(Const<kWide>{}, std::true_type{}); else columns(Const<kWide>{}, std::false_type{});
+        if (!CAP || small)
+          columns(Const<kDegree3>{});
+        else
+          columns(Const<kWide>{});
+        if (masked) {  // cleared afterwards, in the packed words, whatever came out for a pair that is not seen
+#pragma unroll
+          for (int w = 0; w < 16; ++w) {
+            const uint32_t keep = ((see >> (2 * w)) & 1u) * 0x0000ffffu | ((see >> (2 * w + 1)) & 1u) * 0xffff0000u;
+            pk[w] &= keep;
+            dk[w] &= keep;
+          }
         }
         // P^T and dA^T go over this thread's own (already loaded) S^T columns
         tmem_st16(base, pk);

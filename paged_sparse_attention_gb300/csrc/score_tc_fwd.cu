@@ -485,9 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 64; ++c)
               sr[c] = __float_as_uint(p.cap.cap2 * tanh_of<decltype(f)::value>(__uint_as_float(sr[c]), p.cap));
           };
-          if (form == kDegree2)
-            cap_all(Const<kDegree2>{});
-          else if (form == kDegree3)
+          if (form != kWide)
             cap_all(Const<kDegree3>{});
           else
             cap_all(Const<kWide>{});
