@@ -24,6 +24,7 @@ struct ScoreArgs {
   int n_split;            // forward: thread blocks sharing one tile's keys
   float* part_o;          // n_split > 1: [n_split, n_q * Hq, d] partial outputs (normalised)
   float* part_lse;        // n_split > 1: [n_split, n_q * Hq]
+  int32_t* order;         // room for the order of the forward's query tiles
 };
 
 // Keys [b, e) that query row i may see; e >= b, both within [0, total].

@@ -770,11 +770,19 @@ cudaError_t bwd_width(const ScoreArgs& s, cudaStream_t st) {
 
 }  // namespace
 
-size_t score_fwd_workspace_bytes(const Geometry& g, int n_q) {
+// Forward workspace: the parts' outputs, their log-sum-exps, and the order of the query tiles.
+struct FwdSpace {
+  size_t o, lse, order;
+};
+static FwdSpace fwd_space(const Geometry& g, int n_q) {
   const int n = parts_limit(g, n_q);
-  if (n <= 1) return 0;
-  const size_t rows = (size_t)n_q * g.Hq * n;
-  return align_up(rows * g.d * 4, 256) + align_up(rows * 4, 256);
+  const size_t rows = n > 1 ? (size_t)n_q * g.Hq * n : 0;
+  return {align_up(rows * g.d * 4, 256), align_up(rows * 4, 256),
+          tc_supported(g) ? align_up((size_t)n_q / 64 * 4 + 4, 256) : 0};
+}
+size_t score_fwd_workspace_bytes(const Geometry& g, int n_q) {
+  const FwdSpace f = fwd_space(g, n_q);
+  return f.o + f.lse + f.order;
 }
 
 size_t score_bwd_workspace_bytes(const Geometry& g, int n_q) {
@@ -785,10 +793,11 @@ size_t score_bwd_workspace_bytes(const Geometry& g, int n_q) {
 }
 
 cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st) {
-  const int limit = parts_limit(s.a.g, s.a.n_q);
-  s.part_o = reinterpret_cast<float*>(s.a.ws);
-  s.part_lse = reinterpret_cast<float*>(reinterpret_cast<char*>(s.a.ws) +
-                                        align_up((size_t)s.a.n_q * s.a.g.Hq * limit * s.a.g.d * 4, 256));
+  const FwdSpace f = fwd_space(s.a.g, s.a.n_q);
+  char* ws = reinterpret_cast<char*>(s.a.ws);
+  s.part_o = reinterpret_cast<float*>(ws);
+  s.part_lse = reinterpret_cast<float*>(ws + f.o);
+  s.order = reinterpret_cast<int32_t*>(ws + f.o + f.lse);
   const bool f32 = s.a.g.dtype == OOMB_FP32;
   cudaError_t e = tc_supported(s.a.g) ? launch_score_fwd_tc(s, st)
                   : f32               ? fwd_width<float>(s, st)

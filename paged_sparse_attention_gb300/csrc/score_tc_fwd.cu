@@ -2,7 +2,8 @@
 //
 // Two layouts of a thread block's two 128-row tiles A and B:
 //  rows   tiles A and B are neighbouring 128-row tiles of one query head.  Both read the same
-//         pages, each K and V tile loaded once.  Heaviest (last) pairs first.
+//         pages, each K and V tile loaded once.  Heaviest pairs first: the last ones of a causal
+//         chunk; where the rows have ranges, in the order that score_fwd_plan finds.
 //  packed where all rows of the G heads of a group fit one tile (n_q G <= 128: single tokens
 //         and short tails): row r is token r / G, head r % G, so K and V are read once for
 //         the whole group, and A and B hold the same rows and take alternate pages.
@@ -48,6 +49,7 @@ struct ScoreFwdParams {
   CapConst cap;
   float scale_log2;
   int n_tiles, n_pairs;
+  const int32_t* order;  // rows: pair of tiles of each grid row, or nullptr (last pair first)
 };
 
 struct __align__(8) FwdBarriers {
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int G = a.g.G, Hq = a.g.Hq;
   const int h = PACK ? (int)blockIdx.x : (int)blockIdx.x / G;
-  const int pair = p.n_pairs - 1 - (int)blockIdx.y;
+  const int pair = p.order ? p.order[blockIdx.y] : p.n_pairs - 1 - (int)blockIdx.y;
   // With a bias the pages are walked from the nearest to the farthest: the row maximum then
   // comes first and O is hardly ever rescaled (upwards, a head whose bias changes by more than
   // 2^8 over a page would rescale at every page).  The tile that ends the walk last has to be
@@ -251,6 +253,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
+  if (threadIdx.x == 0) {  // Q needs none of what follows
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+    if (PACK) {
+      const uint32_t bytes = (uint32_t)(a.n_q * G) * 128u;
+      mbar_arrive_expect_tx(&bar->q_full, 2 * bytes);
+      tma_load_3d(sm + kOffQ, &tq, &bar->q_full, 0, h * G, 0);
+      tma_load_3d(sm + kOffQ + kHalfBytes, &tq, &bar->q_full, 64, h * G, 0);
+    } else {
+      // a tile past the last one has no pages and is not loaded
+      mbar_arrive_expect_tx(&bar->q_full, (2 * pair + 1 < p.n_tiles ? 2u : 1u) * kTileBytes);
+      for (int i = 0; i < 2; ++i) {
+        if (tile[i] >= p.n_tiles) continue;
+        uint8_t* dst = sm + kOffQ + i * kTileBytes;
+        tma_load_3d(dst, &tq, &bar->q_full, 0, (int)blockIdx.x, tile[i] * kTile);
+        tma_load_3d(dst + kHalfBytes, &tq, &bar->q_full, 64, (int)blockIdx.x, tile[i] * kTile);
+      }
+    }
+  }
   {
     // entries below the first page a tile sees and below the end of the last one, counted by
     // all threads (the selection ascends); the selection is checked in the same pass
@@ -288,25 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0 && t.n_ring > 0) {
-      tma_prefetch_desc(&tq);
-      tma_prefetch_desc(&tk);
-      tma_prefetch_desc(&tv);
-      if (PACK) {
-        const uint32_t bytes = (uint32_t)(a.n_q * G) * 128u;
-        mbar_arrive_expect_tx(&bar->q_full, 2 * bytes);
-        tma_load_3d(sm + kOffQ, &tq, &bar->q_full, 0, h * G, 0);
-        tma_load_3d(sm + kOffQ + kHalfBytes, &tq, &bar->q_full, 64, h * G, 0);
-      } else {
-        // a tile past the last one has no pages and is not loaded
-        mbar_arrive_expect_tx(&bar->q_full, (2 * pair + 1 < p.n_tiles ? 2u : 1u) * kTileBytes);
-        for (int i = 0; i < 2; ++i) {
-          if (tile[i] >= p.n_tiles) continue;
-          uint8_t* dst = sm + kOffQ + i * kTileBytes;
-          tma_load_3d(dst, &tq, &bar->q_full, 0, (int)blockIdx.x, tile[i] * kTile);
-          tma_load_3d(dst + kHalfBytes, &tq, &bar->q_full, 64, (int)blockIdx.x, tile[i] * kTile);
-        }
-      }
+    if (lane == 0) {
       auto row_of = [&](int e) -> int {  // first row of ring entry e's block in the K/V maps
         const int j = entry(PACK ? t.first[e & 1] + (e >> 1) : t.lo + e);
         const int64_t blk = score_block(p.s, h, j, a.sel[(size_t)h * a.max_sel + j]);
@@ -676,6 +679,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Pairs of tiles by the pages that their rows' ranges span, most first (ties: the later pair).
+// One block; the pairs are few.
+constexpr int kMaxPlan = 256;
+__global__ void __launch_bounds__(1024) score_fwd_plan(const __grid_constant__ ScoreArgs s, int n_pairs,
+                                                       int32_t* __restrict__ order) {
+  __shared__ unsigned long long lo[kMaxPlan], hi[kMaxPlan];
+  __shared__ int pages[kMaxPlan];
+  const int lane = threadIdx.x % 32;
+  for (int i = threadIdx.x; i < n_pairs; i += 1024) {
+    lo[i] = ~0ull;
+    hi[i] = 0;
+  }
+  __syncthreads();
+  for (int i0 = (int)threadIdx.x - lane; i0 < s.a.n_q; i0 += 1024) {  // 32 rows of one pair a warp
+    int64_t b = 0, e = 0;
+    if (i0 + lane < s.a.n_q) row_span(s, i0 + lane, b, e);
+    if (e <= b) b = INT64_MAX;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      b = min(b, __shfl_xor_sync(0xffffffffu, b, o));
+      e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+    }
+    if (lane == 0 && e > 0) {
+      atomicMin(&lo[i0 / (2 * kTile)], (unsigned long long)b);
+      atomicMax(&hi[i0 / (2 * kTile)], (unsigned long long)e);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n_pairs; i += 1024)
+    pages[i] = hi[i] ? (int)((hi[i] + kTile - 1) / kTile - lo[i] / kTile) : 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n_pairs; i += 1024) {
+    int rank = 0;
+    for (int k = 0; k < n_pairs; ++k) rank += pages[k] > pages[i] || (pages[k] == pages[i] && k > i);
+    order[rank] = i;
+  }
+}
+
 // 3-D map over a token-major [n, H, 128] bf16 tensor: box = every token, G heads, 64 columns.
 bool make_tmap_group(CUtensorMap* m, const void* base, int n, int H, int G) {
   auto enc = tmap_encoder();
@@ -750,7 +791,16 @@ cudaError_t launch_score_fwd_tc(ScoreArgs& s, cudaStream_t st) {
   p.s = s;
   p.cap = make_cap(s.cap, s.a.scale);
   p.scale_log2 = s.a.scale * kLog2e;
+  p.order = nullptr;
   cudaError_t e;
+  // With ranges the pairs' work is not known here; worth a launch where the blocks queue for SMs.
+  if (!pack && (s.begin || s.end) && p.n_pairs <= kMaxPlan && (int64_t)p.n_pairs * g.Hq * s.n_split > sms) {
+    score_fwd_plan<<<1, 1024, 0, st>>>(s, p.n_pairs, s.order);
+    count_launches(1);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    p.order = s.order;
+  }
   if (s.cap > 0.f)
     e = s.slopes ? launch_pack<true, true>(pack, p, tq, tk, tv, st) : launch_pack<true, false>(pack, p, tq, tk, tv, st);
   else

@@ -169,6 +169,12 @@ def test_ranges_meet_selections(sel, mask):
     Case(mask=mask, sel=sel, seed=5, total=1400, n_q=390, q_start=700, Hq=4, Hkv=2, **TC).run()
 
 
+@pytest.mark.parametrize("mask", ["docs", "random", "empty"])
+def test_more_tiles_than_fit_the_gpu_at_once(mask):
+    """Ranges and enough query tiles for several waves of thread blocks."""
+    Case(mask=mask, sel="all", bias=True, cap=15.0, total=1400, n_q=1100, Hq=32, Hkv=4, **TC).run()
+
+
 @pytest.mark.parametrize("spread", [0.01, 30.0])
 @pytest.mark.parametrize("shape", ["tc_g2_ragged", "fp32_64"])
 def test_cap_small_and_saturated(shape, spread):
