@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(256) score_join(const __grid_constant__ ScoreA
   __shared__ float weight[kMaxParts], acc_s[8][kMaxD], max_s[8];
   const int64_t rh = blockIdx.x, rows = (int64_t)s.a.n_q * s.a.g.Hq;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, Hq = s.a.g.Hq, d = s.a.g.d;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead: the parts are written from here on
   float m = -INFINITY;
   for (int z = threadIdx.x; z < s.n_split; z += 256) {
     weight[z] = s.part_lse[z * rows + rh];
@@ -803,13 +804,19 @@ cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st) {
                   : f32               ? fwd_width<float>(s, st)
                                       : fwd_width<__nv_bfloat16>(s, st);
   if (e != cudaSuccess || s.n_split <= 1) return e;
-  const unsigned blocks = (unsigned)(s.a.n_q * s.a.g.Hq);
-  if (f32)
-    score_join<float><<<blocks, 256, 0, st>>>(s);
-  else
-    score_join<__nv_bfloat16><<<blocks, 256, 0, st>>>(s);
+  // a dependent launch: its set-up overlaps the end of the forward, whose parts it waits for
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(s.a.n_q * s.a.g.Hq));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = f32 ? cudaLaunchKernelEx(&cfg, score_join<float>, s) : cudaLaunchKernelEx(&cfg, score_join<__nv_bfloat16>, s);
   count_launches(1);
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_score_bwd(const ScoreArgs& s, cudaStream_t st) {

@@ -13,7 +13,7 @@
 // are two parts).  A block is bound by the exponential unit with many rows (as the plain
 // forward) and by HBM in the packed layout.
 //
-// Warp roles (576 threads): warp 0 TMA producer (K ring of 3, V ring of 2 tiles), warp 1 MMA
+// Warp roles (576 threads): warp 0 TMA producer (K ring of 3, V ring of 2 or 3 tiles), warp 1 MMA
 // issuer and TMEM owner, warps 2-9 softmax of tile A, 10-17 of tile B.  A query row belongs to
 // two threads, 64 scores each: with one thread a row the score arithmetic of one tile takes
 // longer than the products of the other, and two warps of a scheduler can share the units
@@ -33,7 +33,7 @@ namespace {
 using namespace tc;
 
 constexpr int kKStages = 3;
-constexpr int kVStages = 2;
+constexpr int kVStages = 3;  // two used by the rows layout; the packed one has the third where tile B's Q would be
 constexpr int kThreads = 576;
 constexpr int kTileWarps = 8;  // softmax warps of a tile
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled when the row maximum grows by more
@@ -63,6 +63,7 @@ struct __align__(8) FwdBarriers {
   uint64_t o_done[2];
   uint64_t mma_done;
   float half[2][2][kTile];  // per tile, column half and row: maximum of the scores, at the end the sum of P
+  int kv_row[64];           // first row in the K/V maps of ring entry e, at e % 64
   int64_t lo[8], hi[8];     // key range seen by each 32 rows of the tiles
   int below[4];          // selected pages below: tile A's first, A's end, B's first, B's end
   uint32_t tmem_base;
@@ -73,9 +74,14 @@ struct __align__(8) FwdBarriers {
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = 2 * kTileBytes;
 constexpr uint32_t kOffV = kOffK + kKStages * kTileBytes;
-constexpr uint32_t kOffBar = kOffV + kVStages * kTileBytes;
+constexpr uint32_t kOffBar = kOffV + 2 * kTileBytes;
 // No alignment slack: there is no static shared memory, and the dynamic window starts on a
 // 1 KB boundary (checked at entry; the swizzled tiles need it).
+template <bool PACK>
+constexpr int v_stages() { return PACK ? 3 : 2; }
+__device__ __forceinline__ uint32_t v_offset(int stage) {
+  return stage < 2 ? kOffV + (uint32_t)stage * kTileBytes : kOffQ + kTileBytes;
+}
 constexpr size_t kSmemBytes = kOffBar + sizeof(FwdBarriers);
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
@@ -104,8 +110,9 @@ __device__ __forceinline__ TilePages tile_pages(const ScoreFwdParams& p, const i
     b1 = count - v;
   }
   if (PACK) {
-    // the interval's share of this block, half of it for each tile.  A takes the odd page: its
-    // ring slots were its own before, so every slot that is waited for is freed by its last user
+    // the interval's share of this block, half of it for each tile, A the odd page.  A slot of
+    // either ring is waited for only when its last user has a later page of its own, whose S
+    // tells it that the slot is free (V: entry e waits for e - 3, whose tile also has e - 1)
     const int n = a1 - a0;
     const int c0 = a0 + (int)((int64_t)n * blockIdx.z / p.s.n_split);
     const int c1 = a0 + (int)((int64_t)n * (blockIdx.z + 1) / p.s.n_split);
@@ -182,9 +189,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // B: the later rows in the upward walk, the earlier ones (which start below) in the reversed.
   constexpr bool REVERSED = BIAS;
   const int tile[2] = {2 * pair + (REVERSED ? 1 : 0), 2 * pair + (REVERSED ? 0 : 1)};
-  int count = a.sel_count[h];
-  count = count < 0 ? 0 : min(count, a.max_sel);  // flagged by check_selection
+  const int32_t* sel_row = a.sel + (size_t)h * a.max_sel;
+  const int raw_count = a.sel_count[h];
+  // this thread's first entry and the one before it, asked for early
+  const int tid_entry = min((int)threadIdx.x, a.max_sel - 1);
+  const int sel_mine = sel_row[tid_entry], sel_before = sel_row[max(tid_entry - 1, 0)];
+  const int count = raw_count < 0 ? 0 : min(raw_count, a.max_sel);  // flagged below
   volatile int* abort = &bar->abort;
+  constexpr int kV = v_stages<PACK>();
 
   // softmax thread: its row and query head
   const int x = warp < 2 ? 0 : (warp - 2) >> 3;      // tile
@@ -203,14 +215,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       valid = row < a.n_q;
       hq = (int)blockIdx.x;
     }
-    if (valid) row_span(p.s, row, kb, ke);
-    int64_t lo = valid && ke > kb ? kb : INT64_MAX, hi = valid && ke > kb ? ke : 0;
+    int64_t lo = INT64_MAX, hi = 0;
+    if (!p.s.begin && !p.s.end) {  // causal: the warp's first and last row tell
+      const int first = (warp & 3) * 32, rows = PACK ? a.n_q * G : min(kTile, a.n_q - tile[x] * kTile);
+      if (first < rows) {
+        const int last = min(first + 31, rows - 1), t0 = PACK ? 0 : tile[x] * kTile;
+        lo = 0;
+        hi = a.q_start + t0 + (PACK ? last / G : last) + 1;
+        ke = a.q_start + t0 + (PACK ? first / G : first) + 1;
+      }
+    } else {
+      if (valid) row_span(p.s, row, kb, ke);
+      if (valid && ke > kb) {
+        lo = kb;
+        hi = ke;
+      }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      kb = max(kb, __shfl_xor_sync(0xffffffffu, kb, o));
-      ke = min(ke, __shfl_xor_sync(0xffffffffu, ke, o));
+      for (int o = 16; o > 0; o >>= 1) {
+        lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        kb = max(kb, __shfl_xor_sync(0xffffffffu, kb, o));
+        ke = min(ke, __shfl_xor_sync(0xffffffffu, ke, o));
+      }
     }
     if (lane == 0 && half == 0) {
       bar->lo[4 * x + (warp & 3)] = lo;
@@ -286,16 +312,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       page[2 * t] = hi > 0 ? lo / kTile : 0;
       page[2 * t + 1] = (hi + kTile - 1) / kTile;
     }
-    const int32_t* sel = a.sel + (size_t)h * a.max_sel;
     int n[4] = {0, 0, 0, 0};
     bool bad = false;
     for (int e = threadIdx.x; e < count; e += kThreads) {
-      const int pg = sel[e];
-      bad |= pg < 0 || pg >= p.s.n_view || (e > 0 && sel[e - 1] >= pg);
+      const int pg = e < kThreads ? sel_mine : sel_row[e];
+      const int before = e < kThreads ? sel_before : sel_row[e - 1];
+      bad |= pg < 0 || pg >= p.s.n_view || (e > 0 && before >= pg);
 #pragma unroll
       for (int i = 0; i < 4; ++i) n[i] += pg < page[i] ? 1 : 0;
     }
-    if (bad || (threadIdx.x == 0 && count != a.sel_count[h])) atomicOr(a.err, OOMB_DEVERR_SEL);
+    if (bad || (threadIdx.x == 0 && count != raw_count)) atomicOr(a.err, OOMB_DEVERR_SEL);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int sum = __reduce_add_sync(0xffffffffu, n[i]);
@@ -309,53 +335,66 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      auto row_of = [&](int e) -> int {  // first row of ring entry e's block in the K/V maps
+    // The lanes look up 32 ring entries at a time (page, physical page: two loads that wait for
+    // one another); lane 0 waits for free slots and issues the copies.
+    int jk = 0, jv = 0;
+    bool up = true;
+    for (int base = 0; up && base < t.n_ring; base += 32) {
+      const int e = base + lane;
+      if (e < t.n_ring) {
         const int j = entry(PACK ? t.first[e & 1] + (e >> 1) : t.lo + e);
-        const int64_t blk = score_block(p.s, h, j, a.sel[(size_t)h * a.max_sel + j]);
-        return blk < 0 ? 0 : (int)(blk * kTile);  // a page left out is masked whole: any block will do
-      };
-      int jk = 0, jv = 0;
-      long long last = clock64();
-      while (jv < t.n_ring) {
-        bool progressed = false;
-        if (jk < t.n_ring) {
-          const int ks = jk % kKStages;
-          if (jk < kKStages || mbar_test_wait(&bar->k_empty[ks], ((jk / kKStages) - 1) & 1)) {
-            const int rw = row_of(jk);
-            mbar_arrive_expect_tx(&bar->k_full[ks], kTileBytes);
-            tma_load_2d(sm + kOffK + ks * kTileBytes, &tk, &bar->k_full[ks], 0, rw);
-            tma_load_2d(sm + kOffK + ks * kTileBytes + kHalfBytes, &tk, &bar->k_full[ks], 64, rw);
-            ++jk;
-            progressed = true;
+        const int64_t blk = score_block(p.s, h, j, sel_row[j]);
+        bar->kv_row[e % 64] = blk < 0 ? 0 : (int)(blk * kTile);  // a page left out is masked whole: any block will do
+      }
+      __syncwarp();
+      if (lane == 0) {
+        const int to = min(base + 32, t.n_ring);  // V is at most a few entries behind K
+        long long last = clock64();
+        while (jk < to || (to == t.n_ring && jv < to)) {
+          bool progressed = false;
+          if (jk < to) {
+            const int ks = jk % kKStages;
+            if (jk < kKStages || mbar_test_wait(&bar->k_empty[ks], ((jk / kKStages) - 1) & 1)) {
+              const int rw = bar->kv_row[jk % 64];
+              mbar_arrive_expect_tx(&bar->k_full[ks], kTileBytes);
+              tma_load_2d(sm + kOffK + ks * kTileBytes, &tk, &bar->k_full[ks], 0, rw);
+              tma_load_2d(sm + kOffK + ks * kTileBytes + kHalfBytes, &tk, &bar->k_full[ks], 64, rw);
+              ++jk;
+              progressed = true;
+            }
           }
-        }
-        if (jv < jk) {
-          const int vs = jv % kVStages;
-          if (jv < kVStages || mbar_test_wait(&bar->v_empty[vs], ((jv / kVStages) - 1) & 1)) {
-            const int rw = row_of(jv);
-            mbar_arrive_expect_tx(&bar->v_full[vs], kTileBytes);
-            tma_load_2d(sm + kOffV + vs * kTileBytes, &tv, &bar->v_full[vs], 0, rw);
-            tma_load_2d(sm + kOffV + vs * kTileBytes + kHalfBytes, &tv, &bar->v_full[vs], 64, rw);
-            ++jv;
-            progressed = true;
+          if (jv < jk) {
+            const int vs = jv % kV;
+            if (jv < kV || mbar_test_wait(&bar->v_empty[vs], ((jv / kV) - 1) & 1)) {
+              const int rw = bar->kv_row[jv % 64];
+              mbar_arrive_expect_tx(&bar->v_full[vs], kTileBytes);
+              tma_load_2d(sm + v_offset(vs), &tv, &bar->v_full[vs], 0, rw);
+              tma_load_2d(sm + v_offset(vs) + kHalfBytes, &tv, &bar->v_full[vs], 64, rw);
+              ++jv;
+              progressed = true;
+            }
           }
-        }
-        if (progressed) {
-          last = clock64();
-        } else if (*abort) {
-          break;
-        } else if (clock64() - last > (1ll << 31)) {
-          atomicOr(a.err, kErrMbarTimeout);
-          *abort = 1;
-          break;
+          if (progressed) {
+            last = clock64();
+          } else if (*abort) {
+            up = false;
+            break;
+          } else if (clock64() - last > (1ll << 31)) {
+            atomicOr(a.err, kErrMbarTimeout);
+            *abort = 1;
+            up = false;
+            break;
+          }
         }
       }
+      up = __shfl_sync(0xffffffffu, up, 0);
+    }
+    if (lane == 0) {
       // drain: every armed stage must have landed before the block may exit
       for (int jj = (jk > kKStages ? jk - kKStages : 0); jj < jk; ++jj)
         mbar_wait(&bar->k_full[jj % kKStages], (jj / kKStages) & 1, a.err, nullptr);
-      for (int jj = (jv > kVStages ? jv - kVStages : 0); jj < jv; ++jj)
-        mbar_wait(&bar->v_full[jj % kVStages], (jj / kVStages) & 1, a.err, nullptr);
+      for (int jj = (jv > kV ? jv - kV : 0); jj < jv; ++jj)
+        mbar_wait(&bar->v_full[jj % kV], (jj / kV) & 1, a.err, nullptr);
       mbar_wait(&bar->q_full, 0, a.err, nullptr);
     }
   } else if (warp == 1) {
@@ -378,10 +417,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto issue_pv = [&](int xx, int j) -> bool {  // O += P V_j
         const int e = ring_of<PACK>(t, xx, j);
-        if (!mbar_wait(&bar->v_full[e % kVStages], (e / kVStages) & 1, a.err, abort)) return false;
+        if (!mbar_wait(&bar->v_full[e % kV], (e / kV) & 1, a.err, abort)) return false;
         if (!mbar_wait(&bar->p_full[xx], j & 1, a.err, abort)) return false;
         tc_fence_after();
-        const uint32_t aV = smem_u32(sm + kOffV + (e % kVStages) * kTileBytes);
+        const uint32_t aV = smem_u32(sm + v_offset(e % kV));
         const uint32_t ap = tmem + xx * 128, o = tmem + 256 + xx * 128;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
@@ -418,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* fail = &bar->fail[x][warp & 3];
     const int64_t qpos = a.q_start + row;
     const float slope2 = BIAS ? p.s.slopes[hq] * kLog2e : 0.f;
-    const int32_t* sel = a.sel + (size_t)h * a.max_sel + entry(t.first[x]);
+    const int32_t* sel = sel_row + entry(t.first[x]);
     constexpr int kNext = REVERSED ? -1 : 1;
     const int b_first = t.first[1] - t.lo, b_end = b_first + t.n[1];  // rows: ring entries of tile B
     float m = -INFINITY, l = 0.f;
@@ -443,10 +482,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e = ring_of<PACK>(t, x, j);
         if (PACK) {  // each ring entry has one user
           mbar_arrive(&bar->k_empty[e % kKStages]);
-          if (j > 0) mbar_arrive(&bar->v_empty[ring_of<PACK>(t, x, j - 1) % kVStages]);
+          if (j > 0) mbar_arrive(&bar->v_empty[ring_of<PACK>(t, x, j - 1) % kV]);
         } else if (x == 1 || e < b_first || e >= b_end) {  // the last user of page e
           mbar_arrive(&bar->k_empty[e % kKStages]);
-          if (e > 0) mbar_arrive(&bar->v_empty[(e - 1) % kVStages]);
+          if (e > 0) mbar_arrive(&bar->v_empty[(e - 1) % kV]);
         }
       }
       uint32_t sr[64];
@@ -632,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const float lse = done ? (m + log2f(l)) * kLn2 : -INFINITY;
-    if (done) {
+    if (done && split) {
       tc_fence_after();
 #pragma unroll 1
       for (int cc = 0; cc < 2; ++cc) {
@@ -640,25 +679,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tO + cc * 32, o);
         tmem_wait_ld();
         if (!valid) continue;
-        const size_t at = rh * kD + half * 64 + cc * 32;
-        if (split) {
-          float4* dst = reinterpret_cast<float4*>(p.s.part_o + (size_t)part * rows * kD + at);
+        float4* dst = reinterpret_cast<float4*>(p.s.part_o + ((size_t)part * rows + rh) * kD + half * 64 + cc * 32);
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
-            dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
-                                 __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o_out) + at);
+        for (int v = 0; v < 8; ++v)
+          dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                               __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
+      }
+    } else if (done) {
+      // through shared memory (the tile's Q, read by the last S, is free), so that a warp writes
+      // whole 256-byte rows: 16-byte chunk c of row r stands at c ^ (r & 15)
+      tc_fence_after();
+      uint8_t* stage = sm + kOffQ + x * kTileBytes;
+#pragma unroll 1
+      for (int cc = 0; cc < 2; ++cc) {
+        uint32_t o[32];
+        tmem_ld32(tO + cc * 32, o);
+        tmem_wait_ld();
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint4 w;
-            w.x = pack_bf16x2(__uint_as_float(o[8 * v + 0]) * inv, __uint_as_float(o[8 * v + 1]) * inv);
-            w.y = pack_bf16x2(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv);
-            w.z = pack_bf16x2(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv);
-            w.w = pack_bf16x2(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv);
-            dst[v] = w;
-          }
+        for (int v = 0; v < 4; ++v) {
+          uint4 w;
+          w.x = pack_bf16x2(__uint_as_float(o[8 * v + 0]) * inv, __uint_as_float(o[8 * v + 1]) * inv);
+          w.y = pack_bf16x2(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv);
+          w.z = pack_bf16x2(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv);
+          w.w = pack_bf16x2(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv);
+          const int c = half * 8 + cc * 4 + v;
+          *reinterpret_cast<uint4*>(stage + r * 256 + ((c ^ (r & 15)) * 16)) = w;
         }
+      }
+      named_bar_sync(pair_bar, 64);
+      const int c = lane & 15, row0 = tile[x] * kTile;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // this warp: 16 of the pair's 32 rows, two at a time
+        const int rr = (warp & 3) * 32 + half * 16 + 2 * i + (lane >> 4);
+        if (row0 + rr < a.n_q)
+          *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o_out) + ((size_t)(row0 + rr) * Hq + hq) * kD +
+                                    c * 8) =
+              *reinterpret_cast<const uint4*>(stage + rr * 256 + ((c ^ (rr & 15)) * 16));
       }
     } else if (!split && valid) {
       uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o_out) + rh * kD + half * 64);
@@ -768,7 +824,8 @@ cudaError_t launch_score_fwd_tc(ScoreArgs& s, cudaStream_t st) {
   p.n_tiles = (s.a.n_q + kTile - 1) / kTile;
   p.n_pairs = pack ? 1 : (p.n_tiles + 1) / 2;
   if (pack) {
-    // one block per SM, each with at least two pages for either tile
+    // one block per SM, as long as each has two pages for either tile (with one, the parts'
+    // traffic costs what the shorter walk saves)
     s.n_split = std::max(1, std::min(limit / 2, (s.a.max_sel + 3) / 4));
   } else {
     // waves of blocks, each as long as its pages plus about kFixed pages of set-up and
