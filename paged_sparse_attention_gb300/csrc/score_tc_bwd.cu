@@ -20,8 +20,6 @@
 // owner, warps 2-9 softmax (thread = key row, 32 of a half's 64 query columns) and epilogue,
 // warps 10-13 dQ read-out.  TMEM columns: half a [0,128), half b [128,256): S^T, dP^T, then
 // packed P^T and dA^T over S^T and dQ^T over dP^T; dV [256,384); dK [384,512).
-#include <type_traits>
-
 #include "score_tc_common.cuh"
 
 namespace oomb {
@@ -47,19 +45,16 @@ struct TileSpan {
   int64_t lo, hi, clo, chi;
 };
 
-template <TanhForm F>
-using Const = std::integral_constant<TanhForm, F>;
-
 struct ScoreBwdParams {
   ScoreArgs s;
   CapConst cap;
-  const float* lse2;       // [Hq, n_pad] LSE * log2(e), +inf on rows without keys and padded rows
+  const float* lse2;       // [Hq, n_pad] LSE * log2(e) - cap2, +inf on rows without keys and padded rows
   const float* Dbuf;       // [Hq, n_pad] rowsum(dO * O), 0 on padded rows
   const longlong2* span;   // [n_pad] key range of each row
   const TileSpan* tiles;   // [n_tiles]
   float* dq_acc;
   int n_pad, n_tiles, n_split;
-  float scale, scale_log2;
+  float scale_da, scale_log2;  // scale_da: of what dK and dQ are summed from (4 scale under a cap)
 };
 
 struct __align__(8) BwdBarriers {
@@ -354,43 +349,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float f0 = BIAS ? (float)(a.q_start + q0 - kpos) : 0.f;  // distance of column i: |f0 + i|
         uint32_t pk[16], dk[16];
-        // P and dA of the columns, four at a time
-        auto columns = [&](auto form) {
-          constexpr TanhForm F = decltype(form)::value;
+        // P and dA of the columns, four at a time.  Capped: with r = 1 / (1 + e^2x) the score is
+        // cap (1 - 2 r), whose constant is in lse2 already, and 1 - tanh^2 = 4 (r - r^2), whose
+        // factor is left to scale_da (one form for every x: a polynomial for small x beside it
+        // costs more in instruction cache than the two reciprocal-exponential steps)
 #pragma unroll
-          for (int c4 = 0; c4 < 8; ++c4) {
-            const float4 L = vs4[c4], Dv = vs4[16 + c4];
-            const float l4[4] = {L.x, L.y, L.z, L.w}, d4[4] = {Dv.x, Dv.y, Dv.z, Dv.w};
-            float pr[4], dar[4];
+        for (int c4 = 0; c4 < 8; ++c4) {
+          const float4 L = vs4[c4], Dv = vs4[16 + c4];
+          const float l4[4] = {L.x, L.y, L.z, L.w}, d4[4] = {Dv.x, Dv.y, Dv.z, Dv.w};
+          float pr[4], dar[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = 4 * c4 + e;
-              const float S = __uint_as_float(sr[i]);
-              float shift = -l4[e];
-              if (BIAS) shift = fmaf(-slope2, fabsf(f0 + (float)i), shift);
-              float th = 0.f;
-              if constexpr (CAP) th = tanh_of<F>(S, p.cap);
-              pr[e] = ex2_approx(CAP ? fmaf(th, p.cap.cap2, shift) : fmaf(S, p.scale_log2, shift));
-              dar[e] = pr[e] * (__uint_as_float(dr[i]) - d4[e]);
-              if constexpr (CAP) dar[e] *= fmaf(-th, th, 1.f);
-            }
-            pk[2 * c4] = pack_bf16x2(pr[0], pr[1]);
-            pk[2 * c4 + 1] = pack_bf16x2(pr[2], pr[3]);
-            dk[2 * c4] = pack_bf16x2(dar[0], dar[1]);
-            dk[2 * c4 + 1] = pack_bf16x2(dar[2], dar[3]);
+          for (int e = 0; e < 4; ++e) {
+            const int i = 4 * c4 + e;
+            const float S = __uint_as_float(sr[i]);
+            float shift = -l4[e], r = 0.f;
+            if (BIAS) shift = fmaf(-slope2, fabsf(f0 + (float)i), shift);
+            if constexpr (CAP) r = rcp_approx(1.f + ex2_approx(p.cap.arg * S));
+            pr[e] = ex2_approx(CAP ? fmaf(r, -2.f * p.cap.cap2, shift) : fmaf(S, p.scale_log2, shift));
+            dar[e] = pr[e] * (__uint_as_float(dr[i]) - d4[e]);
+            if constexpr (CAP) dar[e] *= fmaf(-r, r, r);
           }
-        };
-        bool small = true;
-        if constexpr (CAP) {
-          float amax = 0.f;
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) amax = fmax3_abs(amax, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
-          small = __all_sync(0xffffffffu, amax <= p.cap.edge3);
+          pk[2 * c4] = pack_bf16x2(pr[0], pr[1]);
+          pk[2 * c4 + 1] = pack_bf16x2(pr[2], pr[3]);
+          dk[2 * c4] = pack_bf16x2(dar[0], dar[1]);
+          dk[2 * c4 + 1] = pack_bf16x2(dar[2], dar[3]);
         }
-        if (!CAP || small)
-          columns(Const<kDegree3>{});
-        else
-          columns(Const<kWide>{});
         if (masked) {  // cleared afterwards, in the packed words, whatever came out for a pair that is not seen
 #pragma unroll
           for (int w = 0; w < 16; ++w) {
@@ -489,8 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             make_float4(__uint_as_float(a[4 * e]), __uint_as_float(a[4 * e + 1]), __uint_as_float(a[4 * e + 2]),
                         __uint_as_float(a[4 * e + 3]));
         *reinterpret_cast<float4*>(sm + kOffStage + stage_off(j, 32 + c)) =
-            make_float4(p.scale * __uint_as_float(b[4 * e]), p.scale * __uint_as_float(b[4 * e + 1]),
-                        p.scale * __uint_as_float(b[4 * e + 2]), p.scale * __uint_as_float(b[4 * e + 3]));
+            make_float4(p.scale_da * __uint_as_float(b[4 * e]), p.scale_da * __uint_as_float(b[4 * e + 1]),
+                        p.scale_da * __uint_as_float(b[4 * e + 2]), p.scale_da * __uint_as_float(b[4 * e + 3]));
       }
     }
     fence_acq_rel_cluster();
@@ -560,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of the padded range: D = rowsum(dO * O) and LSE * log2(e) into [Hq, n_pad] buffers (rows
 // without keys and padded rows: LSE = +inf, so P = 0) and the row of the fp32 dQ accumulator
 // zeroed.
-__global__ void __launch_bounds__(256) score_bwd_prep(const __grid_constant__ ScoreArgs s, int n_pad, int n_tiles,
+__global__ void __launch_bounds__(256) score_bwd_prep(const __grid_constant__ ScoreArgs s, float cap2, int n_pad, int n_tiles,
                                                       float* __restrict__ Dbuf, float* __restrict__ lse2,
                                                       float* __restrict__ dq_acc, longlong2* __restrict__ span,
                                                       TileSpan* __restrict__ tiles) {
@@ -626,7 +609,7 @@ __global__ void __launch_bounds__(256) score_bwd_prep(const __grid_constant__ Sc
   if (lane == 0) {
     const float l = a.lse_in[(size_t)hq * a.n_q + i];
     Dbuf[(size_t)hq * n_pad + i] = d;
-    lse2[(size_t)hq * n_pad + i] = l == -INFINITY ? INFINITY : l * kLog2e;
+    lse2[(size_t)hq * n_pad + i] = l == -INFINITY ? INFINITY : l * kLog2e - cap2;
   }
   reinterpret_cast<float4*>(dq_acc + ((size_t)hq * a.n_q + i) * kD)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
@@ -714,7 +697,7 @@ cudaError_t launch_score_bwd_tc(const ScoreArgs& s, cudaStream_t st) {
   longlong2* span = reinterpret_cast<longlong2*>(take((size_t)n_pad * sizeof(longlong2)));
   TileSpan* tiles = reinterpret_cast<TileSpan*>(take((size_t)n_tiles * sizeof(TileSpan)));
   const int64_t warps = (int64_t)a.n_q * a.g.Hq, warps_pad = (int64_t)n_pad * a.g.Hq;
-  score_bwd_prep<<<(unsigned)(n_tiles + (warps_pad + 7) / 8), 256, 0, st>>>(s, n_pad, n_tiles, Dbuf, lse2, dq_acc,
+  score_bwd_prep<<<(unsigned)(n_tiles + (warps_pad + 7) / 8), 256, 0, st>>>(s, s.cap * kLog2e, n_pad, n_tiles, Dbuf, lse2, dq_acc,
                                                                            span, tiles);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -732,7 +715,7 @@ cudaError_t launch_score_bwd_tc(const ScoreArgs& s, cudaStream_t st) {
   p.dq_acc = dq_acc;
   p.n_pad = n_pad;
   p.n_tiles = n_tiles;
-  p.scale = a.scale;
+  p.scale_da = s.cap > 0.f ? 4.f * a.scale : a.scale;
   p.scale_log2 = a.scale * kLog2e;
   if (s.cap > 0.f)
     e = s.slopes ? launch_main<true, true>(p, tq, tdo, tk, tv, st) : launch_main<true, false>(p, tq, tdo, tk, tv, st);
@@ -740,7 +723,7 @@ cudaError_t launch_score_bwd_tc(const ScoreArgs& s, cudaStream_t st) {
     e = s.slopes ? launch_main<false, true>(p, tq, tdo, tk, tv, st)
                  : launch_main<false, false>(p, tq, tdo, tk, tv, st);
   if (e != cudaSuccess) return e;
-  score_bwd_convert<<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(dq_acc, a.n_q, a.g.Hq, a.scale,
+  score_bwd_convert<<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(dq_acc, a.n_q, a.g.Hq, p.scale_da,
                                                                  reinterpret_cast<__nv_bfloat16*>(a.dq));
   count_launches(2);
   return cudaGetLastError();
