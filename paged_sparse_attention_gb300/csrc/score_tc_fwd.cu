@@ -23,8 +23,6 @@
 // seen S_X(j) knows that PV_X(j-1) is done and frees the ring slots.
 // TMEM columns: S_A, S_B (P over S, bf16), O_A, O_B, 128 each.
 // Scores and row sums are fp32; P is rounded to bf16, the operand type of the second product.
-#include <type_traits>
-
 #include "score_tc_common.cuh"
 
 namespace oomb {
@@ -40,9 +38,6 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled when the
 constexpr float kGentle = 0.35f;           // log2 units a token: the bias changes by less than 45 over a page
 constexpr float kNarrowScores = 20.0f;     // log2 units: capped scores of this size differ by less than 40
 constexpr float kNothing = -127.0f;        // log2 units: 2^x is zero in fp32 with flushed denormals
-
-template <TanhForm F>
-using Const = std::integral_constant<TanhForm, F>;
 
 struct ScoreFwdParams {
   ScoreArgs s;
@@ -510,7 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                : __all_sync(0xffffffffu, amax <= p.cap.edge3) ? kDegree3
                                                               : kWide;
         ref = fabsf(p.cap.cap2 * tanh_any(amax, p.cap));
-        direct = direct && form != kWide && __all_sync(0xffffffffu, ref <= kNarrowScores);
+        if (direct && !__all_sync(0xffffffffu, ref <= kNarrowScores)) {  // the largest score itself
+          direct = p.cap.arg >= 0.f;
+          if (direct)
+            ref = p.cap.cap2 * tanh_any(row_reduce(sr, [](float u, float v, float w) { return fmax3(u, v, w); }), p.cap);
+        }
       } else {
         ref = p.scale_log2 * row_reduce(sr, [](float u, float v, float w) { return fmax3(u, v, w); });
         if (p.scale_log2 < 0.f) {
@@ -522,15 +521,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool nothing = behind && __all_sync(0xffffffffu, ref - m < kNothing);
       if (!direct && !nothing) {
         if constexpr (CAP) {
-          auto cap_all = [&](auto f) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              sr[c] = __float_as_uint(p.cap.cap2 * tanh_of<decltype(f)::value>(__uint_as_float(sr[c]), p.cap));
-          };
-          if (form != kWide)
-            cap_all(Const<kDegree3>{});
-          else
-            cap_all(Const<kWide>{});
+          for (int c = 0; c < 64; ++c)
+            sr[c] = __float_as_uint(p.cap.cap2 * tanh_of<kWide>(__uint_as_float(sr[c]), p.cap));
         } else {
 #pragma unroll
           for (int c = 0; c < 64; ++c) sr[c] = __float_as_uint(p.scale_log2 * __uint_as_float(sr[c]));
@@ -613,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t S = pair_of(c), z = fmul2(S, S);
             f32x2_split(ffma2(S, ffma2(ffma2(q2, z, q1), z, q0), next_shift(c)), t0, t1);
           });
-        } else {
+        } else if (form == kDegree3) {
           const float* q = p.cap.poly3;
           const float k2 = p.cap.cap2;
           const uint64_t q0 = f32x2(q[0] * k2, q[0] * k2), q1 = f32x2(q[1] * k2, q[1] * k2),
@@ -621,6 +614,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           exponentials([&](int c, float& t0, float& t1) {
             const uint64_t S = pair_of(c), z = fmul2(S, S);
             f32x2_split(ffma2(S, ffma2(ffma2(ffma2(q3, z, q2), z, q1), z, q0), next_shift(c)), t0, t1);
+          });
+        } else {  // cap2 tanh(x) = cap2 - 2 cap2 / (1 + e^2x)
+          const uint64_t k2 = f32x2(p.cap.cap2, p.cap.cap2), one = f32x2(1.f, 1.f);
+          const uint64_t arg2 = f32x2(p.cap.arg, p.cap.arg), m2k = f32x2(-2.f * p.cap.cap2, -2.f * p.cap.cap2);
+          exponentials([&](int c, float& t0, float& t1) {
+            float e0, e1;
+            f32x2_split(fmul2(pair_of(c), arg2), e0, e1);
+            f32x2_split(fadd2(f32x2(ex2_approx(e0), ex2_approx(e1)), one), e0, e1);
+            f32x2_split(ffma2(f32x2(rcp_approx(e0), rcp_approx(e1)), m2k, fadd2(next_shift(c), k2)), t0, t1);
           });
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
