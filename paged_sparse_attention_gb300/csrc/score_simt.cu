@@ -497,11 +497,12 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
 }
 
 // n_split > 1: dK (unscaled) and dV of the block's share of the (row tile, query head) pairs go
-// to part[share][KV head][key tile], two [64, d] tiles.
+// to part[share][KV head][key tile], two [64, d] tiles, where the share has seen any row: the
+// flag of the share says so.
 template <typename T, int C>
 __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
     score_dkdv_simt(const __grid_constant__ ScoreArgs s, const float* __restrict__ Dbuf, float* __restrict__ part,
-                    int n_split) {
+                    int32_t* __restrict__ flags, int n_split) {
   const int d = s.a.g.d, P = s.a.g.P, G = s.a.g.G, ld = tile_ld(d);
   const int h = blockIdx.y;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
@@ -533,7 +534,12 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
   }
   load_keys<T>(s, &kl, sk, sv);
   __syncthreads();
-  if (key_hi < 0) return;  // (the join skips these keys too)
+  const size_t slot = ((size_t)blockIdx.z * gridDim.y + h) * gridDim.x + blockIdx.x;
+  if (key_hi < 0) {
+    if (n_split > 1 && threadIdx.x == 0) flags[slot] = 0;
+    return;
+  }
+  bool seen = false;
   float4 dk[4][C], dv[4][C];
 #pragma unroll
   for (int r = 0; r < 4; ++r)
@@ -548,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
     if (rs.hi <= key_lo || rs.lo > key_hi) continue;  // no row of the tile sees these keys
     for (int gq = max(0, u0 - tile * G); gq < min(G, u1 - tile * G); ++gq) {
       const int hq = h * G + gq;
+      seen = true;
       __syncthreads();
       load_rows<T>(s, s.a.q, i0, hq, sq);
       load_rows<T>(s, s.a.dout, i0, hq, sdo);
@@ -562,11 +569,13 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
       weigh_rows(sda, sq, d, ty, tx, dk);
     }
   }
+  if (n_split > 1 && threadIdx.x == 0) flags[slot] = seen;
+  if (!seen) return;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int key = ty + 16 * r;
     if (n_split > 1) {
-      float* dst = part + (((size_t)blockIdx.z * gridDim.y + h) * gridDim.x + blockIdx.x) * 2 * kKeys * d;
+      float* dst = part + slot * 2 * kKeys * d;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int col = 4 * tx + 64 * c;
@@ -624,28 +633,33 @@ __global__ void __launch_bounds__(256) score_dq_join(const __grid_constant__ Sco
   dst[3] = from_float<T>(acc.w * s.a.scale);
 }
 
-// dK += scale * sum of the shares, dV += sum of the shares, for the 64 keys of a block.
+// dK += scale * sum of the shares, dV += sum of the shares, for 64 / gridDim.z of a tile's keys.
 __global__ void __launch_bounds__(256) score_dkdv_join(const __grid_constant__ ScoreArgs s,
-                                                       const float* __restrict__ part, int n_split) {
+                                                       const float* __restrict__ part,
+                                                       const int32_t* __restrict__ flags, int n_split) {
   const int d = s.a.g.d, d4 = d / 4, P = s.a.g.P, h = blockIdx.y;
   __shared__ KeyList kl;
   const int count = sel_count_checked(s.a, h);
   const int64_t v0 = (int64_t)blockIdx.x * kKeys, v1 = (int64_t)count * P;
   if (v0 >= v1) return;
+  const size_t tile = 2 * (size_t)kKeys * d, shares = (size_t)gridDim.y * gridDim.x;
+  const size_t slot = (size_t)h * gridDim.x + blockIdx.x;
+  bool mine = false;
+  for (int z = threadIdx.x; z < n_split; z += blockDim.x) mine |= flags[z * shares + slot] != 0;
+  if (!__syncthreads_or(mine)) return;
   list_owned_keys(s, h, v0, v1, count, &kl);
   __syncthreads();
-  bool any = false;  // a tile without keys has written no shares
-  for (int r = 0; r < kKeys; ++r) any |= kl.pos[r] >= 0;
-  if (!any) return;
-  const size_t tile = 2 * (size_t)kKeys * d, step = (size_t)gridDim.y * gridDim.x * tile;
-  const float* src = part + ((size_t)h * gridDim.x + blockIdx.x) * tile;
-  for (int idx = threadIdx.x; idx < 2 * kKeys * d4; idx += blockDim.x) {
-    const int r = idx / d4, key = r % kKeys, col = 4 * (idx % d4);
+  const int keys = kKeys / gridDim.z, key0 = keys * blockIdx.z;
+  for (int idx = threadIdx.x; idx < 2 * keys * d4; idx += blockDim.x) {
+    const int r = idx / d4, key = key0 + r % keys, col = 4 * (idx % d4);
+    const bool is_k = r < keys;
     if (kl.pos[key] < 0) continue;
+    const float* src = part + slot * tile + (size_t)(is_k ? key : kKeys + key) * d + col;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int z = 0; z < n_split; ++z) {
-      const float4 x = *reinterpret_cast<const float4*>(src + z * step + (size_t)r * d + col);
+      if (!flags[z * shares + slot]) continue;
+      const float4 x = *reinterpret_cast<const float4*>(src + z * shares * tile);
       acc.x += x.x;
       acc.y += x.y;
       acc.z += x.z;
@@ -654,8 +668,8 @@ __global__ void __launch_bounds__(256) score_dkdv_join(const __grid_constant__ S
     const int j = (int)((v0 + key) / P), t = (int)((v0 + key) % P);
     const int phys = s.a.kv.table[s.a.sel[(size_t)h * s.a.max_sel + j]];  // checked by list_owned_keys
     const size_t at = (grad_block(s.a, h, j, phys) * P + t) * d + col;
-    const float f = r < kKeys ? s.a.scale : 1.f;
-    float4* g = reinterpret_cast<float4*>((r < kKeys ? s.a.dk_pool : s.a.dv_pool) + at);
+    const float f = is_k ? s.a.scale : 1.f;
+    float4* g = reinterpret_cast<float4*>((is_k ? s.a.dk_pool : s.a.dv_pool) + at);
     float4 y = *g;
     y.x += f * acc.x;
     y.y += f * acc.y;
@@ -718,6 +732,9 @@ cudaError_t fwd_simt(ScoreArgs& s, cudaStream_t st) {
 }
 
 // Backward: shares of a tile, so that the tiles fill the SMs (two blocks fit one for d <= 64).
+// Ranges leave an unknown part of the key tiles without rows, so dK/dV are cut finer: blocks
+// without rows cost nothing, the others still fill the SMs.
+constexpr int kDkdvFill = 4;
 struct BwdSplit {
   int dq, dkdv;
   size_t dq_bytes, dkdv_bytes;  // of the shares' sums
@@ -729,11 +746,12 @@ BwdSplit simt_bwd_split(const Geometry& g, int n_q, int max_sel) {
   const int64_t slots = simt_slots(g), row_tiles = (n_q + kRows - 1) / kRows;
   const int64_t key_tiles = ((int64_t)max_sel * g.P + kKeys - 1) / kKeys;
   b.dq = (int)std::min<int64_t>(std::max<int64_t>(1, slots / (row_tiles * g.Hq)), std::max<int64_t>(1, key_tiles / 2));
-  b.dkdv = (int)std::min<int64_t>(std::max<int64_t>(1, slots / (key_tiles * g.Hkv)), row_tiles * g.G);
+  b.dkdv = (int)std::min<int64_t>(std::max<int64_t>(1, kDkdvFill * slots / (key_tiles * g.Hkv)), row_tiles * g.G);
   b.dq_bytes = b.dq > 1 ? align_up((size_t)b.dq * n_q * g.Hq * g.d * 4, 256) : 0;
   b.dkdv_bytes = b.dkdv > 1 ? (size_t)b.dkdv * key_tiles * g.Hkv * dkdv_tile_bytes(g) : 0;
   return b;
 }
+size_t dkdv_flag_bytes(const Geometry& g) { return align_up((size_t)kDkdvFill * simt_slots(g) * 4, 256); }
 
 template <typename T, int C>
 cudaError_t bwd_simt(const ScoreArgs& s, cudaStream_t st) {
@@ -746,7 +764,8 @@ cudaError_t bwd_simt(const ScoreArgs& s, cudaStream_t st) {
   const BwdSplit b = simt_bwd_split(g, s.a.n_q, s.a.max_sel);
   char* ws = reinterpret_cast<char*>(s.a.ws);
   float* Dbuf = reinterpret_cast<float*>(ws);
-  float* part_dq = reinterpret_cast<float*>(ws + align_up((size_t)g.Hq * s.a.n_q * 4, 256));
+  int32_t* flags = reinterpret_cast<int32_t*>(ws + align_up((size_t)g.Hq * s.a.n_q * 4, 256));
+  float* part_dq = reinterpret_cast<float*>(reinterpret_cast<char*>(flags) + dkdv_flag_bytes(g));
   float* part_kv = reinterpret_cast<float*>(reinterpret_cast<char*>(part_dq) + b.dq_bytes);
   const int64_t warps = (int64_t)s.a.n_q * g.Hq;
   score_dot<T><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(s, Dbuf);
@@ -754,8 +773,8 @@ cudaError_t bwd_simt(const ScoreArgs& s, cudaStream_t st) {
   score_dq_simt<T, C><<<gq, kThreads, dq_smem(d), st>>>(s, Dbuf, part_dq, b.dq);
   if (b.dq > 1) score_dq_join<T><<<(unsigned)((warps * d / 4 + 255) / 256), 256, 0, st>>>(s, part_dq, b.dq);
   dim3 gk((unsigned)(((int64_t)s.a.max_sel * g.P + kKeys - 1) / kKeys), g.Hkv, b.dkdv);
-  score_dkdv_simt<T, C><<<gk, kThreads, dkdv_smem(d), st>>>(s, Dbuf, part_kv, b.dkdv);
-  if (b.dkdv > 1) score_dkdv_join<<<dim3(gk.x, gk.y), 256, 0, st>>>(s, part_kv, b.dkdv);
+  score_dkdv_simt<T, C><<<gk, kThreads, dkdv_smem(d), st>>>(s, Dbuf, part_kv, flags, b.dkdv);
+  if (b.dkdv > 1) score_dkdv_join<<<dim3(gk.x, gk.y, 8), 256, 0, st>>>(s, part_kv, flags, b.dkdv);
   count_launches(3 + (b.dq > 1) + (b.dkdv > 1));
   return cudaGetLastError();
 }
@@ -790,7 +809,8 @@ size_t score_bwd_workspace_bytes(const Geometry& g, int n_q) {
   if (tc_supported(g)) return score_bwd_tc_workspace_bytes(g, n_q);
   // D, and the most that the shares of dQ (any number of keys) and of dK/dV can take
   const BwdSplit b = simt_bwd_split(g, n_q, INT_MAX / (2 * g.P));
-  return align_up((size_t)g.Hq * n_q * 4, 256) + b.dq_bytes + (size_t)simt_slots(g) * dkdv_tile_bytes(g);
+  return align_up((size_t)g.Hq * n_q * 4, 256) + dkdv_flag_bytes(g) + b.dq_bytes +
+         (size_t)kDkdvFill * simt_slots(g) * dkdv_tile_bytes(g);
 }
 
 cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st) {
