@@ -76,7 +76,7 @@ typedef enum { OOMB_BF16 = 0, OOMB_FP32 = 1 } oomb_dtype;
 typedef enum {
   OOMB_OP_SELECT = 0,
   OOMB_OP_BWD = 1,
-  OOMB_OP_SCORE_FWD = 2, /* oomb_score_attn_fwd (may be 0) */
+  OOMB_OP_SCORE_FWD = 2, /* oomb_score_attn_fwd */
   OOMB_OP_SCORE_BWD = 3  /* oomb_score_attn_bwd */
 } oomb_op;
 
@@ -370,8 +370,9 @@ typedef struct {
  *  - a selection that is not strictly ascending pages of that view, or a page that is not
  *    mapped, sets OOMB_DEVERR_SEL / OOMB_DEVERR_PAGE; the entry is left out.
  * K and V must be finite in the pages read: a masked key weighs nothing, but 0 times an
- * infinity or a NaN in V is a NaN.  Workspace: oomb_workspace_size(OOMB_OP_SCORE_FWD, n_q)
- * bytes (may be 0), contents scratch; two calls that may run at once need one each.
+ * infinity or a NaN in V is a NaN.  Workspace: oomb_workspace_size(OOMB_OP_SCORE_FWD, n)
+ * bytes, n the most rows of any call it serves (n_q or more), contents scratch; two calls
+ * that may run at once need one each.
  * Capturable in a CUDA graph (the number of tokens appended is the one at capture).
  * Errors: ARG (also a softcap that is negative or not finite), ALIGN, WORKSPACE, CUDA. */
 OOMB_API oomb_status oomb_score_attn_fwd(oomb_pool* pool, const void* q, int64_t q_start, int n_q, const int32_t* sel,
@@ -387,7 +388,7 @@ OOMB_API oomb_status oomb_score_attn_fwd(oomb_pool* pool, const void* q, int64_t
  * pages that no row sees are not touched.  dK/dV, their staging (offload_grads) and dq are
  * as in oomb_chunk_attn_bwd: one writer per pool row in a fixed order (the same bits on
  * every run), dq summed in fp32 (tensor-core shapes: in no fixed order, so equal to
- * rounding).  Workspace: oomb_workspace_size(OOMB_OP_SCORE_BWD, n_q) bytes.
+ * rounding).  Workspace: oomb_workspace_size(OOMB_OP_SCORE_BWD, n) bytes, as above.
  * Errors: those of oomb_score_attn_fwd. */
 OOMB_API oomb_status oomb_score_attn_bwd(oomb_pool* pool, const void* q, const void* o, const void* d_o,
                                          const float* lse, int64_t q_start, int n_q, const int32_t* sel,

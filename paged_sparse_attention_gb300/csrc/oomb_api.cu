@@ -572,7 +572,7 @@ oomb_status oomb_score_attn_fwd(oomb_pool* p, const void* q, int64_t q_start, in
   if (!p || n_q <= 0 || !o || !lse) return OOMB_ERR_ARG;
   ScoreArgs a;
   oomb_status s = make_score_args(p, q, q_start, n_q, sel, sel_count, max_sel, scale, mod, ws, ws_bytes,
-                                  score_fwd_workspace_bytes(p->g, n_q), &a);
+                                  score_fwd_need(p->g, n_q), &a);
   if (s != OOMB_OK) return s;
   if (!aligned(o, 16) || !aligned(lse, 4)) return OOMB_ERR_ALIGN;
   a.a.o_out = o;
@@ -587,7 +587,7 @@ oomb_status oomb_score_attn_bwd(oomb_pool* p, const void* q, const void* o, cons
   if (!p || n_q <= 0 || !o || !d_o || !lse || !dq) return OOMB_ERR_ARG;
   ScoreArgs a;
   oomb_status s = make_score_args(p, q, q_start, n_q, sel, sel_count, max_sel, scale, mod, ws, ws_bytes,
-                                  score_bwd_workspace_bytes(p->g, n_q), &a);
+                                  max_sel > 0 ? score_bwd_need(p->g, n_q, max_sel) : 0, &a);
   if (s != OOMB_OK) return s;
   if (!aligned(o, 16) || !aligned(d_o, 16) || !aligned(dq, 16) || !aligned(lse, 4)) return OOMB_ERR_ALIGN;
   a.a.o = o;

@@ -79,7 +79,9 @@ int score_tc_parts_limit(const Geometry& g, int n_q);  // most parts the keys of
 cudaError_t launch_score_fwd_tc(ScoreArgs& s, cudaStream_t st);
 cudaError_t launch_score_bwd_tc(const ScoreArgs& s, cudaStream_t st);
 size_t score_bwd_tc_workspace_bytes(const Geometry& g, int n_q);
-size_t score_fwd_workspace_bytes(const Geometry& g, int n_q);
+size_t score_fwd_need(const Geometry& g, int n_q);  // bytes that this call uses
+size_t score_bwd_need(const Geometry& g, int n_q, int max_sel);
+size_t score_fwd_workspace_bytes(const Geometry& g, int n_q);  // enough for every call of up to n_q rows
 size_t score_bwd_workspace_bytes(const Geometry& g, int n_q);
 cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st);
 cudaError_t launch_score_bwd(const ScoreArgs& s, cudaStream_t st);

@@ -713,9 +713,11 @@ int simt_split_limit(const Geometry& g, int n_q) {
   return (int)std::min<int64_t>(32, std::max<int64_t>(1, 2 * (int64_t)device_sm_count() / tiles));
 }
 
-// Parts the keys of a row may be cut into.
+// Parts the keys of a row may be cut into, and the most rows x parts that any n_q comes to.
+int64_t part_rows_limit(const Geometry& g) { return (int64_t)device_sm_count() * (tc_supported(g) ? 512 : 128); }
 int parts_limit(const Geometry& g, int n_q) {
-  return tc_supported(g) ? score_tc_parts_limit(g, n_q) : simt_split_limit(g, n_q);
+  const int64_t most = std::max<int64_t>(1, part_rows_limit(g) / ((int64_t)n_q * g.Hq));
+  return (int)std::min<int64_t>(most, tc_supported(g) ? score_tc_parts_limit(g, n_q) : simt_split_limit(g, n_q));
 }
 
 template <typename T, int C>
@@ -724,7 +726,7 @@ cudaError_t fwd_simt(ScoreArgs& s, cudaStream_t st) {
   cudaError_t e = set_smem_limit((const void*)score_fwd_simt<T, C>, fwd_smem(64 * C), smem_set);
   if (e != cudaSuccess) return e;
   const int64_t key_tiles = ((int64_t)s.a.max_sel * s.a.g.P + kKeys - 1) / kKeys;
-  s.n_split = (int)std::min<int64_t>(simt_split_limit(s.a.g, s.a.n_q), std::max<int64_t>(1, key_tiles / 2));
+  s.n_split = (int)std::min<int64_t>(parts_limit(s.a.g, s.a.n_q), std::max<int64_t>(1, key_tiles / 2));
   dim3 grid((s.a.n_q + kRows - 1) / kRows, s.a.g.Hq, s.n_split);
   score_fwd_simt<T, C><<<grid, kThreads, fwd_smem(s.a.g.d), st>>>(s);
   count_launches(1);
@@ -794,23 +796,37 @@ cudaError_t bwd_width(const ScoreArgs& s, cudaStream_t st) {
 struct FwdSpace {
   size_t o, lse, order;
 };
+static size_t order_bytes(const Geometry& g, int n_q) {
+  return tc_supported(g) ? align_up((size_t)n_q / 64 * 4 + 4, 256) : 0;
+}
 static FwdSpace fwd_space(const Geometry& g, int n_q) {
   const int n = parts_limit(g, n_q);
   const size_t rows = n > 1 ? (size_t)n_q * g.Hq * n : 0;
-  return {align_up(rows * g.d * 4, 256), align_up(rows * 4, 256),
-          tc_supported(g) ? align_up((size_t)n_q / 64 * 4 + 4, 256) : 0};
+  return {align_up(rows * g.d * 4, 256), align_up(rows * 4, 256), order_bytes(g, n_q)};
 }
-size_t score_fwd_workspace_bytes(const Geometry& g, int n_q) {
+size_t score_fwd_need(const Geometry& g, int n_q) {
   const FwdSpace f = fwd_space(g, n_q);
   return f.o + f.lse + f.order;
 }
+// Fewer rows are cut into more parts, so what one n_q needs says little about a smaller one.
+// The size that is handed out covers every call of up to n_q rows.
+size_t score_fwd_workspace_bytes(const Geometry& g, int n_q) {
+  const int64_t parts = tc_supported(g) ? score_tc_parts_limit(g, 0) : simt_split_limit(g, 1);
+  const size_t rows = (size_t)std::min(part_rows_limit(g), (int64_t)n_q * g.Hq * parts);
+  return align_up(rows * g.d * 4, 256) + align_up(rows * 4, 256) + order_bytes(g, n_q);
+}
 
+size_t score_bwd_need(const Geometry& g, int n_q, int max_sel) {
+  if (tc_supported(g)) return score_bwd_tc_workspace_bytes(g, n_q);
+  const BwdSplit b = simt_bwd_split(g, n_q, max_sel);
+  return align_up((size_t)g.Hq * n_q * 4, 256) + dkdv_flag_bytes(g) + b.dq_bytes + b.dkdv_bytes;
+}
+// Covers every call of up to n_q rows: D, and the most that the shares of dQ and dK/dV take.
 size_t score_bwd_workspace_bytes(const Geometry& g, int n_q) {
   if (tc_supported(g)) return score_bwd_tc_workspace_bytes(g, n_q);
-  // D, and the most that the shares of dQ (any number of keys) and of dK/dV can take
-  const BwdSplit b = simt_bwd_split(g, n_q, INT_MAX / (2 * g.P));
-  return align_up((size_t)g.Hq * n_q * 4, 256) + dkdv_flag_bytes(g) + b.dq_bytes +
-         (size_t)kDkdvFill * simt_slots(g) * dkdv_tile_bytes(g);
+  const size_t slots = (size_t)simt_slots(g);
+  return align_up((size_t)g.Hq * n_q * 4, 256) + dkdv_flag_bytes(g) +
+         align_up((size_t)std::min(n_q, kRows) * slots * g.d * 4, 256) + kDkdvFill * slots * dkdv_tile_bytes(g);
 }
 
 cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st) {
@@ -820,6 +836,7 @@ cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st) {
   s.part_lse = reinterpret_cast<float*>(ws + f.o);
   s.order = reinterpret_cast<int32_t*>(ws + f.o + f.lse);
   const bool f32 = s.a.g.dtype == OOMB_FP32;
+  s.n_split = parts_limit(s.a.g, s.a.n_q);
   cudaError_t e = tc_supported(s.a.g) ? launch_score_fwd_tc(s, st)
                   : f32               ? fwd_width<float>(s, st)
                                       : fwd_width<__nv_bfloat16>(s, st);

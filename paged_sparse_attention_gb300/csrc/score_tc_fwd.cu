@@ -810,18 +810,20 @@ cudaError_t launch_pack(bool pack, const ScoreFwdParams& p, const CUtensorMap& t
 
 bool score_tc_packs(const Geometry& g, int n_q) { return (int64_t)n_q * g.G <= kTile; }
 
-// Parts the keys of a tile may be cut into.
+// Parts the keys of a tile may be cut into (n_q = 0: for any number of rows).
 int score_tc_parts_limit(const Geometry& g, int n_q) {
-  const int sms = device_sm_count();
-  if (score_tc_packs(g, n_q)) return 2 * std::max(1, std::min(sms, 512) / g.Hkv);
-  const int64_t units = (int64_t)((n_q + 2 * kTile - 1) / (2 * kTile)) * g.Hq;
-  return (int)std::min<int64_t>(1024, std::max<int64_t>(1, 4 * (int64_t)sms / units));
+  const int sms = std::min(device_sm_count(), 512);  // score_join takes up to 1024 parts
+  const int packed = 2 * std::max(1, sms / g.Hkv);
+  const int64_t units = (int64_t)((std::max(n_q, 1) + 2 * kTile - 1) / (2 * kTile)) * g.Hq;
+  const int rows = (int)std::min<int64_t>(1024, std::max<int64_t>(1, 4 * (int64_t)sms / units));
+  if (n_q == 0) return std::max(packed, rows);
+  return score_tc_packs(g, n_q) ? packed : rows;
 }
 
 cudaError_t launch_score_fwd_tc(ScoreArgs& s, cudaStream_t st) {
   const Geometry& g = s.a.g;
-  const bool pack = score_tc_packs(g, s.a.n_q);
-  const int limit = score_tc_parts_limit(g, s.a.n_q), sms = device_sm_count();
+  const int limit = s.n_split, sms = device_sm_count();  // parts that the workspace has room for
+  const bool pack = score_tc_packs(g, s.a.n_q) && limit >= 2;
   ScoreFwdParams p;
   p.n_tiles = (s.a.n_q + kTile - 1) / kTile;
   p.n_pairs = pack ? 1 : (p.n_tiles + 1) / 2;

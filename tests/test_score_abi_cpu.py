@@ -44,6 +44,22 @@ def test_score_attn_refusals(lib, pool):
     assert lib.oomb_workspace_size(pool, 17, 128) == 0
 
 
+@pytest.mark.parametrize("heads,dtype,d,P", [((28, 4), 0, 128, 128), ((2, 1), 1, 64, 64), ((300, 1), 0, 128, 128),
+                                             ((40, 40), 0, 96, 32), ((4000, 2000), 0, 128, 128)])
+def test_a_workspace_serves_every_smaller_call(lib, heads, dtype, d, P):
+    """The sizes grow with n_q although fewer rows are cut into more parts."""
+    de = _lib.PoolDesc()
+    de.n_q_heads, de.n_kv_heads, de.head_dim, de.page_size = *heads, d, P
+    de.num_phys_pages, de.max_logical_pages, de.dtype = 4, 8, dtype
+    for i, f in enumerate(["k_pool", "v_pool", "dk_pool", "dv_pool", "summary", "page_table", "error_word"]):
+        setattr(de, f, (1 << 20) * (i + 1))
+    h = L.oomb_pool_create(de)
+    for op in (L.OOMB_OP_SCORE_FWD, L.OOMB_OP_SCORE_BWD):
+        sizes = [L.oomb_workspace_size(h, op, n) for n in [*range(1, 300), 513, 1000, 4097, 8192, 100000]]
+        assert sizes == sorted(sizes)
+    L.oomb_pool_destroy(h)
+
+
 def test_doc_spans_refusals(lib):
     f = lib.oomb_doc_spans
     assert f(None, None, 1, 0, 4, F, F, None) == ARG
