@@ -247,3 +247,33 @@ def test_refusals():
         L.oomb_block_norm_bwd(t["x"], t["y"], o, du=t["du"], rstd_pre=torch.ones(4, device="cuda"), w_pre=t["w_pre"],
                               workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 9
+
+
+def test_graph_replay_on_a_side_stream():
+    t = {k: None if v is None else v.cuda() for k, v in make(1400, 512, BF, "token", True, seed=8).items()}
+    x_out, u, dx, dy = (torch.empty_like(t["x"]) for _ in range(4))
+    r = [torch.empty(1400, device="cuda") for _ in range(2)]
+    dw = [torch.empty(512, device="cuda") for _ in range(2)]
+    dg = torch.empty_like(t["x"])
+    ws = torch.empty(L.oomb_block_norm_workspace(1400, 512), dtype=torch.uint8, device="cuda")
+    par = dict(w_pre=t["w_pre"], w_post=t["w_post"], gate=t["gate"], res_scale=0.7, rstd_pre=r[0], rstd_post=r[1])
+
+    def step():
+        L.oomb_block_norm_fwd(t["x"], t["y"], x_out, u, **par)
+        L.oomb_block_norm_bwd(t["x"], t["y"], dx, dy, du=t["du"], dx_out=t["dx_out"], dw_pre=dw[0], dw_post=dw[1],
+                              dgate=dg, workspace=ws, **par)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    first = [v.clone() for v in (x_out, u, dx, dy, *dw, dg)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for v in (x_out, u, dx, dy, *dw, dg):
+        v.zero_()
+    g.replay()
+    for a, b in zip(first, (x_out, u, dx, dy, *dw, dg)):
+        assert torch.equal(a, b)

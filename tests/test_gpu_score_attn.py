@@ -320,3 +320,139 @@ def test_refusals():
     assert e.value.status == 9
     L.oomb_check(h)
     c.pool.close()
+
+
+def test_other_stream_and_graph_replay():
+    """Forward and backward on a side stream, and captured once and replayed on other inputs;
+    two graphs with a workspace each, replayed at the same time."""
+    kw = dict(TC, total=800, n_q=290, Hq=4, Hkv=2, cap=12.0, bias=True, mask="docs", sel="all")
+    eager = []
+    for seed in (1, 2):
+        c = Case(seed=seed, **kw)
+        o, lse = c.forward()
+        dq = c.backward(o, lse)
+        eager.append((o, lse, dq, *[t.clone() for t in c.pool.logical_grads(c.total)]))
+        c.pool.close()
+    side = torch.cuda.Stream()
+    graphs = []
+    for seed in (1, 2):
+        c = Case(seed=seed, **kw)
+        do, out = c.do.cuda(), {}
+        ws = [c.pool.workspace(op, c.n_q) for op in (L.OOMB_OP_SCORE_FWD, L.OOMB_OP_SCORE_BWD)]
+        out["o"], out["dq"] = torch.empty_like(c.dq_in), torch.empty_like(c.dq_in)
+        out["lse"] = torch.empty(4, c.n_q, device="cuda")
+
+        def step(c=c, do=do, out=out, ws=ws):
+            c.pool.dk_pool.zero_()
+            c.pool.dv_pool.zero_()
+            a = (c.dsel, c.cnt, c.scale)
+            L.oomb_score_attn_fwd(c.pool.handle, c.dq_in, c.q_start, *a, out["o"], out["lse"], ws[0], **c.mod)
+            L.oomb_score_attn_bwd(c.pool.handle, c.dq_in, out["o"], do, out["lse"], c.q_start, *a, out["dq"], ws[1],
+                                  **c.mod)
+
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()  # on the side stream, eagerly
+        side.synchronize()
+        assert torch.equal(out["o"], eager[seed - 1][0])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        graphs.append((g, c, out))
+    for _ in range(3):
+        for g, c, out in graphs:
+            out["o"].zero_(), out["dq"].zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graphs[0][0].replay()
+        graphs[1][0].replay()
+        torch.cuda.synchronize()
+        for (g, c, out), ref in zip(graphs, eager):
+            assert torch.equal(out["o"], ref[0]) and torch.equal(out["lse"], ref[1])
+            dk, dv = c.pool.logical_grads(c.total)
+            assert torch.equal(dk, ref[3]) and torch.equal(dv, ref[4])
+            # dq is summed in no fixed order: a few fp32 additions apart, then one rounding
+            assert (out["dq"].float() - ref[2].float()).norm() <= 2.0 ** -8 * ref[2].float().norm()
+    # the same graph on other queries
+    g, c, out = graphs[0]
+    c.q = torch.flip(c.q, (0,)).contiguous()
+    c.dq_in.copy_(c.q)
+    g.replay()
+    assert L.oomb_check(c.pool.handle) == 0
+    ref = c.reference(False)
+    check("o", out["o"], ref)
+    for g, c, out in graphs:
+        c.pool.close()
+
+
+def test_offload_pool_matches_resident():
+    """K/V and gradients in host memory: the staged blocks give the resident pool's bits."""
+    kw = dict(TC, total=900, n_q=260, q_start=640, Hq=4, Hkv=2, cap=9.0, bias=True, mask="docs")
+    c = Case(**kw)
+    o, lse = c.forward()
+    c.backward(o, lse)
+    dk, dv = (t.clone() for t in c.pool.logical_grads(c.total))
+    n_pages = -(-c.total // c.P)
+    width = c.dsel.shape[1]
+    off = PagedKVPool(4, 2, 128, 128, n_pages, n_pages, BF, "cuda", page_order=c.order, offload=True,
+                      stage_max_sel=width, offload_grads=True)
+    h = off.handle
+    L.oomb_kv_append(h, c.k.cuda(), c.v.cuda(), 0)
+    L.oomb_prefetch(h, c.dsel, c.cnt, 1)
+    L.oomb_grad_prefetch(h, c.dsel, c.cnt, None, None, 1)
+    L.oomb_pool_set_stage(h, 1)
+    o2, lse2, dq2 = torch.empty_like(o), torch.empty_like(lse), torch.empty_like(o)
+    ws = off.workspace(L.OOMB_OP_SCORE_FWD, c.n_q)
+    a = (c.dsel, c.cnt, c.scale)
+    L.oomb_score_attn_fwd(h, c.dq_in, c.q_start, *a, o2, lse2, ws, **c.mod)
+    L.oomb_score_attn_bwd(h, c.dq_in, o2, c.do.cuda(), lse2, c.q_start, *a, dq2,
+                          off.workspace(L.OOMB_OP_SCORE_BWD, c.n_q), **c.mod)
+    L.oomb_grad_writeback(h, c.dsel, c.cnt, 1)
+    assert L.oomb_check(h) == 0 and L.oomb_check(c.pool.handle) == 0
+    dk2, dv2 = off.logical_grads(c.total)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert torch.equal(dk.cpu(), dk2.cpu()) and torch.equal(dv.cpu(), dv2.cpu())
+    off.close()
+    c.pool.close()
+
+
+def test_one_workspace_for_calls_of_every_size():
+    """A workspace of the largest call serves the smaller ones, which cut their keys finer."""
+    big = Case(sel="all", total=2000, n_q=700, Hq=14, Hkv=2, cap=10.0, **TC)
+    ws = big.pool.workspace(L.OOMB_OP_SCORE_FWD, 700)
+    for n in (1, 9, 18, 100, 256, 300, 700):
+        q = big.dq_in[:n].contiguous()
+        o = torch.full_like(q, float("nan"))
+        lse = torch.full((14, n), float("nan"), device="cuda")
+        guard = ws.clone().fill_(7)
+        L.oomb_score_attn_fwd(big.pool.handle, q, big.q_start, big.dsel, big.cnt, big.scale, o, lse, guard, softcap=10.0)
+        ref = score_attn(big.q[:n], big.k, big.v, [[p for p in r if p * 128 < big.q_start + n] for r in big.sel], 128,
+                         big.q_start, big.scale, 10.0)
+        if n < 700:  # pages of the full chunk are past this call's view: flagged
+            with pytest.raises(L.OombError):
+                L.oomb_check(big.pool.handle)
+        check("o", o, ref)
+        check("lse", lse, ref)
+    big.pool.close()
+
+
+def test_rows_behind_the_last_and_buffers_around_are_left_alone():
+    """Nothing is written outside O, LSE, dq and the touched pages."""
+    c = Case(sel="own", total=700, n_q=77, q_start=560, Hq=4, Hkv=2, cap=5.0, **TC)
+    pad = 4
+    box = torch.full((c.n_q + 2 * pad, 4, 128), 3.0, dtype=BF, device="cuda")
+    lbox = torch.full((4 * c.n_q + 64,), 3.0, device="cuda")
+    o, lse = box[pad:pad + c.n_q], lbox[32:32 + 4 * c.n_q].view(4, c.n_q)
+    L.oomb_score_attn_fwd(c.pool.handle, c.dq_in, c.q_start, c.dsel, c.cnt, c.scale, o, lse,
+                          c.pool.workspace(L.OOMB_OP_SCORE_FWD, c.n_q), **c.mod)
+    qbox = torch.full_like(box, 3.0)
+    L.oomb_score_attn_bwd(c.pool.handle, c.dq_in, o, c.do.cuda(), lse, c.q_start, c.dsel, c.cnt, c.scale,
+                          qbox[pad:pad + c.n_q], c.pool.workspace(L.OOMB_OP_SCORE_BWD, c.n_q), **c.mod)
+    assert L.oomb_check(c.pool.handle) == 0
+    for b in (box, qbox):
+        assert (b[:pad] == 3).all() and (b[-pad:] == 3).all()
+    assert (lbox[:32] == 3).all() and (lbox[-32:] == 3).all()
+    dk, dv = c.pool.logical_grads(c.total)
+    first = min(c.sel[0]) * 128
+    assert not dk[:first].any() and not dv[:first].any() and not dk[637:].any() and not dv[637:].any()
+    c.pool.close()
