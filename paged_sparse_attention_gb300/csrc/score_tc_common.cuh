@@ -56,13 +56,5 @@ __device__ __forceinline__ float tanh_of(float S, const CapConst& c) {
   if constexpr (F == kDegree2) return S * fmaf(fmaf(c.poly2[2], z, c.poly2[1]), z, c.poly2[0]);
   return S * fmaf(fmaf(fmaf(c.poly3[3], z, c.poly3[2]), z, c.poly3[1]), z, c.poly3[0]);
 }
-// A form that holds for every |S| <= amax (NaN: the wide one).
-__device__ __forceinline__ TanhForm tanh_form(float amax, const CapConst& c) {
-  return amax <= c.edge2 ? kDegree2 : amax <= c.edge3 ? kDegree3 : kWide;
-}
-__device__ __forceinline__ float tanh_any(float S, const CapConst& c) {
-  const TanhForm f = tanh_form(fabsf(S), c);
-  return f == kDegree2 ? tanh_of<kDegree2>(S, c) : f == kDegree3 ? tanh_of<kDegree3>(S, c) : tanh_of<kWide>(S, c);
-}
 
 }  // namespace oomb

@@ -35,8 +35,7 @@ constexpr int kVStages = 3;  // two used by the rows layout; the packed one has 
 constexpr int kThreads = 576;
 constexpr int kTileWarps = 8;  // softmax warps of a tile
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O is rescaled when the row maximum grows by more
-constexpr float kGentle = 0.35f;           // log2 units a token: the bias changes by less than 45 over a page
-constexpr float kNarrowScores = 20.0f;     // log2 units: capped scores of this size differ by less than 40
+constexpr float kNear = 90.0f;             // log2 units: 2^-90 and what is 2^-36 of it are fp32 numbers
 constexpr float kNothing = -127.0f;        // log2 units: 2^x is zero in fp32 with flushed denormals
 
 struct ScoreFwdParams {
@@ -487,37 +486,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(tS + half * 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
       tmem_ld32(tS + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
       tmem_wait_ld();
-      // ref: no less than the largest score of this half row.  `direct` (every key visible; a
-      // bias that is linear and gentle over the page; a cap whose argument is small): it is
-      // also within about 2^90 of it, so that P = 2^(score - m) neither overflows nor loses
-      // what counts, and the scores are formed inside the exponent from one pass over the raw
-      // dot products.  `nothing`: that far below the row's maximum every P is zero in fp32.
+      // ref: no less than the largest score of this half row, from one pass over the raw dot
+      // products.  `direct` (every key visible, a bias linear over the page): the scores are
+      // formed inside the exponent, P = 2^(score - m).  That needs an m within about 2^90 of the
+      // row's largest score, so that no P that counts is lost: either ref is that near (kNear),
+      // or it does not raise the m of the pages before.  `nothing`: every P is zero in fp32.
       // Elsewhere the scores are formed in place, in log2 units, and ref is their maximum.
       const float f0 = BIAS ? (float)(qpos - p0) : 0.f;  // distance of key column c: |f0 - c|
       const float b0 = -slope2 * f0;
       const bool behind = BIAS && __all_sync(0xffffffffu, f0 >= 64.f);  // every key behind its row: linear in c
-      bool direct = whole && (!BIAS || (behind && __all_sync(0xffffffffu, fabsf(slope2) <= kGentle)));
       TanhForm form = kWide;
-      float ref;
+      float ref, spread = 0.f;  // spread: how far ref may be above the largest score
       if constexpr (CAP) {
         const float amax = row_reduce(sr, [](float u, float v, float w) { return fmax3_abs(u, v, w); });
         form = __all_sync(0xffffffffu, amax <= p.cap.edge2)   ? kDegree2
                : __all_sync(0xffffffffu, amax <= p.cap.edge3) ? kDegree3
                                                               : kWide;
-        ref = fabsf(p.cap.cap2 * tanh_any(amax, p.cap));
-        if (direct && !__all_sync(0xffffffffu, ref <= kNarrowScores)) {  // the largest score itself
-          direct = p.cap.arg >= 0.f;
-          if (direct)
-            ref = p.cap.cap2 * tanh_any(row_reduce(sr, [](float u, float v, float w) { return fmax3(u, v, w); }), p.cap);
-        }
+        ref = fminf(fabsf(p.scale_log2) * amax, p.cap.cap2);  // |cap tanh(x)| <= |cap x|, cap
+        spread = 2.f * ref;
       } else {
-        ref = p.scale_log2 * row_reduce(sr, [](float u, float v, float w) { return fmax3(u, v, w); });
-        if (p.scale_log2 < 0.f) {
-          ref = INFINITY;
-          direct = false;
-        }
+        const float top = row_reduce(sr, [](float u, float v, float w) { return fmax3(u, v, w); });
+        ref = p.scale_log2 >= 0.f ? p.scale_log2 * top : INFINITY;
       }
-      if constexpr (BIAS) ref += fmaxf(b0, fmaf(slope2, 63.f, b0));
+      if constexpr (BIAS) {
+        ref += fmaxf(b0, fmaf(slope2, 63.f, b0));
+        spread = fmaf(fabsf(slope2), (float)kTile, spread);
+      }
+      const bool direct = whole && (!BIAS || behind) && (CAP || p.scale_log2 >= 0.f) &&
+                          __all_sync(0xffffffffu, spread <= kNear || ref <= m + kRescaleThreshold);
       const bool nothing = behind && __all_sync(0xffffffffu, ref - m < kNothing);
       if (!direct && !nothing) {
         if constexpr (CAP) {
@@ -582,29 +578,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto pair_of = [&](int c) { return f32x2(sr[2 * c], sr[2 * c + 1]); };
         // what the exponent adds to a score: -m, and in the direct case the bias
         const float b0m = b0 + neg_m;
-        const uint64_t step = f32x2(2.f * slope2, 2.f * slope2);
-        uint64_t shift = negm2;
-        auto next_shift = [&](int c) {
-          if constexpr (BIAS) {
-            if (c % 8 == 0)  // restart: the running sum gathers no more than 8 roundings
-              shift = f32x2(fmaf(slope2, (float)(2 * c), b0m), fmaf(slope2, (float)(2 * c + 1), b0m));
-            else
-              shift = fadd2(shift, step);
-          }
-          return shift;
+        auto shift = [&](int c) {
+          return BIAS ? f32x2(fmaf(slope2, (float)(2 * c), b0m), fmaf(slope2, (float)(2 * c + 1), b0m)) : negm2;
         };
         if (!direct) {
           exponentials([&](int c, float& t0, float& t1) { f32x2_split(fadd2(pair_of(c), negm2), t0, t1); });
         } else if constexpr (!CAP) {
           const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2);
-          exponentials([&](int c, float& t0, float& t1) { f32x2_split(ffma2(pair_of(c), sc2, next_shift(c)), t0, t1); });
+          exponentials([&](int c, float& t0, float& t1) { f32x2_split(ffma2(pair_of(c), sc2, shift(c)), t0, t1); });
         } else if (form == kDegree2) {
           const float* q = p.cap.poly2;
           const float k2 = p.cap.cap2;
           const uint64_t q0 = f32x2(q[0] * k2, q[0] * k2), q1 = f32x2(q[1] * k2, q[1] * k2), q2 = f32x2(q[2] * k2, q[2] * k2);
           exponentials([&](int c, float& t0, float& t1) {
             const uint64_t S = pair_of(c), z = fmul2(S, S);
-            f32x2_split(ffma2(S, ffma2(ffma2(q2, z, q1), z, q0), next_shift(c)), t0, t1);
+            f32x2_split(ffma2(S, ffma2(ffma2(q2, z, q1), z, q0), shift(c)), t0, t1);
           });
         } else if (form == kDegree3) {
           const float* q = p.cap.poly3;
@@ -613,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          q2 = f32x2(q[2] * k2, q[2] * k2), q3 = f32x2(q[3] * k2, q[3] * k2);
           exponentials([&](int c, float& t0, float& t1) {
             const uint64_t S = pair_of(c), z = fmul2(S, S);
-            f32x2_split(ffma2(S, ffma2(ffma2(ffma2(q3, z, q2), z, q1), z, q0), next_shift(c)), t0, t1);
+            f32x2_split(ffma2(S, ffma2(ffma2(ffma2(q3, z, q2), z, q1), z, q0), shift(c)), t0, t1);
           });
         } else {  // cap2 tanh(x) = cap2 - 2 cap2 / (1 + e^2x)
           const uint64_t k2 = f32x2(p.cap.cap2, p.cap.cap2), one = f32x2(1.f, 1.f);
@@ -622,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float e0, e1;
             f32x2_split(fmul2(pair_of(c), arg2), e0, e1);
             f32x2_split(fadd2(f32x2(ex2_approx(e0), ex2_approx(e1)), one), e0, e1);
-            f32x2_split(ffma2(f32x2(rcp_approx(e0), rcp_approx(e1)), m2k, fadd2(next_shift(c), k2)), t0, t1);
+            f32x2_split(ffma2(f32x2(rcp_approx(e0), rcp_approx(e1)), m2k, fadd2(shift(c), k2)), t0, t1);
           });
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
