@@ -31,17 +31,18 @@ constexpr int kMaxWidth = 16384;
 // Sum over the block; every thread gets it.  `buf` holds 2 x 32 floats, used in turns so that
 // one barrier a sum is enough; the warps' sums are read as vectors by every thread (a second
 // round of shuffles would wait five times as long).
+// WARPS: the most warps the block may have (a multiple of 4).
+template <int WARPS>
 __device__ __forceinline__ float block_sum(float v, float* buf, int& turn) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  const int warps = blockDim.x / 32;
-  if (warps == 1) return v;
   float* b = buf + 32 * turn;
   turn ^= 1;
   if (threadIdx.x % 32 == 0) b[threadIdx.x / 32] = v;
   __syncthreads();
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int w = 0; w < warps; w += 4) {  // the entries behind the last warp stay 0
+#pragma unroll
+  for (int w = 0; w < WARPS; w += 4) {  // the entries behind the last warp stay 0
     const float4 x = *reinterpret_cast<const float4*>(b + w);
     t.x += x.x;
     t.y += x.y;
@@ -53,7 +54,8 @@ __device__ __forceinline__ float block_sum(float v, float* buf, int& turn) {
 // Before the first sum: no barrier of its own, the first sum's writes come before its barrier
 // and touch other entries.
 __device__ __forceinline__ void clear_sums(float* buf) {
-  if (threadIdx.x < 64 && threadIdx.x % 32 >= blockDim.x / 32) buf[threadIdx.x] = 0.f;
+  for (int i = threadIdx.x; i < 64; i += blockDim.x)
+    if (i % 32 >= (int)blockDim.x / 32) buf[i] = 0.f;
 }
 
 // E consecutive elements as fp32, and back with one rounding.
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(1024, 1) norm_fwd(const __grid_constant__ Norm
         sh.param(a.w_post, w);
 #pragma unroll
         for (int e = 0; e < E; ++e) s += r[e] * r[e];
-        const float rstd = rsqrtf(block_sum(s, buf, turn) * a.inv_D + a.eps);
+        const float rstd = rsqrtf(block_sum<32>(s, buf, turn) * a.inv_D + a.eps);
         if (a.rstd_post && threadIdx.x == 0) a.rstd_post[row] = rstd;
 #pragma unroll
         for (int e = 0; e < E; ++e) r[e] *= rstd * w[e];
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(1024, 1) norm_fwd(const __grid_constant__ Norm
       sh.param(a.w_pre, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) s += f[e] * f[e];
-      const float rstd = rsqrtf(block_sum(s, buf, turn) * a.inv_D + a.eps);
+      const float rstd = rsqrtf(block_sum<32>(s, buf, turn) * a.inv_D + a.eps);
       if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[row] = rstd;
 #pragma unroll
       for (int e = 0; e < E; ++e) w[e] *= f[e] * rstd;
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(1024, 1) norm_bwd(const __grid_constant__ Norm
         t[e] *= w[e];
         s += t[e] * xn[e];
       }
-      const float mean = block_sum(s, buf, turn) * a.inv_D;
+      const float mean = block_sum<32>(s, buf, turn) * a.inv_D;
 #pragma unroll
       for (int e = 0; e < E; ++e) dx[e] += r_pre * (t[e] - xn[e] * mean);
     }
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(1024, 1) norm_bwd(const __grid_constant__ Norm
     }
     if (row_gate && a.dgate) sh.template store<T>(reinterpret_cast<T*>(a.dgate) + row0, dg);
     if (a.w_post) {
-      const float mean = block_sum(s, buf, turn) * a.inv_D;
+      const float mean = block_sum<32>(s, buf, turn) * a.inv_D;
 #pragma unroll
       for (int e = 0; e < E; ++e) dx[e] = r_post * (dx[e] - z[e] * mean);
     }
@@ -276,26 +278,29 @@ __global__ void __launch_bounds__(1024, 1) norm_bwd(const __grid_constant__ Norm
   }
 }
 
-// Column sums over the blocks' parts, in block order: 32 columns a block, 8 strips of the
-// parts each, the strips joined in order.  out[k] is dw_pre, dw_post or dgate (or nullptr).
-__global__ void __launch_bounds__(256) norm_join(const float* __restrict__ part, int n_parts, int D, float* dw_pre,
-                                                 float* dw_post, float* dgate, int accumulate) {
-  __shared__ float strip[8][33];
+// Column sums over the blocks' parts, in block order: 32 columns a block, 16 strips of the
+// parts, one a warp, the strips joined in order.  out is dw_pre, dw_post or dgate (or nullptr).
+constexpr int kStrips = 16;
+__global__ void __launch_bounds__(32 * kStrips) norm_join(const float* __restrict__ part, int n_parts, int D,
+                                                          float* dw_pre, float* dw_post, float* dgate,
+                                                          int accumulate) {
+  __shared__ float strip[kStrips][33];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32, k = blockIdx.y;
   const int c = blockIdx.x * 32 + lane;
   float* out = k == 0 ? dw_pre : k == 1 ? dw_post : dgate;
   if (!out) return;
-  const int p0 = n_parts * w / 8, p1 = n_parts * (w + 1) / 8;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead: the parts are written from here on
+  const int p0 = n_parts * w / kStrips, p1 = n_parts * (w + 1) / kStrips;
   float s = 0.f;
   if (c < D)
-#pragma unroll 8
+#pragma unroll 10
     for (int p = p0; p < p1; ++p) s += part[((size_t)p * 3 + k) * D + c];
   strip[w][lane] = s;
   __syncthreads();
   if (w == 0 && c < D) {
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += strip[i][lane];
+    for (int i = 0; i < kStrips; ++i) s += strip[i][lane];
     out[c] = accumulate ? out[c] + s : s;
   }
 }
@@ -454,7 +459,7 @@ __global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
         uint64_t s = 0;
 #pragma unroll
         for (int e = 0; e < H; ++e) s = fma2(r[e], r[e], s);
-        rstd = rsqrtf(block_sum(halves(s), buf, turn) * a.inv_D + a.eps);
+        rstd = rsqrtf(block_sum<16>(halves(s), buf, turn) * a.inv_D + a.eps);
         if (a.rstd_post && threadIdx.x == 0) a.rstd_post[row] = rstd;
       }
       const uint64_t rs = both(rstd);
@@ -466,7 +471,7 @@ __global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
       uint64_t s = 0;
 #pragma unroll
       for (int e = 0; e < H; ++e) s = fma2(f[e], f[e], s);
-      const float rstd = rsqrtf(block_sum(halves(s), buf, turn) * a.inv_D + a.eps);
+      const float rstd = rsqrtf(block_sum<16>(halves(s), buf, turn) * a.inv_D + a.eps);
       if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[row] = rstd;
       const uint64_t rs = both(rstd);
       if (in) {
@@ -565,7 +570,7 @@ __global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
         }
       }
       // xn mean(t xn) r_pre = x' r_pre^3 sum(t x') / D
-      const float sum = block_sum(halves(s), buf, turn) * a.inv_D;
+      const float sum = block_sum<16>(halves(s), buf, turn) * a.inv_D;
       const uint64_t m2 = both(-(r_pre * r_pre * r_pre) * sum);
 #pragma unroll
       for (int e = 0; e < H; ++e) dx[e] = fma2(xo[e], m2, fma2(t[e], r2, dx[e]));
@@ -588,7 +593,7 @@ __global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
     }
     if (ROWGATE && a.dgate && in) store2<T, E>(reinterpret_cast<T*>(a.dgate) + at, t);
     if (post) {
-      const float mean = block_sum(halves(s), buf, turn) * a.inv_D;
+      const float mean = block_sum<16>(halves(s), buf, turn) * a.inv_D;
       const uint64_t m2 = both(-r_post * mean);
 #pragma unroll
       for (int e = 0; e < H; ++e) dx[e] = fma2(yn[e], m2, mul2(dx[e], rp2));
@@ -738,9 +743,18 @@ cudaError_t bwd(const NormArgs& a, cudaStream_t st) {
   count_launches(1);
   float* dgate = a.gate && !a.gate_rows ? reinterpret_cast<float*>(a.dgate) : nullptr;
   if (a.dw_pre || a.dw_post || dgate) {
-    norm_join<<<dim3((a.D + 31) / 32, 3), 256, 0, st>>>(a.part, (int)grid, a.D, a.dw_pre, a.dw_post, dgate,
-                                                        a.accumulate);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.D + 31) / 32, 3);
+    cfg.blockDim = dim3(32 * kStrips);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;  // a dependent launch: its set-up overlaps the end of the row kernel
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
     count_launches(1);
+    return cudaLaunchKernelEx(&cfg, norm_join, (const float*)a.part, (int)grid, a.D, a.dw_pre, a.dw_post, dgate,
+                              a.accumulate);
   }
   return cudaGetLastError();
 }
