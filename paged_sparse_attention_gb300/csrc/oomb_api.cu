@@ -554,7 +554,8 @@ static oomb_status make_score_args(oomb_pool* p, const void* q, int64_t q_start,
   s->total = p->n_tokens;
   s->n_split = 1;
   if (mod) {
-    if (!(mod->softcap >= 0.f) || std::isinf(mod->softcap)) return OOMB_ERR_ARG;
+    if (!(mod->softcap >= 0.f) || mod->softcap > 1e30f) return OOMB_ERR_ARG;
+    if (mod->softcap > 0.f && !(std::fabs((double)scale) / mod->softcap <= 1e30)) return OOMB_ERR_ARG;
     if (!aligned(mod->slopes, 4) || !aligned(mod->key_begin, 8) || !aligned(mod->key_end, 8)) return OOMB_ERR_ALIGN;
     s->cap = mod->softcap;
     s->slopes = mod->slopes;

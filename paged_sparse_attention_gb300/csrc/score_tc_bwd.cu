@@ -20,6 +20,8 @@
 // owner, warps 2-9 softmax (thread = key row, 32 of a half's 64 query columns) and epilogue,
 // warps 10-13 dQ read-out.  TMEM columns: half a [0,128), half b [128,256): S^T, dP^T, then
 // packed P^T and dA^T over S^T and dQ^T over dP^T; dV [256,384); dK [384,512).
+#include <type_traits>
+
 #include "score_tc_common.cuh"
 
 namespace oomb {
@@ -48,13 +50,13 @@ struct TileSpan {
 struct ScoreBwdParams {
   ScoreArgs s;
   CapConst cap;
-  const float* lse2;       // [Hq, n_pad] LSE * log2(e) - cap2, +inf on rows without keys and padded rows
+  const float* lse2;       // [Hq, n_pad] LSE * log2(e) (kWideCap: - cap2), +inf on rows without keys and padded rows
   const float* Dbuf;       // [Hq, n_pad] rowsum(dO * O), 0 on padded rows
   const longlong2* span;   // [n_pad] key range of each row
   const TileSpan* tiles;   // [n_tiles]
   float* dq_acc;
   int n_pad, n_tiles, n_split;
-  float scale_da, scale_log2;  // scale_da: of what dK and dQ are summed from (4 scale under a cap)
+  float scale_da, scale_log2;  // scale_da: of what dK and dQ are summed from (kWideCap: 4 scale)
 };
 
 struct __align__(8) BwdBarriers {
@@ -106,7 +108,15 @@ __device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
   return x;
 }
 
-template <bool CAP, bool BIAS>
+// How the cap's tanh is formed.  kWideCap: r = 1 / (1 + e^2x) alone; the score cap (1 - 2 r) is
+// then off by about 2^-23 cap, whose constant is folded into lse2, and 1 - tanh^2 = 4 (r - r^2),
+// whose factor is left to scale_da.  One form for every x: a polynomial for small x beside it
+// costs more in instruction cache than it saves (8K chunk: 7.11 against 7.59 ms).  kLargeCap, for
+// caps above kCapLimit, where that error would count: the polynomial where all |x| are small.
+enum CapForm { kNoCap, kWideCap, kLargeCap };
+constexpr float kCapLimit = 256.0f;  // error of a score at most 2^-15, of P then 2^-15 of it
+
+template <CapForm CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
     score_bwd_tc(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tdo,
                  const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -349,31 +359,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float f0 = BIAS ? (float)(a.q_start + q0 - kpos) : 0.f;  // distance of column i: |f0 + i|
         uint32_t pk[16], dk[16];
-        // P and dA of the columns, four at a time.  Capped: with r = 1 / (1 + e^2x) the score is
-        // cap (1 - 2 r), whose constant is in lse2 already, and 1 - tanh^2 = 4 (r - r^2), whose
-        // factor is left to scale_da (one form for every x: a polynomial for small x beside it
-        // costs more in instruction cache than the two reciprocal-exponential steps)
+        // P and dA of the columns, four at a time
+        auto columns = [&](auto small) {
 #pragma unroll
-        for (int c4 = 0; c4 < 8; ++c4) {
-          const float4 L = vs4[c4], Dv = vs4[16 + c4];
-          const float l4[4] = {L.x, L.y, L.z, L.w}, d4[4] = {Dv.x, Dv.y, Dv.z, Dv.w};
-          float pr[4], dar[4];
+          for (int c4 = 0; c4 < 8; ++c4) {
+            const float4 L = vs4[c4], Dv = vs4[16 + c4];
+            const float l4[4] = {L.x, L.y, L.z, L.w}, d4[4] = {Dv.x, Dv.y, Dv.z, Dv.w};
+            float pr[4], dar[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = 4 * c4 + e;
-            const float S = __uint_as_float(sr[i]);
-            float shift = -l4[e], r = 0.f;
-            if (BIAS) shift = fmaf(-slope2, fabsf(f0 + (float)i), shift);
-            if constexpr (CAP) r = rcp_approx(1.f + ex2_approx(p.cap.arg * S));
-            pr[e] = ex2_approx(CAP ? fmaf(r, -2.f * p.cap.cap2, shift) : fmaf(S, p.scale_log2, shift));
-            dar[e] = pr[e] * (__uint_as_float(dr[i]) - d4[e]);
-            if constexpr (CAP) dar[e] *= fmaf(-r, r, r);
+            for (int e = 0; e < 4; ++e) {
+              const int i = 4 * c4 + e;
+              const float S = __uint_as_float(sr[i]);
+              float shift = -l4[e], s2, gate = 1.f;
+              if (BIAS) shift = fmaf(-slope2, fabsf(f0 + (float)i), shift);
+              if constexpr (CAP == kWideCap) {
+                const float r = rcp_approx(1.f + ex2_approx(p.cap.arg * S));
+                s2 = fmaf(r, -2.f * p.cap.cap2, shift);
+                gate = fmaf(-r, r, r);
+              } else if constexpr (CAP == kLargeCap) {
+                const float th = tanh_of<decltype(small)::value ? kDegree3 : kWide>(S, p.cap);
+                s2 = fmaf(th, p.cap.cap2, shift);
+                gate = fmaf(-th, th, 1.f);
+              } else {
+                s2 = fmaf(S, p.scale_log2, shift);
+              }
+              pr[e] = ex2_approx(s2);
+              dar[e] = pr[e] * (__uint_as_float(dr[i]) - d4[e]);
+              if constexpr (CAP != kNoCap) dar[e] *= gate;
+            }
+            pk[2 * c4] = pack_bf16x2(pr[0], pr[1]);
+            pk[2 * c4 + 1] = pack_bf16x2(pr[2], pr[3]);
+            dk[2 * c4] = pack_bf16x2(dar[0], dar[1]);
+            dk[2 * c4 + 1] = pack_bf16x2(dar[2], dar[3]);
           }
-          pk[2 * c4] = pack_bf16x2(pr[0], pr[1]);
-          pk[2 * c4 + 1] = pack_bf16x2(pr[2], pr[3]);
-          dk[2 * c4] = pack_bf16x2(dar[0], dar[1]);
-          dk[2 * c4 + 1] = pack_bf16x2(dar[2], dar[3]);
+        };
+        bool small = false;
+        if constexpr (CAP == kLargeCap) {
+          float amax = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) amax = fmax3_abs(amax, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+          small = __all_sync(0xffffffffu, amax <= p.cap.edge3);
         }
+        if (CAP == kLargeCap && small)
+          columns(std::true_type{});
+        else
+          columns(std::false_type{});
         if (masked) {  // cleared afterwards, in the packed words, whatever came out for a pair that is not seen
 #pragma unroll
           for (int w = 0; w < 16; ++w) {
@@ -541,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Blocks [0, n_tiles): the row ranges of one query tile.  The others, one warp per (row, head)
 // of the padded range: D = rowsum(dO * O) and LSE * log2(e) into [Hq, n_pad] buffers (rows
-// without keys and padded rows: LSE = +inf, so P = 0) and the row of the fp32 dQ accumulator
+// without keys and padded rows: LSE = +inf, so P = 0; cap2 is taken off) and the row of the fp32 dQ accumulator
 // zeroed.
 __global__ void __launch_bounds__(256) score_bwd_prep(const __grid_constant__ ScoreArgs s, float cap2, int n_pad, int n_tiles,
                                                       float* __restrict__ Dbuf, float* __restrict__ lse2,
@@ -643,7 +673,7 @@ cudaLaunchConfig_t cluster_config(cudaLaunchAttribute* attr, unsigned blocks, in
   return cfg;
 }
 
-template <bool CAP, bool BIAS>
+template <CapForm CAP, bool BIAS>
 cudaError_t launch_main(ScoreBwdParams& p, const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
                         const CUtensorMap& tv, cudaStream_t st) {
   static size_t smem_set[kMaxDevices] = {};
@@ -696,8 +726,9 @@ cudaError_t launch_score_bwd_tc(const ScoreArgs& s, cudaStream_t st) {
   float* dq_acc = reinterpret_cast<float*>(take((size_t)a.g.Hq * a.n_q * kD * 4));
   longlong2* span = reinterpret_cast<longlong2*>(take((size_t)n_pad * sizeof(longlong2)));
   TileSpan* tiles = reinterpret_cast<TileSpan*>(take((size_t)n_tiles * sizeof(TileSpan)));
+  const CapForm form = !(s.cap > 0.f) ? kNoCap : s.cap <= kCapLimit ? kWideCap : kLargeCap;
   const int64_t warps = (int64_t)a.n_q * a.g.Hq, warps_pad = (int64_t)n_pad * a.g.Hq;
-  score_bwd_prep<<<(unsigned)(n_tiles + (warps_pad + 7) / 8), 256, 0, st>>>(s, s.cap * kLog2e, n_pad, n_tiles, Dbuf, lse2, dq_acc,
+  score_bwd_prep<<<(unsigned)(n_tiles + (warps_pad + 7) / 8), 256, 0, st>>>(s, form == kWideCap ? s.cap * kLog2e : 0.f, n_pad, n_tiles, Dbuf, lse2, dq_acc,
                                                                            span, tiles);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -715,13 +746,16 @@ cudaError_t launch_score_bwd_tc(const ScoreArgs& s, cudaStream_t st) {
   p.dq_acc = dq_acc;
   p.n_pad = n_pad;
   p.n_tiles = n_tiles;
-  p.scale_da = s.cap > 0.f ? 4.f * a.scale : a.scale;
+  p.scale_da = form == kWideCap ? 4.f * a.scale : a.scale;
   p.scale_log2 = a.scale * kLog2e;
-  if (s.cap > 0.f)
-    e = s.slopes ? launch_main<true, true>(p, tq, tdo, tk, tv, st) : launch_main<true, false>(p, tq, tdo, tk, tv, st);
+  const bool bias = s.slopes != nullptr;
+  if (form == kWideCap)
+    e = bias ? launch_main<kWideCap, true>(p, tq, tdo, tk, tv, st) : launch_main<kWideCap, false>(p, tq, tdo, tk, tv, st);
+  else if (form == kLargeCap)
+    e = bias ? launch_main<kLargeCap, true>(p, tq, tdo, tk, tv, st)
+             : launch_main<kLargeCap, false>(p, tq, tdo, tk, tv, st);
   else
-    e = s.slopes ? launch_main<false, true>(p, tq, tdo, tk, tv, st)
-                 : launch_main<false, false>(p, tq, tdo, tk, tv, st);
+    e = bias ? launch_main<kNoCap, true>(p, tq, tdo, tk, tv, st) : launch_main<kNoCap, false>(p, tq, tdo, tk, tv, st);
   if (e != cudaSuccess) return e;
   score_bwd_convert<<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(dq_acc, a.n_q, a.g.Hq, p.scale_da,
                                                                  reinterpret_cast<__nv_bfloat16*>(a.dq));

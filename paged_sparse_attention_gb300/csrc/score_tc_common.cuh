@@ -36,6 +36,7 @@ inline CapConst make_cap(float cap, float scale) {
   }
   c.edge2 = ak > 0.0 ? (float)(kTanhEdge2 / ak) : INFINITY;
   c.edge3 = ak > 0.0 ? (float)(kTanhEdge3 / ak) : INFINITY;
+  if (ak > 1e4) c.edge2 = c.edge3 = -1.f;  // coefficients (ak^7) out of fp32's range: the wide form only
   c.arg = (float)(2.0 * k * 1.4426950408889634);
   c.cap2 = (float)((double)cap * 1.4426950408889634);
   return c;

@@ -517,9 +517,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool nothing = behind && __all_sync(0xffffffffu, ref - m < kNothing);
       if (!direct && !nothing) {
         if constexpr (CAP) {
+          if (form != kWide) {  // (the wide form is off by 2^-23 of the cap, too much under a large one)
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            sr[c] = __float_as_uint(p.cap.cap2 * tanh_of<kWide>(__uint_as_float(sr[c]), p.cap));
+            for (int c = 0; c < 64; ++c)
+              sr[c] = __float_as_uint(p.cap.cap2 * tanh_of<kDegree3>(__uint_as_float(sr[c]), p.cap));
+          } else {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              sr[c] = __float_as_uint(p.cap.cap2 * tanh_of<kWide>(__uint_as_float(sr[c]), p.cap));
+          }
         } else {
 #pragma unroll
           for (int c = 0; c < 64; ++c) sr[c] = __float_as_uint(p.scale_log2 * __uint_as_float(sr[c]));

@@ -169,6 +169,35 @@ def test_ranges_meet_selections(sel, mask):
     Case(mask=mask, sel=sel, seed=5, total=1400, n_q=390, q_start=700, Hq=4, Hkv=2, **TC).run()
 
 
+@pytest.mark.parametrize("cap", [255.0, 257.0, 1e4, 1e6, 1e30])
+@pytest.mark.parametrize("shape", ["tc_g2_ragged", "tc_few_tokens", "fp32_64"])
+def test_cap_far_above_the_scores(shape, cap):
+    """A cap that hardly bends the scores: held to bounds in which the cap itself has no part
+    (an error of 2^-23 of the cap would not do): the uncapped form, which differs by
+    |s|^3 / (3 cap^2), or above 1e3 not at all."""
+    c = Case(cap=cap, bias=True, mask="docs", sel="all", **SHAPES[shape])
+    c.cap, exact_cap = 0.0, c.cap
+    if cap < 1e3:
+        c.cap = exact_cap
+    c.run()
+
+
+@pytest.mark.parametrize("shape", ["tc_g2_ragged", "tc_few_tokens", "fp32_64"])
+def test_tiny_cap(shape):
+    """Scores that are all but the sign of the dot product; zero queries stay zero."""
+    c = Case(cap=1e-3, **SHAPES[shape])
+    c.q[::2] = 0
+    c.dq_in = c.q.cuda()
+    o, lse = c.forward()
+    dq = c.backward(o, lse)
+    assert L.oomb_check(c.pool.handle) == 0
+    ref = c.reference(False)
+    check("o", o, ref)
+    check("lse", lse, ref)
+    assert torch.isfinite(dq.float()).all()
+    c.pool.close()
+
+
 @pytest.mark.parametrize("mask", ["docs", "random", "empty"])
 def test_more_tiles_than_fit_the_gpu_at_once(mask):
     """Ranges and enough query tiles for several waves of thread blocks."""
@@ -307,7 +336,8 @@ def test_refusals():
     for kw in (dict(q=q.float()), dict(sel=c.dsel.long()), dict(key_end=torch.zeros(40, device="cuda"))):
         with pytest.raises(TypeError):
             call(**kw)
-    for kw in (dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")), dict(q0=261), dict(q0=-1)):
+    for kw in (dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")), dict(softcap=1e31),
+               dict(softcap=1e-35), dict(q0=261), dict(q0=-1)):
         with pytest.raises(L.OombError) as e:
             call(**kw)
         assert e.value.status == 1
