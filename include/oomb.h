@@ -367,10 +367,12 @@ typedef struct {
  *    keys after its own position (a prefix); without it, pages up to the chunk's end.
  *  - pages that no row of a tile can see are not read; where there are few rows the keys are
  *    split over thread blocks, whose parts are joined in a fixed order.
- *  - a selection that is not strictly ascending pages of that view, or a page that is not
- *    mapped, sets OOMB_DEVERR_SEL / OOMB_DEVERR_PAGE; the entry is left out.
+ *  - a page that is not mapped sets OOMB_DEVERR_PAGE and is left out; a selection that is not
+ *    strictly ascending pages of that view sets OOMB_DEVERR_SEL, and what its rows get is not
+ *    defined.
  * K and V must be finite in the pages read: a masked key weighs nothing, but 0 times an
- * infinity or a NaN in V is a NaN.  Workspace: oomb_workspace_size(OOMB_OP_SCORE_FWD, n)
+ * infinity or a NaN in V is a NaN.  Scores are fp32 numbers: a bias of size B is known to
+ * 2^-24 B, which matters to rows whose nearest selected key is far away.  Workspace: oomb_workspace_size(OOMB_OP_SCORE_FWD, n)
  * bytes, n the most rows of any call it serves (n_q or more), contents scratch; two calls
  * that may run at once need one each.
  * Capturable in a CUDA graph (the number of tokens appended is the one at capture).
@@ -385,7 +387,8 @@ OOMB_API oomb_status oomb_score_attn_fwd(oomb_pool* pool, const void* q, int64_t
  * with P = exp(s - LSE), dP = dO V^T, D_i = dO_i . O_i and
  * dA = P (dP - D) (1 - tanh^2(scale q.k / softcap)),
  *   dq = scale dA K (written),  dK_pool += scale dA^T Q,  dV_pool += P^T dO
- * over the G query heads of each KV head.  Masked pairs and rows without keys send nothing;
+ * over the G query heads of each KV head.  Masked pairs and rows without keys send nothing
+ * (q and d_o must be finite in those rows too: they are multiplied by zeros);
  * pages that no row sees are not touched.  dK/dV, their staging (offload_grads) and dq are
  * as in oomb_chunk_attn_bwd: one writer per pool row in a fixed order (the same bits on
  * every run), dq summed in fp32 (tensor-core shapes: in no fixed order, so equal to

@@ -358,7 +358,7 @@ def oomb_bias_rope_axes(x_in, bias, x_out, n_heads: int, positions, pair_axis, t
     a_bias = None if bias is None else _need(f, "bias", bias, bias.shape, torch.float32, dev)
     axes, a_pos, n_axes = None, None, 0
     if mode != 0:
-        axes = bytes(pair_axis)
+        axes = pair_axis if isinstance(pair_axis, bytes) else bytes(list(pair_axis))
         if 2 * len(axes) != d:
             raise ValueError(f"{f}: pair_axis has {len(axes)} entries, needs {d // 2}")
         n_axes = _dims(f, "positions", positions, 2)[0]

@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
       }
       // xn mean(t xn) r_pre = x' r_pre^3 sum(t x') / D
       const float sum = block_sum<16>(halves(s), buf, turn) * a.inv_D;
-      const uint64_t m2 = both(-(r_pre * r_pre * r_pre) * sum);
+      const uint64_t m2 = both(-(r_pre * sum * r_pre) * r_pre);
 #pragma unroll
       for (int e = 0; e < H; ++e) dx[e] = fma2(xo[e], m2, fma2(t[e], r2, dx[e]));
     }

@@ -338,7 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (e < t.n_ring) {
         const int j = entry(PACK ? t.first[e & 1] + (e >> 1) : t.lo + e);
         const int64_t blk = score_block(p.s, h, j, sel_row[j]);
-        bar->kv_row[e % 64] = blk < 0 ? 0 : (int)(blk * kTile);  // a page left out is masked whole: any block will do
+        // a page left out is masked whole and, read from below the pools' first row, all zero
+        bar->kv_row[e % 64] = blk < 0 ? -kTile : (int)(blk * kTile);
       }
       __syncwarp();
       if (lane == 0) {

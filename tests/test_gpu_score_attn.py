@@ -320,6 +320,25 @@ def test_bad_selections_are_flagged_and_left_out():
     c.pool.close()
 
 
+@pytest.mark.parametrize("n_q", [1, 200])
+def test_what_a_page_left_out_holds_does_not_matter(n_q):
+    """An unmapped page in the selection, and NaN in every block of the pools that no page uses."""
+    c = Case(sel="all", total=640, n_q=n_q, Hq=4, Hkv=2, **TC)
+    table = L.oomb_page_table_host(c.pool.handle, 5)
+    gone = min(range(4), key=lambda p: int(table[p]))
+    L.oomb_page_free(c.pool.handle, gone, 1)
+    for pool in (c.pool.k_pool, c.pool.v_pool):
+        pool[[i for i in range(pool.shape[0]) if i not in [int(table[p]) for p in range(5) if p != gone]]] = math.nan
+    o, lse = c.forward()
+    with pytest.raises(L.OombError):
+        L.oomb_check(c.pool.handle)
+    c.sel = [[p for p in r if p != gone] for r in c.sel]
+    ref = c.reference(False)
+    check("o", o, ref)
+    check("lse", lse, ref)
+    c.pool.close()
+
+
 def test_refusals():
     c = Case(total=300, n_q=40, Hq=4, Hkv=2, **TC)
     h, q, o = c.pool.handle, c.dq_in, torch.empty_like(c.dq_in)
