@@ -82,19 +82,6 @@ __device__ __forceinline__ void store_vec(T* p, const float (&f)[E]) {
     *reinterpret_cast<uint4*>(p + i) = w;
   }
 }
-template <int E>
-__device__ __forceinline__ void load_param(const float* p, int c, float (&f)[E], float otherwise) {
-#pragma unroll
-  for (int i = 0; i < E; i += 4) {
-    float4 w = make_float4(otherwise, otherwise, otherwise, otherwise);
-    if (p) w = *reinterpret_cast<const float4*>(p + c + i);
-    f[i] = w.x;
-    f[i + 1] = w.y;
-    f[i + 2] = w.z;
-    f[i + 3] = w.w;
-  }
-}
-
 // How a block's threads share a row.  VEC: E consecutive elements each, 16-byte accesses.  Else
 // elements threadIdx.x + e blockDim.x: any width and any alignment, still whole lines a warp.
 template <int E, bool VEC>
@@ -110,7 +97,6 @@ struct Share {
     }
   }
   __device__ __forceinline__ bool has(int e) const { return (VEC ? c[0] : c[e]) < D; }
-  __device__ __forceinline__ int at(int e) const { return VEC ? c[0] + e : c[e]; }
   template <typename T>
   __device__ __forceinline__ void load(const T* row, float (&f)[E]) const {  // absent elements are 0
 #pragma unroll
@@ -132,6 +118,13 @@ struct Share {
       for (int e = 0; e < E; ++e)
         if (has(e)) row[c[e]] = from_float<T>(f[e]);
     }
+  }
+  __device__ __forceinline__ void add(float* sums, const float (&f)[E]) const {
+    float x[E];
+    load<float>(sums, x);
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] += f[e];
+    store<float>(sums, x);
   }
   __device__ __forceinline__ void param(const float* p, float (&f)[E]) const {  // 1 where there is none
     if (p) {
@@ -242,13 +235,14 @@ __global__ void __launch_bounds__(1024, 1) norm_bwd(const __grid_constant__ Norm
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         xn[e] *= r_pre;
-        if (sh.has(e)) acc[sh.at(e)] += t[e] * xn[e];
-        t[e] *= w[e];
-        s += t[e] * xn[e];
+        w[e] *= t[e];
+        s += w[e] * xn[e];
+        t[e] *= xn[e];
       }
+      sh.add(acc, t);
       const float mean = block_sum<32>(s, buf, turn) * a.inv_D;
 #pragma unroll
-      for (int e = 0; e < E; ++e) dx[e] += r_pre * (t[e] - xn[e] * mean);
+      for (int e = 0; e < E; ++e) dx[e] += r_pre * (w[e] - xn[e] * mean);
     }
     if (a.dx) sh.template store<T>(reinterpret_cast<T*>(a.dx) + row0, dx);
     if (!a.y) continue;
@@ -258,11 +252,12 @@ __global__ void __launch_bounds__(1024, 1) norm_bwd(const __grid_constant__ Norm
     for (int e = 0; e < E; ++e) {
       const float dgz = a.res_scale * dx[e], dz = dgz * g[e];
       dg[e] = dgz * (z[e] * w[e]);
-      if (a.w_post && sh.has(e)) acc[a.D + sh.at(e)] += dz * z[e];
-      if (sum_gate && sh.has(e)) acc[2 * a.D + sh.at(e)] += dg[e];
+      g[e] = dz * z[e];
       dx[e] = dz * w[e];
       s += dx[e] * z[e];
     }
+    if (a.w_post) sh.add(acc + a.D, g);
+    if (sum_gate) sh.add(acc + 2 * a.D, dg);
     if (row_gate && a.dgate) sh.template store<T>(reinterpret_cast<T*>(a.dgate) + row0, dg);
     if (a.w_post) {
       const float mean = block_sum<32>(s, buf, turn) * a.inv_D;
@@ -307,30 +302,40 @@ __global__ void __launch_bounds__(32 * kStrips) norm_join(const float* __restric
 
 // ------------------------------------------------------------ rows through a ring
 // Many rows: a block walks its rows with the next ones in flight.  One thread copies whole
-// rows of every tensor that is read (cp.async.bulk) into a ring of kept stages in shared
-// memory; the threads wait for a stage, take their elements into registers and hand the stage
-// back.  So a block keeps stages x tensors x row bytes of loads in flight whatever its barriers
-// wait for, and two blocks of an SM hide each other's sums.
-constexpr int kNarrow = 448;  // threads up to which a thread holds 8 elements: two blocks fit 72 registers
+// rows of every tensor that is read (cp.async.bulk) into a ring of stages in shared memory; the
+// threads wait for a stage, take their elements into registers and hand the stage back.  So a
+// block keeps stages x tensors x row bytes of loads in flight whatever its barriers wait for,
+// and two blocks of an SM hide each other's sums.
+// Threads of a block up to which two fit an SM (at 64 and 72 registers), and a class between those
+// and 1024 that has registers to spare.
+constexpr int kNarrowFwd = 512, kNarrowBwd = 448, kMiddle = 704;
 constexpr int kMaxStages = 4;
 constexpr int kMaxRowTensors = 5;
+constexpr int kPairs = 4;  // pairs of elements a thread holds
 
 struct RowRing {
   const char* src[kMaxRowTensors];  // tensors read, in the order they stand in a stage
   int n_src;
-  uint32_t row_bytes;
+  uint32_t row_bytes, pitch;  // of a row in memory, and from row to row in a stage
   int stages;
+  int64_t tail;  // row that the copies leave out (its end is no multiple of 16 bytes), or -1
 };
 
 struct __align__(16) RingBars {
   uint64_t full[kMaxStages];
 };
 
+// A row's copy: the 16-byte units it lies in.
 __device__ __forceinline__ void ring_issue(const RowRing& r, uint8_t* base, RingBars* bars, int64_t row, int k) {
-  mbar_arrive_expect_tx(&bars->full[k], r.row_bytes * (uint32_t)r.n_src);
-  uint8_t* dst = base + (size_t)k * r.n_src * r.row_bytes;
-  for (int i = 0; i < r.n_src; ++i)
-    bulk_load(dst + (size_t)i * r.row_bytes, r.src[i] + (size_t)row * r.row_bytes, r.row_bytes, &bars->full[k]);
+  if (row == r.tail) {
+    mbar_arrive(&bars->full[k]);
+    return;
+  }
+  const size_t at = (size_t)row * r.row_bytes, from = at & ~(size_t)15;
+  const uint32_t bytes = (uint32_t)(((at + r.row_bytes + 15) & ~(size_t)15) - from);
+  mbar_arrive_expect_tx(&bars->full[k], bytes * (uint32_t)r.n_src);
+  uint8_t* dst = base + (size_t)k * r.n_src * r.pitch;
+  for (int i = 0; i < r.n_src; ++i) bulk_load(dst + (size_t)i * r.pitch, r.src[i] + from, bytes, &bars->full[k]);
 }
 
 // Sets the ring up and starts the first rows' copies.
@@ -364,87 +369,145 @@ __device__ __forceinline__ float halves(uint64_t v) {
   f32x2_split(v, a, b);
   return a + b;
 }
-template <typename T, int E>
-__device__ __forceinline__ void load2(const T* p, uint64_t (&f)[E / 2]) {
-  constexpr int V = 16 / sizeof(T);
+__device__ __forceinline__ uint64_t unpack(uint32_t bf16x2) { return f32x2(bf16x2 << 16, bf16x2 & 0xffff0000u); }
+
+// How a block's threads share a row through the ring.  VEC: 8 consecutive elements each, 16-byte
+// accesses.  Else pairs of elements, neighbouring threads on neighbouring pairs: rows of any
+// width, at any offset.  (8192 rows, backward: bf16 of 3584 73 against 115 us, fp32 128 against
+// 183; 16-byte accesses in two groups of four of fp32 162.)
+template <bool VEC>
+struct Pairs {
+  int D, first, step;
+  __device__ explicit Pairs(int width)
+      : D(width), first((VEC ? 2 * kPairs : 2) * (int)threadIdx.x), step(VEC ? 2 : 2 * (int)blockDim.x) {}
+  __device__ __forceinline__ int at(int h) const { return first + h * step; }
+  __device__ __forceinline__ bool has(int h) const { return (VEC ? first : at(h)) < D; }
+  __device__ __forceinline__ bool whole(int h) const { return VEC || at(h) + 1 < D; }
+  // A row: `row` where every pair lies on its own size (`even`), else element by element from
+  // `plain`.  Absent elements are 0.
+  template <typename T>
+  __device__ __forceinline__ void load(const T* row, const T* plain, bool even, uint64_t (&f)[kPairs]) const {
 #pragma unroll
-  for (int i = 0; i < E; i += V) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p + i);
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-    if constexpr (sizeof(T) == 2) {
+    for (int h = 0; h < kPairs; ++h) f[h] = 0;
+    if constexpr (VEC) {
+      if (!has(0)) return;
+      constexpr int V = 16 / sizeof(T);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) f[i / 2 + k] = f32x2(x[k] << 16, x[k] & 0xffff0000u);
-    } else {
-      f[i / 2] = f32x2(x[0], x[1]);
-      f[i / 2 + 1] = f32x2(x[2], x[3]);
-    }
-  }
-}
-template <typename T, int E>
-__device__ __forceinline__ void store2(T* p, const uint64_t (&f)[E / 2]) {
-  constexpr int V = 16 / sizeof(T);
+      for (int i = 0; i < 2 * kPairs; i += V) {
+        const uint4 w = *reinterpret_cast<const uint4*>(row + first + i);
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-  for (int i = 0; i < E; i += V) {
-    uint32_t x[4];
-    if constexpr (sizeof(T) == 2) {
+          for (int k = 0; k < 4; ++k) f[i / 2 + k] = unpack(x[k]);
+        } else {
+          f[i / 2] = f32x2(x[0], x[1]);
+          f[i / 2 + 1] = f32x2(x[2], x[3]);
+        }
+      }
+    } else if (even) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float a, b;
-        f32x2_split(f[i / 2 + k], a, b);
-        x[k] = pack_bf16x2(a, b);
+      for (int h = 0; h < kPairs; ++h) {
+        if (whole(h)) {
+          if constexpr (sizeof(T) == 2)
+            f[h] = unpack(*reinterpret_cast<const uint32_t*>(row + at(h)));
+          else
+            f[h] = *reinterpret_cast<const uint64_t*>(row + at(h));
+        } else if (has(h)) {
+          f[h] = f32x2(to_float<T>(row[at(h)]), 0.f);
+        }
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int h = 0; h < kPairs; ++h)
+        if (has(h)) f[h] = f32x2(to_float<T>(plain[at(h)]), whole(h) ? to_float<T>(plain[at(h) + 1]) : 0.f);
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, bool even, const uint64_t (&f)[kPairs]) const {
+    if constexpr (VEC) {
+      if (!has(0)) return;
+      float x[2 * kPairs];
+#pragma unroll
+      for (int h = 0; h < kPairs; ++h) f32x2_split(f[h], x[2 * h], x[2 * h + 1]);
+      store_vec<T, 2 * kPairs>(row + first, x);
+    } else {
+#pragma unroll
+      for (int h = 0; h < kPairs; ++h) {
+        if (!has(h)) continue;
         float a, b;
-        f32x2_split(f[i / 2 + k], a, b);
-        x[2 * k] = __float_as_uint(a);
-        x[2 * k + 1] = __float_as_uint(b);
+        f32x2_split(f[h], a, b);
+        if (even && whole(h)) {
+          if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<uint32_t*>(row + at(h)) = pack_bf16x2(a, b);
+          else
+            *reinterpret_cast<uint64_t*>(row + at(h)) = f[h];
+        } else {
+          row[at(h)] = from_float<T>(a);
+          if (whole(h)) row[at(h) + 1] = from_float<T>(b);
+        }
       }
     }
-    *reinterpret_cast<uint4*>(p + i) = make_uint4(x[0], x[1], x[2], x[3]);
   }
-}
+  // A parameter (1 where there is none; nothing behind the row).
+  __device__ __forceinline__ void param(const float* p, uint64_t (&f)[kPairs]) const {
+#pragma unroll
+    for (int h = 0; h < kPairs; ++h) f[h] = p ? 0 : both(1.f);
+    if (p) load<float>(p, p, VEC, f);
+  }
+};
+
+// A row of a stage.
+template <typename T, bool VEC>
+struct StageRow {
+  const RowRing& r;
+  const uint8_t* base;  // the stage, at the row's offset in its first 16-byte unit
+  size_t at;            // bytes in front of the row in memory
+  bool tail, even;      // even: pairs lie on their own size, in memory and in the stage
+  __device__ StageRow(const RowRing& ring, const uint8_t* stage_mem, int64_t row, int k)
+      : r(ring), at((size_t)row * ring.row_bytes) {
+    base = stage_mem + (size_t)k * ring.n_src * ring.pitch + (VEC ? 0 : at & 15);
+    tail = !VEC && row == ring.tail;
+    even = VEC || at % (2 * sizeof(T)) == 0;
+  }
+  __device__ __forceinline__ void load(const Pairs<VEC>& c, int i, uint64_t (&f)[kPairs]) const {
+    const T* row = reinterpret_cast<const T*>(base + (size_t)i * r.pitch);
+    const T* plain = tail ? reinterpret_cast<const T*>(r.src[i] + at) : row;
+    c.template load<T>(row, plain, even && !tail, f);
+  }
+};
+
+constexpr int kSumWarps(int threads) { return (threads + 127) / 128 * 4; }
 
 // x' = x + (c g) (y r_post), c = res_scale gate w_post of the channel, g the token's gate.
-template <typename T, int E, bool ROWGATE>
-__global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
+template <typename T, bool VEC, bool ROWGATE, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS <= kNarrowFwd ? 2 : 1)
     norm_fwd_ring(const __grid_constant__ NormArgs a, const __grid_constant__ RowRing ring) {
-  constexpr int H = E / 2;
   extern __shared__ __align__(128) uint8_t stage_mem[];
   __shared__ RingBars bars;
   __shared__ __align__(16) float buf[64];
   clear_sums(buf);
   int turn = 0, k = 0;
   uint32_t phase = 0;
-  const int c = threadIdx.x * E;
-  const bool in = c < a.D;
+  const Pairs<VEC> cols(a.D);
   ring_start(ring, stage_mem, &bars, a.n);
-  uint64_t cw[H], w[H];
+  uint64_t cw[kPairs], w[kPairs];
+  {
+    uint64_t g[kPairs];
+    cols.param(a.w_post, cw);
+    cols.param(ROWGATE ? nullptr : reinterpret_cast<const float*>(a.gate), g);
 #pragma unroll
-  for (int e = 0; e < H; ++e) cw[e] = w[e] = 0;
-  if (in) {
-    float f[E], g[E];
-    load_param<E>(a.w_post, c, f, 1.f);
-    load_param<E>(ROWGATE ? nullptr : reinterpret_cast<const float*>(a.gate), c, g, 1.f);
-#pragma unroll
-    for (int e = 0; e < H; ++e)
-      cw[e] = f32x2(a.res_scale * g[2 * e] * f[2 * e], a.res_scale * g[2 * e + 1] * f[2 * e + 1]);
-    load_param<E>(a.w_pre, c, f, 1.f);
-#pragma unroll
-    for (int e = 0; e < H; ++e) w[e] = f32x2(f[2 * e], f[2 * e + 1]);
+    for (int e = 0; e < kPairs; ++e) cw[e] = mul2(both(a.res_scale), mul2(g[e], cw[e]));
+    cols.param(a.w_pre, w);
   }
   for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
-    uint64_t f[H], r[H], g[H];
+    uint64_t f[kPairs], r[kPairs], g[kPairs];
 #pragma unroll
-    for (int e = 0; e < H; ++e) f[e] = r[e] = g[e] = 0;
+    for (int e = 0; e < kPairs; ++e) r[e] = g[e] = 0;
     if (!mbar_wait(&bars.full[k], phase, nullptr)) return;  // the copy cannot fail to end
-    const T* st = reinterpret_cast<const T*>(stage_mem + (size_t)k * ring.n_src * ring.row_bytes) + c;
-    if (in) {
-      load2<T, E>(st, f);
-      if (a.y) load2<T, E>(st + a.D, r);
-      if (ROWGATE) load2<T, E>(st + 2 * a.D, g);
-    }
+    const StageRow<T, VEC> st(ring, stage_mem, row, k);
+    st.load(cols, 0, f);
+    if (a.y) st.load(cols, 1, r);
+    if (ROWGATE) st.load(cols, 2, g);
     __syncthreads();
     const int64_t later = row + (int64_t)ring.stages * gridDim.x;
     if (threadIdx.x == 0 && later < a.n) ring_issue(ring, stage_mem, &bars, later, k);
@@ -452,88 +515,93 @@ __global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
       k = 0;
       phase ^= 1;
     }
-    const size_t at = (size_t)row * a.D + c;
+    const size_t at = (size_t)row * a.D;
     if (a.y) {
       float rstd = 1.f;
       if (a.w_post) {
         uint64_t s = 0;
 #pragma unroll
-        for (int e = 0; e < H; ++e) s = fma2(r[e], r[e], s);
-        rstd = rsqrtf(block_sum<16>(halves(s), buf, turn) * a.inv_D + a.eps);
+        for (int e = 0; e < kPairs; ++e) s = fma2(r[e], r[e], s);
+        rstd = rsqrtf(block_sum<kSumWarps(THREADS)>(halves(s), buf, turn) * a.inv_D + a.eps);
         if (a.rstd_post && threadIdx.x == 0) a.rstd_post[row] = rstd;
       }
       const uint64_t rs = both(rstd);
 #pragma unroll
-      for (int e = 0; e < H; ++e) f[e] = fma2(mul2(r[e], rs), ROWGATE ? mul2(cw[e], g[e]) : cw[e], f[e]);
+      for (int e = 0; e < kPairs; ++e) f[e] = fma2(mul2(r[e], rs), ROWGATE ? mul2(cw[e], g[e]) : cw[e], f[e]);
     }
-    if (a.x_out && in) store2<T, E>(reinterpret_cast<T*>(a.x_out) + at, f);
+    if (a.x_out) cols.template store<T>(reinterpret_cast<T*>(a.x_out) + at, st.even, f);
     if (a.w_pre) {
       uint64_t s = 0;
 #pragma unroll
-      for (int e = 0; e < H; ++e) s = fma2(f[e], f[e], s);
-      const float rstd = rsqrtf(block_sum<16>(halves(s), buf, turn) * a.inv_D + a.eps);
+      for (int e = 0; e < kPairs; ++e) s = fma2(f[e], f[e], s);
+      const float rstd = rsqrtf(block_sum<kSumWarps(THREADS)>(halves(s), buf, turn) * a.inv_D + a.eps);
       if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[row] = rstd;
       const uint64_t rs = both(rstd);
-      if (in) {
 #pragma unroll
-        for (int e = 0; e < H; ++e) f[e] = mul2(mul2(f[e], rs), w[e]);
-        store2<T, E>(reinterpret_cast<T*>(a.u) + at, f);
-      }
+      for (int e = 0; e < kPairs; ++e) f[e] = mul2(mul2(f[e], rs), w[e]);
+      cols.template store<T>(reinterpret_cast<T*>(a.u) + at, st.even, f);
     }
   }
 }
 
 // With c as above and a = dx yn: dz yn = (res_scale gate) a and the gate's gradient is
 // (res_scale w_post) a, so for a gate per channel one sum over the rows of a gives both
-// parameter gradients.  The parameters stand in shared memory ([w_pre | c] x D fp32, a thread
-// reads its own columns), the sums in registers.
-template <typename T, int E, bool ROWGATE>
-__global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
+// parameter gradients.  The parameters stand in shared memory ([w_pre | c], fp32, a thread reads
+// its own columns), the sums in registers.
+template <typename T, bool VEC, bool ROWGATE, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS <= kNarrowBwd ? 2 : 1)
     norm_bwd_ring(const __grid_constant__ NormArgs a, const __grid_constant__ RowRing ring) {
-  constexpr int H = E / 2;
   extern __shared__ __align__(128) uint8_t stage_mem[];
   __shared__ RingBars bars;
   __shared__ __align__(16) float buf[64];
   clear_sums(buf);
   int turn = 0, k = 0;
   uint32_t phase = 0;
-  const int c = threadIdx.x * E;
-  const bool in = c < a.D;
+  const Pairs<VEC> cols(a.D);
   const bool pre = a.w_pre != nullptr, post = a.w_post != nullptr;
-  float* par = reinterpret_cast<float*>(stage_mem + (size_t)ring.stages * ring.n_src * ring.row_bytes);
-  ring_start(ring, stage_mem, &bars, a.n);
-  if (in) {
-    float f[E], g[E];
-    load_param<E>(a.w_pre, c, f, 1.f);
-    store_vec<float, E>(par + c, f);
-    load_param<E>(a.w_post, c, f, 1.f);
-    load_param<E>(ROWGATE ? nullptr : reinterpret_cast<const float*>(a.gate), c, g, 1.f);
+  const int pitch = (a.D + 3) & ~3;  // room for the absent half of the last pair
+  float* par = reinterpret_cast<float*>(stage_mem + (size_t)ring.stages * ring.n_src * ring.pitch);
+  auto own_param = [&](const float* p, uint64_t (&f)[kPairs]) {
+    if constexpr (VEC) {
+      cols.template load<float>(p, p, true, f);
+    } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[e] *= a.res_scale * g[e];
-    store_vec<float, E>(par + a.D + c, f);
+      for (int e = 0; e < kPairs; ++e) f[e] = cols.has(e) ? *reinterpret_cast<const uint64_t*>(p + cols.at(e)) : 0;
+    }
+  };
+  ring_start(ring, stage_mem, &bars, a.n);
+  {
+    uint64_t f[kPairs], g[kPairs];
+    cols.param(a.w_pre, f);
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e)
+      if (cols.has(e)) *reinterpret_cast<uint64_t*>(par + cols.at(e)) = f[e];
+    cols.param(a.w_post, f);
+    cols.param(ROWGATE ? nullptr : reinterpret_cast<const float*>(a.gate), g);
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e)
+      if (cols.has(e)) *reinterpret_cast<uint64_t*>(par + pitch + cols.at(e)) = mul2(both(a.res_scale), mul2(g[e], f[e]));
   }
   // stage order: x (with a pre-norm), y, du, dx', gate rows, each where it is read
   const int at_y = pre ? 1 : 0, at_du = at_y + (a.y ? 1 : 0), at_dx = at_du + (pre ? 1 : 0),
             at_g = at_dx + (a.dx_in ? 1 : 0);
-  uint64_t a_pre[H], a_post[H];
+  uint64_t a_pre[kPairs], a_post[kPairs];
 #pragma unroll
-  for (int e = 0; e < H; ++e) a_pre[e] = a_post[e] = 0;
+  for (int e = 0; e < kPairs; ++e) a_pre[e] = a_post[e] = 0;
   for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
     const float r_post = post ? a.rstd_post[row] : 1.f, r_pre = pre ? a.rstd_pre[row] : 1.f;
-    uint64_t xo[H], yn[H], dx[H], t[H], g[H];
+    uint64_t xo[kPairs], yn[kPairs], dx[kPairs], t[kPairs], g[kPairs];
 #pragma unroll
-    for (int e = 0; e < H; ++e) xo[e] = yn[e] = dx[e] = t[e] = g[e] = 0;
+    for (int e = 0; e < kPairs; ++e) xo[e] = yn[e] = dx[e] = t[e] = g[e] = 0;
     if (!mbar_wait(&bars.full[k], phase, nullptr)) return;  // the copy cannot fail to end
-    const T* st = reinterpret_cast<const T*>(stage_mem + (size_t)k * ring.n_src * ring.row_bytes) + c;
-    if (in) {
-      if (pre) {
-        load2<T, E>(st, xo);
-        load2<T, E>(st + at_du * a.D, t);
-      }
-      if (a.y) load2<T, E>(st + at_y * a.D, yn);
-      if (a.dx_in) load2<T, E>(st + at_dx * a.D, dx);
-      if (ROWGATE) load2<T, E>(st + at_g * a.D, g);
+    const StageRow<T, VEC> st(ring, stage_mem, row, k);
+    if (pre) {
+      st.load(cols, 0, xo);
+      st.load(cols, at_du, t);
     }
+    if (a.y) st.load(cols, at_y, yn);
+    if (a.dx_in) st.load(cols, at_dx, dx);
+    if (ROWGATE) st.load(cols, at_g, g);
     __syncthreads();
     const int64_t later = row + (int64_t)ring.stages * gridDim.x;
     if (threadIdx.x == 0 && later < a.n) ring_issue(ring, stage_mem, &bars, later, k);
@@ -541,47 +609,39 @@ __global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
       k = 0;
       phase ^= 1;
     }
-    const size_t at = (size_t)row * a.D + c;
+    const size_t at = (size_t)row * a.D;
     const uint64_t rp2 = both(r_post);
 #pragma unroll
-    for (int e = 0; e < H; ++e) yn[e] = mul2(yn[e], rp2);
-    uint64_t cw[H];
-    if (in) {
-      load2<float, E>(par + a.D + c, cw);
-    } else {
-#pragma unroll
-      for (int e = 0; e < H; ++e) cw[e] = 0;
-    }
+    for (int e = 0; e < kPairs; ++e) yn[e] = mul2(yn[e], rp2);
+    uint64_t cw[kPairs];
+    own_param(par + pitch, cw);
     if (pre) {
-      uint64_t s = 0;
+      uint64_t s = 0, w[kPairs];
       const uint64_t r2 = both(r_pre);
-      if (in) {
-        uint64_t w[H];
-        load2<float, E>(par + c, w);
-        if (a.y) {
+      own_param(par, w);
+      if (a.y) {
 #pragma unroll
-          for (int e = 0; e < H; ++e) xo[e] = fma2(ROWGATE ? mul2(cw[e], g[e]) : cw[e], yn[e], xo[e]);
-        }
+        for (int e = 0; e < kPairs; ++e) xo[e] = fma2(ROWGATE ? mul2(cw[e], g[e]) : cw[e], yn[e], xo[e]);
+      }
 #pragma unroll
-        for (int e = 0; e < H; ++e) {
-          a_pre[e] = fma2(mul2(t[e], r2), xo[e], a_pre[e]);
-          t[e] = mul2(t[e], w[e]);
-          s = fma2(t[e], xo[e], s);
-        }
+      for (int e = 0; e < kPairs; ++e) {
+        a_pre[e] = fma2(mul2(t[e], r2), xo[e], a_pre[e]);
+        t[e] = mul2(t[e], w[e]);
+        s = fma2(t[e], xo[e], s);
       }
       // xn mean(t xn) r_pre = x' r_pre^3 sum(t x') / D
-      const float sum = block_sum<16>(halves(s), buf, turn) * a.inv_D;
+      const float sum = block_sum<kSumWarps(THREADS)>(halves(s), buf, turn) * a.inv_D;
       const uint64_t m2 = both(-(r_pre * sum * r_pre) * r_pre);
 #pragma unroll
-      for (int e = 0; e < H; ++e) dx[e] = fma2(xo[e], m2, fma2(t[e], r2, dx[e]));
+      for (int e = 0; e < kPairs; ++e) dx[e] = fma2(xo[e], m2, fma2(t[e], r2, dx[e]));
     }
-    if (in && a.dx) store2<T, E>(reinterpret_cast<T*>(a.dx) + at, dx);
+    if (a.dx) cols.template store<T>(reinterpret_cast<T*>(a.dx) + at, st.even, dx);
     if (!a.y) continue;
     uint64_t s = 0;
 #pragma unroll
-    for (int e = 0; e < H; ++e) {
-      const uint64_t p = mul2(dx[e], yn[e]);
+    for (int e = 0; e < kPairs; ++e) {
       if (ROWGATE) {
+        const uint64_t p = mul2(dx[e], yn[e]);
         a_post[e] = fma2(g[e], p, a_post[e]);
         t[e] = mul2(cw[e], p);
         dx[e] = mul2(mul2(cw[e], g[e]), dx[e]);
@@ -591,34 +651,30 @@ __global__ void __launch_bounds__(E == 8 ? kNarrow : 512, E == 8 ? 2 : 1)
       }
       s = fma2(dx[e], yn[e], s);
     }
-    if (ROWGATE && a.dgate && in) store2<T, E>(reinterpret_cast<T*>(a.dgate) + at, t);
+    if (ROWGATE && a.dgate) cols.template store<T>(reinterpret_cast<T*>(a.dgate) + at, st.even, t);
     if (post) {
-      const float mean = block_sum<16>(halves(s), buf, turn) * a.inv_D;
+      const float mean = block_sum<kSumWarps(THREADS)>(halves(s), buf, turn) * a.inv_D;
       const uint64_t m2 = both(-r_post * mean);
 #pragma unroll
-      for (int e = 0; e < H; ++e) dx[e] = fma2(yn[e], m2, mul2(dx[e], rp2));
+      for (int e = 0; e < kPairs; ++e) dx[e] = fma2(yn[e], m2, mul2(dx[e], rp2));
     }
-    if (in && a.dy) store2<T, E>(reinterpret_cast<T*>(a.dy) + at, dx);
+    if (a.dy) cols.template store<T>(reinterpret_cast<T*>(a.dy) + at, st.even, dx);
   }
-  if (in) {
-    float* dst = a.part + (size_t)blockIdx.x * 3 * a.D + c;
-    float s[E], w[E], g[E];
+  const size_t out = (size_t)blockIdx.x * 3 * a.D;
+  float* part = a.part + out;
+  auto even = [&](int i) { return VEC || (out + (size_t)i * a.D) % 2 == 0; };
+  uint64_t w[kPairs], g[kPairs];
+  cols.template store<float>(part, even(0), a_pre);
+  cols.param(a.w_post, w);
+  cols.param(ROWGATE ? nullptr : reinterpret_cast<const float*>(a.gate), g);
 #pragma unroll
-    for (int e = 0; e < H; ++e) f32x2_split(a_pre[e], s[2 * e], s[2 * e + 1]);
-    store_vec<float, E>(dst, s);
-    load_param<E>(a.w_post, c, w, 1.f);
-    load_param<E>(ROWGATE ? nullptr : reinterpret_cast<const float*>(a.gate), c, g, 1.f);
-#pragma unroll
-    for (int e = 0; e < H; ++e) f32x2_split(a_post[e], s[2 * e], s[2 * e + 1]);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float v = a.res_scale * s[e];
-      s[e] = v * g[e];
-      w[e] *= v;
-    }
-    store_vec<float, E>(dst + a.D, s);
-    store_vec<float, E>(dst + 2 * a.D, w);  // not used for a gate per token
+  for (int e = 0; e < kPairs; ++e) {
+    const uint64_t v = mul2(both(a.res_scale), a_post[e]);
+    g[e] = mul2(v, g[e]);
+    w[e] = mul2(v, w[e]);
   }
+  cols.template store<float>(part + a.D, even(1), g);
+  cols.template store<float>(part + 2 * a.D, even(2), w);  // not used for a gate per token
 }
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -626,26 +682,25 @@ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // Elements a thread holds in the 16-byte variant: 1024 threads have to span a row.
 int elements(int D) { return D <= 8192 ? 8 : 16; }
 
-// The 16-byte variant: every row is whole threads' shares, and every row and parameter starts
-// on 16 bytes.
-bool vector_rows(const NormArgs& a) {
+int threads_for(int D, int E) { return (int)align_up((size_t)((D + E - 1) / E), 32); }
+
+// Shared memory of an SM, and of a block what it takes beside the ring.
+constexpr size_t kSmBytes = 228 * 1024, kBesides = 2 * 1024;
+constexpr size_t kRingBytes = kSmBytes - kBesides;  // the most of one block
+
+// Every row and parameter may start on 16 bytes (rows do if their width is right).
+bool on16_all(const NormArgs& a) {
   const void* ptrs[] = {a.x, a.y, a.x_out, a.u, a.gate, a.w_pre, a.w_post, a.du, a.dx_in, a.dx, a.dy, a.dgate};
-  if (a.D % elements(a.D)) return false;
   for (const void* p : ptrs)
     if (!on16(p)) return false;
   return true;
 }
 
-int threads_for(int D, int E) { return (int)align_up((size_t)((D + E - 1) / E), 32); }
-
-int ring_elements(int D) { return D <= 8 * kNarrow ? 8 : 16; }
-
-// Rows through the ring where every block has at least four of them to walk and a stage
-// fits; else a row is read straight into registers.
-constexpr size_t kRingBytes = 200 * 1024;  // of an SM's shared memory, for all its blocks' stages
-bool ring_setup(const NormArgs& a, size_t es, bool backward, RowRing* r, unsigned* grid, size_t* smem) {
-  if (a.D > 8192 || a.D % ring_elements(a.D)) return false;
-  const int T = threads_for(a.D, ring_elements(a.D));
+// Rows through the ring, where a stage fits and (forward) every block walks at least one and a
+// half rows; else a row is read straight into registers.
+bool ring_setup(const NormArgs& a, size_t es, bool backward, bool vec, RowRing* r, unsigned* grid, size_t* smem) {
+  const size_t bytes = es * a.D;
+  if (a.D > 8192 || bytes < 64) return false;
   auto add = [&](const void* p) {
     if (p) r->src[r->n_src++] = reinterpret_cast<const char*>(p);
   };
@@ -660,16 +715,21 @@ bool ring_setup(const NormArgs& a, size_t es, bool backward, RowRing* r, unsigne
     add(a.y);
   }
   if (a.gate_rows) add(a.gate);
-  const size_t bytes = es * a.D;
   r->row_bytes = (uint32_t)bytes;
-  const int per_sm = norm_blocks_per_sm(T);
+  r->pitch = (uint32_t)(vec ? bytes : align_up(bytes, 16) + 16);
+  r->tail = (size_t)a.n * bytes % 16 ? a.n - 1 : -1;
+  const size_t stage = (size_t)r->pitch * r->n_src, fixed = backward ? 2 * align_up((size_t)a.D, 4) * 4 : 0;
+  // as many blocks on an SM as leave each two stages; one block has to do with what there is
+  const int T = threads_for(a.D, 2 * kPairs);
+  int per_sm = T <= (backward ? kNarrowBwd : kNarrowFwd) ? norm_blocks_per_sm(T) : 1;
+  while (per_sm > 1 && kSmBytes / per_sm < kBesides + fixed + 2 * stage) --per_sm;
+  const size_t room = kSmBytes / per_sm - kBesides;
+  if (room < fixed + stage) return false;
   const int64_t blocks = std::min<int64_t>(a.n, (int64_t)per_sm * device_sm_count());
-  if (a.n < 4 * blocks) return false;
-  const size_t fixed = backward ? (size_t)2 * a.D * 4 : 0, room = kRingBytes / per_sm;
-  if (room < fixed + 2 * bytes * r->n_src) return false;
-  r->stages = (int)std::min<size_t>(kMaxStages, (room - fixed) / (bytes * r->n_src));
+  if (!backward && a.n < blocks + blocks / 2) return false;
+  r->stages = (int)std::min<size_t>(kMaxStages, (room - fixed) / stage);
   *grid = (unsigned)blocks;
-  *smem = r->stages * bytes * r->n_src + fixed;
+  *smem = r->stages * stage + fixed;
   return true;
 }
 
@@ -678,18 +738,25 @@ cudaError_t fwd_direct(const NormArgs& a, cudaStream_t st) {
   norm_fwd<T, E, VEC><<<(unsigned)std::min<int64_t>(a.n, 1 << 20), threads_for(a.D, E), 0, st>>>(a);
   return cudaGetLastError();
 }
-template <typename T, int E, bool ROWGATE>
+template <typename T, bool VEC, bool ROWGATE, int THREADS>
 cudaError_t fwd_ring_one(const NormArgs& a, const RowRing& ring, unsigned grid, size_t smem, cudaStream_t st) {
   static size_t set[kMaxDevices] = {};
-  const cudaError_t e = set_smem_limit((const void*)norm_fwd_ring<T, E, ROWGATE>, kRingBytes, set);
+  const cudaError_t e = set_smem_limit((const void*)norm_fwd_ring<T, VEC, ROWGATE, THREADS>, kRingBytes, set);
   if (e != cudaSuccess) return e;
-  norm_fwd_ring<T, E, ROWGATE><<<grid, threads_for(a.D, E), smem, st>>>(a, ring);
+  norm_fwd_ring<T, VEC, ROWGATE, THREADS><<<grid, threads_for(a.D, 2 * kPairs), smem, st>>>(a, ring);
   return cudaGetLastError();
 }
-template <typename T, int E>
+template <typename T, bool VEC, bool ROWGATE>
+cudaError_t fwd_ring_width(const NormArgs& a, const RowRing& ring, unsigned grid, size_t smem, cudaStream_t st) {
+  const int threads = threads_for(a.D, 2 * kPairs);
+  if (threads <= kNarrowFwd) return fwd_ring_one<T, VEC, ROWGATE, kNarrowFwd>(a, ring, grid, smem, st);
+  if (threads <= kMiddle) return fwd_ring_one<T, VEC, ROWGATE, kMiddle>(a, ring, grid, smem, st);
+  return fwd_ring_one<T, VEC, ROWGATE, 1024>(a, ring, grid, smem, st);
+}
+template <typename T, bool VEC>
 cudaError_t fwd_ring(const NormArgs& a, const RowRing& ring, unsigned grid, size_t smem, cudaStream_t st) {
-  return a.gate && a.gate_rows ? fwd_ring_one<T, E, true>(a, ring, grid, smem, st)
-                               : fwd_ring_one<T, E, false>(a, ring, grid, smem, st);
+  return a.gate && a.gate_rows ? fwd_ring_width<T, VEC, true>(a, ring, grid, smem, st)
+                               : fwd_ring_width<T, VEC, false>(a, ring, grid, smem, st);
 }
 template <typename T, int E, bool VEC>
 cudaError_t bwd_direct(const NormArgs& a, unsigned grid, cudaStream_t st) {
@@ -699,30 +766,36 @@ cudaError_t bwd_direct(const NormArgs& a, unsigned grid, cudaStream_t st) {
   norm_bwd<T, E, VEC><<<grid, threads_for(a.D, E), (size_t)3 * a.D * 4, st>>>(a);
   return cudaGetLastError();
 }
-template <typename T, int E, bool ROWGATE>
+template <typename T, bool VEC, bool ROWGATE, int THREADS>
 cudaError_t bwd_ring_one(const NormArgs& a, const RowRing& ring, unsigned grid, size_t smem, cudaStream_t st) {
   static size_t set[kMaxDevices] = {};
-  const cudaError_t e = set_smem_limit((const void*)norm_bwd_ring<T, E, ROWGATE>, kRingBytes, set);
+  const cudaError_t e = set_smem_limit((const void*)norm_bwd_ring<T, VEC, ROWGATE, THREADS>, kRingBytes, set);
   if (e != cudaSuccess) return e;
-  norm_bwd_ring<T, E, ROWGATE><<<grid, threads_for(a.D, E), smem, st>>>(a, ring);
+  norm_bwd_ring<T, VEC, ROWGATE, THREADS><<<grid, threads_for(a.D, 2 * kPairs), smem, st>>>(a, ring);
   return cudaGetLastError();
 }
-template <typename T, int E>
-cudaError_t bwd_ring(const NormArgs& a, const RowRing& ring, unsigned grid, size_t smem, cudaStream_t st) {
-  return a.gate && a.gate_rows ? bwd_ring_one<T, E, true>(a, ring, grid, smem, st)
-                               : bwd_ring_one<T, E, false>(a, ring, grid, smem, st);
+template <typename T, bool VEC, bool ROWGATE>
+cudaError_t bwd_ring_width(const NormArgs& a, const RowRing& ring, unsigned grid, size_t smem, cudaStream_t st) {
+  const int threads = threads_for(a.D, 2 * kPairs);
+  if (threads <= kNarrowBwd) return bwd_ring_one<T, VEC, ROWGATE, kNarrowBwd>(a, ring, grid, smem, st);
+  if (threads <= kMiddle) return bwd_ring_one<T, VEC, ROWGATE, kMiddle>(a, ring, grid, smem, st);
+  return bwd_ring_one<T, VEC, ROWGATE, 1024>(a, ring, grid, smem, st);
 }
-
+template <typename T, bool VEC>
+cudaError_t bwd_ring(const NormArgs& a, const RowRing& ring, unsigned grid, size_t smem, cudaStream_t st) {
+  return a.gate && a.gate_rows ? bwd_ring_width<T, VEC, true>(a, ring, grid, smem, st)
+                               : bwd_ring_width<T, VEC, false>(a, ring, grid, smem, st);
+}
 template <typename T>
 cudaError_t fwd(const NormArgs& a, cudaStream_t st) {
   RowRing ring;
   unsigned grid;
   size_t smem;
   count_launches(1);
-  const bool small = elements(a.D) == 8;
-  if (!vector_rows(a)) return small ? fwd_direct<T, 8, false>(a, st) : fwd_direct<T, 16, false>(a, st);
-  if (ring_setup(a, sizeof(T), false, &ring, &grid, &smem))
-    return ring_elements(a.D) == 8 ? fwd_ring<T, 8>(a, ring, grid, smem, st) : fwd_ring<T, 16>(a, ring, grid, smem, st);
+  const bool small = elements(a.D) == 8, aligned = on16_all(a), vec = aligned && a.D % elements(a.D) == 0;
+  if (aligned && ring_setup(a, sizeof(T), false, a.D % 8 == 0, &ring, &grid, &smem))
+    return a.D % 8 == 0 ? fwd_ring<T, true>(a, ring, grid, smem, st) : fwd_ring<T, false>(a, ring, grid, smem, st);
+  if (!vec) return small ? fwd_direct<T, 8, false>(a, st) : fwd_direct<T, 16, false>(a, st);
   return small ? fwd_direct<T, 8, true>(a, st) : fwd_direct<T, 16, true>(a, st);
 }
 
@@ -732,13 +805,13 @@ cudaError_t bwd(const NormArgs& a, cudaStream_t st) {
   unsigned grid = (unsigned)norm_parts(a.n, a.D);
   RowRing ring;
   cudaError_t e;
-  const bool small = elements(a.D) == 8;
-  if (!vector_rows(a))
-    e = small ? bwd_direct<T, 8, false>(a, grid, st) : bwd_direct<T, 16, false>(a, grid, st);
-  else if (ring_setup(a, sizeof(T), true, &ring, &grid, &smem))
-    e = ring_elements(a.D) == 8 ? bwd_ring<T, 8>(a, ring, grid, smem, st) : bwd_ring<T, 16>(a, ring, grid, smem, st);
-  else
+  const bool small = elements(a.D) == 8, aligned = on16_all(a), vec = aligned && a.D % elements(a.D) == 0;
+  if (aligned && ring_setup(a, sizeof(T), true, a.D % 8 == 0, &ring, &grid, &smem))
+    e = a.D % 8 == 0 ? bwd_ring<T, true>(a, ring, grid, smem, st) : bwd_ring<T, false>(a, ring, grid, smem, st);
+  else if (vec)
     e = small ? bwd_direct<T, 8, true>(a, grid, st) : bwd_direct<T, 16, true>(a, grid, st);
+  else
+    e = small ? bwd_direct<T, 8, false>(a, grid, st) : bwd_direct<T, 16, false>(a, grid, st);
   if (e != cudaSuccess) return e;
   count_launches(1);
   float* dgate = a.gate && !a.gate_rows ? reinterpret_cast<float*>(a.dgate) : nullptr;
@@ -765,9 +838,7 @@ cudaError_t bwd(const NormArgs& a, cudaStream_t st) {
 int norm_blocks_per_sm(int T) { return std::max(1, std::min(8, 1024 / T)); }
 
 int norm_parts(int64_t n, int D) {
-  const int E = ring_elements(D);
-  return (int)std::min<int64_t>(n, (int64_t)norm_blocks_per_sm((int)align_up((size_t)((D + E - 1) / E), 32)) *
-                                       device_sm_count());
+  return (int)std::min<int64_t>(n, (int64_t)norm_blocks_per_sm(std::min(1024, threads_for(D, 2 * kPairs))) * device_sm_count());
 }
 
 }  // namespace oomb

@@ -823,9 +823,12 @@ cudaError_t launch_score_fwd_tc(ScoreArgs& s, cudaStream_t st) {
   p.n_tiles = (s.a.n_q + kTile - 1) / kTile;
   p.n_pairs = pack ? 1 : (p.n_tiles + 1) / 2;
   if (pack) {
-    // one block per SM, as long as each has two pages for either tile (with one, the parts'
-    // traffic costs what the shorter walk saves)
-    s.n_split = std::max(1, std::min(limit / 2, (s.a.max_sel + 3) / 4));
+    // one block per SM, as long as each has a page for either tile; up to 16 pages a block each:
+    // one of its tiles then idles, but the shorter walk counts for more.  28 query heads on 4,
+    // 1 row and 18: 4 pages 9.5 and 13.1 us in 4 blocks, 10.1 and 15.7 in 2; 16 pages 10.9 and 14.8
+    // in 16, 10.9 and 16.7 in 8; 64 pages 13.2 and 19.8 in 32, 13.9 and 20.1 in 16
+    const int pages = s.a.max_sel;
+    s.n_split = std::min(limit / 2, std::max((pages + 1) / 2, std::min(pages, 16)));
   } else {
     // waves of blocks, each as long as its pages plus about kFixed pages of set-up and
     // epilogue (and the join, once the keys are cut)

@@ -162,6 +162,45 @@ def test_many_rows(dtype, n, D, kw):
     compare(run(t, 0.7, 1e-6, dtype), ref, tol)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("n,D", [(1301, 3577), (2001, 517), (901, 5122), (701, 8191), (1303, 132), (1501, 41), (700, 5120)])
+@pytest.mark.parametrize("kw", [dict(gate="channel", post=True), dict(gate="token", post=True)])
+def test_many_rows_of_any_width(dtype, n, D, kw):
+    """Rows that start and end anywhere, the last one off the 16 bytes too."""
+    t = make(n, D, dtype, seed=n, **kw)
+    ref, tol = reference(t, 0.7, 1e-6, dtype)
+    compare(run(t, 0.7, 1e-6, dtype), ref, tol)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("D", [515, 520])
+def test_many_rows_in_place(dtype, D):
+    """x_out over x and dx over dx_out, many rows; what stands around the tensors stays."""
+    n, pad = 2601, 64
+    t = make(n, D, dtype, "token", True, seed=3)
+    ref, tol = reference(t, 0.5, 1e-6, dtype)
+    bufs = {}
+
+    def inside(k, v):  # with NaN around it
+        bufs[k] = torch.full((n * D + 2 * pad,), float("nan"), dtype=dtype, device="cuda")
+        w = bufs[k][pad:-pad].view(n, D)
+        return w if v is None else w.copy_(v)
+
+    d = {k: inside(k, v) if v.dim() == 2 else v.cuda() for k, v in t.items()}
+    x, dx, x0 = inside("x_out", t["x"]), inside("dx", t["dx_out"]), d["x"]
+    u, dy, dg = inside("u", None), inside("dy", None), inside("dgate", None)
+    r1, r2 = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    dw1, dw2 = torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    par = dict(w_pre=d["w_pre"], w_post=d["w_post"], gate=d["gate"], res_scale=0.5, rstd_pre=r1, rstd_post=r2)
+    L.oomb_block_norm_fwd(x, d["y"], x, u, eps=1e-6, **par)
+    ws = torch.empty(L.oomb_block_norm_workspace(n, D), dtype=torch.uint8, device="cuda")
+    L.oomb_block_norm_bwd(x0, d["y"], dx, dy, du=d["du"], dx_out=dx, dgate=dg, dw_pre=dw1, dw_post=dw2, workspace=ws,
+                          **par)
+    compare({"x_out": x, "u": u, "dx": dx, "dy": dy, "dgate": dg, "dw_pre": dw1, "dw_post": dw2}, ref, tol)
+    for k, b in bufs.items():
+        assert b[:pad].isnan().all() and b[-pad:].isnan().all(), k
+
+
 @pytest.mark.parametrize("D", [256, 255])
 @pytest.mark.parametrize("kind", ["pre_only", "post_only", "no_residual_gradient", "gate_only"])
 def test_parts_left_out(kind, D):

@@ -383,7 +383,7 @@ def test_other_stream_and_graph_replay():
         eager.append((o, lse, dq, *[t.clone() for t in c.pool.logical_grads(c.total)]))
         c.pool.close()
     side = torch.cuda.Stream()
-    graphs = []
+    graphs, alive = [], []
     for seed in (1, 2):
         c = Case(seed=seed, **kw)
         do, out = c.do.cuda(), {}
@@ -408,6 +408,7 @@ def test_other_stream_and_graph_replay():
         with torch.cuda.graph(g):
             step()
         graphs.append((g, c, out))
+        alive.append(step)  # holds the inputs and the workspaces that the graph uses
     for _ in range(3):
         for g, c, out in graphs:
             out["o"].zero_(), out["dq"].zero_()
