@@ -23,6 +23,7 @@
 #include <cmath>
 
 #include "score_common.cuh"
+#include "sm103_ptx.cuh"
 
 namespace oomb {
 namespace {
@@ -359,6 +360,48 @@ __global__ void __launch_bounds__(256) score_join(const __grid_constant__ ScoreA
   for (int w = 0; w < 8; ++w) o += acc_s[w][threadIdx.x];
   reinterpret_cast<T*>(s.a.o_out)[rh * d + threadIdx.x] = from_float<T>(den > 0.f ? o / den : 0.f);
   if (threadIdx.x == 0) s.a.lse_out[(size_t)(rh % Hq) * s.a.n_q + rh / Hq] = den > 0.f ? m + logf(den) : m;
+}
+
+// The same for few parts and, usually, many rows: a warp per (row, head), lane z holding part z's
+// log-sum-exp, four columns a lane.
+constexpr int kFewParts = 8;
+template <typename T>
+__global__ void __launch_bounds__(256) score_join_few(const __grid_constant__ ScoreArgs s) {
+  const int64_t rows = (int64_t)s.a.n_q * s.a.g.Hq, rh = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32, Hq = s.a.g.Hq, d = s.a.g.d;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead: the parts are written from here on
+  if (rh >= rows) return;
+  const float lz = lane < s.n_split ? s.part_lse[lane * rows + rh] : -INFINITY;
+  float m = lz;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  const float weight = lz > -INFINITY ? expf(lz - m) : 0.f;
+  float den = weight;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int z = 0; z < kFewParts; ++z) {
+    const float wz = __shfl_sync(0xffffffffu, weight, z);
+    const bool any = __shfl_sync(0xffffffffu, lz, z) > -INFINITY;  // a part without keys has written no O
+    if (any && 4 * lane < d) {
+      const float4 x = *reinterpret_cast<const float4*>(s.part_o + (z * rows + rh) * d + 4 * lane);
+      acc.x += wz * x.x;
+      acc.y += wz * x.y;
+      acc.z += wz * x.z;
+      acc.w += wz * x.w;
+    }
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  if (4 * lane < d) {
+    T* dst = reinterpret_cast<T*>(s.a.o_out) + rh * d + 4 * lane;
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    } else {
+      *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    }
+  }
+  if (lane == 0) s.a.lse_out[(size_t)(rh % Hq) * s.a.n_q + rh / Hq] = den > 0.f ? m + logf(den) : m;
 }
 
 // ----------------------------------------------------------------- backward
@@ -843,7 +886,9 @@ cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st) {
   if (e != cudaSuccess || s.n_split <= 1) return e;
   // a dependent launch: its set-up overlaps the end of the forward, whose parts it waits for
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(s.a.n_q * s.a.g.Hq));
+  const bool few = s.n_split <= kFewParts;
+  const unsigned rows = (unsigned)(s.a.n_q * s.a.g.Hq);
+  cfg.gridDim = dim3(few ? (rows + 7) / 8 : rows);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -851,7 +896,10 @@ cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = f32 ? cudaLaunchKernelEx(&cfg, score_join<float>, s) : cudaLaunchKernelEx(&cfg, score_join<__nv_bfloat16>, s);
+  if (few)
+    e = f32 ? cudaLaunchKernelEx(&cfg, score_join_few<float>, s) : cudaLaunchKernelEx(&cfg, score_join_few<__nv_bfloat16>, s);
+  else
+    e = f32 ? cudaLaunchKernelEx(&cfg, score_join<float>, s) : cudaLaunchKernelEx(&cfg, score_join<__nv_bfloat16>, s);
   count_launches(1);
   return e;
 }

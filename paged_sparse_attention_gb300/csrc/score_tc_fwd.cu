@@ -830,13 +830,15 @@ cudaError_t launch_score_fwd_tc(ScoreArgs& s, cudaStream_t st) {
     const int pages = s.a.max_sel;
     s.n_split = std::min(limit / 2, std::max((pages + 1) / 2, std::min(pages, 16)));
   } else {
-    // waves of blocks, each as long as its pages plus about kFixed pages of set-up and
-    // epilogue (and the join, once the keys are cut)
-    constexpr double kFixed = 4.0;
+    // Waves of blocks, each as long as its pages and about four more for set-up and epilogue; once
+    // the keys are cut, the join takes as long as two pages and one more for every 8000 rows of
+    // parts (28 query heads: 200 rows on 16 pages 25.1 us in 4 parts, 39.4 in one; 300 rows on 8
+    // pages 27.6 in 2, 25.0 in one).
     const int64_t units = (int64_t)p.n_pairs * g.Hq;
     double best = 0.0;
-    for (int n = 1; n <= limit && (n == 1 || s.a.max_sel / n >= 4); ++n) {
-      const double t = (double)((units * n + sms - 1) / sms) * ((double)s.a.max_sel / n + kFixed) + (n > 1 ? kFixed : 0.0);
+    for (int n = 1; n <= limit && (n == 1 || s.a.max_sel / n >= 2); ++n) {
+      const double join = n > 1 ? 2.0 + (double)s.a.n_q * g.Hq * n / 8000.0 : 0.0;
+      const double t = (double)((units * n + sms - 1) / sms) * ((double)s.a.max_sel / n + 4.0) + join;
       if (n == 1 || t < 0.95 * best) {
         best = t;
         s.n_split = n;
