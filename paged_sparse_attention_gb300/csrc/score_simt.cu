@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(256) score_join(const __grid_constant__ ScoreA
 
 // The same for few parts and, usually, many rows: a warp per (row, head), lane z holding part z's
 // log-sum-exp, four columns a lane.
-constexpr int kFewParts = 8;
+constexpr int kFewParts = 16;
 template <typename T>
 __global__ void __launch_bounds__(256) score_join_few(const __grid_constant__ ScoreArgs s) {
   const int64_t rows = (int64_t)s.a.n_q * s.a.g.Hq, rh = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
@@ -560,38 +560,70 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
   __shared__ RowSpans rs;
   __shared__ float slse[kRows], sD[kRows];
   __shared__ int64_t key_lo, key_hi;
+  __shared__ int t_first, t_last;
   const int count = sel_count_checked(s.a, h);
   const int64_t v0 = (int64_t)blockIdx.x * kKeys, v1 = (int64_t)count * P;
   if (v0 >= v1) return;
   list_owned_keys(s, h, v0, v1, count, &kl);
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int64_t lo = INT64_MAX, hi = -1;
-    for (int r = 0; r < kKeys; ++r)
-      if (kl.pos[r] >= 0) {
-        lo = min(lo, kl.pos[r]);
-        hi = max(hi, kl.pos[r]);
-      }
-    key_lo = lo;
-    key_hi = hi;
+  if (threadIdx.x < 32) {
+    const int64_t p = kl.pos[threadIdx.x], q = kl.pos[threadIdx.x + 32];
+    int64_t lo = min(p < 0 ? INT64_MAX : p, q < 0 ? INT64_MAX : q), hi = max(p, q);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    if (threadIdx.x == 0) {
+      key_lo = lo;
+      key_hi = hi;
+      t_first = INT_MAX;
+      t_last = -1;
+    }
   }
-  load_keys<T>(s, &kl, sk, sv);
   __syncthreads();
+  // the row tiles from the first to the last with a row that sees a key of this tile; the shares
+  // cut these, so that a key tile few rows see is still spread over many blocks
+  const int n_tiles = (s.a.n_q + kRows - 1) / kRows;
+  if (key_hi >= 0) {
+    if (!s.begin && !s.end) {
+      if (threadIdx.x == 0 && key_lo < s.a.q_start + s.a.n_q) {
+        t_first = key_lo > s.a.q_start ? (int)((key_lo - s.a.q_start) / kRows) : 0;
+        t_last = n_tiles - 1;
+      }
+    } else {
+      int first = INT_MAX, last = -1;
+      for (int i = threadIdx.x; i < s.a.n_q; i += kThreads) {
+        int64_t b, e;
+        row_span(s, i, b, e);
+        if (e > b && b <= key_hi && e > key_lo) {
+          first = min(first, i / kRows);
+          last = i / kRows;
+        }
+      }
+      if (last >= 0) {
+        atomicMin(&t_first, first);
+        atomicMax(&t_last, last);
+      }
+    }
+  }
+  __syncthreads();
+  const int n_items = t_last < 0 ? 0 : (t_last - t_first + 1) * G;  // (row tile, query head)
+  const int u0 = (int)((int64_t)n_items * blockIdx.z / n_split), u1 = (int)((int64_t)n_items * (blockIdx.z + 1) / n_split);
   const size_t slot = ((size_t)blockIdx.z * gridDim.y + h) * gridDim.x + blockIdx.x;
-  if (key_hi < 0) {
+  if (u0 == u1) {
     if (n_split > 1 && threadIdx.x == 0) flags[slot] = 0;
     return;
   }
+  load_keys<T>(s, &kl, sk, sv);
   bool seen = false;
   float4 dk[4][C], dv[4][C];
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
     for (int c = 0; c < C; ++c) dk[r][c] = dv[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int n_items = (s.a.n_q + kRows - 1) / kRows * G;  // (row tile, query head)
-  const int u0 = (int)((int64_t)n_items * blockIdx.z / n_split), u1 = (int)((int64_t)n_items * (blockIdx.z + 1) / n_split);
   for (int tile = u0 / G; tile * G < u1; ++tile) {
-    const int i0 = tile * kRows;
+    const int i0 = (t_first + tile) * kRows;
     __syncthreads();
     load_spans(s, i0, &rs);
     if (rs.hi <= key_lo || rs.lo > key_hi) continue;  // no row of the tile sees these keys
@@ -700,9 +732,9 @@ __global__ void __launch_bounds__(256) score_dkdv_join(const __grid_constant__ S
     const float* src = part + slot * tile + (size_t)(is_k ? key : kKeys + key) * d + col;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int z = 0; z < n_split; ++z) {
-      if (!flags[z * shares + slot]) continue;
-      const float4 x = *reinterpret_cast<const float4*>(src + z * shares * tile);
+    for (int z = 0; z < n_split; ++z) {  // (loads of shares that have seen no row are left out, not waited for)
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (flags[z * shares + slot]) x = *reinterpret_cast<const float4*>(src + z * shares * tile);
       acc.x += x.x;
       acc.y += x.y;
       acc.z += x.z;
