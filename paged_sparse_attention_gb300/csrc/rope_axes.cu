@@ -10,7 +10,12 @@
 //
 // Bytes: the tensor once in and once out.  A block takes a few tokens: their cos/sin (one per
 // pair) go to shared memory once and serve every head; a thread moves 16-byte vectors of both
-// halves of a head's row.  Shapes or pointers off 16 bytes go element by element.
+// halves of a head's row.  Shapes or pointers off 16 bytes go element by element (24,576 tokens of
+// 28 heads in bf16: 63 us against 154).
+//
+// Bounds (GB300, 8192 tokens of 28 heads, fp32 in, bf16 out): 176 MB in 32 us, 5.5 TB/s, 81 % of
+// the measured copy rate: HBM; the rest is the angles in front of a block's first loads.  Asking
+// for the loads before the angles was slower (36.8), and so were streaming stores (35).
 #include <cmath>
 
 #include "attn_common.cuh"
@@ -130,7 +135,8 @@ cudaError_t launch(RopeArgs& a, cudaStream_t st) {
   // 8 pairs a thread where both halves of every row are whole 16-byte vectors of either type
   auto on16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   const bool wide = a.half % 8 == 0 && on16(a.in) && on16(a.out) && on16(a.bias);
-  // tokens a block: enough work for its threads without leaving SMs idle
+  // tokens a block: enough work for its threads without leaving SMs idle (24,576 tokens of 28 heads:
+  // 1 a block 84 us, 2 68, 4 63, 8 63; 1000 tokens 5.0, 4.9, 5.3, 6.2)
   const int64_t per_token = (int64_t)a.H * (wide ? a.half / 8 : a.half);
   int tokens = (int)std::min<int64_t>(kMaxTokens, std::max<int64_t>(1, 4 * kThreads / per_token));
   while (tokens > 1 && (a.n + tokens - 1) / tokens < 4 * (int64_t)device_sm_count()) tokens /= 2;

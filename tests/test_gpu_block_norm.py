@@ -316,3 +316,28 @@ def test_graph_replay_on_a_side_stream():
     g.replay()
     for a, b in zip(first, (x_out, u, dx, dy, *dw, dg)):
         assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements a tensor: the last rows."""
+    n, D, last = 600500, 3584, 64
+    small = make(last, D, BF, "channel", True, seed=5)
+    ref, tol = reference(small, 0.7, 1e-6, BF)
+    big = {}
+    for k, v in small.items():
+        big[k] = v.cuda()
+        if v.dim() == 2:
+            big[k] = torch.zeros((n, D), dtype=BF, device="cuda")
+            big[k][-last:] = v.cuda()
+    out = {k: torch.empty((n, D), dtype=BF, device="cuda") for k in ("x_out", "u", "dx", "dy")}
+    r1, r2 = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    par = dict(w_pre=big["w_pre"], w_post=big["w_post"], gate=big["gate"], res_scale=0.7, rstd_pre=r1, rstd_post=r2)
+    dw = torch.empty(D, device="cuda")
+    L.oomb_block_norm_fwd(big["x"], big["y"], out["x_out"], out["u"], eps=1e-6, **par)
+    ws = torch.empty(L.oomb_block_norm_workspace(n, D), dtype=torch.uint8, device="cuda")
+    L.oomb_block_norm_bwd(big["x"], big["y"], out["dx"], out["dy"], du=big["du"], dx_out=big["dx_out"], dw_pre=dw,
+                          workspace=ws, **par)
+    for k in out:
+        compare({k: out[k][-last:]}, {k: ref[k]}, tol)
+        assert not out[k][-last - 1].any()  # a row of zeros gives zeros
+    compare({"dw_pre": dw}, {"dw_pre": ref["dw_pre"]}, {"dw_pre": tol["dw_pre"]})

@@ -131,3 +131,29 @@ def test_refusals():
     for kind, f in bad:
         with pytest.raises(kind):
             f()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements, in place: the last tokens get what a call of their own gives them."""
+    n, H, d, last = 600500, 28, 128, 40
+    x = torch.zeros((n, H, d), dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(last, H, d, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    x[-last:] = tail
+    pos = torch.arange(2 * n, device="cuda").view(2, n)
+    axes = bytes(j % 2 for j in range(d // 2))
+    want = torch.empty_like(tail)
+    L.oomb_bias_rope_axes(tail, None, want, H, pos[:, -last:].contiguous(), axes, 1e6, 1)
+    L.oomb_bias_rope_axes(x, None, x, H, pos, axes, 1e6, 1)
+    assert torch.equal(x[-last:], want) and not x[-last - 1].any()
+
+
+@pytest.mark.parametrize("axes", [[0, 1] * 4, torch.tensor([0, 1] * 4), bytearray([0, 1] * 4)])
+def test_axes_as_any_sequence(axes):
+    x = torch.randn(5, 2, 16, generator=torch.Generator().manual_seed(4)).cuda()
+    pos = torch.arange(10, device="cuda").view(2, 5)
+    a, b = torch.empty_like(x), torch.empty_like(x)
+    L.oomb_bias_rope_axes(x, None, a, 2, pos, bytes([0, 1] * 4), 1e4, 1)
+    L.oomb_bias_rope_axes(x, None, b, 2, pos, axes, 1e4, 1)
+    assert torch.equal(a, b)
+    with pytest.raises(TypeError):  # a number of axes is not a list of them
+        L.oomb_bias_rope_axes(x, None, b, 2, pos, 8, 1e4, 1)

@@ -506,3 +506,36 @@ def test_rows_behind_the_last_and_buffers_around_are_left_alone():
     first = min(c.sel[0]) * 128
     assert not dk[:first].any() and not dv[:first].any() and not dk[637:].any() and not dv[637:].any()
     c.pool.close()
+
+
+@pytest.mark.parametrize("dtype,n_q", [(BF, 5), (BF, 300), (FP, 130)])
+def test_offsets_past_32_bits(dtype, n_q):
+    """Pages whose elements stand more than 2^31 from the pools' start."""
+    H, pages, chunk = 8, 16500, 125
+    g = torch.Generator().manual_seed(11)
+    k, v = (torch.randn(chunk * 128, H, 128, generator=g).to(dtype) for _ in range(2))
+    q, do = (torch.randn(n_q, H, 128, generator=g).to(dtype) for _ in range(2))
+    pool = PagedKVPool(H, H, 128, 128, pages, pages, dtype)
+    kd, vd = k.cuda(), v.cuda()
+    for first in range(0, pages, chunk):
+        L.oomb_kv_append(pool.handle, kd, vd, first * 128)
+    sel = [0, 7, 16390, 16444] + list(range(pages - 3, pages))
+    q0 = pages * 128 - n_q
+    dsel = torch.tensor([sel] * H, dtype=torch.int32).cuda()
+    cnt = torch.full((H,), len(sel), dtype=torch.int32).cuda()
+    qd, o, dq = q.cuda(), torch.empty_like(q, device="cuda"), torch.empty_like(q, device="cuda")
+    lse = torch.empty(H, n_q, device="cuda")
+    a = (q0, dsel, cnt, 0.09)
+    L.oomb_score_attn_fwd(pool.handle, qd, *a, o, lse, pool.workspace(L.OOMB_OP_SCORE_FWD, n_q), softcap=12.0)
+    L.oomb_score_attn_bwd(pool.handle, qd, o, do.cuda(), lse, *a, dq, pool.workspace(L.OOMB_OP_SCORE_BWD, n_q),
+                          softcap=12.0)
+    assert L.oomb_check(pool.handle) == 0
+    # the same keys one after another: only the last pages are behind or beside the queries
+    kc, vc = (torch.cat([t[p % chunk * 128:p % chunk * 128 + 128] for p in sel]) for t in (k, v))
+    ref = score_attn(q, kc, vc, [list(range(len(sel)))] * H, 128, kc.shape[0] - n_q, 0.09, 12.0, do=do,
+                     tensor_cores=dtype == BF)
+    table = L.oomb_page_table_host(pool.handle, pages)
+    dk, dv = (torch.cat([t[table[p]].permute(1, 0, 2) for p in sel]) for t in (pool.dk_pool, pool.dv_pool))
+    for name, got in (("o", o), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        check(name, got, ref)
+    pool.close()
