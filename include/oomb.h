@@ -377,7 +377,8 @@ typedef struct {
  * that may run at once need one each.
  * Capturable in a CUDA graph (the number of tokens appended is the one at capture).
  * Errors: ARG (also a softcap that is negative, not a number, above 1e30 or below
- * 1e-30 |softmax_scale|), ALIGN, WORKSPACE, CUDA. */
+ * 1e-30 |softmax_scale|), ALIGN, WORKSPACE, CUDA; UNSUPPORTED for shapes that
+ * oomb_uses_tensor_cores denies, from 2^31 - page_size tokens on. */
 OOMB_API oomb_status oomb_score_attn_fwd(oomb_pool* pool, const void* q, int64_t q_start, int n_q, const int32_t* sel,
                                          const int32_t* sel_count, int max_sel, float softmax_scale,
                                          const oomb_score_mod* mod, void* o, float* lse, void* workspace,

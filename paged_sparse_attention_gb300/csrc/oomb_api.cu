@@ -545,6 +545,8 @@ static oomb_status make_score_args(oomb_pool* p, const void* q, int64_t q_start,
   if (q_start > p->n_tokens || n_q > p->n_tokens - q_start) return OOMB_ERR_ARG;  // own K/V appended
   if (!aligned(q, 16) || !aligned(sel, 4) || !aligned(sel_count, 4)) return OOMB_ERR_ALIGN;
   if (p->d.offload && max_sel > p->d.stage_max_sel) return OOMB_ERR_ARG;
+  // the CUDA-core kernels hold positions in 32 bits
+  if (!tc_supported(p->g) && p->n_tokens > INT_MAX - p->g.P) return OOMB_ERR_UNSUPPORTED;
   if (need > 0 && (!ws || ws_bytes < need)) return OOMB_ERR_WORKSPACE;
   if (ws && !aligned(ws, 16)) return OOMB_ERR_ALIGN;
   std::memset(s, 0, sizeof(*s));

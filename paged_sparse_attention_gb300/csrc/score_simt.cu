@@ -38,31 +38,34 @@ constexpr int kKeys = 64;   // keys of a tile
 constexpr int kThreads = 256;
 constexpr int kMaxD = 128;
 constexpr int kLdP = kKeys + 4;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxParts = 1024;  // of a split forward; 32 on this path, 2 an SM at most on the tensor cores
 
 // fp32 tiles in shared memory: row length d padded to a multiple of 4 plus 4, so that rows
 // start on 16 bytes and 8 rows one apart fall into different banks.
 __host__ __device__ constexpr int tile_ld(int d) { return d + 4; }
 
+// Positions are 32-bit here (the launchers refuse more tokens).
 struct KeyList {
-  int64_t pos[kKeys];  // token position, -1: no key
+  int32_t pos[kKeys];  // token position, -1: no key
   int64_t off[kKeys];  // element offset of the row in the pools, -1: no key
 };
 
 // Keys v0 .. v0 + 63 of the selection's token sequence (entry v / P, token v % P); a key
 // outside positions [lo, hi) is left out, so whatever stands there (a NaN, say) stays there.
-__device__ __forceinline__ void list_keys(const ScoreArgs& s, int h, int64_t v0, int64_t v1, int64_t lo, int64_t hi,
+__device__ __forceinline__ void list_keys(const ScoreArgs& s, int h, int64_t v0, int64_t v1, int lo, int hi,
                                           KeyList* kl) {
   const int P = s.a.g.P;
   if (threadIdx.x < kKeys) {
     const int64_t v = v0 + threadIdx.x;
-    int64_t pos = -1, off = -1;
+    int32_t pos = -1;
+    int64_t off = -1;
     if (v < v1) {
       const int j = (int)(v / P), t = (int)(v % P);
       const int p = s.a.sel[(size_t)h * s.a.max_sel + j];
       const int64_t blk = score_block(s, h, j, p), at = (int64_t)p * P + t;
       if (blk >= 0 && at >= lo && at < hi) {
-        pos = at;
+        pos = (int32_t)at;
         off = (blk * P + t) * s.a.g.d;
       }
     }
@@ -108,25 +111,34 @@ __device__ __forceinline__ void load_rows(const ScoreArgs& s, const void* src, i
   }
 }
 
-// acc[r][c] = A[ty + 16 r] . B[tx + 16 c] over d columns (d is a multiple of 4).
+// acc[r][c] = A[ty + 16 r] . B[tx + 16 c] over d columns (d is a multiple of 4).  Even and odd
+// columns are summed apart, two products an instruction: half the instructions to issue.
 __device__ __forceinline__ void dot_tile(const float* A, const float* B, int d, int ty, int tx, float (&acc)[4][4]) {
   const int ld = tile_ld(d);
+  uint64_t sum[4][4];
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[r][c] = 0.f;
+    for (int c = 0; c < 4; ++c) sum[r][c] = 0;
   for (int e = 0; e < d; e += 4) {
-    float4 x[4], y[4];
+    ulonglong2 x[4], y[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) x[r] = *reinterpret_cast<const float4*>(A + (ty + 16 * r) * ld + e);
+    for (int r = 0; r < 4; ++r) x[r] = *reinterpret_cast<const ulonglong2*>(A + (ty + 16 * r) * ld + e);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const float4*>(B + (tx + 16 * c) * ld + e);
+    for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const ulonglong2*>(B + (tx + 16 * c) * ld + e);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        acc[r][c] += x[r].x * y[c].x + x[r].y * y[c].y + x[r].z * y[c].z + x[r].w * y[c].w;
+      for (int c = 0; c < 4; ++c) sum[r][c] = fma2(x[r].y, y[c].y, fma2(x[r].x, y[c].x, sum[r][c]));
   }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float even, odd;
+      f32x2_split(sum[r][c], even, odd);
+      acc[r][c] = even + odd;
+    }
 }
 
 // acc[r][c] (columns 4 tx + 64 c) += sum_j W[ty + 16 r][j] X[j], j over 64 rows of X.
@@ -159,37 +171,53 @@ __device__ __forceinline__ void weigh_rows(const float* W, const float* X, int d
   }
 }
 
-// Modified score of raw dot product `dot`, and tanh of the capped argument in *t (0 uncapped).
-__device__ __forceinline__ float modify(float dot, float scale, float cap, float slope, int64_t qpos, int64_t kpos,
-                                        float* t) {
-  float x = dot * scale;
+// Scores in units of log2 (s2 = s log2 e), formed from the raw dot product.
+struct ScoreForm {
+  float k;       // capped: scale / cap, else scale log2 e
+  float cap2;    // cap log2 e; 0: not capped
+  float slope2;  // slope log2 e
+};
+__device__ __forceinline__ ScoreForm score_form(const ScoreArgs& s, int hq) {
+  return {s.cap > 0.f ? s.a.scale / s.cap : s.a.scale * kLog2e, s.cap * kLog2e, s.slopes ? s.slopes[hq] * kLog2e : 0.f};
+}
+// tanh: to |x| = 0.6 a polynomial in x^2 fitted for the least relative error of tanh(x) / x
+// (2.5e-9), from there 1 - 2 / (1 + e^2x).  Both are formed: the lanes of a warp differ.
+__device__ __forceinline__ float score_tanh(float x) {
+  const float z = x * x;
+  float p = fmaf(-0.00585216861f, z, 0.0207536292f);
+  p = fmaf(p, z, -0.0537687049f);
+  p = fmaf(p, z, 0.13331689f);
+  p = fmaf(p, z, -0.333332833f);
+  const float far = fmaf(-2.f, rcp_approx(1.f + ex2_approx(2.f * kLog2e * x)), 1.f);
+  return fabsf(x) <= 0.6f ? fmaf(x * z, p, x) : far;
+}
+// The modified score, and in *t the tanh (0 uncapped).
+__device__ __forceinline__ float modify(float dot, const ScoreForm& f, int dist, float* t) {
+  float x = dot * f.k;
   *t = 0.f;
-  if (cap > 0.f) {
-    *t = tanhf(x / cap);
-    x = cap * *t;
+  if (f.cap2 > 0.f) {
+    *t = score_tanh(x);
+    x = f.cap2 * *t;
   }
-  if (slope != 0.f) {
-    const int64_t dist = qpos > kpos ? qpos - kpos : kpos - qpos;
-    x -= slope * (float)dist;
-  }
+  if (f.slope2 != 0.f) x = fmaf(-f.slope2, (float)abs(dist), x);
   return x;
 }
 
 // Ranges of the tile's rows in shared memory and the union [lo, hi) of the non-empty ones.
 struct RowSpans {
-  int64_t b[kRows], e[kRows];
-  int64_t lo, hi;
+  int32_t b[kRows], e[kRows];
+  int32_t lo, hi;
 };
 __device__ __forceinline__ void load_spans(const ScoreArgs& s, int i0, RowSpans* rs) {
   if (threadIdx.x < kRows) {
     int64_t b = 0, e = 0;
     if (i0 + (int)threadIdx.x < s.a.n_q) row_span(s, i0 + threadIdx.x, b, e);
-    rs->b[threadIdx.x] = b;
-    rs->e[threadIdx.x] = e;
+    rs->b[threadIdx.x] = (int32_t)b;
+    rs->e[threadIdx.x] = (int32_t)e;
   }
   __syncthreads();
   if (threadIdx.x < 32) {
-    int64_t lo = INT64_MAX, hi = 0;
+    int32_t lo = INT_MAX, hi = 0;
     for (int r = threadIdx.x; r < kRows; r += 32)
       if (rs->e[r] > rs->b[r]) {
         lo = min(lo, rs->b[r]);
@@ -233,9 +261,9 @@ __global__ void __launch_bounds__(kThreads, 2) score_fwd_simt(const __grid_const
   const int64_t n_tiles = ((int64_t)(j1 - j0) * P + kKeys - 1) / kKeys;
   const int64_t t0 = n_tiles * blockIdx.z / s.n_split, t1 = n_tiles * (blockIdx.z + 1) / s.n_split;
   const int64_t v_end = (int64_t)j1 * P;
-  const float slope = s.slopes ? s.slopes[hq] : 0.f;
+  const ScoreForm form = score_form(s, hq);
 
-  float m[4], l[4];
+  float m[4], l[4];  // m in units of log2
   float4 o[4][C];
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -255,25 +283,26 @@ __global__ void __launch_bounds__(kThreads, 2) score_fwd_simt(const __grid_const
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = ty + 16 * r;
-      const int64_t b = rs.b[row], e = rs.e[row], qpos = s.a.q_start + i0 + row;
+      const int b = rs.b[row], e = rs.e[row], qpos = (int)s.a.q_start + i0 + row;
       float mx = -INFINITY;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const int64_t kpos = kl.pos[tx + 16 * c];
+        const int kpos = kl.pos[tx + 16 * c];
         float th;
         const bool see = kpos >= b && kpos < e;  // an absent key has position -1
-        x[r][c] = see ? modify(x[r][c], s.a.scale, s.cap, slope, qpos, kpos, &th) : -INFINITY;
+        const float v = modify(x[r][c], form, qpos - kpos, &th);
+        x[r][c] = see ? v : -INFINITY;
         mx = fmaxf(mx, x[r][c]);
       }
 #pragma unroll
       for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
       const float m_new = fmaxf(m[r], mx);
       const float shift = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = expf(m[r] - shift);  // 0 while the row has seen nothing
+      const float alpha = ex2_approx(m[r] - shift);  // 0 while the row has seen nothing
       float sum = 0.f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const float p = expf(x[r][c] - shift);
+        const float p = ex2_approx(x[r][c] - shift);
         sp[row * kLdP + tx + 16 * c] = p;
         sum += p;
       }
@@ -297,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_fwd_simt(const __grid_const
     const int i = i0 + ty + 16 * r;
     if (i >= s.a.n_q) continue;
     const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
-    const float lse = l[r] > 0.f ? m[r] + logf(l[r]) : -INFINITY;
+    const float lse = l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 : -INFINITY;
     const size_t rh = (size_t)i * s.a.g.Hq + hq;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -428,22 +457,21 @@ __global__ void __launch_bounds__(256) score_dot(const ScoreArgs s, float* __res
 // dK/dV kernel, [key][row].
 template <bool KEY_MAJOR>
 __device__ __forceinline__ void probs_tile(const ScoreArgs& s, const float (&x)[4][4], const float (&dp)[4][4],
-                                           const RowSpans* rs, const KeyList* kl, const float* slse, const float* sD,
-                                           float slope, int i0, int ty, int tx, float* sp, float* sda) {
+                                           const RowSpans* rs, const KeyList* kl, const float* slse2, const float* sD,
+                                           const ScoreForm& form, int i0, int ty, int tx, float* sp, float* sda) {
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int row = ty + 16 * r;
-    const int64_t b = rs->b[row], e = rs->e[row], qpos = s.a.q_start + i0 + row;
+    const int b = rs->b[row], e = rs->e[row], qpos = (int)s.a.q_start + i0 + row;
+    const float lse2 = slse2[row], D = sD[row];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int key = tx + 16 * c;
-      const int64_t kpos = kl->pos[key];
-      float p = 0.f, da = 0.f;
-      if (kpos >= b && kpos < e && slse[row] > -INFINITY) {
-        float t;
-        p = expf(modify(x[r][c], s.a.scale, s.cap, slope, qpos, kpos, &t) - slse[row]);
-        da = p * (dp[r][c] - sD[row]) * (1.f - t * t);
-      }
+      const int key = tx + 16 * c, kpos = kl->pos[key];
+      const bool see = kpos >= b && kpos < e;
+      float t, p = ex2_approx(modify(x[r][c], form, qpos - kpos, &t) - lse2);
+      float da = p * (dp[r][c] - D) * fmaf(-t, t, 1.f);
+      p = see ? p : 0.f;
+      da = see ? da : 0.f;
       const int at = KEY_MAJOR ? key * kLdP + row : row * kLdP + key;
       if (sp) sp[at] = p;
       sda[at] = da;
@@ -451,11 +479,13 @@ __device__ __forceinline__ void probs_tile(const ScoreArgs& s, const float (&x)[
   }
 }
 
-__device__ __forceinline__ void load_stats(const ScoreArgs& s, const float* Dbuf, int i0, int hq, float* slse,
+// LSE in units of log2, infinite for rows without keys.
+__device__ __forceinline__ void load_stats(const ScoreArgs& s, const float* Dbuf, int i0, int hq, float* slse2,
                                            float* sD) {
   if (threadIdx.x < kRows) {
     const int i = i0 + threadIdx.x;
-    slse[threadIdx.x] = i < s.a.n_q ? s.a.lse_in[(size_t)hq * s.a.n_q + i] : -INFINITY;
+    const float lse = i < s.a.n_q ? s.a.lse_in[(size_t)hq * s.a.n_q + i] : -INFINITY;
+    slse2[threadIdx.x] = lse > -INFINITY ? lse * kLog2e : INFINITY;
     sD[threadIdx.x] = i < s.a.n_q ? Dbuf[(size_t)hq * s.a.n_q + i] : 0.f;
   }
 }
@@ -467,7 +497,7 @@ size_t dkdv_smem(int d) { return (size_t)(4 * kKeys * tile_ld(d) + 2 * kRows * k
 // block owns and is left out.
 __device__ __forceinline__ void list_owned_keys(const ScoreArgs& s, int h, int64_t v0, int64_t v1, int count,
                                                 KeyList* kl) {
-  list_keys(s, h, v0, v1, 0, s.total, kl);
+  list_keys(s, h, v0, v1, 0, (int)s.total, kl);
   if (threadIdx.x < kKeys && kl->pos[threadIdx.x] >= 0) {
     const int j = (int)((v0 + threadIdx.x) / s.a.g.P);
     const int32_t* row = s.a.sel + (size_t)h * s.a.max_sel;
@@ -503,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
   const int j1 = rs.hi > rs.lo ? first_entry(s.a, h, count, (rs.hi + P - 1) / P) : j0;
   const int64_t n_tiles = ((int64_t)(j1 - j0) * P + kKeys - 1) / kKeys;
   const int64_t t0 = n_tiles * blockIdx.z / n_split, t1 = n_tiles * (blockIdx.z + 1) / n_split;
-  const float slope = s.slopes ? s.slopes[hq] : 0.f;
+  const ScoreForm form = score_form(s, hq);
   float4 dq[4][C];
 #pragma unroll
   for (int r = 0; r < 4; ++r)
@@ -518,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
     float x[4][4], dp[4][4];
     dot_tile(sq, sk, d, ty, tx, x);
     dot_tile(sdo, sv, d, ty, tx, dp);
-    probs_tile<false>(s, x, dp, &rs, &kl, slse, sD, slope, i0, ty, tx, nullptr, sda);
+    probs_tile<false>(s, x, dp, &rs, &kl, slse, sD, form, i0, ty, tx, nullptr, sda);
     __syncthreads();
     weigh_rows(sda, sk, d, ty, tx, dq);
   }
@@ -564,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
   __shared__ KeyList kl;
   __shared__ RowSpans rs;
   __shared__ float slse[kRows], sD[kRows];
-  __shared__ int64_t key_lo, key_hi;
+  __shared__ int key_lo, key_hi;
   __shared__ int t_first, t_last;
   const int count = sel_count_checked(s.a, h);
   const int64_t v0 = (int64_t)blockIdx.x * kKeys, v1 = (int64_t)count * P;
@@ -572,8 +602,8 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
   list_owned_keys(s, h, v0, v1, count, &kl);
   __syncthreads();
   if (threadIdx.x < 32) {
-    const int64_t p = kl.pos[threadIdx.x], q = kl.pos[threadIdx.x + 32];
-    int64_t lo = min(p < 0 ? INT64_MAX : p, q < 0 ? INT64_MAX : q), hi = max(p, q);
+    const int p = kl.pos[threadIdx.x], q = kl.pos[threadIdx.x + 32];
+    int lo = min(p < 0 ? INT_MAX : p, q < 0 ? INT_MAX : q), hi = max(p, q);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
@@ -643,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
       float x[4][4], dp[4][4];
       dot_tile(sq, sk, d, ty, tx, x);
       dot_tile(sdo, sv, d, ty, tx, dp);
-      probs_tile<true>(s, x, dp, &rs, &kl, slse, sD, s.slopes ? s.slopes[hq] : 0.f, i0, ty, tx, sp, sda);
+      probs_tile<true>(s, x, dp, &rs, &kl, slse, sD, score_form(s, hq), i0, ty, tx, sp, sda);
       __syncthreads();
       weigh_rows(sp, sdo, d, ty, tx, dv);
       weigh_rows(sda, sq, d, ty, tx, dk);

@@ -42,12 +42,6 @@ inline CapConst make_cap(float cap, float scale) {
   return c;
 }
 
-// 1 / x to one unit in the last place or so (x >= 1 here; infinity gives 0).
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 enum TanhForm { kDegree2, kDegree3, kWide };
 
 template <TanhForm F>

@@ -834,12 +834,13 @@ cudaError_t launch_score_fwd_tc(ScoreArgs& s, cudaStream_t st) {
   p.n_tiles = (s.a.n_q + kTile - 1) / kTile;
   p.n_pairs = pack ? 1 : (p.n_tiles + 1) / 2;
   if (pack) {
-    // one block per SM, as long as each has a page for either tile; up to 16 pages a block each:
-    // one of its tiles then idles, but the shorter walk counts for more.  28 query heads on 4,
-    // 1 row and 18: 4 pages 9.5 and 13.1 us in 4 blocks, 10.1 and 15.7 in 2; 16 pages 10.9 and 14.8
-    // in 16, 10.9 and 16.7 in 8; 64 pages 13.2 and 19.8 in 32, 13.9 and 20.1 in 16
-    const int pages = s.a.max_sel;
-    s.n_split = std::min(limit / 2, std::max((pages + 1) / 2, std::min(pages, 16)));
+    // one block per SM, as long as each has a page for either tile (two where the parts are of many
+    // rows); up to 16 pages a block each: one of its tiles then idles, but the shorter walk counts
+    // for more.  28 query heads on 4, 1 row and 18: 4 pages 9.5 and 13.1 us in 4 blocks, 10.1 and 15.7
+    // in 2; 16 pages 10.9 and 14.8 in 16, 10.9 and 16.7 in 8; 64 pages 13.2 and 19.8 in 32, 13.9 and
+    // 20.1 in 16 (from a cold L2 25.6 and 24.4 for 17 rows)
+    const int pages = s.a.max_sel, each = (int64_t)s.a.n_q * g.Hq > 256 ? 4 : 2;
+    s.n_split = std::min(limit / 2, std::max((pages + each - 1) / each, std::min(pages, 16)));
   } else {
     // Waves of blocks, each as long as its pages and about four more for set-up and epilogue; once
     // the keys are cut, the join takes as long as two pages and one more for every 8000 rows of

@@ -316,6 +316,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// 1 / x to one unit in the last place or so (infinity gives 0).
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Packed fp32x2 arithmetic (one instruction for two lanes of a 64-bit register pair)
 // and the three-input max of sm_100+.
 __device__ __forceinline__ uint64_t f32x2(uint32_t lo, uint32_t hi) {
@@ -351,6 +358,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
+// a b + c of both halves of a pair, denormals kept
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
 // max(|a|, |b|, |c|)
 __device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
   float d;
