@@ -364,11 +364,6 @@ __device__ __forceinline__ void ring_start(const RowRing& r, uint8_t* base, Ring
 
 // Packed pairs of fp32 (two elements an instruction): a row's work is bound by instructions as
 // much as by its bytes.
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ uint64_t both(float v) { return f32x2(v, v); }
 __device__ __forceinline__ float halves(uint64_t v) {
   float a, b;

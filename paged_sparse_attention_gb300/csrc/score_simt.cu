@@ -141,11 +141,11 @@ __device__ __forceinline__ void dot_tile(const float* A, const float* B, int d, 
     }
 }
 
-// acc[r][c] (columns 4 tx + 64 c) += sum_j W[ty + 16 r][j] X[j], j over 64 rows of X.
-// C: groups of 64 columns a row has (1 for d <= 64, else 2).
+// acc[r][c] (columns 4 tx + 64 c) += sum_j W[ty + 16 r][j] X[j], j over 64 rows of X; two columns an
+// instruction.  C: groups of 64 columns a row has (1 for d <= 64, else 2).
 template <int C>
 __device__ __forceinline__ void weigh_rows(const float* W, const float* X, int d, int ty, int tx,
-                                           float4 (&acc)[4][C]) {
+                                           ulonglong2 (&acc)[4][C]) {
   const int ld = tile_ld(d);
   for (int j = 0; j < 64; j += 4) {
     float4 w[4];
@@ -157,18 +157,23 @@ __device__ __forceinline__ void weigh_rows(const float* W, const float* X, int d
       if (col >= d) continue;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float4 x = *reinterpret_cast<const float4*>(X + (j + u) * ld + col);
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(X + (j + u) * ld + col);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float p = u == 0 ? w[r].x : u == 1 ? w[r].y : u == 2 ? w[r].z : w[r].w;
-          acc[r][c].x += p * x.x;
-          acc[r][c].y += p * x.y;
-          acc[r][c].z += p * x.z;
-          acc[r][c].w += p * x.w;
+          const uint64_t pp = f32x2(p, p);
+          acc[r][c].x = fma2(pp, x.x, acc[r][c].x);
+          acc[r][c].y = fma2(pp, x.y, acc[r][c].y);
         }
       }
     }
   }
+}
+__device__ __forceinline__ float4 unpaired(const ulonglong2& v) {
+  float4 f;
+  f32x2_split(v.x, f.x, f.y);
+  f32x2_split(v.y, f.z, f.w);
+  return f;
 }
 
 // Scores in units of log2 (s2 = s log2 e), formed from the raw dot product.
@@ -264,13 +269,13 @@ __global__ void __launch_bounds__(kThreads, 2) score_fwd_simt(const __grid_const
   const ScoreForm form = score_form(s, hq);
 
   float m[4], l[4];  // m in units of log2
-  float4 o[4][C];
+  ulonglong2 o[4][C];
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     m[r] = -INFINITY;
     l[r] = 0.f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < C; ++c) o[r][c] = make_ulonglong2(0, 0);
   }
   for (int64_t t = t0; t < t1; ++t) {
     __syncthreads();
@@ -312,10 +317,8 @@ __global__ void __launch_bounds__(kThreads, 2) score_fwd_simt(const __grid_const
       m[r] = m_new;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        o[r][c].x *= alpha;
-        o[r][c].y *= alpha;
-        o[r][c].z *= alpha;
-        o[r][c].w *= alpha;
+        o[r][c].x = mul2(o[r][c].x, f32x2(alpha, alpha));
+        o[r][c].y = mul2(o[r][c].y, f32x2(alpha, alpha));
       }
     }
     __syncthreads();
@@ -332,7 +335,8 @@ __global__ void __launch_bounds__(kThreads, 2) score_fwd_simt(const __grid_const
     for (int c = 0; c < C; ++c) {
       const int col = 4 * tx + 64 * c;
       if (col >= d) continue;
-      const float v[4] = {o[r][c].x * inv, o[r][c].y * inv, o[r][c].z * inv, o[r][c].w * inv};
+      const float4 w = unpaired(o[r][c]);
+      const float v[4] = {w.x * inv, w.y * inv, w.z * inv, w.w * inv};
       if (s.n_split > 1) {
         float* dst = s.part_o + ((size_t)blockIdx.z * s.a.n_q * s.a.g.Hq + rh) * d + col;
 #pragma unroll
@@ -534,11 +538,11 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
   const int64_t n_tiles = ((int64_t)(j1 - j0) * P + kKeys - 1) / kKeys;
   const int64_t t0 = n_tiles * blockIdx.z / n_split, t1 = n_tiles * (blockIdx.z + 1) / n_split;
   const ScoreForm form = score_form(s, hq);
-  float4 dq[4][C];
+  ulonglong2 dq[4][C];
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int c = 0; c < C; ++c) dq[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < C; ++c) dq[r][c] = make_ulonglong2(0, 0);
   for (int64_t t = t0; t < t1; ++t) {
     __syncthreads();
     list_keys(s, h, (int64_t)j0 * P + t * kKeys, (int64_t)j1 * P, rs.lo, rs.hi, &kl);
@@ -561,15 +565,16 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
       const int col = 4 * tx + 64 * c;
       if (col >= d) continue;
       const size_t at = ((size_t)i * s.a.g.Hq + hq) * d + col;
+      const float4 v = unpaired(dq[r][c]);
       if (n_split > 1) {
-        *reinterpret_cast<float4*>(part + (size_t)blockIdx.z * s.a.n_q * s.a.g.Hq * d + at) = dq[r][c];
+        *reinterpret_cast<float4*>(part + (size_t)blockIdx.z * s.a.n_q * s.a.g.Hq * d + at) = v;
         continue;
       }
       T* dst = reinterpret_cast<T*>(s.a.dq) + at;
-      dst[0] = from_float<T>(dq[r][c].x * s.a.scale);
-      dst[1] = from_float<T>(dq[r][c].y * s.a.scale);
-      dst[2] = from_float<T>(dq[r][c].z * s.a.scale);
-      dst[3] = from_float<T>(dq[r][c].w * s.a.scale);
+      dst[0] = from_float<T>(v.x * s.a.scale);
+      dst[1] = from_float<T>(v.y * s.a.scale);
+      dst[2] = from_float<T>(v.z * s.a.scale);
+      dst[3] = from_float<T>(v.w * s.a.scale);
     }
   }
 }
@@ -652,11 +657,11 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
   }
   load_keys<T>(s, &kl, sk, sv);
   bool seen = false;
-  float4 dk[4][C], dv[4][C];
+  ulonglong2 dk[4][C], dv[4][C];
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int c = 0; c < C; ++c) dk[r][c] = dv[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < C; ++c) dk[r][c] = dv[r][c] = make_ulonglong2(0, 0);
   for (int tile = u0 / G; tile * G < u1; ++tile) {
     const int i0 = (t_first + tile) * kRows;
     __syncthreads();
@@ -690,8 +695,8 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
       for (int c = 0; c < C; ++c) {
         const int col = 4 * tx + 64 * c;
         if (col >= d) continue;
-        *reinterpret_cast<float4*>(dst + key * d + col) = dk[r][c];
-        *reinterpret_cast<float4*>(dst + (kKeys + key) * d + col) = dv[r][c];
+        *reinterpret_cast<float4*>(dst + key * d + col) = unpaired(dk[r][c]);
+        *reinterpret_cast<float4*>(dst + (kKeys + key) * d + col) = unpaired(dv[r][c]);
       }
       continue;
     }
@@ -706,14 +711,15 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
       float4* gk = reinterpret_cast<float4*>(s.a.dk_pool + base + col);
       float4* gv = reinterpret_cast<float4*>(s.a.dv_pool + base + col);
       float4 a = *gk, b = *gv;
-      a.x += s.a.scale * dk[r][c].x;
-      a.y += s.a.scale * dk[r][c].y;
-      a.z += s.a.scale * dk[r][c].z;
-      a.w += s.a.scale * dk[r][c].w;
-      b.x += dv[r][c].x;
-      b.y += dv[r][c].y;
-      b.z += dv[r][c].z;
-      b.w += dv[r][c].w;
+      const float4 k4 = unpaired(dk[r][c]), v4 = unpaired(dv[r][c]);
+      a.x += s.a.scale * k4.x;
+      a.y += s.a.scale * k4.y;
+      a.z += s.a.scale * k4.z;
+      a.w += s.a.scale * k4.w;
+      b.x += v4.x;
+      b.y += v4.y;
+      b.z += v4.z;
+      b.w += v4.w;
       *gk = a;
       *gv = b;
     }

@@ -358,10 +358,15 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
-// a b + c of both halves of a pair, denormals kept
+// a b + c and a b of both halves of a pair, denormals kept
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 // max(|a|, |b|, |c|)
