@@ -3,8 +3,7 @@
 // take; also the join of split forwards and the document ranges.
 //
 // Tiles of 64 query rows x 64 keys, 256 threads, a 4 x 4 block of scores per thread: each
-// 16-byte read of shared memory feeds 8 multiply-adds, so the kernels are bound by the
-// FMA pipe and not by shared memory.  The keys of a tile are 64 consecutive tokens of the
+// 16-byte read of shared memory feeds 8 multiply-adds.  The keys of a tile are 64 consecutive tokens of the
 // selected pages written one after another, so a page may be of any size: a tile can hold
 // several small pages or a part of a large one.  Rows whose range is empty, or meets no
 // selected page, get O = 0 and LSE = -inf and send no gradient.
@@ -21,9 +20,11 @@
 //                    not fill the SMs
 //
 // Shares against none, fp32, 1024 rows of 2 heads on 4096 tokens in documents of 1000, forward and
-// backward with its joins: 185 us against 717.  Of it the forward 36, dQ 45, dK/dV 66 and the joins
-// 28: a block holds 8 warps of 125 registers, two blocks an SM, and waits for shared memory (issue
-// 44 %); a 64 x 64 tile of dK/dV takes 15 us of one block, a third of its share of the FMA pipe.
+// backward with its joins: 150 us against 539.  Of it the forward 31, dQ 37, dK/dV 53, each with a
+// block or two an SM, and the joins 25.  With more rows, 900 of 6 heads on 3000 keys: 172 us (20 of
+// the FMA pipe's 74 TFLOP/s) and 483 (25 with the scores that both passes form).  Bound by shared
+// memory, its reads and their latency at two blocks of 8 warps an SM (128 registers); 8 x 4 scores
+// a thread (194 / 513) and, for d > 64, 2 x 4 (1515 against 1175 backward) are slower.
 #include <climits>
 #include <cmath>
 
@@ -749,6 +750,12 @@ __global__ void __launch_bounds__(256) score_dq_join(const __grid_constant__ Sco
   dst[3] = from_float<T>(acc.w * s.a.scale);
 }
 
+// Ranges leave an unknown part of the key tiles without rows, so dK/dV are cut into this many blocks
+// an SM slot: those without rows leave at once, the others still fill the SMs (1024 fp32 rows in
+// documents on 4096 tokens: 1 184 us, 2 134, 4 125, 6 120 with more to join).
+constexpr int kDkdvFill = 4;
+constexpr int kMaxShares = 2048;
+
 // dK += scale * sum of the shares, dV += sum of the shares, for 64 / gridDim.z of a tile's keys.
 __global__ void __launch_bounds__(256) score_dkdv_join(const __grid_constant__ ScoreArgs s,
                                                        const float* __restrict__ part,
@@ -760,9 +767,22 @@ __global__ void __launch_bounds__(256) score_dkdv_join(const __grid_constant__ S
   if (v0 >= v1) return;
   const size_t tile = 2 * (size_t)kKeys * d, shares = (size_t)gridDim.y * gridDim.x;
   const size_t slot = (size_t)h * gridDim.x + blockIdx.x;
-  bool mine = false;
-  for (int z = threadIdx.x; z < n_split; z += blockDim.x) mine |= flags[z * shares + slot] != 0;
-  if (!__syncthreads_or(mine)) return;
+  // the shares that have seen a row, in order: the reads of several are then in flight at once
+  __shared__ uint16_t seen[kMaxShares];
+  __shared__ int n_seen;
+  if (threadIdx.x < 32) {
+    int n = 0;
+    for (int z0 = 0; z0 < n_split; z0 += 32) {
+      const int z = z0 + threadIdx.x;
+      const bool f = z < n_split && flags[z * shares + slot] != 0;
+      const unsigned mask = __ballot_sync(0xffffffffu, f);
+      if (f) seen[n + __popc(mask & ((1u << threadIdx.x) - 1u))] = (uint16_t)z;
+      n += __popc(mask);
+    }
+    if (threadIdx.x == 0) n_seen = n;
+  }
+  __syncthreads();
+  if (n_seen == 0) return;
   list_owned_keys(s, h, v0, v1, count, &kl);
   __syncthreads();
   const int keys = kKeys / gridDim.z, key0 = keys * blockIdx.z;
@@ -772,10 +792,9 @@ __global__ void __launch_bounds__(256) score_dkdv_join(const __grid_constant__ S
     if (kl.pos[key] < 0) continue;
     const float* src = part + slot * tile + (size_t)(is_k ? key : kKeys + key) * d + col;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int z = 0; z < n_split; ++z) {  // (loads of shares that have seen no row are left out, not waited for)
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (flags[z * shares + slot]) x = *reinterpret_cast<const float4*>(src + z * shares * tile);
+#pragma unroll 8
+    for (int i = 0; i < n_seen; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(src + seen[i] * shares * tile);
       acc.x += x.x;
       acc.y += x.y;
       acc.z += x.z;
@@ -850,9 +869,6 @@ cudaError_t fwd_simt(ScoreArgs& s, cudaStream_t st) {
 }
 
 // Backward: shares of a tile, so that the tiles fill the SMs (two blocks fit one for d <= 64).
-// Ranges leave an unknown part of the key tiles without rows, so dK/dV are cut finer: blocks
-// without rows cost nothing, the others still fill the SMs.
-constexpr int kDkdvFill = 4;
 struct BwdSplit {
   int dq, dkdv;
   size_t dq_bytes, dkdv_bytes;  // of the shares' sums
@@ -864,7 +880,7 @@ BwdSplit simt_bwd_split(const Geometry& g, int n_q, int max_sel) {
   const int64_t slots = simt_slots(g), row_tiles = (n_q + kRows - 1) / kRows;
   const int64_t key_tiles = ((int64_t)max_sel * g.P + kKeys - 1) / kKeys;
   b.dq = (int)std::min<int64_t>(std::max<int64_t>(1, slots / (row_tiles * g.Hq)), std::max<int64_t>(1, key_tiles / 2));
-  b.dkdv = (int)std::min<int64_t>(std::max<int64_t>(1, kDkdvFill * slots / (key_tiles * g.Hkv)), row_tiles * g.G);
+  b.dkdv = (int)std::min<int64_t>({std::max<int64_t>(1, kDkdvFill * slots / (key_tiles * g.Hkv)), row_tiles * g.G, kMaxShares});
   b.dq_bytes = b.dq > 1 ? align_up((size_t)b.dq * n_q * g.Hq * g.d * 4, 256) : 0;
   b.dkdv_bytes = b.dkdv > 1 ? (size_t)b.dkdv * key_tiles * g.Hkv * dkdv_tile_bytes(g) : 0;
   return b;
