@@ -20,14 +20,14 @@
 //
 // Two kinds of kernels: *_ring for many rows (below), which walk them with the next ones in flight,
 // and norm_fwd / norm_bwd, a row straight into registers.  8192 rows, forward / backward with its
-// join, direct against ring: bf16 of 3584 88 / 143 against 43 / 73 us, of 8192 214 / 312 against
-// 106 / 209; fp32 of 3577 116 / 262 against 86 / 188.  512 rows of 3584: 6.4 / 17.9 against 5.7 /
-// 16.2; 64 rows 3.1 / 8.5 against 3.7 / 8.6, so the forward takes the ring from one and a half
-// rows a block on.
+// join, direct against ring: bf16 of 3584 88 / 130 against 43 / 72 us, of 8192 213 / 285 against
+// 106 / 179; fp32 of 3577 117 / 235 against 87 / 147.  512 rows of 3584: 6.5 / 16.4 against 5.7 /
+// 15.3; 64 rows 3.1 / 8.0 against 3.7 / 8.3, so the forward takes the ring from one and a half rows a
+// block on.  The backward takes it wherever a stage fits: its sums then stay in registers.
 //
-// Bounds (GB300, 8192 rows of 3584 in bf16): forward 235 MB in 43 us, 5.4 TB/s; backward 352 MB
-// in 65 us, 5.4 TB/s, and 8 us of join: HBM with 80 % of the measured copy rate; the rest is the
-// two sums of a row, whose barriers two blocks an SM hide only in part (issue 61 %).
+// Bounds (GB300, 8192 rows of 3584 in bf16): forward 235 MB in 43 us, 5.5 TB/s; backward 352 MB
+// in 66 us, 5.3 TB/s, and the join: HBM with 80 % of the measured copy rate; the rest is the two
+// sums of a row, whose barriers two blocks an SM hide only in part (issue 61 %).
 #include <cmath>
 
 #include "attn_common.cuh"
@@ -199,8 +199,9 @@ __global__ void __launch_bounds__(1024, 1) norm_fwd(const __grid_constant__ Norm
 }
 
 // ----------------------------------------------------------------- backward
-// A block's three sums of a column, in shared memory: [dw_pre | dw_post | dgate] x D.  Each
-// column belongs to one thread.
+// A column's sums over the rows: du xn, which is dw_pre, and dx yn (times the token's gate), of which
+// dw_post and a channel's dgate are multiples.  A block holds its own, here in shared memory
+// ([2] x D, each column one thread's), and norm_join adds up those of the blocks.
 template <typename T, int E, bool VEC>
 __global__ void __launch_bounds__(1024, 1) norm_bwd(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) float acc[];
@@ -209,12 +210,11 @@ __global__ void __launch_bounds__(1024, 1) norm_bwd(const __grid_constant__ Norm
   int turn = 0;
   const Share<E, VEC> sh(a.D);
   const bool row_gate = a.gate && a.gate_rows;
-  const bool sum_gate = a.gate && !a.gate_rows && a.dgate;
   {
     float zero[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) zero[e] = 0.f;
-    for (int k = 0; k < 3; ++k) sh.template store<float>(acc + (size_t)k * a.D, zero);
+    for (int k = 0; k < 2; ++k) sh.template store<float>(acc + (size_t)k * a.D, zero);
   }
   for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
     const size_t row0 = (size_t)row * a.D;
@@ -263,12 +263,11 @@ __global__ void __launch_bounds__(1024, 1) norm_bwd(const __grid_constant__ Norm
     for (int e = 0; e < E; ++e) {
       const float dgz = a.res_scale * dx[e], dz = dgz * g[e];
       dg[e] = dgz * (z[e] * w[e]);
-      g[e] = dz * z[e];
+      g[e] = dx[e] * z[e] * (row_gate ? g[e] : 1.f);
       dx[e] = dz * w[e];
       s += dx[e] * z[e];
     }
-    if (a.w_post) sh.add(acc + a.D, g);
-    if (sum_gate) sh.add(acc + 2 * a.D, dg);
+    sh.add(acc + a.D, g);
     if (row_gate && a.dgate) sh.template store<T>(reinterpret_cast<T*>(a.dgate) + row0, dg);
     if (a.w_post) {
       const float mean = block_sum<32>(s, buf, turn) * a.inv_D;
@@ -277,37 +276,45 @@ __global__ void __launch_bounds__(1024, 1) norm_bwd(const __grid_constant__ Norm
     }
     if (a.dy) sh.template store<T>(reinterpret_cast<T*>(a.dy) + row0, dx);
   }
-  for (int k = 0; k < 3; ++k) {
+  for (int k = 0; k < 2; ++k) {
     float f[E];
     sh.template load<float>(acc + (size_t)k * a.D, f);
-    sh.template store<float>(a.part + ((size_t)blockIdx.x * 3 + k) * a.D, f);
+    sh.template store<float>(a.part + ((size_t)k * gridDim.x + blockIdx.x) * a.D, f);
   }
 }
 
-// Column sums over the blocks' parts, in block order: 32 columns a block, 16 strips of the
-// parts, one a warp, the strips joined in order.  out is dw_pre, dw_post or dgate (or nullptr).
-constexpr int kStrips = 16;
-__global__ void __launch_bounds__(32 * kStrips) norm_join(const float* __restrict__ part, int n_parts, int D,
-                                                          float* dw_pre, float* dw_post, float* dgate,
-                                                          int accumulate) {
+// The parameter gradients from the blocks' parts ([2][n_parts][D]), in block order: 32 columns a
+// block, one of the two sums, 32 strips of the parts, one a warp, joined in order.
+constexpr int kStrips = 32;
+__global__ void __launch_bounds__(32 * kStrips) norm_join(const __grid_constant__ NormArgs a, int n_parts) {
   __shared__ float strip[kStrips][33];
-  const int lane = threadIdx.x % 32, w = threadIdx.x / 32, k = blockIdx.y;
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32, D = a.D;
   const int c = blockIdx.x * 32 + lane;
-  float* out = k == 0 ? dw_pre : k == 1 ? dw_post : dgate;
-  if (!out) return;
+  const bool pre = blockIdx.y == 0;
+  float* dgate = a.gate_rows ? nullptr : reinterpret_cast<float*>(a.dgate);
+  if (pre ? !a.dw_pre : !a.dw_post && !dgate) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead: the parts are written from here on
+  const float* part = a.part + (size_t)blockIdx.y * n_parts * D + c;
   const int p0 = n_parts * w / kStrips, p1 = n_parts * (w + 1) / kStrips;
   float s = 0.f;
   if (c < D)
 #pragma unroll 10
-    for (int p = p0; p < p1; ++p) s += part[((size_t)p * 3 + k) * D + c];
+    for (int p = p0; p < p1; ++p) s += part[(size_t)p * D];
   strip[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < D) {
-    s = 0.f;
+  if (w != 0 || c >= D) return;
+  s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kStrips; ++i) s += strip[i][lane];
-    out[c] = accumulate ? out[c] + s : s;
+  for (int i = 0; i < kStrips; ++i) s += strip[i][lane];
+  auto put = [&](float* out, float v) {
+    if (out) out[c] = a.accumulate ? out[c] + v : v;
+  };
+  if (pre) {
+    put(a.dw_pre, s);
+  } else {
+    s *= a.res_scale;
+    put(a.dw_post, a.gate && !a.gate_rows ? s * reinterpret_cast<const float*>(a.gate)[c] : s);
+    put(dgate, a.w_post ? s * a.w_post[c] : s);
   }
 }
 
@@ -329,7 +336,7 @@ struct RowRing {
   int n_src;
   uint32_t row_bytes, pitch;  // of a row in memory, and from row to row in a stage
   int stages;
-  int64_t tail;  // row that the copies leave out (its end is no multiple of 16 bytes), or -1
+  uint32_t tail;  // row that the copies leave out (its end is no multiple of 16 bytes), or ~0
 };
 
 struct __align__(16) RingBars {
@@ -337,7 +344,7 @@ struct __align__(16) RingBars {
 };
 
 // A row's copy: the 16-byte units it lies in.
-__device__ __forceinline__ void ring_issue(const RowRing& r, uint8_t* base, RingBars* bars, int64_t row, int k) {
+__device__ __forceinline__ void ring_issue(const RowRing& r, uint8_t* base, RingBars* bars, uint32_t row, int k) {
   if (row == r.tail) {
     mbar_arrive(&bars->full[k]);
     return;
@@ -350,12 +357,12 @@ __device__ __forceinline__ void ring_issue(const RowRing& r, uint8_t* base, Ring
 }
 
 // Sets the ring up and starts the first rows' copies.
-__device__ __forceinline__ void ring_start(const RowRing& r, uint8_t* base, RingBars* bars, int64_t n) {
+__device__ __forceinline__ void ring_start(const RowRing& r, uint8_t* base, RingBars* bars, uint32_t n) {
   if (threadIdx.x == 0) {
     for (int k = 0; k < r.stages; ++k) mbar_init(&bars->full[k], 1);
     fence_mbar_init();
     for (int k = 0; k < r.stages; ++k) {
-      const int64_t row = blockIdx.x + (int64_t)k * gridDim.x;
+      const uint32_t row = blockIdx.x + (uint32_t)k * gridDim.x;
       if (row < n) ring_issue(r, base, bars, row, k);
     }
   }
@@ -374,8 +381,8 @@ __device__ __forceinline__ uint64_t unpack(uint32_t bf16x2) { return f32x2(bf16x
 
 // How a block's threads share a row through the ring.  VEC: 8 consecutive elements each, 16-byte
 // accesses.  Else pairs of elements, neighbouring threads on neighbouring pairs: rows of any
-// width, at any offset.  (8192 rows, backward: bf16 of 3584 73 against 115 us, fp32 128 against
-// 183; 16-byte accesses in two groups of four of fp32 162.)
+// width, at any offset.  (8192 rows of 3584 and of 3577, backward: bf16 72 and 117 us, fp32 124 and
+// 147.)
 template <bool VEC>
 struct Pairs {
   int D, first, step;
@@ -464,7 +471,7 @@ struct StageRow {
   const uint8_t* base;  // the stage, at the row's offset in its first 16-byte unit
   size_t at;            // bytes in front of the row in memory
   bool tail, even;      // even: pairs lie on their own size, in memory and in the stage
-  __device__ StageRow(const RowRing& ring, const uint8_t* stage_mem, int64_t row, int k)
+  __device__ StageRow(const RowRing& ring, const uint8_t* stage_mem, uint32_t row, int k)
       : r(ring), at((size_t)row * ring.row_bytes) {
     base = stage_mem + (size_t)k * ring.n_src * ring.pitch + (VEC ? 0 : at & 15);
     tail = !VEC && row == ring.tail;
@@ -490,7 +497,8 @@ __global__ void __launch_bounds__(THREADS, THREADS <= kNarrowFwd ? 2 : 1)
   int turn = 0, k = 0;
   uint32_t phase = 0;
   const Pairs<VEC> cols(a.D);
-  ring_start(ring, stage_mem, &bars, a.n);
+  const uint32_t n = (uint32_t)a.n;  // below 2^31: no sum of rows and blocks wraps
+  ring_start(ring, stage_mem, &bars, n);
   uint64_t cw[kPairs], w[kPairs];
   {
     uint64_t g[kPairs];
@@ -500,7 +508,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= kNarrowFwd ? 2 : 1)
     for (int e = 0; e < kPairs; ++e) cw[e] = mul2(both(a.res_scale), mul2(g[e], cw[e]));
     cols.param(a.w_pre, w);
   }
-  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+  for (uint32_t row = blockIdx.x; row < n; row += gridDim.x) {
     uint64_t f[kPairs], r[kPairs], g[kPairs];
 #pragma unroll
     for (int e = 0; e < kPairs; ++e) r[e] = g[e] = 0;
@@ -510,8 +518,8 @@ __global__ void __launch_bounds__(THREADS, THREADS <= kNarrowFwd ? 2 : 1)
     if (a.y) st.load(cols, 1, r);
     if (ROWGATE) st.load(cols, 2, g);
     __syncthreads();
-    const int64_t later = row + (int64_t)ring.stages * gridDim.x;
-    if (threadIdx.x == 0 && later < a.n) ring_issue(ring, stage_mem, &bars, later, k);
+    const uint32_t later = row + (uint32_t)ring.stages * gridDim.x;
+    if (threadIdx.x == 0 && later < n) ring_issue(ring, stage_mem, &bars, later, k);
     if (++k == ring.stages) {
       k = 0;
       phase ^= 1;
@@ -545,13 +553,16 @@ __global__ void __launch_bounds__(THREADS, THREADS <= kNarrowFwd ? 2 : 1)
   }
 }
 
-// With c as above and a = dx yn: dz yn = (res_scale gate) a and the gate's gradient is
-// (res_scale w_post) a, so for a gate per channel one sum over the rows of a gives both
-// parameter gradients.  The parameters stand in shared memory ([w_pre | c], fp32, a thread reads
+// c as above.  The parameters stand in shared memory ([w_pre | c], fp32, a thread reads
 // its own columns), the sums in registers.
 template <typename T, bool VEC, bool ROWGATE, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS <= kNarrowBwd ? 2 : 1)
     norm_bwd_ring(const __grid_constant__ NormArgs a, const __grid_constant__ RowRing ring) {
+  // EARLY: a row is taken into registers at once and its stage handed back.  Where registers are
+  // short (64, or the gate's row too), dx', the gate and c are read where they are used, twice if
+  // need be, and the stage goes back at the row's last barrier.  8192 rows, early against late: bf16
+  // of 3584 72 and 78 us, of 5120 114 and 129, of 8192 206 and 180; with a gate row 3584 107 and 87.
+  constexpr bool EARLY = !ROWGATE && THREADS <= kMiddle;
   extern __shared__ __align__(128) uint8_t stage_mem[];
   __shared__ RingBars bars;
   __shared__ __align__(16) float buf[64];
@@ -570,7 +581,8 @@ __global__ void __launch_bounds__(THREADS, THREADS <= kNarrowBwd ? 2 : 1)
       for (int e = 0; e < kPairs; ++e) f[e] = cols.has(e) ? *reinterpret_cast<const uint64_t*>(p + cols.at(e)) : 0;
     }
   };
-  ring_start(ring, stage_mem, &bars, a.n);
+  const uint32_t n = (uint32_t)a.n;  // below 2^31: no sum of rows and blocks wraps
+  ring_start(ring, stage_mem, &bars, n);
   {
     uint64_t f[kPairs], g[kPairs];
     cols.param(a.w_pre, f);
@@ -589,93 +601,174 @@ __global__ void __launch_bounds__(THREADS, THREADS <= kNarrowBwd ? 2 : 1)
   uint64_t a_pre[kPairs], a_post[kPairs];
 #pragma unroll
   for (int e = 0; e < kPairs; ++e) a_pre[e] = a_post[e] = 0;
-  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
-    const float r_post = post ? a.rstd_post[row] : 1.f, r_pre = pre ? a.rstd_pre[row] : 1.f;
-    uint64_t xo[kPairs], yn[kPairs], dx[kPairs], t[kPairs], g[kPairs];
+  if constexpr (EARLY) {
+    for (uint32_t row = blockIdx.x; row < n; row += gridDim.x) {
+      const float r_post = post ? a.rstd_post[row] : 1.f, r_pre = pre ? a.rstd_pre[row] : 1.f;
+      uint64_t xo[kPairs], yn[kPairs], dx[kPairs], t[kPairs];
 #pragma unroll
-    for (int e = 0; e < kPairs; ++e) xo[e] = yn[e] = dx[e] = t[e] = g[e] = 0;
-    if (!mbar_wait(&bars.full[k], phase, nullptr)) return;  // the copy cannot fail to end
-    const StageRow<T, VEC> st(ring, stage_mem, row, k);
-    if (pre) {
-      st.load(cols, 0, xo);
-      st.load(cols, at_du, t);
-    }
-    if (a.y) st.load(cols, at_y, yn);
-    if (a.dx_in) st.load(cols, at_dx, dx);
-    if (ROWGATE) st.load(cols, at_g, g);
-    __syncthreads();
-    const int64_t later = row + (int64_t)ring.stages * gridDim.x;
-    if (threadIdx.x == 0 && later < a.n) ring_issue(ring, stage_mem, &bars, later, k);
-    if (++k == ring.stages) {
-      k = 0;
-      phase ^= 1;
-    }
-    const size_t at = (size_t)row * a.D;
-    const uint64_t rp2 = both(r_post);
-#pragma unroll
-    for (int e = 0; e < kPairs; ++e) yn[e] = mul2(yn[e], rp2);
-    uint64_t cw[kPairs];
-    own_param(par + pitch, cw);
-    if (pre) {
-      uint64_t s = 0, w[kPairs];
-      const uint64_t r2 = both(r_pre);
-      own_param(par, w);
-      if (a.y) {
-#pragma unroll
-        for (int e = 0; e < kPairs; ++e) xo[e] = fma2(ROWGATE ? mul2(cw[e], g[e]) : cw[e], yn[e], xo[e]);
+      for (int e = 0; e < kPairs; ++e) xo[e] = yn[e] = dx[e] = t[e] = 0;
+      if (!mbar_wait(&bars.full[k], phase, nullptr)) return;  // the copy cannot fail to end
+      const StageRow<T, VEC> st(ring, stage_mem, row, k);
+      if (pre) {
+        st.load(cols, 0, xo);
+        st.load(cols, at_du, t);
       }
+      if (a.y) st.load(cols, at_y, yn);
+      if (a.dx_in) st.load(cols, at_dx, dx);
+      __syncthreads();
+      const uint32_t later = row + (uint32_t)ring.stages * gridDim.x;
+      if (threadIdx.x == 0 && later < n) ring_issue(ring, stage_mem, &bars, later, k);
+      if (++k == ring.stages) {
+        k = 0;
+        phase ^= 1;
+      }
+      const size_t at = (size_t)row * a.D;
+      const uint64_t rp2 = both(r_post);
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e) yn[e] = mul2(yn[e], rp2);
+      uint64_t cw[kPairs];
+      own_param(par + pitch, cw);
+      if (pre) {
+        uint64_t s = 0, w[kPairs];
+        const uint64_t r2 = both(r_pre);
+        own_param(par, w);
+        if (a.y) {
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e) xo[e] = fma2(cw[e], yn[e], xo[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) {
+          t[e] = mul2(t[e], r2);
+          a_pre[e] = fma2(t[e], xo[e], a_pre[e]);
+          t[e] = mul2(t[e], w[e]);
+          s = fma2(t[e], xo[e], s);
+        }
+        // with t = r_pre du w: xn mean(du w xn) r_pre = x' r_pre^2 sum(t x') / D
+        const float sum = block_sum<kSumWarps(THREADS)>(halves(s), buf, turn) * a.inv_D;
+        const uint64_t m2 = both(-(sum * r_pre) * r_pre);
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) dx[e] = fma2(xo[e], m2, add2(t[e], dx[e]));
+      }
+      if (a.dx) cols.template store<T>(reinterpret_cast<T*>(a.dx) + at, st.even, dx);
+      if (!a.y) continue;
+      uint64_t s = 0;
 #pragma unroll
       for (int e = 0; e < kPairs; ++e) {
-        a_pre[e] = fma2(mul2(t[e], r2), xo[e], a_pre[e]);
-        t[e] = mul2(t[e], w[e]);
-        s = fma2(t[e], xo[e], s);
-      }
-      // xn mean(t xn) r_pre = x' r_pre^3 sum(t x') / D
-      const float sum = block_sum<kSumWarps(THREADS)>(halves(s), buf, turn) * a.inv_D;
-      const uint64_t m2 = both(-(r_pre * sum * r_pre) * r_pre);
-#pragma unroll
-      for (int e = 0; e < kPairs; ++e) dx[e] = fma2(xo[e], m2, fma2(t[e], r2, dx[e]));
-    }
-    if (a.dx) cols.template store<T>(reinterpret_cast<T*>(a.dx) + at, st.even, dx);
-    if (!a.y) continue;
-    uint64_t s = 0;
-#pragma unroll
-    for (int e = 0; e < kPairs; ++e) {
-      if (ROWGATE) {
-        const uint64_t p = mul2(dx[e], yn[e]);
-        a_post[e] = fma2(g[e], p, a_post[e]);
-        t[e] = mul2(cw[e], p);
-        dx[e] = mul2(mul2(cw[e], g[e]), dx[e]);
-      } else {
         a_post[e] = fma2(dx[e], yn[e], a_post[e]);
         dx[e] = mul2(cw[e], dx[e]);
+        s = fma2(dx[e], yn[e], s);
       }
-      s = fma2(dx[e], yn[e], s);
-    }
-    if (ROWGATE && a.dgate) cols.template store<T>(reinterpret_cast<T*>(a.dgate) + at, st.even, t);
-    if (post) {
-      const float mean = block_sum<kSumWarps(THREADS)>(halves(s), buf, turn) * a.inv_D;
-      const uint64_t m2 = both(-r_post * mean);
+      if (post) {
+        const float mean = block_sum<kSumWarps(THREADS)>(halves(s), buf, turn) * a.inv_D;
+        const uint64_t m2 = both(-r_post * mean);
 #pragma unroll
-      for (int e = 0; e < kPairs; ++e) dx[e] = fma2(yn[e], m2, mul2(dx[e], rp2));
+        for (int e = 0; e < kPairs; ++e) dx[e] = fma2(yn[e], m2, mul2(dx[e], rp2));
+      }
+      if (a.dy) cols.template store<T>(reinterpret_cast<T*>(a.dy) + at, st.even, dx);
     }
-    if (a.dy) cols.template store<T>(reinterpret_cast<T*>(a.dy) + at, st.even, dx);
-  }
-  const size_t out = (size_t)blockIdx.x * 3 * a.D;
-  float* part = a.part + out;
-  auto even = [&](int i) { return VEC || (out + (size_t)i * a.D) % 2 == 0; };
-  uint64_t w[kPairs], g[kPairs];
-  cols.template store<float>(part, even(0), a_pre);
-  cols.param(a.w_post, w);
-  cols.param(ROWGATE ? nullptr : reinterpret_cast<const float*>(a.gate), g);
+  } else {
+    for (uint32_t row = blockIdx.x; row < n; row += gridDim.x) {
+      const float r_post = post ? a.rstd_post[row] : 1.f, r_pre = pre ? a.rstd_pre[row] : 1.f;
+      uint64_t xo[kPairs], yn[kPairs], dx[kPairs], t[kPairs];
 #pragma unroll
-  for (int e = 0; e < kPairs; ++e) {
-    const uint64_t v = mul2(both(a.res_scale), a_post[e]);
-    g[e] = mul2(v, g[e]);
-    w[e] = mul2(v, w[e]);
+      for (int e = 0; e < kPairs; ++e) yn[e] = dx[e] = 0;
+      if (!mbar_wait(&bars.full[k], phase, nullptr)) return;  // the copy cannot fail to end
+      const StageRow<T, VEC> st(ring, stage_mem, row, k);
+      auto hand_back = [&]() {
+        const uint32_t later = row + (uint32_t)ring.stages * gridDim.x;
+        if (threadIdx.x == 0 && later < n) ring_issue(ring, stage_mem, &bars, later, k);
+        if (++k == ring.stages) {
+          k = 0;
+          phase ^= 1;
+        }
+      };
+      const size_t at = (size_t)row * a.D;
+      const uint64_t rp2 = both(r_post);
+      if (a.y) st.load(cols, at_y, yn);
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e) yn[e] = mul2(yn[e], rp2);
+      uint64_t c[kPairs];
+      if (pre) {
+        uint64_t s = 0;
+        const uint64_t r2 = both(r_pre);
+        st.load(cols, 0, xo);
+        if (a.y) {
+          own_param(par + pitch, c);
+          if (ROWGATE) {
+            uint64_t g[kPairs];
+            st.load(cols, at_g, g);
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) c[e] = mul2(c[e], g[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e) xo[e] = fma2(c[e], yn[e], xo[e]);
+        }
+        st.load(cols, at_du, t);
+        {
+          uint64_t w[kPairs];
+          own_param(par, w);
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e) {
+            t[e] = mul2(t[e], r2);
+            a_pre[e] = fma2(t[e], xo[e], a_pre[e]);
+            t[e] = mul2(t[e], w[e]);
+            s = fma2(t[e], xo[e], s);
+          }
+        }
+        // with t = r_pre du w: xn mean(du w xn) r_pre = x' r_pre^2 sum(t x') / D
+        const float sum = block_sum<kSumWarps(THREADS)>(halves(s), buf, turn) * a.inv_D;
+        const uint64_t m2 = both(-(sum * r_pre) * r_pre);
+        if (a.dx_in) st.load(cols, at_dx, dx);
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) dx[e] = fma2(xo[e], m2, add2(t[e], dx[e]));
+      } else {
+        st.load(cols, at_dx, dx);
+      }
+      if (a.dx) cols.template store<T>(reinterpret_cast<T*>(a.dx) + at, st.even, dx);
+      if (!a.y) {
+        __syncthreads();
+        hand_back();
+        continue;
+      }
+      uint64_t s = 0;
+      {
+        own_param(par + pitch, c);
+        if (ROWGATE) {
+          uint64_t g[kPairs];
+          st.load(cols, at_g, g);
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e) {
+            const uint64_t p = mul2(dx[e], yn[e]);
+            a_post[e] = fma2(g[e], p, a_post[e]);
+            t[e] = mul2(c[e], p);
+            dx[e] = mul2(mul2(c[e], g[e]), dx[e]);
+          }
+          if (a.dgate) cols.template store<T>(reinterpret_cast<T*>(a.dgate) + at, st.even, t);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e) {
+            a_post[e] = fma2(dx[e], yn[e], a_post[e]);
+            dx[e] = mul2(c[e], dx[e]);
+          }
+        }
+      }
+      if (post) {
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) s = fma2(dx[e], yn[e], s);
+        const float mean = block_sum<kSumWarps(THREADS)>(halves(s), buf, turn) * a.inv_D;
+        const uint64_t m2 = both(-r_post * mean);
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) dx[e] = fma2(yn[e], m2, mul2(dx[e], rp2));
+      } else {
+        __syncthreads();
+      }
+      hand_back();
+      if (a.dy) cols.template store<T>(reinterpret_cast<T*>(a.dy) + at, st.even, dx);
+    }
   }
-  cols.template store<float>(part + a.D, even(1), g);
-  cols.template store<float>(part + 2 * a.D, even(2), w);  // not used for a gate per token
+  const size_t out = (size_t)blockIdx.x * a.D, half = (size_t)gridDim.x * a.D;
+  cols.template store<float>(a.part + out, VEC || out % 2 == 0, a_pre);
+  cols.template store<float>(a.part + half + out, VEC || (half + out) % 2 == 0, a_post);
 }
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -718,7 +811,7 @@ bool ring_setup(const NormArgs& a, size_t es, bool backward, bool vec, RowRing* 
   if (a.gate_rows) add(a.gate);
   r->row_bytes = (uint32_t)bytes;
   r->pitch = (uint32_t)(vec ? bytes : align_up(bytes, 16) + 16);
-  r->tail = (size_t)a.n * bytes % 16 ? a.n - 1 : -1;
+  r->tail = (size_t)a.n * bytes % 16 ? (uint32_t)(a.n - 1) : ~0u;
   const size_t stage = (size_t)r->pitch * r->n_src, fixed = backward ? 2 * align_up((size_t)a.D, 4) * 4 : 0;
   // as many blocks on an SM as leave each two stages; one block has to do with what there is
   const int T = threads_for(a.D, 2 * kPairs);
@@ -762,9 +855,9 @@ cudaError_t fwd_ring(const NormArgs& a, const RowRing& ring, unsigned grid, size
 template <typename T, int E, bool VEC>
 cudaError_t bwd_direct(const NormArgs& a, unsigned grid, cudaStream_t st) {
   static size_t set[kMaxDevices] = {};
-  const cudaError_t e = set_smem_limit((const void*)norm_bwd<T, E, VEC>, (size_t)3 * 1024 * E * 4, set);
+  const cudaError_t e = set_smem_limit((const void*)norm_bwd<T, E, VEC>, (size_t)2 * 1024 * E * 4, set);
   if (e != cudaSuccess) return e;
-  norm_bwd<T, E, VEC><<<grid, threads_for(a.D, E), (size_t)3 * a.D * 4, st>>>(a);
+  norm_bwd<T, E, VEC><<<grid, threads_for(a.D, E), (size_t)2 * a.D * 4, st>>>(a);
   return cudaGetLastError();
 }
 template <typename T, bool VEC, bool ROWGATE, int THREADS>
@@ -815,10 +908,9 @@ cudaError_t bwd(const NormArgs& a, cudaStream_t st) {
     e = small ? bwd_direct<T, 8, false>(a, grid, st) : bwd_direct<T, 16, false>(a, grid, st);
   if (e != cudaSuccess) return e;
   count_launches(1);
-  float* dgate = a.gate && !a.gate_rows ? reinterpret_cast<float*>(a.dgate) : nullptr;
-  if (a.dw_pre || a.dw_post || dgate) {
+  if (a.dw_pre || a.dw_post || (a.dgate && !a.gate_rows)) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.D + 31) / 32, 3);
+    cfg.gridDim = dim3((a.D + 31) / 32, 2);
     cfg.blockDim = dim3(32 * kStrips);
     cfg.stream = st;
     cudaLaunchAttribute attr;  // a dependent launch: its set-up overlaps the end of the row kernel
@@ -827,8 +919,7 @@ cudaError_t bwd(const NormArgs& a, cudaStream_t st) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, norm_join, (const float*)a.part, (int)grid, a.D, a.dw_pre, a.dw_post, dgate,
-                              a.accumulate);
+    return cudaLaunchKernelEx(&cfg, norm_join, a, (int)grid);
   }
   return cudaGetLastError();
 }
@@ -850,7 +941,7 @@ extern "C" {
 
 size_t oomb_block_norm_workspace(int n, int D) {
   if (n <= 0 || D <= 0 || D > kMaxWidth) return 0;
-  return align_up((size_t)norm_parts(n, D) * 3 * D * 4, 256);
+  return align_up((size_t)norm_parts(n, D) * 2 * D * 4, 256);
 }
 
 // Checks common to both directions; the tensors' element size.

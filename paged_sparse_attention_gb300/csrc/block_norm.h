@@ -27,7 +27,7 @@ struct NormArgs {
   float* dw_pre;
   void* dgate;
   int accumulate;
-  float* part;         // [norm_parts, 3, D]
+  float* part;         // [2, norm_parts, D]
 };
 
 int norm_blocks_per_sm(int T);
