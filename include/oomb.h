@@ -522,8 +522,8 @@ OOMB_API oomb_status oomb_bias_rope_axes(const void* in, int in_dtype, const flo
  * or NULL (1).  x_out may be NULL when y is (nothing would be added), and may be x.  rstd_post
  * and rstd_pre ([n] fp32, or NULL) keep r_post and r_pre for the backward.  fp32 arithmetic,
  * each output rounded once (u is formed from the unrounded x_out).  Other overlaps of outputs
- * and inputs are not allowed.  Pointers on their element's size; rows of a multiple of 8
- * elements (16 above 8192) with every pointer on 16 bytes take the fast variant.
+ * and inputs are not allowed.  Pointers on their element's size; fastest with every pointer on
+ * 16 bytes, and then with rows of a multiple of 8 elements.
  * Errors: ARG, ALIGN, DTYPE, UNSUPPORTED (D > 16384), CUDA. */
 OOMB_API oomb_status oomb_block_norm_fwd(const void* x, const void* y, const float* w_post, const void* gate,
                                          int gate_rows, const float* w_pre, float res_scale, float eps, int n, int D,

@@ -593,7 +593,8 @@ __global__ void __launch_bounds__(THREADS, THREADS <= kNarrowBwd ? 2 : 1)
     cols.param(ROWGATE ? nullptr : reinterpret_cast<const float*>(a.gate), g);
 #pragma unroll
     for (int e = 0; e < kPairs; ++e)
-      if (cols.has(e)) *reinterpret_cast<uint64_t*>(par + pitch + cols.at(e)) = mul2(both(a.res_scale), mul2(g[e], f[e]));
+      if (cols.has(e))
+        *reinterpret_cast<uint64_t*>(par + pitch + cols.at(e)) = mul2(both(a.res_scale), mul2(g[e], f[e]));
   }
   // stage order: x (with a pre-norm), y, du, dx', gate rows, each where it is read
   const int at_y = pre ? 1 : 0, at_du = at_y + (a.y ? 1 : 0), at_dx = at_du + (pre ? 1 : 0),
@@ -930,7 +931,8 @@ cudaError_t bwd(const NormArgs& a, cudaStream_t st) {
 int norm_blocks_per_sm(int T) { return std::max(1, std::min(8, 1024 / T)); }
 
 int norm_parts(int64_t n, int D) {
-  return (int)std::min<int64_t>(n, (int64_t)norm_blocks_per_sm(std::min(1024, threads_for(D, 2 * kPairs))) * device_sm_count());
+  const int T = std::min(1024, threads_for(D, 2 * kPairs));
+  return (int)std::min<int64_t>(n, (int64_t)norm_blocks_per_sm(T) * device_sm_count());
 }
 
 }  // namespace oomb

@@ -435,7 +435,8 @@ __global__ void __launch_bounds__(256) score_join_few(const __grid_constant__ Sc
   if (4 * lane < d) {
     T* dst = reinterpret_cast<T*>(s.a.o_out) + rh * d + 4 * lane;
     if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     } else {
       *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     }
@@ -650,7 +651,8 @@ __global__ void __launch_bounds__(kThreads, C == 1 ? 2 : 1)
   }
   __syncthreads();
   const int n_items = t_last < 0 ? 0 : (t_last - t_first + 1) * G;  // (row tile, query head)
-  const int u0 = (int)((int64_t)n_items * blockIdx.z / n_split), u1 = (int)((int64_t)n_items * (blockIdx.z + 1) / n_split);
+  const int u0 = (int)((int64_t)n_items * blockIdx.z / n_split);
+  const int u1 = (int)((int64_t)n_items * (blockIdx.z + 1) / n_split);
   const size_t slot = ((size_t)blockIdx.z * gridDim.y + h) * gridDim.x + blockIdx.x;
   if (u0 == u1) {
     if (n_split > 1 && threadIdx.x == 0) flags[slot] = 0;
@@ -880,7 +882,8 @@ BwdSplit simt_bwd_split(const Geometry& g, int n_q, int max_sel) {
   const int64_t slots = simt_slots(g), row_tiles = (n_q + kRows - 1) / kRows;
   const int64_t key_tiles = ((int64_t)max_sel * g.P + kKeys - 1) / kKeys;
   b.dq = (int)std::min<int64_t>(std::max<int64_t>(1, slots / (row_tiles * g.Hq)), std::max<int64_t>(1, key_tiles / 2));
-  b.dkdv = (int)std::min<int64_t>({std::max<int64_t>(1, kDkdvFill * slots / (key_tiles * g.Hkv)), row_tiles * g.G, kMaxShares});
+  const int64_t fill = std::max<int64_t>(1, kDkdvFill * slots / (key_tiles * g.Hkv));
+  b.dkdv = (int)std::min<int64_t>({fill, row_tiles * g.G, kMaxShares});
   b.dq_bytes = b.dq > 1 ? align_up((size_t)b.dq * n_q * g.Hq * g.d * 4, 256) : 0;
   b.dkdv_bytes = b.dkdv > 1 ? (size_t)b.dkdv * key_tiles * g.Hkv * dkdv_tile_bytes(g) : 0;
   return b;
@@ -986,7 +989,8 @@ cudaError_t launch_score_fwd(ScoreArgs& s, cudaStream_t st) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if (few)
-    e = f32 ? cudaLaunchKernelEx(&cfg, score_join_few<float>, s) : cudaLaunchKernelEx(&cfg, score_join_few<__nv_bfloat16>, s);
+    e = f32 ? cudaLaunchKernelEx(&cfg, score_join_few<float>, s)
+            : cudaLaunchKernelEx(&cfg, score_join_few<__nv_bfloat16>, s);
   else
     e = f32 ? cudaLaunchKernelEx(&cfg, score_join<float>, s) : cudaLaunchKernelEx(&cfg, score_join<__nv_bfloat16>, s);
   count_launches(1);

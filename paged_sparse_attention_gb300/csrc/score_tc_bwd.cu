@@ -18,9 +18,10 @@
 //
 // Bounds (GB300).  8192 rows on 193 pages, 28 query heads on 4, cap 50: 7.13 ms, 849 TFLOP/s, 43 % of
 // the measured bf16 peak, by TMEM and shared-memory traffic as the plain backward (915 there, and
-// 910 here without the cap); a step of 128 rows costs 3.6 us a thread block, 3.9 with the cap.  Documents of 1500 tokens, 4001
-// rows: 325 us, 4.9 us a step: 40 % of the steps are cut by a range, and blocks of 25 steps pay
-// for their set-up and for the sum over the cluster (tensor pipe active 46 %).
+// 910 here without the cap); a step of 128 rows costs 3.6 us a thread block, 3.9 with the cap.
+// Documents of 1500 tokens, 4001 rows: 325 us, 4.9 us a step: 40 % of the steps are cut by a range,
+// and blocks of 25 steps pay for their set-up and for the sum over the cluster (tensor pipe active
+// 46 %).
 //
 // Warp roles of score_bwd_tc (448 threads): warp 0 TMA producer, warp 1 MMA issuer and TMEM
 // owner, warps 2-9 softmax (thread = key row, 32 of a half's 64 query columns) and epilogue,
@@ -579,8 +580,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of the padded range: D = rowsum(dO * O) and LSE * log2(e) into [Hq, n_pad] buffers (rows
 // without keys and padded rows: LSE = +inf, so P = 0; cap2 is taken off) and the row of the fp32 dQ accumulator
 // zeroed.
-__global__ void __launch_bounds__(256) score_bwd_prep(const __grid_constant__ ScoreArgs s, float cap2, int n_pad, int n_tiles,
-                                                      float* __restrict__ Dbuf, float* __restrict__ lse2,
+__global__ void __launch_bounds__(256) score_bwd_prep(const __grid_constant__ ScoreArgs s, float cap2, int n_pad,
+                                                      int n_tiles, float* __restrict__ Dbuf, float* __restrict__ lse2,
                                                       float* __restrict__ dq_acc, longlong2* __restrict__ span,
                                                       TileSpan* __restrict__ tiles) {
   const AttnArgs& a = s.a;
@@ -734,8 +735,8 @@ cudaError_t launch_score_bwd_tc(const ScoreArgs& s, cudaStream_t st) {
   TileSpan* tiles = reinterpret_cast<TileSpan*>(take((size_t)n_tiles * sizeof(TileSpan)));
   const CapForm form = !(s.cap > 0.f) ? kNoCap : s.cap <= kCapLimit ? kWideCap : kLargeCap;
   const int64_t warps = (int64_t)a.n_q * a.g.Hq, warps_pad = (int64_t)n_pad * a.g.Hq;
-  score_bwd_prep<<<(unsigned)(n_tiles + (warps_pad + 7) / 8), 256, 0, st>>>(s, form == kWideCap ? s.cap * kLog2e : 0.f, n_pad, n_tiles, Dbuf, lse2, dq_acc,
-                                                                           span, tiles);
+  score_bwd_prep<<<(unsigned)(n_tiles + (warps_pad + 7) / 8), 256, 0, st>>>(
+      s, form == kWideCap ? s.cap * kLog2e : 0.f, n_pad, n_tiles, Dbuf, lse2, dq_acc, span, tiles);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   CUtensorMap tq, tdo, tk, tv;
@@ -756,7 +757,8 @@ cudaError_t launch_score_bwd_tc(const ScoreArgs& s, cudaStream_t st) {
   p.scale_log2 = a.scale * kLog2e;
   const bool bias = s.slopes != nullptr;
   if (form == kWideCap)
-    e = bias ? launch_main<kWideCap, true>(p, tq, tdo, tk, tv, st) : launch_main<kWideCap, false>(p, tq, tdo, tk, tv, st);
+    e = bias ? launch_main<kWideCap, true>(p, tq, tdo, tk, tv, st)
+             : launch_main<kWideCap, false>(p, tq, tdo, tk, tv, st);
   else if (form == kLargeCap)
     e = bias ? launch_main<kLargeCap, true>(p, tq, tdo, tk, tv, st)
              : launch_main<kLargeCap, false>(p, tq, tdo, tk, tv, st);
