@@ -546,6 +546,17 @@ OOMB_API oomb_status oomb_block_norm_bwd(const void* x, const void* y, const flo
                                          void* stream);
 OOMB_API size_t oomb_block_norm_workspace(int n, int D);
 
+/* The block norms have no pool whose error word could tell that a kernel's wait for its own
+ * copies ran out (after about a second), so the current device has a word of its own for them.
+ * Synchronizes `stream`, reads and clears that word: TIMEOUT when a block norm of this device
+ * gave up since the last check (rows are then missing, and the backward's parameter gradients
+ * are NaN), else OK or CUDA.  Not to be called while a stream is being captured. */
+OOMB_API oomb_status oomb_block_norm_check(void* stream, uint32_t* bits_out);
+
+/* For tests of a caller's error handling: while on is not 0, the copy of the first row of calls
+ * with many rows is not started, so that its wait runs out as described above. */
+OOMB_API void oomb_block_norm_test_timeout(int on);
+
 /* dK, dV of tokens [first_token, first_token + n_tokens) read from the paged fp32
  * gradient pool through the page table into token-major [n_tokens, Hkv, d] fp32
  * (device).  With offload_grads the pools are in host memory and are read there: the

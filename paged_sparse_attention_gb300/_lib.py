@@ -88,6 +88,8 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         "oomb_block_norm_bwd": (i32, [vp, vp, vp, vp, i32, vp, f32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                       i32, vp, sz, vp]),
         "oomb_block_norm_workspace": (sz, [i32, i32]),
+        "oomb_block_norm_check": (i32, [vp, C.POINTER(C.c_uint32)]),
+        "oomb_block_norm_test_timeout": (None, [i32]),
         "oomb_grad_gather": (i32, [vp, i64, i32, vp, vp, vp]),
         "oomb_grad_prefetch": (i32, [vp, vp, vp, i32, vp, vp, i32, vp]),
         "oomb_grad_carry": (i32, [vp, vp, vp, i32, vp, vp, i32, vp]),
@@ -412,6 +414,18 @@ def oomb_block_norm_bwd(x, y, dx, dy=None, du=None, dx_out=None, rstd_pre=None, 
 
 def oomb_block_norm_workspace(n: int, D: int) -> int:
     return int(load().oomb_block_norm_workspace(n, D))
+
+
+def oomb_block_norm_check(stream=None) -> int:
+    """Raises OombError if a block norm of the current device gave up waiting since the last check."""
+    bits = C.c_uint32(0)
+    _ok("oomb_block_norm_check", load().oomb_block_norm_check(_stream(stream), C.byref(bits)))
+    return bits.value
+
+
+def oomb_block_norm_test_timeout(on: bool) -> None:
+    """For tests: while on, the first row of calls with many rows never comes, and they give up on it."""
+    load().oomb_block_norm_test_timeout(int(on))
 
 
 def oomb_grad_gather(pool: int, first_token: int, dk, dv, stream=None) -> None:

@@ -28,6 +28,7 @@
 // Bounds (GB300, 8192 rows of 3584 in bf16): forward 235 MB in 43 us, 5.5 TB/s; backward 352 MB
 // in 66 us, 5.3 TB/s, and the join: HBM with 80 % of the measured copy rate; the rest is the two
 // sums of a row, whose barriers two blocks an SM hide only in part (issue 61 %).
+#include <atomic>
 #include <cmath>
 
 #include "attn_common.cuh"
@@ -337,11 +338,15 @@ struct RowRing {
   uint32_t row_bytes, pitch;  // of a row in memory, and from row to row in a stage
   int stages;
   uint32_t tail;  // row that the copies leave out (its end is no multiple of 16 bytes), or ~0
+  uint32_t first;  // rows below never come: 0, but for oomb_block_norm_test_timeout
 };
 
 struct __align__(16) RingBars {
   uint64_t full[kMaxStages];
 };
+
+// Error bits of the block norms on this device since the last oomb_block_norm_check.
+__device__ uint32_t norm_error;
 
 // A row's copy: the 16-byte units it lies in.
 __device__ __forceinline__ void ring_issue(const RowRing& r, uint8_t* base, RingBars* bars, uint32_t row, int k) {
@@ -363,10 +368,35 @@ __device__ __forceinline__ void ring_start(const RowRing& r, uint8_t* base, Ring
     fence_mbar_init();
     for (int k = 0; k < r.stages; ++k) {
       const uint32_t row = blockIdx.x + (uint32_t)k * gridDim.x;
-      if (row < n) ring_issue(r, base, bars, row, k);
+      if (row >= r.first && row < n) ring_issue(r, base, bars, row, k);
     }
   }
   __syncthreads();
+}
+
+// A thread whose wait runs out (mbar_wait raises the error) leaves, at `row` in stage k.  Before that
+// thread 0, which asks for the rows, waits for the copies in flight (this row's and the following
+// ones'), so that none lands in shared memory that is another block's by then.  The others do not
+// hang: a barrier counts the threads that have not left, and without thread 0 their waits run out.
+__device__ __noinline__ void ring_give_up(const RowRing& r, RingBars* bars, uint32_t row, uint32_t n, int k,
+                                          uint32_t phase) {
+  if (threadIdx.x != 0) return;
+  for (int j = 0; j < r.stages && row < n; ++j, row += gridDim.x) {
+    mbar_wait(&bars->full[k], phase, &norm_error);
+    if (++k == r.stages) {
+      k = 0;
+      phase ^= 1;
+    }
+  }
+}
+// In the backward its columns' sums become NaN too: the workspace holds whatever was there before.
+__device__ __noinline__ void lose_sums(const NormArgs& a, int first, int step) {
+  for (int h = 0; h < 2 * kPairs; ++h) {
+    const int c = first + h / 2 * step + h % 2;
+    if (c >= a.D) continue;
+    a.part[(size_t)blockIdx.x * a.D + c] = NAN;
+    a.part[((size_t)gridDim.x + blockIdx.x) * a.D + c] = NAN;
+  }
 }
 
 // Packed pairs of fp32 (two elements an instruction): a row's work is bound by instructions as
@@ -512,7 +542,10 @@ __global__ void __launch_bounds__(THREADS, THREADS <= kNarrowFwd ? 2 : 1)
     uint64_t f[kPairs], r[kPairs], g[kPairs];
 #pragma unroll
     for (int e = 0; e < kPairs; ++e) r[e] = g[e] = 0;
-    if (!mbar_wait(&bars.full[k], phase, nullptr)) return;  // the copy cannot fail to end
+    if (!mbar_wait(&bars.full[k], phase, &norm_error)) {
+      ring_give_up(ring, &bars, row, n, k, phase);
+      return;
+    }
     const StageRow<T, VEC> st(ring, stage_mem, row, k);
     st.load(cols, 0, f);
     if (a.y) st.load(cols, 1, r);
@@ -608,7 +641,11 @@ __global__ void __launch_bounds__(THREADS, THREADS <= kNarrowBwd ? 2 : 1)
       uint64_t xo[kPairs], yn[kPairs], dx[kPairs], t[kPairs];
 #pragma unroll
       for (int e = 0; e < kPairs; ++e) xo[e] = yn[e] = dx[e] = t[e] = 0;
-      if (!mbar_wait(&bars.full[k], phase, nullptr)) return;  // the copy cannot fail to end
+      if (!mbar_wait(&bars.full[k], phase, &norm_error)) {
+        ring_give_up(ring, &bars, row, n, k, phase);
+        lose_sums(a, cols.first, cols.step);
+        return;
+      }
       const StageRow<T, VEC> st(ring, stage_mem, row, k);
       if (pre) {
         st.load(cols, 0, xo);
@@ -673,7 +710,11 @@ __global__ void __launch_bounds__(THREADS, THREADS <= kNarrowBwd ? 2 : 1)
       uint64_t xo[kPairs], yn[kPairs], dx[kPairs], t[kPairs];
 #pragma unroll
       for (int e = 0; e < kPairs; ++e) yn[e] = dx[e] = 0;
-      if (!mbar_wait(&bars.full[k], phase, nullptr)) return;  // the copy cannot fail to end
+      if (!mbar_wait(&bars.full[k], phase, &norm_error)) {
+        ring_give_up(ring, &bars, row, n, k, phase);
+        lose_sums(a, cols.first, cols.step);
+        return;
+      }
       const StageRow<T, VEC> st(ring, stage_mem, row, k);
       auto hand_back = [&]() {
         const uint32_t later = row + (uint32_t)ring.stages * gridDim.x;
@@ -772,6 +813,8 @@ __global__ void __launch_bounds__(THREADS, THREADS <= kNarrowBwd ? 2 : 1)
   cols.template store<float>(a.part + half + out, VEC || (half + out) % 2 == 0, a_post);
 }
 
+std::atomic<bool> g_hold_first_row{false};  // oomb_block_norm_test_timeout
+
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Elements a thread holds in the 16-byte variant: 1024 threads have to span a row.
@@ -813,6 +856,7 @@ bool ring_setup(const NormArgs& a, size_t es, bool backward, bool vec, RowRing* 
   r->row_bytes = (uint32_t)bytes;
   r->pitch = (uint32_t)(vec ? bytes : align_up(bytes, 16) + 16);
   r->tail = (size_t)a.n * bytes % 16 ? (uint32_t)(a.n - 1) : ~0u;
+  r->first = g_hold_first_row.load(std::memory_order_relaxed) ? 1 : 0;
   const size_t stage = (size_t)r->pitch * r->n_src, fixed = backward ? 2 * align_up((size_t)a.D, 4) * 4 : 0;
   // as many blocks on an SM as leave each two stages; one block has to do with what there is
   const int T = threads_for(a.D, 2 * kPairs);
@@ -1038,5 +1082,19 @@ oomb_status oomb_block_norm_bwd(const void* x, const void* y, const float* w_pos
   return cuda_status(dtype == OOMB_FP32 ? bwd<float>(a, (cudaStream_t)stream)
                                         : bwd<__nv_bfloat16>(a, (cudaStream_t)stream));
 }
+
+oomb_status oomb_block_norm_check(void* stream, uint32_t* bits_out) {
+  uint32_t bits = 0;
+  const uint32_t none = 0;
+  cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&bits, norm_error, sizeof(bits));
+  if (e == cudaSuccess && bits) e = cudaMemcpyToSymbol(norm_error, &none, sizeof(none));
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (bits_out) *bits_out = bits;
+  if (e != cudaSuccess) return cuda_status(e);
+  return bits & OOMB_DEVERR_TIMEOUT ? OOMB_ERR_TIMEOUT : bits ? OOMB_ERR_KERNEL : OOMB_OK;
+}
+
+void oomb_block_norm_test_timeout(int on) { g_hold_first_row.store(on != 0); }
 
 }  // extern "C"
