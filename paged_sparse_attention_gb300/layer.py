@@ -160,10 +160,14 @@ class LayerStep:
         ``positions`` int64 [n_axes, N] with ``pair_axis``.  ``doc_start`` int64 [n_docs + 1]
         and optionally ``prefix_len`` int64 [n_docs]: packed documents; a row sees its own
         document only, and keys of this and earlier chunks (so a prefix that is to be seen by
-        all of its rows has to end with its chunk).  With ``w_norm``: ``Y`` [N, Dm], the
+        all of its rows has to end with its chunk).  The library's top-K selection and its sink
+        pages do not know the documents: with ``doc_start`` every page is kept (``top_k`` = -1), a
+        window goes without sinks, or the pages are given.  With ``w_norm``: ``Y`` [N, Dm], the
         previous block's output, and ``dX_out`` [N, Dm], the gradient that reaches the residual
         stream behind this layer; also returned are X_out (the residual stream), dY, and fp32
-        dw_norm, dw_post, dgate (those that exist); dX and dY are then in the pool's dtype."""
+        dw_norm, dw_post, dgate (those that exist); dX and dY are then in the pool's dtype.
+        Errors that kernels met are told by oomb_check (the pool) and, with ``w_norm``,
+        oomb_block_norm_check."""
         pool, h, dev = self.pool, self.pool.handle, self.dev
         N, Dm, Hq, Hkv, d = X.shape[0], self.Dm, self.Hq, self.Hkv, self.d
         if (positions is None) != (self.pair_axis is None):
@@ -174,6 +178,10 @@ class LayerStep:
             raise ValueError("LayerStep: w_post and gate act on Y")
         if prefix_len is not None and doc_start is None:
             raise ValueError("LayerStep: prefix_len needs doc_start")
+        if doc_start is not None and sel_override is None and (self.n_sink > 0 if self.window >= 0 else self.top_k >= 0):
+            raise ValueError("LayerStep: the top-K selection and the sink pages do not know documents and would pick "
+                             "pages that are masked; keep every page (top_k = -1), take a window without sinks, or "
+                             "give the pages (sel_override)")
         self._positions = positions
         self._docs = None if doc_start is None else (doc_start, prefix_len)
         self._scores = self.softcap != 0.0 or self.slopes is not None or self._docs is not None
