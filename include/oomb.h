@@ -506,7 +506,8 @@ OOMB_API oomb_status oomb_bias_rope(const void* in, int in_dtype, const float* b
  * positions: device int64 [n_axes, n], any sign; pair_axis: host [d/2], entries in
  * [0, n_axes), read before the call returns; bias, dtypes, in == out and mode as there
  * (mode 0: bias and cast only, positions and pair_axis not read).  n_axes up to 8.
- * Angles are reduced to a turn in 64-bit integers, so far positions lose nothing.
+ * Angles are reduced to a turn in integers, from frequencies held in 96 bits: for every 64-bit
+ * position they are known to 2^-26 turns, so far positions lose nothing.
  * Errors: those of oomb_bias_rope, ARG also for a bad axis. */
 OOMB_API oomb_status oomb_bias_rope_axes(const void* in, int in_dtype, const float* bias, void* out, int out_dtype,
                                          int n, int H, int d, const int64_t* positions, int n_axes,

@@ -3,10 +3,10 @@
 //
 // out[i, h, :] = R(i) (in[i, h, :] + bias[h, :]), R(i) turning each pair (j, j + d/2) by
 // positions[axis(j), i] * freq_j.  The angle in turns is position * (freq_j / 2 pi): with the
-// factor held as a 64-bit fraction of a turn, the product's low 64 bits are the angle modulo
-// one turn, whatever the position's size and sign (the factor carries double precision, so
-// at position 2^22 the angle is known to 2^-30 turns).  Its top 32 bits go to sincospif:
-// no double-precision arithmetic on the device, where it would bound the kernel.
+// factor held as a 96-bit fraction of a turn (turn_ladder.h), the product modulo one turn is the
+// angle, whatever the position's size and sign.  Its top 32 bits, known to 2^-31
+// turns for every 64-bit position, go to sincospif as a float: 2^-26 turns.  No double-precision
+// arithmetic on the device, where it would bound the kernel.
 //
 // Bytes: the tensor once in and once out.  A block takes a few tokens: their cos/sin (one per
 // pair) go to shared memory once and serve every head; a thread moves 16-byte vectors of both
@@ -19,6 +19,7 @@
 #include <cmath>
 
 #include "attn_common.cuh"
+#include "turn_ladder.h"
 
 namespace oomb {
 namespace {
@@ -35,8 +36,12 @@ struct RopeArgs {
   const int64_t* positions;
   int64_t n;
   int H, half, n_axes, mode, tokens;
-  uint64_t turn[kMaxHalf];  // freq_j / 2 pi as a fraction of 2^64
-  uint8_t axis[kMaxHalf];
+  // Of a pair, read as two words: lanes read different pairs, so a word takes as many cycles as
+  // there are lanes (8192 tokens of 28 heads: 31.5 us, with three arrays 32.2).
+  struct {
+    uint64_t turn;        // freq_j / 2 pi as a fraction of 2^64
+    uint32_t rest, axis;  // the next 32 bits; its axis
+  } pair[kMaxHalf];
 };
 
 template <typename T, int E>
@@ -86,8 +91,12 @@ __global__ void __launch_bounds__(kThreads) rope_axes(const __grid_constant__ Ro
   if (a.mode != 0) {
     for (int idx = threadIdx.x; idx < nt * half; idx += kThreads) {
       const int t = idx / half, j = idx % half;
-      const uint64_t pos = (uint64_t)a.positions[(int64_t)a.axis[j] * a.n + i0 + t];
-      const int32_t frac = (int32_t)((pos * a.turn[j]) >> 32);  // the angle in 2^-32 turns, in [-1/2, 1/2)
+      const uint64_t turn = a.pair[j].turn, word = *reinterpret_cast<const uint64_t*>(&a.pair[j].rest);
+      const uint64_t rest = (uint32_t)word;
+      const int64_t pos = a.positions[(int64_t)(word >> 32) * a.n + i0 + t];
+      const uint64_t up = (uint64_t)pos >> 32, down = (uint32_t)pos;
+      const uint64_t angle = (uint64_t)pos * turn + up * rest + ((down * rest) >> 32) - (pos < 0 ? rest << 32 : 0);
+      const int32_t frac = (int32_t)(angle >> 32);  // the angle in 2^-32 turns, in [-1/2, 1/2)
       float s, c;
       sincospif((float)frac * 0x1p-31f, &s, &c);
       cs[t * half + j] = c;
@@ -169,17 +178,21 @@ extern "C" oomb_status oomb_bias_rope_axes(const void* in, int in_dtype, const f
   if (mode != 0) {
     if (!positions || !pair_axis || n_axes <= 0 || n_axes > kMaxAxes) return OOMB_ERR_ARG;
     if (!(theta > 1.0f) || std::isinf(theta)) return OOMB_ERR_ARG;
-    int count[kMaxAxes] = {}, rank[kMaxAxes] = {};
+    int count[kMaxAxes] = {};
     for (int j = 0; j < half; ++j) {
       if (pair_axis[j] >= n_axes) return OOMB_ERR_ARG;
       ++count[pair_axis[j]];
     }
-    for (int j = 0; j < half; ++j) {
-      const int ax = pair_axis[j];
-      const double e = own_ladder ? (double)rank[ax]++ / (double)count[ax] : (double)j / (double)half;
-      const double turns = std::pow((double)theta, -e) * 0.15915494309189533577;  // freq / 2 pi, below 0.16
-      a.turn[j] = (uint64_t)(turns * 18446744073709551616.0);
-      a.axis[j] = (uint8_t)ax;
+    for (int ax = 0; ax < (own_ladder ? n_axes : 1); ++ax) {  // ladder after ladder
+      const int c = own_ladder ? count[ax] : half;
+      uint64_t hi[kMaxHalf];
+      uint32_t lo[kMaxHalf];
+      if (c > 0) turn_ladder((double)theta, c, hi, lo);
+      for (int j = 0, r = 0; j < half; ++j) {
+        if (own_ladder && pair_axis[j] != ax) continue;
+        a.pair[j] = {hi[r], lo[r], pair_axis[j]};
+        ++r;
+      }
     }
   }
   const uintptr_t ea = dtype_size(in_dtype), eb = dtype_size(out_dtype);
