@@ -508,7 +508,8 @@ OOMB_API oomb_status oomb_bias_rope(const void* in, int in_dtype, const float* b
  * (mode 0: bias and cast only, positions and pair_axis not read).  n_axes up to 8.
  * Angles are reduced to a turn in integers, from frequencies held in 96 bits: for every 64-bit
  * position they are known to 2^-26 turns, so far positions lose nothing.
- * Errors: those of oomb_bias_rope, ARG also for a bad axis. */
+ * Errors: those of oomb_bias_rope, ARG also for a bad axis, UNSUPPORTED from 2^31 elements a
+ * token on. */
 OOMB_API oomb_status oomb_bias_rope_axes(const void* in, int in_dtype, const float* bias, void* out, int out_dtype,
                                          int n, int H, int d, const int64_t* positions, int n_axes,
                                          const uint8_t* pair_axis, float theta, int own_ladder, int mode,

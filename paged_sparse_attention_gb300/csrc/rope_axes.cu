@@ -16,6 +16,7 @@
 // Bounds (GB300, 8192 tokens of 28 heads, fp32 in, bf16 out): 176 MB in 32 us, 5.5 TB/s, 81 % of
 // the measured copy rate: HBM; the rest is the angles in front of a block's first loads.  Asking
 // for the loads before the angles was slower (36.8), and so were streaming stores (35).
+#include <climits>
 #include <cmath>
 
 #include "attn_common.cuh"
@@ -173,6 +174,7 @@ extern "C" oomb_status oomb_bias_rope_axes(const void* in, int in_dtype, const f
   if ((in_dtype != OOMB_BF16 && in_dtype != OOMB_FP32) || (out_dtype != OOMB_BF16 && out_dtype != OOMB_FP32))
     return OOMB_ERR_DTYPE;
   if (in == out && in_dtype != out_dtype) return OOMB_ERR_ARG;
+  if ((int64_t)H * d > INT_MAX) return OOMB_ERR_UNSUPPORTED;  // the kernel counts a token's pairs in 32 bits
   RopeArgs a = {};
   const int half = d / 2;
   if (mode != 0) {
