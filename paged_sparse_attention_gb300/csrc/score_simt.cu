@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(256) score_dkdv_join(const __grid_constant__ S
 // keys [doc_start[c], max(t + 1, min(doc_start[c] + prefix_len[c], doc_start[c + 1]))).
 __global__ void doc_spans(const int64_t* __restrict__ doc_start, const int64_t* __restrict__ prefix_len, int n_docs,
                           int64_t q_start, int n_q, int64_t* __restrict__ key_begin, int64_t* __restrict__ key_end) {
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= n_q) return;
   const int64_t t = q_start + i;
   int lo = 0, hi = n_docs + 1;  // boundaries <= t
@@ -1005,7 +1005,7 @@ cudaError_t launch_score_bwd(const ScoreArgs& s, cudaStream_t st) {
 
 cudaError_t launch_doc_spans(const int64_t* doc_start, const int64_t* prefix_len, int n_docs, int64_t q_start, int n_q,
                              int64_t* key_begin, int64_t* key_end, cudaStream_t st) {
-  doc_spans<<<(n_q + 127) / 128, 128, 0, st>>>(doc_start, prefix_len, n_docs, q_start, n_q, key_begin, key_end);
+  doc_spans<<<(unsigned)(((int64_t)n_q + 127) / 128), 128, 0, st>>>(doc_start, prefix_len, n_docs, q_start, n_q, key_begin, key_end);
   count_launches(1);
   return cudaGetLastError();
 }
