@@ -195,15 +195,20 @@ OOMB_API oomb_status oomb_page_free(oomb_pool* pool, int64_t first_logical_page,
 
 /* Paged KV append (explainer 2.B "Paged KV Cache and Gradient Management"; the
  * lay summary's "Trick A": each chunk's KV drops onto the next free page, no
- * copying of earlier pages).  Opens ceil((first_token+n)/P) - first_token/P new
+ * copying of earlier pages).  Opens ceil((first_token+n)/P) - ceil(first_token/P) new
  * logical pages, taking physical pages from the free list and writing their
  * page-table entries; copies k, v ([n_tokens, Hkv, d], dtype, device) into the
  * pools; zeroes the dK/dV rows of the written tokens (with offload_grads: marks
  * the pages' host gradient blocks as holding nothing yet, see grad_state); writes
  * the page summary
  * (fp32 mean key over the tokens present) of every touched page.
- * first_token must equal the tokens already appended and be a multiple of P.
- * Errors: ARG, ALIGN, OUT_OF_PAGES (nothing is written), CUDA. */
+ * first_token must equal the tokens already appended.  With pools in device memory it may
+ * lie inside the last page, which is then continued (one token after another behind a
+ * prompt): its tokens and their gradients stay, and its summary becomes that of all its
+ * tokens, with the bits of a single append.  With offload, and in the staged, deferred and
+ * fused forms below and above, it has to be a multiple of P.
+ * Errors: ARG (also a last page that was freed), ALIGN, OUT_OF_PAGES (nothing is written),
+ * CUDA. */
 OOMB_API oomb_status oomb_kv_append(oomb_pool* pool, const void* k, const void* v, int64_t first_token, int n_tokens,
                            void* stream);
 
@@ -362,7 +367,8 @@ typedef struct {
  * are in a selected page and in the row's range, LSE its natural-log sum.  A row that sees
  * no key gets O = 0 and LSE = -inf.  Differences from oomb_chunk_attn_fwd:
  *  - q_start may be any position (one new token, a chunk that starts inside a page); the
- *    chunk's own K/V must be appended.
+ *    chunk's own K/V must be appended (oomb_kv_append continues an open page).  A selection
+ *    for such a chunk: oomb_page_select or oomb_window_select from its first page's start.
  *  - with key_end given, the selection may name any appended page, so that a row can see
  *    keys after its own position (a prefix); without it, pages up to the chunk's end.
  *  - pages that no row of a tile can see are not read; where there are few rows the keys are

@@ -56,6 +56,10 @@ AppendJob append_job(const Geometry& g, void* k_pool, void* v_pool, float* dk_po
                      int32_t* table, const void* k, const void* v, int64_t first_token, int64_t total_tokens,
                      int n_new, int first_new_logical, uint8_t* grad_state, const StageArgs* stage, uint32_t* err);
 
+// The part of an append that goes on the open page `phys` (job.first_new_logical, which
+// job.first_token lies in).
+cudaError_t launch_kv_append_open(const AppendJob& job, int phys, cudaStream_t st);
+
 template <typename T>
 __device__ __forceinline__ float append_to_f(T x);
 template <>
@@ -68,7 +72,9 @@ __device__ __forceinline__ float append_to_f<__nv_bfloat16>(__nv_bfloat16 x) { r
 // synchronise on named barrier `bar_id` (the whole block when it has 256 threads).
 // ROWS: K and V rows in flight per thread; every thread still adds its rows in
 // ascending order, so the summary's bits do not depend on it.
-template <typename T, int ROWS = kAppendRowsInFlight>
+// OPEN: the page holds tokens already (first_token lies inside it).  They and their gradients stay
+// as they are; their keys are read back for the summary, which gets the bits of one append.
+template <typename T, int ROWS = kAppendRowsInFlight, bool OPEN = false>
 __device__ void append_unit(const AppendJob& a, int phys, int i, int h, int tid, float* part, int bar_id) {
   const Geometry& g = a.g;
   const int P = g.P, d = g.d, Hkv = g.Hkv;
@@ -87,6 +93,7 @@ __device__ void append_unit(const AppendJob& a, int phys, int i, int h, int tid,
   const int c = tid % nvec, rg = tid / nvec;
   const size_t blk = ((size_t)phys * Hkv + h) * (size_t)P * d;
   const int64_t tok0 = t0 - a.first_token;  // row 0 of the page in the chunk's K/V
+  const int r0 = OPEN ? (int)-tok0 : 0;     // rows that are there
   T* k_pool = reinterpret_cast<T*>(a.k_pool);
   T* v_pool = reinterpret_cast<T*>(a.v_pool);
   const T* k = reinterpret_cast<const T*>(a.k);
@@ -128,7 +135,7 @@ __device__ void append_unit(const AppendJob& a, int phys, int i, int h, int tid,
     const int nvec4 = P * d / 4;
     float4* gk = reinterpret_cast<float4*>(a.dk_pool + blk);
     float4* gv = reinterpret_cast<float4*>(a.dv_pool + blk);
-    for (int idx = tid; idx < nvec4; idx += kAppendThreads) {
+    for (int idx = OPEN ? r0 * (d / 4) + tid : tid; idx < nvec4; idx += kAppendThreads) {
       __stcs(gk + idx, make_float4(0.f, 0.f, 0.f, 0.f));
       __stcs(gv + idx, make_float4(0.f, 0.f, 0.f, 0.f));
     }
@@ -141,7 +148,9 @@ __device__ void append_unit(const AppendJob& a, int phys, int i, int h, int tid,
       for (int u = 0; u < ROWS; ++u) {
         const int r = rb + u * n_rg;
         kr[u] = vr[u] = make_uint4(0, 0, 0, 0);  // absent tail rows of a partial page are zero
-        if (r < m) {
+        if (OPEN && r < r0) {
+          kr[u] = *reinterpret_cast<const uint4*>(k_pool + blk + (size_t)r * d + (size_t)c * VEC);
+        } else if (r < m) {
           const size_t off = ((size_t)(tok0 + r) * Hkv + h) * d + (size_t)c * VEC;
           kr[u] = __ldcs(reinterpret_cast<const uint4*>(k + off));
           vr[u] = __ldcs(reinterpret_cast<const uint4*>(v + off));
@@ -152,7 +161,7 @@ __device__ void append_unit(const AppendJob& a, int phys, int i, int h, int tid,
       for (int u = 0; u < ROWS; ++u) {
         const int r = rb + u * n_rg;
         if (r < P) {
-          if (!stg.skip_pool) {
+          if (!stg.skip_pool && (!OPEN || r >= r0)) {
             const size_t off = blk + (size_t)r * d + (size_t)c * VEC;
             *reinterpret_cast<uint4*>(k_pool + off) = kr[u];
             *reinterpret_cast<uint4*>(v_pool + off) = vr[u];

@@ -35,6 +35,15 @@ __global__ void __launch_bounds__(kAppendThreads)
   append_unit<T>(job, np.phys[i], i, h, threadIdx.x, part, 1);
 }
 
+// The page that first_token lies in (token after token behind a prompt): its own launch, so that
+// the whole pages' kernel and the fused one carry nothing of it.
+template <typename T>
+__global__ void __launch_bounds__(kAppendThreads)
+    kv_append_open_kernel(const __grid_constant__ AppendJob job, int phys) {
+  __shared__ float part[kAppendThreads * 8];
+  append_unit<T, kAppendRowsInFlight, true>(job, phys, 0, blockIdx.x, threadIdx.x, part, 1);
+}
+
 }  // namespace
 
 AppendJob append_job(const Geometry& g, void* k_pool, void* v_pool, float* dk_pool, float* dv_pool, float* summary,
@@ -97,6 +106,15 @@ cudaError_t launch_kv_append(const Geometry& g, void* k_pool, void* v_pool, floa
     count_launches(1);
   }
   return cudaSuccess;
+}
+
+cudaError_t launch_kv_append_open(const AppendJob& job, int phys, cudaStream_t st) {
+  if (job.g.dtype == OOMB_FP32)
+    kv_append_open_kernel<float><<<job.g.Hkv, kAppendThreads, 0, st>>>(job, phys);
+  else
+    kv_append_open_kernel<__nv_bfloat16><<<job.g.Hkv, kAppendThreads, 0, st>>>(job, phys);
+  count_launches(1);
+  return cudaGetLastError();
 }
 
 }  // namespace oomb

@@ -240,11 +240,14 @@ static oomb_status prepare_append(oomb_pool* p, const void* k, const void* v, in
                                   void* stream, PendingAppend* pa) {
   if (!p || !k || !v || n_tokens <= 0 || first_token < 0) return OOMB_ERR_ARG;
   if (first_token != p->n_tokens) return OOMB_ERR_ARG;
-  if (first_token % p->g.P != 0) return OOMB_ERR_ALIGN;
-  if (!aligned(k, 16) || !aligned(v, 16)) return OOMB_ERR_ALIGN;
   const int P = p->g.P;
+  if (first_token % P != 0) {  // the open page is continued, where it is in device memory
+    if (p->d.offload) return OOMB_ERR_ALIGN;
+    if (p->table[first_token / P] < 0) return OOMB_ERR_ARG;  // freed
+  }
+  if (!aligned(k, 16) || !aligned(v, 16)) return OOMB_ERR_ALIGN;
   const int64_t end = first_token + n_tokens;
-  const int64_t first_page = first_token / P;
+  const int64_t first_page = (first_token + P - 1) / P;  // the first new one
   const int64_t end_page = (end + P - 1) / P;
   if (end_page > p->g.max_logical) return OOMB_ERR_ARG;
   const int n_new = (int)(end_page - first_page);
@@ -269,10 +272,18 @@ static oomb_status kv_append_impl(oomb_pool* p, const void* k, const void* v, in
   PendingAppend pa;
   oomb_status s = prepare_append(p, k, v, first_token, n_tokens, stream, &pa);
   if (s != OOMB_OK) return s;
-  cudaError_t e = launch_kv_append(p->g, p->d.k_pool, p->d.v_pool, p->d.dk_pool, p->d.dv_pool, p->d.summary,
-                                   p->d.page_table, k, v, first_token, n_tokens, pa.end, pa.newp.data(), pa.n_new,
-                                   (int)pa.first_page, p->d.offload_grads ? p->d.grad_state : nullptr, stage,
-                                   p->d.error_word, (cudaStream_t)stream);
+  cudaError_t e = cudaSuccess;
+  if (first_token % p->g.P != 0) {
+    const int64_t open = first_token / p->g.P;
+    e = launch_kv_append_open(append_job(p->g, p->d.k_pool, p->d.v_pool, p->d.dk_pool, p->d.dv_pool, p->d.summary,
+                                         p->d.page_table, k, v, first_token, pa.end, 1, (int)open, nullptr, nullptr,
+                                         p->d.error_word),
+                              p->table[open], (cudaStream_t)stream);
+  }
+  if (e == cudaSuccess)
+    e = launch_kv_append(p->g, p->d.k_pool, p->d.v_pool, p->d.dk_pool, p->d.dv_pool, p->d.summary, p->d.page_table, k,
+                         v, first_token, n_tokens, pa.end, pa.newp.data(), pa.n_new, (int)pa.first_page,
+                         p->d.offload_grads ? p->d.grad_state : nullptr, stage, p->d.error_word, (cudaStream_t)stream);
   if (e != cudaSuccess) {
     pa.release(p);
     return cuda_status(e);
