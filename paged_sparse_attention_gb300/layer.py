@@ -37,6 +37,15 @@ from . import _lib as L
 from .pool import PagedKVPool
 
 
+def prefix_cut(doc_start, prefix_len, chunk: int, n: int):
+    """Which documents' prefixes a layer step that goes ``chunk`` by chunk over ``n`` tokens cannot show to
+    all of their rows: those that go past the end of the chunk in which their document starts (a
+    chunk's keys are not there yet when the one before attends).  Bool [n_docs], where doc_start is."""
+    first, last = doc_start[:-1].clamp(0, n), doc_start[1:].clamp(0, n)
+    end = torch.minimum(doc_start[:-1] + torch.minimum(prefix_len, doc_start[1:] - doc_start[:-1]), last)
+    return (end > first) & ((end - 1) // chunk > first // chunk)
+
+
 class LayerStep:
     """Weights Wq [Dm, Hq*d], Wk and Wv [Dm, Hkv*d] (the pool's dtype, device), biases
     fp32 [H*d] or None.  Selection: top-K (``top_k``, ``n_sink``) or a local window
@@ -160,7 +169,8 @@ class LayerStep:
         ``positions`` int64 [n_axes, N] with ``pair_axis``.  ``doc_start`` int64 [n_docs + 1]
         and optionally ``prefix_len`` int64 [n_docs]: packed documents; a row sees its own
         document only, and keys of this and earlier chunks (so a prefix that is to be seen by
-        all of its rows has to end with its chunk).  The library's top-K selection and its sink
+        all of its rows has to end with its chunk; ``prefix_cut`` of the result, bool [n_docs], says
+        whose does not).  The library's top-K selection and its sink
         pages do not know the documents: with ``doc_start`` every page is kept (``top_k`` = -1), a
         window goes without sinks, or the pages are given.  With ``w_norm``: ``Y`` [N, Dm], the
         previous block's output, and ``dX_out`` [N, Dm], the gradient that reaches the residual
@@ -168,8 +178,6 @@ class LayerStep:
         dw_norm, dw_post, dgate (those that exist); dX and dY are then in the pool's dtype.
         Errors that kernels met are told by oomb_check (the pool) and, with ``w_norm``,
         oomb_block_norm_check."""
-        pool, h, dev = self.pool, self.pool.handle, self.dev
-        N, Dm, Hq, Hkv, d = X.shape[0], self.Dm, self.Hq, self.Hkv, self.d
         if (positions is None) != (self.pair_axis is None):
             raise ValueError("LayerStep: positions and pair_axis come together")
         if self.w_norm is None and (Y is not None or dX_out is not None):
@@ -185,6 +193,17 @@ class LayerStep:
         self._positions = positions
         self._docs = None if doc_start is None else (doc_start, prefix_len)
         self._scores = self.softcap != 0.0 or self.slopes is not None or self._docs is not None
+        try:
+            out = self._run(X, dO, sel_override, Y, dX_out)
+        finally:  # nothing of a call is kept for the next
+            self._positions = self._docs = self._ws_fwd = None
+        if prefix_len is not None:
+            out["prefix_cut"] = prefix_cut(doc_start, prefix_len, self.chunk, X.shape[0])
+        return out
+
+    def _run(self, X, dO, sel_override, Y, dX_out) -> dict:
+        pool, h, dev = self.pool, self.pool.handle, self.dev
+        N, Dm, Hq, Hkv, d = X.shape[0], self.Dm, self.Hq, self.Hkv, self.d
         if self._scores:
             self._ws_fwd = pool.workspace(L.OOMB_OP_SCORE_FWD, self.chunk)
         starts = list(range(0, N, self.chunk))

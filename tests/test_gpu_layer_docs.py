@@ -93,3 +93,16 @@ def test_documents_and_pages(cfg, kind):
     err = (out["dbk"].to(F64).cpu() - g64["bk"]).abs()
     assert (err <= tol * gk.abs().sum(0).view(-1)).all() and g64["bk"].abs().max() > 0
     pool.close()
+
+
+def test_prefixes_that_cross_a_chunk_are_told():
+    dev = torch.device("cuda")
+    pool = PagedKVPool(2, 1, 64, 32, 4, 4, torch.float32, dev)
+    W = torch.zeros(8, 128, device=dev), torch.zeros(8, 64, device=dev), torch.zeros(8, 64, device=dev)
+    X, dO = torch.zeros(100, 8, device=dev), torch.zeros(100, 2, 64, device=dev)
+    docs, pre = torch.tensor([0, 20, 60, 70, 100], device=dev), torch.tensor([20, 13, 200, 26], device=dev)
+    step = LayerStep(pool, *W, chunk=32)
+    assert step.run(X, dO, doc_start=docs, prefix_len=pre)["prefix_cut"].tolist() == [False, True, True, False]
+    assert "prefix_cut" not in step.run(X, dO, doc_start=docs)
+    assert L.oomb_check(pool.handle) == 0
+    pool.close()

@@ -42,3 +42,26 @@ def test_what_goes_with_documents(make, kw, run):
     args = {} if run is None else dict(doc_start=DOCS, **run)
     with pytest.raises(AssertionError, match="reached the library"):
         make(**kw).run(X, DO, **args)
+
+
+def test_prefixes_that_cross_a_chunk():
+    """Against the rows themselves: a row of the prefix' document sees less than the prefix."""
+    g = torch.Generator().manual_seed(3)
+    for _ in range(300):
+        chunk, n = int(torch.randint(1, 9, (1,), generator=g)), int(torch.randint(1, 40, (1,), generator=g))
+        cuts = torch.randint(-5, n + 6, (5,), generator=g).sort().values
+        pre = torch.randint(-3, 20, (4,), generator=g)
+        want = []
+        for c in range(4):
+            a, b = int(cuts[c]), int(cuts[c + 1])
+            end = min(a + int(pre[c]), b, n)  # the prefix, as far as there are tokens
+            rows = range(max(a, 0), min(b, n))
+            want.append(any(min(end, (i // chunk + 1) * chunk) < end for i in rows))
+        assert layer.prefix_cut(cuts, pre, chunk, n).tolist() == want, (chunk, n, cuts, pre)
+
+
+def test_nothing_of_a_call_is_kept(make):
+    step = make(softcap=3.0)
+    with pytest.raises(AssertionError):
+        step.run(X, DO, doc_start=DOCS)
+    assert step._docs is None and step._positions is None and step._ws_fwd is None
