@@ -20,11 +20,12 @@
 //                    not fill the SMs
 //
 // Shares against none, fp32, 1024 rows of 2 heads on 4096 tokens in documents of 1000, forward and
-// backward with its joins: 150 us against 539.  Of it the forward 31, dQ 37, dK/dV 53, each with a
-// block or two an SM, and the joins 25.  With more rows, 900 of 6 heads on 3000 keys: 172 us (20 of
+// backward with its joins: 150 us call after call (130 of them on the device) against 539.  One by
+// one from a cold cache the forward takes 29, dQ 36, dK/dV 48, each with a block or two an SM, the
+// joins 27, D and the ranges 7.  With more rows, 900 of 6 heads on 3000 keys: 172 us (20 of
 // the FMA pipe's 74 TFLOP/s) and 483 (25 with the scores that both passes form).  Bound by shared
-// memory, its reads and their latency at two blocks of 8 warps an SM (128 registers); 8 x 4 scores
-// a thread (194 / 513) and, for d > 64, 2 x 4 (1515 against 1175 backward) are slower.
+// memory, its reads and their latency at two blocks of 8 warps an SM (d <= 64; 128 registers); 8 x 4
+// scores a thread (194 / 513) and, for d > 64, 2 x 4 (1515 against 1175 backward) are slower.
 #include <climits>
 #include <cmath>
 
@@ -186,8 +187,10 @@ struct ScoreForm {
 __device__ __forceinline__ ScoreForm score_form(const ScoreArgs& s, int hq) {
   return {s.cap > 0.f ? s.a.scale / s.cap : s.a.scale * kLog2e, s.cap * kLog2e, s.slopes ? s.slopes[hq] * kLog2e : 0.f};
 }
-// tanh: to |x| = 0.6 a polynomial in x^2 fitted for the least relative error of tanh(x) / x
-// (2.5e-9), from there 1 - 2 / (1 + e^2x).  Both are formed: the lanes of a warp differ.
+// tanh: to |x| = 0.6 a polynomial in x^2 fitted for the least largest relative error of tanh(x) / x
+// on [0, 0.6] (a linear program over points of the interval forms it again); with its coefficients
+// rounded to fp32 it is off by 4.9e-9, evaluated in fp32 by 7.2e-8.  From there 1 - 2 / (1 + e^2x).
+// Both are formed: the lanes of a warp differ.
 __device__ __forceinline__ float score_tanh(float x) {
   const float z = x * x;
   float p = fmaf(-0.00585216861f, z, 0.0207536292f);
@@ -844,8 +847,9 @@ __global__ void doc_spans(const int64_t* __restrict__ doc_start, const int64_t* 
   key_end[i] = e;
 }
 
-// Thread blocks that may share one tile's keys: as many as fill the SMs twice (two blocks
-// fit an SM) when the rows alone do not, at most 32 (the join reads every share).
+// Thread blocks that may share one tile's keys: as many as fill the SMs twice when the rows alone do
+// not, at most 32 (the join reads every share).  Two blocks fit an SM up to d = 120; of wider heads
+// only one does, and the second half of the blocks waits for the first.
 int simt_split_limit(const Geometry& g, int n_q) {
   const int64_t tiles = (int64_t)((n_q + kRows - 1) / kRows) * g.Hq;
   return (int)std::min<int64_t>(32, std::max<int64_t>(1, 2 * (int64_t)device_sm_count() / tiles));

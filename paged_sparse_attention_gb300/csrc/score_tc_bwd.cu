@@ -19,9 +19,9 @@
 // Bounds (GB300).  8192 rows on 193 pages, 28 query heads on 4, cap 50: 7.13 ms, 849 TFLOP/s, 43 % of
 // the measured bf16 peak, by TMEM and shared-memory traffic as the plain backward (915 there, and
 // 910 here without the cap); a step of 128 rows costs 3.6 us a thread block, 3.9 with the cap.
-// Documents of 1500 tokens, 4001 rows: 325 us, 4.9 us a step: 40 % of the steps are cut by a range,
-// and blocks of 25 steps pay for their set-up and for the sum over the cluster (tensor pipe active
-// 46 %).
+// Documents of 1500 tokens, 4001 rows: 320 us of this kernel, 369 of the call (score_bwd_prep 24,
+// score_bwd_convert 16), 4.9 us a step: 40 % of the steps are cut by a range, and blocks of 25 steps
+// pay for their set-up and for the sum over the cluster (tensor pipe active 46 %).
 //
 // Warp roles of score_bwd_tc (448 threads): warp 0 TMA producer, warp 1 MMA issuer and TMEM
 // owner, warps 2-9 softmax (thread = key row, 32 of a half's 64 query columns) and epilogue,
@@ -578,8 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Blocks [0, n_tiles): the row ranges of one query tile.  The others, one warp per (row, head)
 // of the padded range: D = rowsum(dO * O) and LSE * log2(e) into [Hq, n_pad] buffers (rows
-// without keys and padded rows: LSE = +inf, so P = 0; cap2 is taken off) and the row of the fp32 dQ accumulator
-// zeroed.
+// without keys and padded rows: LSE = +inf, so P = 0; cap2 is taken off) and the row of the fp32 dQ
+// accumulator zeroed.  D comes from O as the forward rounded it to bf16, the only form of it that a
+// caller keeps: off by 2^-8 |dO| |O| at most, as much as the rounded P of the products.
 __global__ void __launch_bounds__(256) score_bwd_prep(const __grid_constant__ ScoreArgs s, float cap2, int n_pad,
                                                       int n_tiles, float* __restrict__ Dbuf, float* __restrict__ lse2,
                                                       float* __restrict__ dq_acc, longlong2* __restrict__ span,

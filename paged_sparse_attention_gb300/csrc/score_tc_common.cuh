@@ -2,8 +2,9 @@
 //
 // Scores are kept in units of log2: s2 = s log2(e), so that P = 2^(s2 - m).  With
 // x = scale q.k / cap the capped score is cap tanh(x).  Where all of a warp's |x| are small,
-// tanh(x) = x times a polynomial in x^2, fitted for the least relative error: degree 2 up to
-// 1/4 (4.0e-7) and degree 3 up to 1/2 (5.4e-7); the scale and the cap are folded into the
+// tanh(x) = x times a polynomial in x^2, fitted for the least largest relative error on the
+// interval (a linear program over points of it forms them again: 3.9e-7 and 5.3e-7 at best): degree 2
+// up to 1/4 (4.0e-7) and degree 3 up to 1/2 (5.4e-7); the scale and the cap are folded into the
 // coefficients, so a score costs two or three multiply-adds more than an uncapped one.
 // Elsewhere tanh(x) = 1 - 2 / (1 + e^2x), exact at saturation, for two more operations of the
 // exponential unit.  (tanh.approx is one instruction, but off by 2^-11: 0.02 of a score at a

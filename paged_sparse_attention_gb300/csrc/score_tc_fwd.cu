@@ -16,8 +16,9 @@
 // against 28.6, 1024 pages 52.7 against 327.  score_fwd_plan, where rows have ranges: documents of
 // 12000 tokens with prefixes, 8192 rows 555 us with it, 614 without; of 1500, 4001 rows 155 and 204.
 //
-// Bounds (GB300).  Packed, one token on 131,072 with 28 query heads on 4: 58 us for 268 MB, 4.7 TB/s
-// with the join, HBM (about 6.4 TB/s once the loads run; 10 us are launch, set-up and join).  Rows,
+// Bounds (GB300).  Packed, one token on 131,072 with 28 query heads on 4: 56 us for 268 MB with the
+// join, 4.8 TB/s: 18 us of launch, set-up and join, then HBM (twice and four times the tokens take
+// 95 and 172 us: 7.0 TB/s of reads).  Rows,
 // 4096 rows on 97 pages: cap 50 in 572 us, 1064 TFLOP/s, 54 % of the measured bf16 peak; without a
 // modification 498 us, 1221 (the plain forward 531), with a bias 475, with a cap that most scores
 // come near 834: there the exponential unit is the bound, with three operations a score; else the
@@ -838,14 +839,16 @@ cudaError_t launch_score_fwd_tc(ScoreArgs& s, cudaStream_t st) {
     // rows); up to 16 pages a block each: one of its tiles then idles, but the shorter walk counts
     // for more.  28 query heads on 4, 1 row and 18: 4 pages 9.5 and 13.1 us in 4 blocks, 10.1 and 15.7
     // in 2; 16 pages 10.9 and 14.8 in 16, 10.9 and 16.7 in 8; 64 pages 13.2 and 19.8 in 32, 13.9 and
-    // 20.1 in 16 (from a cold L2 25.6 and 24.4 for 17 rows)
+    // 20.1 in 16 (from a cold L2 25.6 and 24.4 for 17 rows).  16 heads on 2 and 8 on 8, 1 row and 8 on
+    // 4 to 1024 pages: within 4 % of the best cut
     const int pages = s.a.max_sel, each = (int64_t)s.a.n_q * g.Hq > 256 ? 4 : 2;
     s.n_split = std::min(limit / 2, std::max((pages + each - 1) / each, std::min(pages, 16)));
   } else {
     // Waves of blocks, each as long as its pages and about four more for set-up and epilogue; once
     // the keys are cut, the join takes as long as two pages and one more for every 8000 rows of
     // parts (28 query heads: 200 rows on 16 pages 25.1 us in 4 parts, 39.4 in one; 300 rows on 8
-    // pages 27.6 in 2, 25.0 in one).
+    // pages 27.6 in 2, 25.0 in one).  Made for many heads: of 16 on 2 and 8 on 8 it cuts too little and
+    // loses up to a quarter (300 rows on 8 pages, 8 on 8: 23.8 us in 3 parts, 18.9 in 8).
     const int64_t units = (int64_t)p.n_pairs * g.Hq;
     double best = 0.0;
     for (int n = 1; n <= limit && (n == 1 || s.a.max_sel / n >= 2); ++n) {

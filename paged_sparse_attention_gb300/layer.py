@@ -273,6 +273,8 @@ class LayerStep:
                             workspace=self.ws)
                 first = False
             if norm:
+                # the norm's backward reads its rows in the residual stream's type, so the gradient of the
+                # normed input, summed in fp32 over the three projections, is rounded to it once here
                 du = dX[s:s + n]
                 if pool.dtype != f32:
                     du = torch.empty((n, Dm), dtype=pool.dtype, device=dev)
