@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(256) score_join(const __grid_constant__ ScoreA
 
 // The same for few parts and, usually, many rows: a warp per (row, head), lane z holding part z's
 // log-sum-exp, four columns a lane (512 rows of 28 heads in 2 parts: the whole forward 35.6 us
-// against 50.7 with a block a row).
+// against 50.7 with a block a row; of 16 heads in 3 32.4 against 40.1, of 8 in 4 26.1 against 30.1).
 constexpr int kFewParts = 16;
 template <typename T>
 __global__ void __launch_bounds__(256) score_join_few(const __grid_constant__ ScoreArgs s) {
