@@ -86,6 +86,7 @@ typedef enum {
 #define OOMB_DEVERR_SEL 0x4u      /* selection index out of range */
 #define OOMB_DEVERR_TMEM 0x8u     /* tensor-memory allocation failed */
 #define OOMB_DEVERR_SMEM 0x10u    /* a kernel's shared-memory window is not 1 KB aligned (nothing computed) */
+#define OOMB_DEVERR_TOKEN 0x20u   /* a token or target at or after the vocabulary's end */
 
 /* Length of the pool's control block (oomb_pool_desc.error_word), in uint32.
  * Word 0 holds the error bits above; words 4..5 are the grid-barrier counters of
@@ -564,6 +565,90 @@ OOMB_API oomb_status oomb_block_norm_check(void* stream, uint32_t* bits_out);
 /* For tests of a caller's error handling: while on is not 0, the copy of the first row of calls
  * with many rows is not started, so that its wait runs out as described above. */
 OOMB_API void oomb_block_norm_test_timeout(int on);
+
+/* ---------------------------------------------------------- a model's two ends
+ * What a training program needs before the first layer and behind the last one: embeddings of
+ * the tokens, the last norm, and the loss over the vocabulary, with their gradients.  Tokens and
+ * targets are int64; a negative one is none (padding, a prompt's token that is not a target): its
+ * row is zero and sends no gradient.  One at or after V is told by OOMB_DEVERR_TOKEN in
+ * error_word (a device uint32, e.g. word 0 of a pool's control block, which oomb_check reads and
+ * clears; oomb_word_check does that for a word outside a pool) and then counts as none. */
+
+/* out[i, :] = scale * table[tokens[i], :], rounded once; zeros where there is no token.
+ * tokens [n], table [V, D] and out [n, D] (dtype, device).  Pointers on their element's size;
+ * fastest with rows that start on 16 bytes.
+ * Errors: ARG (also a scale that is not finite), ALIGN, DTYPE, UNSUPPORTED (D > 2^24), CUDA. */
+OOMB_API oomb_status oomb_embed_fwd(const int64_t* tokens, int n, const void* table, int V, int D, int dtype,
+                                    float scale, void* out, uint32_t* error_word, void* stream);
+
+/* Its gradient: d_table[t, :] (fp32 [V, D]) gets scale * the sum of d_out[i, :] (dtype) over the
+ * rows i with tokens[i] = t, added to what it holds when accumulate is not 0 (chunk after chunk of
+ * a sequence; a projection that shares the table), else written.  Rows that no token names are
+ * left as they are in either case, rows of d_out without a token are not read.  The rows of a
+ * token are summed in fp32 in a fixed order: the same bits on every run.  Workspace:
+ * oomb_embed_workspace(n, D) bytes (it grows with n: one for the longest chunk serves them all),
+ * contents scratch; calls that may run at once need one each.
+ * Errors: those of oomb_embed_fwd, WORKSPACE. */
+OOMB_API oomb_status oomb_embed_bwd(const int64_t* tokens, int n, const void* d_out, int V, int D, int dtype,
+                                    float scale, float* d_table, int accumulate, void* workspace, size_t ws_bytes,
+                                    uint32_t* error_word, void* stream);
+OOMB_API size_t oomb_embed_workspace(int n, int D);
+
+/* Layer norm over rows of D elements: out = (x - mean) * r * w + b with mean the row's mean and
+ * r = 1 / sqrt(its variance + eps).  x, out [n, D] (dtype; out may be x), w, b fp32 [D] or NULL
+ * (1 and 0).  mean and rstd ([n] fp32, or NULL) keep the row's mean and r for the backward.
+ * fp32 arithmetic, the output rounded once.  Pointers on their element's size; fastest with rows
+ * that start on 16 bytes.
+ * Errors: ARG, ALIGN, DTYPE, UNSUPPORTED (D > 16384), CUDA. */
+OOMB_API oomb_status oomb_layer_norm_fwd(const void* x, const float* w, const float* b, float eps, int n, int D,
+                                         int dtype, void* out, float* mean, float* rstd, void* stream);
+
+/* Its backward, from the forward's x, w, mean and rstd: dy is the gradient of out, dx_out one that
+ * reaches x by another way (NULL: none).  Written: dx ([n, D], dtype; may be dx_out) and, where
+ * not NULL, dw and db (fp32 [D], summed over the rows in a fixed order; added to what they hold
+ * when accumulate is not 0).  Workspace: oomb_layer_norm_workspace(n, D) bytes, contents scratch;
+ * it grows with n.  Errors: those of oomb_layer_norm_fwd, WORKSPACE. */
+OOMB_API oomb_status oomb_layer_norm_bwd(const void* x, const float* w, const float* mean, const float* rstd,
+                                         const void* dy, const void* dx_out, int n, int D, int dtype, void* dx,
+                                         float* dw, float* db, int accumulate, void* workspace, size_t ws_bytes,
+                                         void* stream);
+OOMB_API size_t oomb_layer_norm_workspace(int n, int D);
+
+/* Softmax cross entropy of the output projection z = x W^T over a vocabulary of V, without keeping
+ * the logits z: x [n, D] and W [V, D] (dtype), targets [n].  With softcap > 0 the logits are
+ * softcap * tanh(z / softcap).  Written, fp32 [n]: lse = log sum_v exp(z_v) and loss = lse - z at
+ * the target, both 0 in rows without a target, which are not read.  fp32 accumulation; fp32
+ * operands are multiplied in parts that keep all of their 24 bits.  Pointers on their element's
+ * size; W is read in place where its rows start on 16 bytes, else through the workspace.
+ * Workspace: oomb_head_loss_workspace(n, D, V, dtype, 0) bytes on 256 bytes, contents scratch; it
+ * grows with n; calls that may run at once need one each.  A kernel wait that runs out (about a
+ * second) sets OOMB_DEVERR_TIMEOUT in error_word.  Capturable in a CUDA graph.
+ * Errors: ARG (also a softcap that is negative, not a number, above 1e30 or below 1e-30 and not
+ * 0), ALIGN, DTYPE, WORKSPACE, CUDA; UNSUPPORTED for D > 65536. */
+OOMB_API oomb_status oomb_head_loss_fwd(const void* x, const void* w, const int64_t* targets, int n, int D, int V,
+                                        int dtype, float softcap, float* loss, float* lse, void* workspace,
+                                        size_t ws_bytes, uint32_t* error_word, void* stream);
+
+/* Its backward, from the forward's inputs and lse, for the gradient scale * d_loss[i] of loss[i]
+ * (d_loss fp32 [n], or NULL: 1): with dz = scale d_loss (softmax(z) - [target]) (1 - tanh^2),
+ *   dx = dz W (written, dtype, zeros in rows without a target; NULL: not wanted)
+ *   dw = dz^T x (dw_dtype: dtype, or fp32; NULL: not wanted), added to what it holds when
+ *   accumulate is not 0 (fp32 only), else written
+ * The logits are formed again, one piece of the vocabulary after another; a piece's dz / scale is
+ * held in the workspace, in bf16 for bf16 operands (scale is applied to the sums: a mean's factor
+ * costs no rounding).  All sums are in a fixed order: the same bits on every run.  Workspace:
+ * oomb_head_loss_workspace(n, D, V, dtype, 1) bytes on 256 bytes (it serves the forward too).
+ * Errors: those of oomb_head_loss_fwd (ARG also for a scale that is not finite, for neither dx
+ * nor dw, and for accumulate with a dw that is not fp32). */
+OOMB_API oomb_status oomb_head_loss_bwd(const void* x, const void* w, const int64_t* targets, const float* lse,
+                                        const float* d_loss, float scale, int n, int D, int V, int dtype,
+                                        float softcap, void* dx, void* dw, int dw_dtype, int accumulate,
+                                        void* workspace, size_t ws_bytes, uint32_t* error_word, void* stream);
+OOMB_API size_t oomb_head_loss_workspace(int n, int D, int V, int dtype, int backward);
+
+/* Synchronize `stream`, read and clear a device error word outside a pool.  Returns OK, KERNEL or
+ * TIMEOUT (bits in *bits_out if non-NULL), ARG, or CUDA.  Not to be called during a capture. */
+OOMB_API oomb_status oomb_word_check(uint32_t* error_word, void* stream, uint32_t* bits_out);
 
 /* dK, dV of tokens [first_token, first_token + n_tokens) read from the paged fp32
  * gradient pool through the page table into token-major [n_tokens, Hkv, d] fp32

@@ -90,6 +90,17 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         "oomb_block_norm_workspace": (sz, [i32, i32]),
         "oomb_block_norm_check": (i32, [vp, C.POINTER(C.c_uint32)]),
         "oomb_block_norm_test_timeout": (None, [i32]),
+        "oomb_embed_fwd": (i32, [vp, i32, vp, i32, i32, i32, f32, vp, vp, vp]),
+        "oomb_embed_bwd": (i32, [vp, i32, vp, i32, i32, i32, f32, vp, i32, vp, sz, vp, vp]),
+        "oomb_embed_workspace": (sz, [i32, i32]),
+        "oomb_layer_norm_fwd": (i32, [vp, vp, vp, f32, i32, i32, i32, vp, vp, vp, vp]),
+        "oomb_layer_norm_bwd": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, i32, vp, sz, vp]),
+        "oomb_layer_norm_workspace": (sz, [i32, i32]),
+        "oomb_head_loss_fwd": (i32, [vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, sz, vp, vp]),
+        "oomb_head_loss_bwd": (i32, [vp, vp, vp, vp, vp, f32, i32, i32, i32, i32, f32, vp, vp, i32, i32, vp, sz, vp,
+                                     vp]),
+        "oomb_head_loss_workspace": (sz, [i32, i32, i32, i32, i32]),
+        "oomb_word_check": (i32, [vp, vp, C.POINTER(C.c_uint32)]),
         "oomb_grad_gather": (i32, [vp, i64, i32, vp, vp, vp]),
         "oomb_grad_prefetch": (i32, [vp, vp, vp, i32, vp, vp, i32, vp]),
         "oomb_grad_carry": (i32, [vp, vp, vp, i32, vp, vp, i32, vp]),
@@ -426,6 +437,140 @@ def oomb_block_norm_check(stream=None) -> int:
 def oomb_block_norm_test_timeout(on: bool) -> None:
     """For tests: while on, the first row of calls with many rows never comes, and they give up on it."""
     load().oomb_block_norm_test_timeout(int(on))
+
+
+def _word(func: str, t, dev: int) -> int:
+    """Address of a caller's device error word: the first of one or more 32-bit integers."""
+    import torch
+    if t is None:
+        raise ValueError(f"{func}: error_word is missing")
+    if t.dtype not in (torch.int32, torch.uint32):
+        raise TypeError(f"{func}: error_word has to be 32-bit integers, not {t.dtype}")
+    if t.numel() < 1:
+        raise ValueError(f"{func}: error_word is empty")
+    return _need(func, "error_word", t, t.shape, t.dtype, dev)
+
+
+def oomb_embed_fwd(tokens, table, out, error_word, scale: float = 1.0, stream=None) -> None:
+    """out[i] = scale * table[tokens[i]] (int64 tokens; a negative one is none: a row of zeros)."""
+    import torch
+    f, dev = "oomb_embed_fwd", torch.cuda.current_device()
+    n = _dims(f, "tokens", tokens, 1)[0]
+    V, D = _dims(f, "table", table, 2)
+    code = _dtype_code(table)
+    _ok(f, load().oomb_embed_fwd(_need(f, "tokens", tokens, (n,), torch.int64, dev), n,
+                                 _need(f, "table", table, (V, D), table.dtype, dev), V, D, code, scale,
+                                 _need(f, "out", out, (n, D), table.dtype, dev), _word(f, error_word, dev),
+                                 _stream(stream)))
+
+
+def oomb_embed_bwd(tokens, d_out, d_table, workspace, error_word, scale: float = 1.0, accumulate: bool = False,
+                   stream=None) -> None:
+    """d_table[t] (fp32) = (accumulate: +=) scale * the sum of d_out over the rows of token t."""
+    import torch
+    f, dev = "oomb_embed_bwd", torch.cuda.current_device()
+    n = _dims(f, "tokens", tokens, 1)[0]
+    V, D = _dims(f, "d_table", d_table, 2)
+    code = _dtype_code(d_out)
+    ws, ws_bytes = _scratch(f, workspace, dev)
+    _ok(f, load().oomb_embed_bwd(_need(f, "tokens", tokens, (n,), torch.int64, dev), n,
+                                 _need(f, "d_out", d_out, (n, D), d_out.dtype, dev), V, D, code, scale,
+                                 _need(f, "d_table", d_table, (V, D), torch.float32, dev), int(accumulate), ws, ws_bytes,
+                                 _word(f, error_word, dev), _stream(stream)))
+
+
+def oomb_embed_workspace(n: int, D: int) -> int:
+    return int(load().oomb_embed_workspace(n, D))
+
+
+def oomb_layer_norm_fwd(x, w, b, out, eps: float = 1e-5, mean=None, rstd=None, stream=None) -> None:
+    """out = (x - mean) * rstd * w + b over the rows of x [n, D]; w and b fp32 [D] or None."""
+    import torch
+    f, dev, f32 = "oomb_layer_norm_fwd", torch.cuda.current_device(), torch.float32
+    n, D = _dims(f, "x", x, 2)
+    _ok(f, load().oomb_layer_norm_fwd(_need(f, "x", x, (n, D), x.dtype, dev), _opt(f, "w", w, (D,), f32, dev),
+                                      _opt(f, "b", b, (D,), f32, dev), eps, n, D, _dtype_code(x),
+                                      _need(f, "out", out, (n, D), x.dtype, dev), _opt(f, "mean", mean, (n,), f32, dev),
+                                      _opt(f, "rstd", rstd, (n,), f32, dev), _stream(stream)))
+
+
+def oomb_layer_norm_bwd(x, w, mean, rstd, dy, dx, dw=None, db=None, dx_out=None, accumulate: bool = False,
+                        workspace=None, stream=None) -> None:
+    """The backward of oomb_layer_norm_fwd; accumulate adds the parameter gradients to their buffers."""
+    import torch
+    f, dev, f32 = "oomb_layer_norm_bwd", torch.cuda.current_device(), torch.float32
+    n, D = shape = _dims(f, "x", x, 2)
+    dt = x.dtype
+    ws, ws_bytes = _scratch(f, workspace, dev)
+    _ok(f, load().oomb_layer_norm_bwd(_need(f, "x", x, shape, dt, dev), _opt(f, "w", w, (D,), f32, dev),
+                                      _need(f, "mean", mean, (n,), f32, dev), _need(f, "rstd", rstd, (n,), f32, dev),
+                                      _need(f, "dy", dy, shape, dt, dev), _opt(f, "dx_out", dx_out, shape, dt, dev),
+                                      n, D, _dtype_code(x), _need(f, "dx", dx, shape, dt, dev),
+                                      _opt(f, "dw", dw, (D,), f32, dev), _opt(f, "db", db, (D,), f32, dev),
+                                      int(accumulate), ws, ws_bytes, _stream(stream)))
+
+
+def oomb_layer_norm_workspace(n: int, D: int) -> int:
+    return int(load().oomb_layer_norm_workspace(n, D))
+
+
+def _head_call(f: str, x, w, targets, dev: int):
+    """Checks the inputs common to both directions; (n, D, V, dtype code, addresses)."""
+    import torch
+    n, D = _dims(f, "x", x, 2)
+    V = _dims(f, "w", w, 2)[0]
+    return n, D, V, _dtype_code(x), (_need(f, "x", x, (n, D), x.dtype, dev), _need(f, "w", w, (V, D), x.dtype, dev),
+                                     _need(f, "targets", targets, (n,), torch.int64, dev))
+
+
+def oomb_head_loss_fwd(x, w, targets, loss, lse, workspace, error_word, softcap: float = 0.0, stream=None) -> None:
+    """loss[i] = lse[i] - z[i, targets[i]] of the logits z = x w^T, which are not kept (targets int64 [n];
+    a negative one is none: loss and lse are 0)."""
+    import torch
+    f, dev, f32 = "oomb_head_loss_fwd", torch.cuda.current_device(), torch.float32
+    n, D, V, code, (ax, aw, at) = _head_call(f, x, w, targets, dev)
+    ws, ws_bytes = _scratch(f, workspace, dev)
+    _ok(f, load().oomb_head_loss_fwd(ax, aw, at, n, D, V, code, softcap, _need(f, "loss", loss, (n,), f32, dev),
+                                     _need(f, "lse", lse, (n,), f32, dev), ws, ws_bytes, _word(f, error_word, dev),
+                                     _stream(stream)))
+
+
+def oomb_head_loss_bwd(x, w, targets, lse, dx, dw, workspace, error_word, d_loss=None, scale: float = 1.0,
+                       softcap: float = 0.0, accumulate: bool = False, stream=None) -> None:
+    """dx (like x, or None) and dw (like w or fp32, or None; accumulate adds to an fp32 one) for the
+    gradient scale * d_loss[i] of loss[i] (d_loss fp32 [n]; None: 1)."""
+    import torch
+    f, dev, f32 = "oomb_head_loss_bwd", torch.cuda.current_device(), torch.float32
+    n, D, V, code, (ax, aw, at) = _head_call(f, x, w, targets, dev)
+    ws, ws_bytes = _scratch(f, workspace, dev)
+    dw_code = code if dw is None else _dtype_code(dw)
+    _ok(f, load().oomb_head_loss_bwd(ax, aw, at, _need(f, "lse", lse, (n,), f32, dev),
+                                     _opt(f, "d_loss", d_loss, (n,), f32, dev), scale, n, D, V, code, softcap,
+                                     _opt(f, "dx", dx, (n, D), x.dtype, dev),
+                                     None if dw is None else _need(f, "dw", dw, (V, D), dw.dtype, dev), dw_code,
+                                     int(accumulate), ws, ws_bytes, _word(f, error_word, dev), _stream(stream)))
+
+
+def oomb_head_loss_workspace(n: int, D: int, V: int, dtype, backward: bool) -> int:
+    """Bytes for calls of up to n rows; dtype: the tensors' (torch.bfloat16 or torch.float32), or its code."""
+    import torch
+    code = {torch.bfloat16: OOMB_BF16, torch.float32: OOMB_FP32}.get(dtype, dtype)
+    if not isinstance(code, int):
+        raise TypeError(f"unsupported dtype {dtype}")
+    return int(load().oomb_head_loss_workspace(n, D, V, code, int(backward)))
+
+
+def oomb_word_check(error_word, stream=None) -> int:
+    """Raises OombError if kernels have set bits in this device error word since the last check; clears it."""
+    import torch
+    bits = C.c_uint32(0)
+    st = load().oomb_word_check(_word("oomb_word_check", error_word, torch.cuda.current_device()), _stream(stream),
+                                C.byref(bits))
+    if st == 7:
+        _ok("oomb_word_check", st)
+    if st != 0:
+        raise OombError("oomb_word_check", st, f"device error bits 0x{bits.value:x}")
+    return bits.value
 
 
 def oomb_grad_gather(pool: int, first_token: int, dk, dv, stream=None) -> None:
