@@ -1,0 +1,432 @@
+// The four matrix products of the loss over a vocabulary (head_loss.cu), on the tensor cores with
+// tcgen05 in pairs of SMs, each with its own epilogue:
+//
+//   kLse   z = X W^T, a tile of 256 rows and 256 columns: row maxima and sums of exponentials
+//   kDz    the same product again: dz = g (exp(z' - lse) - [target]) (1 - (z'/cap)^2), stored
+//   kDx    dx = dz W over a piece of the vocabulary
+//   kDw    dw = dz^T X over the rows with a target
+//
+// Operands are bf16.  fp32 operands are three bf16 parts of 8 bits each (h + m + l = all 24 bits) and
+// a product is the six products of parts that are above 2^-24 of it, the small ones first, so that
+// the accumulator is small while they are added.
+//
+// A tile is 256 x 256 over the two CTAs of a cluster: each holds 128 rows of A and 128 of the 256
+// columns' rows of B, so a CTA loads 32 KB for 64 steps of K instead of the 48 KB that a tile of
+// its own of the same shape would take; that is what keeps the loads below L2's rate.  Six stages
+// of a ring; two accumulators of 256 columns in tensor memory, so that a tile's epilogue (eight
+// warps, a thread a row) runs while the next tile's product does.  Persistent: a cluster takes
+// tiles c, c + clusters, ... in groups of kGroup row tiles, which share the columns' tiles in L2.
+#pragma once
+#include "head_loss.h"
+#include "tc_common.cuh"
+
+namespace oomb {
+namespace head {
+
+enum Mode { kLse = 0, kDz = 1, kDx = 2, kDw = 3 };
+
+constexpr int kTile = 256, kHalf = 128, kStep = 64;  // tile, a CTA's share of it, columns of K a stage
+constexpr int kStages = 6;
+constexpr uint32_t kOperand = kHalf * kStep * 2;     // 16 KB
+constexpr uint32_t kStageBytes = 2 * kOperand;
+constexpr uint32_t kSmem = kStages * kStageBytes + 1024;
+constexpr int kThreads = 320;                        // producer, issuer, 8 epilogue warps
+constexpr int kEpilogueWarps = 8;
+constexpr int kGroup = 8;
+
+struct Barriers {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t tile_full[2], tile_empty[2], done;
+  uint32_t tmem;
+  int abort;
+};
+
+// ---- tcgen05 in pairs
+__device__ __forceinline__ void tmem_alloc2(uint32_t* dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on this barrier in both CTAs once every MMA issued so far is complete.
+__device__ __forceinline__ void commit2(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// The same, on this CTA's barrier only.
+__device__ __forceinline__ void commit_own(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+// Tile of this CTA's shared memory whose bytes are counted on a barrier of the pair's first CTA.
+__device__ __forceinline__ void tma_load2(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+      "%5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Parts multiplied in pass p of six, the smallest products first.
+__device__ __forceinline__ int part_a(int passes, int p) { return passes == 1 ? 0 : (0x021010 >> (4 * (5 - p))) & 15; }
+__device__ __forceinline__ int part_b(int passes, int p) { return passes == 1 ? 0 : (0x201100 >> (4 * (5 - p))) & 15; }
+
+// Place of tile t among tms x tns tiles: groups of kGroup row tiles, row tiles first within one.
+__device__ __forceinline__ void place(int t, int tms, int tns, int& tm, int& tn) {
+  const int per = kGroup * tns, g = t / per, r = t - g * per, rows = min(kGroup, tms - g * kGroup);
+  tn = r / rows;
+  tm = g * kGroup + (r - tn * rows);
+}
+
+__device__ __forceinline__ void store16(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);
+}
+
+// z' and 1 - (z'/cap)^2 of a capped logit
+__device__ __forceinline__ float capped(float z, float cap, float inv_cap) { return cap * tanhf(z * inv_cap); }
+
+// ---- epilogues: 32 columns of a thread's row; c is the first one within the tile's columns
+struct RowSum {
+  float m = -INFINITY, s = 0.f;  // base 2
+  // n: columns that exist (all: 32)
+  __device__ __forceinline__ void add(float (&z)[32], int n) {
+    if (n <= 0) return;
+    float mx = m;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      z[i] *= tc::kLog2e;
+      if (i < n) mx = fmaxf(mx, z[i]);
+    }
+    const float to = mx == -INFINITY ? 0.f : mx;  // nothing above -infinity yet (a NaN is no maximum, but stays one)
+    s *= ex2_approx(m - to);
+    m = mx;
+    float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t[i & 3] += i < n ? ex2_approx(z[i] - to) : 0.f;
+    s += (t[0] + t[1]) + (t[2] + t[3]);
+  }
+};
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    head_gemm(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+              const __grid_constant__ GemmArgs p) {
+  constexpr bool kAmn = MODE == kDw, kBmn = MODE == kDx || MODE == kDw;
+  extern __shared__ uint8_t raw[];
+  __shared__ Barriers bar;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_ctarank();
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  volatile int* abort = &bar.abort;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.tile_full[i], 1);
+      mbar_init(&bar.tile_empty[i], 2 * kEpilogueWarps);
+    }
+    mbar_init(&bar.done, 1);
+    bar.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&ta);
+    tma_prefetch_desc(&tb);
+  }
+  if (warp == 1) tmem_alloc2(&bar.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("fence.proxy.async;" ::: "memory");  // what earlier kernels stored is read by copies
+  const int count = *p.count;
+  const int tms = MODE == kDw ? p.tms : (count + kTile - 1) / kTile;
+  const int steps_all = MODE == kDw ? (count + kStep - 1) / kStep : p.steps;
+  const int tiles = tms * p.tns * p.splits;
+  const int clusters = gridDim.x / 2, first = blockIdx.x / 2;
+  // steps of K of a tile: its split's share
+  auto range = [&](int t, int& k0, int& k1) {
+    const int s = t / (tms * p.tns);
+    k0 = (int)((int64_t)steps_all * s / p.splits);
+    k1 = (int)((int64_t)steps_all * (s + 1) / p.splits);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ loads
+    if (lane == 0) {
+      const uint32_t full0 = mapa_shared(smem_u32(&bar.full[0]), 0);
+      int s = 0, it = 0;
+      uint32_t phase = 1;  // of the stage before: the first round finds the stages empty
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += clusters) {
+        int tm, tn, k0, k1;
+        place(t % (tms * p.tns), tms, p.tns, tm, tn);
+        range(t, k0, k1);
+        const int ra = tm * kTile + (int)rank * kHalf, rb = tn * kTile + (int)rank * kHalf;
+        for (int q = 0; ok && q < p.passes; ++q) {
+          const int pa = part_a(p.passes, q), pb = part_b(p.passes, q);
+          for (int k = k0; k < k1; ++k) {
+            if (it >= kStages) ok = mbar_wait(&bar.empty[s], phase, p.err, abort);
+            if (!ok) break;
+            if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], 2 * kStageBytes);
+            const uint32_t a = base + s * kStageBytes, b = a + kOperand, f = full0 + 8 * s;
+            if (kAmn) {
+              tma_load2(a, &ta, f, ra, k * kStep, pa);
+              tma_load2(a + kOperand / 2, &ta, f, ra + 64, k * kStep, pa);
+            } else {
+              tma_load2(a, &ta, f, k * kStep, ra, pa);
+            }
+            if (kBmn) {
+              tma_load2(b, &tb, f, rb, p.row_b + k * kStep, pb);
+              tma_load2(b + kOperand / 2, &tb, f, rb + 64, p.row_b + k * kStep, pb);
+            } else {
+              tma_load2(b, &tb, f, k * kStep, p.row_b + rb, pb);
+            }
+            ++it;
+            if (++s == kStages) {
+              s = 0;
+              phase ^= 1;
+            }
+          }
+        }
+      }
+      // Every stage handed on has been read (so its copies have landed and the commits that tell it
+      // have arrived) before the CTA may end; a pair that gave up waits for its copies.
+      const int left = min(it, kStages);
+      for (int i = 0; i < left; ++i) {
+        const int j = it - left + i;
+        if (ok)
+          mbar_wait(&bar.empty[j % kStages], (uint32_t)((j / kStages) & 1), p.err, nullptr);
+        else if (rank == 0)
+          mbar_wait(&bar.full[j % kStages], (uint32_t)((j / kStages) & 1), p.err, nullptr);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ products
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = idesc_bf16_f32(kTile, kTile, kAmn, kBmn);
+      int s = 0, n = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += clusters, ++n) {
+        int k0, k1;
+        range(t, k0, k1);
+        const int buf = n & 1;
+        if (n >= 2) ok = mbar_wait(&bar.tile_empty[buf], (uint32_t)((n / 2 - 1) & 1), p.err, abort);
+        tc_fence_after();
+        const uint32_t d = tmem + buf * kTile;
+        uint32_t acc = 0;
+        for (int k = 0; ok && k < (k1 - k0) * p.passes; ++k) {
+          ok = mbar_wait(&bar.full[s], phase, p.err, abort);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = base + s * kStageBytes, b = a + kOperand;
+#pragma unroll
+          for (int kk = 0; kk < kStep / 16; ++kk) {
+            const uint64_t da = kAmn ? tc::desc_mnmajor(a, kk, kOperand / 2) : tc::desc_kmajor(a, kk);
+            const uint64_t db = kBmn ? tc::desc_mnmajor(b, kk, kOperand / 2) : tc::desc_kmajor(b, kk);
+            mma2(d, da, db, idesc, acc);
+            acc = 1;
+          }
+          commit2(&bar.empty[s]);
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok) commit2(&bar.tile_full[buf]);
+      }
+      // every MMA has ended before tensor memory is given back
+      commit_own(&bar.done);
+      mbar_wait(&bar.done, 0, p.err, nullptr);
+    }
+  } else {
+    // ------------------------------------------------------------------ epilogue
+    const int half = (warp - 2) >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t tcol = tmem + tc::tmem_lane_base(warp) + half * kHalf;
+    const float inv_cap = p.cap > 0.f ? 1.f / p.cap : 0.f;
+    int n = 0;
+    for (int t = first; t < tiles; t += clusters, ++n) {
+      int tm, tn, k0, k1;
+      place(t % (tms * p.tns), tms, p.tns, tm, tn);
+      range(t, k0, k1);
+      const int split = t / (tms * p.tns);
+      const int buf = n & 1;
+      const int row = tm * kTile + (int)rank * kHalf + r;
+      const int col0 = tn * kTile + half * kHalf;
+      // what the row needs, on its way while the product runs
+      int target = -1, out_row = 0;
+      float lse2 = 0.f, g = 1.f;
+      if (MODE != kDw && row < count) {
+        out_row = p.rows[row];
+        if (MODE == kLse || MODE == kDz) {
+          const int64_t tt = p.targets[out_row] - p.v0;
+          target = tt >= 0 && tt < p.cols ? (int)tt : -1;
+        }
+        if (MODE == kDz) {
+          lse2 = p.lse[out_row] * tc::kLog2e;
+          if (p.d_loss) g = p.d_loss[out_row];
+        }
+      }
+      bool ok = mbar_wait(&bar.tile_full[buf], (uint32_t)((n / 2) & 1), p.err, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const bool empty = k1 <= k0;  // nothing was multiplied: the accumulator holds something else
+      RowSum sum;
+#pragma unroll 1
+      for (int c = 0; c < kHalf; c += 32) {
+        __syncwarp();
+        uint32_t v[32];
+        tmem_ld32(tcol + buf * kTile + c, v);
+        tmem_wait_ld();
+        if (c == kHalf - 32) {  // the accumulator is free
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bar.tile_empty[buf]), 0));
+        }
+        const int col = col0 + c;
+        float (&z)[32] = reinterpret_cast<float (&)[32]>(v);
+        if (empty)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) z[i] = 0.f;
+        if constexpr (MODE == kLse) {
+          if (p.cap > 0.f)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = capped(z[i], p.cap, inv_cap);
+          if (target >= col && target < col + 32) {
+            float at = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) at = col + i == target ? z[i] : at;
+            p.at[row] = at;
+          }
+          sum.add(z, p.cols - col);
+        } else if constexpr (MODE == kDz) {
+          if (row >= p.n || col >= p.pitch) continue;
+          // rows without a target and columns behind the last one are zeros
+          const bool live = row < count;
+          float dz[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float zz = z[i], f = g;
+            if (p.cap > 0.f) {
+              const float th = tanhf(zz * inv_cap);
+              zz = p.cap * th;
+              f *= fmaf(-th, th, 1.f);
+            }
+            float q = ex2_approx(fmaf(zz, tc::kLog2e, -lse2));
+            if (col + i == target) q -= 1.f;
+            dz[i] = live && col + i < p.cols ? q * f : 0.f;
+          }
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            if (part > 0 && p.passes == 1) break;
+            __nv_bfloat16* to = p.dz + ((size_t)part * p.n + row) * p.pitch + col;
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              w[i] = pack_bf16x2(dz[2 * i], dz[2 * i + 1]);
+              dz[2 * i] -= __uint_as_float(w[i] << 16);
+              dz[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) store16(to + 2 * i, w[i], w[i + 1], w[i + 2], w[i + 3]);
+          }
+        } else {
+          const int n_cols = p.out_cols - col;
+          if (n_cols <= 0 || row >= (MODE == kDx ? count : p.cols)) continue;
+          if constexpr (MODE == kDx) {
+            // sums of the pieces before, of this split
+            float* acc = p.acc + ((size_t)split * p.n + row) * p.acc_pitch + col;
+            if (p.add) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                if (i >= n_cols) break;
+                const float4 o = *reinterpret_cast<const float4*>(acc + i);
+                z[i] += o.x;
+                z[i + 1] += o.y;
+                z[i + 2] += o.z;
+                z[i + 3] += o.w;
+              }
+            }
+            if (!p.last) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                if (i < n_cols) *reinterpret_cast<float4*>(acc + i) = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
+              continue;
+            }
+          }
+          const size_t at = (size_t)(MODE == kDx ? out_row : p.v0 + row) * p.out_cols + col;
+          if (p.out_fp32) {
+            float* to = reinterpret_cast<float*>(p.out) + at;
+            if (p.out_vec && n_cols >= 32) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (MODE == kDw && p.accumulate) o = *reinterpret_cast<const float4*>(to + i);
+                o.x = fmaf(p.scale, z[i], o.x);
+                o.y = fmaf(p.scale, z[i + 1], o.y);
+                o.z = fmaf(p.scale, z[i + 2], o.z);
+                o.w = fmaf(p.scale, z[i + 3], o.w);
+                *reinterpret_cast<float4*>(to + i) = o;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < n_cols) to[i] = fmaf(p.scale, z[i], MODE == kDw && p.accumulate ? to[i] : 0.f);
+            }
+          } else {
+            __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
+            if (p.out_vec && n_cols >= 32) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+                store16(to + i, pack_bf16x2(p.scale * z[i], p.scale * z[i + 1]),
+                        pack_bf16x2(p.scale * z[i + 2], p.scale * z[i + 3]),
+                        pack_bf16x2(p.scale * z[i + 4], p.scale * z[i + 5]),
+                        pack_bf16x2(p.scale * z[i + 6], p.scale * z[i + 7]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < n_cols) to[i] = __float2bfloat16_rn(p.scale * z[i]);
+            }
+          }
+        }
+      }
+      if (MODE == kLse && row < count && col0 < p.cols)
+        p.part[(size_t)row * p.parts + p.part0 + (col0 / kHalf)] = make_float2(sum.m, sum.s);
+    }
+  }
+  // the pair ends together: neither's shared memory or tensor memory goes while the other may use it
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc2(tmem, 512);
+  cluster_arrive();
+  cluster_wait();
+}
+
+}  // namespace head
+}  // namespace oomb

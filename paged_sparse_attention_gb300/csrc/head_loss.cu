@@ -3,227 +3,473 @@
 //   z = x W^T, z' = c tanh(z / c) with a cap c;  lse_i = log sum_v exp z'_iv;  loss_i = lse_i - z'_i,t
 //   dz = g_i (exp(z' - lse) - [v = t]) (1 - (z'/c)^2);  dx = s dz W;  dW (+)= s dz^T x
 //
-// The simplest form: tiles of the products on the CUDA cores in fp32.
+// The rows that have a target are gathered first (rows without one cost nothing and what they hold
+// is never read).  Forward: one product, whose tiles leave a maximum and a sum of exponentials for
+// every row and 128 columns (head_gemm.cuh), and a join of those.  Backward, piece by piece of the
+// vocabulary: the logits again with dz stored in bf16, then dx += dz W and dw = dz^T x.  A piece is
+// as many columns as keep dz within kDzBytes, so that the sums of dx go through memory a few times
+// only.  W is read in place by the copy engines; fp32, and rows off 16 bytes, in staged pieces.
 #include <climits>
 #include <cmath>
 
-#include "attn_common.cuh"
-#include "sm103_ptx.cuh"
+#include "head_gemm.cuh"
 
 namespace oomb {
+namespace head {
 namespace {
 
-constexpr int kTM = 64, kTN = 64, kTK = 16;
-constexpr int kPieceCols = 2048;
+constexpr int kMaxWidth = 65536;
+// Workspace given to a piece's dz, and to staged parts of W where it cannot be read in place
+// (kStagedOdd: bf16 rows that are on 16 bytes unless the caller's pointer is not).
+constexpr size_t kDzBytes = 256u << 20, kStagedBytes = 256u << 20, kStagedOdd = 32u << 20;
 
-struct HeadArgs {
-  const void* x;
-  const void* w;
-  const int64_t* targets;
-  int n, D, V;
-  float cap, scale;
-  float* loss;
-  const float* lse_in;
-  float* lse;
-  const float* d_loss;
-  void* dx;
-  void* dw;
-  int accumulate;
-  uint32_t* err;
-  float2* part;  // [tiles of V, n] row maximum and sum of a tile
-  float* at;     // [n] logit of the target
-  float* dz;     // [n, piece]
-  float* dxa;    // [n, D] sum over the pieces
-  int v0, cols;  // the piece
-};
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-__device__ __forceinline__ int target_of(const HeadArgs& a, int i) {
-  const int64_t t = a.targets[i];
-  if (t >= a.V) atomicOr(a.err, OOMB_DEVERR_TOKEN);
-  return t < 0 || t >= a.V ? -1 : (int)t;
+// ------------------------------------------------------------------ staging
+// Three bf16 parts of an fp32 value: their sum is the value (24 bits in parts of 8).
+__device__ __forceinline__ void split3(float v, float (&h)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    h[i] = __bfloat162float(__float2bfloat16_rn(v));
+    v -= h[i];
+  }
 }
 
-// acc[i][j] = sum_k fa(row, k) fb(col, k) of a 64 x 64 tile, 4 x 4 a thread
-template <typename FA, typename FB>
-__device__ __forceinline__ void tile_product(FA fa, FB fb, int K, float (&acc)[4][4]) {
-  __shared__ float sa[kTK][kTM + 1], sb[kTK][kTN + 1];
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+// One row of D elements into its bf16 parts, `plane` elements apart, by one warp.
+template <typename T, bool VEC>
+__device__ __forceinline__ void stage_row(const T* in, __nv_bfloat16* out, size_t plane, int D, int lane) {
+  if constexpr (VEC && sizeof(T) == 2) {
+    for (int c = lane * 8; c < D; c += 256)
+      *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(in + c);
+  } else if constexpr (VEC) {
+    for (int c = lane * 8; c < D; c += 256) {
+      const float4 a = *reinterpret_cast<const float4*>(in + c), b = *reinterpret_cast<const float4*>(in + c + 4);
+      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      float h[8][3];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+      for (int e = 0; e < 8; ++e) split3(v[e], h[e]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-  for (int k0 = 0; k0 < K; k0 += kTK) {
-    for (int e = threadIdx.x; e < kTK * kTM; e += 256) {
-      sa[e % kTK][e / kTK] = k0 + e % kTK < K ? fa(e / kTK, k0 + e % kTK) : 0.f;
-      sb[e % kTK][e / kTK] = k0 + e % kTK < K ? fb(e / kTK, k0 + e % kTK) : 0.f;
+      for (int p = 0; p < 3; ++p)
+        *reinterpret_cast<uint4*>(out + p * plane + c) =
+            make_uint4(pack_bf16x2(h[0][p], h[1][p]), pack_bf16x2(h[2][p], h[3][p]), pack_bf16x2(h[4][p], h[5][p]),
+                       pack_bf16x2(h[6][p], h[7][p]));
     }
-    __syncthreads();
+  } else {
+    for (int c = lane; c < D; c += 32) {
+      if constexpr (sizeof(T) == 2) {
+        out[c] = in[c];
+      } else {
+        float h[3];
+        split3(in[c], h);
 #pragma unroll
-    for (int k = 0; k < kTK; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx * 4 + j], acc[i][j]);
-    __syncthreads();
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void logits(const HeadArgs& a, int m0, int v0, float (&z)[4][4]) {
-  const T* x = (const T*)a.x;
-  const T* w = (const T*)a.w;
-  tile_product(
-      [&](int r, int k) { return m0 + r < a.n && a.targets[m0 + r] >= 0 ? to_float<T>(x[(size_t)(m0 + r) * a.D + k]) : 0.f; },
-      [&](int r, int k) { return v0 + r < a.V ? to_float<T>(w[(size_t)(v0 + r) * a.D + k]) : 0.f; }, a.D, z);
-  if (a.cap > 0.f)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) z[i][j] = a.cap * tanhf(z[i][j] / a.cap);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) head_fwd_tile(const HeadArgs a) {
-  const int m0 = blockIdx.x * kTM, v0 = blockIdx.y * kTN;
-  float z[4][4];
-  logits<T>(a, m0, v0, z);
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  for (int i = 0; i < 4; ++i) {
-    const int r = m0 + ty * 4 + i;
-    const int t = r < a.n ? target_of(a, r) : -1;
-    float m = -INFINITY, s = 0.f;
-    for (int j = 0; j < 4; ++j)
-      if (v0 + tx * 4 + j < a.V) m = fmaxf(m, z[i][j]);
-    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int j = 0; j < 4; ++j) {
-      const int v = v0 + tx * 4 + j;
-      if (v < a.V) s += __expf(z[i][j] - m);
-      if (v == t && r < a.n) a.at[r] = z[i][j];
-    }
-    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (tx == 0 && r < a.n) a.part[(size_t)blockIdx.y * a.n + r] = make_float2(m, s);
-  }
-}
-
-__global__ void __launch_bounds__(128) head_fwd_join(const HeadArgs a, int tiles) {
-  const int r = blockIdx.x * blockDim.x + threadIdx.x;
-  if (r >= a.n) return;
-  float m = -INFINITY, s = 0.f;
-  for (int t = 0; t < tiles; ++t) m = fmaxf(m, a.part[(size_t)t * a.n + r].x);
-  for (int t = 0; t < tiles; ++t) {
-    const float2 p = a.part[(size_t)t * a.n + r];
-    s += p.y * __expf(p.x - m);
-  }
-  const bool has = target_of(a, r) >= 0;
-  const float lse = m + logf(s);
-  a.lse[r] = has ? lse : 0.f;
-  a.loss[r] = has ? lse - a.at[r] : 0.f;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) head_dz_tile(const HeadArgs a) {
-  const int m0 = blockIdx.x * kTM, c0 = blockIdx.y * kTN;
-  float z[4][4];
-  logits<T>(a, m0, a.v0 + c0, z);
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  for (int i = 0; i < 4; ++i) {
-    const int r = m0 + ty * 4 + i;
-    if (r >= a.n) continue;
-    const int t = target_of(a, r);
-    for (int j = 0; j < 4; ++j) {
-      const int c = c0 + tx * 4 + j;
-      if (c >= a.cols) continue;
-      float d = 0.f;
-      if (t >= 0) {
-        d = __expf(z[i][j] - a.lse_in[r]) - (a.v0 + c == t ? 1.f : 0.f);
-        if (a.cap > 0.f) d *= 1.f - (z[i][j] / a.cap) * (z[i][j] / a.cap);
-        if (a.d_loss) d *= a.d_loss[r];
+        for (int p = 0; p < 3; ++p) out[p * plane + c] = __float2bfloat16_rn(h[p]);
       }
-      a.dz[(size_t)r * kPieceCols + c] = d;
     }
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) head_dx_tile(const HeadArgs a) {
-  const int m0 = blockIdx.x * kTM, c0 = blockIdx.y * kTN;
-  const T* w = (const T*)a.w;
-  float acc[4][4];
-  tile_product([&](int r, int k) { return m0 + r < a.n ? a.dz[(size_t)(m0 + r) * kPieceCols + k] : 0.f; },
-               [&](int c, int k) { return c0 + c < a.D ? to_float<T>(w[(size_t)(a.v0 + k) * a.D + c0 + c]) : 0.f; }, a.cols,
-               acc);
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int r = m0 + ty * 4 + i, c = c0 + tx * 4 + j;
-      if (r >= a.n || c >= a.D) continue;
-      const float v = (a.v0 ? a.dxa[(size_t)r * a.D + c] : 0.f) + acc[i][j];
-      a.dxa[(size_t)r * a.D + c] = v;
-      if (a.v0 + a.cols == a.V) ((T*)a.dx)[(size_t)r * a.D + c] = from_float<T>(a.scale * v);
-    }
-}
-
-template <typename T, typename TW>
-__global__ void __launch_bounds__(256) head_dw_tile(const HeadArgs a) {
-  const int m0 = blockIdx.x * kTM, c0 = blockIdx.y * kTN;
-  const T* x = (const T*)a.x;
-  float acc[4][4];
-  tile_product([&](int r, int k) { return m0 + r < a.cols ? a.dz[(size_t)k * kPieceCols + m0 + r] : 0.f; },
-               [&](int c, int k) {
-                 return c0 + c < a.D && a.targets[k] >= 0 ? to_float<T>(x[(size_t)k * a.D + c0 + c]) : 0.f;
-               },
-               a.n, acc);
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int r = m0 + ty * 4 + i, c = c0 + tx * 4 + j;
-      if (r >= a.cols || c >= a.D) continue;
-      TW* to = (TW*)a.dw + (size_t)(a.v0 + r) * a.D + c;
-      *to = from_float<TW>(a.accumulate ? to_float<TW>(*to) + a.scale * acc[i][j] : a.scale * acc[i][j]);
-    }
-}
-
-int tiles(int64_t x, int t) { return (int)((x + t - 1) / t); }
-
-template <typename T>
-cudaError_t forward(const HeadArgs& a, cudaStream_t st) {
-  count_launches(2);
-  head_fwd_tile<T><<<dim3(tiles(a.n, kTM), tiles(a.V, kTN)), 256, 0, st>>>(a);
-  head_fwd_join<<<tiles(a.n, 128), 128, 0, st>>>(a, tiles(a.V, kTN));
-  return cudaGetLastError();
-}
-template <typename T>
-cudaError_t backward(HeadArgs a, int dw_dtype, cudaStream_t st) {
-  for (a.v0 = 0; a.v0 < a.V; a.v0 += kPieceCols) {
-    a.cols = std::min(kPieceCols, a.V - a.v0);
-    head_dz_tile<T><<<dim3(tiles(a.n, kTM), tiles(a.cols, kTN)), 256, 0, st>>>(a);
-    count_launches(1);
-    if (a.dx) head_dx_tile<T><<<dim3(tiles(a.n, kTM), tiles(a.D, kTN)), 256, 0, st>>>(a), count_launches(1);
-    if (!a.dw) continue;
-    count_launches(1);
-    const dim3 grid(tiles(a.cols, kTM), tiles(a.D, kTN));
-    if (dw_dtype == OOMB_FP32)
-      head_dw_tile<T, float><<<grid, 256, 0, st>>>(a);
-    else
-      head_dw_tile<T, __nv_bfloat16><<<grid, 256, 0, st>>>(a);
-  }
-  return cudaGetLastError();
-}
-
-struct Space {
-  size_t part, at, dz, dxa, bytes;
+struct GatherArgs {
+  const void* in;         // x [n, D], or W's rows of the piece
+  __nv_bfloat16* out;     // [parts, n, pitch]
+  int n, D, pitch;
+  // x only
+  const int64_t* targets;
+  int V;
+  int* rows;
+  int* count;
+  float* loss;            // forward: written in rows without a target
+  float* lse;
+  void* dx;               // backward: the same
+  uint32_t* err;
 };
-Space space(int64_t n, int D, int V, bool bwd) {
-  Space s = {};
-  s.part = 0;
-  s.at = align_up((size_t)tiles(V, kTN) * n * 8, 256);
-  s.bytes = s.at + align_up((size_t)n * 4, 256);
-  if (bwd) {
-    s.dz = 0;
-    s.dxa = align_up((size_t)n * kPieceCols * 4, 256);
-    s.bytes = std::max(s.bytes, s.dxa + align_up((size_t)n * D * 4, 256));
+
+// Gathers the rows of x that have a target.  A block takes a contiguous range of rows; how many
+// rows before it have a target it counts itself, so that one launch is enough.
+constexpr int kStageThreads = 256;
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kStageThreads) stage_x(const __grid_constant__ GatherArgs a) {
+  __shared__ int warp_sum[kStageThreads / 32], place[kStageThreads];
+  let_next_launch();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int begin = (int)((int64_t)a.n * blockIdx.x / gridDim.x), end = (int)((int64_t)a.n * (blockIdx.x + 1) / gridDim.x);
+  // sum of one flag a thread over the block; `before`: over the threads before
+  auto block_count = [&](int v, int& before) {
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int all = 0, off = 0;
+#pragma unroll
+    for (int w = 0; w < kStageThreads / 32; ++w) {
+      if (w < warp) off += warp_sum[w];
+      all += warp_sum[w];
+    }
+    before = off + inc - v;
+    return all;
+  };
+  int mine = 0, unused;
+  for (int i = threadIdx.x; i < begin; i += kStageThreads) {
+    const int64_t t = a.targets[i];
+    mine += t >= 0 && t < a.V;
   }
-  return s;
+  int at = block_count(mine, unused);
+  const size_t plane = (size_t)a.n * a.pitch;
+  for (int i0 = begin; i0 < end; i0 += kStageThreads) {
+    const int i = i0 + threadIdx.x;
+    const int64_t t = i < end ? a.targets[i] : -1;
+    if (t >= a.V) atomicOr(a.err, OOMB_DEVERR_TOKEN);
+    const int has = t >= 0 && t < a.V;
+    int before;
+    const int all = block_count(has, before);
+    place[threadIdx.x] = has ? at + before : -1;
+    if (has) a.rows[at + before] = i;
+    if (i < end && !has && a.loss) a.loss[i] = a.lse[i] = 0.f;
+    __syncthreads();
+    for (int j = warp; j < min(kStageThreads, end - i0); j += kStageThreads / 32) {
+      const int to = place[j];
+      if (to >= 0) {
+        stage_row<T, VEC>(reinterpret_cast<const T*>(a.in) + (size_t)(i0 + j) * a.D, a.out + (size_t)to * a.pitch, plane,
+                          a.D, lane);
+      } else if (a.dx) {
+        T* d = reinterpret_cast<T*>(a.dx) + (size_t)(i0 + j) * a.D;
+        for (int c = lane; c < a.D; c += 32) d[c] = from_float<T>(0.f);
+      }
+    }
+    at += all;
+  }
+  if (blockIdx.x == gridDim.x - 1) {
+    if (threadIdx.x == 0) *a.count = at;
+    // rows up to the next step of K are read by the product over rows
+    const int tail = min(a.n, (at + kStep - 1) / kStep * kStep);
+    for (int r = at + warp; r < tail; r += kStageThreads / 32)
+      for (int p = 0; p < (sizeof(T) == 2 ? 1 : 3); ++p)
+        for (int c = lane; c < a.D; c += 32) a.out[p * plane + (size_t)r * a.pitch + c] = __float2bfloat16_rn(0.f);
+  }
+}
+
+// Rows of W that are not read in place.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) stage_w(const __grid_constant__ GatherArgs a) {
+  wait_for_launch_before();
+  let_next_launch();
+  const int warps = gridDim.x * 8;
+  for (int r = blockIdx.x * 8 + threadIdx.x / 32; r < a.n; r += warps)
+    stage_row<T, VEC>(reinterpret_cast<const T*>(a.in) + (size_t)r * a.D, a.out + (size_t)r * a.pitch,
+                      (size_t)a.n * a.pitch, a.D, threadIdx.x % 32);
+}
+
+// ------------------------------------------------------------------ joins
+// Log-sum-exp of a row from its columns' parts, a warp a row.
+__global__ void __launch_bounds__(256) join_lse(const __grid_constant__ GemmArgs a, float* loss, float* lse) {
+  wait_for_launch_before();
+  let_next_launch();
+  const int count = *a.count, lane = threadIdx.x % 32;
+  for (int r = blockIdx.x * 8 + threadIdx.x / 32; r < count; r += gridDim.x * 8) {
+    const float2* part = a.part + (size_t)r * a.parts;
+    float m = -INFINITY, s = 0.f;
+#pragma unroll 4
+    for (int i = lane; i < a.parts; i += 32) {
+      const float2 p = part[i];
+      const float to = fmaxf(m, p.x), ref = to == -INFINITY ? 0.f : to;
+      s = s * ex2_approx(m - ref) + p.y * ex2_approx(p.x - ref);
+      m = to;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+      const float to = fmaxf(m, m2), ref = to == -INFINITY ? 0.f : to;
+      // the same order in both lanes of a pair: every lane gets the same bits
+      const float lo = s * ex2_approx(m - ref), hi = s2 * ex2_approx(m2 - ref);
+      s = lo + hi;
+      m = to;
+    }
+    if (lane == 0) {
+      const float l = (m + log2f(s)) * tc::kLn2;
+      const int row = a.rows[r];
+      lse[row] = l;
+      loss[row] = l - a.at[r];
+    }
+  }
+}
+
+// dx of few rows: its splits' sums, added in order.
+template <typename T>
+__global__ void __launch_bounds__(256) join_dx(const __grid_constant__ GemmArgs a) {
+  wait_for_launch_before();
+  let_next_launch();
+  const int count = *a.count;
+  const int64_t total = (int64_t)count * a.out_cols;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int r = (int)(i / a.out_cols), c = (int)(i % a.out_cols);
+    float v = 0.f;
+    for (int s = 0; s < a.splits; ++s) v += a.acc[((size_t)s * a.n + r) * a.acc_pitch + c];
+    reinterpret_cast<T*>(a.out)[(size_t)a.rows[r] * a.out_cols + c] = from_float<T>(a.scale * v);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+int tiles(int64_t x, int t) { return (int)((x + t - 1) / t); }
+int clusters() { return std::max(1, device_sm_count() / 2); }
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Parts that the product of few rows with W is cut into along the vocabulary.
+int dx_splits(int64_t n, int D) { return std::max(1, std::min(16, clusters() / (tiles(n, kTile) * tiles(D, kTile)))); }
+
+// Where things lie in the workspace, and the pieces of the vocabulary.
+struct Plan {
+  int parts_of, pitch_d;       // bf16 parts of an operand, elements of a staged row
+  bool staged;                 // W is read through the workspace
+  int piece;                   // columns of a piece (the last may have fewer)
+  int pitch_z, splits, row_parts;
+  size_t count, rows, at, x, w, part, dz, acc, bytes;
+};
+Plan make_plan(int64_t n, int D, int V, int dtype, bool backward, bool w_on16) {
+  Plan p = {};
+  p.parts_of = dtype == OOMB_FP32 ? 3 : 1;
+  p.pitch_d = (int)align_up((size_t)D, 8);
+  const bool never_in_place = dtype == OOMB_FP32 || D % 8 != 0;
+  p.staged = never_in_place || !w_on16;
+  const size_t row_bytes = (size_t)p.parts_of * p.pitch_d * 2;
+  const int64_t v256 = (int64_t)align_up((size_t)V, kTile);
+  // the pieces' sizes are multiples of a tile, about equal
+  int64_t most = v256;
+  const int64_t staged_rows = std::min<int64_t>(
+      v256, std::max<int64_t>(kTile, (int64_t)((never_in_place ? kStagedBytes : kStagedOdd) / row_bytes) / kTile * kTile));
+  if (p.staged) most = staged_rows;
+  const size_t z_bytes = (size_t)p.parts_of * n * 2;  // of a column of dz
+  if (backward) most = std::min<int64_t>(most, std::max<int64_t>(kTile, (int64_t)(kDzBytes / z_bytes) / kTile * kTile));
+  const int64_t pieces = (V + most - 1) / most;
+  p.piece = (int)std::min<int64_t>(V, (int64_t)align_up((size_t)((V + pieces - 1) / pieces), kTile));
+  p.pitch_z = (int)align_up((size_t)p.piece, 64);
+  p.splits = dx_splits(n, D);
+  p.row_parts = tiles(V, kHalf);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align_up(bytes, 256);
+    return here;
+  };
+  p.count = take(4);
+  p.rows = take((size_t)n * 4);
+  p.at = take((size_t)n * 4);
+  p.x = take((size_t)n * row_bytes);
+  p.w = take((size_t)staged_rows * row_bytes);  // the same for every n
+  const size_t common = at;
+  p.part = take((size_t)n * p.row_parts * 8);
+  const size_t forward_bytes = at;
+  at = common;
+  // room that grows with n although a piece of more rows has fewer columns
+  p.dz = take(std::min<size_t>(z_bytes * align_up((size_t)V, 64), std::max<size_t>(kDzBytes, z_bytes * kTile)));
+  size_t acc_rows = (size_t)n;
+  for (int64_t m = kTile; m <= n && m <= (int64_t)kTile * clusters(); m += kTile)
+    acc_rows = std::max(acc_rows, (size_t)m * dx_splits(m, D));
+  acc_rows = std::max(acc_rows, (size_t)n * p.splits);
+  p.acc = take(acc_rows * align_up((size_t)D, 4) * 4);
+  p.bytes = backward ? std::max(forward_bytes, at) : forward_bytes;
+  return p;
+}
+
+// Map of a [planes, rows, cols] bf16 array with rows of `pitch` elements, boxes of 64 columns.
+bool make_map(CUtensorMap* m, const void* base, uint64_t planes, uint64_t rows, uint64_t cols, uint64_t pitch, int box) {
+  auto enc = tc::tmap_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {cols, rows, planes};
+  cuuint64_t strides[2] = {pitch * 2, (planes > 1 ? rows : 1) * pitch * 2};
+  cuuint32_t boxes[3] = {64, (cuuint32_t)box, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, boxes, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename K, typename... A>
+cudaError_t launch_after(K kernel, unsigned grid, unsigned threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;  // a dependent launch: its set-up overlaps the end of the one before
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int MODE>
+cudaError_t gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& p, int64_t most_tiles, cudaStream_t st) {
+  static size_t set[kMaxDevices] = {};
+  const cudaError_t e = set_smem_limit((const void*)head_gemm<MODE>, kSmem, set);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = 2 * (unsigned)std::min<int64_t>(clusters(), most_tiles);
+  return launch_after(head_gemm<MODE>, grid, (unsigned)kThreads, kSmem, st, a, b, p);
+}
+
+// What both directions share: the rows with a target, gathered.
+template <typename T>
+cudaError_t gather(const void* x, const GatherArgs& s, cudaStream_t st) {
+  const unsigned grid = (unsigned)std::min(s.n, 2 * device_sm_count());
+  count_launches(1);
+  if (s.D % 8 == 0 && on16(x))
+    stage_x<T, true><<<grid, kStageThreads, 0, st>>>(s);
+  else
+    stage_x<T, false><<<grid, kStageThreads, 0, st>>>(s);
+  return cudaGetLastError();
+}
+
+// The map of the piece's rows of W, in place or staged here; row_b: where the piece starts in it.
+template <typename T>
+cudaError_t weights(const void* w, const Plan& pl, char* ws, int D, int V, int v0, int cols, CUtensorMap* m128,
+                    CUtensorMap* m64, int* row_b, cudaStream_t st) {
+  const void* base = w;
+  uint64_t rows = V, planes = 1, pitch = D;
+  *row_b = v0;
+  if (pl.staged) {
+    GatherArgs s = {};
+    s.in = reinterpret_cast<const T*>(w) + (size_t)v0 * D;
+    s.out = reinterpret_cast<__nv_bfloat16*>(ws + pl.w);
+    s.n = cols;
+    s.D = D;
+    s.pitch = pl.pitch_d;
+    const unsigned grid = (unsigned)std::min(tiles(cols, 8), 8 * device_sm_count());
+    const cudaError_t e = D % 8 == 0 && on16(s.in) ? launch_after(stage_w<T, true>, grid, 256u, 0, st, s)
+                                                   : launch_after(stage_w<T, false>, grid, 256u, 0, st, s);
+    if (e != cudaSuccess) return e;
+    base = s.out;
+    rows = cols;
+    planes = pl.parts_of;
+    pitch = pl.pitch_d;
+    *row_b = 0;
+  }
+  if (!make_map(m128, base, planes, rows, D, pitch, kHalf)) return cudaErrorInvalidValue;
+  if (m64 && !make_map(m64, base, planes, rows, D, pitch, kStep)) return cudaErrorInvalidValue;
+  return cudaSuccess;
+}
+
+template <typename T>
+cudaError_t forward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, char* ws, int V, float* loss, float* lse,
+                    cudaStream_t st) {
+  cudaError_t e = gather<T>(s.in, s, st);
+  if (e != cudaSuccess) return e;
+  CUtensorMap mx, mw;
+  if (!make_map(&mx, s.out, pl.parts_of, s.n, s.D, s.pitch, kHalf)) return cudaErrorInvalidValue;
+  g.steps = tiles(s.D, kStep);
+  for (int v0 = 0; v0 < V; v0 += pl.piece) {
+    g.v0 = v0;
+    g.cols = std::min(pl.piece, V - v0);
+    e = weights<T>(w, pl, ws, s.D, V, v0, g.cols, &mw, nullptr, &g.row_b, st);
+    if (e != cudaSuccess) return e;
+    g.tns = tiles(g.cols, kTile);
+    g.part0 = v0 / kHalf;
+    e = gemm<kLse>(mx, mw, g, (int64_t)tiles(s.n, kTile) * g.tns, st);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_after(join_lse, (unsigned)std::min(tiles(s.n, 8), 8 * device_sm_count()), 256u, 0, st, g, loss, lse);
+}
+
+template <typename T>
+cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, char* ws, int V, void* dx, void* dw,
+                     int dw_dtype, int accumulate, cudaStream_t st) {
+  cudaError_t e = gather<T>(s.in, s, st);
+  if (e != cudaSuccess) return e;
+  const int D = s.D;
+  CUtensorMap mx, mx64, mw, mw64, mz, mz64;
+  if (!make_map(&mx, s.out, pl.parts_of, s.n, D, s.pitch, kHalf) ||
+      !make_map(&mx64, s.out, pl.parts_of, s.n, D, s.pitch, kStep))
+    return cudaErrorInvalidValue;
+  const int tms = tiles(s.n, kTile), tds = tiles(D, kTile);
+  g.pitch = pl.pitch_z;
+  GemmArgs gx = g, gw = g;
+  for (int v0 = 0; v0 < V; v0 += pl.piece) {
+    const int cols = std::min(pl.piece, V - v0);
+    int row_b;
+    e = weights<T>(w, pl, ws, D, V, v0, cols, &mw, &mw64, &row_b, st);
+    if (e != cudaSuccess) return e;
+    if (!make_map(&mz, g.dz, pl.parts_of, s.n, cols, g.pitch, kHalf) ||
+        !make_map(&mz64, g.dz, pl.parts_of, s.n, cols, g.pitch, kStep))
+      return cudaErrorInvalidValue;
+    for (GemmArgs* a : {&g, &gx, &gw}) {
+      a->v0 = v0;
+      a->cols = cols;
+    }
+    g.steps = tiles(D, kStep);
+    g.row_b = row_b;
+    g.tns = tiles(cols, kTile);
+    e = gemm<kDz>(mx, mw, g, (int64_t)tms * g.tns, st);
+    if (e != cudaSuccess) return e;
+    if (dx) {
+      const bool last = v0 + cols == V;
+      gx.steps = tiles(cols, kStep);
+      gx.splits = std::min(pl.splits, gx.steps);
+      gx.row_b = row_b;
+      gx.tns = tds;
+      gx.add = v0 > 0;
+      gx.last = last && pl.splits == 1;
+      gx.out = dx;
+      gx.out_cols = D;
+      gx.out_fp32 = sizeof(T) == 4;
+      gx.out_vec = D % (16 / (int)sizeof(T)) == 0 && on16(dx);
+      e = gemm<kDx>(mz, mw64, gx, (int64_t)tms * tds * gx.splits, st);
+      if (e != cudaSuccess) return e;
+      if (last && pl.splits > 1) {
+        gx.splits = std::min(pl.splits, tiles(pl.piece, kStep));  // of the first piece: no other has more
+        e = launch_after(join_dx<T>, (unsigned)std::min<int64_t>(((int64_t)s.n * D + 255) / 256, 8 * device_sm_count()),
+                         256u, 0, st, gx);
+        if (e != cudaSuccess) return e;
+      }
+    }
+    if (dw) {
+      gw.tms = tiles(cols, kTile);
+      gw.tns = tds;
+      gw.out = dw;
+      gw.out_cols = D;
+      gw.out_fp32 = dw_dtype == OOMB_FP32;
+      gw.out_vec = D % (16 / (int)dtype_size(dw_dtype)) == 0 && on16(dw);
+      gw.accumulate = accumulate;
+      e = gemm<kDw>(mz64, mx64, gw, (int64_t)gw.tms * tds, st);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+GemmArgs arguments(const void* x, const int64_t* targets, int n, int D, int V, int dtype, float cap, const Plan& pl,
+                   char* ws, uint32_t* err, GatherArgs* s) {
+  *s = {};
+  s->in = x;
+  s->out = reinterpret_cast<__nv_bfloat16*>(ws + pl.x);
+  s->n = n;
+  s->D = D;
+  s->pitch = pl.pitch_d;
+  s->targets = targets;
+  s->V = V;
+  s->rows = reinterpret_cast<int*>(ws + pl.rows);
+  s->count = reinterpret_cast<int*>(ws + pl.count);
+  s->err = err;
+  GemmArgs g = {};
+  g.count = s->count;
+  g.rows = s->rows;
+  g.n = n;
+  g.splits = 1;
+  g.passes = pl.parts_of == 1 ? 1 : 6;
+  g.targets = targets;
+  g.cap = cap;
+  g.part = reinterpret_cast<float2*>(ws + pl.part);
+  g.parts = pl.row_parts;
+  g.at = reinterpret_cast<float*>(ws + pl.at);
+  g.dz = reinterpret_cast<__nv_bfloat16*>(ws + pl.dz);
+  g.acc = reinterpret_cast<float*>(ws + pl.acc);
+  g.acc_pitch = (int)align_up((size_t)D, 4);
+  g.err = err;
+  return g;
 }
 
 oomb_status check(const void* x, const void* w, const int64_t* targets, int n, int D, int V, int dtype, float cap,
@@ -231,7 +477,7 @@ oomb_status check(const void* x, const void* w, const int64_t* targets, int n, i
   if (!x || !w || !targets || !lse || !word || n <= 0 || D <= 0 || V <= 0 || V > INT_MAX - 1024) return OOMB_ERR_ARG;
   if (!(cap >= 0.f) || cap > 1e30f || (cap > 0.f && cap < 1e-30f)) return OOMB_ERR_ARG;
   if (dtype != OOMB_BF16 && dtype != OOMB_FP32) return OOMB_ERR_DTYPE;
-  if (D > 65536) return OOMB_ERR_UNSUPPORTED;
+  if (D > kMaxWidth) return OOMB_ERR_UNSUPPORTED;
   const uintptr_t es = dtype_size(dtype);
   if (reinterpret_cast<uintptr_t>(x) % es || reinterpret_cast<uintptr_t>(w) % es ||
       reinterpret_cast<uintptr_t>(targets) % 8 || reinterpret_cast<uintptr_t>(lse) % 4 ||
@@ -241,15 +487,17 @@ oomb_status check(const void* x, const void* w, const int64_t* targets, int n, i
 }
 
 }  // namespace
+}  // namespace head
 }  // namespace oomb
 
 using namespace oomb;
+using namespace oomb::head;
 
 extern "C" {
 
 size_t oomb_head_loss_workspace(int n, int D, int V, int dtype, int backward) {
-  if (n <= 0 || D <= 0 || D > 65536 || V <= 0 || V > INT_MAX - 1024 || (dtype != OOMB_BF16 && dtype != OOMB_FP32)) return 0;
-  return space(n, D, V, backward != 0).bytes;
+  if (n <= 0 || D <= 0 || D > kMaxWidth || V <= 0 || V > INT_MAX - 1024 || (dtype != OOMB_BF16 && dtype != OOMB_FP32)) return 0;
+  return make_plan(n, D, V, dtype, backward != 0, true).bytes;
 }
 
 oomb_status oomb_head_loss_fwd(const void* x, const void* w, const int64_t* targets, int n, int D, int V, int dtype,
@@ -259,23 +507,16 @@ oomb_status oomb_head_loss_fwd(const void* x, const void* w, const int64_t* targ
   if (s != OOMB_OK) return s;
   if (!loss) return OOMB_ERR_ARG;
   if (reinterpret_cast<uintptr_t>(loss) % 4) return OOMB_ERR_ALIGN;
-  const Space p = space(n, D, V, false);
-  if (!workspace || ws_bytes < p.bytes) return OOMB_ERR_WORKSPACE;
-  HeadArgs a = {};
-  a.x = x;
-  a.w = w;
-  a.targets = targets;
-  a.n = n;
-  a.D = D;
-  a.V = V;
-  a.cap = softcap;
-  a.loss = loss;
-  a.lse = lse;
-  a.err = error_word;
-  a.part = reinterpret_cast<float2*>((char*)workspace + p.part);
-  a.at = reinterpret_cast<float*>((char*)workspace + p.at);
-  cudaStream_t st = (cudaStream_t)stream;
-  return cuda_status(dtype == OOMB_FP32 ? forward<float>(a, st) : forward<__nv_bfloat16>(a, st));
+  const Plan pl = make_plan(n, D, V, dtype, false, on16(w));
+  if (!workspace || ws_bytes < pl.bytes) return OOMB_ERR_WORKSPACE;
+  char* ws = reinterpret_cast<char*>(workspace);
+  GatherArgs st;
+  GemmArgs g = arguments(x, targets, n, D, V, dtype, softcap, pl, ws, error_word, &st);
+  st.loss = loss;
+  st.lse = lse;
+  cudaStream_t on = (cudaStream_t)stream;
+  return cuda_status(dtype == OOMB_FP32 ? forward<float>(g, st, w, pl, ws, V, loss, lse, on)
+                                        : forward<__nv_bfloat16>(g, st, w, pl, ws, V, loss, lse, on));
 }
 
 oomb_status oomb_head_loss_bwd(const void* x, const void* w, const int64_t* targets, const float* lse,
@@ -290,28 +531,18 @@ oomb_status oomb_head_loss_bwd(const void* x, const void* w, const int64_t* targ
   if (reinterpret_cast<uintptr_t>(dx) % dtype_size(dtype) || reinterpret_cast<uintptr_t>(d_loss) % 4 ||
       (dw && reinterpret_cast<uintptr_t>(dw) % dtype_size(dw_dtype)))
     return OOMB_ERR_ALIGN;
-  const Space p = space(n, D, V, true);
-  if (!workspace || ws_bytes < p.bytes) return OOMB_ERR_WORKSPACE;
-  HeadArgs a = {};
-  a.x = x;
-  a.w = w;
-  a.targets = targets;
-  a.n = n;
-  a.D = D;
-  a.V = V;
-  a.cap = softcap;
-  a.scale = scale;
-  a.lse_in = lse;
-  a.d_loss = d_loss;
-  a.dx = dx;
-  a.dw = dw;
-  a.accumulate = accumulate != 0;
-  a.err = error_word;
-  a.dz = reinterpret_cast<float*>((char*)workspace + p.dz);
-  a.dxa = reinterpret_cast<float*>((char*)workspace + p.dxa);
-  cudaStream_t st = (cudaStream_t)stream;
-  return cuda_status(dtype == OOMB_FP32 ? backward<float>(a, dw_dtype, st)
-                                        : backward<__nv_bfloat16>(a, dw_dtype, st));
+  const Plan pl = make_plan(n, D, V, dtype, true, on16(w));
+  if (!workspace || ws_bytes < pl.bytes) return OOMB_ERR_WORKSPACE;
+  char* ws = reinterpret_cast<char*>(workspace);
+  GatherArgs st;
+  GemmArgs g = arguments(x, targets, n, D, V, dtype, softcap, pl, ws, error_word, &st);
+  st.dx = dx;
+  g.lse = lse;
+  g.d_loss = d_loss;
+  g.scale = scale;
+  cudaStream_t on = (cudaStream_t)stream;
+  return cuda_status(dtype == OOMB_FP32 ? backward<float>(g, st, w, pl, ws, V, dx, dw, dw_dtype, accumulate, on)
+                                        : backward<__nv_bfloat16>(g, st, w, pl, ws, V, dx, dw, dw_dtype, accumulate, on));
 }
 
 oomb_status oomb_word_check(uint32_t* error_word, void* stream, uint32_t* bits_out) {
