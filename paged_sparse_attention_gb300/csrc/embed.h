@@ -3,9 +3,11 @@
 #include <cstddef>
 #include <cstdint>
 
+#include <vector_types.h>
+
 namespace oomb {
 
-constexpr int kTileRows = 16;  // sorted rows whose pieces one block sums
+constexpr int kTileRows = 4;  // sorted rows whose pieces one block sums
 
 struct EmbedArgs {
   const int64_t* tokens;  // [n]
@@ -19,11 +21,14 @@ struct EmbedArgs {
   int accumulate;
   float scale;
   uint32_t* err;
+  int section;            // keys ranked against each other
   int* order;             // [n] rows, by token and then by row
   int* sorted;            // [n] their tokens
   int* sec_order;         // the same, each section by itself
   int* sec_sorted;
-  float* part;            // sums of the pieces of long runs
+  int* n_long;            // tokens whose rows lie in several windows
+  int2* long_runs;        // each: the token and its last window
+  float* part;            // sums of their pieces
   int64_t pitch;
 };
 

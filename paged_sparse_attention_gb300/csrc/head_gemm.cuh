@@ -94,32 +94,39 @@ __device__ __forceinline__ void store16(void* p, uint32_t a, uint32_t b, uint32_
   *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);
 }
 
-// z' and 1 - (z'/cap)^2 of a capped logit
-__device__ __forceinline__ float capped(float z, float cap, float inv_cap) { return cap * tanhf(z * inv_cap); }
+// tanh(u) from one exponential and one reciprocal, known to 2^-23 or so of one (not of itself: a
+// logit's own error is larger, it is a sum of products up to that size).
+__device__ __forceinline__ float tanh_fast(float u) {
+  return fmaf(-2.f, rcp_approx(1.f + ex2_approx(u * (2.f * tc::kLog2e))), 1.f);
+}
 
-// ---- epilogues: 32 columns of a thread's row; c is the first one within the tile's columns
+// Maximum and sum of exponentials of a row's columns, base 2.
 struct RowSum {
-  float m = -INFINITY, s = 0.f;  // base 2
-  // n: columns that exist (all: 32)
+  float m = -INFINITY, s = 0.f;
+  // n: how many of the 32 columns exist
   __device__ __forceinline__ void add(float (&z)[32], int n) {
     if (n <= 0) return;
     float mx = m;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      z[i] *= tc::kLog2e;
-      if (i < n) mx = fmaxf(mx, z[i]);
+      z[i] = i < n ? z[i] * tc::kLog2e : -INFINITY;
+      mx = fmaxf(mx, z[i]);
     }
     const float to = mx == -INFINITY ? 0.f : mx;  // nothing above -infinity yet (a NaN is no maximum, but stays one)
     s *= ex2_approx(m - to);
     m = mx;
     float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) t[i & 3] += i < n ? ex2_approx(z[i] - to) : 0.f;
+    for (int i = 0; i < 32; ++i) t[i & 3] += ex2_approx(z[i] - to);
     s += (t[0] + t[1]) + (t[2] + t[3]);
   }
 };
 
-template <int MODE>
+// CHUNKED: K is cut in pieces of p.chunk steps whose sums are added in fp32 in registers.  The tensor
+// cores cut a partial sum's last bits instead of rounding them, so a sum of K products loses up to
+// K / 16 halves of a unit in its last place, always towards zero: 6e-6 of a logit over K = 3584,
+// which a loss in fp32 would show, and 4e-7 over 256.  Not for sums that are rounded to bf16 anyway.
+template <int MODE, bool CHUNKED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     head_gemm(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
               const __grid_constant__ GemmArgs p) {
@@ -183,9 +190,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         place(t % (tms * p.tns), tms, p.tns, tm, tn);
         range(t, k0, k1);
         const int ra = tm * kTile + (int)rank * kHalf, rb = tn * kTile + (int)rank * kHalf;
+        const int chunk = CHUNKED ? p.chunk : max(1, k1 - k0);
+        for (int c0 = k0; ok && c0 < k1; c0 += chunk)
         for (int q = 0; ok && q < p.passes; ++q) {
-          const int pa = part_a(p.passes, q), pb = part_b(p.passes, q);
-          for (int k = k0; k < k1; ++k) {
+          const int pa = part_a(p.passes, q), pb = part_b(p.passes, q), c1 = min(k1, c0 + chunk);
+          for (int k = c0; k < c1; ++k) {
             if (it >= kStages) ok = mbar_wait(&bar.empty[s], phase, p.err, abort);
             if (!ok) break;
             if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], 2 * kStageBytes);
@@ -228,15 +237,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int s = 0, n = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = first; ok && t < tiles; t += clusters, ++n) {
+      for (int t = first; ok && t < tiles; t += clusters) {
         int k0, k1;
         range(t, k0, k1);
-        const int buf = n & 1;
+        const int chunk = CHUNKED ? p.chunk : max(1, k1 - k0);
+        int c0 = k0;
+        do {  // one turn without products where K is empty
+        const int buf = n & 1, len = min(k1, c0 + chunk) - c0;
         if (n >= 2) ok = mbar_wait(&bar.tile_empty[buf], (uint32_t)((n / 2 - 1) & 1), p.err, abort);
         tc_fence_after();
         const uint32_t d = tmem + buf * kTile;
         uint32_t acc = 0;
-        for (int k = 0; ok && k < (k1 - k0) * p.passes; ++k) {
+        for (int k = 0; ok && k < len * p.passes; ++k) {
           ok = mbar_wait(&bar.full[s], phase, p.err, abort);
           if (!ok) break;
           tc_fence_after();
@@ -255,6 +267,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if (ok) commit2(&bar.tile_full[buf]);
+        ++n;
+        c0 += chunk;
+        } while (ok && c0 < k1);
       }
       // every MMA has ended before tensor memory is given back
       commit_own(&bar.done);
@@ -265,13 +280,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int half = (warp - 2) >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t tcol = tmem + tc::tmem_lane_base(warp) + half * kHalf;
     const float inv_cap = p.cap > 0.f ? 1.f / p.cap : 0.f;
-    int n = 0;
-    for (int t = first; t < tiles; t += clusters, ++n) {
+    int n = 0;  // accumulators read
+    bool ok = true;
+    for (int t = first; t < tiles; t += clusters) {
       int tm, tn, k0, k1;
       place(t % (tms * p.tns), tms, p.tns, tm, tn);
       range(t, k0, k1);
       const int split = t / (tms * p.tns);
-      const int buf = n & 1;
       const int row = tm * kTile + (int)rank * kHalf + r;
       const int col0 = tn * kTile + half * kHalf;
       // what the row needs, on its way while the product runs
@@ -288,73 +303,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (p.d_loss) g = p.d_loss[out_row];
         }
       }
-      bool ok = mbar_wait(&bar.tile_full[buf], (uint32_t)((n / 2) & 1), p.err, abort);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const bool empty = k1 <= k0;  // nothing was multiplied: the accumulator holds something else
       RowSum sum;
-#pragma unroll 1
-      for (int c = 0; c < kHalf; c += 32) {
-        __syncwarp();
-        uint32_t v[32];
-        tmem_ld32(tcol + buf * kTile + c, v);
-        tmem_wait_ld();
-        if (c == kHalf - 32) {  // the accumulator is free
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bar.tile_empty[buf]), 0));
-        }
-        const int col = col0 + c;
-        float (&z)[32] = reinterpret_cast<float (&)[32]>(v);
-        if (empty)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) z[i] = 0.f;
+
+      // what becomes of 32 columns of the row, from col on
+      auto finish = [&](float (&z)[32], int col) {
         if constexpr (MODE == kLse) {
           if (p.cap > 0.f)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] = capped(z[i], p.cap, inv_cap);
-          if (target >= col && target < col + 32) {
-            float at = 0.f;
+            for (int i = 0; i < 32; ++i) z[i] = p.cap * tanh_fast(z[i] * inv_cap);
+          // the target's logit is known better (stage_x) and joins the sum there
+          if (target >= col && target < col + 32)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) at = col + i == target ? z[i] : at;
-            p.at[row] = at;
-          }
+            for (int i = 0; i < 32; ++i)
+              if (col + i == target) z[i] = -INFINITY;
           sum.add(z, p.cols - col);
         } else if constexpr (MODE == kDz) {
-          if (row >= p.n || col >= p.pitch) continue;
+          if (row >= p.n || col >= p.pitch) return;
           // rows without a target and columns behind the last one are zeros
           const bool live = row < count;
-          float dz[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            float zz = z[i], f = g;
+            float f = g;
             if (p.cap > 0.f) {
-              const float th = tanhf(zz * inv_cap);
-              zz = p.cap * th;
+              const float th = tanh_fast(z[i] * inv_cap);
+              z[i] = p.cap * th;
               f *= fmaf(-th, th, 1.f);
             }
-            float q = ex2_approx(fmaf(zz, tc::kLog2e, -lse2));
+            float q = ex2_approx(fmaf(z[i], tc::kLog2e, -lse2));
             if (col + i == target) q -= 1.f;
-            dz[i] = live && col + i < p.cols ? q * f : 0.f;
+            z[i] = live && col + i < p.cols ? q * f : 0.f;
           }
 #pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            if (part > 0 && p.passes == 1) break;
+          for (int part = 0; part < (CHUNKED ? 3 : 1); ++part) {
             __nv_bfloat16* to = p.dz + ((size_t)part * p.n + row) * p.pitch + col;
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              w[i] = pack_bf16x2(dz[2 * i], dz[2 * i + 1]);
-              dz[2 * i] -= __uint_as_float(w[i] << 16);
-              dz[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+              w[i] = pack_bf16x2(z[2 * i], z[2 * i + 1]);
+              z[2 * i] -= __uint_as_float(w[i] << 16);
+              z[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
             }
 #pragma unroll
             for (int i = 0; i < 16; i += 4) store16(to + 2 * i, w[i], w[i + 1], w[i + 2], w[i + 3]);
           }
         } else {
           const int n_cols = p.out_cols - col;
-          if (n_cols <= 0 || row >= (MODE == kDx ? count : p.cols)) continue;
+          if (n_cols <= 0 || row >= (MODE == kDx ? count : p.cols)) return;
           if constexpr (MODE == kDx) {
             // sums of the pieces before, of this split
             float* acc = p.acc + ((size_t)split * p.n + row) * p.acc_pitch + col;
@@ -373,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
                 if (i < n_cols) *reinterpret_cast<float4*>(acc + i) = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
-              continue;
+              return;
             }
           }
           const size_t at = (size_t)(MODE == kDx ? out_row : p.v0 + row) * p.out_cols + col;
@@ -411,7 +405,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
+      };
+
+      // waits for the next accumulator; 32 columns of it; gives it back
+      auto next = [&]() {
+        ok = mbar_wait(&bar.tile_full[n & 1], (uint32_t)((n / 2) & 1), p.err, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) tc_fence_after();
+        return ok;
+      };
+      auto load = [&](uint32_t (&v)[32], int c) {
+        tmem_ld32(tcol + (n & 1) * kTile + c, v);
+        tmem_wait_ld();
+      };
+      auto give_back = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bar.tile_empty[n & 1]), 0));
+        ++n;
+      };
+      const bool nothing = k1 <= k0;  // no products: the accumulator holds something else
+      if constexpr (CHUNKED) {
+        float run[kHalf / 32][32];
+#pragma unroll
+        for (int c = 0; c < kHalf; ++c) run[c / 32][c % 32] = 0.f;
+        int c0 = k0;
+        do {
+          if (!next()) break;
+          if (!nothing)
+#pragma unroll
+            for (int c = 0; c < kHalf; c += 16) {
+              uint32_t v[16];
+              tmem_ld16(tcol + (n & 1) * kTile + c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) run[c / 32][c % 32 + i] += __uint_as_float(v[i]);
+            }
+          give_back();
+          c0 += p.chunk;
+        } while (c0 < k1);
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < kHalf / 32; ++c) finish(run[c], col0 + 32 * c);
+      } else {
+        if (!next()) break;
+#pragma unroll 1
+        for (int c = 0; c < kHalf; c += 32) {
+          __syncwarp();
+          uint32_t v[32];
+          load(v, c);
+          if (c == kHalf - 32) give_back();
+          float(&z)[32] = reinterpret_cast<float(&)[32]>(v);
+          if (nothing)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = 0.f;
+          finish(z, col0 + c);
+        }
       }
+      __syncwarp();
       if (MODE == kLse && row < count && col0 < p.cols)
         p.part[(size_t)row * p.parts + p.part0 + (col0 / kHalf)] = make_float2(sum.m, sum.s);
     }

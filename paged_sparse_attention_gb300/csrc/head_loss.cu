@@ -78,13 +78,45 @@ struct GatherArgs {
   int V;
   int* rows;
   int* count;
+  const void* w;          // forward: W and the cap, for the logits of the targets
+  int w_vec;
+  float cap;
+  float* at;              // [n]
   float* loss;            // forward: written in rows without a target
   float* lse;
   void* dx;               // backward: the same
   uint32_t* err;
 };
 
-// Gathers the rows of x that have a target.  A block takes a contiguous range of rows; how many
+// Logit of a row and its target, fp32 products by one warp; the same order for every alignment.
+template <typename T, bool VEC>
+__device__ __forceinline__ float dot_row(const T* x, const T* w, int D, int lane) {
+  constexpr int E = 16 / sizeof(T);
+  float s[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) s[e] = 0.f;
+#pragma unroll 4
+  for (int c = lane * E; c < D; c += 32 * E) {
+    if constexpr (VEC) {
+      const uint4 a = *reinterpret_cast<const uint4*>(x + c), b = *reinterpret_cast<const uint4*>(w + c);
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        s[e] = fmaf(to_float<T>(reinterpret_cast<const T*>(&a)[e]), to_float<T>(reinterpret_cast<const T*>(&b)[e]), s[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (c + e < D) s[e] = fmaf(to_float<T>(x[c + e]), to_float<T>(w[c + e]), s[e]);
+    }
+  }
+  float v = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) v += s[e];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Gathers the rows of x that have a target; forward: forms the targets' logits.  A block takes a contiguous range of rows; how many
 // rows before it have a target it counts itself, so that one launch is enough.
 constexpr int kStageThreads = 256;
 template <typename T, bool VEC>
@@ -136,6 +168,13 @@ __global__ void __launch_bounds__(kStageThreads) stage_x(const __grid_constant__
       if (to >= 0) {
         stage_row<T, VEC>(reinterpret_cast<const T*>(a.in) + (size_t)(i0 + j) * a.D, a.out + (size_t)to * a.pitch, plane,
                           a.D, lane);
+        if (a.at) {
+          const T* x = reinterpret_cast<const T*>(a.in) + (size_t)(i0 + j) * a.D;
+          const T* w = reinterpret_cast<const T*>(a.w) + (size_t)a.targets[i0 + j] * a.D;
+          float z = VEC && a.w_vec ? dot_row<T, VEC>(x, w, a.D, lane) : dot_row<T, false>(x, w, a.D, lane);
+          if (a.cap > 0.f) z = a.cap * tanhf(z / a.cap);
+          if (lane == 0) a.at[to] = z;
+        }
       } else if (a.dx) {
         T* d = reinterpret_cast<T*>(a.dx) + (size_t)(i0 + j) * a.D;
         for (int c = lane; c < a.D; c += 32) d[c] = from_float<T>(0.f);
@@ -190,10 +229,12 @@ __global__ void __launch_bounds__(256) join_lse(const __grid_constant__ GemmArgs
       m = to;
     }
     if (lane == 0) {
-      const float l = (m + log2f(s)) * tc::kLn2;
+      // the target's logit z and the rest: a sure row's loss is small and keeps its own precision
+      const float z = a.at[r], rest = (m + log2f(s)) * tc::kLn2;
+      const float l = z >= rest ? log1pf(s * exp2f(m - z * tc::kLog2e)) : (rest - z) + log1pf(expf(z - rest));
       const int row = a.rows[r];
-      lse[row] = l;
-      loss[row] = l - a.at[r];
+      loss[row] = l;
+      lse[row] = z >= rest ? z + l : rest + log1pf(expf(z - rest));
     }
   }
 }
@@ -304,13 +345,18 @@ cudaError_t launch_after(K kernel, unsigned grid, unsigned threads, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int MODE>
-cudaError_t gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& p, int64_t most_tiles, cudaStream_t st) {
+template <int MODE, bool CHUNKED>
+cudaError_t gemm_of(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& p, int64_t most_tiles, cudaStream_t st) {
   static size_t set[kMaxDevices] = {};
-  const cudaError_t e = set_smem_limit((const void*)head_gemm<MODE>, kSmem, set);
+  const cudaError_t e = set_smem_limit((const void*)head_gemm<MODE, CHUNKED>, kSmem, set);
   if (e != cudaSuccess) return e;
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(clusters(), most_tiles);
-  return launch_after(head_gemm<MODE>, grid, (unsigned)kThreads, kSmem, st, a, b, p);
+  return launch_after(head_gemm<MODE, CHUNKED>, grid, (unsigned)kThreads, kSmem, st, a, b, p);
+}
+template <int MODE>
+cudaError_t gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& p, int64_t most_tiles, cudaStream_t st) {
+  if (MODE == kLse || p.passes > 1) return gemm_of<MODE, true>(a, b, p, most_tiles, st);
+  return gemm_of<MODE, MODE == kLse>(a, b, p, most_tiles, st);
 }
 
 // What both directions share: the rows with a target, gathered.
@@ -460,11 +506,12 @@ GemmArgs arguments(const void* x, const int64_t* targets, int n, int D, int V, i
   g.n = n;
   g.splits = 1;
   g.passes = pl.parts_of == 1 ? 1 : 6;
+  g.chunk = pl.parts_of == 1 ? 8 : 4;
   g.targets = targets;
   g.cap = cap;
   g.part = reinterpret_cast<float2*>(ws + pl.part);
   g.parts = pl.row_parts;
-  g.at = reinterpret_cast<float*>(ws + pl.at);
+  g.at = reinterpret_cast<const float*>(ws + pl.at);
   g.dz = reinterpret_cast<__nv_bfloat16*>(ws + pl.dz);
   g.acc = reinterpret_cast<float*>(ws + pl.acc);
   g.acc_pitch = (int)align_up((size_t)D, 4);
@@ -514,6 +561,10 @@ oomb_status oomb_head_loss_fwd(const void* x, const void* w, const int64_t* targ
   GemmArgs g = arguments(x, targets, n, D, V, dtype, softcap, pl, ws, error_word, &st);
   st.loss = loss;
   st.lse = lse;
+  st.w = w;
+  st.w_vec = on16(w);
+  st.cap = softcap;
+  st.at = reinterpret_cast<float*>(ws + pl.at);
   cudaStream_t on = (cudaStream_t)stream;
   return cuda_status(dtype == OOMB_FP32 ? forward<float>(g, st, w, pl, ws, V, loss, lse, on)
                                         : forward<__nv_bfloat16>(g, st, w, pl, ws, V, loss, lse, on));

@@ -17,6 +17,7 @@ struct GemmArgs {
   int steps;        // of K (not kDw)
   int splits;       // K is cut in this many parts (kDx)
   int passes;       // 1, or 6 products of parts
+  int chunk;        // steps of K that are summed on the tensor cores
   int row_b;        // first row of the piece in W's map
   // the piece of the vocabulary: columns [v0, v0 + cols)
   int v0, cols;
@@ -25,7 +26,7 @@ struct GemmArgs {
   // kLse
   float2* part;     // [n, parts] maximum and sum of 128 columns, base 2
   int parts, part0;
-  float* at;        // [n] logit of the target
+  const float* at;  // [n] logit of the target, which is not in the sums
   // kDz
   const float* lse;
   const float* d_loss;

@@ -39,6 +39,7 @@ struct LnArgs {
   float* part;  // [2, blocks, D]
   int64_t n;
   int D, accumulate;
+  int param_vec;  // w and b start on 16 bytes
   float eps, inv_D;
 };
 
@@ -114,19 +115,30 @@ struct Row {
     }
   }
 };
-// fp32 parameters at the same columns
+// fp32 parameters at the same columns (vec: on 16 bytes)
 template <int E, int NV>
-__device__ __forceinline__ void load_param(const float* p, int D, float (&f)[NV * E], float absent) {
+__device__ __forceinline__ void load_param(const float* p, int D, bool vec, float (&f)[NV * E], float absent) {
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = (v * (int)blockDim.x + (int)threadIdx.x) * E;
+    if (E % 4 == 0 && vec && p && c < D) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[v * E + e] = p && c < D ? __ldg(p + c + e) : absent;
+      for (int e = 0; e < E; e += 4) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(p + c + e));
+        f[v * E + e] = x.x;
+        f[v * E + (E > 1 ? e + 1 : 0)] = x.y;
+        f[v * E + (E > 1 ? e + 2 : 0)] = x.z;
+        f[v * E + (E > 1 ? e + 3 : 0)] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[v * E + e] = p && c < D ? __ldg(p + c + e) : absent;
+    }
   }
 }
 
-template <typename T, int E, int NV>
-__global__ void __launch_bounds__(1024, 1) ln_fwd(const __grid_constant__ LnArgs a) {
+template <typename T, int E, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 1024 / THREADS : 1) ln_fwd(const __grid_constant__ LnArgs a) {
   __shared__ __align__(16) float buf[64];
   if (threadIdx.x < 64) buf[threadIdx.x] = 0.f;
   for (int i = threadIdx.x + blockDim.x; i < 64; i += blockDim.x) buf[i] = 0.f;
@@ -155,8 +167,8 @@ __global__ void __launch_bounds__(1024, 1) ln_fwd(const __grid_constant__ LnArgs
     block_sums<1>(s, buf, turn);
     const float r = rsqrtf(fmaf(s[0], a.inv_D, a.eps));
     float w[NV * E], b[NV * E];
-    load_param<E, NV>(a.w, a.D, w, 1.f);
-    load_param<E, NV>(a.b, a.D, b, 0.f);
+    load_param<E, NV>(a.w, a.D, a.param_vec, w, 1.f);
+    load_param<E, NV>(a.b, a.D, a.param_vec, b, 0.f);
 #pragma unroll
     for (int k = 0; k < NV * E; ++k) x[k] = fmaf(x[k] * r, w[k], b[k]);
     Row<T, E, NV>::store(reinterpret_cast<T*>(a.out) + (size_t)i * a.D, a.D, x);
@@ -167,16 +179,17 @@ __global__ void __launch_bounds__(1024, 1) ln_fwd(const __grid_constant__ LnArgs
   }
 }
 
-// WIDE: rows of more than 8 columns a thread of a full block; their sums are in shared memory.
-template <typename T, int E, int NV, bool WIDE>
-__global__ void __launch_bounds__(1024, 1) ln_bwd(const __grid_constant__ LnArgs a) {
+// WIDE: 16 columns a thread, whose sums are in shared memory; else 8, in registers.  AHEAD rows are
+// in flight beside the one in hand.
+template <typename T, int E, int NV, bool WIDE, int AHEAD, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) ln_bwd(const __grid_constant__ LnArgs a) {
   constexpr int C = NV * E;
   extern __shared__ __align__(16) float acc[];  // WIDE: [2 C, T]
   __shared__ __align__(16) float buf[128];
   let_next_launch();
   for (int i = threadIdx.x; i < 128; i += blockDim.x) buf[i] = 0.f;
   float w[C], dw[C], db[C];
-  load_param<E, NV>(a.w, a.D, w, 1.f);
+  load_param<E, NV>(a.w, a.D, a.param_vec, w, 1.f);
 #pragma unroll
   for (int k = 0; k < C; ++k) {
     dw[k] = db[k] = 0.f;
@@ -184,46 +197,55 @@ __global__ void __launch_bounds__(1024, 1) ln_bwd(const __grid_constant__ LnArgs
   }
   __syncthreads();
   int turn = 0;
-  Row<T, E, NV> nx, ny, nz;
-  float n_mean = 0.f, n_rstd = 0.f;
-  auto fetch = [&](int64_t i) {
+  Row<T, E, NV> nx[AHEAD], ny[AHEAD], nz[AHEAD];
+  float n_mean[AHEAD], n_rstd[AHEAD];
+  auto fetch = [&](int64_t i, int u) {
+    if (i >= a.n) return;
     const size_t at = (size_t)i * a.D;
-    nx.load(reinterpret_cast<const T*>(a.x) + at, a.D);
-    ny.load(reinterpret_cast<const T*>(a.dy) + at, a.D);
-    if (a.dx_in) nz.load(reinterpret_cast<const T*>(a.dx_in) + at, a.D);
-    n_mean = a.mean[i];
-    n_rstd = a.rstd[i];
+    nx[u].load(reinterpret_cast<const T*>(a.x) + at, a.D);
+    ny[u].load(reinterpret_cast<const T*>(a.dy) + at, a.D);
+    if (a.dx_in) nz[u].load(reinterpret_cast<const T*>(a.dx_in) + at, a.D);
+    n_mean[u] = a.mean[i];
+    n_rstd[u] = a.rstd[i];
   };
-  if (blockIdx.x < a.n) fetch(blockIdx.x);
-  for (int64_t i = blockIdx.x; i < a.n; i += gridDim.x) {
-    float xn[C], t[C], z[C], s[2] = {0.f, 0.f};
-    nx.get(a.D, xn);
-    ny.get(a.D, t);
-    if (a.dx_in) nz.get(a.D, z);
-    const float mean = n_mean, r = n_rstd;
-    if (i + gridDim.x < a.n) fetch(i + gridDim.x);
 #pragma unroll
-    for (int k = 0; k < C; ++k) {
-      xn[k] = (xn[k] - mean) * r;  // absent columns: t is 0 there
-      if constexpr (WIDE) {
-        acc[k * blockDim.x + threadIdx.x] += t[k] * xn[k];
-        acc[(C + k) * blockDim.x + threadIdx.x] += t[k];
-      } else {
-        dw[k] = fmaf(t[k], xn[k], dw[k]);
-        db[k] += t[k];
+  for (int u = 0; u < AHEAD; ++u) fetch(blockIdx.x + (int64_t)u * gridDim.x, u);
+  for (int64_t i0 = blockIdx.x; i0 < a.n; i0 += (int64_t)AHEAD * gridDim.x) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int64_t i = i0 + (int64_t)u * gridDim.x;
+      if (i >= a.n) break;
+      float xn[C], t[C], s[2] = {0.f, 0.f};
+      Row<T, E, NV> rz = nz[u];
+      nx[u].get(a.D, xn);
+      ny[u].get(a.D, t);
+      const float mean = n_mean[u], r = n_rstd[u];
+      fetch(i + (int64_t)AHEAD * gridDim.x, u);
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        xn[k] = (xn[k] - mean) * r;  // absent columns: t is 0 there
+        if constexpr (WIDE) {
+          acc[k * blockDim.x + threadIdx.x] += t[k] * xn[k];
+          acc[(C + k) * blockDim.x + threadIdx.x] += t[k];
+        } else {
+          dw[k] = fmaf(t[k], xn[k], dw[k]);
+          db[k] += t[k];
+        }
+        t[k] *= w[k];
+        s[0] += t[k];
+        s[1] = fmaf(t[k], xn[k], s[1]);
       }
-      t[k] *= w[k];
-      s[0] += t[k];
-      s[1] = fmaf(t[k], xn[k], s[1]);
-    }
-    block_sums<2>(s, buf, turn);
-    const float m0 = s[0] * a.inv_D, m1 = s[1] * a.inv_D;
+      block_sums<2>(s, buf, turn);
+      const float m0 = s[0] * a.inv_D, m1 = s[1] * a.inv_D;
 #pragma unroll
-    for (int k = 0; k < C; ++k) {
-      const float v = r * (t[k] - m0 - xn[k] * m1);
-      t[k] = a.dx_in ? z[k] + v : v;
+      for (int k = 0; k < C; ++k) t[k] = r * (t[k] - m0 - xn[k] * m1);
+      if (a.dx_in) {
+        rz.get(a.D, xn);
+#pragma unroll
+        for (int k = 0; k < C; ++k) t[k] += xn[k];
+      }
+      Row<T, E, NV>::store(reinterpret_cast<T*>(a.dx) + (size_t)i * a.D, a.D, t);
     }
-    Row<T, E, NV>::store(reinterpret_cast<T*>(a.dx) + (size_t)i * a.D, a.D, t);
   }
   float* pw = a.part + (size_t)blockIdx.x * a.D;
   float* pb = a.part + ((size_t)gridDim.x + blockIdx.x) * a.D;
@@ -267,17 +289,24 @@ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int threads_for(int D, int cols) { return (int)align_up((size_t)(D + cols - 1) / cols, 32); }
 
-int bwd_cols(int D) { return D <= 1024 * kCols ? kCols : 2 * kCols; }
-// Blocks of the backward, each with its own parts of the parameter gradients.
+int bwd_cols(int D) { return D <= 512 * kCols ? kCols : 2 * kCols; }
+// Blocks of the backward, each with its own parts of the parameter gradients: 512 threads an SM.
 int bwd_blocks(int64_t n, int D) {
-  const int per_sm = std::max(1, std::min(8, 1024 / threads_for(D, bwd_cols(D))));
+  const int per_sm = std::max(1, std::min(8, 512 / threads_for(D, bwd_cols(D))));
   return (int)std::min<int64_t>(n, (int64_t)per_sm * device_sm_count());
 }
 
 template <typename T, int E, int NV>
 cudaError_t fwd(const LnArgs& a, cudaStream_t st) {
   count_launches(1);
-  ln_fwd<T, E, NV><<<(unsigned)std::min<int64_t>(a.n, 1 << 20), threads_for(a.D, E * NV), 0, st>>>(a);
+  const int threads = threads_for(a.D, E * NV);
+  const unsigned grid = (unsigned)std::min<int64_t>(a.n, 1 << 20);
+  if (threads <= 128)
+    ln_fwd<T, E, NV, 128><<<grid, threads, 0, st>>>(a);
+  else if (threads <= 512)
+    ln_fwd<T, E, NV, 512><<<grid, threads, 0, st>>>(a);
+  else
+    ln_fwd<T, E, NV, 1024><<<grid, threads, 0, st>>>(a);
   return cudaGetLastError();
 }
 template <typename T>
@@ -287,30 +316,33 @@ cudaError_t fwd_any(const LnArgs& a, cudaStream_t st) {
   return fwd<T, 1, 16>(a, st);
 }
 
-template <typename T, int E, int NV, bool WIDE>
+template <typename T, int E, int NV, bool WIDE, int AHEAD, int THREADS>
 cudaError_t bwd(const LnArgs& a, int blocks, cudaStream_t st) {
   const int threads = threads_for(a.D, E * NV);
   size_t smem = 0;
   if constexpr (WIDE) {
     static size_t set[kMaxDevices] = {};
-    const cudaError_t e = set_smem_limit((const void*)ln_bwd<T, E, NV, WIDE>, (size_t)2 * E * NV * 1024 * 4, set);
+    const cudaError_t e =
+        set_smem_limit((const void*)ln_bwd<T, E, NV, WIDE, AHEAD, THREADS>, (size_t)2 * E * NV * THREADS * 4, set);
     if (e != cudaSuccess) return e;
     smem = (size_t)2 * E * NV * threads * 4;
   }
   count_launches(1);
-  ln_bwd<T, E, NV, WIDE><<<(unsigned)blocks, threads, smem, st>>>(a);
+  ln_bwd<T, E, NV, WIDE, AHEAD, THREADS><<<(unsigned)blocks, threads, smem, st>>>(a);
   return cudaGetLastError();
+}
+template <typename T, int E>
+cudaError_t bwd_width(const LnArgs& a, int blocks, cudaStream_t st) {
+  if (bwd_cols(a.D) == kCols) return bwd<T, E, kCols / E, false, sizeof(T) == 2 ? 3 : 2, 512>(a, blocks, st);
+  if (a.D <= 512 * 2 * kCols) return bwd<T, E, 2 * kCols / E, true, 1, 512>(a, blocks, st);
+  return bwd<T, E, 2 * kCols / E, true, 1, 1024>(a, blocks, st);
 }
 template <typename T>
 cudaError_t bwd_any(const LnArgs& a, cudaStream_t st) {
   constexpr int E = 16 / sizeof(T);
   const int blocks = bwd_blocks(a.n, a.D);
-  const bool wide = bwd_cols(a.D) > kCols;
-  cudaError_t e;
-  if (a.D % E == 0 && on16(a.x) && on16(a.dy) && on16(a.dx_in) && on16(a.dx))
-    e = wide ? bwd<T, E, 2 * kCols / E, true>(a, blocks, st) : bwd<T, E, kCols / E, false>(a, blocks, st);
-  else
-    e = wide ? bwd<T, 1, 2 * kCols, true>(a, blocks, st) : bwd<T, 1, kCols, false>(a, blocks, st);
+  const bool vec = a.D % E == 0 && on16(a.x) && on16(a.dy) && on16(a.dx_in) && on16(a.dx);
+  const cudaError_t e = vec ? bwd_width<T, E>(a, blocks, st) : bwd_width<T, 1>(a, blocks, st);
   if (e != cudaSuccess || (!a.dw && !a.db)) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.D + 31) / 32, 2);
@@ -352,6 +384,7 @@ oomb_status oomb_layer_norm_fwd(const void* x, const float* w, const float* b, f
   a.x = x;
   a.w = w;
   a.b = b;
+  a.param_vec = on16(w) && on16(b);
   a.eps = eps;
   a.n = n;
   a.D = D;
@@ -384,6 +417,7 @@ oomb_status oomb_layer_norm_bwd(const void* x, const float* w, const float* mean
   LnArgs a = {};
   a.x = x;
   a.w = w;
+  a.param_vec = on16(w);
   a.n = n;
   a.D = D;
   a.inv_D = 1.f / (float)D;
