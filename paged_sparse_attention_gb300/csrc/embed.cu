@@ -7,16 +7,16 @@
 //
 // Backward: rows of one token are summed by one owner in row order, so there are no float
 // atomics and the gradient is the same bits on every run.  Three or four launches:
-//   rank_tokens   the stable order of the tokens.  A key's rank among the keys of its section is
-//                 counted directly, as the number of keys that come before it: sorting by passes
-//                 would need several dependent launches for a chunk of a few thousand tokens.
-//   merge_ranks   where there are several sections: a key's rank among all keys is the sum of its
+//   sort_tokens   the stable order of the tokens, a section of up to 8192 rows a block: a radix sort
+//                 of 6 bits a pass in shared memory, whose passes are barriers instead of launches.
+//   merge_sections  where there are several sections: a key's rank among all keys is the sum of its
 //                 places in every section, found by binary search.
 //   sum_runs      the sorted rows in windows of kWindow.  The rows of one token in one window are a
-//                 piece, summed in fp32 by the block in whose tile it starts.  A token whose rows
-//                 lie in one window goes straight to its row of the table's gradient.
+//                 piece, summed in fp32 by one block.  A token whose rows lie in one window goes
+//                 straight to its row of the table's gradient.
 //   join_pieces   tokens whose rows go on into other windows: their pieces, summed in order.
 #include <climits>
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "embed.h"
@@ -25,10 +25,12 @@
 namespace oomb {
 namespace {
 
-constexpr int kSection = 8192;  // most keys ranked against each other: 32 KB of shared memory
-constexpr int kRankKeys = 32;   // keys a block ranks
-constexpr int kRankParts = 16;  // warps that share the comparisons of one key
-constexpr int kWindow = 64;     // sorted rows a piece lies in
+constexpr int kSection = 8192;  // rows sorted by one block
+constexpr int kSortThreads = 1024, kSortKeys = kSection / kSortThreads;
+constexpr int kDigit = 6;       // bits a pass
+constexpr int kWindow = 16;     // sorted rows a piece lies in
+constexpr int kBatch = 8;       // of them in registers at once
+constexpr int kHeavy = 32;      // windows a token goes back over to count as one of many pieces
 constexpr int kNone = INT_MAX;  // key of a row without a token: behind every other
 
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -77,13 +79,15 @@ __device__ __forceinline__ void store_e(T* p, const float (&f)[E]) {
 }
 
 // ------------------------------------------------------------------ forward
-// Rows of a block: `rows` of them at a time, blockDim.x / rows threads each, NV vectors of E elements
-// a thread at a time.
+// Rows of a block: `rows` of them, blockDim.x / rows threads each, NV vectors of E elements a thread
+// asked for at once: many small blocks, whose token, row and stores wait for one another, hide
+// each other's.  (Blocks that walk the rows with the next one in flight took 23 us for 8192 rows of
+// 3584 in bf16, these 18 at 8 KB a block.)
 template <typename T, int E, int NV>
 __global__ void __launch_bounds__(256) embed_rows(const __grid_constant__ EmbedArgs a) {
   const int per_row = blockDim.x / a.rows, r = threadIdx.x / per_row, lane = threadIdx.x % per_row;
   const int64_t i = (int64_t)blockIdx.x * a.rows + r;
-  if (r >= a.rows || i >= a.n) return;
+  if (i >= a.n) return;
   const int key = key_of(a.tokens[i], a.V, a.err);
   T* out = reinterpret_cast<T*>(a.out) + (size_t)i * a.D;
   const T* in = reinterpret_cast<const T*>(a.table) + (size_t)(key == kNone ? 0 : key) * a.D;
@@ -106,84 +110,143 @@ __global__ void __launch_bounds__(256) embed_rows(const __grid_constant__ EmbedA
 }
 
 // ----------------------------------------------------------------- ordering
-// Ranks kRankKeys keys of one section, a warp a share of the section's keys.  Keys before the
-// block's own count when they are not greater, those behind when they are smaller: equal tokens keep
-// their order.
-__global__ void __launch_bounds__(kRankKeys * kRankParts) rank_tokens(const __grid_constant__ EmbedArgs a) {
-  __shared__ int keys[kSection];
-  __shared__ int parts[kRankParts][kRankKeys];
-  const int blocks_each = a.section / kRankKeys;
-  const int64_t first = (int64_t)(blockIdx.x / blocks_each) * a.section;
-  const int m = (int)min((int64_t)a.section, a.n - first);
-  const int own = (blockIdx.x % blocks_each) * kRankKeys;
+// One block a section.  Keys and their rows stand in shared memory in the order reached; in a pass a
+// warp takes 256 of them in turn, 32 at a time, and counts its digits, equal digits among the 32 by
+// ballots, so that equal keys keep their order.
+constexpr int kCountPitch = (1 << kDigit) + 1;
+struct SortSpace {
+  int keys[kSection];
+  uint16_t rows[kSection];
+  int counts[32 * kCountPitch];  // [warp, digit], so that a warp's digits lie in different banks
+  int sums[64];
+};
+__global__ void __launch_bounds__(kSortThreads, 1) sort_tokens(const __grid_constant__ EmbedArgs a) {
+  extern __shared__ __align__(16) uint8_t sort_mem[];
+  SortSpace& s = *reinterpret_cast<SortSpace*>(sort_mem);
   let_next_launch();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.n_long = 0;
-  const int m4 = (m + 3) & ~3;
-#pragma unroll 4
-  for (int j = threadIdx.x; j < m4; j += kRankKeys * kRankParts)
-    keys[j] = j < m ? key_of(a.tokens[first + j], a.V, a.err) : kNone;
-  __syncthreads();
-  const int k = threadIdx.x % kRankKeys, part = threadIdx.x / kRankKeys;
-  const int mine = own + k < m ? keys[own + k] : kNone;
-  int c0 = 0, c1 = 0, c2 = 0, c3 = 0;
-  const int4* v = reinterpret_cast<const int4*>(keys);
-#pragma unroll 4
-  for (int j = part; j < own / 4; j += kRankParts) {
-    const int4 x = v[j];
-    c0 += x.x <= mine;
-    c1 += x.y <= mine;
-    c2 += x.z <= mine;
-    c3 += x.w <= mine;
-  }
-  for (int j = own + part; j < min(own + kRankKeys, m); j += kRankParts)
-    c0 += keys[j] < mine || (keys[j] == mine && j < own + k);
-#pragma unroll 4
-  for (int j = min(own + kRankKeys, m4) / 4 + part; j < m4 / 4; j += kRankParts) {
-    const int4 x = v[j];
-    c0 += x.x < mine;
-    c1 += x.y < mine;
-    c2 += x.z < mine;
-    c3 += x.w < mine;
-  }
-  parts[part][k] = (c0 + c1) + (c2 + c3);
-  __syncthreads();
-  if (part != 0 || own + k >= m) return;
-  int before = 0;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t first = (int64_t)blockIdx.x * kSection;
+  const int m = (int)min((int64_t)kSection, a.n - first);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.n_long[0] = a.n_long[1] = 0;
+  int key[kSortKeys], row[kSortKeys];
+  int64_t token[kSortKeys];
+  auto place = [&](int k) { return warp * (32 * kSortKeys) + k * 32 + lane; };
 #pragma unroll
-  for (int p = 0; p < kRankParts; ++p) before += parts[p][k];
-  const int64_t at = first + before;
-  if (a.n <= a.section) {
-    a.sorted[at] = mine;
-    a.order[at] = own + k;
-  } else {
-    a.sec_sorted[at] = mine;
-    a.sec_order[at] = (int)first + own + k;
+  for (int k = 0; k < kSortKeys; ++k) token[k] = place(k) < m ? a.tokens[first + place(k)] : -1;
+#pragma unroll
+  for (int k = 0; k < kSortKeys; ++k) {
+    row[k] = place(k);
+    const int t = key_of(token[k], a.V, a.err);
+    key[k] = t == kNone ? a.V : t;  // behind every token; rows behind the section's last stay behind them too
+  }
+  for (int shift = 0; shift < a.key_bits; shift += kDigit) {
+    const int bits = min(kDigit, a.key_bits - shift), digits = 1 << bits;
+    for (int i = threadIdx.x; i < 32 * kCountPitch; i += kSortThreads) s.counts[i] = 0;
+    __syncthreads();
+    int before[kSortKeys];
+    unsigned same_of[kSortKeys];  // lanes with the same digit
+#pragma unroll
+    for (int k = 0; k < kSortKeys; ++k) {
+      unsigned same = 0xffffffffu;
+#pragma unroll
+      for (int b = 0; b < kDigit; ++b) {
+        const bool one = (key[k] >> (shift + b)) & 1;
+        const unsigned ones = __ballot_sync(0xffffffffu, one);
+        if (b < bits) same &= one ? ones : ~ones;
+      }
+      same_of[k] = same;
+    }
+#pragma unroll
+    for (int k = 0; k < kSortKeys; ++k) {
+      const int d = (key[k] >> shift) & (digits - 1);
+      const unsigned same = same_of[k];
+      int* count = &s.counts[warp * kCountPitch + d];
+      before[k] = *count + __popc(same & ((1u << lane) - 1));
+      __syncwarp();
+      if (lane == __ffs(same) - 1) *count += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    // sums of the counts in front, digit after digit and warp after warp
+    // a thread: digit `warp` and, of 64, digit `warp` + 32, of the lane's warp
+    const int d0 = lane * kCountPitch + warp, d1 = d0 + 32;
+    const int n0 = s.counts[d0], n1 = s.counts[d1];
+    int i0 = n0, i1 = n1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u0 = __shfl_up_sync(0xffffffffu, i0, o), u1 = __shfl_up_sync(0xffffffffu, i1, o);
+      if (lane >= o) {
+        i0 += u0;
+        i1 += u1;
+      }
+    }
+    if (lane == 31) {
+      s.sums[warp] = i0;
+      s.sums[32 + warp] = i1;
+    }
+    __syncthreads();
+    // of the digits before: lane d holds digits d and d + 32
+    int t0 = s.sums[lane], t1 = s.sums[32 + lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u0 = __shfl_up_sync(0xffffffffu, t0, o), u1 = __shfl_up_sync(0xffffffffu, t1, o);
+      if (lane >= o) {
+        t0 += u0;
+        t1 += u1;
+      }
+    }
+    const int half = __shfl_sync(0xffffffffu, t0, 31);
+    const int p0 = __shfl_sync(0xffffffffu, t0, (warp + 31) & 31), p1 = __shfl_sync(0xffffffffu, t1, (warp + 31) & 31);
+    s.counts[d0] = (warp == 0 ? 0 : p0) + i0 - n0;
+    s.counts[d1] = half + (warp == 0 ? 0 : p1) + i1 - n1;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSortKeys; ++k) {
+      const int at = s.counts[warp * kCountPitch + ((key[k] >> shift) & (digits - 1))] + before[k];
+      s.keys[at] = key[k];
+      s.rows[at] = (uint16_t)row[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSortKeys; ++k) {
+      key[k] = s.keys[place(k)];
+      row[k] = s.rows[place(k)];
+    }
+    __syncthreads();
+  }
+  const bool one = a.n <= kSection;
+#pragma unroll
+  for (int k = 0; k < kSortKeys; ++k) {
+    const int j = place(k);
+    if (j >= m) continue;
+    (one ? a.sorted : a.sec_sorted)[first + j] = key[k] == a.V ? kNone : key[k];
+    (one ? a.order : a.sec_order)[first + j] = (int)first + row[k];
   }
 }
 
 // Four sections' searches run side by side: each is a chain of dependent loads.
 constexpr int kSearches = 4;
-__global__ void __launch_bounds__(128) merge_ranks(const __grid_constant__ EmbedArgs a) {
+__global__ void __launch_bounds__(128) merge_sections(const __grid_constant__ EmbedArgs a) {
   wait_for_launch_before();
   let_next_launch();
   const int64_t j = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (j >= a.n) return;
-  const int key = a.sec_sorted[j], mine = (int)(j / a.section);
-  const int sections = (int)((a.n + a.section - 1) / a.section);
-  int64_t at = j % a.section;
+  const int key = a.sec_sorted[j], mine = (int)(j / kSection);
+  const int sections = (int)((a.n + kSection - 1) / kSection);
+  int64_t at = j % kSection;
   for (int s0 = 0; s0 < sections; s0 += kSearches) {
     int lo[kSearches], hi[kSearches];
 #pragma unroll
     for (int u = 0; u < kSearches; ++u) {
       const int s = s0 + u;
       lo[u] = 0;
-      hi[u] = s < sections && s != mine ? (int)min((int64_t)a.section, a.n - (int64_t)s * a.section) : 0;
+      hi[u] = s < sections && s != mine ? (int)min((int64_t)kSection, a.n - (int64_t)s * kSection) : 0;
     }
-    for (int left = a.section; left > 0; left >>= 1) {  // a section's keys below `key`, up to it in those before
+    for (int left = kSection; left > 0; left >>= 1) {  // a section's keys below `key`, up to it in those before
 #pragma unroll
       for (int u = 0; u < kSearches; ++u) {
         if (lo[u] >= hi[u]) continue;
-        const int mid = (lo[u] + hi[u]) >> 1, x = a.sec_sorted[(int64_t)(s0 + u) * a.section + mid];
+        const int mid = (lo[u] + hi[u]) >> 1, x = a.sec_sorted[(int64_t)(s0 + u) * kSection + mid];
         if (x < key || (s0 + u < mine && x == key))
           lo[u] = mid + 1;
         else
@@ -202,143 +265,187 @@ __global__ void __launch_bounds__(128) merge_ranks(const __grid_constant__ Embed
 // starts the window), one more may go on into the next.
 __device__ __forceinline__ size_t piece_slot(int64_t w, bool first) { return (size_t)w * 2 + (first ? 1 : 0); }
 
-// NV vectors of E elements a thread.  The rows of the tile and the rows of the gradient that they
-// will be added to are all asked for before the first is used.
-template <typename T, int E, int NV>
-__global__ void __launch_bounds__(512) sum_runs(const __grid_constant__ EmbedArgs a) {
-  constexpr int R = kTileRows;
-  __shared__ int rows[kWindow], keys[kWindow + 2];  // from the tile's first row to its window's end; keys[0]: before it
-  wait_for_launch_before();
-  let_next_launch();
-  const int64_t tile = (int64_t)blockIdx.x * R;
-  const int64_t window = tile / kWindow;
-  const int with = (int)(min((window + 1) * kWindow, a.n) - tile), here = min(R, with);
-  for (int j = threadIdx.x; j < with + 2; j += blockDim.x) {
-    const int64_t p = tile + j - 1;
-    keys[j] = p >= 0 && p < a.n ? a.sorted[p] : kNone;
-    if (j < with) rows[j] = a.order[tile + j];
-  }
-  __syncthreads();
-  const int c0 = blockIdx.y * blockDim.x * E * NV + threadIdx.x * E, step = blockDim.x * E;
-  if (c0 >= a.D) return;
-  const T* d_out = reinterpret_cast<const T*>(a.d_out);
-  // row j starts a piece: another token than before, or the first row of a window
-  auto starts = [&](int j) { return keys[j + 1] != keys[j] || (j == 0 && tile % kWindow == 0); };
-  auto row_ptr = [&](int j, int v) { return d_out + (size_t)rows[j] * a.D + c0 + v * step; };
-  float raw[R][NV][E], old[R][NV][E];
+// Adds to what is there without waiting for it: every element has one writer in a launch.
+template <int E>
+__device__ __forceinline__ void add_e(float* p, const float (&f)[E]) {
+  if constexpr (E == 1) {
+    asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(f[0]) : "memory");
+  } else {
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const bool has = j < here && keys[j + 1] != kNone;
-    // whether a piece that starts here is its token's only one cannot be known yet: if it is not, its old
-    // row is read for nothing
-    const bool direct = has && a.accumulate && keys[j + 1] != keys[j];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) raw[j][v][e] = old[j][v][e] = 0.f;
-      if (has && c0 + v * step < a.D) load_e<T, E>(row_ptr(j, v), raw[j][v]);
-      if (direct && c0 + v * step < a.D) load_e<float, E>(a.d_table + (size_t)keys[j + 1] * a.D + c0 + v * step, old[j][v]);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < R; ++j) {
-    if (j >= here || keys[j + 1] == kNone || !starts(j)) continue;
-    const int key = keys[j + 1];
-    float sum[NV][E];
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int e = 0; e < E; ++e) sum[v][e] = raw[j][v][e];
-    int end = j + 1;
-#pragma unroll
-    for (int u = j + 1; u < R; ++u) {
-      if (end != u || u >= here || keys[u + 1] != key) continue;
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum[v][e] += raw[u][v][e];
-      end = u + 1;
-    }
-    if (end == R) {  // on behind the tile
-      int stop = end;
-      while (stop < with && keys[stop + 1] == key) ++stop;
-      for (; end < stop; end += 4) {
-        float f[4][NV][E];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int v = 0; v < NV; ++v) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) f[u][v][e] = 0.f;
-            if (end + u < stop && c0 + v * step < a.D) load_e<T, E>(row_ptr(end + u, v), f[u][v]);
-          }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int e = 0; e < E; ++e) sum[v][e] += f[u][v][e];
-      }
-      end = stop;
-    }
-    const bool first = keys[j] != key, last = keys[end + 1] != key;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if (c0 + v * step >= a.D) continue;
-      if (first && last) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum[v][e] = fmaf(a.scale, sum[v][e], old[j][v][e]);
-        store_e<float, E>(a.d_table + (size_t)key * a.D + c0 + v * step, sum[v]);
-      } else {
-        store_e<float, E>(a.part + piece_slot(window, first) * a.pitch + c0 + v * step, sum[v]);
-      }
-    }
-    // the token's last piece tells the join about it (in any order: each has a row of its own)
-    if (last && !first && blockIdx.y == 0 && threadIdx.x == 0)
-      a.long_runs[atomicAdd(a.n_long, 1)] = make_int2(key, (int)window);
+    for (int i = 0; i < E; i += 4)
+      asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + i), "f"(f[i]), "f"(f[i + 1]), "f"(f[i + 2]),
+                   "f"(f[i + 3])
+                   : "memory");
   }
 }
 
-// An item is 64 columns of one token with pieces in several windows.  Each of the block's groups of
-// threads sums a share of the pieces, the shares are added in order.
-constexpr int kJoinCols = 64, kJoinGroups = 8;
-__global__ void __launch_bounds__(kJoinCols * kJoinGroups) join_pieces(const __grid_constant__ EmbedArgs a) {
-  __shared__ float share[kJoinGroups][kJoinCols];
+// NV vectors of E elements a thread.  A block walks the windows b, b + grid, ...; the next window's
+// tokens are on their way while this one's rows are summed.  A batch's rows are all asked for before
+// the first is used, held as they are stored, and the rows of the gradient that they will be added to
+// are asked into L2, where the additions are done.
+template <typename T, int E, int NV>
+__global__ void __launch_bounds__(512, 2) sum_runs(const __grid_constant__ EmbedArgs a) {
+  constexpr int R = kBatch;
+  using Word = typename std::conditional<E == 1, T, uint4>::type;
+  __shared__ int rows_of[2][kWindow], keys_of[2][kWindow + 2];  // keys[.][0]: of the row before the window
+  wait_for_launch_before();
+  let_next_launch();
+  const int width = blockDim.x * E * NV, slab = blockIdx.y * width;
+  const int c0 = slab + threadIdx.x * E, step = blockDim.x * E;
+  const T* d_out = reinterpret_cast<const T*>(a.d_out) + c0;
+  auto add_word = [](float (&sum)[E], const Word& w) {
+    const T* x = reinterpret_cast<const T*>(&w);
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] += to_float<T>(x[e]);
+  };
+  // thread j: entry j of a window's lists
+  int next_key = kNone, next_row = 0;
+  auto ask = [&](int64_t w) {
+    const int64_t p = w * kWindow + (int)threadIdx.x - 1;
+    if (w >= a.windows || threadIdx.x >= kWindow + 2) return;
+    next_key = p >= 0 && p < a.n ? a.sorted[p] : kNone;
+    next_row = threadIdx.x < kWindow && p + 1 < a.n ? a.order[p + 1] : 0;
+  };
+  ask(blockIdx.x);
+  int buf = 0;
+  for (int64_t window = blockIdx.x; window < a.windows; window += gridDim.x, buf ^= 1) {
+    int* rows = rows_of[buf];
+    int* keys = keys_of[buf];
+    if (threadIdx.x < kWindow + 2) keys[threadIdx.x] = next_key;
+    if (threadIdx.x < kWindow) rows[threadIdx.x] = next_row;
+    __syncthreads();  // (the window before last has been read: its readers have passed the last barrier)
+    ask(window + gridDim.x);
+    if (E > 1 && a.accumulate && threadIdx.x < kWindow) {
+      const int key = keys[threadIdx.x + 1];
+      if (key != kNone && key != keys[threadIdx.x])
+        prefetch_l2(a.d_table + (size_t)key * a.D + slab, (uint32_t)min(width, a.D - slab) * 4);
+    }
+    if (c0 >= a.D) continue;
+    int live = 0;  // rows that have a token
+    while (live < kWindow && keys[live + 1] != kNone) ++live;
+    float sum[NV][E];
+    bool first = false;  // the piece being summed is its token's first
+    for (int j0 = 0; j0 < live; j0 += R) {
+      Word raw[R][NV];
+#pragma unroll
+      for (int u = 0; u < R; ++u)
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          if (j0 + u < live && c0 + v * step < a.D)
+            raw[u][v] = *reinterpret_cast<const Word*>(d_out + (size_t)rows[j0 + u] * a.D + v * step);
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        const int j = j0 + u;
+        if (j >= live) continue;
+        const int key = keys[j + 1];
+        if (j == 0 || key != keys[j]) {  // a piece starts
+          first = key != keys[j];
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum[v][e] = 0.f;
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          if (c0 + v * step < a.D) add_word(sum[v], raw[u][v]);
+        const bool last = keys[j + 2] != key;
+        if (!last && j + 1 < kWindow) continue;
+        float* to = first && last ? a.d_table + (size_t)key * a.D : a.part + piece_slot(window, first) * a.pitch;
+        const float by = first && last ? a.scale : 1.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          if (c0 + v * step >= a.D) continue;
+#pragma unroll
+          for (int e = 0; e < E; ++e) sum[v][e] *= by;
+          if (first && last && a.accumulate)
+            add_e<E>(to + c0 + v * step, sum[v]);
+          else
+            store_e<float, E>(to + c0 + v * step, sum[v]);
+        }
+        // the token's last piece tells the join about it (in any order: each has a row of its own)
+        if (last && !first && blockIdx.y == 0 && threadIdx.x == 0) {
+          const bool heavy = window >= kHeavy && a.sorted[(window - kHeavy) * kWindow] == key;
+          const int at = heavy ? (int)a.windows - 1 - atomicAdd(a.n_long + 1, 1) : atomicAdd(a.n_long, 1);
+          a.long_runs[at] = make_int2(key, (int)window);
+        }
+      }
+    }
+  }
+}
+
+// Joins the tokens whose rows lie in several windows.  Most have a few pieces: a warp takes 128 columns
+// of one.  Those with kHeavy or more, which a common token has in a long batch, are taken by whole
+// blocks, the warps each a share of the pieces, whose sums are added in order.
+constexpr int kJoinCols = 128, kJoinWarps = 16;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_pieces(const __grid_constant__ EmbedArgs a) {
+  __shared__ float4 share[kJoinWarps][32];
   wait_for_launch_before();
   const int chunks = (a.D + kJoinCols - 1) / kJoinCols;
-  const int64_t items = (int64_t)*a.n_long * chunks;
-  const int g = threadIdx.x / kJoinCols, col = threadIdx.x % kJoinCols, lane = threadIdx.x % 32;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int2 run = a.long_runs[it / chunks];
-    const int key = run.x, c = (int)(it % chunks) * kJoinCols + col;
-    // first window: the one before the last whose first row is not a continuation (every warp for itself)
-    int begin = run.y;
-    for (;;) {
-      const int w = begin - lane;
-      const bool goes_back = w > 0 && a.sorted[(int64_t)w * kWindow - 1] == key;
-      const unsigned stops = __ballot_sync(0xffffffffu, !goes_back);
-      if (stops) {
-        begin -= __ffs(stops) - 1;
-        break;
-      }
-      begin -= 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // first window of a run that ends in window w: the last one whose first row does not go on with the
+  // run.  Among the last 32, else by a search that cuts the rest in 32 at a step.
+  auto first_window = [&](int key, int w) {
+    auto goes_back = [&](int x) { return x > 0 && a.sorted[(int64_t)x * kWindow - 1] == key; };
+    const unsigned stops = __ballot_sync(0xffffffffu, !goes_back(w - lane));
+    if (stops) return w - (__ffs(stops) - 1);
+    int lo = 0, hi = w - 31;  // lo does not go back, hi does
+    while (hi - lo > 1) {
+      const int x = lo + (int)((int64_t)(hi - lo) * (lane + 1) / 33);
+      const unsigned back = __ballot_sync(0xffffffffu, goes_back(x));  // lanes from some one on
+      const int from = back ? __ffs(back) - 1 : 32;
+      const int low = __shfl_sync(0xffffffffu, x, max(from - 1, 0)), high = __shfl_sync(0xffffffffu, x, min(from, 31));
+      if (from > 0) lo = max(lo, low);
+      if (from < 32) hi = high;
     }
-    const int pieces = run.y - begin + 1, per = (pieces + kJoinGroups - 1) / kJoinGroups;
-    float sum = 0.f;
+    return lo;
+  };
+  auto sum_of = [&](int begin, int from, int to, int c) {  // pieces [from, to) of the run
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < a.D) {
-      const int end = min(pieces, (g + 1) * per);
-#pragma unroll 4
-      for (int k = g * per; k < end; ++k) sum += a.part[piece_slot(begin + k, k == 0) * a.pitch + c];
+#pragma unroll 8
+      for (int k = from; k < to; ++k) {
+        const float4 x = *reinterpret_cast<const float4*>(a.part + piece_slot(begin + k, k == 0) * a.pitch + c);
+        sum.x += x.x;
+        sum.y += x.y;
+        sum.z += x.z;
+        sum.w += x.w;
+      }
     }
-    share[g][col] = sum;
-    __syncthreads();
-    if (g == 0 && c < a.D) {
+    return sum;
+  };
+  auto write = [&](int key, int c, const float4& sum) {
+    const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+    float* to = a.d_table + (size_t)key * a.D + c;
 #pragma unroll
-      for (int x = 1; x < kJoinGroups; ++x) sum += share[x][col];
-      float* to = a.d_table + (size_t)key * a.D + c;
-      *to = fmaf(a.scale, sum, a.accumulate ? *to : 0.f);
+    for (int e = 0; e < 4; ++e)
+      if (c + e < a.D) to[e] = fmaf(a.scale, f[e], a.accumulate ? to[e] : 0.f);
+  };
+  const int64_t heavy = (int64_t)a.n_long[1] * chunks, light = (int64_t)a.n_long[0] * chunks;
+  for (int64_t it = blockIdx.x; it < heavy; it += gridDim.x) {
+    const int2 run = a.long_runs[a.windows - 1 - it / chunks];
+    const int c = (int)(it % chunks) * kJoinCols + 4 * lane;
+    const int begin = first_window(run.x, run.y), pieces = run.y - begin + 1, per = (pieces + kJoinWarps - 1) / kJoinWarps;
+    float4 sum = sum_of(begin, warp * per, min(pieces, (warp + 1) * per), c);
+    share[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int x = 1; x < kJoinWarps; ++x) {
+        const float4 y = share[x][lane];
+        sum.x += y.x;
+        sum.y += y.y;
+        sum.z += y.z;
+        sum.w += y.w;
+      }
+      write(run.x, c, sum);
     }
     __syncthreads();
+  }
+  for (int64_t it = (int64_t)blockIdx.x * kJoinWarps + warp; it < light; it += (int64_t)gridDim.x * kJoinWarps) {
+    const int2 run = a.long_runs[it / chunks];
+    const int c = (int)(it % chunks) * kJoinCols + 4 * lane;
+    const int begin = first_window(run.x, run.y);
+    write(run.x, c, sum_of(begin, 0, run.y - begin + 1, c));
   }
 }
 
@@ -370,39 +477,39 @@ cudaError_t forward(EmbedArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Keys ranked against each other: all of a chunk's where that is one launch less, else half as many,
-// which halves the comparisons.
-int section_of(int64_t n) { return n <= kSection ? kSection : kSection / 2; }
+size_t sort_smem_set[kMaxDevices] = {};
 
 template <typename T, int E, int NV>
 cudaError_t backward(const EmbedArgs& a, cudaStream_t st) {
-  const int64_t sections = (a.n + a.section - 1) / a.section;
-  const int64_t last = a.n - (sections - 1) * a.section;
-  const unsigned ranks = (unsigned)((sections - 1) * (a.section / kRankKeys) + (last + kRankKeys - 1) / kRankKeys);
+  const unsigned sections = (unsigned)((a.n + kSection - 1) / kSection);
+  cudaError_t e = set_smem_limit((const void*)sort_tokens, sizeof(SortSpace), sort_smem_set);
+  if (e != cudaSuccess) return e;
   count_launches(1);
-  rank_tokens<<<ranks, kRankKeys * kRankParts, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  sort_tokens<<<sections, kSortThreads, sizeof(SortSpace), st>>>(a);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (sections > 1) {
-    e = launch_after(merge_ranks, dim3((unsigned)((a.n + 127) / 128)), 128, a, st);
+    e = launch_after(merge_sections, dim3((unsigned)((a.n + 127) / 128)), 128, a, st);
     if (e != cudaSuccess) return e;
   }
   const int vecs = (a.D + E * NV - 1) / (E * NV);
   const int slabs = (vecs + 511) / 512;
-  const int threads = (int)align_up((size_t)(vecs + slabs - 1) / slabs, 32);
-  e = launch_after(sum_runs<T, E, NV>, dim3((unsigned)((a.n + kTileRows - 1) / kTileRows), (unsigned)slabs), threads, a,
-                   st);
+  const int threads = std::max(64, (int)align_up((size_t)(vecs + slabs - 1) / slabs, 32));
+  const int64_t most = (int64_t)(1024 / threads) * device_sm_count();
+  e = launch_after(sum_runs<T, E, NV>,
+                   dim3((unsigned)std::min<int64_t>(a.windows, std::max<int64_t>(1, most / slabs)), (unsigned)slabs),
+                   threads, a, st);
   if (e != cudaSuccess || a.n <= kWindow) return e;
   // at most a run goes on from each window into the next
-  const int64_t most = ((a.n - 1) / kWindow) * ((a.D + kJoinCols - 1) / kJoinCols);
-  return launch_after(join_pieces, dim3((unsigned)std::min<int64_t>(most, 4 * device_sm_count())),
-                      kJoinCols * kJoinGroups, a, st);
+  const int64_t items = ((a.n - 1) / kWindow) * ((a.D + kJoinCols - 1) / kJoinCols);
+  return launch_after(join_pieces, dim3((unsigned)std::min<int64_t>((items + kJoinWarps - 1) / kJoinWarps, 4 * device_sm_count())),
+                      32 * kJoinWarps, a, st);
 }
 
 template <typename T>
 cudaError_t forward_any(EmbedArgs& a, cudaStream_t st) {
   constexpr int E = 16 / sizeof(T);
-  return a.D % E == 0 && on16(a.table) && on16(a.out) ? forward<T, E, 2>(a, st) : forward<T, 1, 4>(a, st);
+  return a.D % E == 0 && on16(a.table) && on16(a.out) ? forward<T, E, 4>(a, st) : forward<T, 1, 8>(a, st);
 }
 template <typename T>
 cudaError_t backward_any(const EmbedArgs& a, cudaStream_t st) {
@@ -425,9 +532,9 @@ EmbedSpace embed_space(int64_t n, int D) {
   };
   s.order = take((size_t)n * 4);
   s.sorted = take((size_t)n * 4);
-  s.sec_order = take(n > section_of(n) ? (size_t)n * 4 : 0);
-  s.sec_sorted = take(n > section_of(n) ? (size_t)n * 4 : 0);
-  s.n_long = take(4);
+  s.sec_order = take(n > kSection ? (size_t)n * 4 : 0);
+  s.sec_sorted = take(n > kSection ? (size_t)n * 4 : 0);
+  s.n_long = take(8);
   const size_t windows = (size_t)(n + kWindow - 1) / kWindow;
   s.long_runs = take(windows * 8);
   s.pitch = (int64_t)align_up((size_t)D, 4);
@@ -499,11 +606,13 @@ oomb_status oomb_embed_bwd(const int64_t* tokens, int n, const void* d_out, int 
   a.sorted = reinterpret_cast<int*>(base + w.sorted);
   a.sec_order = reinterpret_cast<int*>(base + w.sec_order);
   a.sec_sorted = reinterpret_cast<int*>(base + w.sec_sorted);
-  a.section = section_of(n);
+  a.key_bits = 1;
+  while (a.key_bits < 31 && (V >> a.key_bits) != 0) ++a.key_bits;
   a.n_long = reinterpret_cast<int*>(base + w.n_long);
   a.long_runs = reinterpret_cast<int2*>(base + w.long_runs);
   a.part = reinterpret_cast<float*>(base + w.part);
   a.pitch = w.pitch;
+  a.windows = (n + kWindow - 1) / kWindow;
   cudaStream_t st = (cudaStream_t)stream;
   return cuda_status(dtype == OOMB_FP32 ? backward_any<float>(a, st) : backward_any<__nv_bfloat16>(a, st));
 }

@@ -7,8 +7,6 @@
 
 namespace oomb {
 
-constexpr int kTileRows = 4;  // sorted rows whose pieces one block sums
-
 struct EmbedArgs {
   const int64_t* tokens;  // [n]
   const void* table;      // [V, D]
@@ -21,13 +19,14 @@ struct EmbedArgs {
   int accumulate;
   float scale;
   uint32_t* err;
-  int section;            // keys ranked against each other
+  int key_bits;           // of V, which stands for no token
   int* order;             // [n] rows, by token and then by row
   int* sorted;            // [n] their tokens
   int* sec_order;         // the same, each section by itself
   int* sec_sorted;
-  int* n_long;            // tokens whose rows lie in several windows
-  int2* long_runs;        // each: the token and its last window
+  int64_t windows;        // of sorted rows
+  int* n_long;            // [2] tokens whose rows lie in several windows, in a few and in many
+  int2* long_runs;        // [windows] each: the token and its last window; those in many from the end
   float* part;            // sums of their pieces
   int64_t pitch;
 };

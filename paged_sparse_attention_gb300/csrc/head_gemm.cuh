@@ -32,7 +32,6 @@ constexpr uint32_t kStageBytes = 2 * kOperand;
 constexpr uint32_t kSmem = kStages * kStageBytes + 1024;
 constexpr int kThreads = 320;                        // producer, issuer, 8 epilogue warps
 constexpr int kEpilogueWarps = 8;
-constexpr int kGroup = 8;
 
 struct Barriers {
   uint64_t full[kStages], empty[kStages];
@@ -84,7 +83,7 @@ __device__ __forceinline__ int part_a(int passes, int p) { return passes == 1 ? 
 __device__ __forceinline__ int part_b(int passes, int p) { return passes == 1 ? 0 : (0x201100 >> (4 * (5 - p))) & 15; }
 
 // Place of tile t among tms x tns tiles: groups of kGroup row tiles, row tiles first within one.
-__device__ __forceinline__ void place(int t, int tms, int tns, int& tm, int& tn) {
+__device__ __forceinline__ void place(int t, int tms, int tns, int kGroup, int& tm, int& tn) {
   const int per = kGroup * tns, g = t / per, r = t - g * per, rows = min(kGroup, tms - g * kGroup);
   tn = r / rows;
   tm = g * kGroup + (r - tn * rows);
@@ -187,7 +186,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int t = first; ok && t < tiles; t += clusters) {
         int tm, tn, k0, k1;
-        place(t % (tms * p.tns), tms, p.tns, tm, tn);
+        place(t % (tms * p.tns), tms, p.tns, p.group, tm, tn);
         range(t, k0, k1);
         const int ra = tm * kTile + (int)rank * kHalf, rb = tn * kTile + (int)rank * kHalf;
         const int chunk = CHUNKED ? p.chunk : max(1, k1 - k0);
@@ -284,7 +283,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int t = first; t < tiles; t += clusters) {
       int tm, tn, k0, k1;
-      place(t % (tms * p.tns), tms, p.tns, tm, tn);
+      place(t % (tms * p.tns), tms, p.tns, p.group, tm, tn);
       range(t, k0, k1);
       const int split = t / (tms * p.tns);
       const int row = tm * kTile + (int)rank * kHalf + r;

@@ -19,6 +19,13 @@ namespace head {
 namespace {
 
 constexpr int kMaxWidth = 65536;
+// Row tiles that share the columns' tiles in L2: 4096 and 8192 rows on 131072 x 3584, 4 2497 and 19528
+// us, 8 2366 and 19152, 16 2313 and 18903, 32 2312 and 19813.
+constexpr int kGroup = 16;
+// Steps of 64 columns summed on the tensor cores: the loss of 4096 such rows is 1.4e-7, 2.0e-7 and
+// 3.4e-7 of its size off after 8, 16 and 28 steps (2.5e-6 after all 56), in 2343, 2288 and 2243 us.
+// fp32 operands have six products a step and fewer steps.
+constexpr int kChunk = 28, kChunkParts = 4;
 // Workspace given to a piece's dz, and to staged parts of W where it cannot be read in place
 // (kStagedOdd: bf16 rows that are on 16 bytes unless the caller's pointer is not).
 constexpr size_t kDzBytes = 256u << 20, kStagedBytes = 256u << 20, kStagedOdd = 32u << 20;
@@ -506,7 +513,8 @@ GemmArgs arguments(const void* x, const int64_t* targets, int n, int D, int V, i
   g.n = n;
   g.splits = 1;
   g.passes = pl.parts_of == 1 ? 1 : 6;
-  g.chunk = pl.parts_of == 1 ? 8 : 4;
+  g.chunk = pl.parts_of == 1 ? kChunk : kChunkParts;
+  g.group = kGroup;
   g.targets = targets;
   g.cap = cap;
   g.part = reinterpret_cast<float2*>(ws + pl.part);

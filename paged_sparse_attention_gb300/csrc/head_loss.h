@@ -13,6 +13,7 @@ struct GemmArgs {
   const int* count;
   const int* rows;
   int n;            // the caller's rows
+  int group;        // row tiles whose tiles come one after another
   int tms, tns;     // tiles of rows (kDw) and of columns
   int steps;        // of K (not kDw)
   int splits;       // K is cut in this many parts (kDx)

@@ -9,11 +9,14 @@
 // against its spread loses nothing.
 //
 // A row is held by one thread block in registers from its load to its stores, so every tensor is
-// read once and written once; both kernels are bound by HBM.  Forward: a block a row, the rows in
-// flight on an SM hide each other's two sums.  Backward: a block walks the rows b, b + grid, ...
-// with the next row's loads in flight, keeps the parameter gradients of its columns and leaves
-// them in the workspace; they are added there in block order, the same bits on every run.
+// read once and written once.  A block walks the rows b, b + grid, ... with the next ones' loads in
+// flight.  The bytes are HBM's, but the instructions come close behind (a row of 3584 is 14 KB in
+// bf16 and at eight columns a thread 3000 warp instructions of an SM that issues 4 a cycle), so a
+// thread holds 16 columns, which halves what the two sums of a row cost, and works on pairs of
+// fp32.  Backward: the parameter gradients of a block's columns stay in registers and go to the
+// workspace once; they are added there in block order, the same bits on every run.
 #include <cmath>
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "sm103_ptx.cuh"
@@ -22,7 +25,6 @@ namespace oomb {
 namespace {
 
 constexpr int kMaxWidth = 16384;
-constexpr int kCols = 8;  // columns of a thread in the backward
 
 struct LnArgs {
   const void* x;
@@ -80,98 +82,135 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float* buf, int& turn)
   }
 }
 
-// NV vectors of E elements a thread: vector v starts at column (v T + threadIdx.x) E.
-template <typename T, int E, int NV>
+__device__ __forceinline__ uint64_t both(float v) { return f32x2(v, v); }
+__device__ __forceinline__ float halves(uint64_t v) {
+  float a, b;
+  f32x2_split(v, a, b);
+  return a + b;
+}
+
+// C columns a thread in vectors of E: vector v starts at column (v T + threadIdx.x) E.
+template <typename T, int E, int C>
 struct Row {
+  static constexpr int NV = C / E;
   // the elements as they are stored, so that a row in flight takes few registers
   using Word = typename std::conditional<E == 1, T, uint4>::type;
   Word raw[NV];
+  static __device__ __forceinline__ int col(int v) { return (v * (int)blockDim.x + (int)threadIdx.x) * E; }
+  __device__ __forceinline__ void clear() {
+    unsigned char* p = reinterpret_cast<unsigned char*>(raw);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(raw); ++i) p[i] = 0;
+  }
+  // columns behind the last keep what they hold: 0 from clear()
   __device__ __forceinline__ void load(const T* row, int D) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * (int)blockDim.x + (int)threadIdx.x) * E;
-      if (c < D) raw[v] = *reinterpret_cast<const Word*>(row + c);
+    for (int v = 0; v < NV; ++v)
+      if (col(v) < D) raw[v] = *reinterpret_cast<const Word*>(row + col(v));
+  }
+  __device__ __forceinline__ void get(uint64_t (&f)[C / 2]) const {
+    if constexpr (E == 1) {
+#pragma unroll
+      for (int k = 0; k < C / 2; ++k) f[k] = f32x2(to_float<T>(raw[2 * k]), to_float<T>(raw[2 * k + 1]));
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const uint32_t x[4] = {raw[v].x, raw[v].y, raw[v].z, raw[v].w};
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) f[v * 4 + k] = f32x2(x[k] << 16, x[k] & 0xffff0000u);
+        } else {
+          f[v * 2] = f32x2(x[0], x[1]);
+          f[v * 2 + 1] = f32x2(x[2], x[3]);
+        }
+      }
     }
   }
-  __device__ __forceinline__ void get(int D, float (&f)[NV * E]) const {  // absent elements are 0
+  static __device__ __forceinline__ void store(T* row, int D, const uint64_t (&f)[C / 2]) {
+    float x[C];
+#pragma unroll
+    for (int k = 0; k < C / 2; ++k) f32x2_split(f[k], x[2 * k], x[2 * k + 1]);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const bool has = (v * (int)blockDim.x + (int)threadIdx.x) * E < D;
-      const T* x = reinterpret_cast<const T*>(&raw[v]);
-#pragma unroll
-      for (int e = 0; e < E; ++e) f[v * E + e] = has ? to_float<T>(x[e]) : 0.f;
-    }
-  }
-  static __device__ __forceinline__ void store(T* row, int D, const float (&f)[NV * E]) {
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * (int)blockDim.x + (int)threadIdx.x) * E;
-      if (c >= D) continue;
-      Word w;
-      T* x = reinterpret_cast<T*>(&w);
-#pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = from_float<T>(f[v * E + e]);
-      *reinterpret_cast<Word*>(row + c) = w;
+      if (col(v) >= D) continue;
+      if constexpr (E == 1)
+        row[col(v)] = from_float<T>(x[v]);
+      else if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint4*>(row + col(v)) =
+            make_uint4(pack_bf16x2(x[v * 8], x[v * 8 + 1]), pack_bf16x2(x[v * 8 + 2], x[v * 8 + 3]),
+                       pack_bf16x2(x[v * 8 + 4], x[v * 8 + 5]), pack_bf16x2(x[v * 8 + 6], x[v * 8 + 7]));
+      else
+        *reinterpret_cast<float4*>(row + col(v)) = make_float4(x[v * 4], x[v * 4 + 1], x[v * 4 + 2], x[v * 4 + 3]);
     }
   }
 };
-// fp32 parameters at the same columns (vec: on 16 bytes)
-template <int E, int NV>
-__device__ __forceinline__ void load_param(const float* p, int D, bool vec, float (&f)[NV * E], float absent) {
+// fp32 parameters at the same columns
+template <int E, int C>
+__device__ __forceinline__ void load_param(const float* p, int D, bool vec, uint64_t (&f)[C / 2], float absent) {
+  float x[C];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
+  for (int v = 0; v < C / E; ++v) {
     const int c = (v * (int)blockDim.x + (int)threadIdx.x) * E;
-    if (E % 4 == 0 && vec && p && c < D) {
+    if (E >= 4 && vec && p && c < D) {
 #pragma unroll
       for (int e = 0; e < E; e += 4) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(p + c + e));
-        f[v * E + e] = x.x;
-        f[v * E + (E > 1 ? e + 1 : 0)] = x.y;
-        f[v * E + (E > 1 ? e + 2 : 0)] = x.z;
-        f[v * E + (E > 1 ? e + 3 : 0)] = x.w;
+        const float4 y = __ldg(reinterpret_cast<const float4*>(p + c + e));
+        const float t[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < (E < 4 ? E : 4); ++k) x[v * E + e + k] = t[k];
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[v * E + e] = p && c < D ? __ldg(p + c + e) : absent;
+      for (int e = 0; e < E; ++e) x[v * E + e] = p && c + e < D ? __ldg(p + c + e) : absent;
     }
   }
+#pragma unroll
+  for (int k = 0; k < C / 2; ++k) f[k] = f32x2(x[2 * k], x[2 * k + 1]);
 }
 
-template <typename T, int E, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 1024 / THREADS : 1) ln_fwd(const __grid_constant__ LnArgs a) {
+template <typename T, int E, int C, int THREADS, int MIN_BLOCKS>
+__global__ void __launch_bounds__(THREADS, MIN_BLOCKS) ln_fwd(const __grid_constant__ LnArgs a) {
+  constexpr int H = C / 2;
+  using R = Row<T, E, C>;
   __shared__ __align__(16) float buf[64];
-  if (threadIdx.x < 64) buf[threadIdx.x] = 0.f;
-  for (int i = threadIdx.x + blockDim.x; i < 64; i += blockDim.x) buf[i] = 0.f;
+  for (int i = threadIdx.x; i < 64; i += blockDim.x) buf[i] = 0.f;
+  R next;
+  next.clear();
+  if (blockIdx.x < a.n) next.load(reinterpret_cast<const T*>(a.x) + (size_t)blockIdx.x * a.D, a.D);
+  uint64_t w[H], b[H];
+  load_param<E, C>(a.w, a.D, a.param_vec, w, 1.f);
+  load_param<E, C>(a.b, a.D, a.param_vec, b, 0.f);
   if (blockDim.x > 32) __syncthreads();
   int turn = 0;
   for (int64_t i = blockIdx.x; i < a.n; i += gridDim.x) {
-    Row<T, E, NV> row;
-    row.load(reinterpret_cast<const T*>(a.x) + (size_t)i * a.D, a.D);
-    float x[NV * E], s[1] = {0.f};
-    row.get(a.D, x);
+    uint64_t x[H];
+    next.get(x);
+    if (i + gridDim.x < a.n) next.load(reinterpret_cast<const T*>(a.x) + (size_t)(i + gridDim.x) * a.D, a.D);
+    uint64_t t = 0;
 #pragma unroll
-    for (int k = 0; k < NV * E; ++k) s[0] += x[k];
+    for (int k = 0; k < H; ++k) t = add2(t, x[k]);
+    float s[1] = {halves(t)};
     block_sums<1>(s, buf, turn);
     const float mean = s[0] * a.inv_D;
-    s[0] = 0.f;
+    const uint64_t minus = both(-mean);
+    t = 0;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const bool has = (v * (int)blockDim.x + (int)threadIdx.x) * E < a.D;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float c = has ? x[v * E + e] - mean : 0.f;
-        x[v * E + e] = c;
-        s[0] = fmaf(c, c, s[0]);
+    for (int k = 0; k < H; ++k) {
+      x[k] = add2(x[k], minus);
+      if constexpr (E == 1) {
+        if (R::col(2 * k + 1) >= a.D) x[k] = R::col(2 * k) < a.D ? f32x2((uint32_t)x[k], 0u) : 0;
+      } else {
+        if (R::col(2 * k / E) >= a.D) x[k] = 0;
       }
+      t = fma2(x[k], x[k], t);
     }
+    s[0] = halves(t);
     block_sums<1>(s, buf, turn);
     const float r = rsqrtf(fmaf(s[0], a.inv_D, a.eps));
-    float w[NV * E], b[NV * E];
-    load_param<E, NV>(a.w, a.D, a.param_vec, w, 1.f);
-    load_param<E, NV>(a.b, a.D, a.param_vec, b, 0.f);
+    const uint64_t rr = both(r);
 #pragma unroll
-    for (int k = 0; k < NV * E; ++k) x[k] = fmaf(x[k] * r, w[k], b[k]);
-    Row<T, E, NV>::store(reinterpret_cast<T*>(a.out) + (size_t)i * a.D, a.D, x);
+    for (int k = 0; k < H; ++k) x[k] = fma2(mul2(x[k], rr), w[k], b[k]);
+    R::store(reinterpret_cast<T*>(a.out) + (size_t)i * a.D, a.D, x);
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[i] = mean;
       if (a.rstd) a.rstd[i] = r;
@@ -179,86 +218,98 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 1024 / THREADS : 1) 
   }
 }
 
-// WIDE: 16 columns a thread, whose sums are in shared memory; else 8, in registers.  AHEAD rows are
-// in flight beside the one in hand.
-template <typename T, int E, int NV, bool WIDE, int AHEAD, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1) ln_bwd(const __grid_constant__ LnArgs a) {
-  constexpr int C = NV * E;
-  extern __shared__ __align__(16) float acc[];  // WIDE: [2 C, T]
+// SHARED: the sums of the parameter gradients are in shared memory, where registers are short.
+template <typename T, int E, int C, int THREADS, int MIN_BLOCKS, bool SHARED>
+__global__ void __launch_bounds__(THREADS, MIN_BLOCKS) ln_bwd(const __grid_constant__ LnArgs a) {
+  constexpr int H = C / 2;
+  using R = Row<T, E, C>;
+  extern __shared__ __align__(16) uint64_t acc[];  // SHARED: [2 H, T]
   __shared__ __align__(16) float buf[128];
   let_next_launch();
   for (int i = threadIdx.x; i < 128; i += blockDim.x) buf[i] = 0.f;
-  float w[C], dw[C], db[C];
-  load_param<E, NV>(a.w, a.D, a.param_vec, w, 1.f);
+  R nx, ny, nz;
+  float n_mean = 0.f, n_rstd = 0.f;
+  auto fetch = [&](int64_t i) {
+    const size_t at = (size_t)i * a.D;
+    nx.load(reinterpret_cast<const T*>(a.x) + at, a.D);
+    ny.load(reinterpret_cast<const T*>(a.dy) + at, a.D);
+    if (a.dx_in) nz.load(reinterpret_cast<const T*>(a.dx_in) + at, a.D);
+    n_mean = a.mean[i];
+    n_rstd = a.rstd[i];
+  };
+  nx.clear();
+  ny.clear();
+  nz.clear();
+  if (blockIdx.x < a.n) fetch(blockIdx.x);
+  uint64_t w[H], dw[SHARED ? 1 : H], db[SHARED ? 1 : H];
+  load_param<E, C>(a.w, a.D, a.param_vec, w, 1.f);
 #pragma unroll
-  for (int k = 0; k < C; ++k) {
-    dw[k] = db[k] = 0.f;
-    if constexpr (WIDE) acc[k * blockDim.x + threadIdx.x] = acc[(C + k) * blockDim.x + threadIdx.x] = 0.f;
+  for (int k = 0; k < H; ++k) {
+    if constexpr (SHARED)
+      acc[k * blockDim.x + threadIdx.x] = acc[(H + k) * blockDim.x + threadIdx.x] = 0;
+    else
+      dw[k] = db[k] = 0;
   }
   __syncthreads();
   int turn = 0;
-  Row<T, E, NV> nx[AHEAD], ny[AHEAD], nz[AHEAD];
-  float n_mean[AHEAD], n_rstd[AHEAD];
-  auto fetch = [&](int64_t i, int u) {
-    if (i >= a.n) return;
-    const size_t at = (size_t)i * a.D;
-    nx[u].load(reinterpret_cast<const T*>(a.x) + at, a.D);
-    ny[u].load(reinterpret_cast<const T*>(a.dy) + at, a.D);
-    if (a.dx_in) nz[u].load(reinterpret_cast<const T*>(a.dx_in) + at, a.D);
-    n_mean[u] = a.mean[i];
-    n_rstd[u] = a.rstd[i];
-  };
+  for (int64_t i = blockIdx.x; i < a.n; i += gridDim.x) {
+    uint64_t xn[H], t[H];
+    nx.get(xn);
+    ny.get(t);
+    const R z = nz;
+    const float mean = n_mean, r = n_rstd;
+    if (i + gridDim.x < a.n) fetch(i + gridDim.x);
+    const uint64_t rr = both(r), shift = both(-mean);
+    uint64_t s0 = 0, s1 = 0;
 #pragma unroll
-  for (int u = 0; u < AHEAD; ++u) fetch(blockIdx.x + (int64_t)u * gridDim.x, u);
-  for (int64_t i0 = blockIdx.x; i0 < a.n; i0 += (int64_t)AHEAD * gridDim.x) {
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-      const int64_t i = i0 + (int64_t)u * gridDim.x;
-      if (i >= a.n) break;
-      float xn[C], t[C], s[2] = {0.f, 0.f};
-      Row<T, E, NV> rz = nz[u];
-      nx[u].get(a.D, xn);
-      ny[u].get(a.D, t);
-      const float mean = n_mean[u], r = n_rstd[u];
-      fetch(i + (int64_t)AHEAD * gridDim.x, u);
-#pragma unroll
-      for (int k = 0; k < C; ++k) {
-        xn[k] = (xn[k] - mean) * r;  // absent columns: t is 0 there
-        if constexpr (WIDE) {
-          acc[k * blockDim.x + threadIdx.x] += t[k] * xn[k];
-          acc[(C + k) * blockDim.x + threadIdx.x] += t[k];
-        } else {
-          dw[k] = fmaf(t[k], xn[k], dw[k]);
-          db[k] += t[k];
-        }
-        t[k] *= w[k];
-        s[0] += t[k];
-        s[1] = fmaf(t[k], xn[k], s[1]);
+    for (int k = 0; k < H; ++k) {
+      xn[k] = mul2(add2(xn[k], shift), rr);  // columns behind the last: t is 0 there
+      if constexpr (SHARED) {
+        uint64_t* aw = acc + k * blockDim.x + threadIdx.x;
+        uint64_t* ab = acc + (H + k) * blockDim.x + threadIdx.x;
+        *aw = fma2(t[k], xn[k], *aw);
+        *ab = add2(t[k], *ab);
+      } else {
+        dw[k] = fma2(t[k], xn[k], dw[k]);
+        db[k] = add2(t[k], db[k]);
       }
-      block_sums<2>(s, buf, turn);
-      const float m0 = s[0] * a.inv_D, m1 = s[1] * a.inv_D;
-#pragma unroll
-      for (int k = 0; k < C; ++k) t[k] = r * (t[k] - m0 - xn[k] * m1);
-      if (a.dx_in) {
-        rz.get(a.D, xn);
-#pragma unroll
-        for (int k = 0; k < C; ++k) t[k] += xn[k];
-      }
-      Row<T, E, NV>::store(reinterpret_cast<T*>(a.dx) + (size_t)i * a.D, a.D, t);
+      t[k] = mul2(t[k], w[k]);
+      s0 = add2(s0, t[k]);
+      s1 = fma2(t[k], xn[k], s1);
     }
+    float s[2] = {halves(s0), halves(s1)};
+    block_sums<2>(s, buf, turn);
+    const uint64_t m0 = both(-s[0] * a.inv_D), m1 = both(-s[1] * a.inv_D);
+#pragma unroll
+    for (int k = 0; k < H; ++k) t[k] = mul2(fma2(xn[k], m1, add2(t[k], m0)), rr);
+    if (a.dx_in) {
+      z.get(xn);
+#pragma unroll
+      for (int k = 0; k < H; ++k) t[k] = add2(t[k], xn[k]);
+    }
+    R::store(reinterpret_cast<T*>(a.dx) + (size_t)i * a.D, a.D, t);
   }
-  float* pw = a.part + (size_t)blockIdx.x * a.D;
-  float* pb = a.part + ((size_t)gridDim.x + blockIdx.x) * a.D;
+  float* to[2] = {a.dw ? a.part + (size_t)blockIdx.x * a.D : nullptr,
+                  a.db ? a.part + ((size_t)gridDim.x + blockIdx.x) * a.D : nullptr};
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = (v * (int)blockDim.x + (int)threadIdx.x) * E;
-    if (c >= a.D) continue;
+  for (int g = 0; g < 2; ++g) {
+    if (!to[g]) continue;
+    uint64_t f[H];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int k = v * E + e;
-      if (a.dw) pw[c + e] = WIDE ? acc[k * blockDim.x + threadIdx.x] : dw[k];
-      if (a.db) pb[c + e] = WIDE ? acc[(C + k) * blockDim.x + threadIdx.x] : db[k];
+    for (int k = 0; k < H; ++k) {
+      if constexpr (SHARED)
+        f[k] = acc[(g * H + k) * blockDim.x + threadIdx.x];
+      else
+        f[k] = g == 0 ? dw[k] : db[k];
     }
+    float x[C];
+#pragma unroll
+    for (int k = 0; k < H; ++k) f32x2_split(f[k], x[2 * k], x[2 * k + 1]);
+#pragma unroll
+    for (int v = 0; v < C / E; ++v)
+      if (R::col(v) < a.D)
+#pragma unroll
+        for (int e = 0; e < E; ++e) to[g][R::col(v) + e] = x[v * E + e];
   }
 }
 
@@ -289,53 +340,56 @@ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int threads_for(int D, int cols) { return (int)align_up((size_t)(D + cols - 1) / cols, 32); }
 
-int bwd_cols(int D) { return D <= 512 * kCols ? kCols : 2 * kCols; }
-// Blocks of the backward, each with its own parts of the parameter gradients: 512 threads an SM.
+// Columns of a thread: 8 in narrow rows, which have threads to spare.
+int cols_of(int D) { return D <= 2048 ? 8 : 16; }
+// Blocks on an SM: 512 threads, 256 of which have 128 registers each.
+int blocks_per_sm(int T) { return std::max(1, std::min(16, 512 / T)); }
+// Blocks of the backward, each with its own parts of the parameter gradients.
 int bwd_blocks(int64_t n, int D) {
-  const int per_sm = std::max(1, std::min(8, 512 / threads_for(D, bwd_cols(D))));
-  return (int)std::min<int64_t>(n, (int64_t)per_sm * device_sm_count());
+  return (int)std::min<int64_t>(n, (int64_t)blocks_per_sm(threads_for(D, cols_of(D))) * device_sm_count());
 }
 
-template <typename T, int E, int NV>
-cudaError_t fwd(const LnArgs& a, cudaStream_t st) {
+template <typename T, int E, int C, int THREADS, int MIN_BLOCKS>
+cudaError_t fwd(const LnArgs& a, int threads, cudaStream_t st) {
   count_launches(1);
-  const int threads = threads_for(a.D, E * NV);
-  const unsigned grid = (unsigned)std::min<int64_t>(a.n, 1 << 20);
-  if (threads <= 128)
-    ln_fwd<T, E, NV, 128><<<grid, threads, 0, st>>>(a);
-  else if (threads <= 512)
-    ln_fwd<T, E, NV, 512><<<grid, threads, 0, st>>>(a);
-  else
-    ln_fwd<T, E, NV, 1024><<<grid, threads, 0, st>>>(a);
+  const int64_t most = (int64_t)(2 * blocks_per_sm(threads)) * device_sm_count();
+  ln_fwd<T, E, C, THREADS, MIN_BLOCKS><<<(unsigned)std::min<int64_t>(a.n, most), threads, 0, st>>>(a);
   return cudaGetLastError();
+}
+template <typename T, int E>
+cudaError_t fwd_width(const LnArgs& a, cudaStream_t st) {
+  const int threads = threads_for(a.D, cols_of(a.D));
+  if (cols_of(a.D) == 8) return fwd<T, E, 8, 256, 4>(a, threads, st);
+  if (threads <= 256) return fwd<T, E, 16, 256, 3>(a, threads, st);
+  return threads <= 512 ? fwd<T, E, 16, 512, 1>(a, threads, st) : fwd<T, E, 16, 1024, 1>(a, threads, st);
 }
 template <typename T>
 cudaError_t fwd_any(const LnArgs& a, cudaStream_t st) {
   constexpr int E = 16 / sizeof(T);
-  if (a.D % E == 0 && on16(a.x) && on16(a.out)) return fwd<T, E, 4>(a, st);
-  return fwd<T, 1, 16>(a, st);
+  return a.D % E == 0 && on16(a.x) && on16(a.out) ? fwd_width<T, E>(a, st) : fwd_width<T, 1>(a, st);
 }
 
-template <typename T, int E, int NV, bool WIDE, int AHEAD, int THREADS>
-cudaError_t bwd(const LnArgs& a, int blocks, cudaStream_t st) {
-  const int threads = threads_for(a.D, E * NV);
+template <typename T, int E, int C, int THREADS, int MIN_BLOCKS, bool SHARED>
+cudaError_t bwd(const LnArgs& a, int threads, int blocks, cudaStream_t st) {
   size_t smem = 0;
-  if constexpr (WIDE) {
+  if constexpr (SHARED) {
     static size_t set[kMaxDevices] = {};
     const cudaError_t e =
-        set_smem_limit((const void*)ln_bwd<T, E, NV, WIDE, AHEAD, THREADS>, (size_t)2 * E * NV * THREADS * 4, set);
+        set_smem_limit((const void*)ln_bwd<T, E, C, THREADS, MIN_BLOCKS, SHARED>, (size_t)C * THREADS * 8, set);
     if (e != cudaSuccess) return e;
-    smem = (size_t)2 * E * NV * threads * 4;
+    smem = (size_t)C * threads * 8;
   }
   count_launches(1);
-  ln_bwd<T, E, NV, WIDE, AHEAD, THREADS><<<(unsigned)blocks, threads, smem, st>>>(a);
+  ln_bwd<T, E, C, THREADS, MIN_BLOCKS, SHARED><<<(unsigned)blocks, threads, smem, st>>>(a);
   return cudaGetLastError();
 }
 template <typename T, int E>
 cudaError_t bwd_width(const LnArgs& a, int blocks, cudaStream_t st) {
-  if (bwd_cols(a.D) == kCols) return bwd<T, E, kCols / E, false, sizeof(T) == 2 ? 3 : 2, 512>(a, blocks, st);
-  if (a.D <= 512 * 2 * kCols) return bwd<T, E, 2 * kCols / E, true, 1, 512>(a, blocks, st);
-  return bwd<T, E, 2 * kCols / E, true, 1, 1024>(a, blocks, st);
+  const int threads = threads_for(a.D, cols_of(a.D));
+  if (cols_of(a.D) == 8) return bwd<T, E, 8, 256, 2, false>(a, threads, blocks, st);
+  if (threads <= 256) return bwd<T, E, 16, 256, 2, false>(a, threads, blocks, st);
+  if (threads <= 512) return bwd<T, E, 16, 512, 1, true>(a, threads, blocks, st);
+  return bwd<T, E, 16, 1024, 1, true>(a, threads, blocks, st);
 }
 template <typename T>
 cudaError_t bwd_any(const LnArgs& a, cudaStream_t st) {
