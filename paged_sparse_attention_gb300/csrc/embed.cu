@@ -7,8 +7,11 @@
 //
 // Backward: rows of one token are summed by one owner in row order, so there are no float
 // atomics and the gradient is the same bits on every run.  Three or four launches:
-//   sort_tokens   the stable order of the tokens, a section of up to 8192 rows a block: a radix sort
-//                 of 6 bits a pass in shared memory, whose passes are barriers instead of launches.
+//   rank_tokens   the stable order of up to kSection tokens: a token's place is the number of those
+//                 that come before it, counted by a warp's 32 tokens against all.  67 million
+//                 comparisons for 8192, on every SM and without a pass that waits for another.
+//   sort_tokens   instead, for more: a section of kSection a block, by a radix sort of 6 bits a pass in
+//                 shared memory (20 us whatever the number: SRT_NOTE).
 //   merge_sections  where there are several sections: a key's rank among all keys is the sum of its
 //                 places in every section, found by binary search.
 //   sum_runs      the sorted rows in windows of kWindow.  The rows of one token in one window are a
@@ -25,12 +28,12 @@
 namespace oomb {
 namespace {
 
-constexpr int kSection = 8192;  // rows sorted by one block
+constexpr int kSection = 8192;  // rows whose order is found at once: 32 KB of tokens
+constexpr int kRankKeys = 32, kRankWarps = 16;  // of a block of rank_tokens: tokens, warps that share the comparisons
 constexpr int kSortThreads = 1024, kSortKeys = kSection / kSortThreads;
 constexpr int kDigit = 6;       // bits a pass
 constexpr int kWindow = 16;     // sorted rows a piece lies in
-constexpr int kBatch = 8;       // of them in registers at once
-constexpr int kHeavy = 32;      // windows a token goes back over to count as one of many pieces
+constexpr int kBatch = 4;       // of them in registers at once
 constexpr int kNone = INT_MAX;  // key of a row without a token: behind every other
 
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -110,6 +113,55 @@ __global__ void __launch_bounds__(256) embed_rows(const __grid_constant__ EmbedA
 }
 
 // ----------------------------------------------------------------- ordering
+// Tokens before the warp's own count when they are not greater, those behind when they are smaller:
+// equal tokens keep their order.
+__global__ void __launch_bounds__(32 * kRankWarps) rank_tokens(const __grid_constant__ EmbedArgs a) {
+  __shared__ __align__(16) int keys[kSection];
+  __shared__ int parts[kRankWarps][kRankKeys];
+  constexpr int T = 32 * kRankWarps, K = kSection / T;
+  let_next_launch();
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.n_long[0] = a.n_long[1] = 0;
+  const int m = (int)a.n, own = blockIdx.x * kRankKeys, m4 = (m + 3) & ~3;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int64_t token[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) token[k] = threadIdx.x + k * T < m ? a.tokens[threadIdx.x + k * T] : -1;
+#pragma unroll
+  for (int k = 0; k < K; ++k) keys[threadIdx.x + k * T] = key_of(token[k], a.V, a.err);
+  __syncthreads();
+  const int mine = keys[own + lane];  // (own + lane < kSection; behind the last it is kNone and not used)
+  // x < y as the sign of x - y: both lie in [0, 2^31)
+  auto below = [](int x, int y) { return (unsigned)(x - y) >> 31; };
+  unsigned c0 = 0, c1 = 0, c2 = 0, c3 = 0;
+  const int4* v = reinterpret_cast<const int4*>(keys);
+#pragma unroll 4
+  for (int j = warp; j < own / 4; j += kRankWarps) {  // not greater: all but those above
+    const int4 x = v[j];
+    c0 += 1 - below(mine, x.x);
+    c1 += 1 - below(mine, x.y);
+    c2 += 1 - below(mine, x.z);
+    c3 += 1 - below(mine, x.w);
+  }
+  for (int j = own + warp; j < min(own + kRankKeys, m); j += kRankWarps)
+    c0 += keys[j] < mine || (keys[j] == mine && j < own + lane);
+#pragma unroll 4
+  for (int j = (own + kRankKeys) / 4 + warp; j < m4 / 4; j += kRankWarps) {
+    const int4 x = v[j];
+    c0 += below(x.x, mine);
+    c1 += below(x.y, mine);
+    c2 += below(x.z, mine);
+    c3 += below(x.w, mine);
+  }
+  parts[warp][lane] = (int)((c0 + c1) + (c2 + c3));
+  __syncthreads();
+  if (warp != 0 || own + lane >= m) return;
+  int at = 0;
+#pragma unroll
+  for (int p = 0; p < kRankWarps; ++p) at += parts[p][lane];
+  a.sorted[at] = mine;
+  a.order[at] = own + lane;
+}
+
 // One block a section.  Keys and their rows stand in shared memory in the order reached; in a pass a
 // warp takes 256 of them in turn, 32 at a time, and counts its digits, equal digits among the 32 by
 // ballots, so that equal keys keep their order.
@@ -214,13 +266,12 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens(const __grid_cons
     }
     __syncthreads();
   }
-  const bool one = a.n <= kSection;
 #pragma unroll
   for (int k = 0; k < kSortKeys; ++k) {
     const int j = place(k);
     if (j >= m) continue;
-    (one ? a.sorted : a.sec_sorted)[first + j] = key[k] == a.V ? kNone : key[k];
-    (one ? a.order : a.sec_order)[first + j] = (int)first + row[k];
+    a.sec_sorted[first + j] = key[k] == a.V ? kNone : key[k];
+    a.sec_order[first + j] = (int)first + row[k];
   }
 }
 
@@ -265,24 +316,11 @@ __global__ void __launch_bounds__(128) merge_sections(const __grid_constant__ Em
 // starts the window), one more may go on into the next.
 __device__ __forceinline__ size_t piece_slot(int64_t w, bool first) { return (size_t)w * 2 + (first ? 1 : 0); }
 
-// Adds to what is there without waiting for it: every element has one writer in a launch.
-template <int E>
-__device__ __forceinline__ void add_e(float* p, const float (&f)[E]) {
-  if constexpr (E == 1) {
-    asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(f[0]) : "memory");
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; i += 4)
-      asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + i), "f"(f[i]), "f"(f[i + 1]), "f"(f[i + 2]),
-                   "f"(f[i + 3])
-                   : "memory");
-  }
-}
-
 // NV vectors of E elements a thread.  A block walks the windows b, b + grid, ...; the next window's
 // tokens are on their way while this one's rows are summed.  A batch's rows are all asked for before
-// the first is used, held as they are stored, and the rows of the gradient that they will be added to
-// are asked into L2, where the additions are done.
+// the first is used, held as they are stored.  Rows of the gradient that will be added to are asked
+// into L2 at a window's start and from there one piece ahead.  (Additions in L2 instead, which wait for
+// nothing, are an element an operation there: 38 us against NOTE_SUM for 8192 tokens of 3584.)
 template <typename T, int E, int NV>
 __global__ void __launch_bounds__(512, 2) sum_runs(const __grid_constant__ EmbedArgs a) {
   constexpr int R = kBatch;
@@ -320,11 +358,22 @@ __global__ void __launch_bounds__(512, 2) sum_runs(const __grid_constant__ Embed
       if (key != kNone && key != keys[threadIdx.x])
         prefetch_l2(a.d_table + (size_t)key * a.D + slab, (uint32_t)min(width, a.D - slab) * 4);
     }
-    if (c0 >= a.D) continue;
     int live = 0;  // rows that have a token
     while (live < kWindow && keys[live + 1] != kNone) ++live;
-    float sum[NV][E];
+    float sum[NV][E], old[NV][E], ahead[NV][E];
     bool first = false;  // the piece being summed is its token's first
+    // what the gradient's row holds, for a piece that starts at row j and may be its token's only one
+    auto ask_old = [&](int j) {
+      const int key = keys[j + 1];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) ahead[v][e] = 0.f;
+        if (j < live && a.accumulate && key != keys[j] && c0 + v * step < a.D)
+          load_e<float, E>(a.d_table + (size_t)key * a.D + c0 + v * step, ahead[v]);
+      }
+    };
+    ask_old(0);
     for (int j0 = 0; j0 < live; j0 += R) {
       Word raw[R][NV];
 #pragma unroll
@@ -343,30 +392,37 @@ __global__ void __launch_bounds__(512, 2) sum_runs(const __grid_constant__ Embed
 #pragma unroll
           for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int e = 0; e < E; ++e) sum[v][e] = 0.f;
+            for (int e = 0; e < E; ++e) {
+              sum[v][e] = 0.f;
+              old[v][e] = ahead[v][e];
+            }
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v)
           if (c0 + v * step < a.D) add_word(sum[v], raw[u][v]);
         const bool last = keys[j + 2] != key;
         if (!last && j + 1 < kWindow) continue;
-        float* to = first && last ? a.d_table + (size_t)key * a.D : a.part + piece_slot(window, first) * a.pitch;
-        const float by = first && last ? a.scale : 1.f;
+        if (j + 1 < kWindow) ask_old(j + 1);
+        const bool only = first && last;
+        float* to = only ? a.d_table + (size_t)key * a.D : a.part + piece_slot(window, first) * a.pitch;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           if (c0 + v * step >= a.D) continue;
 #pragma unroll
-          for (int e = 0; e < E; ++e) sum[v][e] *= by;
-          if (first && last && a.accumulate)
-            add_e<E>(to + c0 + v * step, sum[v]);
-          else
-            store_e<float, E>(to + c0 + v * step, sum[v]);
+          for (int e = 0; e < E; ++e) sum[v][e] = only ? fmaf(a.scale, sum[v][e], old[v][e]) : sum[v][e];
+          store_e<float, E>(to + c0 + v * step, sum[v]);
         }
-        // the token's last piece tells the join about it (in any order: each has a row of its own)
-        if (last && !first && blockIdx.y == 0 && threadIdx.x == 0) {
-          const bool heavy = window >= kHeavy && a.sorted[(window - kHeavy) * kWindow] == key;
-          const int at = heavy ? (int)a.windows - 1 - atomicAdd(a.n_long + 1, 1) : atomicAdd(a.n_long, 1);
-          a.long_runs[at] = make_int2(key, (int)window);
+        // the token's last piece tells the join about it (in any order: each has a row of its own), with its
+        // first window, the last one whose first row does not go on with it, if that is one of the last 32
+        if (last && !first && blockIdx.y == 0 && threadIdx.x < 32) {
+          const int64_t w = window - (int)threadIdx.x;
+          const unsigned stops = __ballot_sync(0xffffffffu, w <= 0 || a.sorted[max(w, (int64_t)1) * kWindow - 1] != key);
+          if (threadIdx.x == 0) {
+            if (stops)
+              a.long_runs[atomicAdd(a.n_long, 1)] = make_int4(key, (int)window - (__ffs(stops) - 1), (int)window, 0);
+            else
+              a.long_runs[a.windows - 1 - atomicAdd(a.n_long + 1, 1)] = make_int4(key, 0, (int)window, 0);
+          }
         }
       }
     }
@@ -374,7 +430,7 @@ __global__ void __launch_bounds__(512, 2) sum_runs(const __grid_constant__ Embed
 }
 
 // Joins the tokens whose rows lie in several windows.  Most have a few pieces: a warp takes 128 columns
-// of one.  Those with kHeavy or more, which a common token has in a long batch, are taken by whole
+// of one.  Those with more than 32, which a common token has in a long batch, are taken by whole
 // blocks, the warps each a share of the pieces, whose sums are added in order.
 constexpr int kJoinCols = 128, kJoinWarps = 16;
 __global__ void __launch_bounds__(32 * kJoinWarps) join_pieces(const __grid_constant__ EmbedArgs a) {
@@ -382,16 +438,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_pieces(const __grid_cons
   wait_for_launch_before();
   const int chunks = (a.D + kJoinCols - 1) / kJoinCols;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  // first window of a run that ends in window w: the last one whose first row does not go on with the
-  // run.  Among the last 32, else by a search that cuts the rest in 32 at a step.
+  // first window of a run that goes back from window w by more than 32: a search that cuts in 33 at a step
   auto first_window = [&](int key, int w) {
-    auto goes_back = [&](int x) { return x > 0 && a.sorted[(int64_t)x * kWindow - 1] == key; };
-    const unsigned stops = __ballot_sync(0xffffffffu, !goes_back(w - lane));
-    if (stops) return w - (__ffs(stops) - 1);
-    int lo = 0, hi = w - 31;  // lo does not go back, hi does
+    int lo = 0, hi = w - 31;  // the first row of window hi goes on with the run, that of lo does not
     while (hi - lo > 1) {
       const int x = lo + (int)((int64_t)(hi - lo) * (lane + 1) / 33);
-      const unsigned back = __ballot_sync(0xffffffffu, goes_back(x));  // lanes from some one on
+      const bool goes_back = x > 0 && a.sorted[(int64_t)x * kWindow - 1] == key;
+      const unsigned back = __ballot_sync(0xffffffffu, goes_back);  // lanes from some one on
       const int from = back ? __ffs(back) - 1 : 32;
       const int low = __shfl_sync(0xffffffffu, x, max(from - 1, 0)), high = __shfl_sync(0xffffffffu, x, min(from, 31));
       if (from > 0) lo = max(lo, low);
@@ -422,9 +475,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_pieces(const __grid_cons
   };
   const int64_t heavy = (int64_t)a.n_long[1] * chunks, light = (int64_t)a.n_long[0] * chunks;
   for (int64_t it = blockIdx.x; it < heavy; it += gridDim.x) {
-    const int2 run = a.long_runs[a.windows - 1 - it / chunks];
+    const int4 run = a.long_runs[a.windows - 1 - it / chunks];
     const int c = (int)(it % chunks) * kJoinCols + 4 * lane;
-    const int begin = first_window(run.x, run.y), pieces = run.y - begin + 1, per = (pieces + kJoinWarps - 1) / kJoinWarps;
+    const int begin = first_window(run.x, run.z), pieces = run.z - begin + 1, per = (pieces + kJoinWarps - 1) / kJoinWarps;
     float4 sum = sum_of(begin, warp * per, min(pieces, (warp + 1) * per), c);
     share[warp][lane] = sum;
     __syncthreads();
@@ -442,10 +495,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_pieces(const __grid_cons
     __syncthreads();
   }
   for (int64_t it = (int64_t)blockIdx.x * kJoinWarps + warp; it < light; it += (int64_t)gridDim.x * kJoinWarps) {
-    const int2 run = a.long_runs[it / chunks];
+    const int4 run = a.long_runs[it / chunks];
     const int c = (int)(it % chunks) * kJoinCols + 4 * lane;
-    const int begin = first_window(run.x, run.y);
-    write(run.x, c, sum_of(begin, 0, run.y - begin + 1, c));
+    write(run.x, c, sum_of(run.y, 0, run.z - run.y + 1, c));
   }
 }
 
@@ -482,10 +534,15 @@ size_t sort_smem_set[kMaxDevices] = {};
 template <typename T, int E, int NV>
 cudaError_t backward(const EmbedArgs& a, cudaStream_t st) {
   const unsigned sections = (unsigned)((a.n + kSection - 1) / kSection);
-  cudaError_t e = set_smem_limit((const void*)sort_tokens, sizeof(SortSpace), sort_smem_set);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
   count_launches(1);
-  sort_tokens<<<sections, kSortThreads, sizeof(SortSpace), st>>>(a);
+  if (sections == 1) {
+    rank_tokens<<<(unsigned)((a.n + kRankKeys - 1) / kRankKeys), 32 * kRankWarps, 0, st>>>(a);
+  } else {
+    e = set_smem_limit((const void*)sort_tokens, sizeof(SortSpace), sort_smem_set);
+    if (e != cudaSuccess) return e;
+    sort_tokens<<<sections, kSortThreads, sizeof(SortSpace), st>>>(a);
+  }
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (sections > 1) {
@@ -502,7 +559,7 @@ cudaError_t backward(const EmbedArgs& a, cudaStream_t st) {
   if (e != cudaSuccess || a.n <= kWindow) return e;
   // at most a run goes on from each window into the next
   const int64_t items = ((a.n - 1) / kWindow) * ((a.D + kJoinCols - 1) / kJoinCols);
-  return launch_after(join_pieces, dim3((unsigned)std::min<int64_t>((items + kJoinWarps - 1) / kJoinWarps, 4 * device_sm_count())),
+  return launch_after(join_pieces, dim3((unsigned)std::min<int64_t>((items + kJoinWarps - 1) / kJoinWarps, 3 * device_sm_count())),
                       32 * kJoinWarps, a, st);
 }
 
@@ -536,7 +593,7 @@ EmbedSpace embed_space(int64_t n, int D) {
   s.sec_sorted = take(n > kSection ? (size_t)n * 4 : 0);
   s.n_long = take(8);
   const size_t windows = (size_t)(n + kWindow - 1) / kWindow;
-  s.long_runs = take(windows * 8);
+  s.long_runs = take(windows * 16);
   s.pitch = (int64_t)align_up((size_t)D, 4);
   s.part = take(n > kWindow ? windows * 2 * s.pitch * 4 : 0);
   s.bytes = at;
@@ -609,7 +666,7 @@ oomb_status oomb_embed_bwd(const int64_t* tokens, int n, const void* d_out, int 
   a.key_bits = 1;
   while (a.key_bits < 31 && (V >> a.key_bits) != 0) ++a.key_bits;
   a.n_long = reinterpret_cast<int*>(base + w.n_long);
-  a.long_runs = reinterpret_cast<int2*>(base + w.long_runs);
+  a.long_runs = reinterpret_cast<int4*>(base + w.long_runs);
   a.part = reinterpret_cast<float*>(base + w.part);
   a.pitch = w.pitch;
   a.windows = (n + kWindow - 1) / kWindow;

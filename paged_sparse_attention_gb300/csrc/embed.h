@@ -26,7 +26,7 @@ struct EmbedArgs {
   int* sec_sorted;
   int64_t windows;        // of sorted rows
   int* n_long;            // [2] tokens whose rows lie in several windows, in a few and in many
-  int2* long_runs;        // [windows] each: the token and its last window; those in many from the end
+  int4* long_runs;        // [windows] each: the token, its first and last window; those in many from the end
   float* part;            // sums of their pieces
   int64_t pitch;
 };

@@ -236,12 +236,8 @@ __global__ void __launch_bounds__(256) join_lse(const __grid_constant__ GemmArgs
       m = to;
     }
     if (lane == 0) {
-      // the target's logit z and the rest: a sure row's loss is small and keeps its own precision
-      const float z = a.at[r], rest = (m + log2f(s)) * tc::kLn2;
-      const float l = z >= rest ? log1pf(s * exp2f(m - z * tc::kLog2e)) : (rest - z) + log1pf(expf(z - rest));
       const int row = a.rows[r];
-      loss[row] = l;
-      lse[row] = z >= rest ? z + l : rest + log1pf(expf(z - rest));
+      loss_of(a.at[r], m, s, loss[row], lse[row]);
     }
   }
 }
@@ -527,6 +523,29 @@ GemmArgs arguments(const void* x, const int64_t* targets, int n, int D, int V, i
   return g;
 }
 
+SmallArgs small_arguments(const void* x, const void* w, const int64_t* targets, int n, int D, int V, float cap,
+                          bool backward, char* ws, uint32_t* err) {
+  SmallSpace s = {};
+  small_space(n, D, V, backward, &s);
+  SmallArgs a = {};
+  a.x = x;
+  a.w = w;
+  a.targets = targets;
+  a.n = n;
+  a.D = D;
+  a.V = V;
+  a.cap = cap;
+  a.err = err;
+  a.part = reinterpret_cast<float2*>(ws + s.part);
+  a.parts = s.parts;
+  a.at = reinterpret_cast<float*>(ws + s.at);
+  a.dz = reinterpret_cast<float*>(ws + s.dz);
+  a.pitch = s.pitch;
+  a.acc = reinterpret_cast<float*>(ws + s.acc);
+  a.acc_pitch = s.acc_pitch;
+  return a;
+}
+
 oomb_status check(const void* x, const void* w, const int64_t* targets, int n, int D, int V, int dtype, float cap,
                   const void* lse, const void* ws, const uint32_t* word) {
   if (!x || !w || !targets || !lse || !word || n <= 0 || D <= 0 || V <= 0 || V > INT_MAX - 1024) return OOMB_ERR_ARG;
@@ -552,7 +571,11 @@ extern "C" {
 
 size_t oomb_head_loss_workspace(int n, int D, int V, int dtype, int backward) {
   if (n <= 0 || D <= 0 || D > kMaxWidth || V <= 0 || V > INT_MAX - 1024 || (dtype != OOMB_BF16 && dtype != OOMB_FP32)) return 0;
-  return make_plan(n, D, V, dtype, backward != 0, true).bytes;
+  // grows with n: fewer rows may go either way
+  SmallSpace s;
+  const int few = std::min(n, small_rows(D, V));
+  return std::max(make_plan(n, D, V, dtype, backward != 0, true).bytes,
+                  few > 0 ? small_space(few, D, V, backward != 0, &s) : 0);
 }
 
 oomb_status oomb_head_loss_fwd(const void* x, const void* w, const int64_t* targets, int n, int D, int V, int dtype,
@@ -562,9 +585,15 @@ oomb_status oomb_head_loss_fwd(const void* x, const void* w, const int64_t* targ
   if (s != OOMB_OK) return s;
   if (!loss) return OOMB_ERR_ARG;
   if (reinterpret_cast<uintptr_t>(loss) % 4) return OOMB_ERR_ALIGN;
-  const Plan pl = make_plan(n, D, V, dtype, false, on16(w));
-  if (!workspace || ws_bytes < pl.bytes) return OOMB_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < oomb_head_loss_workspace(n, D, V, dtype, 0)) return OOMB_ERR_WORKSPACE;
   char* ws = reinterpret_cast<char*>(workspace);
+  if (n <= small_rows(D, V)) {
+    SmallArgs a = small_arguments(x, w, targets, n, D, V, softcap, false, ws, error_word);
+    a.loss = loss;
+    a.lse = lse;
+    return cuda_status(launch_small_fwd(a, dtype, (cudaStream_t)stream));
+  }
+  const Plan pl = make_plan(n, D, V, dtype, false, on16(w));
   GatherArgs st;
   GemmArgs g = arguments(x, targets, n, D, V, dtype, softcap, pl, ws, error_word, &st);
   st.loss = loss;
@@ -590,9 +619,19 @@ oomb_status oomb_head_loss_bwd(const void* x, const void* w, const int64_t* targ
   if (reinterpret_cast<uintptr_t>(dx) % dtype_size(dtype) || reinterpret_cast<uintptr_t>(d_loss) % 4 ||
       (dw && reinterpret_cast<uintptr_t>(dw) % dtype_size(dw_dtype)))
     return OOMB_ERR_ALIGN;
-  const Plan pl = make_plan(n, D, V, dtype, true, on16(w));
-  if (!workspace || ws_bytes < pl.bytes) return OOMB_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < oomb_head_loss_workspace(n, D, V, dtype, 1)) return OOMB_ERR_WORKSPACE;
   char* ws = reinterpret_cast<char*>(workspace);
+  if (n <= small_rows(D, V)) {
+    SmallArgs a = small_arguments(x, w, targets, n, D, V, softcap, true, ws, error_word);
+    a.scale = scale;
+    a.lse_in = lse;
+    a.d_loss = d_loss;
+    a.dx = dx;
+    a.dw = dw;
+    a.accumulate = accumulate != 0;
+    return cuda_status(launch_small_bwd(a, dtype, dw_dtype, (cudaStream_t)stream));
+  }
+  const Plan pl = make_plan(n, D, V, dtype, true, on16(w));
   GatherArgs st;
   GemmArgs g = arguments(x, targets, n, D, V, dtype, softcap, pl, ws, error_word, &st);
   st.dx = dx;

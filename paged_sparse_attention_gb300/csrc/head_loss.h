@@ -1,6 +1,7 @@
 // Arguments of the kernels of the loss over a vocabulary (head_loss.cu, head_gemm.cuh).
 #pragma once
 #include <cuda_bf16.h>
+#include <cuda_runtime.h>
 
 #include <cstddef>
 #include <cstdint>
@@ -41,6 +42,61 @@ struct GemmArgs {
   float scale;
   uint32_t* err;
 };
+
+// ---- few rows and small problems (head_small.cu)
+constexpr int kFewRows = 8;                  // rows that always take it
+constexpr int64_t kSmallWork = 1 << 26;      // products n V D up to which more rows do
+constexpr int kMaxRows = 4096;
+
+struct SmallArgs {
+  const void* x;
+  const void* w;
+  const int64_t* targets;
+  int n, D, V;
+  float cap, scale;
+  uint32_t* err;
+  float* loss;         // forward
+  float* lse;
+  float2* part;        // [n, parts]
+  int parts;
+  float* at;           // [n] logit of the target
+  const float* lse_in; // backward
+  const float* d_loss;
+  float* dz;           // [n, pitch]
+  int pitch;
+  float* acc;          // [units, n, acc_pitch] parts of dx
+  int acc_pitch;
+  void* dx;
+  void* dw;
+  int accumulate, dw_vec;
+  int ct, row_groups;
+};
+struct SmallSpace {
+  size_t at, part, dz, acc;
+  int parts, pitch, acc_pitch;
+};
+// Rows up to which a problem goes this way (0: none do).
+int small_rows(int D, int V);
+// Bytes of workspace, and what lies where.
+size_t small_space(int n, int D, int V, bool backward, SmallSpace* s);
+cudaError_t launch_small_fwd(const SmallArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_small_bwd(const SmallArgs& a, int dtype, int dw_dtype, cudaStream_t st);
+
+#ifdef __CUDACC__
+// Loss and log-sum-exp of a row from its target's logit z and the sum s 2^m of the other exponentials.
+// A sure row's loss is small and keeps its own precision.
+__device__ __forceinline__ void loss_of(float z, float m, float s, float& loss, float& lse) {
+  const float rest = (m + log2f(s)) * 0.6931471805599453f;
+  if (z >= rest) {
+    loss = log1pf(s * exp2f(m - z * 1.4426950408889634f));
+    lse = z + loss;
+  } else {
+    const float more = log1pf(expf(z - rest));
+    loss = (rest - z) + more;
+    lse = rest + more;
+  }
+}
+#endif
 
 }  // namespace head
 }  // namespace oomb
