@@ -444,11 +444,32 @@ def _word(func: str, t, dev: int) -> int:
     import torch
     if t is None:
         raise ValueError(f"{func}: error_word is missing")
-    if t.dtype not in (torch.int32, torch.uint32):
+    if t.dtype is not torch.int32 and t.dtype is not torch.uint32:
         raise TypeError(f"{func}: error_word has to be 32-bit integers, not {t.dtype}")
     if t.numel() < 1:
         raise ValueError(f"{func}: error_word is empty")
+    if t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     return _need(func, "error_word", t, t.shape, t.dtype, dev)
+
+
+def _lead(func: str, name: str, t, n: int, dev: int):
+    """Shape and address of a tensor that sets the sizes the others are checked against."""
+    if t is None or len(shape := t.shape) != n:
+        raise ValueError(f"{func}: {name} has to have {n} dimensions")
+    if t.get_device() == dev and t.is_contiguous():
+        return shape, t.data_ptr()
+    return shape, _need(func, name, t, shape, t.dtype, dev)
+
+
+def _code(torch, t) -> int:
+    return OOMB_BF16 if t.dtype is torch.bfloat16 else OOMB_FP32 if t.dtype is torch.float32 else _dtype_code(t)
+
+
+def _on(torch, stream, dev: int):
+    """Raw stream of a call on device ``dev``."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) if stream is None else None
+    return _stream(stream) if raw is None else raw(dev)
 
 
 def oomb_embed_fwd(tokens, table, out, error_word, scale: float = 1.0, stream=None) -> None:
@@ -456,12 +477,11 @@ def oomb_embed_fwd(tokens, table, out, error_word, scale: float = 1.0, stream=No
     import torch
     f, dev = "oomb_embed_fwd", torch.cuda.current_device()
     n = _dims(f, "tokens", tokens, 1)[0]
-    V, D = _dims(f, "table", table, 2)
-    code = _dtype_code(table)
-    _ok(f, load().oomb_embed_fwd(_need(f, "tokens", tokens, (n,), torch.int64, dev), n,
-                                 _need(f, "table", table, (V, D), table.dtype, dev), V, D, code, scale,
-                                 _need(f, "out", out, (n, D), table.dtype, dev), _word(f, error_word, dev),
-                                 _stream(stream)))
+    code = _code(torch, table)
+    at = _need(f, "tokens", tokens, (n,), torch.int64, dev)
+    (V, D), atab = _lead(f, "table", table, 2, dev)
+    _ok(f, load().oomb_embed_fwd(at, n, atab, V, D, code, scale, _need(f, "out", out, (n, D), table.dtype, dev),
+                                 _word(f, error_word, dev), _on(torch, stream, dev)))
 
 
 def oomb_embed_bwd(tokens, d_out, d_table, workspace, error_word, scale: float = 1.0, accumulate: bool = False,
@@ -471,12 +491,11 @@ def oomb_embed_bwd(tokens, d_out, d_table, workspace, error_word, scale: float =
     f, dev = "oomb_embed_bwd", torch.cuda.current_device()
     n = _dims(f, "tokens", tokens, 1)[0]
     V, D = _dims(f, "d_table", d_table, 2)
-    code = _dtype_code(d_out)
     ws, ws_bytes = _scratch(f, workspace, dev)
     _ok(f, load().oomb_embed_bwd(_need(f, "tokens", tokens, (n,), torch.int64, dev), n,
-                                 _need(f, "d_out", d_out, (n, D), d_out.dtype, dev), V, D, code, scale,
+                                 _need(f, "d_out", d_out, (n, D), d_out.dtype, dev), V, D, _code(torch, d_out), scale,
                                  _need(f, "d_table", d_table, (V, D), torch.float32, dev), int(accumulate), ws, ws_bytes,
-                                 _word(f, error_word, dev), _stream(stream)))
+                                 _word(f, error_word, dev), _on(torch, stream, dev)))
 
 
 def oomb_embed_workspace(n: int, D: int) -> int:
@@ -487,11 +506,12 @@ def oomb_layer_norm_fwd(x, w, b, out, eps: float = 1e-5, mean=None, rstd=None, s
     """out = (x - mean) * rstd * w + b over the rows of x [n, D]; w and b fp32 [D] or None."""
     import torch
     f, dev, f32 = "oomb_layer_norm_fwd", torch.cuda.current_device(), torch.float32
-    n, D = _dims(f, "x", x, 2)
-    _ok(f, load().oomb_layer_norm_fwd(_need(f, "x", x, (n, D), x.dtype, dev), _opt(f, "w", w, (D,), f32, dev),
-                                      _opt(f, "b", b, (D,), f32, dev), eps, n, D, _dtype_code(x),
-                                      _need(f, "out", out, (n, D), x.dtype, dev), _opt(f, "mean", mean, (n,), f32, dev),
-                                      _opt(f, "rstd", rstd, (n,), f32, dev), _stream(stream)))
+    shape, ax = _lead(f, "x", x, 2, dev)
+    n, D = shape
+    _ok(f, load().oomb_layer_norm_fwd(ax, _opt(f, "w", w, (D,), f32, dev), _opt(f, "b", b, (D,), f32, dev), eps, n, D,
+                                      _code(torch, x), _need(f, "out", out, shape, x.dtype, dev),
+                                      _opt(f, "mean", mean, (n,), f32, dev), _opt(f, "rstd", rstd, (n,), f32, dev),
+                                      _on(torch, stream, dev)))
 
 
 def oomb_layer_norm_bwd(x, w, mean, rstd, dy, dx, dw=None, db=None, dx_out=None, accumulate: bool = False,
@@ -499,28 +519,29 @@ def oomb_layer_norm_bwd(x, w, mean, rstd, dy, dx, dw=None, db=None, dx_out=None,
     """The backward of oomb_layer_norm_fwd; accumulate adds the parameter gradients to their buffers."""
     import torch
     f, dev, f32 = "oomb_layer_norm_bwd", torch.cuda.current_device(), torch.float32
-    n, D = shape = _dims(f, "x", x, 2)
+    shape, ax = _lead(f, "x", x, 2, dev)
+    n, D = shape
     dt = x.dtype
     ws, ws_bytes = _scratch(f, workspace, dev)
-    _ok(f, load().oomb_layer_norm_bwd(_need(f, "x", x, shape, dt, dev), _opt(f, "w", w, (D,), f32, dev),
-                                      _need(f, "mean", mean, (n,), f32, dev), _need(f, "rstd", rstd, (n,), f32, dev),
-                                      _need(f, "dy", dy, shape, dt, dev), _opt(f, "dx_out", dx_out, shape, dt, dev),
-                                      n, D, _dtype_code(x), _need(f, "dx", dx, shape, dt, dev),
-                                      _opt(f, "dw", dw, (D,), f32, dev), _opt(f, "db", db, (D,), f32, dev),
-                                      int(accumulate), ws, ws_bytes, _stream(stream)))
+    _ok(f, load().oomb_layer_norm_bwd(ax, _opt(f, "w", w, (D,), f32, dev), _need(f, "mean", mean, (n,), f32, dev),
+                                      _need(f, "rstd", rstd, (n,), f32, dev), _need(f, "dy", dy, shape, dt, dev),
+                                      _opt(f, "dx_out", dx_out, shape, dt, dev), n, D, _code(torch, x),
+                                      _need(f, "dx", dx, shape, dt, dev), _opt(f, "dw", dw, (D,), f32, dev),
+                                      _opt(f, "db", db, (D,), f32, dev), int(accumulate), ws, ws_bytes,
+                                      _on(torch, stream, dev)))
 
 
 def oomb_layer_norm_workspace(n: int, D: int) -> int:
     return int(load().oomb_layer_norm_workspace(n, D))
 
 
-def _head_call(f: str, x, w, targets, dev: int):
+def _head_call(torch, f: str, x, w, targets, dev: int):
     """Checks the inputs common to both directions; (n, D, V, dtype code, addresses)."""
-    import torch
     n, D = _dims(f, "x", x, 2)
     V = _dims(f, "w", w, 2)[0]
-    return n, D, V, _dtype_code(x), (_need(f, "x", x, (n, D), x.dtype, dev), _need(f, "w", w, (V, D), x.dtype, dev),
-                                     _need(f, "targets", targets, (n,), torch.int64, dev))
+    code = _code(torch, x)
+    ax = _lead(f, "x", x, 2, dev)[1]
+    return n, D, V, code, (ax, _need(f, "w", w, (V, D), x.dtype, dev), _need(f, "targets", targets, (n,), torch.int64, dev))
 
 
 def oomb_head_loss_fwd(x, w, targets, loss, lse, workspace, error_word, softcap: float = 0.0, stream=None) -> None:
@@ -528,11 +549,11 @@ def oomb_head_loss_fwd(x, w, targets, loss, lse, workspace, error_word, softcap:
     a negative one is none: loss and lse are 0)."""
     import torch
     f, dev, f32 = "oomb_head_loss_fwd", torch.cuda.current_device(), torch.float32
-    n, D, V, code, (ax, aw, at) = _head_call(f, x, w, targets, dev)
+    n, D, V, code, (ax, aw, at) = _head_call(torch, f, x, w, targets, dev)
     ws, ws_bytes = _scratch(f, workspace, dev)
     _ok(f, load().oomb_head_loss_fwd(ax, aw, at, n, D, V, code, softcap, _need(f, "loss", loss, (n,), f32, dev),
                                      _need(f, "lse", lse, (n,), f32, dev), ws, ws_bytes, _word(f, error_word, dev),
-                                     _stream(stream)))
+                                     _on(torch, stream, dev)))
 
 
 def oomb_head_loss_bwd(x, w, targets, lse, dx, dw, workspace, error_word, d_loss=None, scale: float = 1.0,
@@ -541,14 +562,14 @@ def oomb_head_loss_bwd(x, w, targets, lse, dx, dw, workspace, error_word, d_loss
     gradient scale * d_loss[i] of loss[i] (d_loss fp32 [n]; None: 1)."""
     import torch
     f, dev, f32 = "oomb_head_loss_bwd", torch.cuda.current_device(), torch.float32
-    n, D, V, code, (ax, aw, at) = _head_call(f, x, w, targets, dev)
+    n, D, V, code, (ax, aw, at) = _head_call(torch, f, x, w, targets, dev)
     ws, ws_bytes = _scratch(f, workspace, dev)
-    dw_code = code if dw is None else _dtype_code(dw)
+    dw_code = code if dw is None else _code(torch, dw)
     _ok(f, load().oomb_head_loss_bwd(ax, aw, at, _need(f, "lse", lse, (n,), f32, dev),
                                      _opt(f, "d_loss", d_loss, (n,), f32, dev), scale, n, D, V, code, softcap,
                                      _opt(f, "dx", dx, (n, D), x.dtype, dev),
                                      None if dw is None else _need(f, "dw", dw, (V, D), dw.dtype, dev), dw_code,
-                                     int(accumulate), ws, ws_bytes, _word(f, error_word, dev), _stream(stream)))
+                                     int(accumulate), ws, ws_bytes, _word(f, error_word, dev), _on(torch, stream, dev)))
 
 
 def oomb_head_loss_workspace(n: int, D: int, V: int, dtype, backward: bool) -> int:

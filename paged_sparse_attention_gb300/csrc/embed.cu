@@ -33,7 +33,6 @@ constexpr int kRankKeys = 32, kRankWarps = 16;  // of a block of rank_tokens: to
 constexpr int kSortThreads = 1024, kSortKeys = kSection / kSortThreads;
 constexpr int kDigit = 6;       // bits a pass
 constexpr int kWindow = 16;     // sorted rows a piece lies in
-constexpr int kBatch = 4;       // of them in registers at once
 constexpr int kNone = INT_MAX;  // key of a row without a token: behind every other
 
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -323,7 +322,7 @@ __device__ __forceinline__ size_t piece_slot(int64_t w, bool first) { return (si
 // nothing, are an element an operation there: 38 us against NOTE_SUM for 8192 tokens of 3584.)
 template <typename T, int E, int NV>
 __global__ void __launch_bounds__(512, 2) sum_runs(const __grid_constant__ EmbedArgs a) {
-  constexpr int R = kBatch;
+  constexpr int R = 4;  // rows of a batch
   using Word = typename std::conditional<E == 1, T, uint4>::type;
   __shared__ int rows_of[2][kWindow], keys_of[2][kWindow + 2];  // keys[.][0]: of the row before the window
   wait_for_launch_before();
@@ -357,6 +356,13 @@ __global__ void __launch_bounds__(512, 2) sum_runs(const __grid_constant__ Embed
       const int key = keys[threadIdx.x + 1];
       if (key != kNone && key != keys[threadIdx.x])
         prefetch_l2(a.d_table + (size_t)key * a.D + slab, (uint32_t)min(width, a.D - slab) * 4);
+    } else if (E == 1 && a.accumulate) {  // rows off 16 bytes: line by line
+      for (int j = threadIdx.x / 32; j < kWindow; j += blockDim.x / 32) {
+        const int key = keys[j + 1];
+        if (key == kNone || key == keys[j]) continue;
+        for (int c = slab + threadIdx.x % 32 * 32; c < min(a.D, slab + width); c += 32 * 32)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(a.d_table + (size_t)key * a.D + c));
+      }
     }
     int live = 0;  // rows that have a token
     while (live < kWindow && keys[live + 1] != kNone) ++live;
@@ -373,7 +379,7 @@ __global__ void __launch_bounds__(512, 2) sum_runs(const __grid_constant__ Embed
           load_e<float, E>(a.d_table + (size_t)key * a.D + c0 + v * step, ahead[v]);
       }
     };
-    ask_old(0);
+    if (E > 1) ask_old(0);
     for (int j0 = 0; j0 < live; j0 += R) {
       Word raw[R][NV];
 #pragma unroll
@@ -394,7 +400,7 @@ __global__ void __launch_bounds__(512, 2) sum_runs(const __grid_constant__ Embed
 #pragma unroll
             for (int e = 0; e < E; ++e) {
               sum[v][e] = 0.f;
-              old[v][e] = ahead[v][e];
+              if (E > 1) old[v][e] = ahead[v][e];
             }
         }
 #pragma unroll
@@ -402,8 +408,11 @@ __global__ void __launch_bounds__(512, 2) sum_runs(const __grid_constant__ Embed
           if (c0 + v * step < a.D) add_word(sum[v], raw[u][v]);
         const bool last = keys[j + 2] != key;
         if (!last && j + 1 < kWindow) continue;
-        if (j + 1 < kWindow) ask_old(j + 1);
+        if (E > 1 && j + 1 < kWindow) ask_old(j + 1);
         const bool only = first && last;
+        if (E == 1 && only)
+#pragma unroll
+          for (int v = 0; v < NV; ++v) old[v][0] = a.accumulate && c0 + v * step < a.D ? a.d_table[(size_t)key * a.D + c0 + v * step] : 0.f;
         float* to = only ? a.d_table + (size_t)key * a.D : a.part + piece_slot(window, first) * a.pitch;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -454,24 +463,35 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_pieces(const __grid_cons
   };
   auto sum_of = [&](int begin, int from, int to, int c) {  // pieces [from, to) of the run
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < a.D) {
-#pragma unroll 8
-      for (int k = from; k < to; ++k) {
-        const float4 x = *reinterpret_cast<const float4*>(a.part + piece_slot(begin + k, k == 0) * a.pitch + c);
-        sum.x += x.x;
-        sum.y += x.y;
-        sum.z += x.z;
-        sum.w += x.w;
+    if (c >= a.D) return sum;
+    constexpr int B = 8;  // asked for together
+    for (int k = from; k < to; k += B) {
+      float4 x[B];
+#pragma unroll
+      for (int u = 0; u < B; ++u)
+        x[u] = k + u < to ? *reinterpret_cast<const float4*>(a.part + piece_slot(begin + k + u, k + u == 0) * a.pitch + c)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        sum.x += x[u].x;
+        sum.y += x[u].y;
+        sum.z += x[u].z;
+        sum.w += x[u].w;
       }
     }
     return sum;
   };
-  auto write = [&](int key, int c, const float4& sum) {
+  auto read = [&](int key, int c, float (&old)[4]) {
+    const float* from = a.d_table + (size_t)key * a.D + c;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) old[e] = a.accumulate && c + e < a.D ? from[e] : 0.f;
+  };
+  auto write = [&](int key, int c, const float4& sum, const float (&old)[4]) {
     const float f[4] = {sum.x, sum.y, sum.z, sum.w};
     float* to = a.d_table + (size_t)key * a.D + c;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (c + e < a.D) to[e] = fmaf(a.scale, f[e], a.accumulate ? to[e] : 0.f);
+      if (c + e < a.D) to[e] = fmaf(a.scale, f[e], old[e]);
   };
   const int64_t heavy = (int64_t)a.n_long[1] * chunks, light = (int64_t)a.n_long[0] * chunks;
   for (int64_t it = blockIdx.x; it < heavy; it += gridDim.x) {
@@ -490,14 +510,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_pieces(const __grid_cons
         sum.z += y.z;
         sum.w += y.w;
       }
-      write(run.x, c, sum);
+      float old[4];
+      read(run.x, c, old);
+      write(run.x, c, sum, old);
     }
     __syncthreads();
   }
   for (int64_t it = (int64_t)blockIdx.x * kJoinWarps + warp; it < light; it += (int64_t)gridDim.x * kJoinWarps) {
     const int4 run = a.long_runs[it / chunks];
     const int c = (int)(it % chunks) * kJoinCols + 4 * lane;
-    write(run.x, c, sum_of(run.y, 0, run.z - run.y + 1, c));
+    float old[4];
+    read(run.x, c, old);
+    write(run.x, c, sum_of(run.y, 0, run.z - run.y + 1, c), old);
   }
 }
 
