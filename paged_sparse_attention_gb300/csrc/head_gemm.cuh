@@ -14,7 +14,8 @@
 // columns' rows of B, so a CTA loads 32 KB for 64 steps of K instead of the 48 KB that a tile of
 // its own of the same shape would take; that is what keeps the loads below L2's rate.  Six stages
 // of a ring; two accumulators of 256 columns in tensor memory, so that a tile's epilogue (eight
-// warps, a thread a row) runs while the next tile's product does.  Persistent: a cluster takes
+// warps, a thread a row, whose results go through shared memory to be written in lines) runs while the
+// next tile's product does.  Persistent: a cluster takes
 // tiles c, c + clusters, ... in groups of kGroup row tiles, which share the columns' tiles in L2.
 #pragma once
 #include "head_loss.h"
@@ -26,15 +27,24 @@ namespace head {
 enum Mode { kLse = 0, kDz = 1, kDx = 2, kDw = 3 };
 
 constexpr int kTile = 256, kHalf = 128, kStep = 64;  // tile, a CTA's share of it, columns of K a stage
-constexpr int kStages = 6;
 constexpr uint32_t kOperand = kHalf * kStep * 2;     // 16 KB
-constexpr uint32_t kStageBytes = 2 * kOperand;
-constexpr uint32_t kSmem = kStages * kStageBytes + 1024;
 constexpr int kThreads = 320;                        // producer, issuer, 8 epilogue warps
 constexpr int kEpilogueWarps = 8;
+constexpr int kMaxStages = 9;
+// Tiles of TN columns: 256, or 64 where there are few tiles and a cluster's time is its loop over K.
+constexpr int kNarrow = 64;
+template <int TN>
+struct Shape {
+  static constexpr int half = TN / 2;                           // columns of an epilogue warp, rows of B a CTA loads
+  static constexpr uint32_t b_bytes = half * kStep * 2;
+  static constexpr uint32_t stage = kOperand + b_bytes;
+  static constexpr int stages = TN == 256 ? 6 : kMaxStages;
+  static constexpr uint32_t turn = kEpilogueWarps * 32 * 33 * 4;  // where the epilogue turns rows into lines
+  static constexpr uint32_t smem = stages * stage + turn + 1024;
+};
 
 struct Barriers {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t tile_full[2], tile_empty[2], done;
   uint32_t tmem;
   int abort;
@@ -125,11 +135,15 @@ struct RowSum {
 // cores cut a partial sum's last bits instead of rounding them, so a sum of K products loses up to
 // K / 16 halves of a unit in its last place, always towards zero: 6e-6 of a logit over K = 3584,
 // which a loss in fp32 would show, and 4e-7 over 256.  Not for sums that are rounded to bf16 anyway.
-template <int MODE, bool CHUNKED>
+template <int MODE, bool CHUNKED, int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     head_gemm(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
               const __grid_constant__ GemmArgs p) {
   constexpr bool kAmn = MODE == kDw, kBmn = MODE == kDx || MODE == kDw;
+  static_assert(TN == 256 || !kBmn, "a narrow tile's half of B is no whole swizzled row");
+  using S = Shape<TN>;
+  constexpr int kStages = S::stages, kCols = S::half;
+  constexpr uint32_t kStageBytes = S::stage;
   extern __shared__ uint8_t raw[];
   __shared__ Barriers bar;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -188,7 +202,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int tm, tn, k0, k1;
         place(t % (tms * p.tns), tms, p.tns, p.group, tm, tn);
         range(t, k0, k1);
-        const int ra = tm * kTile + (int)rank * kHalf, rb = tn * kTile + (int)rank * kHalf;
+        const int ra = tm * kTile + (int)rank * kHalf, rb = tn * TN + (int)rank * kCols;
         const int chunk = CHUNKED ? p.chunk : max(1, k1 - k0);
         for (int c0 = k0; ok && c0 < k1; c0 += chunk)
         for (int q = 0; ok && q < p.passes; ++q) {
@@ -232,7 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------------ products
     if (lane == 0 && rank == 0) {
-      const uint32_t idesc = idesc_bf16_f32(kTile, kTile, kAmn, kBmn);
+      const uint32_t idesc = idesc_bf16_f32(kTile, TN, kAmn, kBmn);
       int s = 0, n = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -276,9 +290,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------------ epilogue
-    const int half = (warp - 2) >> 2, r = (warp & 3) * 32 + lane;
-    const uint32_t tcol = tmem + tc::tmem_lane_base(warp) + half * kHalf;
+    const int half = (warp - 2) >> 2, r0 = (warp & 3) * 32;
+    const uint32_t tcol = tmem + tc::tmem_lane_base(warp) + half * kCols;
     const float inv_cap = p.cap > 0.f ? 1.f / p.cap : 0.f;
+    float* turn = reinterpret_cast<float*>(raw + (base - smem_u32(raw)) + kStages * kStageBytes) + (warp - 2) * 32 * 33;
     int n = 0;  // accumulators read
     bool ok = true;
     for (int t = first; t < tiles; t += clusters) {
@@ -286,8 +301,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       place(t % (tms * p.tns), tms, p.tns, p.group, tm, tn);
       range(t, k0, k1);
       const int split = t / (tms * p.tns);
-      const int row = tm * kTile + (int)rank * kHalf + r;
-      const int col0 = tn * kTile + half * kHalf;
+      const int row0 = tm * kTile + (int)rank * kHalf + r0, row = row0 + lane;
+      const int col0 = tn * TN + half * kCols;
       // what the row needs, on its way while the product runs
       int target = -1, out_row = 0;
       float lse2 = 0.f, g = 1.f;
@@ -316,8 +331,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i)
               if (col + i == target) z[i] = -INFINITY;
           sum.add(z, p.cols - col);
-        } else if constexpr (MODE == kDz) {
-          if (row >= p.n || col >= p.pitch) return;
+          return;
+        }
+        if constexpr (MODE == kDz) {
           // rows without a target and columns behind the last one are zeros
           const bool live = row < count;
 #pragma unroll
@@ -332,75 +348,102 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (col + i == target) q -= 1.f;
             z[i] = live && col + i < p.cols ? q * f : 0.f;
           }
+        }
+        // 32 rows of 32 columns, a row a lane, become lines: neighbouring lanes on neighbouring columns
+        const int n_rows = min(32, (MODE == kDz ? p.n : MODE == kDx ? count : p.cols) - row0);
+        const int n_cols = min(32, (MODE == kDz ? p.pitch : p.out_cols) - col);
+        __syncwarp();
 #pragma unroll
-          for (int part = 0; part < (CHUNKED ? 3 : 1); ++part) {
-            __nv_bfloat16* to = p.dz + ((size_t)part * p.n + row) * p.pitch + col;
-            uint32_t w[16];
+        for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = z[i];
+        __syncwarp();
+        if (n_rows <= 0 || n_cols <= 0) return;
+        if constexpr (MODE == kDz) {  // (the pitch is a multiple of 64)
+          const int c = lane % 4 * 8;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              w[i] = pack_bf16x2(z[2 * i], z[2 * i + 1]);
-              z[2 * i] -= __uint_as_float(w[i] << 16);
-              z[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+          for (int r = lane / 4; r < 32; r += 8) {
+            if (r >= n_rows) break;
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = turn[r * 33 + c + e];
+#pragma unroll
+            for (int part = 0; part < (CHUNKED ? 3 : 1); ++part) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+                f[2 * e] -= __uint_as_float(w[e] << 16);
+                f[2 * e + 1] -= __uint_as_float(w[e] & 0xffff0000u);
+              }
+              store16(p.dz + ((size_t)part * p.n + row0 + r) * p.pitch + col + c, w[0], w[1], w[2], w[3]);
             }
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) store16(to + 2 * i, w[i], w[i + 1], w[i + 2], w[i + 3]);
           }
         } else {
-          const int n_cols = p.out_cols - col;
-          if (n_cols <= 0 || row >= (MODE == kDx ? count : p.cols)) return;
-          if constexpr (MODE == kDx) {
+          if (MODE == kDx && (p.add || !p.last)) {
             // sums of the pieces before, of this split
-            float* acc = p.acc + ((size_t)split * p.n + row) * p.acc_pitch + col;
-            if (p.add) {
+            const int c = lane % 8 * 4;
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                if (i >= n_cols) break;
-                const float4 o = *reinterpret_cast<const float4*>(acc + i);
-                z[i] += o.x;
-                z[i + 1] += o.y;
-                z[i + 2] += o.z;
-                z[i + 3] += o.w;
+            for (int r = lane / 8; r < 32; r += 4) {
+              if (r >= n_rows || c >= n_cols) break;
+              float* acc = p.acc + ((size_t)split * p.n + row0 + r) * p.acc_pitch + col + c;
+              float4 o = p.add ? *reinterpret_cast<const float4*>(acc) : make_float4(0.f, 0.f, 0.f, 0.f);
+              o.x += turn[r * 33 + c];
+              o.y += turn[r * 33 + c + 1];
+              o.z += turn[r * 33 + c + 2];
+              o.w += turn[r * 33 + c + 3];
+              if (!p.last) {
+                *reinterpret_cast<float4*>(acc) = o;
+              } else {
+                turn[r * 33 + c] = o.x;
+                turn[r * 33 + c + 1] = o.y;
+                turn[r * 33 + c + 2] = o.z;
+                turn[r * 33 + c + 3] = o.w;
               }
             }
-            if (!p.last) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                if (i < n_cols) *reinterpret_cast<float4*>(acc + i) = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
-              return;
-            }
+            if (!p.last) return;
+            __syncwarp();
           }
-          const size_t at = (size_t)(MODE == kDx ? out_row : p.v0 + row) * p.out_cols + col;
-          if (p.out_fp32) {
-            float* to = reinterpret_cast<float*>(p.out) + at;
-            if (p.out_vec && n_cols >= 32) {
+          auto place_of = [&](int r) {
+            const int to = MODE == kDx ? __shfl_sync(0xffffffffu, out_row, r) : p.v0 + row0 + r;
+            return (size_t)to * p.out_cols + col;
+          };
+          const bool vec = p.out_vec && n_cols == 32;
+          if (vec && !p.out_fp32) {
+            const int c = lane % 4 * 8;
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (MODE == kDw && p.accumulate) o = *reinterpret_cast<const float4*>(to + i);
-                o.x = fmaf(p.scale, z[i], o.x);
-                o.y = fmaf(p.scale, z[i + 1], o.y);
-                o.z = fmaf(p.scale, z[i + 2], o.z);
-                o.w = fmaf(p.scale, z[i + 3], o.w);
-                *reinterpret_cast<float4*>(to + i) = o;
+            for (int r = lane / 4; r < 32; r += 8) {
+              const size_t at = place_of(r);
+              if (r < n_rows) {
+                const float* f = turn + r * 33 + c;
+                store16(reinterpret_cast<__nv_bfloat16*>(p.out) + at + c, pack_bf16x2(p.scale * f[0], p.scale * f[1]),
+                        pack_bf16x2(p.scale * f[2], p.scale * f[3]), pack_bf16x2(p.scale * f[4], p.scale * f[5]),
+                        pack_bf16x2(p.scale * f[6], p.scale * f[7]));
               }
-            } else {
+            }
+          } else if (vec) {
+            const int c = lane % 8 * 4;
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < n_cols) to[i] = fmaf(p.scale, z[i], MODE == kDw && p.accumulate ? to[i] : 0.f);
+            for (int r = lane / 8; r < 32; r += 4) {
+              const size_t at = place_of(r);
+              if (r < n_rows) {
+                const float* f = turn + r * 33 + c;
+                float* to = reinterpret_cast<float*>(p.out) + at + c;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (MODE == kDw && p.accumulate) o = *reinterpret_cast<const float4*>(to);
+                *reinterpret_cast<float4*>(to) = make_float4(fmaf(p.scale, f[0], o.x), fmaf(p.scale, f[1], o.y),
+                                                             fmaf(p.scale, f[2], o.z), fmaf(p.scale, f[3], o.w));
+              }
             }
           } else {
-            __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
-            if (p.out_vec && n_cols >= 32) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 8)
-                store16(to + i, pack_bf16x2(p.scale * z[i], p.scale * z[i + 1]),
-                        pack_bf16x2(p.scale * z[i + 2], p.scale * z[i + 3]),
-                        pack_bf16x2(p.scale * z[i + 4], p.scale * z[i + 5]),
-                        pack_bf16x2(p.scale * z[i + 6], p.scale * z[i + 7]));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < n_cols) to[i] = __float2bfloat16_rn(p.scale * z[i]);
+            for (int r = 0; r < n_rows; ++r) {
+              const size_t at = place_of(r) + lane;
+              if (lane >= n_cols) continue;
+              const float f = p.scale * turn[r * 33 + lane];
+              if (p.out_fp32) {
+                float* to = reinterpret_cast<float*>(p.out) + at;
+                *to = MODE == kDw && p.accumulate ? *to + f : f;
+              } else {
+                reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(f);
+              }
             }
           }
         }
@@ -413,10 +456,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (ok) tc_fence_after();
         return ok;
       };
-      auto load = [&](uint32_t (&v)[32], int c) {
-        tmem_ld32(tcol + (n & 1) * kTile + c, v);
-        tmem_wait_ld();
-      };
       auto give_back = [&]() {
         tc_fence_before();
         __syncwarp();
@@ -425,15 +464,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       const bool nothing = k1 <= k0;  // no products: the accumulator holds something else
       if constexpr (CHUNKED) {
-        float run[kHalf / 32][32];
+        float run[kCols / 32][32];
 #pragma unroll
-        for (int c = 0; c < kHalf; ++c) run[c / 32][c % 32] = 0.f;
+        for (int c = 0; c < kCols; ++c) run[c / 32][c % 32] = 0.f;
         int c0 = k0;
         do {
           if (!next()) break;
           if (!nothing)
 #pragma unroll
-            for (int c = 0; c < kHalf; c += 16) {
+            for (int c = 0; c < kCols; c += 16) {
               uint32_t v[16];
               tmem_ld16(tcol + (n & 1) * kTile + c, v);
               tmem_wait_ld();
@@ -445,15 +484,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         } while (c0 < k1);
         if (!ok) break;
 #pragma unroll
-        for (int c = 0; c < kHalf / 32; ++c) finish(run[c], col0 + 32 * c);
+        for (int c = 0; c < kCols / 32; ++c) finish(run[c], col0 + 32 * c);
       } else {
         if (!next()) break;
 #pragma unroll 1
-        for (int c = 0; c < kHalf; c += 32) {
+        for (int c = 0; c < kCols; c += 32) {
           __syncwarp();
           uint32_t v[32];
-          load(v, c);
-          if (c == kHalf - 32) give_back();
+          tmem_ld32(tcol + (n & 1) * kTile + c, v);
+          tmem_wait_ld();
+          if (c == kCols - 32) give_back();
           float(&z)[32] = reinterpret_cast<float(&)[32]>(v);
           if (nothing)
 #pragma unroll
@@ -463,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (MODE == kLse && row < count && col0 < p.cols)
-        p.part[(size_t)row * p.parts + p.part0 + (col0 / kHalf)] = make_float2(sum.m, sum.s);
+        p.part[(size_t)row * p.parts + p.part0 + (col0 / kCols)] = make_float2(sum.m, sum.s);
     }
   }
   // the pair ends together: neither's shared memory or tensor memory goes while the other may use it

@@ -43,14 +43,16 @@ __device__ __forceinline__ void split3(float v, float (&h)[3]) {
   }
 }
 
-// One row of D elements into its bf16 parts, `plane` elements apart, by one warp.
+// Columns [lane E .. of every `lanes` lanes] of a row into its bf16 parts, `plane` elements apart.
 template <typename T, bool VEC>
-__device__ __forceinline__ void stage_row(const T* in, __nv_bfloat16* out, size_t plane, int D, int lane) {
+__device__ __forceinline__ void stage_row(const T* in, __nv_bfloat16* out, size_t plane, int D, int lane, int lanes) {
   if constexpr (VEC && sizeof(T) == 2) {
-    for (int c = lane * 8; c < D; c += 256)
+#pragma unroll 4
+    for (int c = lane * 8; c < D; c += lanes * 8)
       *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(in + c);
   } else if constexpr (VEC) {
-    for (int c = lane * 8; c < D; c += 256) {
+#pragma unroll 2
+    for (int c = lane * 8; c < D; c += lanes * 8) {
       const float4 a = *reinterpret_cast<const float4*>(in + c), b = *reinterpret_cast<const float4*>(in + c + 4);
       const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
       float h[8][3];
@@ -63,14 +65,24 @@ __device__ __forceinline__ void stage_row(const T* in, __nv_bfloat16* out, size_
                        pack_bf16x2(h[6][p], h[7][p]));
     }
   } else {
-    for (int c = lane; c < D; c += 32) {
-      if constexpr (sizeof(T) == 2) {
-        out[c] = in[c];
-      } else {
-        float h[3];
-        split3(in[c], h);
+    constexpr int B = 8;  // asked for together
+    for (int c0 = lane; c0 < D; c0 += lanes * B) {
+      T x[B];
 #pragma unroll
-        for (int p = 0; p < 3; ++p) out[p * plane + c] = __float2bfloat16_rn(h[p]);
+      for (int u = 0; u < B; ++u)
+        if (c0 + u * lanes < D) x[u] = in[c0 + u * lanes];
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        const int c = c0 + u * lanes;
+        if (c >= D) continue;
+        if constexpr (sizeof(T) == 2) {
+          out[c] = x[u];
+        } else {
+          float h[3];
+          split3(x[u], h);
+#pragma unroll
+          for (int p = 0; p < 3; ++p) out[p * plane + c] = __float2bfloat16_rn(h[p]);
+        }
       }
     }
   }
@@ -95,15 +107,15 @@ struct GatherArgs {
   uint32_t* err;
 };
 
-// Logit of a row and its target, fp32 products by one warp; the same order for every alignment.
+// A lane's share of the product of a row and its target's row of W; the same columns for every alignment.
 template <typename T, bool VEC>
-__device__ __forceinline__ float dot_row(const T* x, const T* w, int D, int lane) {
+__device__ __forceinline__ float dot_share(const T* x, const T* w, int D, int lane, int lanes) {
   constexpr int E = 16 / sizeof(T);
   float s[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) s[e] = 0.f;
 #pragma unroll 4
-  for (int c = lane * E; c < D; c += 32 * E) {
+  for (int c = lane * E; c < D; c += lanes * E) {
     if constexpr (VEC) {
       const uint4 a = *reinterpret_cast<const uint4*>(x + c), b = *reinterpret_cast<const uint4*>(w + c);
 #pragma unroll
@@ -125,10 +137,12 @@ __device__ __forceinline__ float dot_row(const T* x, const T* w, int D, int lane
 
 // Gathers the rows of x that have a target; forward: forms the targets' logits.  A block takes a contiguous range of rows; how many
 // rows before it have a target it counts itself, so that one launch is enough.
+// ROW_WARPS: warps that share a row (all of them where there are few rows).
 constexpr int kStageThreads = 256;
-template <typename T, bool VEC>
+template <typename T, bool VEC, int ROW_WARPS>
 __global__ void __launch_bounds__(kStageThreads) stage_x(const __grid_constant__ GatherArgs a) {
   __shared__ int warp_sum[kStageThreads / 32], place[kStageThreads];
+  __shared__ float shares[kStageThreads / 32];
   let_next_launch();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int begin = (int)((int64_t)a.n * blockIdx.x / gridDim.x), end = (int)((int64_t)a.n * (blockIdx.x + 1) / gridDim.x);
@@ -170,21 +184,31 @@ __global__ void __launch_bounds__(kStageThreads) stage_x(const __grid_constant__
     if (has) a.rows[at + before] = i;
     if (i < end && !has && a.loss) a.loss[i] = a.lse[i] = 0.f;
     __syncthreads();
-    for (int j = warp; j < min(kStageThreads, end - i0); j += kStageThreads / 32) {
+    constexpr int kGroups = kStageThreads / 32 / ROW_WARPS, kLanes = 32 * ROW_WARPS;
+    const int member = threadIdx.x % kLanes;
+    for (int j = threadIdx.x / kLanes; j < min(kStageThreads, end - i0); j += kGroups) {
       const int to = place[j];
       if (to >= 0) {
-        stage_row<T, VEC>(reinterpret_cast<const T*>(a.in) + (size_t)(i0 + j) * a.D, a.out + (size_t)to * a.pitch, plane,
-                          a.D, lane);
+        const T* x = reinterpret_cast<const T*>(a.in) + (size_t)(i0 + j) * a.D;
+        stage_row<T, VEC>(x, a.out + (size_t)to * a.pitch, plane, a.D, member, kLanes);
         if (a.at) {
-          const T* x = reinterpret_cast<const T*>(a.in) + (size_t)(i0 + j) * a.D;
           const T* w = reinterpret_cast<const T*>(a.w) + (size_t)a.targets[i0 + j] * a.D;
-          float z = VEC && a.w_vec ? dot_row<T, VEC>(x, w, a.D, lane) : dot_row<T, false>(x, w, a.D, lane);
+          float z = VEC && a.w_vec ? dot_share<T, VEC>(x, w, a.D, member, kLanes)
+                                   : dot_share<T, false>(x, w, a.D, member, kLanes);
+          if constexpr (ROW_WARPS > 1) {
+            __syncthreads();
+            if (lane == 0) shares[warp] = z;
+            __syncthreads();
+            z = 0.f;
+#pragma unroll
+            for (int u = 0; u < ROW_WARPS; ++u) z += shares[u];
+          }
           if (a.cap > 0.f) z = a.cap * tanhf(z / a.cap);
-          if (lane == 0) a.at[to] = z;
+          if (member == 0) a.at[to] = z;
         }
       } else if (a.dx) {
         T* d = reinterpret_cast<T*>(a.dx) + (size_t)(i0 + j) * a.D;
-        for (int c = lane; c < a.D; c += 32) d[c] = from_float<T>(0.f);
+        for (int c = member; c < a.D; c += kLanes) d[c] = from_float<T>(0.f);
       }
     }
     at += all;
@@ -193,21 +217,27 @@ __global__ void __launch_bounds__(kStageThreads) stage_x(const __grid_constant__
     if (threadIdx.x == 0) *a.count = at;
     // rows up to the next step of K are read by the product over rows
     const int tail = min(a.n, (at + kStep - 1) / kStep * kStep);
-    for (int r = at + warp; r < tail; r += kStageThreads / 32)
-      for (int p = 0; p < (sizeof(T) == 2 ? 1 : 3); ++p)
-        for (int c = lane; c < a.D; c += 32) a.out[p * plane + (size_t)r * a.pitch + c] = __float2bfloat16_rn(0.f);
+    const size_t many = (size_t)(tail - at) * a.pitch / 8;  // rows of a multiple of 8 elements, on 16 bytes
+    for (int p = 0; p < (sizeof(T) == 2 ? 1 : 3); ++p)
+      for (size_t k = threadIdx.x; k < many; k += kStageThreads)
+        reinterpret_cast<uint4*>(a.out + p * plane + (size_t)at * a.pitch)[k] = make_uint4(0, 0, 0, 0);
   }
 }
 
-// Rows of W that are not read in place.
+// Rows of W that are not read in place, a warp 1024 columns of one.
+constexpr int kStageCols = 1024;
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) stage_w(const __grid_constant__ GatherArgs a) {
   wait_for_launch_before();
   let_next_launch();
-  const int warps = gridDim.x * 8;
-  for (int r = blockIdx.x * 8 + threadIdx.x / 32; r < a.n; r += warps)
-    stage_row<T, VEC>(reinterpret_cast<const T*>(a.in) + (size_t)r * a.D, a.out + (size_t)r * a.pitch,
-                      (size_t)a.n * a.pitch, a.D, threadIdx.x % 32);
+  const int chunks = (a.D + kStageCols - 1) / kStageCols, lane = threadIdx.x % 32;
+  const int64_t items = (int64_t)a.n * chunks;
+  for (int64_t it = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; it < items; it += (int64_t)gridDim.x * 8) {
+    const int64_t r = it / chunks;
+    const int c = (int)(it % chunks) * kStageCols;
+    stage_row<T, VEC>(reinterpret_cast<const T*>(a.in) + (size_t)r * a.D + c, a.out + (size_t)r * a.pitch + c,
+                      (size_t)a.n * a.pitch, min(kStageCols, a.D - c), lane, 32);
+  }
 }
 
 // ------------------------------------------------------------------ joins
@@ -270,7 +300,7 @@ struct Plan {
   int parts_of, pitch_d;       // bf16 parts of an operand, elements of a staged row
   bool staged;                 // W is read through the workspace
   int piece;                   // columns of a piece (the last may have fewer)
-  int pitch_z, splits, row_parts;
+  int pitch_z, splits;
   size_t count, rows, at, x, w, part, dz, acc, bytes;
 };
 Plan make_plan(int64_t n, int D, int V, int dtype, bool backward, bool w_on16) {
@@ -292,7 +322,6 @@ Plan make_plan(int64_t n, int D, int V, int dtype, bool backward, bool w_on16) {
   p.piece = (int)std::min<int64_t>(V, (int64_t)align_up((size_t)((V + pieces - 1) / pieces), kTile));
   p.pitch_z = (int)align_up((size_t)p.piece, 64);
   p.splits = dx_splits(n, D);
-  p.row_parts = tiles(V, kHalf);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -305,7 +334,12 @@ Plan make_plan(int64_t n, int D, int V, int dtype, bool backward, bool w_on16) {
   p.x = take((size_t)n * row_bytes);
   p.w = take((size_t)staged_rows * row_bytes);  // the same for every n
   const size_t common = at;
-  p.part = take((size_t)n * p.row_parts * 8);
+  // parts of wide tiles, or of narrow ones for as many rows as may have them (most where W is staged: its
+  // pieces are the smallest)
+  const int64_t staged_pieces = (V + staged_rows - 1) / staged_rows;
+  const int64_t staged_piece = (int64_t)align_up((size_t)((V + staged_pieces - 1) / staged_pieces), kTile);
+  const int64_t narrow_rows = std::min<int64_t>(n, (int64_t)kTile * (clusters() / 2 / tiles(staged_piece, kTile)));
+  p.part = take(std::max((size_t)n * tiles(V, kHalf), (size_t)narrow_rows * tiles(V, kNarrow / 2)) * 8);
   const size_t forward_bytes = at;
   at = common;
   // room that grows with n although a piece of more rows has fewer columns
@@ -348,36 +382,45 @@ cudaError_t launch_after(K kernel, unsigned grid, unsigned threads, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int MODE, bool CHUNKED>
+template <int MODE, bool CHUNKED, int TN>
 cudaError_t gemm_of(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& p, int64_t most_tiles, cudaStream_t st) {
   static size_t set[kMaxDevices] = {};
-  const cudaError_t e = set_smem_limit((const void*)head_gemm<MODE, CHUNKED>, kSmem, set);
+  const cudaError_t e = set_smem_limit((const void*)head_gemm<MODE, CHUNKED, TN>, Shape<TN>::smem, set);
   if (e != cudaSuccess) return e;
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(clusters(), most_tiles);
-  return launch_after(head_gemm<MODE, CHUNKED>, grid, (unsigned)kThreads, kSmem, st, a, b, p);
+  return launch_after(head_gemm<MODE, CHUNKED, TN>, grid, (unsigned)kThreads, Shape<TN>::smem, st, a, b, p);
 }
 template <int MODE>
-cudaError_t gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& p, int64_t most_tiles, cudaStream_t st) {
-  if (MODE == kLse || p.passes > 1) return gemm_of<MODE, true>(a, b, p, most_tiles, st);
-  return gemm_of<MODE, MODE == kLse>(a, b, p, most_tiles, st);
+cudaError_t gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& p, int64_t most_tiles, bool narrow,
+                 cudaStream_t st) {
+  constexpr bool always = MODE == kLse;
+  if constexpr (MODE == kLse || MODE == kDz)
+    if (narrow)
+      return always || p.passes > 1 ? gemm_of<MODE, true, kNarrow>(a, b, p, most_tiles, st)
+                                    : gemm_of<MODE, always, kNarrow>(a, b, p, most_tiles, st);
+  return always || p.passes > 1 ? gemm_of<MODE, true, 256>(a, b, p, most_tiles, st)
+                                : gemm_of<MODE, always, 256>(a, b, p, most_tiles, st);
 }
+// Whether the logits of `rows` and `cols` leave so many clusters without a tile that narrow ones are faster.
+bool is_narrow(int64_t rows, int64_t cols) { return 2 * (int64_t)tiles(rows, kTile) * tiles(cols, kTile) <= clusters(); }
 
 // What both directions share: the rows with a target, gathered.
 template <typename T>
 cudaError_t gather(const void* x, const GatherArgs& s, cudaStream_t st) {
   const unsigned grid = (unsigned)std::min(s.n, 2 * device_sm_count());
   count_launches(1);
-  if (s.D % 8 == 0 && on16(x))
-    stage_x<T, true><<<grid, kStageThreads, 0, st>>>(s);
+  const bool vec = s.D % 8 == 0 && on16(x), few = s.n <= 4 * (int)grid;
+  if (few)
+    vec ? stage_x<T, true, 8><<<grid, kStageThreads, 0, st>>>(s) : stage_x<T, false, 8><<<grid, kStageThreads, 0, st>>>(s);
   else
-    stage_x<T, false><<<grid, kStageThreads, 0, st>>>(s);
+    vec ? stage_x<T, true, 1><<<grid, kStageThreads, 0, st>>>(s) : stage_x<T, false, 1><<<grid, kStageThreads, 0, st>>>(s);
   return cudaGetLastError();
 }
 
 // The map of the piece's rows of W, in place or staged here; row_b: where the piece starts in it.
 template <typename T>
-cudaError_t weights(const void* w, const Plan& pl, char* ws, int D, int V, int v0, int cols, CUtensorMap* m128,
-                    CUtensorMap* m64, int* row_b, cudaStream_t st) {
+cudaError_t weights(const void* w, const Plan& pl, char* ws, int D, int V, int v0, int cols, bool narrow,
+                    CUtensorMap* m128, CUtensorMap* m64, int* row_b, cudaStream_t st) {
   const void* base = w;
   uint64_t rows = V, planes = 1, pitch = D;
   *row_b = v0;
@@ -388,7 +431,7 @@ cudaError_t weights(const void* w, const Plan& pl, char* ws, int D, int V, int v
     s.n = cols;
     s.D = D;
     s.pitch = pl.pitch_d;
-    const unsigned grid = (unsigned)std::min(tiles(cols, 8), 8 * device_sm_count());
+    const unsigned grid = (unsigned)std::min(tiles((int64_t)cols * tiles(D, kStageCols), 8), 8 * device_sm_count());
     const cudaError_t e = D % 8 == 0 && on16(s.in) ? launch_after(stage_w<T, true>, grid, 256u, 0, st, s)
                                                    : launch_after(stage_w<T, false>, grid, 256u, 0, st, s);
     if (e != cudaSuccess) return e;
@@ -398,7 +441,7 @@ cudaError_t weights(const void* w, const Plan& pl, char* ws, int D, int V, int v
     pitch = pl.pitch_d;
     *row_b = 0;
   }
-  if (!make_map(m128, base, planes, rows, D, pitch, kHalf)) return cudaErrorInvalidValue;
+  if (!make_map(m128, base, planes, rows, D, pitch, narrow ? kNarrow / 2 : kHalf)) return cudaErrorInvalidValue;
   if (m64 && !make_map(m64, base, planes, rows, D, pitch, kStep)) return cudaErrorInvalidValue;
   return cudaSuccess;
 }
@@ -411,14 +454,17 @@ cudaError_t forward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, cha
   CUtensorMap mx, mw;
   if (!make_map(&mx, s.out, pl.parts_of, s.n, s.D, s.pitch, kHalf)) return cudaErrorInvalidValue;
   g.steps = tiles(s.D, kStep);
+  const bool narrow = is_narrow(s.n, pl.piece);
+  const int tn = narrow ? kNarrow : kTile;
+  g.parts = tiles(V, tn / 2);
   for (int v0 = 0; v0 < V; v0 += pl.piece) {
     g.v0 = v0;
     g.cols = std::min(pl.piece, V - v0);
-    e = weights<T>(w, pl, ws, s.D, V, v0, g.cols, &mw, nullptr, &g.row_b, st);
+    e = weights<T>(w, pl, ws, s.D, V, v0, g.cols, narrow, &mw, nullptr, &g.row_b, st);
     if (e != cudaSuccess) return e;
-    g.tns = tiles(g.cols, kTile);
-    g.part0 = v0 / kHalf;
-    e = gemm<kLse>(mx, mw, g, (int64_t)tiles(s.n, kTile) * g.tns, st);
+    g.tns = tiles(g.cols, tn);
+    g.part0 = v0 / (tn / 2);
+    e = gemm<kLse>(mx, mw, g, (int64_t)tiles(s.n, kTile) * g.tns, narrow, st);
     if (e != cudaSuccess) return e;
   }
   return launch_after(join_lse, (unsigned)std::min(tiles(s.n, 8), 8 * device_sm_count()), 256u, 0, st, g, loss, lse);
@@ -440,7 +486,8 @@ cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, ch
   for (int v0 = 0; v0 < V; v0 += pl.piece) {
     const int cols = std::min(pl.piece, V - v0);
     int row_b;
-    e = weights<T>(w, pl, ws, D, V, v0, cols, &mw, &mw64, &row_b, st);
+    const bool narrow = is_narrow(s.n, cols);
+    e = weights<T>(w, pl, ws, D, V, v0, cols, narrow, &mw, &mw64, &row_b, st);
     if (e != cudaSuccess) return e;
     if (!make_map(&mz, g.dz, pl.parts_of, s.n, cols, g.pitch, kHalf) ||
         !make_map(&mz64, g.dz, pl.parts_of, s.n, cols, g.pitch, kStep))
@@ -451,8 +498,8 @@ cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, ch
     }
     g.steps = tiles(D, kStep);
     g.row_b = row_b;
-    g.tns = tiles(cols, kTile);
-    e = gemm<kDz>(mx, mw, g, (int64_t)tms * g.tns, st);
+    g.tns = tiles(cols, narrow ? kNarrow : kTile);
+    e = gemm<kDz>(mx, mw, g, (int64_t)tms * g.tns, narrow, st);
     if (e != cudaSuccess) return e;
     if (dx) {
       const bool last = v0 + cols == V;
@@ -466,7 +513,7 @@ cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, ch
       gx.out_cols = D;
       gx.out_fp32 = sizeof(T) == 4;
       gx.out_vec = D % (16 / (int)sizeof(T)) == 0 && on16(dx);
-      e = gemm<kDx>(mz, mw64, gx, (int64_t)tms * tds * gx.splits, st);
+      e = gemm<kDx>(mz, mw64, gx, (int64_t)tms * tds * gx.splits, false, st);
       if (e != cudaSuccess) return e;
       if (last && pl.splits > 1) {
         gx.splits = std::min(pl.splits, tiles(pl.piece, kStep));  // of the first piece: no other has more
@@ -483,7 +530,7 @@ cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, ch
       gw.out_fp32 = dw_dtype == OOMB_FP32;
       gw.out_vec = D % (16 / (int)dtype_size(dw_dtype)) == 0 && on16(dw);
       gw.accumulate = accumulate;
-      e = gemm<kDw>(mz64, mx64, gw, (int64_t)gw.tms * tds, st);
+      e = gemm<kDw>(mz64, mx64, gw, (int64_t)gw.tms * tds, false, st);
       if (e != cudaSuccess) return e;
     }
   }
@@ -514,7 +561,6 @@ GemmArgs arguments(const void* x, const int64_t* targets, int n, int D, int V, i
   g.targets = targets;
   g.cap = cap;
   g.part = reinterpret_cast<float2*>(ws + pl.part);
-  g.parts = pl.row_parts;
   g.at = reinterpret_cast<const float*>(ws + pl.at);
   g.dz = reinterpret_cast<__nv_bfloat16*>(ws + pl.dz);
   g.acc = reinterpret_cast<float*>(ws + pl.acc);

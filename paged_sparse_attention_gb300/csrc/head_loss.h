@@ -26,7 +26,7 @@ struct GemmArgs {
   const int64_t* targets;
   float cap;
   // kLse
-  float2* part;     // [n, parts] maximum and sum of 128 columns, base 2
+  float2* part;     // [n, parts] maximum and sum of half a tile's columns, base 2
   int parts, part0;
   const float* at;  // [n] logit of the target, which is not in the sums
   // kDz
@@ -45,8 +45,8 @@ struct GemmArgs {
 
 // ---- few rows and small problems (head_small.cu)
 constexpr int kFewRows = 8;                  // rows that always take it
-constexpr int64_t kSmallWork = 1 << 26;      // products n V D up to which more rows do
-constexpr int kMaxRows = 4096;
+constexpr int64_t kSmallWork = 1 << 24;      // products n V D up to which more rows do
+constexpr int kMaxRows = 64;                 // and how many more
 
 struct SmallArgs {
   const void* x;

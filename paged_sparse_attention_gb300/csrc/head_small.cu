@@ -96,8 +96,16 @@ __global__ void __launch_bounds__(kThreads, 2) dot_rows(const __grid_constant__ 
   for (int t = 0; t < NT; ++t) {
     const bool has = t0 + t < a.n && has_target(a, t0 + t);
     const T* x = reinterpret_cast<const T*>(a.x) + (size_t)(t0 + t) * a.D;
-    for (int c = threadIdx.x; c < pitch; c += kThreads)
-      xs[t * pitch + (c & ~255) + (c & 4) * 32 + (c & 248) / 2 + (c & 3)] = has && c < a.D ? to_float<T>(x[c]) : 0.f;
+#pragma unroll 2
+    for (int c = threadIdx.x * kCols; c < pitch; c += kThreads * kCols) {
+      Eight<T, VEC> raw;
+      raw.load(x, has ? c : a.D, a.D);
+      uint64_t f[kCols / 2];
+      raw.pairs(f);
+      float* to = xs + t * pitch + (c & ~255) + (c & 255) / 2;
+      *reinterpret_cast<ulonglong2*>(to) = make_ulonglong2(f[0], f[1]);
+      *reinterpret_cast<ulonglong2*>(to + 128) = make_ulonglong2(f[2], f[3]);
+    }
   }
   __syncthreads();
   // after the reduction lane l has sum l >> (5 - LOG): row and token
@@ -242,7 +250,8 @@ __global__ void __launch_bounds__(kThreads) join_loss(const __grid_constant__ Sm
 }
 
 // ------------------------------------------------------------------ gradients
-// grid.z: 0 dx, 1 dw.  grid.y: slabs of columns; threadIdx.x % ct: eight columns, / ct: row group.
+// grid.z: dx of eight tokens each, then dw.  grid.y: slabs of columns; threadIdx.x % ct: eight columns,
+// / ct: row group.
 template <typename T, typename TW, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) grad_rows(const __grid_constant__ SmallArgs a) {
   constexpr int NT = 8;
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_rows(const __grid_constant__
   if (group >= a.row_groups || c >= a.D) return;
   const int chunks = (a.V + kRows - 1) / kRows;
   const int first = (int)((int64_t)chunks * unit / units), end = (int)((int64_t)chunks * (unit + 1) / units);
-  if (a.dw && (blockIdx.z == 1 || !a.dx)) {
+  if (a.dw && blockIdx.z == gridDim.z - 1) {
     for (int ch = first; ch < end; ++ch) {
       const int v0 = ch * kRows;
       uint64_t acc[kRows][kCols / 2];
@@ -264,20 +273,30 @@ __global__ void __launch_bounds__(kThreads, 2) grad_rows(const __grid_constant__
       for (int r = 0; r < kRows; ++r)
 #pragma unroll
         for (int k = 0; k < kCols / 2; ++k) acc[r][k] = 0;
-#pragma unroll 2
-      for (int t = 0; t < a.n; ++t) {
-        if (!has[t]) continue;
-        Eight<T, VEC> raw;
-        raw.load(reinterpret_cast<const T*>(a.x) + (size_t)t * a.D, c, a.D);
-        const float4 d = *reinterpret_cast<const float4*>(a.dz + (size_t)t * a.pitch + v0);  // (rows behind the last: not used)
-        uint64_t x[kCols / 2];
-        raw.pairs(x);
-        const float dd[kRows] = {d.x, d.y, d.z, d.w};
+      constexpr int B = 4;  // tokens asked for together
+      for (int t0 = 0; t0 < a.n; t0 += B) {
+        Eight<T, VEC> raw[B];
+        float4 d[B];
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          const uint64_t dr = f32x2(dd[r], dd[r]);
+        for (int u = 0; u < B; ++u) {
+          const bool live = t0 + u < a.n && has[t0 + u];  // (a token without a target is not read)
+          raw[u].load(reinterpret_cast<const T*>(a.x) + (size_t)(live ? t0 + u : 0) * a.D, live ? c : a.D, a.D);
+          // (rows of W behind the last: not used)
+          d[u] = live ? *reinterpret_cast<const float4*>(a.dz + (size_t)(t0 + u) * a.pitch + v0)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
 #pragma unroll
-          for (int k = 0; k < kCols / 2; ++k) acc[r][k] = fma2(dr, x[k], acc[r][k]);
+        for (int u = 0; u < B; ++u) {
+          if (t0 + u >= a.n) break;
+          uint64_t x[kCols / 2];
+          raw[u].pairs(x);
+          const float dd[kRows] = {d[u].x, d[u].y, d[u].z, d[u].w};
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) {
+            const uint64_t dr = f32x2(dd[r], dd[r]);
+#pragma unroll
+            for (int k = 0; k < kCols / 2; ++k) acc[r][k] = fma2(dr, x[k], acc[r][k]);
+          }
         }
       }
 #pragma unroll
@@ -311,7 +330,8 @@ __global__ void __launch_bounds__(kThreads, 2) grad_rows(const __grid_constant__
     }
     return;
   }
-  for (int t0 = 0; t0 < a.n; t0 += NT) {
+  {
+    const int t0 = blockIdx.z * NT;
     uint64_t acc[NT][kCols / 2];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -414,17 +434,23 @@ cudaError_t dot(const SmallArgs& a, cudaStream_t st) {
 }
 template <typename T, bool VEC, bool DZ>
 cudaError_t dot_tokens(const SmallArgs& a, cudaStream_t st) {
-  // as many tokens at a time as there are and shared memory holds
+  // as many tokens at a time as there are and shared memory holds, but no more than leave every SM a
+  // block: a short vocabulary's rows are in L2 for the next tokens
+  auto takes = [&](int nt) {
+    return a.n > nt / 2 && nt * vector_bytes(a.D) <= kMaxVectors &&
+           (int64_t)dot_blocks(a.V) * ((a.n + nt - 1) / nt) >= device_sm_count();
+  };
   if constexpr (sizeof(T) == 2)  // (fp32: the registers hold four tokens' sums)
-    if (a.n > 4 && 8 * vector_bytes(a.D) <= kMaxVectors) return dot<T, VEC, 8, DZ>(a, st);
-  if (a.n > 2 && 4 * vector_bytes(a.D) <= kMaxVectors) return dot<T, VEC, 4, DZ>(a, st);
-  if (a.n > 1 && 2 * vector_bytes(a.D) <= kMaxVectors) return dot<T, VEC, 2, DZ>(a, st);
+    if (takes(8)) return dot<T, VEC, 8, DZ>(a, st);
+  if (takes(4)) return dot<T, VEC, 4, DZ>(a, st);
+  if (takes(2)) return dot<T, VEC, 2, DZ>(a, st);
   return dot<T, VEC, 1, DZ>(a, st);
 }
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Columns' threads, row groups of a block, slabs and blocks of grad_rows.
+// Columns' threads, row groups of a block, slabs and blocks of grad_rows: up to 512 parts of the
+// vocabulary, over two blocks an SM before more go into one block.
 struct GradGrid {
   int ct, row_groups, slabs, blocks;
 };
@@ -433,10 +459,9 @@ GradGrid grad_grid(int D, int V) {
   const int threads = (D + kCols - 1) / kCols;
   g.slabs = (threads + kThreads - 1) / kThreads;
   g.ct = (threads + g.slabs - 1) / g.slabs;
-  g.row_groups = std::max(1, kThreads / g.ct);
-  const int chunks = (V + kRows - 1) / kRows;
-  g.blocks = std::max(1, std::min((chunks + g.row_groups - 1) / g.row_groups,
-                                  std::max(1, std::min(2 * device_sm_count() / g.slabs, 512 / g.row_groups))));
+  const int units = std::min(512, (V + kRows - 1) / kRows), most = std::max(1, 2 * device_sm_count() / g.slabs);
+  g.blocks = std::min(units, most);
+  g.row_groups = std::max(1, std::min(kThreads / g.ct, (units + g.blocks - 1) / g.blocks));
   return g;
 }
 
@@ -449,7 +474,7 @@ cudaError_t backward(SmallArgs a, int dw_dtype, cudaStream_t st) {
   a.ct = g.ct;
   a.row_groups = g.row_groups;
   a.dw_vec = a.D % 8 == 0 && on16(a.dw);
-  const dim3 grid((unsigned)g.blocks, (unsigned)g.slabs, a.dx && a.dw ? 2 : 1);
+  const dim3 grid((unsigned)g.blocks, (unsigned)g.slabs, (unsigned)((a.dx ? (a.n + 7) / 8 : 0) + (a.dw ? 1 : 0)));
   if (dw_dtype == OOMB_FP32)
     e = vec ? launch(grad_rows<T, float, true>, grid, 0, true, st, a) : launch(grad_rows<T, float, false>, grid, 0, true, st, a);
   else

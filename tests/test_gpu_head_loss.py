@@ -75,8 +75,9 @@ def test_caps_masks_weights_and_scale(dtype, cap, masked):
 
 
 def test_several_pieces_of_the_vocabulary():
-    """A vocabulary of many pieces for few rows, and one whose last piece is a single row."""
-    for n, V, D, dt in ((70, 40961, 64, BF), (70, 40961, 72, FP), (2100, 33000, 64, BF)):
+    """Pieces that dz's share of the workspace sets (many rows) and that staged rows of W set (wide fp32)."""
+    for n, V, D, dt in ((70, 40961, 64, BF), (70, 40961, 72, FP), (4600, 33000, 64, BF), (1500, 33001, 40, FP),
+                        (300, 3000, 20000, FP)):
         x, w, t, g = make(n, V, D, dt, seed=3, masked=0.2)
         kw = dict(d_loss=g, scale=0.5)
         ref, tol = head_reference(x, w, t, **kw)
@@ -159,6 +160,37 @@ def test_tensors_off_16_bytes(dtype):
     assert L.oomb_word_check(err) == 0
     for k in want:
         assert torch.equal(out[k], want[k]), k
+
+
+def test_a_wide_projection_off_16_bytes():
+    """bf16 rows that are read through the workspace, in two pieces."""
+    x, w, t, g = make(20, 9000, 2048, BF, seed=13, masked=0.2)
+    want = run(x, w, t, d_loss=g)
+    wo = torch.empty(w.numel() + 1, dtype=BF, device="cuda")[1:].view(w.shape).copy_(w)
+    out = {k: torch.empty_like(v) for k, v in want.items()}
+    xs, ts, gs, err = x.cuda(), t.cuda(), g.cuda(), word()
+    ws = torch.empty(L.oomb_head_loss_workspace(20, 2048, 9000, BF, True), dtype=torch.uint8, device="cuda")
+    L.oomb_head_loss_fwd(xs, wo, ts, out["loss"], out["lse"], ws, err)
+    L.oomb_head_loss_bwd(xs, wo, ts, out["lse"], out["dx"], out["dw"], ws, err, d_loss=gs)
+    assert L.oomb_word_check(err) == 0
+    ref, tol = head_reference(x, w, t, d_loss=g)
+    check(out, ref, tol)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("n,V,D", [(9, 700, 3000), (40, 300, 517), (64, 257, 1000), (65, 257, 1000), (100, 9800, 72),
+                                   (200, 20, 3), (2000, 40, 65), (257, 12000, 130), (8, 1842, 3840), (7, 13710, 108),
+                                   (3, 1, 20), (63, 2, 9000), (2, 5, 30000)])
+def test_the_ways_of_few_rows_and_few_tiles(dtype, n, V, D):
+    """On both sides of the rules that choose the kernels, with targets missing and at the ends."""
+    x, w, t, g = make(n, V, D, dtype, seed=n + D, masked=0.25)
+    t[0], t[-1] = 0, V - 1
+    kw = dict(d_loss=g, cap=20.0, scale=2.0)
+    ref, tol = head_reference(x, w, t, **kw)
+    check(run(x, w, t, **kw), ref, tol)
+    out = run(x, w, t, dw_dtype=FP, **kw)
+    ref, tol = head_reference(x, w, t, dw_dtype=FP, **kw)
+    check(out, ref, tol)
 
 
 def test_large_and_far_logits():
