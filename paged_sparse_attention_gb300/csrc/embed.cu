@@ -87,6 +87,8 @@ __device__ __forceinline__ void store_e(T* p, const float (&f)[E]) {
 // 3584 in bf16, these 18 at 8 KB a block.)
 template <typename T, int E, int NV>
 __global__ void __launch_bounds__(256) embed_rows(const __grid_constant__ EmbedArgs a) {
+  wait_for_launch_before();
+  let_next_launch();
   const int per_row = blockDim.x / a.rows, r = threadIdx.x / per_row, lane = threadIdx.x % per_row;
   const int64_t i = (int64_t)blockIdx.x * a.rows + r;
   if (i >= a.n) return;
@@ -118,6 +120,7 @@ __global__ void __launch_bounds__(32 * kRankWarps) rank_tokens(const __grid_cons
   __shared__ __align__(16) int keys[kSection];
   __shared__ int parts[kRankWarps][kRankKeys];
   constexpr int T = 32 * kRankWarps, K = kSection / T;
+  wait_for_launch_before();
   let_next_launch();
   if (blockIdx.x == 0 && threadIdx.x == 0) a.n_long[0] = a.n_long[1] = 0;
   const int m = (int)a.n, own = blockIdx.x * kRankKeys, m4 = (m + 3) & ~3;
@@ -174,6 +177,7 @@ struct SortSpace {
 __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens(const __grid_constant__ EmbedArgs a) {
   extern __shared__ __align__(16) uint8_t sort_mem[];
   SortSpace& s = *reinterpret_cast<SortSpace*>(sort_mem);
+  wait_for_launch_before();
   let_next_launch();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t first = (int64_t)blockIdx.x * kSection;
@@ -526,12 +530,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_pieces(const __grid_cons
 }
 
 template <typename K>
-cudaError_t launch_after(K kernel, dim3 grid, int threads, const EmbedArgs& a, cudaStream_t st) {
+cudaError_t launch_after(K kernel, dim3 grid, int threads, const EmbedArgs& a, cudaStream_t st, size_t smem = 0) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr;  // a dependent launch: its set-up overlaps the end of the one before
+  cudaLaunchAttribute attr;  // a dependent launch: its set-up overlaps the end of the one before, which it waits for
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
@@ -548,9 +553,7 @@ cudaError_t forward(EmbedArgs& a, cudaStream_t st) {
   const int per_row = (int)std::min<size_t>(256, align_up((size_t)vecs, 32));
   a.rows = 256 / per_row;
   while (a.rows > 1 && (a.n + a.rows - 1) / a.rows < 2 * device_sm_count()) a.rows /= 2;
-  count_launches(1);
-  embed_rows<T, E, NV><<<(unsigned)((a.n + a.rows - 1) / a.rows), per_row * a.rows, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(embed_rows<T, E, NV>, dim3((unsigned)((a.n + a.rows - 1) / a.rows)), per_row * a.rows, a, st);
 }
 
 size_t sort_smem_set[kMaxDevices] = {};
@@ -559,15 +562,12 @@ template <typename T, int E, int NV>
 cudaError_t backward(const EmbedArgs& a, cudaStream_t st) {
   const unsigned sections = (unsigned)((a.n + kSection - 1) / kSection);
   cudaError_t e = cudaSuccess;
-  count_launches(1);
   if (sections == 1) {
-    rank_tokens<<<(unsigned)((a.n + kRankKeys - 1) / kRankKeys), 32 * kRankWarps, 0, st>>>(a);
+    e = launch_after(rank_tokens, dim3((unsigned)((a.n + kRankKeys - 1) / kRankKeys)), 32 * kRankWarps, a, st);
   } else {
     e = set_smem_limit((const void*)sort_tokens, sizeof(SortSpace), sort_smem_set);
-    if (e != cudaSuccess) return e;
-    sort_tokens<<<sections, kSortThreads, sizeof(SortSpace), st>>>(a);
+    if (e == cudaSuccess) e = launch_after(sort_tokens, dim3(sections), kSortThreads, a, st, sizeof(SortSpace));
   }
-  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (sections > 1) {
     e = launch_after(merge_sections, dim3((unsigned)((a.n + 127) / 128)), 128, a, st);

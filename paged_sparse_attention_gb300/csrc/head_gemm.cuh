@@ -182,13 +182,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int count = *p.count;
   const int tms = MODE == kDw ? p.tms : (count + kTile - 1) / kTile;
   const int steps_all = MODE == kDw ? (count + kStep - 1) / kStep : p.steps;
-  const int tiles = tms * p.tns * p.splits;
   const int clusters = gridDim.x / 2, first = blockIdx.x / 2;
+  const int all_splits = MODE == kDx ? p.count[1] : 1, splits = min(all_splits, max(1, steps_all));
+  const bool last = MODE != kDx || (p.last && all_splits == 1);
+  const int tiles = tms * p.tns * splits;
   // steps of K of a tile: its split's share
   auto range = [&](int t, int& k0, int& k1) {
     const int s = t / (tms * p.tns);
-    k0 = (int)((int64_t)steps_all * s / p.splits);
-    k1 = (int)((int64_t)steps_all * (s + 1) / p.splits);
+    k0 = (int)((int64_t)steps_all * s / splits);
+    k1 = (int)((int64_t)steps_all * (s + 1) / splits);
   };
 
   if (warp == 0) {
@@ -320,7 +322,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       RowSum sum;
 
       // what becomes of 32 columns of the row, from col on
+      const bool none = MODE == kLse && row0 >= count;  // no row of the warp has a target
       auto finish = [&](float (&z)[32], int col) {
+        if (none) return;
         if constexpr (MODE == kLse) {
           if (p.cap > 0.f)
 #pragma unroll
@@ -378,7 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         } else {
-          if (MODE == kDx && (p.add || !p.last)) {
+          if (MODE == kDx && (p.add || !last)) {
             // sums of the pieces before, of this split
             const int c = lane % 8 * 4;
 #pragma unroll
@@ -390,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               o.y += turn[r * 33 + c + 1];
               o.z += turn[r * 33 + c + 2];
               o.w += turn[r * 33 + c + 3];
-              if (!p.last) {
+              if (!last) {
                 *reinterpret_cast<float4*>(acc) = o;
               } else {
                 turn[r * 33 + c] = o.x;
@@ -399,7 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 turn[r * 33 + c + 3] = o.w;
               }
             }
-            if (!p.last) return;
+            if (!last) return;
             __syncwarp();
           }
           auto place_of = [&](int r) {

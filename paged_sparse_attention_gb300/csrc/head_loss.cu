@@ -28,7 +28,7 @@ constexpr int kGroup = 16;
 constexpr int kChunk = 28, kChunkParts = 4;
 // Workspace given to a piece's dz, and to staged parts of W where it cannot be read in place
 // (kStagedOdd: bf16 rows that are on 16 bytes unless the caller's pointer is not).
-constexpr size_t kDzBytes = 256u << 20, kStagedBytes = 256u << 20, kStagedOdd = 32u << 20;
+constexpr size_t kAccBytes = 256u << 20, kDzBytes = 256u << 20, kStagedBytes = 256u << 20, kStagedOdd = 32u << 20;
 
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -104,6 +104,8 @@ struct GatherArgs {
   float* loss;            // forward: written in rows without a target
   float* lse;
   void* dx;               // backward: the same
+  int most_splits, clusters, tns, steps0;  // backward: parts K of dx may be cut into, clusters of the GPU, tiles of
+                                           // columns, steps of K
   uint32_t* err;
 };
 
@@ -143,6 +145,7 @@ template <typename T, bool VEC, int ROW_WARPS>
 __global__ void __launch_bounds__(kStageThreads) stage_x(const __grid_constant__ GatherArgs a) {
   __shared__ int warp_sum[kStageThreads / 32], place[kStageThreads];
   __shared__ float shares[kStageThreads / 32];
+  wait_for_launch_before();
   let_next_launch();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int begin = (int)((int64_t)a.n * blockIdx.x / gridDim.x), end = (int)((int64_t)a.n * (blockIdx.x + 1) / gridDim.x);
@@ -214,7 +217,33 @@ __global__ void __launch_bounds__(kStageThreads) stage_x(const __grid_constant__
     at += all;
   }
   if (blockIdx.x == gridDim.x - 1) {
-    if (threadIdx.x == 0) *a.count = at;
+    if (threadIdx.x == 0) a.count[0] = at;
+    if (warp == 0 && a.most_splits > 0) {
+      // parts that K of dx is cut into: those that leave the clusters idle for the least time, of 8 steps at
+      // least; a lane tries two
+      const int dx_tiles = (at + kTile - 1) / kTile * a.tns;
+      float least = 1e30f;
+      int best = 1;
+      for (int s = lane + 1; s <= a.most_splits; s += 32) {
+        if (s > 1 && s * 8 > a.steps0) break;
+        // rounds of the parts, and what writing and adding one more of them costs
+        const float cost = (float)((dx_tiles * s + a.clusters - 1) / a.clusters) / (float)s + 0.004f * (float)s;
+        if (cost < least) {
+          least = cost;
+          best = s;
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float c2 = __shfl_xor_sync(0xffffffffu, least, o);
+        const int b2 = __shfl_xor_sync(0xffffffffu, best, o);
+        if (c2 < least || (c2 == least && b2 < best)) {
+          least = c2;
+          best = b2;
+        }
+      }
+      if (lane == 0) a.count[1] = best;
+    }
     // rows up to the next step of K are read by the product over rows
     const int tail = min(a.n, (at + kStep - 1) / kStep * kStep);
     const size_t many = (size_t)(tail - at) * a.pitch / 8;  // rows of a multiple of 8 elements, on 16 bytes
@@ -277,12 +306,13 @@ template <typename T>
 __global__ void __launch_bounds__(256) join_dx(const __grid_constant__ GemmArgs a) {
   wait_for_launch_before();
   let_next_launch();
-  const int count = *a.count;
+  const int count = a.count[0], splits = a.count[1];
+  if (splits == 1) return;  // written already
   const int64_t total = (int64_t)count * a.out_cols;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int r = (int)(i / a.out_cols), c = (int)(i % a.out_cols);
     float v = 0.f;
-    for (int s = 0; s < a.splits; ++s) v += a.acc[((size_t)s * a.n + r) * a.acc_pitch + c];
+    for (int s = 0; s < splits; ++s) v += a.acc[((size_t)s * a.n + r) * a.acc_pitch + c];
     reinterpret_cast<T*>(a.out)[(size_t)a.rows[r] * a.out_cols + c] = from_float<T>(a.scale * v);
   }
 }
@@ -292,15 +322,17 @@ int tiles(int64_t x, int t) { return (int)((x + t - 1) / t); }
 int clusters() { return std::max(1, device_sm_count() / 2); }
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Parts that the product of few rows with W is cut into along the vocabulary.
-int dx_splits(int64_t n, int D) { return std::max(1, std::min(16, clusters() / (tiles(n, kTile) * tiles(D, kTile)))); }
+// Parts that K of dx may be cut into: as many as kAccBytes hold, 64 at most.
+int most_splits(int64_t n, int D) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(64, (int64_t)(kAccBytes / ((size_t)n * align_up((size_t)D, 4) * 4))));
+}
 
 // Where things lie in the workspace, and the pieces of the vocabulary.
 struct Plan {
   int parts_of, pitch_d;       // bf16 parts of an operand, elements of a staged row
   bool staged;                 // W is read through the workspace
   int piece;                   // columns of a piece (the last may have fewer)
-  int pitch_z, splits;
+  int pitch_z;
   size_t count, rows, at, x, w, part, dz, acc, bytes;
 };
 Plan make_plan(int64_t n, int D, int V, int dtype, bool backward, bool w_on16) {
@@ -321,14 +353,13 @@ Plan make_plan(int64_t n, int D, int V, int dtype, bool backward, bool w_on16) {
   const int64_t pieces = (V + most - 1) / most;
   p.piece = (int)std::min<int64_t>(V, (int64_t)align_up((size_t)((V + pieces - 1) / pieces), kTile));
   p.pitch_z = (int)align_up((size_t)p.piece, 64);
-  p.splits = dx_splits(n, D);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at += align_up(bytes, 256);
     return here;
   };
-  p.count = take(4);
+  p.count = take(8);
   p.rows = take((size_t)n * 4);
   p.at = take((size_t)n * 4);
   p.x = take((size_t)n * row_bytes);
@@ -344,11 +375,8 @@ Plan make_plan(int64_t n, int D, int V, int dtype, bool backward, bool w_on16) {
   at = common;
   // room that grows with n although a piece of more rows has fewer columns
   p.dz = take(std::min<size_t>(z_bytes * align_up((size_t)V, 64), std::max<size_t>(kDzBytes, z_bytes * kTile)));
-  size_t acc_rows = (size_t)n;
-  for (int64_t m = kTile; m <= n && m <= (int64_t)kTile * clusters(); m += kTile)
-    acc_rows = std::max(acc_rows, (size_t)m * dx_splits(m, D));
-  acc_rows = std::max(acc_rows, (size_t)n * p.splits);
-  p.acc = take(acc_rows * align_up((size_t)D, 4) * 4);
+  const size_t acc = (size_t)n * align_up((size_t)D, 4) * 4;
+  p.acc = take(std::max(acc, std::min(64 * acc, kAccBytes)));
   p.bytes = backward ? std::max(forward_bytes, at) : forward_bytes;
   return p;
 }
@@ -408,13 +436,12 @@ bool is_narrow(int64_t rows, int64_t cols) { return 2 * (int64_t)tiles(rows, kTi
 template <typename T>
 cudaError_t gather(const void* x, const GatherArgs& s, cudaStream_t st) {
   const unsigned grid = (unsigned)std::min(s.n, 2 * device_sm_count());
-  count_launches(1);
   const bool vec = s.D % 8 == 0 && on16(x), few = s.n <= 4 * (int)grid;
   if (few)
-    vec ? stage_x<T, true, 8><<<grid, kStageThreads, 0, st>>>(s) : stage_x<T, false, 8><<<grid, kStageThreads, 0, st>>>(s);
-  else
-    vec ? stage_x<T, true, 1><<<grid, kStageThreads, 0, st>>>(s) : stage_x<T, false, 1><<<grid, kStageThreads, 0, st>>>(s);
-  return cudaGetLastError();
+    return vec ? launch_after(stage_x<T, true, 8>, grid, kStageThreads, 0, st, s)
+               : launch_after(stage_x<T, false, 8>, grid, kStageThreads, 0, st, s);
+  return vec ? launch_after(stage_x<T, true, 1>, grid, kStageThreads, 0, st, s)
+             : launch_after(stage_x<T, false, 1>, grid, kStageThreads, 0, st, s);
 }
 
 // The map of the piece's rows of W, in place or staged here; row_b: where the piece starts in it.
@@ -473,6 +500,10 @@ cudaError_t forward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, cha
 template <typename T>
 cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, char* ws, int V, void* dx, void* dw,
                      int dw_dtype, int accumulate, cudaStream_t st) {
+  s.most_splits = most_splits(s.n, s.D);
+  s.clusters = clusters();
+  s.tns = tiles(s.D, kTile);
+  s.steps0 = tiles(pl.piece, kStep);
   cudaError_t e = gather<T>(s.in, s, st);
   if (e != cudaSuccess) return e;
   const int D = s.D;
@@ -504,19 +535,17 @@ cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, ch
     if (dx) {
       const bool last = v0 + cols == V;
       gx.steps = tiles(cols, kStep);
-      gx.splits = std::min(pl.splits, gx.steps);
       gx.row_b = row_b;
       gx.tns = tds;
       gx.add = v0 > 0;
-      gx.last = last && pl.splits == 1;
+      gx.last = last;
       gx.out = dx;
       gx.out_cols = D;
       gx.out_fp32 = sizeof(T) == 4;
       gx.out_vec = D % (16 / (int)sizeof(T)) == 0 && on16(dx);
-      e = gemm<kDx>(mz, mw64, gx, (int64_t)tms * tds * gx.splits, false, st);
+      e = gemm<kDx>(mz, mw64, gx, (int64_t)tms * tds * s.most_splits, false, st);
       if (e != cudaSuccess) return e;
-      if (last && pl.splits > 1) {
-        gx.splits = std::min(pl.splits, tiles(pl.piece, kStep));  // of the first piece: no other has more
+      if (last && s.most_splits > 1) {
         e = launch_after(join_dx<T>, (unsigned)std::min<int64_t>(((int64_t)s.n * D + 255) / 256, 8 * device_sm_count()),
                          256u, 0, st, gx);
         if (e != cudaSuccess) return e;
@@ -554,9 +583,10 @@ GemmArgs arguments(const void* x, const int64_t* targets, int n, int D, int V, i
   g.count = s->count;
   g.rows = s->rows;
   g.n = n;
-  g.splits = 1;
   g.passes = pl.parts_of == 1 ? 1 : 6;
-  g.chunk = pl.parts_of == 1 ? kChunk : kChunkParts;
+  // about equal pieces of K
+  const int steps = tiles(D, kStep), pieces = tiles(steps, kChunk);
+  g.chunk = pl.parts_of == 1 ? tiles(steps, pieces) : kChunkParts;
   g.group = kGroup;
   g.targets = targets;
   g.cap = cap;

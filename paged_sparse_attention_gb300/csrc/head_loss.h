@@ -11,13 +11,12 @@ namespace head {
 
 // Rows with a target are gathered: row r of a product is row rows[r] of the caller's, r < *count.
 struct GemmArgs {
-  const int* count;
+  const int* count; // rows with a target; behind it the parts that K of dx is cut into
   const int* rows;
   int n;            // the caller's rows
   int group;        // row tiles whose tiles come one after another
   int tms, tns;     // tiles of rows (kDw) and of columns
   int steps;        // of K (not kDw)
-  int splits;       // K is cut in this many parts (kDx)
   int passes;       // 1, or 6 products of parts
   int chunk;        // steps of K that are summed on the tensor cores
   int row_b;        // first row of the piece in W's map

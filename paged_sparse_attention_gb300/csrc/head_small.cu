@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 2) dot_rows(const __grid_constant__ 
   // [NT, steps of 256 columns], zeros behind a row; of a step first every lane's first four columns, then the
   // others, so that a warp's 16-byte reads lie side by side
   extern __shared__ __align__(16) float xs[];
-  if (DZ) wait_for_launch_before();  // lse may be the launch before's
+  wait_for_launch_before();
   let_next_launch();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int t0 = blockIdx.y * NT, steps = (a.D + 255) / 256, pitch = steps * 256;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_rows(const __grid_constant__
   __shared__ unsigned char has[kMaxRows];
   wait_for_launch_before();
   let_next_launch();
-  for (int t = threadIdx.x; t < a.n; t += kThreads) has[t] = has_target(a, t);
+  for (int t = threadIdx.x; t < a.n; t += blockDim.x) has[t] = has_target(a, t);
   __syncthreads();
   const int group = threadIdx.x / a.ct, c = (blockIdx.y * a.ct + threadIdx.x % a.ct) * kCols;
   const int units = gridDim.x * a.row_groups, unit = blockIdx.x * a.row_groups + group;
@@ -404,17 +404,17 @@ __global__ void __launch_bounds__(kThreads) join_rows(const __grid_constant__ Sm
 
 // ------------------------------------------------------------------ host side
 template <typename K, typename... A>
-cudaError_t launch(K kernel, dim3 grid, size_t smem, bool after, cudaStream_t st, const A&... args) {
+cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr;  // a dependent launch: its set-up overlaps the end of the one before
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = after ? 1 : 0;
+  cfg.numAttrs = 1;
   count_launches(1);
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
@@ -430,7 +430,7 @@ cudaError_t dot(const SmallArgs& a, cudaStream_t st) {
   const cudaError_t e = set_smem_limit((const void*)dot_rows<T, VEC, NT, DZ>, kMaxVectors, set);
   if (e != cudaSuccess) return e;
   return launch(dot_rows<T, VEC, NT, DZ>, dim3((unsigned)dot_blocks(a.V), (unsigned)((a.n + NT - 1) / NT)),
-                NT * vector_bytes(a.D), false, st, a);
+                kThreads, NT * vector_bytes(a.D), st, a);
 }
 template <typename T, bool VEC, bool DZ>
 cudaError_t dot_tokens(const SmallArgs& a, cudaStream_t st) {
@@ -474,14 +474,15 @@ cudaError_t backward(SmallArgs a, int dw_dtype, cudaStream_t st) {
   a.ct = g.ct;
   a.row_groups = g.row_groups;
   a.dw_vec = a.D % 8 == 0 && on16(a.dw);
+  const int threads = (int)align_up((size_t)g.ct * g.row_groups, 32);
   const dim3 grid((unsigned)g.blocks, (unsigned)g.slabs, (unsigned)((a.dx ? (a.n + 7) / 8 : 0) + (a.dw ? 1 : 0)));
   if (dw_dtype == OOMB_FP32)
-    e = vec ? launch(grad_rows<T, float, true>, grid, 0, true, st, a) : launch(grad_rows<T, float, false>, grid, 0, true, st, a);
+    e = vec ? launch(grad_rows<T, float, true>, grid, threads, 0, st, a) : launch(grad_rows<T, float, false>, grid, threads, 0, st, a);
   else
-    e = vec ? launch(grad_rows<T, __nv_bfloat16, true>, grid, 0, true, st, a)
-            : launch(grad_rows<T, __nv_bfloat16, false>, grid, 0, true, st, a);
+    e = vec ? launch(grad_rows<T, __nv_bfloat16, true>, grid, threads, 0, st, a)
+            : launch(grad_rows<T, __nv_bfloat16, false>, grid, threads, 0, st, a);
   if (e != cudaSuccess || !a.dx) return e;
-  return launch(join_rows<T>, dim3((unsigned)((a.D + 31) / 32), (unsigned)a.n), 0, true, st, a, g.blocks * g.row_groups);
+  return launch(join_rows<T>, dim3((unsigned)((a.D + 31) / 32), (unsigned)a.n), kThreads, 0, st, a, g.blocks * g.row_groups);
 }
 
 }  // namespace
@@ -520,7 +521,7 @@ cudaError_t launch_small_fwd(const SmallArgs& a, int dtype, cudaStream_t st) {
   else
     e = vec ? dot_tokens<__nv_bfloat16, true, false>(a, st) : dot_tokens<__nv_bfloat16, false, false>(a, st);
   if (e != cudaSuccess) return e;
-  return launch(join_loss, dim3((unsigned)a.n), 0, true, st, a);
+  return launch(join_loss, dim3((unsigned)a.n), kThreads, 0, st, a);
 }
 
 cudaError_t launch_small_bwd(const SmallArgs& a, int dtype, int dw_dtype, cudaStream_t st) {

@@ -174,6 +174,8 @@ __global__ void __launch_bounds__(THREADS, MIN_BLOCKS) ln_fwd(const __grid_const
   using R = Row<T, E, C>;
   __shared__ __align__(16) float buf[64];
   for (int i = threadIdx.x; i < 64; i += blockDim.x) buf[i] = 0.f;
+  wait_for_launch_before();
+  let_next_launch();
   R next;
   next.clear();
   if (blockIdx.x < a.n) next.load(reinterpret_cast<const T*>(a.x) + (size_t)blockIdx.x * a.D, a.D);
@@ -225,8 +227,9 @@ __global__ void __launch_bounds__(THREADS, MIN_BLOCKS) ln_bwd(const __grid_const
   using R = Row<T, E, C>;
   extern __shared__ __align__(16) uint64_t acc[];  // SHARED: [2 H, T]
   __shared__ __align__(16) float buf[128];
-  let_next_launch();
   for (int i = threadIdx.x; i < 128; i += blockDim.x) buf[i] = 0.f;
+  wait_for_launch_before();
+  let_next_launch();
   R nx, ny, nz;
   float n_mean = 0.f, n_rstd = 0.f;
   auto fetch = [&](int64_t i) {
@@ -340,6 +343,23 @@ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int threads_for(int D, int cols) { return (int)align_up((size_t)(D + cols - 1) / cols, 32); }
 
+// A dependent launch: its set-up overlaps the end of the one before, which the kernel waits for.
+template <typename K, typename... A>
+cudaError_t launch_after(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Columns of a thread: 8 in narrow rows, which have threads to spare.
 int cols_of(int D) { return D <= 2048 ? 8 : 16; }
 // Blocks on an SM: 512 threads, 256 of which have 128 registers each.
@@ -351,10 +371,8 @@ int bwd_blocks(int64_t n, int D) {
 
 template <typename T, int E, int C, int THREADS, int MIN_BLOCKS>
 cudaError_t fwd(const LnArgs& a, int threads, cudaStream_t st) {
-  count_launches(1);
   const int64_t most = (int64_t)(2 * blocks_per_sm(threads)) * device_sm_count();
-  ln_fwd<T, E, C, THREADS, MIN_BLOCKS><<<(unsigned)std::min<int64_t>(a.n, most), threads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(ln_fwd<T, E, C, THREADS, MIN_BLOCKS>, dim3((unsigned)std::min<int64_t>(a.n, most)), threads, 0, st, a);
 }
 template <typename T, int E>
 cudaError_t fwd_width(const LnArgs& a, cudaStream_t st) {
@@ -379,9 +397,7 @@ cudaError_t bwd(const LnArgs& a, int threads, int blocks, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     smem = (size_t)C * threads * 8;
   }
-  count_launches(1);
-  ln_bwd<T, E, C, THREADS, MIN_BLOCKS, SHARED><<<(unsigned)blocks, threads, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(ln_bwd<T, E, C, THREADS, MIN_BLOCKS, SHARED>, dim3((unsigned)blocks), threads, smem, st, a);
 }
 template <typename T, int E>
 cudaError_t bwd_width(const LnArgs& a, int blocks, cudaStream_t st) {
@@ -398,17 +414,7 @@ cudaError_t bwd_any(const LnArgs& a, cudaStream_t st) {
   const bool vec = a.D % E == 0 && on16(a.x) && on16(a.dy) && on16(a.dx_in) && on16(a.dx);
   const cudaError_t e = vec ? bwd_width<T, E>(a, blocks, st) : bwd_width<T, 1>(a, blocks, st);
   if (e != cudaSuccess || (!a.dw && !a.db)) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.D + 31) / 32, 2);
-  cfg.blockDim = dim3(32 * kStrips);
-  cfg.stream = st;
-  cudaLaunchAttribute attr;  // a dependent launch: its set-up overlaps the end of the row kernel
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  count_launches(1);
-  return cudaLaunchKernelEx(&cfg, ln_join, a, blocks);
+  return launch_after(ln_join, dim3((a.D + 31) / 32, 2), 32 * kStrips, 0, st, a, blocks);
 }
 
 oomb_status check_ln(const void* x, const float* w, int n, int D, int dtype) {
