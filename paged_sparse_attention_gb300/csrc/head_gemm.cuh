@@ -183,8 +183,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int tms = MODE == kDw ? p.tms : (count + kTile - 1) / kTile;
   const int steps_all = MODE == kDw ? (count + kStep - 1) / kStep : p.steps;
   const int clusters = gridDim.x / 2, first = blockIdx.x / 2;
-  const int all_splits = MODE == kDx ? p.count[1] : 1, splits = min(all_splits, max(1, steps_all));
-  const bool last = MODE != kDx || (p.last && all_splits == 1);
+  // K in parts: kDx in as many as the rows with a target ask for, kDw in as many as the host says
+  const int all_splits = MODE == kDx ? p.count[1] : MODE == kDw ? p.dw_splits : 1;
+  const int splits = MODE == kDx ? min(all_splits, max(1, steps_all)) : all_splits;
+  const bool last = MODE == kDx ? p.last && all_splits == 1 : all_splits == 1;  // else the sums are kept
   const int tiles = tms * p.tns * splits;
   // steps of K of a tile: its split's share
   auto range = [&](int t, int& k0, int& k1) {
@@ -382,14 +384,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         } else {
-          if (MODE == kDx && (p.add || !last)) {
-            // sums of the pieces before, of this split
+          if ((MODE == kDx && p.add) || !last) {
+            // sums of the pieces before (kDx), of this split
             const int c = lane % 8 * 4;
 #pragma unroll
             for (int r = lane / 8; r < 32; r += 4) {
               if (r >= n_rows || c >= n_cols) break;
-              float* acc = p.acc + ((size_t)split * p.n + row0 + r) * p.acc_pitch + col + c;
-              float4 o = p.add ? *reinterpret_cast<const float4*>(acc) : make_float4(0.f, 0.f, 0.f, 0.f);
+              float* acc = p.acc + ((size_t)split * (MODE == kDx ? p.n : p.cols) + row0 + r) * p.acc_pitch + col + c;
+              float4 o = MODE == kDx && p.add ? *reinterpret_cast<const float4*>(acc) : make_float4(0.f, 0.f, 0.f, 0.f);
               o.x += turn[r * 33 + c];
               o.y += turn[r * 33 + c + 1];
               o.z += turn[r * 33 + c + 2];

@@ -137,8 +137,9 @@ __device__ __forceinline__ float dot_share(const T* x, const T* w, int D, int la
   return v;
 }
 
-// Gathers the rows of x that have a target; forward: forms the targets' logits.  A block takes a contiguous range of rows; how many
-// rows before it have a target it counts itself, so that one launch is enough.
+// Gathers the rows of x that have a target; forward: forms the targets' logits.  A block takes a
+// contiguous range of rows; how many rows before it have a target it counts itself, so that one launch is
+// enough.
 // ROW_WARPS: warps that share a row (all of them where there are few rows).
 constexpr int kStageThreads = 256;
 template <typename T, bool VEC, int ROW_WARPS>
@@ -301,6 +302,21 @@ __global__ void __launch_bounds__(256) join_lse(const __grid_constant__ GemmArgs
   }
 }
 
+// dw of a small piece: its splits' sums, added in order.
+template <typename TW>
+__global__ void __launch_bounds__(256) join_dw(const __grid_constant__ GemmArgs a) {
+  wait_for_launch_before();
+  let_next_launch();
+  const int64_t total = (int64_t)a.cols * a.out_cols;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int r = (int)(i / a.out_cols), c = (int)(i % a.out_cols);
+    float v = 0.f;
+    for (int s = 0; s < a.dw_splits; ++s) v += a.acc[((size_t)s * a.cols + r) * a.acc_pitch + c];
+    TW* to = reinterpret_cast<TW*>(a.out) + (size_t)(a.v0 + r) * a.out_cols + c;
+    *to = from_float<TW>(fmaf(a.scale, v, a.accumulate ? to_float<TW>(*to) : 0.f));
+  }
+}
+
 // dx of few rows: its splits' sums, added in order.
 template <typename T>
 __global__ void __launch_bounds__(256) join_dx(const __grid_constant__ GemmArgs a) {
@@ -333,7 +349,7 @@ struct Plan {
   bool staged;                 // W is read through the workspace
   int piece;                   // columns of a piece (the last may have fewer)
   int pitch_z;
-  size_t count, rows, at, x, w, part, dz, acc, bytes;
+  size_t count, rows, at, x, w, part, dz, acc, acc_w, bytes;
 };
 Plan make_plan(int64_t n, int D, int V, int dtype, bool backward, bool w_on16) {
   Plan p = {};
@@ -369,7 +385,7 @@ Plan make_plan(int64_t n, int D, int V, int dtype, bool backward, bool w_on16) {
   // pieces are the smallest)
   const int64_t staged_pieces = (V + staged_rows - 1) / staged_rows;
   const int64_t staged_piece = (int64_t)align_up((size_t)((V + staged_pieces - 1) / staged_pieces), kTile);
-  const int64_t narrow_rows = std::min<int64_t>(n, (int64_t)kTile * (clusters() / 2 / tiles(staged_piece, kTile)));
+  const int64_t narrow_rows = std::min<int64_t>(n, (int64_t)kTile * (clusters() / tiles(staged_piece, kNarrow)));
   p.part = take(std::max((size_t)n * tiles(V, kHalf), (size_t)narrow_rows * tiles(V, kNarrow / 2)) * 8);
   const size_t forward_bytes = at;
   at = common;
@@ -377,6 +393,7 @@ Plan make_plan(int64_t n, int D, int V, int dtype, bool backward, bool w_on16) {
   p.dz = take(std::min<size_t>(z_bytes * align_up((size_t)V, 64), std::max<size_t>(kDzBytes, z_bytes * kTile)));
   const size_t acc = (size_t)n * align_up((size_t)D, 4) * 4;
   p.acc = take(std::max(acc, std::min(64 * acc, kAccBytes)));
+  p.acc_w = take((size_t)clusters() * kTile * kTile * 4);  // a tile a cluster at most
   p.bytes = backward ? std::max(forward_bytes, at) : forward_bytes;
   return p;
 }
@@ -429,8 +446,9 @@ cudaError_t gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& p, 
   return always || p.passes > 1 ? gemm_of<MODE, true, 256>(a, b, p, most_tiles, st)
                                 : gemm_of<MODE, always, 256>(a, b, p, most_tiles, st);
 }
-// Whether the logits of `rows` and `cols` leave so many clusters without a tile that narrow ones are faster.
-bool is_narrow(int64_t rows, int64_t cols) { return 2 * (int64_t)tiles(rows, kTile) * tiles(cols, kTile) <= clusters(); }
+// Whether every cluster has one narrow tile of the logits of `rows` and `cols` at most.  (A step of K takes a
+// narrow tile 0.30 us and a wide one 0.33, so it does not pay to have more of them.)
+bool is_narrow(int64_t rows, int64_t cols) { return (int64_t)tiles(rows, kTile) * tiles(cols, kNarrow) <= clusters(); }
 
 // What both directions share: the rows with a target, gathered.
 template <typename T>
@@ -559,7 +577,15 @@ cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, ch
       gw.out_fp32 = dw_dtype == OOMB_FP32;
       gw.out_vec = D % (16 / (int)dtype_size(dw_dtype)) == 0 && on16(dw);
       gw.accumulate = accumulate;
-      e = gemm<kDw>(mz64, mx64, gw, (int64_t)gw.tms * tds, false, st);
+      // few tiles: the rows are cut in parts of 8 steps at least
+      gw.dw_splits = std::max(1, std::min(clusters() / (gw.tms * tds), tiles(s.n, kStep) / 8));
+      gw.acc = reinterpret_cast<float*>(ws + pl.acc_w);
+      e = gemm<kDw>(mz64, mx64, gw, (int64_t)gw.tms * tds * gw.dw_splits, false, st);
+      if (e == cudaSuccess && gw.dw_splits > 1) {
+        const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)cols * D + 255) / 256, 8 * device_sm_count());
+        e = dw_dtype == OOMB_FP32 ? launch_after(join_dw<float>, grid, 256u, 0, st, gw)
+                                  : launch_after(join_dw<__nv_bfloat16>, grid, 256u, 0, st, gw);
+      }
       if (e != cudaSuccess) return e;
     }
   }

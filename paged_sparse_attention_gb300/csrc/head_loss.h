@@ -34,8 +34,8 @@ struct GemmArgs {
   __nv_bfloat16* dz;  // [passes == 1 ? 1 : 3, n, pitch]
   int pitch;
   // kDx, kDw
-  float* acc;       // kDx: [splits, n, acc_pitch] sums of the pieces
-  int acc_pitch, add, last;
+  float* acc;       // kDx: [splits, n, acc_pitch] sums of the pieces; kDw: [dw_splits, cols, acc_pitch]
+  int acc_pitch, add, last, dw_splits;
   void* out;
   int out_cols, out_fp32, out_vec, accumulate;
   float scale;

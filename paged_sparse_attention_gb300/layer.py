@@ -160,7 +160,9 @@ class LayerStep:
     # ------------------------------------------------------------------ the step
     def run(self, X, dO, sel_override: Optional[List] = None, Y=None, dX_out=None, positions=None, doc_start=None,
             prefix_len=None) -> dict:
-        """X [N, Dm] (pool dtype, device), dO [N, Hq, d] (pool dtype, device).
+        """X [N, Dm] (pool dtype, device), dO [N, Hq, d] (pool dtype, device), or a function that
+        forms a chunk's dO when the reverse sweep has recomputed its output: dO(first token, o [n, Hq, d])
+        (ModelEnds.behind: the loss of the chunk).
         ``sel_override[c]``: (sel, count) device tensors fed to chunk c's attention
         instead of the library's own selection (which is still computed and returned).
         Returns O (per chunk), sel (the library's selections, per chunk), dX, dWq, dWk,
@@ -255,7 +257,8 @@ class LayerStep:
             a_sel = att[ci]
             self._attend(q, s, a_sel, o, lse)
             dq = torch.empty_like(q)
-            self._attend_bwd(q, o, dO[s:s + n], lse, s, a_sel, dq, ws_bwd)
+            d_o = dO(s, o) if callable(dO) else dO[s:s + n]
+            self._attend_bwd(q, o, d_o, lse, s, a_sel, dq, ws_bwd)
             # the chunk's own dK/dV are complete: back through the rotation and projections
             g = {"q": torch.empty((n, Hq * d), dtype=f32, device=dev),
                  "k": torch.empty((n, Hkv * d), dtype=f32, device=dev),

@@ -137,3 +137,16 @@ def test_python_calls_refuse_host_and_wrong_tensors(lib, monkeypatch):
         L.oomb_word_check(t)
     with pytest.raises(ValueError, match="empty"):
         L.oomb_word_check(word[:0])
+
+
+def test_model_ends_refusals():
+    from paged_sparse_attention_gb300.ends import ModelEnds
+    t = torch.zeros(10, 8)
+    for kw, match in ((dict(head=torch.zeros(9, 8)), "one dtype"), (dict(head=t.bfloat16()), "one dtype"),
+                      (dict(b_norm=torch.zeros(8)), "w_norm"), (dict(chunk=0), "positive")):
+        with pytest.raises(ValueError, match=match):
+            ModelEnds(t, **kw)
+    with pytest.raises(ValueError, match="one dtype"):
+        ModelEnds(t[0])
+    ends = ModelEnds(t, chunk=4)  # (nothing runs before the first call)
+    assert ends.d_head is ends.d_table and ends.ws.numel() > 0
