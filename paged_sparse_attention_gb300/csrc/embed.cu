@@ -6,7 +6,8 @@
 // Forward: one pass, a row a group of threads; bound by HBM (distinct rows read, all written).
 //
 // Backward: rows of one token are summed by one owner in row order, so there are no float
-// atomics and the gradient is the same bits on every run.  Three or four launches:
+// atomics and the gradient is the same bits on every run.  Up to 32 rows: sum_few, whose warps see all
+// tokens at once.  More, in three or four launches:
 //   rank_tokens   the stable order of up to kSection tokens: a token's place is the number of those
 //                 that come before it, counted by a warp's 32 tokens against all.  67 million
 //                 comparisons for 8192, on every SM and without a pass that waits for another: 13.7 us.
@@ -315,6 +316,47 @@ __global__ void __launch_bounds__(128) merge_sections(const __grid_constant__ Em
 }
 
 // ------------------------------------------------------------------ sums
+// Up to 32 rows.  A warp takes 32 E columns; lane i holds token i, and the lanes that hold the same one are
+// known to all.  The tokens' sums are dealt out over grid.y.
+template <typename T, int E>
+__global__ void __launch_bounds__(128) sum_few(const __grid_constant__ EmbedArgs a) {
+  wait_for_launch_before();
+  let_next_launch();
+  const int lane = threadIdx.x % 32, c = ((blockIdx.x * 4 + threadIdx.x / 32) * 32 + lane) * E;
+  const int key = lane < a.n ? key_of(a.tokens[lane], a.V, a.err) : kNone;
+  const unsigned same = __match_any_sync(0xffffffffu, key);
+  unsigned firsts = __ballot_sync(0xffffffffu, key != kNone && lane == __ffs(same) - 1);
+  for (int k = 0; firsts; firsts &= firsts - 1, ++k) {
+    if (k % gridDim.y != blockIdx.y) continue;
+    const int first = __ffs(firsts) - 1, token = __shfl_sync(0xffffffffu, key, first);
+    unsigned rows = __shfl_sync(0xffffffffu, same, first);
+    if (c >= a.D) continue;
+    float* to = a.d_table + (size_t)token * a.D + c;
+    float old[E], sum[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) old[e] = sum[e] = 0.f;
+    if (a.accumulate) load_e<float, E>(to, old);
+    while (rows) {
+      constexpr int B = 4;  // asked for together
+      float f[B][E];
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[u][e] = 0.f;
+        if (rows) load_e<T, E>(reinterpret_cast<const T*>(a.d_out) + (size_t)(__ffs(rows) - 1) * a.D + c, f[u]);
+        rows &= rows - 1;  // (0 stays 0)
+      }
+#pragma unroll
+      for (int u = 0; u < B; ++u)
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e] += f[u][e];
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] = fmaf(a.scale, sum[e], old[e]);
+    store_e<float, E>(to, sum);
+  }
+}
+
 // Where the partial sum of a piece of window w is kept: one may come from the window before (it
 // starts the window), one more may go on into the next.
 __device__ __forceinline__ size_t piece_slot(int64_t w, bool first) { return (size_t)w * 2 + (first ? 1 : 0); }
@@ -563,6 +605,10 @@ size_t sort_smem_set[kMaxDevices] = {};
 
 template <typename T, int E, int NV>
 cudaError_t backward(const EmbedArgs& a, cudaStream_t st) {
+  if (a.n <= 32) {
+    const int64_t warps = ((int64_t)a.D + 32 * E - 1) / (32 * E);
+    return launch_after(sum_few<T, E>, dim3((unsigned)((warps + 3) / 4), (unsigned)std::min<int64_t>(a.n, 16)), 128, a, st);
+  }
   const unsigned sections = (unsigned)((a.n + kSection - 1) / kSection);
   cudaError_t e = cudaSuccess;
   if (sections == 1) {

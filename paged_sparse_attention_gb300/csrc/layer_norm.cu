@@ -292,8 +292,10 @@ __global__ void __launch_bounds__(THREADS, MIN_BLOCKS) ln_bwd(const __grid_const
     }
     R::store(reinterpret_cast<T*>(a.dx) + (size_t)i * a.D, a.D, t);
   }
-  float* to[2] = {a.dw ? a.part + (size_t)blockIdx.x * a.D : nullptr,
-                  a.db ? a.part + ((size_t)gridDim.x + blockIdx.x) * a.D : nullptr};
+  // one block has the whole sums, several leave theirs in the workspace
+  const bool whole = gridDim.x == 1;
+  float* to[2] = {whole ? a.dw : a.dw ? a.part + (size_t)blockIdx.x * a.D : nullptr,
+                  whole ? a.db : a.db ? a.part + ((size_t)gridDim.x + blockIdx.x) * a.D : nullptr};
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     if (!to[g]) continue;
@@ -312,7 +314,10 @@ __global__ void __launch_bounds__(THREADS, MIN_BLOCKS) ln_bwd(const __grid_const
     for (int v = 0; v < C / E; ++v)
       if (R::col(v) < a.D)
 #pragma unroll
-        for (int e = 0; e < E; ++e) to[g][R::col(v) + e] = x[v * E + e];
+        for (int e = 0; e < E; ++e) {
+          float* p = to[g] + R::col(v) + e;
+          *p = whole && a.accumulate ? *p + x[v * E + e] : x[v * E + e];
+        }
   }
 }
 
@@ -364,8 +369,11 @@ cudaError_t launch_after(K kernel, dim3 grid, int threads, size_t smem, cudaStre
 int cols_of(int D) { return D <= 2048 ? 8 : 16; }
 // Blocks on an SM: 512 threads, 256 of which have 128 registers each.
 int blocks_per_sm(int T) { return std::max(1, std::min(16, 512 / T)); }
-// Blocks of the backward, each with its own parts of the parameter gradients.
+// Blocks of the backward, each with its own parts of the parameter gradients.  Few rows take one, and a
+// launch less (a row after another takes it 0.6 us).
+constexpr int kOneBlock = 16;
 int bwd_blocks(int64_t n, int D) {
+  if (n <= kOneBlock) return 1;
   return (int)std::min<int64_t>(n, (int64_t)blocks_per_sm(threads_for(D, cols_of(D))) * device_sm_count());
 }
 
@@ -413,7 +421,7 @@ cudaError_t bwd_any(const LnArgs& a, cudaStream_t st) {
   const int blocks = bwd_blocks(a.n, a.D);
   const bool vec = a.D % E == 0 && on16(a.x) && on16(a.dy) && on16(a.dx_in) && on16(a.dx);
   const cudaError_t e = vec ? bwd_width<T, E>(a, blocks, st) : bwd_width<T, 1>(a, blocks, st);
-  if (e != cudaSuccess || (!a.dw && !a.db)) return e;
+  if (e != cudaSuccess || (!a.dw && !a.db) || blocks == 1) return e;
   return launch_after(ln_join, dim3((a.D + 31) / 32, 2), 32 * kStrips, 0, st, a, blocks);
 }
 
