@@ -379,7 +379,9 @@ int bwd_blocks(int64_t n, int D) {
 
 template <typename T, int E, int C, int THREADS, int MIN_BLOCKS>
 cudaError_t fwd(const LnArgs& a, int threads, cudaStream_t st) {
-  const int64_t most = (int64_t)(2 * blocks_per_sm(threads)) * device_sm_count();
+  // as many blocks as are resident: each walks its rows with the next one in flight
+  constexpr int kRegisters = 65536 / (THREADS * MIN_BLOCKS);
+  const int64_t most = (int64_t)std::min(16, 65536 / (kRegisters * threads)) * device_sm_count();
   return launch_after(ln_fwd<T, E, C, THREADS, MIN_BLOCKS>, dim3((unsigned)std::min<int64_t>(a.n, most)), threads, 0, st, a);
 }
 template <typename T, int E>
