@@ -67,12 +67,21 @@ __device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_
       : "memory");
 }
 // Arrives on this barrier in both CTAs once every MMA issued so far is complete.
-__device__ __forceinline__ void commit2(uint64_t* bar) {
+__device__ __forceinline__ void commit2(uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
       "h"((uint16_t)3)
       : "memory");
+}
+// Whether a barrier's phase has been passed; does not wait.
+__device__ __forceinline__ bool passed(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 // The same, on this CTA's barrier only.
 __device__ __forceinline__ void commit_own(uint64_t* bar) {
@@ -198,7 +207,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------------ loads
     if (lane == 0) {
-      const uint32_t full0 = mapa_shared(smem_u32(&bar.full[0]), 0);
+      const uint32_t full0 = mapa_shared(smem_u32(&bar.full[0]), 0), empty0 = smem_u32(&bar.empty[0]);
       int s = 0, it = 0;
       uint32_t phase = 1;  // of the stage before: the first round finds the stages empty
       bool ok = true;
@@ -208,30 +217,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         range(t, k0, k1);
         const int ra = tm * kTile + (int)rank * kHalf, rb = tn * TN + (int)rank * kCols;
         const int chunk = CHUNKED ? p.chunk : max(1, k1 - k0);
-        for (int c0 = k0; ok && c0 < k1; c0 += chunk)
-        for (int q = 0; ok && q < p.passes; ++q) {
-          const int pa = part_a(p.passes, q), pb = part_b(p.passes, q), c1 = min(k1, c0 + chunk);
-          for (int k = c0; k < c1; ++k) {
-            if (it >= kStages) ok = mbar_wait(&bar.empty[s], phase, p.err, abort);
-            if (!ok) break;
-            if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], 2 * kStageBytes);
-            const uint32_t a = base + s * kStageBytes, b = a + kOperand, f = full0 + 8 * s;
-            if (kAmn) {
-              tma_load2(a, &ta, f, ra, k * kStep, pa);
-              tma_load2(a + kOperand / 2, &ta, f, ra + 64, k * kStep, pa);
-            } else {
-              tma_load2(a, &ta, f, k * kStep, ra, pa);
-            }
-            if (kBmn) {
-              tma_load2(b, &tb, f, rb, p.row_b + k * kStep, pb);
-              tma_load2(b + kOperand / 2, &tb, f, rb + 64, p.row_b + k * kStep, pb);
-            } else {
-              tma_load2(b, &tb, f, k * kStep, p.row_b + rb, pb);
-            }
-            ++it;
-            if (++s == kStages) {
-              s = 0;
-              phase ^= 1;
+        for (int c0 = k0; ok && c0 < k1; c0 += chunk) {
+          const int c1 = min(k1, c0 + chunk);
+          for (int q = 0; ok && q < p.passes; ++q) {
+            const int pa = part_a(p.passes, q), pb = part_b(p.passes, q);
+            for (int k = c0; k < c1; ++k) {
+              if (it >= kStages && !passed(empty0 + 8 * s, phase)) {
+                ok = mbar_wait(&bar.empty[s], phase, p.err, abort);
+                if (!ok) break;
+              }
+              if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], 2 * kStageBytes);
+              const uint32_t a = base + s * kStageBytes, b = a + kOperand, f = full0 + 8 * s;
+              if (kAmn) {
+                tma_load2(a, &ta, f, ra, k * kStep, pa);
+                tma_load2(a + kOperand / 2, &ta, f, ra + 64, k * kStep, pa);
+              } else {
+                tma_load2(a, &ta, f, k * kStep, ra, pa);
+              }
+              if (kBmn) {
+                tma_load2(b, &tb, f, rb, p.row_b + k * kStep, pb);
+                tma_load2(b + kOperand / 2, &tb, f, rb + 64, p.row_b + k * kStep, pb);
+              } else {
+                tma_load2(b, &tb, f, k * kStep, p.row_b + rb, pb);
+              }
+              ++it;
+              if (++s == kStages) {
+                s = 0;
+                phase ^= 1;
+              }
             }
           }
         }
@@ -249,8 +262,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ products
+    // One thread issues them all, so its instructions a step have to take less time than the step's
+    // products (512 cycles of a wide tile): descriptors are added to, not formed, and a barrier that has
+    // been passed already costs one test (4096 rows on 131072 x 3584: 2295 to 2276 us).
     if (lane == 0 && rank == 0) {
       const uint32_t idesc = idesc_bf16_f32(kTile, TN, kAmn, kBmn);
+      constexpr uint64_t kNextA = (kAmn ? 2048 : 32) >> 4, kNextB = (kBmn ? 2048 : 32) >> 4;  // 16 columns of K on
+      const uint64_t a0 = kAmn ? tc::desc_mnmajor(base, 0, kOperand / 2) : tc::desc_kmajor(base, 0);
+      const uint64_t b0 =
+          kBmn ? tc::desc_mnmajor(base + kOperand, 0, kOperand / 2) : tc::desc_kmajor(base + kOperand, 0);
+      const uint32_t full0 = smem_u32(&bar.full[0]), empty0 = smem_u32(&bar.empty[0]);
+      uint64_t da = a0, db = b0;
       int s = 0, n = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -260,32 +282,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int chunk = CHUNKED ? p.chunk : max(1, k1 - k0);
         int c0 = k0;
         do {  // one turn without products where K is empty
-        const int buf = n & 1, len = min(k1, c0 + chunk) - c0;
-        if (n >= 2) ok = mbar_wait(&bar.tile_empty[buf], (uint32_t)((n / 2 - 1) & 1), p.err, abort);
-        tc_fence_after();
-        const uint32_t d = tmem + buf * kTile;
-        uint32_t acc = 0;
-        for (int k = 0; ok && k < len * p.passes; ++k) {
-          ok = mbar_wait(&bar.full[s], phase, p.err, abort);
-          if (!ok) break;
+          const int buf = n & 1;
+          if (n >= 2) ok = mbar_wait(&bar.tile_empty[buf], (uint32_t)((n / 2 - 1) & 1), p.err, abort);
           tc_fence_after();
-          const uint32_t a = base + s * kStageBytes, b = a + kOperand;
-#pragma unroll
-          for (int kk = 0; kk < kStep / 16; ++kk) {
-            const uint64_t da = kAmn ? tc::desc_mnmajor(a, kk, kOperand / 2) : tc::desc_kmajor(a, kk);
-            const uint64_t db = kBmn ? tc::desc_mnmajor(b, kk, kOperand / 2) : tc::desc_kmajor(b, kk);
+          const uint32_t d = tmem + buf * kTile;
+          uint32_t acc = 0;
+          for (int k = (min(k1, c0 + chunk) - c0) * p.passes; ok && k > 0; --k) {
+            if (!passed(full0 + 8 * s, phase)) {
+              ok = mbar_wait(&bar.full[s], phase, p.err, abort);
+              if (!ok) break;
+            }
+            tc_fence_after();
             mma2(d, da, db, idesc, acc);
+            mma2(d, da + kNextA, db + kNextB, idesc, 1);
+            mma2(d, da + 2 * kNextA, db + 2 * kNextB, idesc, 1);
+            mma2(d, da + 3 * kNextA, db + 3 * kNextB, idesc, 1);
             acc = 1;
+            commit2(empty0 + 8 * s);
+            da += kStageBytes >> 4;
+            db += kStageBytes >> 4;
+            if (++s == kStages) {
+              s = 0;
+              phase ^= 1;
+              da = a0;
+              db = b0;
+            }
           }
-          commit2(&bar.empty[s]);
-          if (++s == kStages) {
-            s = 0;
-            phase ^= 1;
-          }
-        }
-        if (ok) commit2(&bar.tile_full[buf]);
-        ++n;
-        c0 += chunk;
+          if (ok) commit2(smem_u32(&bar.tile_full[buf]));
+          ++n;
+          c0 += chunk;
         } while (ok && c0 < k1);
       }
       // every MMA has ended before tensor memory is given back
