@@ -90,10 +90,22 @@ def test_embed_matches(dtype, kind, n, V, D):
                 scale=1.0 if n % 2 else 45.25)
 
 
-@pytest.mark.parametrize("runs", [[64], [65], [128], [129], [1, 64, 1], [63, 65, 64], [16, 16, 16, 200], [3, 300, 2, 70, 64],
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 34])
+def test_embed_few_rows(dtype, n):
+    """On both sides of the gradient in one launch."""
+    g = torch.Generator().manual_seed(n)
+    for kind, V, D in (("few", 9, 264), ("distinct", 50, 33), ("padded", 2 ** 20, 8), ("same", 3, 5000), ("none", 5, 8)):
+        t = ids(kind, n, V, g)
+        for acc in (True, False):
+            check_embed(t, torch.randn(V, D, generator=g).to(dtype), torch.randn(n, D, generator=g).to(dtype), scale=0.3,
+                        accumulate=acc)
+
+
+@pytest.mark.parametrize("runs", [[16], [17], [33], [15, 2, 15], [5, 600, 5], [513, 513], [64], [65], [128], [129], [1, 64, 1], [63, 65, 64], [16, 16, 16, 200], [3, 300, 2, 70, 64],
                                   [65, 65, 65, 65], [1] * 40 + [90] + [1] * 20 + [66]])
 def test_runs_around_the_piece(runs):
-    """Tokens that occur a piece's rows, one more, two pieces; long runs next to one another."""
+    """Tokens that occur a window's rows, one more, two windows; long runs next to one another."""
     g = torch.Generator().manual_seed(len(runs))
     t = torch.cat([torch.full((m,), 2 * i) for i, m in enumerate(runs)])
     n, V = t.numel(), 2 * len(runs) + 3
@@ -320,6 +332,27 @@ def test_constant_rows_and_no_eps():
     t = ln_make(4, 128, BF, seed=4)
     ref, tol = ln_reference(t, 0.0, BF)
     check(ln_run(t, 0.0), ref, tol)
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 33])
+def test_layer_norm_few_rows_accumulate(n):
+    """Up to 16 rows are one block's, which adds to the parameter gradients itself; one gradient alone."""
+    for D in (40, 2056, 5000):
+        t = ln_make(n, D, BF, seed=n)
+        ref, tol = ln_reference(t, 1e-5, BF)
+        a, c = ln_run(t, 1e-5), ln_run(t, 1e-5, accumulate=True, base=2.0)
+        check(a, ref, tol)
+        for k in ("dw", "db"):
+            assert torch.equal(c[k], a[k] + 2.0)
+        d = {k: v.cuda() for k, v in t.items()}
+        mean, rstd = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        L.oomb_layer_norm_fwd(d["x"], d["w"], d["b"], torch.empty_like(d["x"]), mean=mean, rstd=rstd)
+        ws = torch.empty(L.oomb_layer_norm_workspace(n, D), dtype=torch.uint8, device="cuda")
+        for key in ("dw", "db", None):
+            g = torch.full((D,), 7.0, device="cuda")
+            L.oomb_layer_norm_bwd(d["x"], d["w"], mean, rstd, d["dy"], torch.empty_like(d["x"]), dx_out=d["dx_out"],
+                                  workspace=ws, **({key: g} if key else {}))
+            assert torch.equal(g, a[key] if key else torch.full_like(g, 7.0))
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])

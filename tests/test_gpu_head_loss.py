@@ -85,15 +85,16 @@ def test_several_pieces_of_the_vocabulary():
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
-def test_rows_without_a_target(dtype):
+@pytest.mark.parametrize("n", [150, 24])
+def test_rows_without_a_target(dtype, n):
     """No row has one; or only a few do, and the others hold infinities and NaN."""
-    x, w, t, _ = make(150, 300, 64, dtype, seed=1)
+    x, w, t, _ = make(n, 300, 64, dtype, seed=1)
     none = torch.full_like(t, -1)
     out = run(x, w, none)
     for k in ("loss", "lse", "dx", "dw"):
         assert (out[k] == 0).all(), k
     few = none.clone()
-    few[[3, 127, 128, 149]] = t[[3, 127, 128, 149]]
+    few[[3, n * 5 // 6, n - 2, n - 1]] = t[[3, n * 5 // 6, n - 2, n - 1]]
     bad = x.clone()
     bad[few < 0] = float("nan")
     bad[0, 0], bad[1, 1] = float("inf"), float("-inf")
@@ -122,8 +123,26 @@ def test_a_target_behind_the_vocabulary_is_told():
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
-def test_one_gradient_alone_and_fp32_weights_gradient(dtype):
-    x, w, t, g = make(140, 700, 88, dtype, seed=5, masked=0.1)
+@pytest.mark.parametrize("cap", [3e2, 1e5, 1e30, 1e-3, 1e-30])
+@pytest.mark.parametrize("n", [20, 100])
+def test_caps_far_above_and_below_the_logits(dtype, cap, n):
+    """A cap far above the logits leaves them as they are; under one far below they are all alike."""
+    x, w, t, _ = make(n, 500, 72, dtype, seed=17)
+    ref, tol = head_reference(x, w, t, cap=cap)
+    check(run(x, w, t, cap=cap), ref, tol)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_the_widest_rows(dtype):
+    x, w, t, g = make(3, 5, 65536, dtype, seed=19)
+    ref, tol = head_reference(x, w, t, d_loss=g)
+    check(run(x, w, t, d_loss=g), ref, tol)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("n", [140, 20])
+def test_one_gradient_alone_and_fp32_weights_gradient(dtype, n):
+    x, w, t, g = make(n, 700, 88, dtype, seed=5, masked=0.1)
     both = run(x, w, t, d_loss=g)
     assert torch.equal(run(x, w, t, d_loss=g, dw=False)["dx"], both["dx"])
     assert torch.equal(run(x, w, t, d_loss=g, dx=False)["dw"], both["dw"])
@@ -138,8 +157,9 @@ def test_one_gradient_alone_and_fp32_weights_gradient(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
-def test_the_same_bits_on_every_run(dtype):
-    x, w, t, g = make(300, 5000, 200, dtype, seed=9, masked=0.3)
+@pytest.mark.parametrize("n", [300, 7])
+def test_the_same_bits_on_every_run(dtype, n):
+    x, w, t, g = make(n, 5000, 200, dtype, seed=9, masked=0.3)
     a, b = run(x, w, t, cap=30.0, d_loss=g), run(x, w, t, cap=30.0, d_loss=g)
     for k in a:
         assert torch.equal(a[k], b[k]), k
@@ -205,6 +225,28 @@ def test_large_and_far_logits():
         check(run(x, w, t, cap=cap), ref, tol)
 
 
+def test_two_calls_at_once_on_two_streams():
+    """Each with a workspace of its own, one of them for few rows; the error word is shared."""
+    sets = [make(n, 3000, 256, BF, seed=n, masked=0.2) for n in (500, 5, 300)]
+    want = [run(x, w, t, d_loss=g) for x, w, t, g in sets]
+    err, jobs = word(), []
+    for x, w, t, g in sets:
+        x, w, t, g = x.cuda(), w.cuda(), t.cuda(), g.cuda()
+        ws = torch.empty(L.oomb_head_loss_workspace(x.shape[0], 256, 3000, BF, True), dtype=torch.uint8, device="cuda")
+        out = {"loss": torch.empty_like(g), "lse": torch.empty_like(g), "dx": torch.empty_like(x), "dw": torch.empty_like(w)}
+        jobs.append((torch.cuda.Stream(), x, w, t, g, ws, out))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, x, w, t, g, ws, out in jobs:
+            L.oomb_head_loss_fwd(x, w, t, out["loss"], out["lse"], ws, err, stream=s)
+            L.oomb_head_loss_bwd(x, w, t, out["lse"], out["dx"], out["dw"], ws, err, d_loss=g, stream=s)
+    torch.cuda.synchronize()
+    assert L.oomb_word_check(err) == 0
+    for job, ref in zip(jobs, want):
+        for k in ref:
+            assert torch.equal(job[6][k], ref[k]), k
+
+
 def test_gradients_against_differences():
     x, w, t, g = make(4, 30, 16, FP, seed=6)
     kw = dict(cap=3.0, d_loss=g, scale=0.7)
@@ -240,8 +282,9 @@ def test_workspace_of_a_longer_call_and_nothing_behind_it():
         check(run(x, w, t, ws=big), ref, tol)
 
 
-def test_graph_replays_on_a_side_stream_with_new_data():
-    n, V, D = 150, 2000, 128
+@pytest.mark.parametrize("n", [150, 6])
+def test_graph_replays_on_a_side_stream_with_new_data(n):
+    V, D = 2000, 128
     x, w, t, g = make(n, V, D, BF, seed=1, masked=0.2)
     xs, wsd, ts, gs = x.cuda(), w.cuda(), t.cuda(), g.cuda()
     out = {"loss": torch.empty(n, device="cuda"), "lse": torch.empty(n, device="cuda"), "dx": torch.empty_like(xs),
