@@ -675,7 +675,7 @@ size_t oomb_head_loss_workspace(int n, int D, int V, int dtype, int backward) {
   if (n <= 0 || D <= 0 || D > kMaxWidth || V <= 0 || V > INT_MAX - 1024 || (dtype != OOMB_BF16 && dtype != OOMB_FP32)) return 0;
   // grows with n: fewer rows may go either way
   SmallSpace s;
-  const int few = std::min(n, small_rows(D, V));
+  const int few = std::min(n, small_rows(D, V, dtype));
   return std::max(make_plan(n, D, V, dtype, backward != 0, true).bytes,
                   few > 0 ? small_space(few, D, V, backward != 0, &s) : 0);
 }
@@ -689,7 +689,7 @@ oomb_status oomb_head_loss_fwd(const void* x, const void* w, const int64_t* targ
   if (reinterpret_cast<uintptr_t>(loss) % 4) return OOMB_ERR_ALIGN;
   if (!workspace || ws_bytes < oomb_head_loss_workspace(n, D, V, dtype, 0)) return OOMB_ERR_WORKSPACE;
   char* ws = reinterpret_cast<char*>(workspace);
-  if (n <= small_rows(D, V)) {
+  if (n <= small_rows(D, V, dtype)) {
     SmallArgs a = small_arguments(x, w, targets, n, D, V, softcap, false, ws, error_word);
     a.loss = loss;
     a.lse = lse;
@@ -723,7 +723,7 @@ oomb_status oomb_head_loss_bwd(const void* x, const void* w, const int64_t* targ
     return OOMB_ERR_ALIGN;
   if (!workspace || ws_bytes < oomb_head_loss_workspace(n, D, V, dtype, 1)) return OOMB_ERR_WORKSPACE;
   char* ws = reinterpret_cast<char*>(workspace);
-  if (n <= small_rows(D, V)) {
+  if (n <= small_rows(D, V, dtype)) {
     SmallArgs a = small_arguments(x, w, targets, n, D, V, softcap, true, ws, error_word);
     a.scale = scale;
     a.lse_in = lse;

@@ -43,9 +43,16 @@ struct GemmArgs {
 };
 
 // ---- few rows and small problems (head_small.cu)
-constexpr int kFewRows = 8;                  // rows that always take it
-constexpr int64_t kSmallWork = 1 << 24;      // products n V D up to which more rows do
-constexpr int kMaxRows = 64;                 // and how many more
+// What goes there, by the operands' type: fp32 costs the tensor cores six products, these cores one.
+// Both sides measured, forward and backward, us on CUDA cores / tensor cores, n of V x D:
+//   bf16:  12 of 10000 x 1000: 81 / 63   32 of 2000 x 1000: 70 / 48   64 of 1000 x 256: 35 / 41
+//          48 of 1000 x 500: 55 / 49     32 of 8000 x 64: 67 / 41
+//   fp32:  16 of 30000 x 4096: 1110 / 1572   24 of the same: 1599 / 1592   24 of 10000 x 1000: 179 / 180
+//          64 of 1000 x 1000: 76 / 116   128 of 1000 x 500: 150 / 90   32 of 8000 x 64: 78 / 71
+constexpr int kFewRows = 8, kFewRows32 = 16;  // rows that always take it (bf16, fp32)
+constexpr int64_t kSmallWork = 1 << 24, kSmallWork32 = 1 << 26;  // products n V D up to which more rows do
+constexpr int kSmallWidth = 256;              // a logit costs as much as of this many columns at least
+constexpr int kMaxRows = 64;                  // and how many more
 
 struct SmallArgs {
   const void* x;
@@ -75,7 +82,7 @@ struct SmallSpace {
   int parts, pitch, acc_pitch;
 };
 // Rows up to which a problem goes this way (0: none do).
-int small_rows(int D, int V);
+int small_rows(int D, int V, int dtype);
 // Bytes of workspace, and what lies where.
 size_t small_space(int n, int D, int V, bool backward, SmallSpace* s);
 cudaError_t launch_small_fwd(const SmallArgs& a, int dtype, cudaStream_t st);

@@ -1,6 +1,6 @@
 // The loss over a vocabulary (head_loss.cu) for few rows, and for small problems, on the CUDA cores.
 //
-// One to eight rows leave nearly all of a tensor-core tile empty and W is what has to be read: a warp
+// A few rows leave nearly all of a tensor-core tile empty and W is what has to be read: a warp
 // takes four of W's rows at a time, whole rows in order, and the vectors x of up to eight tokens stand
 // in shared memory in fp32.  A warp's 4 x 8 sums are joined over its lanes by a transposing
 // reduction (31 shuffles for 32 sums), after which each lane has one logit.  fp32 arithmetic throughout,
@@ -487,10 +487,11 @@ cudaError_t backward(SmallArgs a, int dw_dtype, cudaStream_t st) {
 
 }  // namespace
 
-int small_rows(int D, int V) {
+int small_rows(int D, int V, int dtype) {
   if (vector_bytes(D) > kMaxVectors) return 0;
-  const int64_t rows = kSmallWork / ((int64_t)D * V);
-  return (int)std::min<int64_t>(kMaxRows, std::max<int64_t>(kFewRows, rows));
+  const bool fp32 = dtype == OOMB_FP32;
+  const int64_t rows = (fp32 ? kSmallWork32 : kSmallWork) / ((int64_t)std::max(D, kSmallWidth) * V);
+  return (int)std::min<int64_t>(kMaxRows, std::max<int64_t>(fp32 ? kFewRows32 : kFewRows, rows));
 }
 
 size_t small_space(int n, int D, int V, bool backward, SmallSpace* s) {

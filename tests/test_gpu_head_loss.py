@@ -213,6 +213,16 @@ def test_the_ways_of_few_rows_and_few_tiles(dtype, n, V, D):
     check(out, ref, tol)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("n,V,D", [(8, 9000, 520), (16, 9000, 520), (17, 9000, 520), (24, 3000, 40), (64, 1000, 1000),
+                                   (65, 1000, 100)])
+def test_both_sides_of_the_rows_that_count_as_few(dtype, n, V, D):
+    x, w, t, g = make(n, V, D, dtype, seed=V, masked=0.1)
+    kw = dict(cap=9.0, d_loss=g, scale=0.1)
+    ref, tol = head_reference(x, w, t, **kw)
+    check(run(x, w, t, **kw), ref, tol)
+
+
 def test_large_and_far_logits():
     """Logits of thousands in both signs: the loss of a sure row is the distance, and nothing overflows."""
     D, V = 64, 600
