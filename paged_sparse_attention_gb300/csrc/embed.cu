@@ -8,11 +8,12 @@
 // Backward: rows of one token are summed by one owner in row order, so there are no float
 // atomics and the gradient is the same bits on every run.  Up to 32 rows: sum_few, whose warps see all
 // tokens at once.  More, in three or four launches:
-//   rank_tokens   the stable order of up to kSection tokens: a token's place is the number of those
-//                 that come before it, counted by a warp's 32 tokens against all.  67 million
-//                 comparisons for 8192, on every SM and without a pass that waits for another: 13.7 us.
-//   sort_tokens   instead, for more: a section of kSection a block, by a radix sort of 6 bits a pass in
-//                 shared memory (20 us for one section or many; for 8192 tokens too).
+//   rank_tokens   the stable order of a section: a token's place is the number of those that come
+//                 before it, counted by a warp's 32 tokens against the section's.  No pass waits for another
+//                 and every SM has a part.  8192 tokens in sections of 1024, with the merge: 4 us less than
+//                 at once, 14 less than sorted.
+//   sort_tokens   instead, for many tokens: a section a block, by a radix sort of 6 bits a pass in
+//                 shared memory (20 us for one section or nine).
 //   merge_sections  where there are several sections: a key's rank among all keys is the sum of its
 //                 places in every section, found by binary search.
 //   sum_runs      the sorted rows in windows of kWindow.  The rows of one token in one window are a
@@ -29,7 +30,9 @@
 namespace oomb {
 namespace {
 
-constexpr int kSection = 8192;  // rows whose order is found at once: 32 KB of tokens
+constexpr int kRankAll = 4096;       // tokens up to which every one is ranked among all
+constexpr int kRankSection = 1024, kRankMost = 28 * 1024;  // ranked in sections up to so many, sorted in sections of
+constexpr int kSection = 8192;       // these above
 constexpr int kRankKeys = 32, kRankWarps = 16;  // of a block of rank_tokens: tokens, warps that share the comparisons
 constexpr int kSortThreads = 1024, kSortKeys = kSection / kSortThreads;
 constexpr int kDigit = 6;       // bits a pass
@@ -117,22 +120,25 @@ __global__ void __launch_bounds__(256) embed_rows(const __grid_constant__ EmbedA
 // ----------------------------------------------------------------- ordering
 // Tokens before the warp's own count when they are not greater, those behind when they are smaller:
 // equal tokens keep their order.
+template <int SECTION>
 __global__ void __launch_bounds__(32 * kRankWarps) rank_tokens(const __grid_constant__ EmbedArgs a) {
-  __shared__ __align__(16) int keys[kSection];
+  __shared__ __align__(16) int keys[SECTION];
   __shared__ int parts[kRankWarps][kRankKeys];
-  constexpr int T = 32 * kRankWarps, K = kSection / T;
+  constexpr int T = 32 * kRankWarps, K = SECTION / T;
   wait_for_launch_before();
   let_next_launch();
   if (blockIdx.x == 0 && threadIdx.x == 0) a.n_long[0] = a.n_long[1] = 0;
-  const int m = (int)a.n, own = blockIdx.x * kRankKeys, m4 = (m + 3) & ~3;
+  const int64_t first = (int64_t)blockIdx.x * kRankKeys / SECTION * SECTION;  // of the block's section
+  const int m = (int)min((int64_t)SECTION, a.n - first), own = (int)((int64_t)blockIdx.x * kRankKeys - first), m4 = (m + 3) & ~3;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t* tokens = a.tokens + first;
   int64_t token[K];
 #pragma unroll
-  for (int k = 0; k < K; ++k) token[k] = threadIdx.x + k * T < m ? a.tokens[threadIdx.x + k * T] : -1;
+  for (int k = 0; k < K; ++k) token[k] = threadIdx.x + k * T < m ? tokens[threadIdx.x + k * T] : -1;
 #pragma unroll
   for (int k = 0; k < K; ++k) keys[threadIdx.x + k * T] = key_of(token[k], a.V, a.err);
   __syncthreads();
-  const int mine = keys[own + lane];  // (own + lane < kSection; behind the last it is kNone and not used)
+  const int mine = keys[own + lane];  // (own + lane < SECTION; behind the last it is kNone and not used)
   // x < y as the sign of x - y: both lie in [0, 2^31)
   auto below = [](int x, int y) { return (unsigned)(x - y) >> 31; };
   unsigned c0 = 0, c1 = 0, c2 = 0, c3 = 0;
@@ -161,8 +167,9 @@ __global__ void __launch_bounds__(32 * kRankWarps) rank_tokens(const __grid_cons
   int at = 0;
 #pragma unroll
   for (int p = 0; p < kRankWarps; ++p) at += parts[p][lane];
-  a.sorted[at] = mine;
-  a.order[at] = own + lane;
+  const bool alone = a.n <= SECTION;
+  (alone ? a.sorted : a.sec_sorted)[first + at] = mine;
+  (alone ? a.order : a.sec_order)[first + at] = (int)first + own + lane;
 }
 
 // One block a section.  Keys and their rows stand in shared memory in the order reached; in a pass a
@@ -279,30 +286,33 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_tokens(const __grid_cons
   }
 }
 
-// Four sections' searches run side by side: each is a chain of dependent loads.
-constexpr int kSearches = 4;
-__global__ void __launch_bounds__(128) merge_sections(const __grid_constant__ EmbedArgs a) {
+// LANES lanes a key share the other sections; four searches of a lane run side by side, as each is a chain of
+// dependent loads.
+constexpr int kSearches = 4, kMergeThreads = 256;
+template <int SECTION, int LANES>
+__global__ void __launch_bounds__(kMergeThreads) merge_sections(const __grid_constant__ EmbedArgs a) {
   wait_for_launch_before();
   let_next_launch();
-  const int64_t j = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (j >= a.n) return;
-  const int key = a.sec_sorted[j], mine = (int)(j / kSection);
-  const int sections = (int)((a.n + kSection - 1) / kSection);
-  int64_t at = j % kSection;
-  for (int s0 = 0; s0 < sections; s0 += kSearches) {
+  const int64_t j = ((int64_t)blockIdx.x * kMergeThreads + threadIdx.x) / LANES;
+  const int part = threadIdx.x % LANES;
+  const bool live = j < a.n;
+  const int key = live ? a.sec_sorted[j] : 0, mine = (int)(j / SECTION);
+  const int sections = live ? (int)((a.n + SECTION - 1) / SECTION) : 0;
+  int at = 0;
+  for (int s0 = part; s0 < sections; s0 += LANES * kSearches) {
     int lo[kSearches], hi[kSearches];
 #pragma unroll
     for (int u = 0; u < kSearches; ++u) {
-      const int s = s0 + u;
+      const int s = s0 + u * LANES;
       lo[u] = 0;
-      hi[u] = s < sections && s != mine ? (int)min((int64_t)kSection, a.n - (int64_t)s * kSection) : 0;
+      hi[u] = s < sections && s != mine ? (int)min((int64_t)SECTION, a.n - (int64_t)s * SECTION) : 0;
     }
-    for (int left = kSection; left > 0; left >>= 1) {  // a section's keys below `key`, up to it in those before
+    for (int left = SECTION; left > 0; left >>= 1) {  // a section's keys below `key`, up to it in those before
 #pragma unroll
       for (int u = 0; u < kSearches; ++u) {
         if (lo[u] >= hi[u]) continue;
-        const int mid = (lo[u] + hi[u]) >> 1, x = a.sec_sorted[(int64_t)(s0 + u) * kSection + mid];
-        if (x < key || (s0 + u < mine && x == key))
+        const int s = s0 + u * LANES, mid = (lo[u] + hi[u]) >> 1, x = a.sec_sorted[(int64_t)s * SECTION + mid];
+        if (x < key || (s < mine && x == key))
           lo[u] = mid + 1;
         else
           hi[u] = mid;
@@ -311,8 +321,12 @@ __global__ void __launch_bounds__(128) merge_sections(const __grid_constant__ Em
 #pragma unroll
     for (int u = 0; u < kSearches; ++u) at += lo[u];
   }
-  a.sorted[at] = key;
-  a.order[at] = a.sec_order[j];
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) at += __shfl_xor_sync(0xffffffffu, at, o);
+  if (!live || part != 0) return;
+  const int64_t to = j % SECTION + at;
+  a.sorted[to] = key;
+  a.order[to] = a.sec_order[j];
 }
 
 // ------------------------------------------------------------------ sums
@@ -603,25 +617,34 @@ cudaError_t forward(EmbedArgs& a, cudaStream_t st) {
 
 size_t sort_smem_set[kMaxDevices] = {};
 
+// The sorted order.  Both sides of the two bounds, gradient of 8 columns, us by the three ways (ranks of
+// all, ranks of sections, sorted sections): 4096 tokens 15.1 / 16.4 / 30.6, 6000: 20.3 / 18.0, 8192: 23.5 /
+// 19.1 / 33.3, 24000: - / 30.5 / 40.4, 33000: - / 45.7 / 42.7, 65537: - / 97 / 62.
+cudaError_t order_tokens(const EmbedArgs& a, cudaStream_t st) {
+  auto merge = [&](auto kernel, int lanes) {
+    return launch_after(kernel, dim3((unsigned)((a.n * lanes + kMergeThreads - 1) / kMergeThreads)), kMergeThreads, a, st);
+  };
+  const dim3 rank_grid((unsigned)((a.n + kRankKeys - 1) / kRankKeys));
+  if (a.n <= kRankAll) return launch_after(rank_tokens<kRankAll>, rank_grid, 32 * kRankWarps, a, st);
+  cudaError_t e;
+  if (a.n <= kRankMost) {
+    e = launch_after(rank_tokens<kRankSection>, rank_grid, 32 * kRankWarps, a, st);
+    return e == cudaSuccess ? merge(merge_sections<kRankSection, 8>, 8) : e;
+  }
+  e = set_smem_limit((const void*)sort_tokens, sizeof(SortSpace), sort_smem_set);
+  if (e != cudaSuccess) return e;
+  e = launch_after(sort_tokens, dim3((unsigned)((a.n + kSection - 1) / kSection)), kSortThreads, a, st, sizeof(SortSpace));
+  return e == cudaSuccess ? merge(merge_sections<kSection, 2>, 2) : e;
+}
+
 template <typename T, int E, int NV>
 cudaError_t backward(const EmbedArgs& a, cudaStream_t st) {
   if (a.n <= 32) {
     const int64_t warps = ((int64_t)a.D + 32 * E - 1) / (32 * E);
     return launch_after(sum_few<T, E>, dim3((unsigned)((warps + 3) / 4), (unsigned)std::min<int64_t>(a.n, 16)), 128, a, st);
   }
-  const unsigned sections = (unsigned)((a.n + kSection - 1) / kSection);
-  cudaError_t e = cudaSuccess;
-  if (sections == 1) {
-    e = launch_after(rank_tokens, dim3((unsigned)((a.n + kRankKeys - 1) / kRankKeys)), 32 * kRankWarps, a, st);
-  } else {
-    e = set_smem_limit((const void*)sort_tokens, sizeof(SortSpace), sort_smem_set);
-    if (e == cudaSuccess) e = launch_after(sort_tokens, dim3(sections), kSortThreads, a, st, sizeof(SortSpace));
-  }
+  cudaError_t e = order_tokens(a, st);
   if (e != cudaSuccess) return e;
-  if (sections > 1) {
-    e = launch_after(merge_sections, dim3((unsigned)((a.n + 127) / 128)), 128, a, st);
-    if (e != cudaSuccess) return e;
-  }
   const int vecs = (a.D + E * NV - 1) / (E * NV);
   const int slabs = (vecs + 511) / 512;
   const int threads = std::max(64, (int)align_up((size_t)(vecs + slabs - 1) / slabs, 32));
@@ -662,8 +685,8 @@ EmbedSpace embed_space(int64_t n, int D) {
   };
   s.order = take((size_t)n * 4);
   s.sorted = take((size_t)n * 4);
-  s.sec_order = take(n > kSection ? (size_t)n * 4 : 0);
-  s.sec_sorted = take(n > kSection ? (size_t)n * 4 : 0);
+  s.sec_order = take(n > kRankAll ? (size_t)n * 4 : 0);
+  s.sec_sorted = take(n > kRankAll ? (size_t)n * 4 : 0);
   s.n_long = take(8);
   const size_t windows = (size_t)(n + kWindow - 1) / kWindow;
   s.long_runs = take(windows * 16);

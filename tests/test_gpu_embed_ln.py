@@ -90,6 +90,15 @@ def test_embed_matches(dtype, kind, n, V, D):
                 scale=1.0 if n % 2 else 45.25)
 
 
+@pytest.mark.parametrize("kind", ["same", "few", "distinct", "spread", "padded", "none"])
+@pytest.mark.parametrize("n", [1023, 4095, 4097, 5120, 5121, 28672, 28673, 70001])
+def test_embed_orders(n, kind):
+    """On both sides of the ways to the tokens' order; small vocabularies and ones of few bits to spare."""
+    g = torch.Generator().manual_seed(n)
+    for V, D in ((511, 8), (70000, 3)):
+        check_embed(ids(kind, n, V, g), torch.randn(V, D, generator=g).to(BF), torch.randn(n, D, generator=g).to(BF))
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 34])
 def test_embed_few_rows(dtype, n):
