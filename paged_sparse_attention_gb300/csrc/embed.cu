@@ -85,35 +85,50 @@ __device__ __forceinline__ void store_e(T* p, const float (&f)[E]) {
 }
 
 // ------------------------------------------------------------------ forward
-// Rows of a block: `rows` of them, blockDim.x / rows threads each, NV vectors of E elements a thread
-// asked for at once: many small blocks, whose token, row and stores wait for one another, hide
+// A block: `rows` sets of RR rows, blockDim.x / rows threads each, NV vectors of E elements of each row a thread
+// asked for at once (element by element, four rows of four against one of eight: 65000 rows of 65 in fp32 in
+// 8 us, 14; 8000 of 3001 in bf16 22, 28): many small blocks, whose token, row and stores wait for one another, hide
 // each other's.  (Blocks that walk the rows with the next one in flight took 23 us for 8192 rows of
 // 3584 in bf16, these 18 at 8 KB a block.)
-template <typename T, int E, int NV>
+template <typename T, int E, int NV, int RR>
 __global__ void __launch_bounds__(256) embed_rows(const __grid_constant__ EmbedArgs a) {
   wait_for_launch_before();
   let_next_launch();
   const int per_row = blockDim.x / a.rows, r = threadIdx.x / per_row, lane = threadIdx.x % per_row;
-  const int64_t i = (int64_t)blockIdx.x * a.rows + r;
+  const int64_t i = ((int64_t)blockIdx.x * a.rows + r) * RR;
   if (i >= a.n) return;
-  const int key = key_of(a.tokens[i], a.V, a.err);
+  const int live = (int)min((int64_t)RR, a.n - i);
+  int64_t token[RR];
+  const T* in[RR];
+  bool has[RR];
+#pragma unroll
+  for (int q = 0; q < RR; ++q) token[q] = q < live ? a.tokens[i + q] : -1;
+#pragma unroll
+  for (int q = 0; q < RR; ++q) {
+    const int key = key_of(token[q], a.V, a.err);
+    has[q] = key != kNone;
+    in[q] = reinterpret_cast<const T*>(a.table) + (size_t)(has[q] ? key : 0) * a.D;
+  }
   T* out = reinterpret_cast<T*>(a.out) + (size_t)i * a.D;
-  const T* in = reinterpret_cast<const T*>(a.table) + (size_t)(key == kNone ? 0 : key) * a.D;
   const int step = per_row * E;
   for (int c = lane * E; c < a.D; c += NV * step) {
-    float f[NV][E];
+    float f[RR][NV][E];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
+    for (int q = 0; q < RR; ++q)
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[v][e] = 0.f;
-      if (key != kNone && c + v * step < a.D) load_e<T, E>(in + c + v * step, f[v]);
-    }
+      for (int v = 0; v < NV; ++v) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
+        for (int e = 0; e < E; ++e) f[q][v][e] = 0.f;
+        if (has[q] && c + v * step < a.D) load_e<T, E>(in[q] + c + v * step, f[q][v]);
+      }
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[v][e] *= a.scale;
-      if (c + v * step < a.D) store_e<T, E>(out + c + v * step, f[v]);
-    }
+    for (int q = 0; q < RR; ++q)
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[q][v][e] *= a.scale;
+        if (q < live && c + v * step < a.D) store_e<T, E>(out + (size_t)q * a.D + c + v * step, f[q][v]);
+      }
   }
 }
 
@@ -375,6 +390,10 @@ __global__ void __launch_bounds__(128) sum_few(const __grid_constant__ EmbedArgs
 // starts the window), one more may go on into the next.
 __device__ __forceinline__ size_t piece_slot(int64_t w, bool first) { return (size_t)w * 2 + (first ? 1 : 0); }
 
+// Threads of a block, at most.  (Element by element, 512 take 83 us for 8000 rows of 3001 in fp32, 320 take 73;
+// longer vectors hold more loads each.)
+constexpr int run_threads(int E) { return E == 1 ? 320 : 512; }
+
 // NV vectors of E elements a thread.  A block walks the windows b, b + grid, ...; the next window's
 // tokens are on their way while this one's rows are summed.  A batch's rows are all asked for before
 // the first is used, held as they are stored.  Rows of the gradient that will be added to are asked
@@ -502,12 +521,14 @@ __global__ void __launch_bounds__(512, 2) sum_runs(const __grid_constant__ Embed
 
 // Joins the tokens whose rows lie in several windows.  Most have a few pieces: a warp takes 128 columns
 // of one.  Those with more than 32, which a common token has in a long batch, are taken by whole
-// blocks, the warps each a share of the pieces, whose sums are added in order.
+// blocks, 32 columns each, whose groups of eight lanes take a share of the pieces each; the shares' sums are added
+// in order.
 constexpr int kJoinCols = 128, kJoinWarps = 16;
+constexpr int kHeavyCols = 32, kGroup = kHeavyCols / 4, kShares = kJoinWarps * 32 / kGroup;
 __global__ void __launch_bounds__(32 * kJoinWarps) join_pieces(const __grid_constant__ EmbedArgs a) {
   __shared__ float4 share[kJoinWarps][32];
   wait_for_launch_before();
-  const int chunks = (a.D + kJoinCols - 1) / kJoinCols;
+  const int chunks = (a.D + kJoinCols - 1) / kJoinCols, strips = (a.D + kHeavyCols - 1) / kHeavyCols;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   // first window of a run that goes back from window w by more than 32: a search that cuts in 33 at a step
   auto first_window = [&](int key, int w) {
@@ -555,24 +576,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_pieces(const __grid_cons
     for (int e = 0; e < 4; ++e)
       if (c + e < a.D) to[e] = fmaf(a.scale, f[e], old[e]);
   };
-  const int64_t heavy = (int64_t)a.n_long[1] * chunks, light = (int64_t)a.n_long[0] * chunks;
+  const int64_t heavy = (int64_t)a.n_long[1] * strips, light = (int64_t)a.n_long[0] * chunks;
   for (int64_t it = blockIdx.x; it < heavy; it += gridDim.x) {
-    const int4 run = a.long_runs[a.windows - 1 - it / chunks];
-    const int c = (int)(it % chunks) * kJoinCols + 4 * lane;
+    const int4 run = a.long_runs[a.windows - 1 - it / strips];
+    const int c = (int)(it % strips) * kHeavyCols + 4 * (lane % kGroup);
     const int begin = first_window(run.x, run.z), pieces = run.z - begin + 1;
-    const int per = (pieces + kJoinWarps - 1) / kJoinWarps;
-    float4 sum = sum_of(begin, warp * per, min(pieces, (warp + 1) * per), c);
+    const int per = (pieces + kShares - 1) / kShares, mine = warp * (32 / kGroup) + lane / kGroup;
+    float4 sum = sum_of(begin, mine * per, min(pieces, (mine + 1) * per), c);
+    auto add = [&](const float4& y) {
+      sum.x += y.x;
+      sum.y += y.y;
+      sum.z += y.z;
+      sum.w += y.w;
+    };
     share[warp][lane] = sum;
     __syncthreads();
-    if (warp == 0) {
-#pragma unroll
-      for (int x = 1; x < kJoinWarps; ++x) {
-        const float4 y = share[x][lane];
-        sum.x += y.x;
-        sum.y += y.y;
-        sum.z += y.z;
-        sum.w += y.w;
-      }
+    if (warp == 0 && lane < kGroup) {
+#pragma unroll 8
+      for (int x = 1; x < kShares; ++x) add(share[x / (32 / kGroup)][x % (32 / kGroup) * kGroup + lane]);
       float old[4];
       read(run.x, c, old);
       write(run.x, c, sum, old);
@@ -606,13 +627,14 @@ cudaError_t launch_after(K kernel, dim3 grid, int threads, const EmbedArgs& a, c
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <typename T, int E, int NV>
+template <typename T, int E, int NV, int RR>
 cudaError_t forward(EmbedArgs& a, cudaStream_t st) {
   const int vecs = (a.D + E * NV - 1) / (E * NV);
   const int per_row = (int)std::min<size_t>(256, align_up((size_t)vecs, 32));
+  const int64_t sets = (a.n + RR - 1) / RR;
   a.rows = 256 / per_row;
-  while (a.rows > 1 && (a.n + a.rows - 1) / a.rows < 2 * device_sm_count()) a.rows /= 2;
-  return launch_after(embed_rows<T, E, NV>, dim3((unsigned)((a.n + a.rows - 1) / a.rows)), per_row * a.rows, a, st);
+  while (a.rows > 1 && (sets + a.rows - 1) / a.rows < 2 * device_sm_count()) a.rows /= 2;
+  return launch_after(embed_rows<T, E, NV, RR>, dim3((unsigned)((sets + a.rows - 1) / a.rows)), per_row * a.rows, a, st);
 }
 
 size_t sort_smem_set[kMaxDevices] = {};
@@ -646,7 +668,7 @@ cudaError_t backward(const EmbedArgs& a, cudaStream_t st) {
   cudaError_t e = order_tokens(a, st);
   if (e != cudaSuccess) return e;
   const int vecs = (a.D + E * NV - 1) / (E * NV);
-  const int slabs = (vecs + 511) / 512;
+  const int slabs = (vecs + run_threads(E) - 1) / run_threads(E);
   const int threads = std::max(64, (int)align_up((size_t)(vecs + slabs - 1) / slabs, 32));
   const int64_t most = (int64_t)(1024 / threads) * device_sm_count();
   e = launch_after(sum_runs<T, E, NV>,
@@ -662,7 +684,7 @@ cudaError_t backward(const EmbedArgs& a, cudaStream_t st) {
 template <typename T>
 cudaError_t forward_any(EmbedArgs& a, cudaStream_t st) {
   constexpr int E = 16 / sizeof(T);
-  return a.D % E == 0 && on16(a.table) && on16(a.out) ? forward<T, E, 4>(a, st) : forward<T, 1, 8>(a, st);
+  return a.D % E == 0 && on16(a.table) && on16(a.out) ? forward<T, E, 4, 1>(a, st) : forward<T, 1, 4, 4>(a, st);
 }
 template <typename T>
 cudaError_t backward_any(const EmbedArgs& a, cudaStream_t st) {
