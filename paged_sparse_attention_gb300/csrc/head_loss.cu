@@ -354,7 +354,9 @@ struct Plan {
 Plan make_plan(int64_t n, int D, int V, int dtype, bool backward, bool w_on16) {
   Plan p = {};
   p.parts_of = dtype == OOMB_FP32 ? 3 : 1;
-  p.pitch_d = (int)align_up((size_t)D, 8);
+  // rows on lines of 128 bytes: a box of 64 columns that straddles two asks for both (951 rows on 32001 x 1000 in
+  // fp32: 303 us, 230)
+  p.pitch_d = (int)align_up((size_t)D, 64);
   const bool never_in_place = dtype == OOMB_FP32 || D % 8 != 0;
   p.staged = never_in_place || !w_on16;
   const size_t row_bytes = (size_t)p.parts_of * p.pitch_d * 2;
