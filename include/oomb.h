@@ -572,7 +572,8 @@ OOMB_API void oomb_block_norm_test_timeout(int on);
  * targets are int64; a negative one is none (padding, a prompt's token that is not a target): its
  * row is zero and sends no gradient.  One at or after V is told by OOMB_DEVERR_TOKEN in
  * error_word (a device uint32, e.g. word 0 of a pool's control block, which oomb_check reads and
- * clears; oomb_word_check does that for a word outside a pool) and then counts as none. */
+ * clears; oomb_word_check does that for a word outside a pool) and then counts as none.  Outputs
+ * overlap neither inputs nor one another unless it is said. */
 
 /* out[i, :] = scale * table[tokens[i], :], rounded once; zeros where there is no token.
  * tokens [n], table [V, D] and out [n, D] (dtype, device).  Pointers on their element's size;
