@@ -27,8 +27,10 @@ constexpr int kGroup = 16;
 // fp32 operands have six products a step and fewer steps.
 constexpr int kChunk = 28, kChunkParts = 4;
 // Workspace given to a piece's dz, and to staged parts of W where it cannot be read in place
-// (kStagedOdd: bf16 rows that are on 16 bytes unless the caller's pointer is not).
-constexpr size_t kAccBytes = 256u << 20, kDzBytes = 256u << 20, kStagedBytes = 256u << 20, kStagedOdd = 32u << 20;
+// (kStagedOdd: bf16 rows that are on 16 bytes unless the caller's pointer is not).  Both directions with 256, 512
+// and 1024 MB for dz: 8192 rows on 131072 x 3584 18882, 18762 and 18773 us, 1600 of 4001 on 50001 x 2048 988, 870
+// and 919, 951 on 32001 x 1000 in fp32 1077, 1081 and 1119.
+constexpr size_t kAccBytes = 256u << 20, kDzBytes = 512u << 20, kStagedBytes = 256u << 20, kStagedOdd = 32u << 20;
 
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

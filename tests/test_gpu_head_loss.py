@@ -84,6 +84,21 @@ def test_several_pieces_of_the_vocabulary():
         check(run(x, w, t, **kw), ref, tol)
 
 
+@pytest.mark.parametrize("n,V,dtype", [(16500, 16700, BF), (9500, 9700, FP)])
+def test_several_pieces_for_many_rows_of_which_few_count(n, V, dtype):
+    """dz has room for every row; those without a target neither add to the gradients nor are read."""
+    x, w, t, g = make(n, V, 72, dtype, seed=4, masked=0.96)
+    has = t >= 0
+    kw = dict(cap=20.0, d_loss=g, scale=0.5)
+    x[~has] = float("nan")
+    out = run(x, w, t, **kw)
+    for k in ("loss", "lse", "dx"):
+        assert (out[k].cpu()[~has] == 0).all(), k
+        out[k] = out[k].cpu()[has]
+    ref, tol = head_reference(x[has], w, t[has], cap=20.0, d_loss=g[has], scale=0.5)
+    check(out, ref, tol)
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("n", [150, 24])
 def test_rows_without_a_target(dtype, n):
