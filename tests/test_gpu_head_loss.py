@@ -172,6 +172,17 @@ def test_one_gradient_alone_and_fp32_weights_gradient(dtype, n):
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("n,V,D", [(140, 700, 89), (140, 31000, 261), (140, 31000, 264), (600, 31001, 33)])
+def test_gradients_added_in_rows_of_every_alignment(dtype, n, V, D):
+    x, w, t, g = make(n, V, D, dtype, seed=6, masked=0.1)
+    plain = run(x, w, t, d_loss=g, dw_dtype=FP)["dw"].cpu()
+    base = torch.randn(V, D, generator=torch.Generator().manual_seed(9))
+    add = run(x, w, t, d_loss=g, accumulate=True, base=base)["dw"].cpu()
+    slack = 2 ** -23 * (base.abs() + plain.abs())  # a rounding of each
+    assert ((add.double() - (base.double() + plain.double())).abs() <= slack).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("n", [300, 7])
 def test_the_same_bits_on_every_run(dtype, n):
     x, w, t, g = make(n, 5000, 200, dtype, seed=9, masked=0.3)
