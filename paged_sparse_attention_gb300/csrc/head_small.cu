@@ -40,12 +40,14 @@ __device__ __forceinline__ bool has_target(const SmallArgs& a, int i) {
   return t >= 0 && t < a.V;
 }
 
-// Eight columns of a row, as they are stored: VEC 16 bytes an access, else element by element (columns
-// behind the last are 0).
+// Eight columns of a row, as they are stored: VEC eight that follow one another from c, 16 bytes an access; else
+// c, c + step, ... element by element, so that neighbouring threads read neighbouring columns.  Columns behind the
+// last are 0.  (One row on 131072 x 3583: 230 us forward in bf16 and 287 in
+// fp32, with eight that follow one another here too 279 and 462.)
 template <typename T, bool VEC>
 struct Eight {
   uint4 raw[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* row, int c, int D) {
+  __device__ __forceinline__ void load(const T* row, int c, int step, int D) {
     if constexpr (VEC) {
 #pragma unroll
       for (int i = 0; i < (int)sizeof(T) / 2; ++i)
@@ -53,7 +55,7 @@ struct Eight {
     } else {
       T* x = reinterpret_cast<T*>(raw);
 #pragma unroll
-      for (int e = 0; e < kCols; ++e) x[e] = c + e < D ? row[c + e] : from_float<T>(0.f);
+      for (int e = 0; e < kCols; ++e) x[e] = c + e * step < D ? row[c + e * step] : from_float<T>(0.f);
     }
   }
   __device__ __forceinline__ void pairs(uint64_t (&f)[kCols / 2]) const {
@@ -82,6 +84,7 @@ __device__ __forceinline__ float cap_logit(float z, float cap, float& th) {
 // NT: tokens at a time.  grid.y: groups of NT tokens.  DZ: dz is stored, else parts of the row sums.
 template <typename T, bool VEC, int NT, bool DZ>
 __global__ void __launch_bounds__(kThreads, 2) dot_rows(const __grid_constant__ SmallArgs a) {
+  constexpr int kStride = VEC ? kCols : 1;  // between the first columns of two lanes
   constexpr int K = kRows * NT, LOG = K == 32 ? 5 : K == 16 ? 4 : K == 8 ? 3 : 2, DEPTH = sizeof(T) == 4 ? (NT <= 2 ? 2 : 1) : NT == 8 ? 1 : NT == 4 ? 2 : 3;
   // [NT, steps of 256 columns], zeros behind a row; of a step first every lane's first four columns, then the
   // others, so that a warp's 16-byte reads lie side by side
@@ -99,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 2) dot_rows(const __grid_constant__ 
 #pragma unroll 2
     for (int c = threadIdx.x * kCols; c < pitch; c += kThreads * kCols) {
       Eight<T, VEC> raw;
-      raw.load(x, has ? c : a.D, a.D);
+      raw.load(x, VEC ? c : (c & ~255) + (c & 255) / kCols, 32, has ? a.D : 0);
       uint64_t f[kCols / 2];
       raw.pairs(f);
       float* to = xs + t * pitch + (c & ~255) + (c & 255) / 2;
@@ -134,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 2) dot_rows(const __grid_constant__ 
     for (int u = 0; u < DEPTH; ++u)
 #pragma unroll
       for (int r = 0; r < kRows; ++r)
-        if (u < steps) raw[u][r].load(w[r], u * 256 + lane * kCols, a.D);
+        if (u < steps) raw[u][r].load(w[r], u * 256 + lane * kStride, 32, a.D);
     for (int s0 = 0; s0 < steps; s0 += DEPTH) {
 #pragma unroll
       for (int u = 0; u < DEPTH; ++u) {
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 2) dot_rows(const __grid_constant__ 
         for (int r = 0; r < kRows; ++r) raw[u][r].pairs(f[r]);
         if (s0 + u + DEPTH < steps)
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) raw[u][r].load(w[r], (s0 + u + DEPTH) * 256 + lane * kCols, a.D);
+          for (int r = 0; r < kRows; ++r) raw[u][r].load(w[r], (s0 + u + DEPTH) * 256 + lane * kStride, 32, a.D);
         const float* xp = xs + (s0 + u) * 256 + lane * 4;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -260,7 +263,8 @@ __global__ void __launch_bounds__(kThreads, 2) grad_rows(const __grid_constant__
   let_next_launch();
   for (int t = threadIdx.x; t < a.n; t += blockDim.x) has[t] = has_target(a, t);
   __syncthreads();
-  const int group = threadIdx.x / a.ct, c = (blockIdx.y * a.ct + threadIdx.x % a.ct) * kCols;
+  const int group = threadIdx.x / a.ct, step = VEC ? 1 : a.ct;  // step: between a thread's columns
+  const int c = blockIdx.y * a.ct * kCols + threadIdx.x % a.ct * (VEC ? kCols : 1);
   const int units = gridDim.x * a.row_groups, unit = blockIdx.x * a.row_groups + group;
   if (group >= a.row_groups || c >= a.D) return;
   const int chunks = (a.V + kRows - 1) / kRows;
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_rows(const __grid_constant__
 #pragma unroll
         for (int u = 0; u < B; ++u) {
           const bool live = t0 + u < a.n && has[t0 + u];  // (a token without a target is not read)
-          raw[u].load(reinterpret_cast<const T*>(a.x) + (size_t)(live ? t0 + u : 0) * a.D, live ? c : a.D, a.D);
+          raw[u].load(reinterpret_cast<const T*>(a.x) + (size_t)(live ? t0 + u : 0) * a.D, c, step, live ? a.D : 0);
           // (rows of W behind the last: not used)
           d[u] = live ? *reinterpret_cast<const float4*>(a.dz + (size_t)(t0 + u) * a.pitch + v0)
                       : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -299,32 +303,59 @@ __global__ void __launch_bounds__(kThreads, 2) grad_rows(const __grid_constant__
           }
         }
       }
+      // rows whose old values (fp32 only) are asked for together (a row of 131072 x 3584 in bf16, backward with dw
+      // added: 951 us, a vector at a time 1089)
+      constexpr int R = 2;
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        if (v0 + r >= a.V) break;
-        TW* to = reinterpret_cast<TW*>(a.dw) + (size_t)(v0 + r) * a.D + c;
-        float f[kCols];
+      for (int r0 = 0; r0 < kRows; r0 += R) {
+        float old[R][kCols];
 #pragma unroll
-        for (int k = 0; k < kCols / 2; ++k) f32x2_split(acc[r][k], f[2 * k], f[2 * k + 1]);
-        if (a.dw_vec) {
-          if constexpr (sizeof(TW) == 2) {
-            *reinterpret_cast<uint4*>(to) =
-                make_uint4(pack_bf16x2(a.scale * f[0], a.scale * f[1]), pack_bf16x2(a.scale * f[2], a.scale * f[3]),
-                           pack_bf16x2(a.scale * f[4], a.scale * f[5]), pack_bf16x2(a.scale * f[6], a.scale * f[7]));
-          } else {
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int e = 0; e < kCols; e += 4) {
-              float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (a.accumulate) o = *reinterpret_cast<const float4*>(to + e);
-              *reinterpret_cast<float4*>(to + e) =
-                  make_float4(fmaf(a.scale, f[e], o.x), fmaf(a.scale, f[e + 1], o.y), fmaf(a.scale, f[e + 2], o.z),
-                              fmaf(a.scale, f[e + 3], o.w));
+          for (int e = 0; e < kCols; ++e) old[r][e] = 0.f;
+        if (sizeof(TW) == 4 && a.accumulate) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float* from = reinterpret_cast<const float*>(a.dw) + (size_t)min(v0 + r0 + r, a.V - 1) * a.D + c;
+            if (a.dw_vec) {
+#pragma unroll
+              for (int e = 0; e < kCols; e += 4) {
+                const float4 o = *reinterpret_cast<const float4*>(from + e);
+                old[r][e] = o.x;
+                old[r][e + 1] = o.y;
+                old[r][e + 2] = o.z;
+                old[r][e + 3] = o.w;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < kCols; ++e)
+                if (c + e * step < a.D) old[r][e] = from[e * step];
             }
           }
-        } else {
+        }
 #pragma unroll
-          for (int e = 0; e < kCols; ++e)
-            if (c + e < a.D) to[e] = from_float<TW>(fmaf(a.scale, f[e], a.accumulate ? to_float<TW>(to[e]) : 0.f));
+        for (int r = 0; r < R; ++r) {
+          if (v0 + r0 + r >= a.V) break;
+          TW* to = reinterpret_cast<TW*>(a.dw) + (size_t)(v0 + r0 + r) * a.D + c;
+          float f[kCols];
+#pragma unroll
+          for (int k = 0; k < kCols / 2; ++k) f32x2_split(acc[r0 + r][k], f[2 * k], f[2 * k + 1]);
+#pragma unroll
+          for (int e = 0; e < kCols; ++e) f[e] = fmaf(a.scale, f[e], old[r][e]);
+          if (a.dw_vec) {
+            if constexpr (sizeof(TW) == 2) {
+              *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                         pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < kCols; e += 4)
+                *reinterpret_cast<float4*>(to + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < kCols; ++e)
+              if (c + e * step < a.D) to[e * step] = from_float<TW>(f[e]);
+          }
         }
       }
     }
@@ -342,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_rows(const __grid_constant__
       Eight<T, VEC> raw[kRows];
 #pragma unroll
       for (int r = 0; r < kRows; ++r)
-        raw[r].load(reinterpret_cast<const T*>(a.w) + (size_t)min(v0 + r, a.V - 1) * a.D, c, a.D);
+        raw[r].load(reinterpret_cast<const T*>(a.w) + (size_t)min(v0 + r, a.V - 1) * a.D, c, step, a.D);
       float dd[NT][kRows];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -374,8 +405,14 @@ __global__ void __launch_bounds__(kThreads, 2) grad_rows(const __grid_constant__
       float f[kCols];
 #pragma unroll
       for (int k = 0; k < kCols / 2; ++k) f32x2_split(acc[t][k], f[2 * k], f[2 * k + 1]);
+      if constexpr (VEC) {
 #pragma unroll
-      for (int e = 0; e < kCols; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        for (int e = 0; e < kCols; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kCols; ++e)
+          if (c + e * step < a.D) to[e * step] = f[e];
+      }
     }
   }
 }
@@ -473,7 +510,7 @@ cudaError_t backward(SmallArgs a, int dw_dtype, cudaStream_t st) {
   const GradGrid g = grad_grid(a.D, a.V);
   a.ct = g.ct;
   a.row_groups = g.row_groups;
-  a.dw_vec = a.D % 8 == 0 && on16(a.dw);
+  a.dw_vec = vec && on16(a.dw);
   const int threads = (int)align_up((size_t)g.ct * g.row_groups, 32);
   const dim3 grid((unsigned)g.blocks, (unsigned)g.slabs, (unsigned)((a.dx ? (a.n + 7) / 8 : 0) + (a.dw ? 1 : 0)));
   if (dw_dtype == OOMB_FP32)
