@@ -24,7 +24,9 @@ constexpr int kMaxWidth = 65536;
 constexpr int kGroup = 16;
 // Steps of 64 columns summed on the tensor cores: the loss of 4096 such rows is 1.4e-7, 2.0e-7 and
 // 3.4e-7 of its size off after 8, 16 and 28 steps (2.5e-6 after all 56), in 2343, 2288 and 2243 us.
-// fp32 operands have six products a step and fewer steps.
+// fp32 operands have six products a step and fewer steps, an eighth of a short K for the logits: dx and dw of 300
+// rows on 1000 x 256 are off by 7.9e-7 of their size, by four steps 2.6e-6 (82 us, 80); 951 on 32001 x 1000 by
+// 6.4e-7, 8.6e-7 (1097 us, 1061).
 constexpr int kChunk = 28, kChunkParts = 4;
 // Workspace given to a piece's dz, and to staged parts of W where it cannot be read in place
 // (kStagedOdd: bf16 rows that are on 16 bytes unless the caller's pointer is not).  Both directions with 256, 512
@@ -576,6 +578,7 @@ cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, ch
   const int tms = tiles(s.n, kTile), tds = tiles(D, kTile);
   g.pitch = pl.pitch_z;
   GemmArgs gx = g, gw = g;
+  if (pl.parts_of > 1) gx.chunk = gw.chunk = kChunkParts;  // of a K of their own
   for (int v0 = 0; v0 < V; v0 += pl.piece) {
     const int cols = std::min(pl.piece, V - v0);
     int row_b;
@@ -656,7 +659,7 @@ GemmArgs arguments(const void* x, const int64_t* targets, int n, int D, int V, i
   g.passes = pl.parts_of == 1 ? 1 : 6;
   // about equal pieces of K
   const int steps = tiles(D, kStep), pieces = tiles(steps, kChunk);
-  g.chunk = pl.parts_of == 1 ? tiles(steps, pieces) : kChunkParts;
+  g.chunk = pl.parts_of == 1 ? tiles(steps, pieces) : std::max(1, std::min(kChunkParts, steps / 8));
   g.group = kGroup;
   g.targets = targets;
   g.cap = cap;
