@@ -19,6 +19,7 @@
 // tiles c, c + clusters, ... in groups of kGroup row tiles, which share the columns' tiles in L2.
 #pragma once
 #include "head_loss.h"
+#include "head_plan.h"
 #include "tc_common.cuh"
 
 namespace oomb {
@@ -26,13 +27,11 @@ namespace head {
 
 enum Mode { kLse = 0, kDz = 1, kDx = 2, kDw = 3 };
 
-constexpr int kTile = 256, kHalf = 128, kStep = 64;  // tile, a CTA's share of it, columns of K a stage
 constexpr uint32_t kOperand = kHalf * kStep * 2;     // 16 KB
 constexpr int kThreads = 320;                        // producer, issuer, 8 epilogue warps
 constexpr int kEpilogueWarps = 8;
 constexpr int kMaxStages = 9;
-// Tiles of TN columns: 256, or 64 where there are few tiles and a cluster's time is its loop over K.
-constexpr int kNarrow = 64;
+// Tiles of TN columns: kTile, or kNarrow where there are few tiles.
 template <int TN>
 struct Shape {
   static constexpr int half = TN / 2;                           // columns of an epilogue warp, rows of B a CTA loads

@@ -13,6 +13,7 @@
 #include <cmath>
 
 #include "head_gemm.cuh"
+#include "head_plan.h"
 
 namespace oomb {
 namespace head {
@@ -28,11 +29,6 @@ constexpr int kGroup = 16;
 // rows on 1000 x 256 are off by 7.9e-7 of their size, by four steps 2.6e-6 (82 us, 80); 951 on 32001 x 1000 by
 // 6.4e-7, 8.6e-7 (1097 us, 1061).
 constexpr int kChunk = 28, kChunkParts = 4;
-// Workspace given to a piece's dz, and to staged parts of W where it cannot be read in place
-// (kStagedOdd: bf16 rows that are on 16 bytes unless the caller's pointer is not).  Both directions with 256, 512
-// and 1024 MB for dz: 8192 rows on 131072 x 3584 18882, 18762 and 18773 us, 1600 of 4001 on 50001 x 2048 988, 870
-// and 919, 951 on 32001 x 1000 in fp32 1077, 1081 and 1119.
-constexpr size_t kAccBytes = 256u << 20, kDzBytes = 512u << 20, kStagedBytes = 256u << 20, kStagedOdd = 32u << 20;
 
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -377,71 +373,8 @@ __global__ void __launch_bounds__(256) join_dx(const __grid_constant__ GemmArgs 
 }
 
 // ------------------------------------------------------------------ host side
-int tiles(int64_t x, int t) { return (int)((x + t - 1) / t); }
 int clusters() { return std::max(1, device_sm_count() / 2); }
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Parts that K of dx may be cut into: as many as kAccBytes hold, 64 at most.
-int most_splits(int64_t n, int D) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(64, (int64_t)(kAccBytes / ((size_t)n * align_up((size_t)D, 4) * 4))));
-}
-
-// Where things lie in the workspace, and the pieces of the vocabulary.
-struct Plan {
-  int parts_of, pitch_d;       // bf16 parts of an operand, elements of a staged row
-  bool staged;                 // W is read through the workspace
-  int piece;                   // columns of a piece (the last may have fewer)
-  int pitch_z;
-  size_t count, rows, at, x, w, part, dz, acc, acc_w, bytes;
-};
-Plan make_plan(int64_t n, int D, int V, int dtype, bool backward, bool w_on16) {
-  Plan p = {};
-  p.parts_of = dtype == OOMB_FP32 ? 3 : 1;
-  // rows on lines of 128 bytes: a box of 64 columns that straddles two asks for both (951 rows on 32001 x 1000 in
-  // fp32: 303 us, 230)
-  p.pitch_d = (int)align_up((size_t)D, 64);
-  const bool never_in_place = dtype == OOMB_FP32 || D % 8 != 0;
-  p.staged = never_in_place || !w_on16;
-  const size_t row_bytes = (size_t)p.parts_of * p.pitch_d * 2;
-  const int64_t v256 = (int64_t)align_up((size_t)V, kTile);
-  // the pieces' sizes are multiples of a tile, about equal
-  int64_t most = v256;
-  const int64_t staged_rows = std::min<int64_t>(
-      v256, std::max<int64_t>(kTile, (int64_t)((never_in_place ? kStagedBytes : kStagedOdd) / row_bytes) / kTile * kTile));
-  if (p.staged) most = staged_rows;
-  const size_t z_bytes = (size_t)p.parts_of * n * 2;  // of a column of dz
-  if (backward) most = std::min<int64_t>(most, std::max<int64_t>(kTile, (int64_t)(kDzBytes / z_bytes) / kTile * kTile));
-  const int64_t pieces = (V + most - 1) / most;
-  p.piece = (int)std::min<int64_t>(V, (int64_t)align_up((size_t)((V + pieces - 1) / pieces), kTile));
-  p.pitch_z = (int)align_up((size_t)p.piece, 64);
-  size_t at = 0;
-  auto take = [&](size_t bytes) {
-    const size_t here = at;
-    at += align_up(bytes, 256);
-    return here;
-  };
-  p.count = take(8);
-  p.rows = take((size_t)n * 4);
-  p.at = take((size_t)n * 4);
-  p.x = take((size_t)n * row_bytes);
-  p.w = take((size_t)staged_rows * row_bytes);  // the same for every n
-  const size_t common = at;
-  // parts of wide tiles, or of narrow ones for as many rows as may have them (most where W is staged: its
-  // pieces are the smallest)
-  const int64_t staged_pieces = (V + staged_rows - 1) / staged_rows;
-  const int64_t staged_piece = (int64_t)align_up((size_t)((V + staged_pieces - 1) / staged_pieces), kTile);
-  const int64_t narrow_rows = std::min<int64_t>(n, (int64_t)kTile * (clusters() / tiles(staged_piece, kNarrow)));
-  p.part = take(std::max((size_t)n * tiles(V, kHalf), (size_t)narrow_rows * tiles(V, kNarrow / 2)) * 8);
-  const size_t forward_bytes = at;
-  at = common;
-  // room that grows with n although a piece of more rows has fewer columns
-  p.dz = take(std::min<size_t>(z_bytes * align_up((size_t)V, 64), std::max<size_t>(kDzBytes, z_bytes * kTile)));
-  const size_t acc = (size_t)n * align_up((size_t)D, 4) * 4;
-  p.acc = take(std::max(acc, std::min(64 * acc, kAccBytes)));
-  p.acc_w = take((size_t)clusters() * kTile * kTile * 4);  // a tile a cluster at most
-  p.bytes = backward ? std::max(forward_bytes, at) : forward_bytes;
-  return p;
-}
 
 // Map of a [planes, rows, cols] bf16 array with rows of `pitch` elements, boxes of 64 columns.
 bool make_map(CUtensorMap* m, const void* base, uint64_t planes, uint64_t rows, uint64_t cols, uint64_t pitch, int box) {
@@ -491,10 +424,6 @@ cudaError_t gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& p, 
   return always || p.passes > 1 ? gemm_of<MODE, true, 256>(a, b, p, most_tiles, st)
                                 : gemm_of<MODE, always, 256>(a, b, p, most_tiles, st);
 }
-// Whether every cluster has one narrow tile of the logits of `rows` and `cols` at most.  (A step of K takes a
-// narrow tile 0.30 us and a wide one 0.33, so it does not pay to have more of them.)
-bool is_narrow(int64_t rows, int64_t cols) { return (int64_t)tiles(rows, kTile) * tiles(cols, kNarrow) <= clusters(); }
-
 // What both directions share: the rows with a target, gathered.  (8192 rows of 3584, with their targets' logits: 31 us by
 // four blocks an SM, 49 by two, 46 by six, which take two rounds.)
 template <typename T>
@@ -540,14 +469,16 @@ cudaError_t weights(const void* w, const Plan& pl, char* ws, int D, int V, int v
 template <typename T>
 cudaError_t forward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, char* ws, int V, float* loss, float* lse,
                     cudaStream_t st) {
+  const RowParts of = row_parts(s.n, V, pl.piece, clusters());
+  const bool narrow = of.narrow;
+  const int tn = narrow ? kNarrow : kTile;
+  g.parts = of.parts;
+  if (pl.part + (size_t)s.n * g.parts * 8 > pl.bytes) return cudaErrorInvalidValue;  // (never, by the plan)
   cudaError_t e = gather<T>(s.in, s, st);
   if (e != cudaSuccess) return e;
   CUtensorMap mx, mw;
   if (!make_map(&mx, s.out, pl.parts_of, s.n, s.D, s.pitch, kHalf)) return cudaErrorInvalidValue;
   g.steps = tiles(s.D, kStep);
-  const bool narrow = is_narrow(s.n, pl.piece);
-  const int tn = narrow ? kNarrow : kTile;
-  g.parts = tiles(V, tn / 2);
   for (int v0 = 0; v0 < V; v0 += pl.piece) {
     g.v0 = v0;
     g.cols = std::min(pl.piece, V - v0);
@@ -582,7 +513,7 @@ cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, ch
   for (int v0 = 0; v0 < V; v0 += pl.piece) {
     const int cols = std::min(pl.piece, V - v0);
     int row_b;
-    const bool narrow = is_narrow(s.n, cols);
+    const bool narrow = is_narrow(s.n, cols, clusters());
     e = weights<T>(w, pl, ws, D, V, v0, cols, narrow, &mw, &mw64, &row_b, st);
     if (e != cudaSuccess) return e;
     if (!make_map(&mz, g.dz, pl.parts_of, s.n, cols, g.pitch, kHalf) ||
@@ -624,8 +555,7 @@ cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, ch
       gw.out_fp32 = dw_dtype == OOMB_FP32;
       gw.out_vec = D % (16 / (int)dtype_size(dw_dtype)) == 0 && on16(dw);
       gw.accumulate = accumulate;
-      // few tiles: the rows are cut in parts of 8 steps at least
-      gw.dw_splits = std::max(1, std::min(clusters() / (gw.tms * tds), tiles(s.n, kStep) / 8));
+      gw.dw_splits = dw_splits(s.n, D, cols, clusters());
       gw.acc = reinterpret_cast<float*>(ws + pl.acc_w);
       e = gemm<kDw>(mz64, mx64, gw, (int64_t)gw.tms * tds * gw.dw_splits, false, st);
       if (e == cudaSuccess && gw.dw_splits > 1) {
@@ -723,7 +653,7 @@ size_t oomb_head_loss_workspace(int n, int D, int V, int dtype, int backward) {
   // grows with n: fewer rows may go either way
   SmallSpace s;
   const int few = std::min(n, small_rows(D, V, dtype));
-  return std::max(make_plan(n, D, V, dtype, backward != 0, true).bytes,
+  return std::max(make_plan(n, D, V, dtype, backward != 0, true, clusters()).bytes,
                   few > 0 ? small_space(few, D, V, backward != 0, &s) : 0);
 }
 
@@ -742,7 +672,7 @@ oomb_status oomb_head_loss_fwd(const void* x, const void* w, const int64_t* targ
     a.lse = lse;
     return cuda_status(launch_small_fwd(a, dtype, (cudaStream_t)stream));
   }
-  const Plan pl = make_plan(n, D, V, dtype, false, on16(w));
+  const Plan pl = make_plan(n, D, V, dtype, false, on16(w), clusters());
   GatherArgs st;
   GemmArgs g = arguments(x, targets, n, D, V, dtype, softcap, pl, ws, error_word, &st);
   st.loss = loss;
@@ -780,7 +710,7 @@ oomb_status oomb_head_loss_bwd(const void* x, const void* w, const int64_t* targ
     a.accumulate = accumulate != 0;
     return cuda_status(launch_small_bwd(a, dtype, dw_dtype, (cudaStream_t)stream));
   }
-  const Plan pl = make_plan(n, D, V, dtype, true, on16(w));
+  const Plan pl = make_plan(n, D, V, dtype, true, on16(w), clusters());
   GatherArgs st;
   GemmArgs g = arguments(x, targets, n, D, V, dtype, softcap, pl, ws, error_word, &st);
   st.dx = dx;
