@@ -174,9 +174,10 @@ struct RowSum {
 };
 
 // CHUNKED: K is cut in pieces of p.chunk steps whose sums are added in fp32 in registers.  The tensor
-// cores cut a partial sum's last bits instead of rounding them, so a sum of K products loses up to
-// K / 16 halves of a unit in its last place, always towards zero: 6e-6 of a logit over K = 3584,
-// which a loss in fp32 would show, and 4e-7 over 256.  Not for sums that are rounded to bf16 anyway.
+// cores cut a partial sum's last bits instead of rounding them, always towards zero: 6e-6 of a logit
+// over K = 3584 is lost, which a loss in fp32 would show, and 4e-7 over 256; of sums of one sign 1.8e-7 of the
+// partial sum for every 16 products (a dw over 65536 rows: 3.8e-4).  The host asks for pieces wherever the
+// output would show it.
 template <int MODE, bool CHUNKED, int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     head_gemm(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,

@@ -28,7 +28,11 @@ constexpr int kGroup = 16;
 // fp32 operands have six products a step and fewer steps, an eighth of a short K for the logits: dx and dw of 300
 // rows on 1000 x 256 are off by 7.9e-7 of their size, by four steps 2.6e-6 (82 us, 80); 951 on 32001 x 1000 by
 // 6.4e-7, 8.6e-7 (1097 us, 1061).
-constexpr int kChunk = 28, kChunkParts = 4;
+// Gradients of bf16 operands: a dw in fp32 has its rows summed in such pieces too (65536 rows of one sign are off by
+// 4e-4 of their sum without; backward of 8192 rows on 131072 x 3584, dw added in fp32: 13890 to 14160 us, 13870 in
+// one sum, 2500 on 57899 x 1664 1140, 1085); what is rounded to bf16 has only sums of more than kChunkBf16 steps, which are cut by less
+// than a quarter of a step of bf16 below it.
+constexpr int kChunk = 28, kChunkParts = 4, kChunkBf16 = 2048;
 
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -413,16 +417,17 @@ cudaError_t gemm_of(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& 
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(clusters(), most_tiles);
   return launch_after(head_gemm<MODE, CHUNKED, TN>, grid, (unsigned)kThreads, Shape<TN>::smem, st, a, b, p);
 }
+// chunked: K in pieces of p.chunk steps (the row sums always are).
 template <int MODE>
-cudaError_t gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& p, int64_t most_tiles, bool narrow,
+cudaError_t gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmArgs& p, int64_t most_tiles, bool narrow, bool chunked,
                  cudaStream_t st) {
   constexpr bool always = MODE == kLse;
   if constexpr (MODE == kLse || MODE == kDz)
     if (narrow)
-      return always || p.passes > 1 ? gemm_of<MODE, true, kNarrow>(a, b, p, most_tiles, st)
-                                    : gemm_of<MODE, always, kNarrow>(a, b, p, most_tiles, st);
-  return always || p.passes > 1 ? gemm_of<MODE, true, 256>(a, b, p, most_tiles, st)
-                                : gemm_of<MODE, always, 256>(a, b, p, most_tiles, st);
+      return always || chunked ? gemm_of<MODE, true, kNarrow>(a, b, p, most_tiles, st)
+                               : gemm_of<MODE, always, kNarrow>(a, b, p, most_tiles, st);
+  return always || chunked ? gemm_of<MODE, true, 256>(a, b, p, most_tiles, st)
+                           : gemm_of<MODE, always, 256>(a, b, p, most_tiles, st);
 }
 // What both directions share: the rows with a target, gathered.  (8192 rows of 3584, with their targets' logits: 31 us by
 // four blocks an SM, 49 by two, 46 by six, which take two rounds.)
@@ -486,7 +491,7 @@ cudaError_t forward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, cha
     if (e != cudaSuccess) return e;
     g.tns = tiles(g.cols, tn);
     g.part0 = v0 / (tn / 2);
-    e = gemm<kLse>(mx, mw, g, (int64_t)tiles(s.n, kTile) * g.tns, narrow, st);
+    e = gemm<kLse>(mx, mw, g, (int64_t)tiles(s.n, kTile) * g.tns, narrow, true, st);
     if (e != cudaSuccess) return e;
   }
   return launch_after(join_lse, (unsigned)std::min(tiles(s.n, 8), 8 * device_sm_count()), 256u, 0, st, g, loss, lse);
@@ -509,7 +514,10 @@ cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, ch
   const int tms = tiles(s.n, kTile), tds = tiles(D, kTile);
   g.pitch = pl.pitch_z;
   GemmArgs gx = g, gw = g;
-  if (pl.parts_of > 1) gx.chunk = gw.chunk = kChunkParts;  // of a K of their own
+  gx.chunk = gw.chunk = pl.parts_of > 1 ? kChunkParts : kChunk;  // of a K of their own
+  // Whether a sum of `steps` is cut in pieces: always in parts, else where it is longer than a piece and stays fp32, or
+  // so long that the cuts come near a half of a step of bf16 all the same.
+  auto chunked = [&](int steps, bool fp32) { return pl.parts_of > 1 || steps > (fp32 ? kChunk : kChunkBf16); };
   for (int v0 = 0; v0 < V; v0 += pl.piece) {
     const int cols = std::min(pl.piece, V - v0);
     int row_b;
@@ -526,7 +534,7 @@ cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, ch
     g.steps = tiles(D, kStep);
     g.row_b = row_b;
     g.tns = tiles(cols, narrow ? kNarrow : kTile);
-    e = gemm<kDz>(mx, mw, g, (int64_t)tms * g.tns, narrow, st);
+    e = gemm<kDz>(mx, mw, g, (int64_t)tms * g.tns, narrow, pl.parts_of > 1, st);
     if (e != cudaSuccess) return e;
     if (dx) {
       const bool last = v0 + cols == V;
@@ -539,7 +547,7 @@ cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, ch
       gx.out_cols = D;
       gx.out_fp32 = sizeof(T) == 4;
       gx.out_vec = D % (16 / (int)sizeof(T)) == 0 && on16(dx);
-      e = gemm<kDx>(mz, mw64, gx, (int64_t)tms * tds * s.most_splits, false, st);
+      e = gemm<kDx>(mz, mw64, gx, (int64_t)tms * tds * s.most_splits, false, chunked(gx.steps, false), st);
       if (e != cudaSuccess) return e;
       if (last && s.most_splits > 1) {
         e = launch_after(join_dx<T>, (unsigned)std::min<int64_t>(((int64_t)s.n * tiles(D, 4) + 255) / 256, 8 * device_sm_count()),
@@ -557,7 +565,8 @@ cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, ch
       gw.accumulate = accumulate;
       gw.dw_splits = dw_splits(s.n, D, cols, clusters());
       gw.acc = reinterpret_cast<float*>(ws + pl.acc_w);
-      e = gemm<kDw>(mz64, mx64, gw, (int64_t)gw.tms * tds * gw.dw_splits, false, st);
+      e = gemm<kDw>(mz64, mx64, gw, (int64_t)gw.tms * tds * gw.dw_splits, false,
+                    chunked(tiles(tiles(s.n, kStep), gw.dw_splits), gw.out_fp32), st);
       if (e == cudaSuccess && gw.dw_splits > 1) {
         const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)cols * tiles(D, 4) + 255) / 256, 8 * device_sm_count());
         e = dw_dtype == OOMB_FP32 ? launch_after(join_dw<float>, grid, 256u, 0, st, gw)
