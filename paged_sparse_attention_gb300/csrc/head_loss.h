@@ -3,6 +3,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
 
@@ -90,11 +91,11 @@ cudaError_t launch_small_bwd(const SmallArgs& a, int dtype, int dw_dtype, cudaSt
 
 #ifdef __CUDACC__
 // Loss and log-sum-exp of a row from its target's logit z and the sum s 2^m of the other exponentials.
-// A sure row's loss is small and keeps its own precision.
+// A sure row's loss is small and keeps its own precision; a target's logit of +infinity makes it no number (inf - inf).
 __device__ __forceinline__ void loss_of(float z, float m, float s, float& loss, float& lse) {
   const float rest = (m + log2f(s)) * 0.6931471805599453f;
   if (z >= rest) {
-    loss = log1pf(s * exp2f(m - z * 1.4426950408889634f));
+    loss = z < INFINITY ? log1pf(s * exp2f(m - z * 1.4426950408889634f)) : z - z;
     lse = z + loss;
   } else {
     const float more = log1pf(expf(z - rest));
