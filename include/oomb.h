@@ -608,7 +608,8 @@ OOMB_API oomb_status oomb_layer_norm_fwd(const void* x, const float* w, const fl
  * reaches x by another way (NULL: none).  Written: dx ([n, D], dtype; may be dx_out) and, where
  * not NULL, dw and db (fp32 [D], summed over the rows in a fixed order; added to what they hold
  * when accumulate is not 0).  Workspace: oomb_layer_norm_workspace(n, D) bytes, contents scratch;
- * it grows with n.  Errors: those of oomb_layer_norm_fwd, WORKSPACE. */
+ * it grows with n; without dw and db there is none to give (NULL, 0).  Errors: those of
+ * oomb_layer_norm_fwd, WORKSPACE. */
 OOMB_API oomb_status oomb_layer_norm_bwd(const void* x, const float* w, const float* mean, const float* rstd,
                                          const void* dy, const void* dx_out, int n, int D, int dtype, void* dx,
                                          float* dw, float* db, int accumulate, void* workspace, size_t ws_bytes,

@@ -516,7 +516,8 @@ def oomb_layer_norm_fwd(x, w, b, out, eps: float = 1e-5, mean=None, rstd=None, s
 
 def oomb_layer_norm_bwd(x, w, mean, rstd, dy, dx, dw=None, db=None, dx_out=None, accumulate: bool = False,
                         workspace=None, stream=None) -> None:
-    """The backward of oomb_layer_norm_fwd; accumulate adds the parameter gradients to their buffers."""
+    """The backward of oomb_layer_norm_fwd; accumulate adds the parameter gradients to their buffers.  Without dw and
+    db no workspace is needed."""
     import torch
     f, dev, f32 = "oomb_layer_norm_bwd", torch.cuda.current_device(), torch.float32
     shape, ax = _lead(f, "x", x, 2, dev)

@@ -529,7 +529,7 @@ oomb_status oomb_layer_norm_bwd(const void* x, const float* w, const float* mean
   const oomb_status s = check_ln(x, w, n, D, dtype);
   if (s != OOMB_OK) return s;
   if (!mean || !rstd || !dy || !dx) return OOMB_ERR_ARG;
-  if (!workspace || ws_bytes < oomb_layer_norm_workspace(n, D)) return OOMB_ERR_WORKSPACE;
+  if ((dw || db) && (!workspace || ws_bytes < oomb_layer_norm_workspace(n, D))) return OOMB_ERR_WORKSPACE;
   const uintptr_t es = dtype_size(dtype);
   if (reinterpret_cast<uintptr_t>(dy) % es || reinterpret_cast<uintptr_t>(dx_out) % es ||
       reinterpret_cast<uintptr_t>(dx) % es || reinterpret_cast<uintptr_t>(mean) % 4 ||

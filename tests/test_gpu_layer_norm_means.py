@@ -97,3 +97,15 @@ def test_rows_of_both_kinds_by_their_blocks():
     t = ln_make(3000, 520, FP, seed=8, through=False)
     t["x"][::3] += 2e4
     check(run(t), *near(t))
+
+
+@pytest.mark.parametrize("n,D", [(5, 64), (16, 1000), (17, 1000), (700, 3584)])
+def test_backward_without_parameter_gradients_needs_no_workspace(n, D):
+    t = ln_make(n, D, BF, seed=n)
+    d = {k: v.cuda() for k, v in t.items()}
+    want = run(t)
+    dx = torch.full_like(d["x"], float("nan"))
+    L.oomb_layer_norm_bwd(d["x"], d["w"], want["mean"], want["rstd"], d["dy"], dx, dx_out=d["dx_out"])
+    assert torch.equal(dx, want["dx"])
+    with pytest.raises(L.OombError, match="ERR_WORKSPACE"):
+        L.oomb_layer_norm_bwd(d["x"], d["w"], want["mean"], want["rstd"], d["dy"], dx, dw=torch.empty(D, device="cuda"))
