@@ -589,7 +589,8 @@ OOMB_API oomb_status oomb_embed_fwd(const int64_t* tokens, int n, const void* ta
  * token are summed in fp32 in a fixed order: the same bits on every run.  Workspace:
  * oomb_embed_workspace(n, D) bytes (it grows with n: one for the longest chunk serves them all),
  * contents scratch; calls that may run at once need one each.
- * Errors: those of oomb_embed_fwd, WORKSPACE. */
+ * Errors: those of oomb_embed_fwd (UNSUPPORTED also for more than 2^26 rows, whose order would take seconds to hours:
+ * call it for parts of them, added), WORKSPACE. */
 OOMB_API oomb_status oomb_embed_bwd(const int64_t* tokens, int n, const void* d_out, int V, int D, int dtype,
                                     float scale, float* d_table, int accumulate, void* workspace, size_t ws_bytes,
                                     uint32_t* error_word, void* stream);

@@ -38,6 +38,7 @@ constexpr int kSortThreads = 1024, kSortKeys = kSection / kSortThreads;
 constexpr int kDigit = 6;       // bits a pass
 constexpr int kWindow = 16;     // sorted rows a piece lies in
 constexpr int kNone = INT_MAX;  // key of a row without a token: behind every other
+constexpr int kMostRows = 1 << 26;  // of a gradient: each section is searched for every row (2^24 rows take 0.33 s, 2^26 5)
 
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -761,6 +762,7 @@ oomb_status oomb_embed_bwd(const int64_t* tokens, int n, const void* d_out, int 
   const oomb_status s = check_embed(tokens, n, V, D, dtype, scale, error_word);
   if (s != OOMB_OK) return s;
   if (!d_out || !d_table) return OOMB_ERR_ARG;
+  if (n > kMostRows) return OOMB_ERR_UNSUPPORTED;
   const EmbedSpace w = embed_space(n, D);
   if (!workspace || ws_bytes < w.bytes) return OOMB_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(d_out) % dtype_size(dtype) || reinterpret_cast<uintptr_t>(d_table) % 4 ||

@@ -19,3 +19,16 @@ def test_layer_norm_backward_asks_only_for_parameter_gradients():
         assert bwd(F, None, n) == WORKSPACE and bwd(None, F, n) == WORKSPACE and bwd(F, F, n) == WORKSPACE
         assert bwd(F, F, n, F, lib.oomb_layer_norm_workspace(n, 64) - 1) == WORKSPACE
         assert bwd(F, F, n, F, lib.oomb_layer_norm_workspace(n, 64)) == ALIGN
+
+
+def test_embed_gradient_of_too_many_rows_is_refused():
+    """Its order is quadratic in the rows, and their number of windows has to fit an int."""
+    build.build()
+    lib = L.load()
+
+    def bwd(n, d_out=F + 1):
+        return lib.oomb_embed_bwd(F, n, d_out, 10, 1, 0, 1.0, F, 1, F, 1 << 50, F, None)
+
+    for n in ((1 << 26) + 1, 2 ** 31 - 16, 2 ** 31 - 15, 2 ** 31 - 1):
+        assert bwd(n) == 8
+    assert bwd(1 << 26) == ALIGN
