@@ -46,6 +46,20 @@ def prefix_cut(doc_start, prefix_len, chunk: int, n: int):
     return (end > first) & ((end - 1) // chunk > first // chunk)
 
 
+def chunk_gradient(d_o, o):
+    """A chunk's dO, whose memory the kernels read as that of ``o``: of its dtype and device, as many elements,
+    contiguous.  Anything else is refused."""
+    if not isinstance(d_o, torch.Tensor) or d_o.dtype is not o.dtype:
+        raise TypeError(f"LayerStep: dO has to be {o.dtype}, not {getattr(d_o, 'dtype', type(d_o).__name__)}")
+    if d_o.device != o.device:
+        raise ValueError(f"LayerStep: dO is on {d_o.device}, not on {o.device}")
+    if d_o.numel() != o.numel():
+        raise ValueError(f"LayerStep: dO of a chunk has shape {tuple(d_o.shape)}, needs {tuple(o.shape)}")
+    if not d_o.is_contiguous():
+        raise ValueError("LayerStep: dO is not contiguous")
+    return d_o
+
+
 class LayerStep:
     """Weights Wq [Dm, Hq*d], Wk and Wv [Dm, Hkv*d] (the pool's dtype, device), biases
     fp32 [H*d] or None.  Selection: top-K (``top_k``, ``n_sink``) or a local window
@@ -257,7 +271,7 @@ class LayerStep:
             a_sel = att[ci]
             self._attend(q, s, a_sel, o, lse)
             dq = torch.empty_like(q)
-            d_o = dO(s, o) if callable(dO) else dO[s:s + n]
+            d_o = chunk_gradient(dO(s, o) if callable(dO) else dO[s:s + n], o)
             self._attend_bwd(q, o, d_o, lse, s, a_sel, dq, ws_bwd)
             # the chunk's own dK/dV are complete: back through the rotation and projections
             g = {"q": torch.empty((n, Hq * d), dtype=f32, device=dev),
