@@ -20,12 +20,13 @@ from . import _lib as L
 
 class ModelEnds:
     """``table`` [V, Dm] (bf16 or fp32, device): the embeddings.  ``head`` [V, Dm] (the same dtype): the
-    output projection; None: the table itself, whose gradient then holds both shares.  ``w_norm``,
-    ``b_norm`` (fp32 [Dm] or None): the last layer norm, there when ``w_norm`` is.  ``scale``: factor of
+    output projection, with a gradient of its own; None: the table itself, whose gradient then holds both
+    shares.  ``w_norm``, ``b_norm`` (fp32 [Dm] or None): the last layer norm, there when ``w_norm`` is.  ``scale``: factor of
     the embeddings; ``softcap``: cap of the logits (0: none).  ``chunk``: most tokens of a call.
 
     Gradients, zeroed by ``zero_grad``: d_table, d_head (the same tensor when shared), and dw_norm,
-    db_norm where the norm has them, all fp32.  Errors that kernels met (a token behind the vocabulary)
+    db_norm where the norm has them, all fp32.  Calls of one object follow one another on one stream: they share a
+    workspace and the gradients.  Errors that kernels met (a token behind the vocabulary)
     are told by ``check``."""
 
     def __init__(self, table, head=None, w_norm=None, b_norm=None, chunk: int = 4096, scale: float = 1.0,
