@@ -31,8 +31,11 @@ constexpr int kGroup = 16;
 // Gradients of bf16 operands: a dw in fp32 has its rows summed in such pieces too (65536 rows of one sign are off by
 // 4e-4 of their sum without; backward of 8192 rows on 131072 x 3584, dw added in fp32: 13890 to 14160 us, 13870 in
 // one sum, 2500 on 57899 x 1664 1140, 1085); what is rounded to bf16 has only sums of more than kChunkBf16 steps, which are cut by less
-// than a quarter of a step of bf16 below it.
-constexpr int kChunk = 28, kChunkParts = 4, kChunkBf16 = 2048;
+// than a quarter of a step of bf16 below it.  dz's logits of bf16 operands are one sum up to kDzSteps: it is cut by 5e-6 of a
+// logit at most, which is a quarter of a step of dz for logits of 200 (in pieces, 8192 rows on 131072 x 3584 both ways
+// 18570 to 18770 us, 1600 of 4001 on 50001 x 2048 under a cap 958 to 984).  Wider rows would form other logits than the
+// forward did: probabilities were 1 % off at logits of 160 over 8192 columns, 7 % over 65536.
+constexpr int kChunk = 28, kChunkParts = 4, kChunkBf16 = 2048, kDzSteps = 2 * kChunk;
 
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -534,7 +537,7 @@ cudaError_t backward(GemmArgs g, GatherArgs s, const void* w, const Plan& pl, ch
     g.steps = tiles(D, kStep);
     g.row_b = row_b;
     g.tns = tiles(cols, narrow ? kNarrow : kTile);
-    e = gemm<kDz>(mx, mw, g, (int64_t)tms * g.tns, narrow, pl.parts_of > 1, st);
+    e = gemm<kDz>(mx, mw, g, (int64_t)tms * g.tns, narrow, pl.parts_of > 1 || g.steps > kDzSteps, st);
     if (e != cudaSuccess) return e;
     if (dx) {
       const bool last = v0 + cols == V;

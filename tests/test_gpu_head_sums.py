@@ -66,3 +66,23 @@ def test_bf16_gradient_of_very_many_rows():
     got, want = flat(n, 1024, 2560, BF, BF)
     half = torch.ldexp(torch.ones_like(want), torch.frexp(want).exponent - 9)  # of a step of bf16 at this value
     assert ((got - want).abs() <= half + cuts(n) * want).all(), float((((got - want).abs() - half) / want).max())
+
+
+@pytest.mark.parametrize("D", [8192, 65536])
+@pytest.mark.parametrize("dw_dtype", [BF, FP])
+def test_probabilities_of_wide_rows(D, dw_dtype):
+    """Every logit of a row is the same long sum of one sign: each probability is 1 / V, a power of two, unless the backward
+    forms other logits than the forward did.  (Off by less than 2^-9 it is rounded to 1 / V.)"""
+    n, V = 300, 2048
+    x = torch.rand(n, D, generator=torch.Generator("cuda").manual_seed(D), device="cuda").add_(1.0).to(BF)
+    w = torch.full((V, D), 213 / 128 * 2.0 ** -10 * 65536 / D, dtype=BF, device="cuda")  # logits of about 160
+    t = torch.zeros(n, dtype=torch.int64, device="cuda")
+    loss, lse, err = torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), word()
+    dw = torch.full((V, D), float("nan"), dtype=dw_dtype, device="cuda")
+    ws = torch.empty(L.oomb_head_loss_workspace(n, D, V, BF, True), dtype=torch.uint8, device="cuda")
+    L.oomb_head_loss_fwd(x, w, t, loss, lse, ws, err)
+    L.oomb_head_loss_bwd(x, w, t, lse, None, dw, ws, err)
+    assert L.oomb_word_check(err) == 0
+    want = x.to(F64).sum(0) / V
+    tol = cuts(n) + (torch.finfo(BF).eps / 2 if dw_dtype is BF else 0.0)
+    assert ((dw[1:].to(F64) - want).abs() <= tol * want).all(), float(((dw[1:].to(F64) - want).abs() / want).max())
