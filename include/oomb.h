@@ -639,7 +639,7 @@ OOMB_API oomb_status oomb_head_loss_fwd(const void* x, const void* w, const int6
  *   accumulate is not 0 (fp32 only), else written
  * The logits are formed again, one piece of the vocabulary after another; a piece's dz / scale is
  * held in the workspace, in bf16 for bf16 operands (scale is applied to the sums: a mean's factor
- * costs no rounding).  All sums are in a fixed order: the same bits on every run.  Workspace:
+ * costs no rounding; dx and dw are off by 0.0017 of their size for it, an fp32 dw too).  All sums are in a fixed order: the same bits on every run.  Workspace:
  * oomb_head_loss_workspace(n, D, V, dtype, 1) bytes on 256 bytes (it serves the forward too).
  * Errors: those of oomb_head_loss_fwd (ARG also for a scale that is not finite, for neither dx
  * nor dw, and for accumulate with a dw that is not fp32). */

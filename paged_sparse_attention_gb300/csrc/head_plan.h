@@ -16,8 +16,9 @@ constexpr int kNarrow = 64;
 
 // Workspace given to a piece's dz, and to staged parts of W where it cannot be read in place
 // (kStagedOdd: bf16 rows that are on 16 bytes unless the caller's pointer is not).  Both directions with 256, 512
-// and 1024 MB for dz: 8192 rows on 131072 x 3584 18882, 18762 and 18773 us, 1600 of 4001 on 50001 x 2048 988, 870
-// and 919, 951 on 32001 x 1000 in fp32 1077, 1081 and 1119.
+// and 1024 MB for dz: 8192 rows on 131072 x 3584 18882, 18762 and 18773 us, 951 on 32001 x 1000 in fp32 1077, 1081 and
+// 1119; 1600 of 4001 on 50001 x 2048 with 256 and 512 MB 932 and 876 us in a run of 20 ms, 992 and 952 in one of a
+// second (1024 MB: 6 % above 512).
 constexpr size_t kAccBytes = 256u << 20, kDzBytes = 512u << 20, kStagedBytes = 256u << 20, kStagedOdd = 32u << 20;
 
 inline int tiles(int64_t x, int t) { return (int)((x + t - 1) / t); }
