@@ -589,8 +589,8 @@ OOMB_API oomb_status oomb_embed_fwd(const int64_t* tokens, int n, const void* ta
  * token are summed in fp32 in a fixed order: the same bits on every run.  Workspace:
  * oomb_embed_workspace(n, D) bytes (it grows with n: one for the longest chunk serves them all),
  * contents scratch; calls that may run at once need one each.
- * Errors: those of oomb_embed_fwd (UNSUPPORTED also for more than 2^26 rows, whose order would take seconds to hours:
- * call it for parts of them, added), WORKSPACE. */
+ * Errors: those of oomb_embed_fwd (UNSUPPORTED also for more than 2^26 rows, whose order would take
+ * seconds to hours: call it for parts of them, added), WORKSPACE. */
 OOMB_API oomb_status oomb_embed_bwd(const int64_t* tokens, int n, const void* d_out, int V, int D, int dtype,
                                     float scale, float* d_table, int accumulate, void* workspace, size_t ws_bytes,
                                     uint32_t* error_word, void* stream);
@@ -639,7 +639,8 @@ OOMB_API oomb_status oomb_head_loss_fwd(const void* x, const void* w, const int6
  *   accumulate is not 0 (fp32 only), else written
  * The logits are formed again, one piece of the vocabulary after another; a piece's dz / scale is
  * held in the workspace, in bf16 for bf16 operands (scale is applied to the sums: a mean's factor
- * costs no rounding; dx and dw are off by 0.0017 of their size for it, an fp32 dw too).  All sums are in a fixed order: the same bits on every run.  Workspace:
+ * costs no rounding; dx and dw are off by 0.0017 of their size for it, an fp32 dw too).  All sums
+ * are in a fixed order: the same bits on every run.  Workspace:
  * oomb_head_loss_workspace(n, D, V, dtype, 1) bytes on 256 bytes (it serves the forward too).
  * Errors: those of oomb_head_loss_fwd (ARG also for a scale that is not finite, for neither dx
  * nor dw, and for accumulate with a dw that is not fp32). */
